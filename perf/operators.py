@@ -202,7 +202,7 @@ def prepare(case, seed):
             s["ws"] = torch.empty(max(R.repro_distill_ws_bytes(n, V), 16), dtype=torch.uint8, device="cuda")
             s["hp"] = dict(tau=c["tau"], w_kd=c["w_kd"], w_ce=c["w_ce"], w_z=c["w_z"], logprobs=c["logprobs"])
             if op == "distill_bwd":   # the forward's row statistics, kept for the backward
-                s["stats"] = torch.empty((n, R.REPRO_DISTILL_STATS), device="cuda")
+                s["stats"] = torch.empty((n, R.REPRO_DISTILL_STATS + K), device="cuda")
                 R.repro_distill_fwd(s["logits"], s["t_idx"], s["t_logits"], torch.empty(n, device="cuda"),
                                     s["stats"], labels=s["labels"], ws=s["ws"], **s["hp"])
         elif op == "distill_bwd":
@@ -375,13 +375,12 @@ def _own(s):
         return [dq, dk] + (dg if c["gain"] else [])
     if op == "distill_fwd":
         loss = torch.empty(c["n"], device=dev)
-        stats = torch.empty((c["n"], R.REPRO_DISTILL_STATS), device=dev)
+        stats = torch.empty((c["n"], R.REPRO_DISTILL_STATS + c["K"]), device=dev)
         R.repro_distill_fwd(s["logits"], s["t_idx"], s["t_logits"], loss, stats, labels=s["labels"],
                             ws=s["ws"], **s["hp"])
         return [loss, stats[:, R.REPRO_DISTILL_STAT_LSE]]
     dz = torch.empty_like(s["logits"])
-    R.repro_distill_bwd(s["logits"], s["t_idx"], s["t_logits"], s["stats"], s["g"], dz, labels=s["labels"],
-                        **s["hp"])
+    R.repro_distill_bwd(s["logits"], s["t_idx"], s["stats"], s["g"], dz, labels=s["labels"], **s["hp"])
     return dz
 
 
