@@ -69,9 +69,15 @@ int scan_inputs(void* stream, std::initializer_list<FloatSpan> spans)
     if (!err)
         return REPRO_ERR_LAUNCH;
     for (const FloatSpan& f : spans)
-        if (f.p && f.n > 0 &&
-            launch_check_finite(f.p, f.n, err, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-            return REPRO_ERR_LAUNCH;
+        if (f.p && f.n > 0) {
+            // the fast scan loads 16 bytes at a time; row statistics and gains may start on 4
+            const cudaStream_t st = static_cast<cudaStream_t>(stream);
+            const cudaError_t e = ((uintptr_t)f.p & 15u) == 0
+                                      ? launch_check_finite(f.p, f.n, err, st)
+                                      : launch_check_finite_rows(f.p, REPRO_F32, 1, f.n, f.n, err, st);
+            if (e != cudaSuccess)
+                return REPRO_ERR_LAUNCH;
+        }
     return REPRO_OK;
 }
 
@@ -207,6 +213,7 @@ const char* repro_status_str(int s)
     case REPRO_ERR_WORKSPACE: return "workspace missing or too small";
     case REPRO_ERR_ALIAS: return "buffers that must not overlap do";
     case REPRO_ERR_SELFTEST: return "the tensor-core forward differs from the exact CUDA-core forward";
+    case REPRO_ERR_INDEX: return "a token, position, teacher index or label was out of range";
     case REPRO_ERR_NONFINITE: return "debug mode: a float input held a NaN or an infinity";
     default: return "unknown status";
     }
@@ -296,7 +303,9 @@ int repro_device_check(void* stream)
         const int zero = 0;
         if (cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int)) != cudaSuccess)
             return REPRO_ERR_LAUNCH;
-        return (v & kErrTimeoutBit) || !(v & kErrNonfiniteBit) ? REPRO_ERR_TIMEOUT : REPRO_ERR_NONFINITE;
+        if (v & kErrTimeoutBit)
+            return REPRO_ERR_TIMEOUT;
+        return v & kErrIndexBit ? REPRO_ERR_INDEX : v & kErrNonfiniteBit ? REPRO_ERR_NONFINITE : REPRO_ERR_TIMEOUT;
     }
     const int dev = current_device();
     if (dev >= 0 && dev < kMaxDevices && g_tc_notice[dev].exchange(0) != 0)
@@ -884,6 +893,454 @@ int repro_attn_bwd(const float* q, const float* k, const int8_t* vq, const float
         return st;
     return status_of(launch_attn_bwd(q, k, vq, s_v, o, dout, m, l, dq, dk, dv, B, T, Hq, Hkv, W,
                                      ws, fwd_ws, as_stream(stream)));
+}
+
+// ---------------------------------------------------------------- around the blocks
+
+namespace {
+
+// what a call touches, checked together: no output overlaps anything else
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+
+size_t type_bytes(int type) { return type == REPRO_F32 ? 4 : type == REPRO_BF16 ? 2 : 1; }
+bool float_type(int type) { return type == REPRO_F32 || type == REPRO_BF16; }
+bool aligned_to(const void* p, size_t b) { return (uintptr_t)p % b == 0; }
+float flushed(float v) { return v != 0.0f && v > -1.17549435e-38f && v < 1.17549435e-38f ? 0.0f : v; }
+bool finite_f(float v) { return v - v == 0.0f; }
+
+// elements from the first to one past the last of `rows` rows of D, ld apart
+size_t row_span(int64_t rows, int64_t ld, int64_t D) { return (size_t)((rows - 1) * ld + D); }
+// whether that count fits comfortably in 63 bits of bytes
+bool rows_fit(int64_t rows, int64_t ld, int64_t D)
+{
+    return rows <= (int64_t)1 << 31 && ld <= (int64_t)1 << 28 && D <= (int64_t)1 << 28;
+}
+
+bool any_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins)
+{
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span& i : ins)
+            if (overlap(o->p, o->bytes, i.p, i.bytes))
+                return true;
+        for (const Span* q = o + 1; q != outs.end(); ++q)
+            if (overlap(o->p, o->bytes, q->p, q->bytes))
+                return true;
+    }
+    return false;
+}
+
+// debug mode: the scan of a strided tensor
+int scan_rows(void* stream, const void* p, int type, int64_t rows, int64_t D, int64_t ld)
+{
+    if ((g_debug.load(std::memory_order_relaxed) & REPRO_DEBUG_CHECK_FINITE) == 0 || !p || rows <= 0)
+        return REPRO_OK;
+    int* err = device_error_word();
+    if (!err)
+        return REPRO_ERR_LAUNCH;
+    return status_of(launch_check_finite_rows(p, type, rows, D, ld, err, as_stream(stream)));
+}
+
+} // namespace
+
+int repro_embed_fwd(const void* table, int table_type, int64_t table_ld, const float* s_w,
+                    const void* tokens, int index_bytes, int64_t n, int64_t V, int64_t D, float scale,
+                    int64_t pad, void* out, int out_type, int64_t out_ld, void* stream)
+{
+    if ((!float_type(table_type) && table_type != REPRO_I8) || !float_type(out_type) ||
+        (index_bytes != 4 && index_bytes != 8) || !finite_f(scale) ||
+        (table_type == REPRO_I8) != (s_w != nullptr))
+        return REPRO_ERR_ARG;
+    if (n < 0 || V < 1 || D < 1 || table_ld < D || out_ld < D || !rows_fit(V, table_ld, D) ||
+        !rows_fit(n, out_ld, D) || n > INT32_MAX)
+        return REPRO_ERR_SHAPE;
+    if (n == 0)
+        return REPRO_OK;
+    if (!table || !tokens || !out)
+        return REPRO_ERR_ARG;
+    const size_t tb = type_bytes(table_type), ob = type_bytes(out_type);
+    if (!aligned_to(table, tb) || !aligned_to(out, ob) || !aligned_to(tokens, index_bytes) || !al4(s_w))
+        return REPRO_ERR_ALIGN;
+    if (any_overlap({{out, row_span(n, out_ld, D) * ob}},
+                    {{table, row_span(V, table_ld, D) * tb}, {tokens, (size_t)n * index_bytes}, {s_w, 4}}))
+        return REPRO_ERR_ALIAS;
+    int st = check_arch();
+    if (st != REPRO_OK)
+        return st;
+    if ((table_type != REPRO_I8 && (st = scan_rows(stream, table, table_type, V, D, table_ld)) != REPRO_OK) ||
+        (st = scan_inputs(stream, {{s_w, s_w ? 1 : 0}})) != REPRO_OK)
+        return st;
+    int* err = device_error_word();
+    if (!err)
+        return REPRO_ERR_LAUNCH;
+    return status_of(launch_embed_fwd({table, table_type, table_ld, s_w, tokens, index_bytes, n, V, D, scale,
+                                       pad, out, out_type, out_ld, err}, as_stream(stream)));
+}
+
+size_t repro_embed_bwd_ws_bytes(int64_t n, int64_t V, int64_t D)
+{
+    if (n < 0 || n > INT32_MAX || V < 1 || V > REPRO_EMBED_MAX_V || D < 1 || D > (int64_t)1 << 28)
+        return 0;
+    return embed_bwd_ws_bytes(n, D);
+}
+
+int repro_embed_bwd(const void* dout, int dout_type, int64_t dout_ld, const void* tokens, int index_bytes,
+                    int64_t n, int64_t V, int64_t D, float scale, int64_t pad, float* dtable,
+                    int64_t dtable_ld, int flags, void* ws, size_t ws_bytes, void* stream)
+{
+    if (!float_type(dout_type) || (index_bytes != 4 && index_bytes != 8) || !finite_f(scale) ||
+        (flags & ~REPRO_BWD_DW_ACCUMULATE) || !dtable)
+        return REPRO_ERR_ARG;
+    if (n < 0 || n > INT32_MAX || V < 1 || V > REPRO_EMBED_MAX_V || D < 1 || dout_ld < D || dtable_ld < D ||
+        !rows_fit(n, dout_ld, D) || !rows_fit(V, dtable_ld, D))
+        return REPRO_ERR_SHAPE;
+    const bool accumulate = (flags & REPRO_BWD_DW_ACCUMULATE) != 0;
+    if (n == 0 && accumulate)
+        return REPRO_OK;
+    if (n > 0 && (!dout || !tokens))
+        return REPRO_ERR_ARG;
+    const size_t db = type_bytes(dout_type), need = embed_bwd_ws_bytes(n, D);
+    if (!aligned_to(dout, db) || !al4(dtable) || !aligned_to(tokens, index_bytes))
+        return REPRO_ERR_ALIGN;
+    if (!ws || ws_bytes < need)
+        return REPRO_ERR_WORKSPACE;
+    if (!al16(ws))
+        return REPRO_ERR_ALIGN;
+    if (any_overlap({{dtable, row_span(V, dtable_ld, D) * 4}, {ws, need}},
+                    {{dout, n > 0 ? row_span(n, dout_ld, D) * db : 0}, {tokens, (size_t)n * index_bytes}}))
+        return REPRO_ERR_ALIAS;
+    int st = check_arch();
+    if (st != REPRO_OK)
+        return st;
+    if ((st = scan_rows(stream, dout, dout_type, n, D, dout_ld)) != REPRO_OK ||
+        (accumulate && (st = scan_rows(stream, dtable, REPRO_F32, V, D, dtable_ld)) != REPRO_OK))
+        return st;
+    int* err = device_error_word();
+    if (!err)
+        return REPRO_ERR_LAUNCH;
+    return status_of(launch_embed_bwd({dout, dout_type, dout_ld, tokens, index_bytes, n, V, D, scale, pad,
+                                       dtable, dtable_ld, accumulate, err}, ws, as_stream(stream)));
+}
+
+// arguments that the norm's forward and backward share; OK, or what is wrong
+static int check_qk(const void* q, int64_t q_ld, int64_t q_hs, const void* k, int64_t k_ld, int64_t k_hs,
+                    int type, const float* gain_q, const float* gain_k, const float* rope, int64_t P,
+                    const int32_t* positions, int64_t T, float eps, int64_t n, int64_t Hq, int64_t Hkv,
+                    int64_t D, int64_t R, int flags, int allowed)
+{
+    if (!float_type(type) || (flags & ~allowed) || !(eps >= 0.0f) || !finite_f(eps))
+        return REPRO_ERR_ARG;
+    if (n < 0 || Hq < 1 || Hkv < 0 || D < 1 || D > REPRO_QK_MAX_D || R < 0 || R > D || R % 2 != 0)
+        return REPRO_ERR_SHAPE;
+    if (q_hs < D || q_ld < 1 || !rows_fit(n, q_ld, q_hs) || (Hkv > 0 && (k_hs < D || k_ld < 1 || !rows_fit(n, k_ld, k_hs))))
+        return REPRO_ERR_SHAPE;
+    if (Hq > 65535 || Hkv > 65535 || n * (Hq + Hkv) > INT32_MAX)
+        return REPRO_ERR_SHAPE;
+    if (R > 0 && (P < 1 || P > INT32_MAX || (!positions && T < 1) || T > INT32_MAX))
+        return REPRO_ERR_SHAPE;
+    if (n == 0)
+        return REPRO_OK;
+    if (!q || (R > 0 && !rope) || (Hkv > 0 && !k) || (Hkv == 0 && gain_k))
+        return REPRO_ERR_ARG;
+    const size_t b = type_bytes(type);
+    if (!aligned_to(q, b) || !aligned_to(k, b) || !al4(gain_q) || !al4(gain_k) || !al16(rope) || !al4(positions))
+        return REPRO_ERR_ALIGN;
+    return REPRO_OK;
+}
+
+// bytes from the first to past the last element of n tokens of H strided heads
+static size_t head_span(int64_t n, int64_t ld, int64_t hs, int64_t H, int64_t D, int type)
+{
+    return n > 0 && H > 0 ? (size_t)((n - 1) * ld + (H - 1) * hs + D) * type_bytes(type) : 0;
+}
+
+// debug mode: the scan of n tokens of H strided heads, head by head
+static int scan_heads(void* stream, const void* p, int type, int64_t n, int64_t ld, int64_t hs, int64_t H, int64_t D)
+{
+    for (int64_t h = 0; h < H; ++h) {
+        const int st = scan_rows(stream, static_cast<const char*>(p) + (size_t)(h * hs) * type_bytes(type), type, n, D, ld);
+        if (st != REPRO_OK)
+            return st;
+    }
+    return REPRO_OK;
+}
+
+int repro_qk_norm_rope_fwd(const void* q, int64_t q_ld, int64_t q_hs, const void* k, int64_t k_ld,
+                           int64_t k_hs, int type, const float* gain_q, const float* gain_k,
+                           const float* rope, int64_t P, const int32_t* positions, int64_t T, float eps,
+                           int64_t n, int64_t Hq, int64_t Hkv, int64_t D, int64_t R, int flags,
+                           float* q_out, float* k_out, void* stream)
+{
+    int st = check_qk(q, q_ld, q_hs, k, k_ld, k_hs, type, gain_q, gain_k, rope, P, positions, T, eps, n, Hq,
+                      Hkv, D, R, flags, REPRO_QK_INTERLEAVED);
+    if (st != REPRO_OK || n == 0)
+        return st;
+    if (!q_out || (Hkv > 0 && !k_out))
+        return REPRO_ERR_ARG;
+    if (!al16(q_out) || !al16(k_out))
+        return REPRO_ERR_ALIGN;
+    const Span ropes = {rope, (size_t)(P * R) * 4}, pos = {positions, (size_t)n * 4};
+    if (any_overlap({{q_out, (size_t)(n * Hq * D) * 4}, {k_out, (size_t)(n * Hkv * D) * 4}},
+                    {{q, head_span(n, q_ld, q_hs, Hq, D, type)}, {k, head_span(n, k_ld, k_hs, Hkv, D, type)},
+                     ropes, pos, {gain_q, (size_t)D * 4}, {gain_k, (size_t)D * 4}}))
+        return REPRO_ERR_ALIAS;
+    st = check_arch();
+    if (st != REPRO_OK)
+        return st;
+    if ((st = scan_heads(stream, q, type, n, q_ld, q_hs, Hq, D)) != REPRO_OK ||
+        (st = scan_heads(stream, k, type, n, k_ld, k_hs, Hkv, D)) != REPRO_OK ||
+        (st = scan_inputs(stream, {{rope, P * R}, {gain_q, D}, {gain_k, D}})) != REPRO_OK)
+        return st;
+    QkArgs a = {};
+    a.t[0] = {q, q_ld, q_hs, Hq, gain_q, q_out, nullptr, nullptr, 0, 0, nullptr};
+    a.t[1] = {k, k_ld, k_hs, Hkv, gain_k, k_out, nullptr, nullptr, 0, 0, nullptr};
+    a.type = type;
+    a.rope = rope;
+    a.P = P;
+    a.positions = positions;
+    a.T = T;
+    a.eps = eps;
+    a.n = n;
+    a.D = D;
+    a.R = R;
+    a.interleaved = (flags & REPRO_QK_INTERLEAVED) != 0;
+    a.err = device_error_word();
+    if (!a.err)
+        return REPRO_ERR_LAUNCH;
+    return status_of(launch_qk_fwd(a, as_stream(stream)));
+}
+
+size_t repro_qk_norm_rope_bwd_ws_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64_t D)
+{
+    if (n < 0 || Hq < 1 || Hkv < 0 || Hq > 65535 || Hkv > 65535 || D < 1 || D > REPRO_QK_MAX_D ||
+        n > INT32_MAX || n * (Hq + Hkv) > INT32_MAX)
+        return 0;
+    return qk_bwd_ws_bytes(n, Hq, Hkv, D);
+}
+
+int repro_qk_norm_rope_bwd(const float* dq_out, const float* dk_out, const void* q, int64_t q_ld,
+                           int64_t q_hs, const void* k, int64_t k_ld, int64_t k_hs, int type,
+                           const float* gain_q, const float* gain_k, const float* rope, int64_t P,
+                           const int32_t* positions, int64_t T, float eps, int64_t n, int64_t Hq,
+                           int64_t Hkv, int64_t D, int64_t R, int flags, void* dq, int64_t dq_ld,
+                           int64_t dq_hs, void* dk, int64_t dk_ld, int64_t dk_hs, float* dgain_q,
+                           float* dgain_k, void* ws, size_t ws_bytes, void* stream)
+{
+    int st = check_qk(q, q_ld, q_hs, k, k_ld, k_hs, type, gain_q, gain_k, rope, P, positions, T, eps, n, Hq,
+                      Hkv, D, R, flags, REPRO_QK_INTERLEAVED | REPRO_BWD_DW_ACCUMULATE);
+    if (st != REPRO_OK)
+        return st;
+    if ((gain_q != nullptr) != (dgain_q != nullptr) || (gain_k != nullptr) != (dgain_k != nullptr))
+        return REPRO_ERR_ARG;
+    if (dq_hs < D || dq_ld < 1 || !rows_fit(n, dq_ld, dq_hs) ||
+        (Hkv > 0 && (dk_hs < D || dk_ld < 1 || !rows_fit(n, dk_ld, dk_hs))))
+        return REPRO_ERR_SHAPE;
+    const bool accumulate = (flags & REPRO_BWD_DW_ACCUMULATE) != 0;
+    if (!al4(dgain_q) || !al4(dgain_k))
+        return REPRO_ERR_ALIGN;
+    if (n == 0) {   // the gains' gradients of no rows are +0
+        if (accumulate || (!dgain_q && !dgain_k))
+            return REPRO_OK;
+        if ((st = check_arch()) != REPRO_OK)
+            return st;
+        for (float* d : {dgain_q, dgain_k})
+            if (d && cudaMemsetAsync(d, 0, (size_t)D * 4, as_stream(stream)) != cudaSuccess)
+                return REPRO_ERR_LAUNCH;
+        return REPRO_OK;
+    }
+    if (!dq_out || !dq || (Hkv > 0 && (!dk_out || !dk)))
+        return REPRO_ERR_ARG;
+    const size_t b = type_bytes(type);
+    if (!al16(dq_out) || !al16(dk_out) || !aligned_to(dq, b) || !aligned_to(dk, b))
+        return REPRO_ERR_ALIGN;
+    const size_t need = gain_q || gain_k ? qk_bwd_ws_bytes(n, Hq, Hkv, D) : 0;
+    if (need > 0 && (!ws || ws_bytes < need))
+        return REPRO_ERR_WORKSPACE;
+    if (need > 0 && !al16(ws))
+        return REPRO_ERR_ALIGN;
+    // dq and dk may lie between one another, as in the gradient of the fused output; each is
+    // checked against everything else, and they must not share a row range head by head
+    const Span sq = {dq, head_span(n, dq_ld, dq_hs, Hq, D, type)}, sk = {dk, head_span(n, dk_ld, dk_hs, Hkv, D, type)};
+    const Span dg[2] = {{dgain_q, (size_t)D * 4}, {dgain_k, (size_t)D * 4}}, wss = {ws, need};
+    const Span in[8] = {{dq_out, (size_t)(n * Hq * D) * 4}, {dk_out, (size_t)(n * Hkv * D) * 4},
+                        {q, head_span(n, q_ld, q_hs, Hq, D, type)}, {k, head_span(n, k_ld, k_hs, Hkv, D, type)},
+                        {rope, (size_t)(P * R) * 4}, {positions, (size_t)n * 4}, {gain_q, (size_t)D * 4},
+                        {gain_k, (size_t)D * 4}};
+    for (const Span& o : {sq, sk, dg[0], dg[1], wss})
+        for (const Span& i : in)
+            if (overlap(o.p, o.bytes, i.p, i.bytes))
+                return REPRO_ERR_ALIAS;
+    if (any_overlap({dg[0], dg[1], wss}, {sq, sk}))
+        return REPRO_ERR_ALIAS;
+    if (overlap(sq.p, sq.bytes, sk.p, sk.bytes)) {
+        // interleaved in one buffer: allowed when the token strides agree and a token's
+        // heads of q and k are disjoint
+        const int64_t off = ((const char*)dk - (const char*)dq) / (int64_t)b;
+        const int64_t wq = (Hq - 1) * dq_hs + D, wk = (Hkv - 1) * dk_hs + D;
+        const bool ok = dq_ld == dk_ld && (off >= 0 ? off >= wq && off + wk <= dq_ld : -off >= wk && -off + wq <= dq_ld);
+        if (!ok)
+            return REPRO_ERR_ALIAS;
+    }
+    st = check_arch();
+    if (st != REPRO_OK)
+        return st;
+    if ((st = scan_heads(stream, q, type, n, q_ld, q_hs, Hq, D)) != REPRO_OK ||
+        (st = scan_heads(stream, k, type, n, k_ld, k_hs, Hkv, D)) != REPRO_OK ||
+        (st = scan_inputs(stream, {{dq_out, n * Hq * D}, {dk_out, n * Hkv * D}, {rope, P * R}, {gain_q, D},
+                                   {gain_k, D}})) != REPRO_OK)
+        return st;
+    QkArgs a = {};
+    a.t[0] = {q, q_ld, q_hs, Hq, gain_q, nullptr, dq_out, dq, dq_ld, dq_hs, dgain_q};
+    a.t[1] = {k, k_ld, k_hs, Hkv, gain_k, nullptr, dk_out, dk, dk_ld, dk_hs, dgain_k};
+    a.type = type;
+    a.rope = rope;
+    a.P = P;
+    a.positions = positions;
+    a.T = T;
+    a.eps = eps;
+    a.n = n;
+    a.D = D;
+    a.R = R;
+    a.interleaved = (flags & REPRO_QK_INTERLEAVED) != 0;
+    a.accumulate = accumulate;
+    a.err = device_error_word();
+    if (!a.err)
+        return REPRO_ERR_LAUNCH;
+    return status_of(launch_qk_bwd(a, ws, as_stream(stream)));
+}
+
+size_t repro_distill_ws_bytes(int64_t n, int64_t V)
+{
+    if (n < 0 || V < 1 || n > INT32_MAX || V > (int64_t)1 << 28)
+        return 0;
+    return distill_ws_bytes(n, V);
+}
+
+// arguments that the loss and its gradient share
+static int check_distill(const void* z, int z_type, int64_t z_ld, const void* t_idx, const void* labels,
+                         int index_bytes, int64_t n, int64_t V, int64_t K, const repro_distill_hparams* hp)
+{
+    if (!float_type(z_type) || (index_bytes != 4 && index_bytes != 8) || !hp)
+        return REPRO_ERR_ARG;
+    if (!(hp->tau >= 1e-4f && hp->tau <= 1e4f) || !finite_f(hp->w_kd) || !finite_f(hp->w_ce) || !finite_f(hp->w_z))
+        return REPRO_ERR_ARG;
+    if (n < 0 || V < 1 || K < 0 || z_ld < V || !rows_fit(n, z_ld, V) || K > 65536 || n > INT32_MAX ||
+        n * ((V + REPRO_DISTILL_BLOCK - 1) / REPRO_DISTILL_BLOCK) > INT32_MAX)
+        return REPRO_ERR_SHAPE;
+    if (n == 0)
+        return REPRO_OK;
+    if (!z || (K > 0 && !t_idx) || (flushed(hp->w_ce) != 0.0f && !labels))
+        return REPRO_ERR_ARG;
+    if (!aligned_to(z, type_bytes(z_type)) || !aligned_to(t_idx, index_bytes) || !aligned_to(labels, index_bytes))
+        return REPRO_ERR_ALIGN;
+    return REPRO_OK;
+}
+
+int repro_distill_fwd(const void* z, int z_type, int64_t z_ld, const void* t_idx, const void* t_val,
+                      int t_type, const void* labels, int index_bytes, int64_t n, int64_t V, int64_t K,
+                      const repro_distill_hparams* hp, int flags, float* loss, float* stats, void* ws,
+                      size_t ws_bytes, void* stream)
+{
+    int st = check_distill(z, z_type, z_ld, t_idx, labels, index_bytes, n, V, K, hp);
+    if (st != REPRO_OK)
+        return st;
+    if (!float_type(t_type) || (flags & ~REPRO_DISTILL_LOGPROBS))
+        return REPRO_ERR_ARG;
+    if (n == 0)
+        return REPRO_OK;
+    if (!loss || !stats || (K > 0 && !t_val))
+        return REPRO_ERR_ARG;
+    if (!aligned_to(t_val, type_bytes(t_type)) || !al4(loss) || !al4(stats))
+        return REPRO_ERR_ALIGN;
+    const size_t need = distill_ws_bytes(n, V);
+    if (!ws || ws_bytes < need)
+        return REPRO_ERR_WORKSPACE;
+    if (!al16(ws))
+        return REPRO_ERR_ALIGN;
+    if (any_overlap({{loss, (size_t)n * 4}, {stats, (size_t)(n * (REPRO_DISTILL_STATS + K)) * 4}, {ws, need}},
+                    {{z, row_span(n, z_ld, V) * type_bytes(z_type)}, {t_idx, (size_t)(n * K) * index_bytes},
+                     {t_val, (size_t)(n * K) * type_bytes(t_type)}, {labels, (size_t)n * index_bytes}}))
+        return REPRO_ERR_ALIAS;
+    st = check_arch();
+    if (st != REPRO_OK)
+        return st;
+    if ((st = scan_rows(stream, z, z_type, n, V, z_ld)) != REPRO_OK)
+        return st;
+    DistillArgs a = {};
+    a.z = z;
+    a.z_type = z_type;
+    a.z_ld = z_ld;
+    a.t_idx = t_idx;
+    a.t_val = t_val;
+    a.t_type = t_type;
+    a.labels = labels;
+    a.index_bytes = index_bytes;
+    a.n = n;
+    a.V = V;
+    a.K = K;
+    a.tau = hp->tau;
+    a.w_kd = flushed(hp->w_kd);
+    a.w_ce = flushed(hp->w_ce);
+    a.w_z = flushed(hp->w_z);
+    a.logprobs = (flags & REPRO_DISTILL_LOGPROBS) != 0;
+    a.loss = loss;
+    a.stats = stats;
+    a.err = device_error_word();
+    if (!a.err)
+        return REPRO_ERR_LAUNCH;
+    return status_of(launch_distill_fwd(a, ws, as_stream(stream)));
+}
+
+int repro_distill_bwd(const void* z, int z_type, int64_t z_ld, const void* t_idx, const void* labels,
+                      int index_bytes, int64_t n, int64_t V, int64_t K, const repro_distill_hparams* hp,
+                      const float* stats, const float* g, int64_t g_n, void* dz, int64_t dz_ld, void* stream)
+{
+    int st = check_distill(z, z_type, z_ld, t_idx, labels, index_bytes, n, V, K, hp);
+    if (st != REPRO_OK)
+        return st;
+    if (dz_ld < V || !rows_fit(n, dz_ld, V))
+        return REPRO_ERR_SHAPE;
+    if (n == 0)
+        return REPRO_OK;
+    if (!stats || !g || !dz || (g_n != 1 && g_n != n))
+        return REPRO_ERR_ARG;
+    const size_t b = type_bytes(z_type);
+    if (!al4(stats) || !al4(g) || !aligned_to(dz, b))
+        return REPRO_ERR_ALIGN;
+    const Span out = {dz, row_span(n, dz_ld, V) * b};
+    if (any_overlap({out}, {{t_idx, (size_t)(n * K) * index_bytes}, {labels, (size_t)n * index_bytes},
+                            {stats, (size_t)(n * (REPRO_DISTILL_STATS + K)) * 4}, {g, (size_t)g_n * 4}}))
+        return REPRO_ERR_ALIAS;
+    if (!(dz == z && dz_ld == z_ld) && overlap(dz, out.bytes, z, row_span(n, z_ld, V) * b))
+        return REPRO_ERR_ALIAS;
+    st = check_arch();
+    if (st != REPRO_OK)
+        return st;
+    if ((st = scan_rows(stream, z, z_type, n, V, z_ld)) != REPRO_OK ||
+        (st = scan_inputs(stream, {{g, g_n}})) != REPRO_OK)
+        return st;
+    DistillArgs a = {};
+    a.z = z;
+    a.z_type = z_type;
+    a.z_ld = z_ld;
+    a.t_idx = t_idx;
+    a.labels = labels;
+    a.index_bytes = index_bytes;
+    a.n = n;
+    a.V = V;
+    a.K = K;
+    a.tau = hp->tau;
+    a.w_kd = flushed(hp->w_kd);
+    a.w_ce = flushed(hp->w_ce);
+    a.w_z = flushed(hp->w_z);
+    a.stats = const_cast<float*>(stats);
+    a.g = g;
+    a.g_stride = g_n == 1 ? 0 : 1;
+    a.dz = dz;
+    a.dz_ld = dz_ld;
+    return status_of(launch_distill_bwd(a, as_stream(stream)));
 }
 
 size_t repro_state_hash_ws_bytes(const int64_t* nbytes, int nbuf)

@@ -32,8 +32,9 @@ struct FloatSpan {
 int scan_inputs(void* stream, std::initializer_list<FloatSpan> spans);
 int num_sms();
 int* device_error_word();   // device address of the error word: bit 0 a bounded wait gave up,
-                            // bit 1 the debug scan found a non-finite input
-constexpr int kErrTimeoutBit = 1, kErrNonfiniteBit = 2;
+                            // bit 1 the debug scan found a non-finite input,
+                            // bit 2 a token, position, index or label out of range
+constexpr int kErrTimeoutBit = 1, kErrNonfiniteBit = 2, kErrIndexBit = 4;
 int arch_status();          // REPRO_OK when the current device is a GB300
 void count_launches(int k); // adds k to the process-wide launch counter
 // status code of a CUDA runtime result, the same for every entry point
@@ -120,6 +121,113 @@ cudaError_t launch_check_finite(const float* p, int64_t n, int* err, cudaStream_
 // ---- forward exactness self-test (k_selftest.cu)
 size_t selftest_ws_bytes();
 int run_selftest(void* ws, cudaStream_t st);
+
+// ---- embedding (k_embed.cu); types as REPRO_F32, REPRO_BF16, REPRO_I8
+struct EmbedFwdArgs {
+    const void* table;
+    int table_type;
+    int64_t table_ld;
+    const float* s_w;
+    const void* tokens;
+    int index_bytes;
+    int64_t n, V, D;
+    float scale;
+    int64_t pad;
+    void* out;
+    int out_type;
+    int64_t out_ld;
+    int* err;
+};
+cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, cudaStream_t st);
+struct EmbedBwdArgs {
+    const void* dout;
+    int dout_type;
+    int64_t dout_ld;
+    const void* tokens;
+    int index_bytes;
+    int64_t n, V, D;
+    float scale;
+    int64_t pad;
+    float* table;
+    int64_t table_ld;
+    bool accumulate;
+    int* err;
+};
+size_t embed_bwd_ws_bytes(int64_t n, int64_t D);
+cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st);
+
+// ---- pairwise tree over partial rows (k_rowtree.cu), shared by the table's and the gains' gradients
+struct RowTree {
+    float* parts;        // partial rows, `pitch` floats apart (used as scratch)
+    int64_t pitch;
+    const int4* joins;   // {first sorted index, chunks, output row, 0}, or NULL: one join over
+                         // `count` consecutive partial rows
+    const int* njoins;   // device count of joins
+    int64_t count;
+    int64_t D;
+    float* out;
+    int64_t out_ld;
+    float scale;         // applied to the sum (1: leaves it)
+    bool accumulate;     // out (+) the scaled sum
+};
+cudaError_t launch_row_tree(const RowTree& t, int max_ctas, cudaStream_t st);
+
+// ---- norm of query and key heads with the rotation (k_qknorm.cu)
+struct QkTensor {        // one of q, k
+    const void* x;
+    int64_t ld, hs;      // token and head strides
+    int64_t H;
+    const float* gain;
+    float* out;          // forward: [n][H][D]
+    const float* dout;   // backward: [n][H][D]
+    void* dx;
+    int64_t dx_ld, dx_hs;
+    float* dgain;
+};
+struct QkArgs {
+    QkTensor t[2];
+    int type;
+    const float* rope;
+    int64_t P;
+    const int32_t* positions;
+    int64_t T;
+    float eps;
+    int64_t n, D, R;
+    bool interleaved, accumulate;
+    int* err;
+};
+cudaError_t launch_qk_fwd(const QkArgs& a, cudaStream_t st);
+size_t qk_bwd_ws_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64_t D);
+cudaError_t launch_qk_bwd(const QkArgs& a, void* ws, cudaStream_t st);
+
+// ---- loss against a teacher's top logits (k_distill.cu)
+struct DistillArgs {
+    const void* z;
+    int z_type;
+    int64_t z_ld;
+    const void* t_idx;
+    const void* t_val;
+    int t_type;
+    const void* labels;
+    int index_bytes;
+    int64_t n, V, K;
+    float tau, w_kd, w_ce, w_z;
+    bool logprobs;
+    float* loss;
+    float* stats;
+    const float* g;
+    int64_t g_stride;
+    void* dz;
+    int64_t dz_ld;
+    int* err;
+};
+size_t distill_ws_bytes(int64_t n, int64_t V);
+cudaError_t launch_distill_fwd(const DistillArgs& a, void* ws, cudaStream_t st);
+cudaError_t launch_distill_bwd(const DistillArgs& a, cudaStream_t st);
+
+// ---- debug scan of strided rows (k_rowtree.cu): n rows of D elements of `type`, ld apart
+cudaError_t launch_check_finite_rows(const void* p, int type, int64_t n, int64_t D, int64_t ld, int* err,
+                                     cudaStream_t st);
 
 // ---- state hash (k_hash.cu)
 int64_t hash_leaf_count(const int64_t* nbytes, int nbuf, int64_t leaf_bytes);

@@ -1,0 +1,553 @@
+// k_embed.cu -- token embedding with a scale, and the table's gradient in a
+// fixed order.
+//
+// Forward: out_i = W[tok_i] (x) scale.  One read of the distinct rows, one write
+// of n x D: bound by HBM.  A warp takes a 512-column piece of one row, four
+// 4-element groups per lane in flight, so that a wide row spreads over several
+// warps and few tokens over many SMs.
+//
+// Backward: dW_v = canonical sum over {i : tok_i = v}, i ascending, of dout_i,
+// (x) scale.  An atomic add per element would be shorter and its order, so its
+// bits, would change from run to run; here the positions are sorted by token
+// (stably, so ascending within a token) and every table element is summed by one
+// thread in the canonical order:
+//   1. k_embed_sort: one cluster of 8 CTAs sorts (token, position) by 8 bits a
+//      pass and lists the chunks of up to 64 positions.  The other clusters of the
+//      same launch zero the table rows that no token names (each marks its own
+//      rows' tokens in a bitmap first), so the sort hides behind the
+//      part of the write that needs no order.
+//   2. k_embed_sum: one warp per (chunk, 256 columns), left to right from the
+//      first term; a token's only chunk is scaled and stored, others leave their
+//      partial row in the workspace.
+//   3. k_row_tree (k_rowtree.cu): the pairwise tree over a token's partial rows;
+//      only launched when n > 64, below which no token can have two chunks.
+#include <cooperative_groups.h>
+
+#include "elem.cuh"
+#include "internal.h"
+#include "launch.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace repro {
+namespace {
+
+// ---------------------------------------------------------------- forward
+
+constexpr int EF_U = 4;            // 4-element groups per lane
+constexpr int EF_COLS = 32 * 4 * EF_U;
+
+__device__ __forceinline__ float4 table4(const float* p, float) { return flush4(load4(p)); }
+__device__ __forceinline__ float4 table4(const __nv_bfloat16* p, float) { return flush4(load4(p)); }
+__device__ __forceinline__ float4 table4(const int8_t* p, float s)
+{
+    const char4 q = *reinterpret_cast<const char4*>(p);
+    return make_float4(dequant((signed char)q.x, s), dequant((signed char)q.y, s),
+                       dequant((signed char)q.z, s), dequant((signed char)q.w, s));
+}
+__device__ __forceinline__ float table1(const float* p, float) { return flush(*p); }
+__device__ __forceinline__ float table1(const __nv_bfloat16* p, float) { return flush(__bfloat162float(*p)); }
+__device__ __forceinline__ float table1(const int8_t* p, float s) { return dequant(*p, s); }
+
+template <typename TT, typename TO, bool VEC>
+__global__ void __launch_bounds__(256)
+k_embed_fwd(const TT* __restrict__ table, int64_t table_ld, const float* __restrict__ s_w,
+            const void* __restrict__ tokens, int index_bytes, int64_t n, int64_t V, int64_t D,
+            float scale, int64_t pad, TO* __restrict__ out, int64_t out_ld, int segs, int* err)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (item >= n * segs)
+        return;
+    const int64_t row = item / segs;
+    const int64_t c0 = (item - row * segs) * EF_COLS;
+    const int64_t tok = load_index(tokens, index_bytes, row);
+    const bool ok = tok >= 0 && tok < V && tok != pad;
+    if (!ok && tok != pad && c0 == 0 && lane == 0)
+        atomicOr(err, kErrIndexBit);
+    const float sw = s_w ? flush(*s_w) : 0.0f;
+    const float sc = flush(scale);
+    const TT* src = table + (ok ? tok : 0) * table_ld;
+    TO* dst = out + row * out_ld;
+    if (VEC) {
+        float4 v[EF_U];
+#pragma unroll
+        for (int u = 0; u < EF_U; ++u) {
+            const int64_t c = c0 + 4 * (lane + 32 * u);
+            if (c < D)
+                v[u] = ok ? table4(src + c, sw) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int u = 0; u < EF_U; ++u) {
+            const int64_t c = c0 + 4 * (lane + 32 * u);
+            if (c < D) {
+                float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (ok)
+                    r = make_float4(fmul_flush(v[u].x, sc), fmul_flush(v[u].y, sc),
+                                    fmul_flush(v[u].z, sc), fmul_flush(v[u].w, sc));
+                store4(dst + c, r);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4 * EF_U; ++u) {
+            const int64_t c = c0 + lane + 32 * u;
+            if (c < D)
+                dst[c] = from_f32<TO>(ok ? fmul_flush(table1(src + c, sw), sc) : 0.0f);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- sort
+
+constexpr int SORT_CTAS = 8;      // CTAs of the sorting cluster
+constexpr int SORT_NT = 1024;
+constexpr int SORT_W = SORT_NT / 32;
+constexpr int DIGITS = 256;
+
+struct SortArgs {
+    const void* tokens;
+    int index_bytes;
+    int n, V;
+    int passes;
+    int64_t pad;
+    uint2* a;            // (token, position), written by passes 0, 2, ..
+    uint2* b;            // .. and by passes 1, 3
+    int* counts;         // [0] chunks listed, [1] tokens with several chunks
+    int4* chunks;        // {first sorted index, length, token, partial row or -1}
+    int4* joins;         // {first sorted index, chunks, token, 0}
+    float* table;        // rows to zero, or NULL
+    int64_t table_ld;
+    int64_t D;
+    bool vec;            // the table's rows begin on 16 bytes
+    int* err;
+};
+
+struct SortSmem {
+    unsigned hist[SORT_W][DIGITS];   // per warp, then its running offsets
+    unsigned total[DIGITS];          // this CTA's digit counts (read by the cluster)
+    unsigned warp_total[DIGITS / 32];
+};
+
+__device__ __forceinline__ unsigned sort_key(const SortArgs& a, int i, bool report)
+{
+    const int64_t t = load_index(a.tokens, a.index_bytes, i);
+    if (t >= 0 && t < a.V && t != a.pad)
+        return (unsigned)t;
+    if (report && t != a.pad)
+        atomicOr(a.err, kErrIndexBit);
+    return (unsigned)a.V;
+}
+
+__device__ __forceinline__ uint2 ld_pair(const uint2* p) { return __ldcg(p); }
+__device__ __forceinline__ unsigned ld_tok(const uint2* s, int i) { return __ldcg(&s[i].x); }
+
+// first index in [0, hi] whose token is >= key, given that s[hi] has it
+__device__ int lower_bound(const uint2* s, int hi, unsigned key)
+{
+    int lo = 0;
+    while (lo < hi) {
+        const int m = (lo + hi) >> 1;
+        if (ld_tok(s, m) < key)
+            lo = m + 1;
+        else
+            hi = m;
+    }
+    return lo;
+}
+
+// one past the last index of `key`, given that s[lo] has it
+__device__ int upper_bound(const uint2* s, int lo, int hi, unsigned key)
+{
+    while (lo < hi) {
+        const int m = (lo + hi) >> 1;
+        if (ld_tok(s, m) <= key)
+            lo = m + 1;
+        else
+            hi = m;
+    }
+    return lo;
+}
+
+__device__ void sort_cluster(const SortArgs& a, SortSmem& sm)
+{
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // each warp owns a run of 32-element rounds, so that (CTA, warp, round, lane) is position order
+    const int rounds = (a.n + SORT_CTAS * SORT_NT - 1) / (SORT_CTAS * SORT_NT);
+    const int base = (rank * SORT_W + warp) * rounds * 32;
+    if (rank == 0 && tid < 2)
+        a.counts[tid] = 0;
+    const uint2* src = nullptr;
+    uint2* dst = a.a;
+    for (int pass = 0; pass < a.passes; ++pass) {
+        const int shift = 8 * pass;
+        for (int i = tid; i < SORT_W * DIGITS; i += SORT_NT)
+            (&sm.hist[0][0])[i] = 0;
+        __syncthreads();
+        for (int r = 0; r < rounds; ++r) {
+            const int i = base + 32 * r + lane;
+            const bool in = i < a.n;
+            const unsigned key = !in ? 0u : pass == 0 ? sort_key(a, i, true) : ld_tok(src, i);
+            const unsigned d = in ? (key >> shift) & (DIGITS - 1) : (unsigned)DIGITS;
+            const unsigned same = __match_any_sync(0xffffffffu, d);
+            if (in && lane == __ffs(same) - 1)
+                sm.hist[warp][d] += __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        if (tid < DIGITS) {
+            unsigned run = 0;
+            for (int w = 0; w < SORT_W; ++w) {
+                const unsigned c = sm.hist[w][tid];
+                sm.hist[w][tid] = run;
+                run += c;
+            }
+            sm.total[tid] = run;
+        }
+        cluster.sync();
+        if (tid < DIGITS) {
+            unsigned before = 0, all = 0;
+            for (int r = 0; r < SORT_CTAS; ++r) {
+                const unsigned c = cluster.map_shared_rank(&sm, r)->total[tid];
+                before += r < rank ? c : 0u;
+                all += c;
+            }
+            // exclusive scan of the digit counts: within warps, then over the 8 warps
+            unsigned inc = all;
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned up = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o)
+                    inc += up;
+            }
+            if (lane == 31)
+                sm.warp_total[warp] = inc;
+            asm volatile("bar.sync 1, 256;" ::: "memory");   // the eight warps that hold the digits
+            unsigned off = 0;
+            for (int w = 0; w < warp; ++w)
+                off += sm.warp_total[w];
+            const unsigned start = inc - all + off + before;
+            for (int w = 0; w < SORT_W; ++w)
+                sm.hist[w][tid] += start;
+        }
+        __syncthreads();
+        for (int r = 0; r < rounds; ++r) {
+            const int i = base + 32 * r + lane;
+            const bool in = i < a.n;
+            uint2 kv = make_uint2(0u, 0u);
+            if (in)
+                kv = pass == 0 ? make_uint2(sort_key(a, i, false), (unsigned)i) : ld_pair(src + i);
+            const unsigned d = in ? (kv.x >> shift) & (DIGITS - 1) : (unsigned)DIGITS;
+            const unsigned same = __match_any_sync(0xffffffffu, d);
+            unsigned at = 0;
+            if (in)
+                at = sm.hist[warp][d] + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (in) {
+                dst[at] = kv;
+                if (lane == __ffs(same) - 1)
+                    sm.hist[warp][d] += __popc(same);
+            }
+            __syncwarp();
+        }
+        __threadfence();
+        cluster.sync();   // the scattered pairs are visible to the cluster, and total[] free again
+        src = dst;
+        dst = dst == a.a ? a.b : a.a;
+    }
+    // the chunks: sorted index i starts one when it is a multiple of 64 past its token's first
+    for (int i = rank * SORT_NT + tid; i < a.n; i += SORT_CTAS * SORT_NT) {
+        const unsigned key = ld_tok(src, i);
+        if (key >= (unsigned)a.V)
+            continue;
+        int first = i;
+        if (i > 0 && ld_tok(src, i - 1) == key) {
+            if (i < 64 || ld_tok(src, i - 64) != key)
+                continue;
+            first = lower_bound(src, i, key);
+            if ((i - first) & 63)
+                continue;
+        }
+        const int hi = i + 64 < a.n ? i + 64 : a.n;
+        const int end = ld_tok(src, hi - 1) == key ? hi : upper_bound(src, i, hi, key);
+        const bool several = first != i || (end == i + 64 && end < a.n && ld_tok(src, end) == key);
+        // a partial row of its own: in a run of 64 sorted indexes at most one chunk of a
+        // token with several starts that is its first, and at most one that is not
+        const int slot = several ? 2 * (i >> 6) + (first == i ? 1 : 0) : -1;
+        a.chunks[atomicAdd(&a.counts[0], 1)] = make_int4(i, end - i, (int)key, slot);
+        if (several && first == i)
+            a.joins[atomicAdd(&a.counts[1], 1)] =
+                make_int4(i, (upper_bound(src, i, a.n, key) - i + 63) / 64, (int)key, 0);
+    }
+}
+
+// zero the table rows in [v0, v1) that no token names
+__device__ void zero_rows(const SortArgs& a, unsigned* bits, int v0, int v1)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int words = (v1 - v0 + 31) / 32;
+    for (int i = tid; i < words; i += SORT_NT)
+        bits[i] = 0u;
+    __syncthreads();
+    for (int i = tid; i < a.n; i += SORT_NT) {
+        const int64_t t = load_index(a.tokens, a.index_bytes, i);
+        if (t >= v0 && t < v1 && t != a.pad)
+            atomicOr(&bits[(t - v0) >> 5], 1u << ((t - v0) & 31));
+    }
+    __syncthreads();
+    for (int v = v0 + warp; v < v1; v += SORT_W) {
+        if (bits[(v - v0) >> 5] >> ((v - v0) & 31) & 1u)
+            continue;
+        float* row = a.table + (int64_t)v * a.table_ld;
+        if (a.vec) {
+            for (int64_t c = 4 * lane; c < a.D; c += 128)
+                store4(row + c, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        } else {
+            for (int64_t c = lane; c < a.D; c += 32)
+                row[c] = 0.0f;
+        }
+    }
+}
+
+__global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_NT, 1)
+k_embed_sort(const SortArgs a)
+{
+    extern __shared__ unsigned dyn[];
+    if (blockIdx.x < SORT_CTAS) {
+        sort_cluster(a, *reinterpret_cast<SortSmem*>(dyn));
+    } else {
+        const int ctas = gridDim.x - SORT_CTAS, c = blockIdx.x - SORT_CTAS;
+        const int per = (a.V + ctas - 1) / ctas;
+        const int64_t v0 = (int64_t)c * per, v1 = v0 + per < a.V ? v0 + per : a.V;
+        if (v0 < v1)
+            zero_rows(a, dyn, (int)v0, (int)v1);
+    }
+}
+
+// ---------------------------------------------------------------- chunk sums
+
+constexpr int ES_G = 2;             // 4-element groups per lane
+constexpr int ES_COLS = 32 * 4 * ES_G;
+constexpr int ES_U = 4;             // rows in flight
+
+template <typename TD>
+__global__ void __launch_bounds__(256)
+k_embed_sum(const TD* __restrict__ dout, int64_t dout_ld, const uint2* __restrict__ sorted,
+            const int* __restrict__ counts, const int4* __restrict__ chunks, int64_t D, float scale,
+            float* __restrict__ table, int64_t table_ld, bool accumulate, float* __restrict__ parts,
+            int segs, bool vec_in, bool vec_out)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t items = (int64_t)counts[0] * segs;
+    const float sc = flush(scale);
+    for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < items;
+         item += (int64_t)gridDim.x * 8) {
+        const int64_t ch = item / segs;
+        const int4 c = chunks[ch];
+        const int64_t c0 = (item - ch * segs) * ES_COLS;
+        // positions of the chunk's rows, one or two per lane
+        const unsigned p0 = lane < c.y ? sorted[c.x + lane].y : 0u;
+        const unsigned p1 = lane + 32 < c.y ? sorted[c.x + lane + 32].y : 0u;
+        float acc[ES_G][4];
+        // column of group g, element e: four neighbours, or lane-strided when rows are unaligned
+        auto col = [&](int g, int e) {
+            return c0 + (vec_in ? 4 * (lane + 32 * g) + e : lane + 32 * (4 * g + e));
+        };
+        auto row = [&](int j, float (&x)[ES_G][4]) {
+            const unsigned pos = __shfl_sync(0xffffffffu, j < 32 ? p0 : p1, j & 31);
+            const TD* s = dout + (int64_t)pos * dout_ld;
+#pragma unroll
+            for (int g = 0; g < ES_G; ++g) {
+                if (vec_in) {
+                    if (col(g, 0) < D) {
+                        const float4 v = load4(s + col(g, 0));
+                        x[g][0] = v.x, x[g][1] = v.y, x[g][2] = v.z, x[g][3] = v.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col(g, e) < D)
+                            x[g][e] = to_f32<TD>(s[col(g, e)]);
+                }
+            }
+        };
+        float x[ES_U][ES_G][4] = {};
+        row(0, x[0]);
+#pragma unroll
+        for (int g = 0; g < ES_G; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[g][e] = flush(x[0][g][e]);
+        int j = 1;
+        for (; j + ES_U <= c.y; j += ES_U) {
+#pragma unroll
+            for (int u = 0; u < ES_U; ++u)
+                row(j + u, x[u]);
+#pragma unroll
+            for (int u = 0; u < ES_U; ++u)
+#pragma unroll
+                for (int g = 0; g < ES_G; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[g][e] = fadd_ftz(acc[g][e], x[u][g][e]);
+        }
+        for (; j < c.y; ++j) {
+            row(j, x[0]);
+#pragma unroll
+            for (int g = 0; g < ES_G; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[g][e] = fadd_ftz(acc[g][e], x[0][g][e]);
+        }
+        const bool part = c.w >= 0;
+        float* dst = part ? parts + (int64_t)c.w * ((D + 3) & ~3LL) : table + (int64_t)c.z * table_ld;
+#pragma unroll
+        for (int g = 0; g < ES_G; ++g) {
+            if (!part) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[g][e] = fmul_flush(acc[g][e], sc);
+                    if (accumulate && col(g, e) < D)
+                        acc[g][e] = fadd_ftz(dst[col(g, e)], acc[g][e]);
+                }
+            }
+            if (vec_in && (part || vec_out)) {
+                if (col(g, 0) < D)
+                    store4(dst + col(g, 0), make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col(g, e) < D)
+                        dst[col(g, e)] = acc[g][e];
+            }
+        }
+    }
+}
+
+// workspace: sorted pairs twice, chunk and join lists, counters, partial rows
+struct EmbedWs {
+    size_t a, b, chunks, joins, counts, parts, total;
+};
+
+EmbedWs embed_ws(int64_t n, int64_t D)
+{
+    EmbedWs w;
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    const int64_t blocks = (n + 63) / 64;
+    w.a = 0;
+    w.b = w.a + up((size_t)n * 8);
+    w.chunks = w.b + up((size_t)n * 8);
+    w.joins = w.chunks + up((size_t)n * 16);
+    w.counts = w.joins + up((size_t)blocks * 16);
+    w.parts = w.counts + 256;
+    // a token with several chunks has more than 64 positions
+    w.total = w.parts + (n > 64 ? (size_t)(2 * blocks) * (size_t)((D + 3) & ~3LL) * 4 : 0);
+    return w;
+}
+
+template <typename TT, typename TO>
+cudaError_t fwd_typed(const EmbedFwdArgs& a, cudaStream_t st)
+{
+    const int segs = (int)((a.D + EF_COLS - 1) / EF_COLS);
+    const int64_t ctas = (a.n * segs + 7) / 8;
+    const bool vec = a.D % 4 == 0 && rows4<TT>(a.table, a.table_ld) && rows4<TO>(a.out, a.out_ld);
+    const TT* table = static_cast<const TT*>(a.table);
+    TO* out = static_cast<TO*>(a.out);
+    auto go = [&](auto kernel) {
+        kernel<<<(unsigned)ctas, 256, 0, st>>>(table, a.table_ld, a.s_w, a.tokens, a.index_bytes, a.n, a.V,
+                                               a.D, a.scale, a.pad, out, a.out_ld, segs, a.err);
+    };
+    if (vec)
+        go(k_embed_fwd<TT, TO, true>);
+    else
+        go(k_embed_fwd<TT, TO, false>);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, cudaStream_t st)
+{
+    const bool of = a.out_type == 0;
+    switch (a.table_type) {
+    case 0: return of ? fwd_typed<float, float>(a, st) : fwd_typed<float, __nv_bfloat16>(a, st);
+    case 1: return of ? fwd_typed<__nv_bfloat16, float>(a, st) : fwd_typed<__nv_bfloat16, __nv_bfloat16>(a, st);
+    default: return of ? fwd_typed<int8_t, float>(a, st) : fwd_typed<int8_t, __nv_bfloat16>(a, st);
+    }
+}
+
+size_t embed_bwd_ws_bytes(int64_t n, int64_t D) { return embed_ws(n, D).total; }
+
+cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
+{
+    const EmbedWs w = embed_ws(a.n, a.D);
+    char* p = static_cast<char*>(ws);
+    SortArgs s;
+    s.tokens = a.tokens;
+    s.index_bytes = a.index_bytes;
+    s.n = (int)a.n;
+    s.V = (int)a.V;
+    s.pad = a.pad;
+    s.a = reinterpret_cast<uint2*>(p + w.a);
+    s.b = reinterpret_cast<uint2*>(p + w.b);
+    s.chunks = reinterpret_cast<int4*>(p + w.chunks);
+    s.joins = reinterpret_cast<int4*>(p + w.joins);
+    s.counts = reinterpret_cast<int*>(p + w.counts);
+    s.table = a.table;
+    s.table_ld = a.table_ld;
+    s.D = a.D;
+    s.vec = a.D % 4 == 0 && rows4<float>(a.table, a.table_ld);
+    s.err = a.err;
+    s.passes = 1;
+    while (((int64_t)1 << (8 * s.passes)) <= a.V)   // keys 0 .. V
+        ++s.passes;
+    const uint2* sorted = (s.passes & 1) ? s.a : s.b;
+    const int fill = a.accumulate ? 0 : (num_sms() / SORT_CTAS - 1) * SORT_CTAS;
+    const int per = fill > 0 ? (int)((a.V + fill - 1) / fill) : 0;
+    size_t smem = sizeof(SortSmem);
+    if ((size_t)(per + 31) / 32 * 4 > smem)
+        smem = (size_t)(per + 31) / 32 * 4;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)smem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    k_embed_sort<<<SORT_CTAS + fill, SORT_NT, smem, st>>>(s);
+    count_launches(1);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || a.n == 0)
+        return e;
+    float* parts = reinterpret_cast<float*>(p + w.parts);
+    const int segs = (int)((a.D + ES_COLS - 1) / ES_COLS);
+    const int64_t most = (a.n * segs + 7) / 8, cap = (int64_t)num_sms() * 8;
+    const unsigned grid = (unsigned)(most < cap ? most : cap);
+    const bool vec_out = s.vec;
+    auto sum = [&](auto kernel, auto type) {
+        using T = decltype(type);
+        const bool vec_in = a.D % 4 == 0 && rows4<T>(a.dout, a.dout_ld);
+        return launch_pdl(kernel, dim3(grid), dim3(256), 0, st, static_cast<const T*>(a.dout), a.dout_ld,
+                          sorted, (const int*)s.counts, (const int4*)s.chunks, a.D, a.scale, a.table,
+                          a.table_ld, a.accumulate, parts, segs, vec_in, vec_out);
+    };
+    e = a.dout_type == 0 ? sum(k_embed_sum<float>, float()) : sum(k_embed_sum<__nv_bfloat16>, __nv_bfloat16());
+    count_launches(1);
+    if (e != cudaSuccess || a.n <= 64)
+        return e;
+    RowTree t;
+    t.parts = parts;
+    t.pitch = (a.D + 3) & ~3LL;
+    t.joins = s.joins;
+    t.njoins = s.counts + 1;
+    t.D = a.D;
+    t.out = a.table;
+    t.out_ld = a.table_ld;
+    t.scale = a.scale;
+    t.accumulate = a.accumulate;
+    return launch_row_tree(t, num_sms() * 2, st);
+}
+
+} // namespace repro

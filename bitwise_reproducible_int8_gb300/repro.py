@@ -20,16 +20,25 @@ STATUS_NAMES = {
     0: "REPRO_OK", -1: "REPRO_ERR_ARG", -2: "REPRO_ERR_SHAPE", -3: "REPRO_ERR_ALIGN",
     -4: "REPRO_ERR_ARCH", -5: "REPRO_ERR_LAUNCH", -6: "REPRO_ERR_TIMEOUT",
     -7: "REPRO_ERR_WORKSPACE", -8: "REPRO_ERR_ALIAS", -9: "REPRO_ERR_SELFTEST",
-    -10: "REPRO_ERR_NONFINITE",
+    -10: "REPRO_ERR_NONFINITE", -11: "REPRO_ERR_INDEX",
 }
 REPRO_ERR_TIMEOUT = -6
 REPRO_ERR_NONFINITE = -10
+REPRO_ERR_INDEX = -11
 REPRO_DEBUG_CHECK_FINITE = 1
 REPRO_SCALE_WEIGHT_MEANABS = 0
 REPRO_SCALE_ACT_AMAX = 1
 REPRO_BWD_DW_ACCUMULATE = 1
 REPRO_QMAX = 127
 REPRO_MAX_REPLICAS = 64
+REPRO_F32, REPRO_BF16, REPRO_I8 = 0, 1, 2
+REPRO_EMBED_MAX_V = 16777215
+REPRO_QK_INTERLEAVED = 2
+REPRO_QK_MAX_D = 512
+REPRO_DISTILL_BLOCK = 1024
+REPRO_DISTILL_STATS = 8
+REPRO_DISTILL_STAT_LSE = 2
+REPRO_DISTILL_LOGPROBS = 1
 
 
 class ReproError(RuntimeError):
@@ -42,6 +51,10 @@ class ReproError(RuntimeError):
 class AdamWHparams(ctypes.Structure):
     _fields_ = [(k, ctypes.c_float) for k in
                 ("lr", "beta1", "beta2", "eps", "weight_decay", "max_norm")]
+
+
+class DistillHparams(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_float) for k in ("tau", "w_kd", "w_ce", "w_z")]
 
 
 class LaunchCfg(ctypes.Structure):
@@ -86,6 +99,22 @@ _SIGNATURES = {
     "repro_attn_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
                               _i64, _i64, _i64, _i64, _vp, _sz, _vp, _sz, _vp]),
     "repro_attn_bwd_ws_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "repro_embed_fwd": (_int, [_vp, _int, _i64, _vp, _vp, _int, _i64, _i64, _i64, ctypes.c_float, _i64,
+                               _vp, _int, _i64, _vp]),
+    "repro_embed_bwd": (_int, [_vp, _int, _i64, _vp, _int, _i64, _i64, _i64, ctypes.c_float, _i64, _vp,
+                               _i64, _int, _vp, _sz, _vp]),
+    "repro_embed_bwd_ws_bytes": (_sz, [_i64, _i64, _i64]),
+    "repro_qk_norm_rope_fwd": (_int, [_vp, _i64, _i64, _vp, _i64, _i64, _int, _vp, _vp, _vp, _i64, _vp, _i64,
+                                      ctypes.c_float, _i64, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp]),
+    "repro_qk_norm_rope_bwd": (_int, [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _int, _vp, _vp, _vp, _i64,
+                                      _vp, _i64, ctypes.c_float, _i64, _i64, _i64, _i64, _i64, _int, _vp, _i64,
+                                      _i64, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "repro_qk_norm_rope_bwd_ws_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "repro_distill_fwd": (_int, [_vp, _int, _i64, _vp, _vp, _int, _vp, _int, _i64, _i64, _i64,
+                                 ctypes.POINTER(DistillHparams), _int, _vp, _vp, _vp, _sz, _vp]),
+    "repro_distill_ws_bytes": (_sz, [_i64, _i64]),
+    "repro_distill_bwd": (_int, [_vp, _int, _i64, _vp, _vp, _int, _i64, _i64, _i64,
+                                 ctypes.POINTER(DistillHparams), _vp, _vp, _i64, _vp, _i64, _vp]),
     "repro_selftest": (_int, [_vp, _sz, _vp]),
     "repro_selftest_ws_bytes": (_sz, []),
     "repro_status_str": (ctypes.c_char_p, [_int]),
@@ -350,6 +379,245 @@ def repro_attn_bwd(q, k, vq, s_v, o, dout, m, l, dq, dk, dv, W: int = 0, ws=None
         _ptr(dq, f32, "dq"), _ptr(dk, f32, "dk"), _ptr(dv, f32, "dv"), B, T, Hq, Hkv, D, int(W),
         _ptr(ws, None, "ws"), ws.numel() * ws.element_size(), _ptr(fwd_ws, None, "fwd_ws"),
         fwd_ws.numel() * fwd_ws.element_size() if fwd_ws is not None else 0, _stream(stream)))
+
+
+_FLOAT_TYPES = {torch.float32: REPRO_F32, torch.bfloat16: REPRO_BF16}
+
+
+def _dev_ptr(t, name, contiguous=True):
+    """Data pointer of a CUDA tensor (None: NULL)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _float_type(t, name) -> int:
+    if t.dtype not in _FLOAT_TYPES:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return _FLOAT_TYPES[t.dtype]
+
+
+def _index_bytes(name, *ts) -> int:
+    kinds = {t.dtype for t in ts if t is not None}
+    if len(kinds) > 1 or not kinds <= {torch.int32, torch.int64}:
+        raise ValueError(f"{name} must be int32 or int64 (all of one type)")
+    return 4 if kinds == {torch.int32} else 8
+
+
+def _rows2d(t, name):
+    """(rows, width, row stride) of a matrix, or of an array whose leading
+    dimensions collapse into one; elements of a row adjacent."""
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have at least two dimensions")
+    D = t.shape[-1]
+    if D > 1 and t.stride(-1) != 1 and t.numel() > 0:
+        raise ValueError(f"{name}: the elements of a row must be adjacent")
+    n, ld = 1, None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = stride
+        elif t.numel() > 0 and stride != ld * n:
+            raise ValueError(f"{name}: the rows must lie at one stride")
+        n *= size
+    return n, D, D if ld is None else int(ld)
+
+
+def repro_embed_fwd(table: torch.Tensor, tokens: torch.Tensor, out: torch.Tensor, scale: float = 1.0,
+                    s_w=None, pad: int = -1, stream=None) -> None:
+    """out[..., D] <- table[tokens] (x) scale; +0 rows where a token equals pad.
+    table [V, D] float32, bfloat16, or int8 codes with their scale s_w [1]; rows
+    of table and out at any stride; tokens int32 or int64."""
+    V, D, table_ld = _rows2d(table, "table")
+    n, D2, out_ld = _rows2d(out, "out")
+    if D2 != D or n != tokens.numel():
+        raise ValueError("shape mismatch: table [V, D], out [..., D] with a row per token")
+    if table.dtype == torch.int8:
+        if s_w is None:
+            raise ValueError("an int8 table needs its scale s_w")
+        kind = REPRO_I8
+    else:
+        kind = _float_type(table, "table")
+    _check("repro_embed_fwd", lib().repro_embed_fwd(
+        _dev_ptr(table, "table", False), kind, table_ld, _ptr(s_w, torch.float32, "s_w"),
+        _dev_ptr(tokens, "tokens"), _index_bytes("tokens", tokens), n, V, D, float(scale), int(pad),
+        _dev_ptr(out, "out", False), _float_type(out, "out"), out_ld, _stream(stream)))
+
+
+def repro_embed_bwd_ws_bytes(n: int, V: int, D: int) -> int:
+    return int(lib().repro_embed_bwd_ws_bytes(int(n), int(V), int(D)))
+
+
+def repro_embed_bwd(dout: torch.Tensor, tokens: torch.Tensor, dtable: torch.Tensor, scale: float = 1.0,
+                    pad: int = -1, accumulate: bool = False, ws=None, stream=None) -> None:
+    """dtable [V, D] <- (or (+)=) the sum of dout's rows by token, in canonical
+    order over ascending positions, (x) scale."""
+    n, D, dout_ld = _rows2d(dout, "dout")
+    V, D2, dtable_ld = _rows2d(dtable, "dtable")
+    if D2 != D or n != tokens.numel():
+        raise ValueError("shape mismatch: dout [..., D] with a row per token, dtable [V, D]")
+    if dtable.dtype != torch.float32:
+        raise ValueError(f"dtable must be {torch.float32}, got {dtable.dtype}")
+    if ws is None:
+        ws = _workspace(repro_embed_bwd_ws_bytes(n, V, D), dtable.device)
+    _check("repro_embed_bwd", lib().repro_embed_bwd(
+        _dev_ptr(dout, "dout", False), _float_type(dout, "dout"), dout_ld, _dev_ptr(tokens, "tokens"),
+        _index_bytes("tokens", tokens), n, V, D, float(scale), int(pad), _dev_ptr(dtable, "dtable", False),
+        dtable_ld, REPRO_BWD_DW_ACCUMULATE if accumulate else 0, _dev_ptr(ws, "ws"),
+        ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def _heads(t, name):
+    """(tokens, heads, width, token stride, head stride) of [n, H, D] or [B, T, H, D]."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [n, H, D] or [B, T, H, D]")
+    H, D = t.shape[-2:]
+    if D > 1 and t.stride(-1) != 1 and t.numel() > 0:
+        raise ValueError(f"{name}: the elements of a head must be adjacent")
+    n, _, ld = _rows2d(t[..., 0, :], name) if H > 0 else (t.shape[:-2].numel(), D, D)
+    if n <= 1:
+        ld = max(ld, 1)
+    return n, H, D, ld, int(t.stride(-2)) if H > 1 else D
+
+
+def _qk_common(q, k, rope, g_q, g_k, positions):
+    n, Hq, D, q_ld, q_hs = _heads(q, "q")
+    kind = _float_type(q, "q")
+    Hkv, k_ld, k_hs = 0, D, D
+    if k is not None:
+        nk, Hkv, Dk, k_ld, k_hs = _heads(k, "k")
+        if nk != n or Dk != D or k.dtype != q.dtype:
+            raise ValueError("k must have q's tokens, width and type")
+    P, R = (rope.shape if rope is not None else (0, 0))
+    for g, name in ((g_q, "g_q"), (g_k, "g_k")):
+        if g is not None and g.numel() != D:
+            raise ValueError(f"{name} must have D elements")
+    if positions is not None and positions.numel() != n:
+        raise ValueError("positions must have an entry per token")
+    T = q.shape[1] if q.dim() == 4 else n
+    return n, Hq, D, q_ld, q_hs, Hkv, k_ld, k_hs, kind, P, R, max(int(T), 1)
+
+
+def repro_qk_norm_rope_fwd(q: torch.Tensor, k, rope, q_out: torch.Tensor, k_out, g_q=None, g_k=None,
+                           positions=None, eps: float = 1e-6, interleaved: bool = False,
+                           stream=None) -> None:
+    """q_out, k_out <- the RMS-normalised heads of q, k (gains g_q, g_k [D] if
+    given), turned by the positions' angles.  q [B, T, Hq, D] or [n, Hq, D], k the
+    same with its own heads (or None), float32 or bfloat16, at any token and head
+    strides; rope [P, R] float32, cosines then sines (None: no rotation);
+    positions int32 per token (None: 0 .. T - 1 in every sequence); outputs dense
+    float32."""
+    f32 = torch.float32
+    n, Hq, D, q_ld, q_hs, Hkv, k_ld, k_hs, kind, P, R, T = _qk_common(q, k, rope, g_q, g_k, positions)
+    if q_out.numel() != n * Hq * D or (k is not None and k_out.numel() != n * Hkv * D):
+        raise ValueError("outputs must have the inputs' sizes")
+    _check("repro_qk_norm_rope_fwd", lib().repro_qk_norm_rope_fwd(
+        _dev_ptr(q, "q", False), q_ld, q_hs, _dev_ptr(k, "k", False), k_ld, k_hs, kind,
+        _ptr(g_q, f32, "g_q"), _ptr(g_k, f32, "g_k"), _ptr(rope, f32, "rope"), P,
+        _ptr(positions, torch.int32, "positions"), T, float(eps), n, Hq, Hkv, D, R,
+        REPRO_QK_INTERLEAVED if interleaved else 0, _ptr(q_out, f32, "q_out"),
+        _ptr(k_out if k is not None else None, f32, "k_out"), _stream(stream)))
+
+
+def repro_qk_norm_rope_bwd_ws_bytes(n: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().repro_qk_norm_rope_bwd_ws_bytes(int(n), int(Hq), int(Hkv), int(D)))
+
+
+def repro_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out, q: torch.Tensor, k, rope, dq: torch.Tensor, dk,
+                           g_q=None, g_k=None, dg_q=None, dg_k=None, positions=None, eps: float = 1e-6,
+                           interleaved: bool = False, accumulate: bool = False, ws=None,
+                           stream=None) -> None:
+    """dq, dk (q's type, any token and head strides) and the gains' gradients
+    dg_q, dg_k [D] (added to with accumulate) from the gradients dq_out, dk_out
+    of the forward's outputs (dense float32) and the forward's inputs."""
+    f32 = torch.float32
+    n, Hq, D, q_ld, q_hs, Hkv, k_ld, k_hs, kind, P, R, T = _qk_common(q, k, rope, g_q, g_k, positions)
+    strides = []
+    for t, g, x, H, name in ((dq, dq_out, q, Hq, "q"), (dk, dk_out, k, Hkv, "k")):
+        if x is None:
+            strides.append((D, D))
+            continue
+        nd, Hd, Dd, ld, hs = _heads(t, "d" + name)
+        if (nd, Hd, Dd) != (n, H, D) or t.dtype != q.dtype or g.numel() != n * H * D:
+            raise ValueError(f"d{name} must have {name}'s shape and type, d{name}_out its size")
+        strides.append((ld, hs))
+    for g, name in ((dg_q, "dg_q"), (dg_k, "dg_k")):
+        if g is not None and g.numel() != D:
+            raise ValueError(f"{name} must have D elements")
+    if ws is None and (g_q is not None or g_k is not None):
+        ws = _workspace(repro_qk_norm_rope_bwd_ws_bytes(n, Hq, Hkv, D), q.device)
+    flags = (REPRO_QK_INTERLEAVED if interleaved else 0) | (REPRO_BWD_DW_ACCUMULATE if accumulate else 0)
+    has_k = k is not None
+    _check("repro_qk_norm_rope_bwd", lib().repro_qk_norm_rope_bwd(
+        _ptr(dq_out, f32, "dq_out"), _ptr(dk_out if has_k else None, f32, "dk_out"),
+        _dev_ptr(q, "q", False), q_ld, q_hs, _dev_ptr(k, "k", False), k_ld, k_hs, kind,
+        _ptr(g_q, f32, "g_q"), _ptr(g_k, f32, "g_k"), _ptr(rope, f32, "rope"), P,
+        _ptr(positions, torch.int32, "positions"), T, float(eps), n, Hq, Hkv, D, R, flags,
+        _dev_ptr(dq, "dq", False), *strides[0], _dev_ptr(dk if has_k else None, "dk", False), *strides[1],
+        _ptr(dg_q, f32, "dg_q"), _ptr(dg_k, f32, "dg_k"), _dev_ptr(ws, "ws"),
+        ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
+
+
+def repro_distill_ws_bytes(n: int, V: int) -> int:
+    return int(lib().repro_distill_ws_bytes(int(n), int(V)))
+
+
+def _distill_common(logits, t_idx, labels, tau, w_kd, w_ce, w_z):
+    n, V, ld = _rows2d(logits, "logits")
+    if t_idx.dim() < 2 or t_idx.numel() != n * t_idx.shape[-1]:
+        raise ValueError("t_idx must be [..., K] with a row per row of logits")
+    if labels is not None and labels.numel() != n:
+        raise ValueError("labels must have an entry per row of logits")
+    hp = DistillHparams(tau, w_kd, w_ce, w_z)
+    return n, V, ld, int(t_idx.shape[-1]), _index_bytes("t_idx and labels", t_idx, labels), hp
+
+
+def repro_distill_fwd(logits: torch.Tensor, t_idx: torch.Tensor, t_logits: torch.Tensor, loss: torch.Tensor,
+                      stats: torch.Tensor, labels=None, tau: float = 1.0, w_kd: float = 1.0,
+                      w_ce: float = 0.0, w_z: float = 0.0, logprobs: bool = False, ws=None,
+                      stream=None) -> None:
+    """loss [n] <- w_kd tau^2 KL(teacher, student) over the teacher's K entries a
+    row (t_idx [n, K], negative: empty; t_logits [n, K], or its log-probabilities
+    with logprobs) + w_ce cross entropy of labels (negative: none) + w_z lse^2.
+    logits [n, V] float32 or bfloat16, rows at any stride; stats
+    [n, REPRO_DISTILL_STATS + K] float32 is the backward's input."""
+    n, V, ld, K, ib, hp = _distill_common(logits, t_idx, labels, tau, w_kd, w_ce, w_z)
+    if t_logits.shape != t_idx.shape:
+        raise ValueError("t_logits must have t_idx's shape")
+    if loss.numel() != n or stats.numel() != n * (REPRO_DISTILL_STATS + K):
+        raise ValueError("loss must be [n], stats [n, REPRO_DISTILL_STATS + K]")
+    if ws is None:
+        ws = _workspace(repro_distill_ws_bytes(n, V), logits.device)
+    _check("repro_distill_fwd", lib().repro_distill_fwd(
+        _dev_ptr(logits, "logits", False), _float_type(logits, "logits"), ld, _dev_ptr(t_idx, "t_idx"),
+        _dev_ptr(t_logits, "t_logits"), _float_type(t_logits, "t_logits"), _dev_ptr(labels, "labels"), ib,
+        n, V, K, ctypes.byref(hp), REPRO_DISTILL_LOGPROBS if logprobs else 0,
+        _ptr(loss, torch.float32, "loss"), _ptr(stats, torch.float32, "stats"), _dev_ptr(ws, "ws"),
+        ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def repro_distill_bwd(logits: torch.Tensor, t_idx: torch.Tensor, stats: torch.Tensor, g: torch.Tensor,
+                      dlogits: torch.Tensor, labels=None, tau: float = 1.0, w_kd: float = 1.0,
+                      w_ce: float = 0.0, w_z: float = 0.0, logprobs: bool = False, stream=None) -> None:
+    """dlogits [n, V] (logits' type; may be logits itself) <- the gradient of the
+    rows' losses for upstream gradients g ([n], or [1] for every row), from the
+    forward's arguments and stats (logprobs is accepted so that one set of
+    keywords serves both calls; stats holds its effect)."""
+    n, V, ld, K, ib, hp = _distill_common(logits, t_idx, labels, tau, w_kd, w_ce, w_z)
+    nd, Vd, dld = _rows2d(dlogits, "dlogits")
+    if (nd, Vd) != (n, V) or dlogits.dtype != logits.dtype:
+        raise ValueError("dlogits must have the shape and type of logits")
+    if stats.numel() != n * (REPRO_DISTILL_STATS + K):
+        raise ValueError("stats must be [n, REPRO_DISTILL_STATS + K]")
+    _check("repro_distill_bwd", lib().repro_distill_bwd(
+        _dev_ptr(logits, "logits", False), _float_type(logits, "logits"), ld, _dev_ptr(t_idx, "t_idx"),
+        _dev_ptr(labels, "labels"), ib, n, V, K, ctypes.byref(hp), _ptr(stats, torch.float32, "stats"),
+        _ptr(g, torch.float32, "g"), g.numel(), _dev_ptr(dlogits, "dlogits", False), dld, _stream(stream)))
 
 
 def repro_selftest(device=None, stream=None) -> int:

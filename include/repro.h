@@ -77,8 +77,10 @@ typedef enum {
     REPRO_ERR_WORKSPACE = -7, /* workspace NULL or smaller than *_ws_bytes() */
     REPRO_ERR_ALIAS = -8,     /* two buffers that must not overlap do */
     REPRO_ERR_SELFTEST = -9,  /* repro_selftest found the tensor-core forward inexact */
-    REPRO_ERR_NONFINITE = -10 /* debug mode: a float input held a NaN or an infinity
+    REPRO_ERR_NONFINITE = -10, /* debug mode: a float input held a NaN or an infinity
                                  (repro_device_check; see repro_set_debug) */
+    REPRO_ERR_INDEX = -11     /* a token, position, teacher index or label was out of range
+                                 (repro_device_check) */
 } repro_status;
 
 typedef enum {
@@ -344,6 +346,154 @@ int repro_attn_bwd(const float* q, const float* k, const int8_t* vq, const float
 size_t repro_attn_bwd_ws_bytes(int64_t B, int64_t T, int64_t Hq, int64_t W);
 
 /* ------------------------------------------------------------------------
+ * The operators around the decoder blocks: what turns tokens into the first
+ * activations, what stands between the QKV linear and the attention, and what
+ * turns the last linear's outputs into a loss and its gradient.  The pages name
+ * the model's embedding, QK norm, rotary positions and loss (none of them
+ * quantised there) and fix no order; the library's is stated per call, every
+ * operation binary32, rounded, subnormals flushed, never fused.
+ *
+ * Types: REPRO_F32, or REPRO_BF16 (read exactly; a result written as bf16 is
+ * the binary32 result rounded once more, to nearest even), or REPRO_I8 codes
+ * for an embedding table.  Strides are in elements and may exceed the row;
+ * rows whose strides or widths are not multiples of 4 elements are taken
+ * element by element.  Tokens, teacher indexes and labels are int32 or int64
+ * (index_bytes 4 or 8); one that is out of range is passed over as stated and
+ * makes the next repro_device_check() return REPRO_ERR_INDEX.
+ * ------------------------------------------------------------------------ */
+#define REPRO_F32 0
+#define REPRO_BF16 1
+#define REPRO_I8 2
+
+/* Embedding lookup.  out_id = w (x) scale, w = W[tok_i][d], or for codes
+ * i2f(W[tok_i][d]) (x) *s_w (s_w: 1 float, device; NULL for other types).  A row
+ * whose token equals pad is +0 (no token is negative, so pad = -1 pads with
+ * -1); a token that is neither pad nor in [0, V) gives +0 and sets the error
+ * word.  out: REPRO_F32 or REPRO_BF16, rows out_ld apart; W rows table_ld
+ * apart.  n >= 0 tokens, V >= 1, D >= 1, strides >= D. */
+int repro_embed_fwd(const void* table, int table_type, int64_t table_ld, const float* s_w,
+                    const void* tokens, int index_bytes, int64_t n, int64_t V, int64_t D,
+                    float scale, int64_t pad, void* out, int out_type, int64_t out_ld,
+                    void* stream);
+
+/* The table's gradient: dtable_vd = canonical sum over the positions i with
+ * tok_i = v, ascending, of dout_id, (x) scale; +0 for a row without tokens.  With
+ * REPRO_BWD_DW_ACCUMULATE in flags: dtable (+) that, rows without tokens left
+ * alone.  Padding and out-of-range tokens contribute nothing.  dtable [V][D]
+ * fp32, rows dtable_ld apart.  V <= REPRO_EMBED_MAX_V, n < 2^31.  ws:
+ * repro_embed_bwd_ws_bytes(n, V, D) bytes: the sorted positions and the partial
+ * sums of tokens that occur more than 64 times. */
+#define REPRO_EMBED_MAX_V 16777215
+int repro_embed_bwd(const void* dout, int dout_type, int64_t dout_ld, const void* tokens,
+                    int index_bytes, int64_t n, int64_t V, int64_t D, float scale, int64_t pad,
+                    float* dtable, int64_t dtable_ld, int flags, void* ws, size_t ws_bytes,
+                    void* stream);
+size_t repro_embed_bwd_ws_bytes(int64_t n, int64_t V, int64_t D);
+
+/* RMS norm of every query and key head, then the position rotation.  For token
+ * i and head h of q (k alike), with x_d the head's D values:
+ *   S = sum of x_d (x) x_d: groups of 4 consecutive terms left to right, the
+ *     group sums by the stride-doubling pairwise tree;
+ *   r = 1 (/) sqrt((S (/) D) (+) eps);  y_d = x_d (x) r, (x) gain_d if given;
+ *   for each pair j < R / 2 with (a, b) = (j, j + R / 2), or (2j, 2j + 1) with
+ *   REPRO_QK_INTERLEAVED, and c, s = rope[p_i][j], rope[p_i][R / 2 + j]:
+ *     out_a = (y_a (x) c) (-) (y_b (x) s);  out_b = (y_b (x) c) (+) (y_a (x) s);
+ *   out_d = y_d for d >= R.
+ * rope: [P][R] fp32, R / 2 cosines then R / 2 sines per position (the caller's
+ * table, part of the state it hashes).  p_i = positions[i] (int32), or with
+ * positions NULL i mod T (T >= 1).  A position outside [0, P) gives +0 rows and
+ * sets the error word.  q: n tokens, token and head strides ld and hs (hs >= D,
+ * ld >= 1), heads in memory as the strides say: a slice of the fused QKV output
+ * is taken as it is.  q_out [n][Hq][D], k_out [n][Hkv][D] dense fp32, as
+ * repro_attn_fwd takes them.  Hkv = 0 (k, k_out, gain_k NULL) does q alone.
+ * 1 <= D <= REPRO_QK_MAX_D, R even, 0 <= R <= D (R = 0: rope NULL, P = 0 and
+ * positions are not looked at), eps >= 0. */
+#define REPRO_QK_INTERLEAVED 2
+#define REPRO_QK_MAX_D 512
+int repro_qk_norm_rope_fwd(const void* q, int64_t q_ld, int64_t q_hs, const void* k, int64_t k_ld,
+                           int64_t k_hs, int type, const float* gain_q, const float* gain_k,
+                           const float* rope, int64_t P, const int32_t* positions, int64_t T,
+                           float eps, int64_t n, int64_t Hq, int64_t Hkv, int64_t D, int64_t R,
+                           int flags, float* q_out, float* k_out, void* stream);
+
+/* Its backward, from the forward's inputs and the gradients dq_out [n][Hq][D],
+ * dk_out [n][Hkv][D] (dense fp32, what repro_attn_bwd writes):
+ *   dy_a = (do_a (x) c) (+) (do_b (x) s), dy_b = (do_b (x) c) (-) (do_a (x) s);
+ *   h_d = x_d (x) r;  u_d = dy_d (x) gain_d (dy_d without a gain);
+ *   c1 = S'(u_d (x) h_d) (/) D, S' the order of S;
+ *   dx_d = r (x) (u_d (-) (h_d (x) c1)), written to dq (dk) in q's type with the
+ *     strides dq_ld, dq_hs;
+ *   dgain_d = canonical sum of dy_d (x) h_d over the rows (token, head), token
+ *     major (a row of an out-of-range position gives a +0 term), (+) into
+ *     dgain with REPRO_BWD_DW_ACCUMULATE.
+ * dgain_q (dgain_k) is required when gain_q (gain_k) is given, else NULL.  ws:
+ * repro_qk_norm_rope_bwd_ws_bytes(n, Hq, Hkv, D) bytes, needed with gains only. */
+int repro_qk_norm_rope_bwd(const float* dq_out, const float* dk_out, const void* q, int64_t q_ld,
+                           int64_t q_hs, const void* k, int64_t k_ld, int64_t k_hs, int type,
+                           const float* gain_q, const float* gain_k, const float* rope, int64_t P,
+                           const int32_t* positions, int64_t T, float eps, int64_t n, int64_t Hq,
+                           int64_t Hkv, int64_t D, int64_t R, int flags, void* dq, int64_t dq_ld,
+                           int64_t dq_hs, void* dk, int64_t dk_ld, int64_t dk_hs, float* dgain_q,
+                           float* dgain_k, void* ws, size_t ws_bytes, void* stream);
+size_t repro_qk_norm_rope_bwd_ws_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64_t D);
+
+/* Loss of every row of logits z [n][V] (rows z_ld apart) against a teacher's
+ * top logits: t_idx [n][K] (index_bytes; negative: an empty entry) and t_val
+ * [n][K] (fp32 or bf16), with the label's cross entropy and the log-partition
+ * penalty from the same pass.  it = 1 (/) tau, u_j = z_j (x) it:
+ *   e(x) = 2^t for x <= 0, t = x (x) RN(1 / ln 2): k = rint(t), f = t (-) k, the
+ *     degree-6 polynomial of 2^f (coefficients in k_distill.cu) in Horner form,
+ *     times 2^k; 0 below t = -125;
+ *   blocks of REPRO_DISTILL_BLOCK consecutive logits: the block's maximum M_b
+ *     (a zero maximum is +0, a NaN stays) and S_b = sum of e(u_j (-) M_b (x) it) in
+ *     128 chains (element j of the block in chain j mod 128, ascending from
+ *     +0), the chains by the pairwise tree;
+ *   M = max M_b; l = sum over blocks of S_b (x) e((M_b (x) it) (-) (M (x) it)) in 32
+ *     chains (block b in chain b mod 32) and the tree; l1 the same with it = 1;
+ *   the teacher's weights p_k over the non-empty entries: a_k = t_k (x) it,
+ *     m = max a_k, p_k = e(a_k (-) m) (/) lt, lt the sum of the e(.) in 32 chains and
+ *     the tree, P = 1; with REPRO_DISTILL_LOGPROBS t_k are the teacher's own
+ *     log-probabilities: a_k = t_k, p_k = e(a_k), P their sum in that order.  No
+ *     entry (or only -infinities): every p_k and P are 0.
+ *   loss = w_kd tau^2 sum_k p_k (ln p_k - ln softmax(u)_k) + w_ce (lse(z) - z_label)
+ *     + w_z lse(z)^2, its row terms in binary64, unfused, rounded once; ln of a
+ *     sum by its atanh series, the terms over k in 32 chains and the tree.
+ * p_k = 0 adds nothing.  A negative label adds no cross entropy.  An index or a
+ * label >= V is passed over and sets the error word.  A row with no logit above
+ * -infinity has loss 0 and gradient 0.  A NaN among a row's logits makes its
+ * loss and gradient NaN.
+ * stats [n][REPRO_DISTILL_STATS + K] fp32 (dense): M, l, lse(u), l1, lse(z), m, lt, P,
+ * then the p_k; the backward's input.  (l1 and lse(z) are 0 when tau != 1 and
+ * both w_ce and w_z are 0.)  loss [n] fp32.  hp: HOST struct, tau > 0 finite.
+ * labels may be NULL when w_ce is 0.  ws: repro_distill_ws_bytes(n, V) bytes. */
+#define REPRO_DISTILL_BLOCK 1024
+#define REPRO_DISTILL_STATS 8
+#define REPRO_DISTILL_STAT_LSE 2
+#define REPRO_DISTILL_LOGPROBS 1
+typedef struct {
+    float tau, w_kd, w_ce, w_z;
+} repro_distill_hparams;
+int repro_distill_fwd(const void* z, int z_type, int64_t z_ld, const void* t_idx, const void* t_val,
+                      int t_type, const void* labels, int index_bytes, int64_t n, int64_t V,
+                      int64_t K, const repro_distill_hparams* hp, int flags, float* loss,
+                      float* stats, void* ws, size_t ws_bytes, void* stream);
+size_t repro_distill_ws_bytes(int64_t n, int64_t V);
+
+/* The logits' gradient for upstream gradients g of the row losses (g_n = n
+ * floats, or g_n = 1: one for every row), from the forward's inputs and stats:
+ *   gk = (g (x) w_kd) (x) tau;  a = gk (x) P;  b = g (x) ([label >= 0] w_ce (+) (2 (x) w_z) (x) lse(z))
+ *   tau = 1: dz_j = e(u_j (-) M) (x) ((a (+) b) (/) l);
+ *   else dz_j = e(u_j (-) M (x) it) (x) (a (/) l), (+) e(z_j (-) M) (x) (b (/) l1) if w_ce or w_z
+ *   then, entry by entry in ascending k, dz at t_idx_k (-)= gk (x) p_k (w_kd not 0),
+ *   and dz at the label (-)= g (x) w_ce.
+ * dz in z's type, rows dz_ld apart; it may be z itself (same pointer and
+ * stride), otherwise must not overlap it. */
+int repro_distill_bwd(const void* z, int z_type, int64_t z_ld, const void* t_idx, const void* labels,
+                      int index_bytes, int64_t n, int64_t V, int64_t K,
+                      const repro_distill_hparams* hp, const float* stats, const float* g,
+                      int64_t g_n, void* dz, int64_t dz_ld, void* stream);
+
+/* ------------------------------------------------------------------------
  * Per-step state hash ([rit] paragraph 4, [limits]: a hash of the state is
  * recorded after every step and a replay must reproduce it; the pages hash on
  * the host and name on-device hashing as future work).  The pages fix no
@@ -373,8 +523,9 @@ size_t repro_state_hash_ws_bytes(const int64_t* nbytes, int nbuf);
  * repro_status_str: static description of a status code.
  * repro_version: REPRO_VERSION.
  * repro_device_check: synchronises `stream`, then reads and clears the
- *   device error word set by bounded device-side waits; returns REPRO_OK,
- *   REPRO_ERR_TIMEOUT, or REPRO_ERR_SELFTEST once after the forward's
+ *   device error word set by bounded device-side waits (and by out-of-range
+ *   tokens, positions, indexes and labels); returns REPRO_OK,
+ *   REPRO_ERR_TIMEOUT, REPRO_ERR_INDEX, or REPRO_ERR_SELFTEST once after the forward's
  *   exactness check failed on the current device (REPRO_ERR_LAUNCH if the
  *   stream reported an error).
  * repro_launch_count: number of kernels this library has enqueued in this

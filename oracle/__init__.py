@@ -63,6 +63,7 @@ class AdamWHparams(ctypes.Structure):
 _f32p = ctypes.POINTER(ctypes.c_float)
 _i8p = ctypes.POINTER(ctypes.c_int8)
 _i64p = ctypes.POINTER(ctypes.c_int64)
+_i32p = ctypes.POINTER(ctypes.c_int32)
 _i64 = ctypes.c_int64
 
 
@@ -126,6 +127,20 @@ def load(path: str) -> ctypes.CDLL:
         "oracle_attn_bwd_rows": (None, [_f32p, _f32p, _i8p, ctypes.c_float, _f32p, _f32p,
                                         _f32p, _f32p, _i64p, _i64, _f32p, _i64p, _i64, _f32p,
                                         _f32p, _i64, _i64, _i64, _i64, _i64, _i64]),
+        "oracle_embed_fwd": (None, [_f32p, _i8p, ctypes.c_float, _i64p, _i64, _i64, _i64,
+                                    ctypes.c_float, _i64, _f32p]),
+        "oracle_embed_bwd": (None, [_f32p, _i64p, _i64, _i64, _i64, ctypes.c_float, _i64,
+                                    ctypes.c_int, _f32p]),
+        "oracle_qk_fwd": (None, [_f32p, _f32p, _i32p, _i64, _f32p, ctypes.c_float, ctypes.c_int,
+                                 _i64, _i64, _i64, _i64, _f32p]),
+        "oracle_qk_bwd": (None, [_f32p, _f32p, _f32p, _i32p, _i64, _f32p, ctypes.c_float,
+                                 ctypes.c_int, _i64, _i64, _i64, _i64, _f32p, _f32p, ctypes.c_int]),
+        "oracle_exp2_neg": (ctypes.c_float, [ctypes.c_float]),
+        "oracle_ln": (ctypes.c_double, [ctypes.c_float]),
+        "oracle_distill_fwd": (None, [_f32p, _i64, _i64, _i64p, _f32p, _i64, _i64p,
+                                      *[ctypes.c_float] * 4, ctypes.c_int, _f32p, _f32p]),
+        "oracle_distill_bwd": (None, [_f32p, _i64, _i64, _i64p, _i64, _i64p, _f32p, _f32p, _i64,
+                                      *[ctypes.c_float] * 4, _f32p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -436,3 +451,98 @@ def attn_bwd_rows(q, k, vq, s_v: float, o, dout, m, l, W: int, qrows, krows):
 
 
 from .merkle import LEAF_BYTES as HASH_LEAF_BYTES, state_hash, mth, audit_path  # noqa: E402,F401
+
+
+# ---------------------------------------------------------------- around the blocks
+
+DISTILL_STATS = 8
+
+
+def _i64a(a):
+    return None if a is None else np.ascontiguousarray(a, dtype=np.int64)
+
+
+def _opt(a, t):
+    return None if a is None else _p(a, t)
+
+
+def embed_fwd(W, tokens, scale: float = 1.0, s_w: float | None = None, pad: int = -1) -> np.ndarray:
+    """W [V, D] float32, or int8 codes with their scale s_w."""
+    tok = _i64a(tokens).ravel()
+    V, D = W.shape
+    out = np.empty((tok.size, D), dtype=np.float32)
+    Wf, Wq = (_f32(W), None) if s_w is None else (None, _i8(W))
+    lib().oracle_embed_fwd(_opt(Wf, _f32p), _opt(Wq, _i8p), float(s_w or 0.0), _p(tok, _i64p), tok.size,
+                           V, D, float(scale), int(pad), _p(out, _f32p))
+    return out
+
+
+def embed_bwd(dout, tokens, V: int, scale: float = 1.0, pad: int = -1, acc=None) -> np.ndarray:
+    """The table's gradient, or acc (+) it on the rows that have tokens."""
+    tok = _i64a(tokens).ravel()
+    dout = _f32(dout)
+    D = dout.shape[-1]
+    dW = np.empty((V, D), dtype=np.float32) if acc is None else _f32(acc).copy()
+    lib().oracle_embed_bwd(_p(dout, _f32p), _p(tok, _i64p), tok.size, V, D, float(scale), int(pad),
+                           int(acc is not None), _p(dW, _f32p))
+    return dW
+
+
+def qk_fwd(x, rope, pos, gain=None, eps: float = 1e-6, interleaved: bool = False) -> np.ndarray:
+    """One of q, k: x [n, H, D], rope [P, R], pos [n]."""
+    x, rope = _f32(x), _f32(rope)
+    pos = np.ascontiguousarray(pos, dtype=np.int32)
+    gain = None if gain is None else _f32(gain)
+    n, H, D = x.shape
+    out = np.empty(x.shape, dtype=np.float32)
+    lib().oracle_qk_fwd(_p(x, _f32p), _p(rope, _f32p), _p(pos, _i32p), rope.shape[0], _opt(gain, _f32p),
+                        float(eps), int(interleaved), n, H, D, rope.shape[1], _p(out, _f32p))
+    return out
+
+
+def qk_bwd(dout, x, rope, pos, gain=None, eps: float = 1e-6, interleaved: bool = False, acc=None):
+    """(dx, dg); dg is None without a gain."""
+    dout, x, rope = _f32(dout), _f32(x), _f32(rope)
+    pos = np.ascontiguousarray(pos, dtype=np.int32)
+    gain = None if gain is None else _f32(gain)
+    n, H, D = x.shape
+    dx = np.empty(x.shape, dtype=np.float32)
+    dg = None
+    if gain is not None:
+        dg = np.empty(D, dtype=np.float32) if acc is None else _f32(acc).copy()
+    lib().oracle_qk_bwd(_p(dout, _f32p), _p(x, _f32p), _p(rope, _f32p), _p(pos, _i32p), rope.shape[0],
+                        _opt(gain, _f32p), float(eps), int(interleaved), n, H, D, rope.shape[1],
+                        _p(dx, _f32p), _opt(dg, _f32p), int(acc is not None))
+    return dx, dg
+
+
+def exp2_neg(t: float) -> np.float32:
+    return np.float32(lib().oracle_exp2_neg(float(t)))
+
+
+def ln(x: float) -> float:
+    return float(lib().oracle_ln(float(x)))
+
+
+def distill_fwd(z, idx, tl, label=None, tau=1.0, w_kd=1.0, w_ce=0.0, w_z=0.0, logprobs=False):
+    """(loss [n], stats [n, 8 + K])."""
+    z, tl, idx, label = _f32(z), _f32(tl), _i64a(idx), _i64a(label)
+    n, V = z.shape
+    K = idx.shape[1]
+    loss = np.empty(n, dtype=np.float32)
+    stats = np.empty((n, DISTILL_STATS + K), dtype=np.float32)
+    lib().oracle_distill_fwd(_p(z, _f32p), n, V, _p(idx, _i64p), _p(tl, _f32p), K, _opt(label, _i64p),
+                             float(tau), float(w_kd), float(w_ce), float(w_z), int(logprobs),
+                             _p(loss, _f32p), _p(stats, _f32p))
+    return loss, stats
+
+
+def distill_bwd(z, idx, stats, g, label=None, tau=1.0, w_kd=1.0, w_ce=0.0, w_z=0.0) -> np.ndarray:
+    """g [n], or [1] for every row."""
+    z, idx, label, stats, g = _f32(z), _i64a(idx), _i64a(label), _f32(stats), _f32(g).ravel()
+    n, V = z.shape
+    dz = np.empty(z.shape, dtype=np.float32)
+    lib().oracle_distill_bwd(_p(z, _f32p), n, V, _p(idx, _i64p), idx.shape[1], _opt(label, _i64p),
+                             _p(stats, _f32p), _p(g, _f32p), 0 if g.size == 1 else 1, float(tau),
+                             float(w_kd), float(w_ce), float(w_z), _p(dz, _f32p))
+    return dz

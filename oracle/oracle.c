@@ -796,3 +796,407 @@ void oracle_set_threads(int n)
     (void)n;
 #endif
 }
+
+/* ------------------------------------------------------------------------ */
+/* The operators around the decoder blocks: token embedding, per-head norm of */
+/* queries and keys with the position rotation, and the loss against a        */
+/* teacher's top logits.  The pages name the model's parts and fix no order;  */
+/* the definitions are those of include/repro.h.                              */
+/* ------------------------------------------------------------------------ */
+
+/* pairwise tree with stride doubling over n values, in place; n = 0 gives +0 */
+static float tree_inplace(float* t, int64_t n)
+{
+    for (int64_t s = 1; s < n; s *= 2)
+        for (int64_t j = 0; j + s < n; j += 2 * s)
+            t[j] = oracle_add(t[j], t[j + s]);
+    return n > 0 ? t[0] : 0.0f;
+}
+
+/* ---- embedding ---------------------------------------------------------- */
+
+void oracle_embed_fwd(const float* W, const int8_t* Wq, float s_w, const int64_t* tok, int64_t n,
+                      int64_t V, int64_t D, float scale, int64_t pad, float* out)
+{
+    for (int64_t i = 0; i < n; ++i) {
+        const int ok = tok[i] >= 0 && tok[i] < V && tok[i] != pad;
+        for (int64_t d = 0; d < D; ++d) {
+            float w = 0.0f;
+            if (ok)
+                w = W ? oracle_flush(W[tok[i] * D + d]) : oracle_mul((float)Wq[tok[i] * D + d], s_w);
+            out[i * D + d] = ok ? oracle_mul(w, scale) : 0.0f;
+        }
+    }
+}
+
+void oracle_embed_bwd(const float* dout, const int64_t* tok, int64_t n, int64_t V, int64_t D,
+                      float scale, int64_t pad, int accumulate, float* dW)
+{
+#pragma omp parallel
+    {
+        float* terms = (float*)malloc(sizeof(float) * (size_t)(n > 0 ? n : 1));
+        int64_t* rows = (int64_t*)malloc(sizeof(int64_t) * (size_t)(n > 0 ? n : 1));
+#pragma omp for schedule(dynamic, 16)
+        for (int64_t v = 0; v < V; ++v) {
+            int64_t L = 0;
+            for (int64_t i = 0; i < n; ++i)
+                if (tok[i] == v && v != pad)
+                    rows[L++] = i;
+            for (int64_t d = 0; d < D; ++d) {
+                for (int64_t j = 0; j < L; ++j)
+                    terms[j] = dout[rows[j] * D + d];
+                float* w = dW + v * D + d;
+                if (L > 0) {
+                    const float g = oracle_mul(oracle_canon_sum(terms, L), scale);
+                    *w = accumulate ? oracle_add(*w, g) : g;
+                } else if (!accumulate) {
+                    *w = 0.0f;
+                }
+            }
+        }
+        free(terms);
+        free(rows);
+    }
+}
+
+/* ---- norm of every head and the rotation -------------------------------- */
+
+/* groups of 4 consecutive terms left to right, the group sums by the tree */
+static float sum4_tree(const float* t, int64_t D)
+{
+    float g[128];
+    const int64_t G = (D + 3) / 4;
+    for (int64_t k = 0; k < G; ++k) {
+        float s = oracle_flush(t[4 * k]);
+        for (int64_t d = 4 * k + 1; d < D && d < 4 * k + 4; ++d)
+            s = oracle_add(s, t[d]);
+        g[k] = s;
+    }
+    return tree_inplace(g, G);
+}
+
+static float head_rnorm(const float* x, int64_t D, float eps)
+{
+    float t[512];
+    for (int64_t d = 0; d < D; ++d)
+        t[d] = oracle_mul(x[d], x[d]);
+    return oracle_div(1.0f, oracle_sqrt(oracle_add(oracle_div(sum4_tree(t, D), (float)D), eps)));
+}
+
+/* the two members of rotation pair j */
+static void pair_of(int64_t j, int64_t R, int interleaved, int64_t* a, int64_t* b)
+{
+    *a = interleaved ? 2 * j : j;
+    *b = interleaved ? 2 * j + 1 : j + R / 2;
+}
+
+void oracle_qk_fwd(const float* x, const float* rope, const int32_t* pos, int64_t P, const float* gain,
+                   float eps, int interleaved, int64_t n, int64_t H, int64_t D, int64_t R, float* out)
+{
+#pragma omp parallel for schedule(static)
+    for (int64_t u = 0; u < n * H; ++u) {
+        const float* xr = x + u * D;
+        float* o = out + u * D;
+        const int64_t p = pos[u / H];
+        if (p < 0 || p >= P) {
+            for (int64_t d = 0; d < D; ++d)
+                o[d] = 0.0f;
+            continue;
+        }
+        const float r = head_rnorm(xr, D, eps);
+        for (int64_t d = 0; d < D; ++d) {
+            o[d] = oracle_mul(xr[d], r);
+            if (gain)
+                o[d] = oracle_mul(o[d], gain[d]);
+        }
+        for (int64_t j = 0; j < R / 2; ++j) {
+            int64_t a, b;
+            pair_of(j, R, interleaved, &a, &b);
+            const float c = rope[p * R + j], s = rope[p * R + R / 2 + j], ya = o[a], yb = o[b];
+            o[a] = oracle_add(oracle_mul(ya, c), -oracle_mul(yb, s));
+            o[b] = oracle_add(oracle_mul(yb, c), oracle_mul(ya, s));
+        }
+    }
+}
+
+/* dx, and dg (when gain) = canonical sum over the rows (token, head) ascending */
+void oracle_qk_bwd(const float* dout, const float* x, const float* rope, const int32_t* pos, int64_t P,
+                   const float* gain, float eps, int interleaved, int64_t n, int64_t H, int64_t D,
+                   int64_t R, float* dx, float* dg, int accumulate)
+{
+    float* gt = gain ? (float*)malloc(sizeof(float) * (size_t)(n * H * D + 1)) : NULL;
+#pragma omp parallel for schedule(static)
+    for (int64_t u = 0; u < n * H; ++u) {
+        const float *xr = x + u * D, *dr = dout + u * D;
+        const int64_t p = pos[u / H];
+        float dy[512], xh[512], t[512];
+        if (p < 0 || p >= P) {
+            for (int64_t d = 0; d < D; ++d) {
+                dx[u * D + d] = 0.0f;
+                if (gt)
+                    gt[d * n * H + u] = 0.0f;
+            }
+            continue;
+        }
+        const float r = head_rnorm(xr, D, eps);
+        for (int64_t d = 0; d < D; ++d) {
+            dy[d] = oracle_flush(dr[d]);
+            xh[d] = oracle_mul(xr[d], r);
+        }
+        for (int64_t j = 0; j < R / 2; ++j) {
+            int64_t a, b;
+            pair_of(j, R, interleaved, &a, &b);
+            const float c = rope[p * R + j], s = rope[p * R + R / 2 + j], da = dr[a], db = dr[b];
+            dy[a] = oracle_add(oracle_mul(da, c), oracle_mul(db, s));
+            dy[b] = oracle_add(oracle_mul(db, c), -oracle_mul(da, s));
+        }
+        for (int64_t d = 0; d < D; ++d) {
+            if (gt)
+                gt[d * n * H + u] = oracle_mul(dy[d], xh[d]);
+            if (gain)
+                dy[d] = oracle_mul(dy[d], gain[d]);
+            t[d] = oracle_mul(dy[d], xh[d]);
+        }
+        const float c1 = oracle_div(sum4_tree(t, D), (float)D);
+        for (int64_t d = 0; d < D; ++d)
+            dx[u * D + d] = oracle_mul(r, oracle_add(dy[d], -oracle_mul(xh[d], c1)));
+    }
+    if (gt) {
+        for (int64_t d = 0; d < D; ++d) {
+            const float s = oracle_canon_sum(gt + d * n * H, n * H);
+            dg[d] = accumulate ? oracle_add(dg[d], s) : s;
+        }
+        free(gt);
+    }
+}
+
+/* ---- loss against a teacher's top logits -------------------------------- */
+
+#define DISTILL_BLOCK 1024
+#define DISTILL_CHAINS 128
+#define DISTILL_STATS 8
+
+/* 2^t for t <= 0: t = k + f, k = rint(t), and the degree-6 minimax polynomial
+ * of 2^f on [-1/2, 1/2] (relative error 2.6e-9, constant term 1; coefficients
+ * by the exchange algorithm of Remez, rounded to binary32); 0 below -125 */
+float oracle_exp2_neg(float t)
+{
+    static const float c[7] = {1.0f, 0x1.62e432p-1f, 0x1.ebfbe2p-3f, 0x1.c6ae72p-5f, 0x1.3b270ep-7f,
+                               0x1.5f7278p-10f, 0x1.470b5p-13f};
+    if (t < -125.0f)
+        return 0.0f;
+    if (t != t)
+        return t;
+    const float k = nearbyintf(t);
+    const float f = oracle_add(t, -k);
+    float p = c[6];
+    for (int i = 5; i >= 0; --i)
+        p = oracle_add(oracle_mul(p, f), c[i]);
+    return oracle_mul(p, ldexpf(1.0f, (int)k));
+}
+
+/* e^x for x <= 0 */
+static float exp_neg(float x) { return oracle_exp2_neg(oracle_mul(x, EXP_LOG2E)); }
+
+/* ln of a positive binary32 value in binary64: x = m 2^e with m in
+ * [sqrt(1/2), sqrt(2)), ln m = 2 atanh((m - 1) / (m + 1)) by its power series
+ * to the 21st power, in Horner form; NaN for anything else */
+double oracle_ln(float x)
+{
+    if (!(x > 0.0f) || x > FLT_MAX)
+        return (double)NAN;
+    int e;
+    double m = frexp((double)x, &e); /* [1/2, 1) */
+    if (m < 0.70710678118654752440) {
+        m *= 2.0;
+        e -= 1;
+    }
+    const double s = (m - 1.0) / (m + 1.0), w = s * s;
+    double p = 1.0 / 21.0;
+    for (int k = 19; k >= 1; k -= 2)
+        p = p * w + 1.0 / (double)k;
+    return (double)e * 0.69314718055994530942 + (2.0 * s) * p;
+}
+
+static float max_nan(float a, float b)
+{
+    if (a != a || b != b)
+        return NAN;
+    if (a == 0.0f && b == 0.0f)
+        return 0.0f;
+    return a > b ? a : b;
+}
+
+/* chain i sums the terms j = i (mod chains) ascending from +0; tree over chains */
+static float chains_sum(const float* t, int64_t n, int chains)
+{
+    float s[DISTILL_CHAINS];
+    for (int i = 0; i < chains; ++i) {
+        s[i] = 0.0f;
+        for (int64_t j = i; j < n; j += chains)
+            s[i] = oracle_add(s[i], t[j]);
+    }
+    return tree_inplace(s, chains);
+}
+
+static double chains_sum_d(const double* t, int64_t n, int chains)
+{
+    double s[DISTILL_CHAINS];
+    for (int i = 0; i < chains; ++i) {
+        s[i] = 0.0;
+        for (int64_t j = i; j < n; j += chains)
+            s[i] += t[j];
+    }
+    for (int st = 1; st < chains; st *= 2)
+        for (int j = 0; j + st < chains; j += 2 * st)
+            s[j] += s[j + st];
+    return s[0];
+}
+
+/* max and sum of e^(it z - it max) over a row, block by block */
+static float row_sum(const float* z, int64_t V, float it, float* mx)
+{
+    const int64_t C = (V + DISTILL_BLOCK - 1) / DISTILL_BLOCK;
+    float* S = (float*)malloc(sizeof(float) * (size_t)C);
+    float* M = (float*)malloc(sizeof(float) * (size_t)C);
+    float t[DISTILL_BLOCK], m = -INFINITY;
+    for (int64_t c = 0; c < C; ++c) {
+        const int64_t lo = c * DISTILL_BLOCK, n = V - lo < DISTILL_BLOCK ? V - lo : DISTILL_BLOCK;
+        M[c] = -INFINITY;
+        for (int64_t j = 0; j < n; ++j)
+            M[c] = max_nan(M[c], oracle_flush(z[lo + j]));
+        M[c] = M[c] == 0.0f ? 0.0f : M[c]; /* a zero maximum is +0 */
+        const float Mu = oracle_mul(M[c], it);
+        for (int64_t j = 0; j < n; ++j)
+            t[j] = exp_neg(oracle_add(oracle_mul(z[lo + j], it), -Mu));
+        S[c] = M[c] == -INFINITY ? 0.0f : chains_sum(t, n, DISTILL_CHAINS);
+        m = max_nan(m, M[c]);
+    }
+    m = m == 0.0f ? 0.0f : m;
+    *mx = m;
+    float l = 0.0f;
+    if (m != -INFINITY) {
+        for (int64_t c = 0; c < C; ++c)
+            S[c] = oracle_mul(S[c], exp_neg(oracle_add(oracle_mul(M[c], it), -oracle_mul(m, it))));
+        l = chains_sum(S, C, 32);
+    }
+    free(S);
+    free(M);
+    return l;
+}
+
+void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx, const float* tl,
+                        int64_t K, const int64_t* label, float tau, float w_kd, float w_ce, float w_z,
+                        int logprobs, float* loss, float* stats)
+{
+    const float it = oracle_div(1.0f, tau);
+#pragma omp parallel for schedule(dynamic, 1)
+    for (int64_t r = 0; r < n; ++r) {
+        const float* zr = z + r * V;
+        float* st = stats + r * (DISTILL_STATS + K);
+        float* p = st + DISTILL_STATS;
+        float mz, m1;
+        const float l = row_sum(zr, V, it, &mz);
+        const float l1 = row_sum(zr, V, 1.0f, &m1);
+        const float Mu = oracle_mul(mz, it);
+        /* the teacher's weights */
+        float mt = -INFINITY, lt = 0.0f, P = 0.0f;
+        for (int64_t k = 0; k < K; ++k) {
+            const int64_t j = idx[r * K + k];
+            p[k] = -INFINITY;
+            if (j >= 0 && j < V)
+                p[k] = logprobs ? oracle_flush(tl[r * K + k]) : oracle_mul(tl[r * K + k], it);
+            mt = max_nan(mt, p[k]);
+        }
+        mt = mt == 0.0f ? 0.0f : mt;
+        float* a = (float*)malloc(sizeof(float) * (size_t)(K + 1));
+        double* term = (double*)malloc(sizeof(double) * (size_t)(K + 1));
+        memcpy(a, p, sizeof(float) * (size_t)K);
+        if (logprobs)
+            mt = 0.0f;
+        if (mt == -INFINITY) {
+            for (int64_t k = 0; k < K; ++k)
+                p[k] = 0.0f;
+        } else {
+            for (int64_t k = 0; k < K; ++k)
+                p[k] = exp_neg(oracle_add(a[k], -mt));
+            lt = chains_sum(p, K, 32);
+            if (logprobs) {
+                P = lt;
+                lt = 1.0f;
+            } else {
+                for (int64_t k = 0; k < K; ++k)
+                    p[k] = oracle_div(p[k], lt);
+                P = lt == lt ? 1.0f : lt;
+            }
+        }
+        const double lse_t = (double)Mu + oracle_ln(l), lse1 = (double)mz + oracle_ln(l1);
+        double v = 0.0;
+        if (mz != -INFINITY) {
+            if (w_kd != 0.0f && mt != -INFINITY) {
+                const double cst = lse_t - ((double)mt + oracle_ln(lt));
+                for (int64_t k = 0; k < K; ++k)
+                    term[k] = p[k] == 0.0f ? 0.0
+                                           : (double)p[k] * (((double)a[k] -
+                                                              (double)oracle_mul(zr[idx[r * K + k]], it)) + cst);
+                v = ((double)w_kd * ((double)tau * (double)tau)) * chains_sum_d(term, K, 32);
+            }
+            if (w_ce != 0.0f && label[r] >= 0 && label[r] < V)
+                v = v + (double)w_ce * (lse1 - (double)oracle_flush(zr[label[r]]));
+            if (w_z != 0.0f)
+                v = v + (double)w_z * (lse1 * lse1);
+        }
+        const int need1 = w_ce != 0.0f || w_z != 0.0f || tau == 1.0f;
+        loss[r] = oracle_flush((float)v);
+        st[0] = mz;
+        st[1] = l;
+        st[2] = mz == -INFINITY ? mz : oracle_flush((float)lse_t);
+        st[3] = need1 ? l1 : 0.0f;
+        st[4] = !need1 ? 0.0f : mz == -INFINITY ? mz : oracle_flush((float)lse1);
+        st[5] = mt;
+        st[6] = lt;
+        st[7] = P;
+        free(a);
+        free(term);
+    }
+}
+
+void oracle_distill_bwd(const float* z, int64_t n, int64_t V, const int64_t* idx, int64_t K,
+                        const int64_t* label, const float* stats, const float* g, int64_t g_stride,
+                        float tau, float w_kd, float w_ce, float w_z, float* dz)
+{
+    const float it = oracle_div(1.0f, tau);
+#pragma omp parallel for schedule(dynamic, 1)
+    for (int64_t r = 0; r < n; ++r) {
+        const float *zr = z + r * V, *st = stats + r * (DISTILL_STATS + K), *p = st + DISTILL_STATS;
+        float* d = dz + r * V;
+        if (st[0] == -INFINITY) {
+            for (int64_t j = 0; j < V; ++j)
+                d[j] = 0.0f;
+            continue;
+        }
+        const float gr = g[r * g_stride];
+        const int lab = w_ce != 0.0f && label[r] >= 0 && label[r] < V;
+        const float gk = oracle_mul(oracle_mul(gr, w_kd), tau);
+        const float a = oracle_mul(gk, st[7]);
+        const float b = oracle_mul(gr, oracle_add(lab ? w_ce : 0.0f,
+                                                  oracle_mul(oracle_mul(2.0f, w_z), w_z != 0.0f ? st[4] : 0.0f)));
+        const int two = tau != 1.0f && (w_ce != 0.0f || w_z != 0.0f);
+        const float ca = tau == 1.0f ? oracle_div(oracle_add(a, b), st[1]) : oracle_div(a, st[1]);
+        const float cb = two ? oracle_div(b, st[3]) : 0.0f;
+        const float Mu = oracle_mul(st[0], it);
+        for (int64_t j = 0; j < V; ++j) {
+            d[j] = oracle_mul(exp_neg(oracle_add(oracle_mul(zr[j], it), -Mu)), ca);
+            if (two)
+                d[j] = oracle_add(d[j], oracle_mul(exp_neg(oracle_add(zr[j], -st[0])), cb));
+        }
+        if (w_kd != 0.0f)
+            for (int64_t k = 0; k < K; ++k) {
+                const int64_t j = idx[r * K + k];
+                if (j >= 0 && j < V)
+                    d[j] = oracle_add(d[j], -oracle_mul(gk, p[k]));
+            }
+        if (lab)
+            d[label[r]] = oracle_add(d[label[r]], -oracle_mul(gr, w_ce));
+    }
+}

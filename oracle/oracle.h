@@ -153,6 +153,27 @@ void oracle_attn_bwd_rows(const float* q, const float* k, const int8_t* vq, floa
                           const int64_t* krows, int64_t nk, float* dk, float* dv, int64_t B,
                           int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t W);
 
+/* Token embedding, per-head norm with rotation, distillation loss (definitions
+ * in include/repro.h; see oracle.c).  Tensors dense; tokens, indexes and labels
+ * widened to int64. */
+void oracle_embed_fwd(const float* W, const int8_t* Wq, float s_w, const int64_t* tok, int64_t n,
+                      int64_t V, int64_t D, float scale, int64_t pad, float* out);
+void oracle_embed_bwd(const float* dout, const int64_t* tok, int64_t n, int64_t V, int64_t D,
+                      float scale, int64_t pad, int accumulate, float* dW);
+void oracle_qk_fwd(const float* x, const float* rope, const int32_t* pos, int64_t P, const float* gain,
+                   float eps, int interleaved, int64_t n, int64_t H, int64_t D, int64_t R, float* out);
+void oracle_qk_bwd(const float* dout, const float* x, const float* rope, const int32_t* pos, int64_t P,
+                   const float* gain, float eps, int interleaved, int64_t n, int64_t H, int64_t D,
+                   int64_t R, float* dx, float* dg, int accumulate);
+float oracle_exp2_neg(float t);
+double oracle_ln(float x);
+void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx, const float* tl,
+                        int64_t K, const int64_t* label, float tau, float w_kd, float w_ce, float w_z,
+                        int logprobs, float* loss, float* stats);
+void oracle_distill_bwd(const float* z, int64_t n, int64_t V, const int64_t* idx, int64_t K,
+                        const int64_t* label, const float* stats, const float* g, int64_t g_stride,
+                        float tau, float w_kd, float w_ce, float w_z, float* dz);
+
 int oracle_threads(void);
 void oracle_set_threads(int n);
 
