@@ -983,7 +983,7 @@ size_t repro_embed_bwd_ws_bytes(int64_t n, int64_t V, int64_t D)
 {
     if (n < 0 || n > INT32_MAX || V < 1 || V > REPRO_EMBED_MAX_V || D < 1 || D > (int64_t)1 << 28)
         return 0;
-    return embed_bwd_ws_bytes(n, D);
+    return embed_bwd_ws_bytes(n, V, D);
 }
 
 int repro_embed_bwd(const void* dout, int dout_type, int64_t dout_ld, const void* tokens, int index_bytes,
@@ -1001,7 +1001,7 @@ int repro_embed_bwd(const void* dout, int dout_type, int64_t dout_ld, const void
         return REPRO_OK;
     if (n > 0 && (!dout || !tokens))
         return REPRO_ERR_ARG;
-    const size_t db = type_bytes(dout_type), need = embed_bwd_ws_bytes(n, D);
+    const size_t db = type_bytes(dout_type), need = embed_bwd_ws_bytes(n, V, D);
     if (!aligned_to(dout, db) || !al4(dtable) || !aligned_to(tokens, index_bytes))
         return REPRO_ERR_ALIGN;
     if (!ws || ws_bytes < need)
@@ -1106,6 +1106,7 @@ int repro_qk_norm_rope_fwd(const void* q, int64_t q_ld, int64_t q_hs, const void
     a.D = D;
     a.R = R;
     a.interleaved = (flags & REPRO_QK_INTERLEAVED) != 0;
+    a.inv = (D & (D - 1)) == 0 ? 1.0f / (float)D : 0.0f;
     a.err = device_error_word();
     if (!a.err)
         return REPRO_ERR_LAUNCH;
@@ -1204,6 +1205,7 @@ int repro_qk_norm_rope_bwd(const float* dq_out, const float* dk_out, const void*
     a.D = D;
     a.R = R;
     a.interleaved = (flags & REPRO_QK_INTERLEAVED) != 0;
+    a.inv = (D & (D - 1)) == 0 ? 1.0f / (float)D : 0.0f;
     a.accumulate = accumulate;
     a.err = device_error_word();
     if (!a.err)

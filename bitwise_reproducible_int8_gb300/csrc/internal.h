@@ -153,7 +153,7 @@ struct EmbedBwdArgs {
     bool accumulate;
     int* err;
 };
-size_t embed_bwd_ws_bytes(int64_t n, int64_t D);
+size_t embed_bwd_ws_bytes(int64_t n, int64_t V, int64_t D);
 cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st);
 
 // ---- pairwise tree over partial rows (k_rowtree.cu), shared by the table's and the gains' gradients
@@ -194,6 +194,7 @@ struct QkArgs {
     float eps;
     int64_t n, D, R;
     bool interleaved, accumulate;
+    float inv;           // 1 / D where D is a power of two, else 0
     int* err;
 };
 cudaError_t launch_qk_fwd(const QkArgs& a, cudaStream_t st);

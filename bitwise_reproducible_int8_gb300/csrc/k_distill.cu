@@ -18,8 +18,10 @@
 // from one read, with no running rescale.  128 chains per block and the pairwise
 // tree over them: chain j mod 128 puts a chain's terms into one lane whether the
 // lane loads single elements (lane, lane + 32, ..: rows of any alignment) or four
-// neighbours.  k_distill_rows joins the blocks' (maximum, sum) pairs per row, so
-// few rows over a long vocabulary still spread over the card.
+// neighbours.  The blocks' (maximum, sum) pairs of a row are joined once all are
+// there, in the same CTA when there are rows enough for a CTA to own its rows
+// (k_distill_fwd), else by a second kernel, so that few rows over a long
+// vocabulary still spread over the card (k_distill_blocks, k_distill_rows).
 #include <math_constants.h>
 
 #include "elem.cuh"
@@ -39,7 +41,9 @@ constexpr float LOG2E = 0x1.715476p+0f;   // RN(1 / ln 2)
 // which sums a call needs
 constexpr int ONE = 0;      // tau = 1: one sum serves all terms
 constexpr int SOFT = 1;     // tau != 1, only the softened softmax
-constexpr int BOTH = 2;     // tau != 1 and the softmax of z itself
+constexpr int BOTH = 2;     // tau != 1 and the softmax of z itself: a second e^x per logit,
+constexpr int SQR1 = 3;     // .. or for tau = 2 the square of the first,
+constexpr int SQR2 = 4;     // .. or for tau = 4 its fourth power
 
 __device__ __forceinline__ float max_nan(float a, float b)
 {
@@ -53,32 +57,40 @@ __device__ __forceinline__ u64 dup2(float v) { return pack2(v, v); }
 // e^x of a packed pair, x <= 0 (a NaN stays a NaN): t = x (x) log2 e, k = rint(t) by
 // adding and subtracting 1.5 * 2^23, f = t (-) k, the degree-6 minimax polynomial
 // of 2^f on [-1/2, 1/2] (relative error 2.6e-9, constant term 1; by the exchange
-// algorithm of Remez, rounded to binary32) in Horner form, times 2^k; 0 below
-// t = -125, so nothing here is subnormal
+// algorithm of Remez, rounded to binary32) in Horner form, times 2^k; 0 where
+// k < -125, so nothing here is subnormal.  The coefficients below are doubled and
+// the power halved, both exact: 2^(k - 1) then has the bits (k + 126) << 23 down to
+// k = -125, and k = -126, where smaller t are clamped, gives the factor +0.
 __device__ __forceinline__ u64 exp_neg2(u64 x)
 {
-    const u64 z = dup2(-0.0f), big = dup2(0x1.8p23f), nbig = dup2(-0x1.8p23f);
-    const u64 t = fadd2_ftz(fmul2_rn(x, dup2(LOG2E)), z);
-    const u64 m = fadd2_ftz(t, big);
-    const u64 k = fadd2_ftz(m, nbig);
-    float k0, k1, m0, m1, t0, t1;
-    unpack2(k, k0, k1);
+    float t0, t1, k0, k1, m0, m1;
+    unpack2(fmul2_rn(x, dup2(LOG2E)), t0, t1);   // subnormal t: consumed by flushing sums only
+    const u64 t = pack2(max_nan(t0, -126.0f), max_nan(t1, -126.0f));
+    const u64 m = fadd2_ftz(t, dup2(0x1.8p23f));
+    unpack2(fadd2_ftz(m, dup2(-0x1.8p23f)), k0, k1);
     const u64 f = fadd2_ftz(t, pack2(-k0, -k1));
-    u64 p = dup2(0x1.470b5p-13f);
-    p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.5f7278p-10f));
-    p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.3b270ep-7f));
-    p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.c6ae72p-5f));
-    p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.ebfbe2p-3f));
-    p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.62e432p-1f));
-    p = fadd2_ftz(fmul2_rn(p, f), dup2(1.0f));
+    u64 p = dup2(0x1.470b5p-12f);
+    p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.5f7278p-9f));
+    p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.3b270ep-6f));
+    p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.c6ae72p-4f));
+    p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.ebfbe2p-2f));
+    p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.62e432p+0f));
+    p = fadd2_ftz(fmul2_rn(p, f), dup2(2.0f));
     unpack2(m, m0, m1);
-    unpack2(t, t0, t1);
-    // the low bits of 1.5 * 2^23 + k are k: shifted into the exponent of 1.0
-    const u64 s = pack2(__int_as_float((__float_as_int(m0) << 23) + 0x3f800000),
-                        __int_as_float((__float_as_int(m1) << 23) + 0x3f800000));
-    float r0, r1;
-    unpack2(fmul2_rn(p, s), r0, r1);
-    return pack2(t0 < -125.0f ? 0.0f : r0, t1 < -125.0f ? 0.0f : r1);
+    // the low bits of 1.5 * 2^23 + k are k
+    const u64 s = pack2(__int_as_float((__float_as_int(m0) << 23) + (126 << 23)),
+                        __int_as_float((__float_as_int(m1) << 23) + (126 << 23)));
+    return fmul2_rn(p, s);
+}
+
+// the softmax-of-z term from the softened one, e(x)^tau by squaring
+template <int SUMS> __device__ __forceinline__ u64 power2(u64 e)
+{
+    const u64 z = dup2(-0.0f);
+    u64 q = fadd2_ftz(fmul2_rn(e, e), z);
+    if (SUMS == SQR2)
+        q = fadd2_ftz(fmul2_rn(q, q), z);
+    return q;
 }
 
 __device__ __forceinline__ float exp_neg(float x)
@@ -168,21 +180,9 @@ __device__ __forceinline__ void load_block(const T* p, int len, int lane, float 
     }
 }
 
-// sum over the block of e(x_i (x) it (-) Mu): four chains per lane, then the tree
-// over the 128 chains in their order
-template <bool VEC, bool SCALE>
-__device__ __forceinline__ float block_sum(const float (&x)[PER], float it, float Mu)
+// the tree over a block's 128 chains: this lane's four, in slots i mod 4
+template <bool VEC> __device__ __forceinline__ float chains_tree(u64 a, u64 b)
 {
-    const u64 nm = dup2(-Mu), sc = dup2(it), z = dup2(-0.0f);
-    u64 a = dup2(0.0f), b = dup2(0.0f);
-#pragma unroll
-    for (int i = 0; i < PER; i += 4) {
-        u64 v = pack2(x[i], x[i + 1]), w = pack2(x[i + 2], x[i + 3]);
-        v = SCALE ? fmul2_rn(fadd2_ftz(v, z), sc) : v;
-        w = SCALE ? fmul2_rn(fadd2_ftz(w, z), sc) : w;
-        a = fadd2_ftz(a, exp_neg2(fadd2_ftz(v, nm)));
-        b = fadd2_ftz(b, exp_neg2(fadd2_ftz(w, nm)));
-    }
     float s0, s1, s2, s3;
     unpack2(a, s0, s1);
     unpack2(b, s2, s3);
@@ -192,280 +192,385 @@ __device__ __forceinline__ float block_sum(const float (&x)[PER], float it, floa
     return fadd_ftz(fadd_ftz(warp_tree(s0), warp_tree(s1)), fadd_ftz(warp_tree(s2), warp_tree(s3)));
 }
 
+// maximum of one block and the sums over it of e(z_i (x) it (-) m (x) it) and, where the
+// call needs it, of e(z_i (-) m)
 template <typename T, int SUMS, bool VEC>
-__global__ void __launch_bounds__(256)
-k_distill_blocks(const T* __restrict__ z, int64_t z_ld, int64_t V, int64_t nblk, int64_t items, float it,
-                 float2* __restrict__ ms, float* __restrict__ s1)
+__device__ __forceinline__ void block_stats(const T* p, int len, int lane, float it, float& m, float& s, float& s1)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (item >= items)
-        return;
-    const int64_t row = item / nblk, blk = item - row * nblk;
-    const int len = (int)(V - blk * BLK < BLK ? V - blk * BLK : BLK);
     float x[PER];
-    load_block<T, VEC>(z + row * z_ld + blk * BLK, len, lane, x);
-    float m = -CUDART_INF_F;
+    load_block<T, VEC>(p, len, lane, x);
+    float t = -CUDART_INF_F;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        m = max_nan(m, x[i]);
-    m = warp_max(m);
-    m = flush(m);
-    m = m == 0.0f ? 0.0f : m;
-    const bool none = m == -CUDART_INF_F;
-    float s = 0.0f, o = 0.0f;
-    if (!none) {
-        s = block_sum<VEC, SUMS != ONE>(x, it, fmul_flush(m, it));
-        if (SUMS == BOTH)
-            o = block_sum<VEC, false>(x, 1.0f, m);
+        t = max_nan(t, x[i]);
+    t = flush(warp_max(t));
+    m = t == 0.0f ? 0.0f : t;
+    s = s1 = 0.0f;
+    if (m == -CUDART_INF_F)
+        return;
+    const u64 nu = dup2(-fmul_flush(m, it)), nm = dup2(-m), sc = dup2(it);
+    u64 a = dup2(0.0f), b = dup2(0.0f), a1 = a, b1 = b;
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+        const u64 v = pack2(x[i], x[i + 1]), w = pack2(x[i + 2], x[i + 3]);
+        // a subnormal logit is not flushed before it is scaled: it is far below half a step
+        // of any maximum that e(.) can tell from 0
+        const u64 ev = exp_neg2(fadd2_ftz(SUMS == ONE ? v : fmul2_rn(v, sc), nu));
+        const u64 ew = exp_neg2(fadd2_ftz(SUMS == ONE ? w : fmul2_rn(w, sc), nu));
+        a = fadd2_ftz(a, ev);
+        b = fadd2_ftz(b, ew);
+        if (SUMS >= BOTH) {
+            a1 = fadd2_ftz(a1, SUMS == BOTH ? exp_neg2(fadd2_ftz(v, nm)) : power2<SUMS>(ev));
+            b1 = fadd2_ftz(b1, SUMS == BOTH ? exp_neg2(fadd2_ftz(w, nm)) : power2<SUMS>(ew));
+        }
     }
-    if (lane == 0) {
-        ms[item] = make_float2(m, s);
-        if (SUMS == BOTH)
-            s1[item] = o;
-    }
+    s = chains_tree<VEC>(a, b);
+    if (SUMS >= BOTH)
+        s1 = chains_tree<VEC>(a1, b1);
 }
 
-struct RowArgs {
+struct FwdArgs {
     const void* t_idx;
     const void* t_val;
     int t_type;
     const void* labels;
     int index_bytes;
-    int64_t n, V, K, nblk;
+    int n, V, K, nblk;
     float it, tau, w_kd, w_ce, w_z;
     bool logprobs;
-    const float2* ms;
-    const float* s1;
+    float2* ms;      // [n][nblk] block maxima and sums
+    float* s1;       // [n][nblk]
     float* loss;
     float* stats;
     int* err;
 };
 
-// one warp per row: joins the blocks, forms the teacher's weights and the loss
-template <typename T, int SUMS>
-__global__ void __launch_bounds__(128)
-k_distill_rows(const T* __restrict__ z, int64_t z_ld, const RowArgs a)
+template <typename T, int SUMS, bool VEC>
+__device__ __forceinline__ void do_block(const T* z, int64_t z_ld, const FwdArgs& a, int row, int blk, int lane)
 {
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= a.n)
-        return;
-    const float2* ms = a.ms + row * a.nblk;
-    float M = -CUDART_INF_F;
-    for (int64_t b = lane; b < a.nblk; b += 32)
-        M = max_nan(M, ms[b].x);
-    M = warp_max(M);
-    M = M == 0.0f ? 0.0f : M;
-    const float Mu = fmul_flush(M, a.it);
-    const bool none = M == -CUDART_INF_F;
-    float l = 0.0f, l1 = 0.0f;
-    if (!none) {
-        for (int64_t b = lane; b < a.nblk; b += 32) {
-            const float2 v = ms[b];
-            l = fadd_ftz(l, fmul_rn(v.y, exp_neg(fadd_ftz(fmul_rn(v.x, a.it), -Mu))));
-            if (SUMS == BOTH)
-                l1 = fadd_ftz(l1, fmul_rn(a.s1[row * a.nblk + b], exp_neg(fadd_ftz(v.x, -M))));
-        }
-        l = warp_tree(l);
-        l1 = SUMS == BOTH ? warp_tree(l1) : l;
-    }
-    if (SUMS == SOFT)
-        l1 = 0.0f;
-    // the teacher's weights
-    float* st = a.stats + row * (STATS + a.K);
-    float* p = st + STATS;
-    auto value = [&](int64_t k, int64_t& j) {   // a_k, and the column or -1
-        j = load_index(a.t_idx, a.index_bytes, row * a.K + k);
-        if (j >= a.V)
-            atomicOr(a.err, kErrIndexBit);
-        if (j < 0 || j >= a.V) {
-            j = -1;
-            return -CUDART_INF_F;
-        }
-        const float t = a.t_type == 0 ? static_cast<const float*>(a.t_val)[row * a.K + k]
-                                      : __bfloat162float(static_cast<const __nv_bfloat16*>(a.t_val)[row * a.K + k]);
-        return a.logprobs ? flush(t) : fmul_flush(flush(t), a.it);
-    };
-    float mt = -CUDART_INF_F;
-    int64_t j;
-    if (a.logprobs) {
-        mt = 0.0f;
-    } else {
-        for (int64_t k = lane; k < a.K; k += 32)
-            mt = max_nan(mt, value(k, j));
-        mt = warp_max(mt);
-        mt = mt == 0.0f ? 0.0f : mt;
-    }
-    float lt = 0.0f, P = 0.0f;
-    if (mt == -CUDART_INF_F) {
-        for (int64_t k = lane; k < a.K; k += 32)
-            p[k] = 0.0f;
-    } else {
-        for (int64_t k = lane; k < a.K; k += 32) {
-            const float e = exp_neg(fadd_ftz(value(k, j), -mt));
-            lt = fadd_ftz(lt, e);
-            p[k] = e;
-        }
-        lt = warp_tree(lt);
-        if (a.logprobs) {
-            P = lt;
-            lt = 1.0f;
-        } else {
-            P = lt == lt ? 1.0f : lt;
-        }
-    }
-    const double lse_t = none ? 0.0 : (double)Mu + ln_d(l);
-    const double lse1 = none || SUMS == SOFT ? 0.0 : (double)M + ln_d(l1);
-    double v = 0.0;
-    if (mt != -CUDART_INF_F) {
-        const double cst = none ? 0.0 : lse_t - ((double)mt + ln_d(lt));
-        double sum = 0.0;
-        for (int64_t k = lane; k < a.K; k += 32) {
-            float w = p[k];
-            if (!a.logprobs) {
-                w = flush(__fdiv_rn(w, lt));
-                p[k] = w;
-            }
-            if (w != 0.0f && !none && a.w_kd != 0.0f) {
-                const float ak = value(k, j);
-                const float u = fmul_flush(flush(to_f32<T>(z[row * z_ld + j])), a.it);
-                sum = sum + (double)w * (((double)ak - (double)u) + cst);
-            }
-        }
-        if (!none && a.w_kd != 0.0f)
-            v = ((double)a.w_kd * ((double)a.tau * (double)a.tau)) * warp_tree(sum);
-    }
+    const int lo = blk * BLK;
+    float m, s, s1;
+    block_stats<T, SUMS, VEC>(z + (int64_t)row * z_ld + lo, min(a.V - lo, BLK), lane, a.it, m, s, s1);
     if (lane == 0) {
-        if (a.w_ce != 0.0f) {
-            const int64_t lab = load_index(a.labels, a.index_bytes, row);
-            if (lab >= a.V)
-                atomicOr(a.err, kErrIndexBit);
-            else if (lab >= 0 && !none)
-                v = v + (double)a.w_ce * (lse1 - (double)flush(to_f32<T>(z[row * z_ld + lab])));
-        }
-        if (a.w_z != 0.0f && !none)
-            v = v + (double)a.w_z * (lse1 * lse1);
-        a.loss[row] = flush(__double2float_rn(v));
-        st[0] = M;
-        st[1] = l;
-        st[2] = none ? M : flush(__double2float_rn(lse_t));
-        st[3] = l1;
-        st[4] = SUMS == SOFT ? 0.0f : none ? M : flush(__double2float_rn(lse1));
-        st[5] = mt;
-        st[6] = lt;
-        st[7] = P;
+        const int64_t at = (int64_t)row * a.nblk + blk;
+        a.ms[at] = make_float2(m, s);
+        if (SUMS >= BOTH)
+            a.s1[at] = s1;
     }
+}
+
+constexpr int WARPS = 8;
+constexpr int MAX_ROWS = 8;   // rows a CTA joins at a time
+
+struct RowShared {
+    float M[MAX_ROWS], l[MAX_ROWS], l1[MAX_ROWS], mt[MAX_ROWS], lt[MAX_ROWS], P[MAX_ROWS];
+    double ln[3][MAX_ROWS];
+};
+
+// a_k of an entry, and its column (-1: empty)
+__device__ __forceinline__ float teacher(const FwdArgs& a, int64_t at, int& j)
+{
+    const int64_t c = load_index(a.t_idx, a.index_bytes, at);
+    if (c >= a.V)
+        atomicOr(a.err, kErrIndexBit);
+    j = c < 0 || c >= a.V ? -1 : (int)c;
+    if (j < 0)
+        return -CUDART_INF_F;
+    const float t = flush(a.t_type == 0 ? static_cast<const float*>(a.t_val)[at]
+                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(a.t_val)[at]));
+    return a.logprobs ? t : fmul_flush(t, a.it);
+}
+
+// joins the blocks of rows [r0, r0 + cnt), forms the teacher's weights and the
+// losses.  A warp per row, but the logarithms: binary64 runs at 1/64 of the
+// binary32 rate here whether one lane needs it or 32, so one warp takes all of the
+// CTA's logarithms, a lane each.
+template <typename T, int SUMS>
+__device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, int cnt, RowShared& sh)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int r = warp; r < cnt; r += WARPS) {
+        const int64_t row = r0 + r;
+        const float2* ms = a.ms + row * a.nblk;
+        float M = -CUDART_INF_F;
+        for (int b = lane; b < a.nblk; b += 32)
+            M = max_nan(M, ms[b].x);
+        M = warp_max(M);
+        M = M == 0.0f ? 0.0f : M;
+        const float Mu = fmul_flush(M, a.it);
+        float l = 0.0f, l1 = 0.0f;
+        if (M != -CUDART_INF_F) {
+            for (int b = lane; b < a.nblk; b += 32) {
+                const float2 v = ms[b];
+                l = fadd_ftz(l, fmul_rn(v.y, exp_neg(fadd_ftz(fmul_rn(v.x, a.it), -Mu))));
+                if (SUMS >= BOTH)
+                    l1 = fadd_ftz(l1, fmul_rn(a.s1[row * a.nblk + b], exp_neg(fadd_ftz(v.x, -M))));
+            }
+            l = warp_tree(l);
+            l1 = SUMS >= BOTH ? warp_tree(l1) : SUMS == ONE ? l : 0.0f;
+        }
+        float* p = a.stats + row * (STATS + a.K) + STATS;
+        float mt = a.logprobs ? 0.0f : -CUDART_INF_F, lt = 0.0f, P = 0.0f;
+        int j;
+        if (!a.logprobs) {
+            for (int k = lane; k < a.K; k += 32)
+                mt = max_nan(mt, teacher(a, row * a.K + k, j));
+            mt = warp_max(mt);
+            mt = mt == 0.0f ? 0.0f : mt;
+        }
+        if (mt == -CUDART_INF_F) {
+            for (int k = lane; k < a.K; k += 32)
+                p[k] = 0.0f;
+        } else {
+            for (int k = lane; k < a.K; k += 32) {
+                const float e = exp_neg(fadd_ftz(teacher(a, row * a.K + k, j), -mt));
+                lt = fadd_ftz(lt, e);
+                p[k] = e;
+            }
+            lt = warp_tree(lt);
+            P = a.logprobs ? lt : lt == lt ? 1.0f : lt;
+            lt = a.logprobs ? 1.0f : lt;
+        }
+        if (lane == 0) {
+            sh.M[r] = M;
+            sh.l[r] = l;
+            sh.l1[r] = l1;
+            sh.mt[r] = mt;
+            sh.lt[r] = lt;
+            sh.P[r] = P;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 3 * MAX_ROWS) {
+        const int which = threadIdx.x / MAX_ROWS, r = threadIdx.x % MAX_ROWS;
+        if (r < cnt)
+            sh.ln[which][r] = ln_d(which == 0 ? sh.l[r] : which == 1 ? sh.lt[r] : sh.l1[r]);
+    }
+    __syncthreads();
+    for (int r = warp; r < cnt; r += WARPS) {
+        const int64_t row = r0 + r;
+        const float M = sh.M[r], mt = sh.mt[r], lt = sh.lt[r];
+        const bool none = M == -CUDART_INF_F;
+        const double lse_t = none ? 0.0 : (double)fmul_flush(M, a.it) + sh.ln[0][r];
+        const double lse1 = none || SUMS == SOFT ? 0.0 : (double)M + sh.ln[2][r];
+        float* st = a.stats + row * (STATS + a.K);
+        float* p = st + STATS;
+        double v = 0.0;
+        if (mt != -CUDART_INF_F) {
+            const double cst = none ? 0.0 : lse_t - ((double)mt + sh.ln[1][r]);
+            double sum = 0.0;
+            for (int k = lane; k < a.K; k += 32) {
+                float w = p[k];
+                if (!a.logprobs) {
+                    w = flush(__fdiv_rn(w, lt));
+                    p[k] = w;
+                }
+                if (w != 0.0f && !none && a.w_kd != 0.0f) {
+                    int j;
+                    const float ak = teacher(a, row * a.K + k, j);
+                    const float u = fmul_flush(flush(to_f32<T>(z[row * z_ld + j])), a.it);
+                    sum = sum + (double)w * (((double)ak - (double)u) + cst);
+                }
+            }
+            if (!none && a.w_kd != 0.0f)
+                v = ((double)a.w_kd * ((double)a.tau * (double)a.tau)) * warp_tree(sum);
+        }
+        if (lane == 0) {
+            if (a.w_ce != 0.0f) {
+                const int64_t lab = load_index(a.labels, a.index_bytes, row);
+                if (lab >= a.V)
+                    atomicOr(a.err, kErrIndexBit);
+                else if (lab >= 0 && !none)
+                    v = v + (double)a.w_ce * (lse1 - (double)flush(to_f32<T>(z[row * z_ld + lab])));
+            }
+            if (a.w_z != 0.0f && !none)
+                v = v + (double)a.w_z * (lse1 * lse1);
+            a.loss[row] = flush(__double2float_rn(v));
+            st[0] = M;
+            st[1] = sh.l[r];
+            st[2] = none ? M : flush(__double2float_rn(lse_t));
+            st[3] = sh.l1[r];
+            st[4] = SUMS == SOFT ? 0.0f : none ? M : flush(__double2float_rn(lse1));
+            st[5] = mt;
+            st[6] = lt;
+            st[7] = sh.P[r];
+        }
+    }
+}
+
+// a CTA owns `rows` rows: their blocks, then their losses
+template <typename T, int SUMS, bool VEC>
+__global__ void __launch_bounds__(32 * WARPS)
+k_distill_fwd(const T* z, int64_t z_ld, const __grid_constant__ FwdArgs a, int rows)
+{
+    __shared__ RowShared sh;
+    const int lane = threadIdx.x & 31;
+    const int r0 = blockIdx.x * rows, cnt = min(rows, a.n - r0), items = cnt * a.nblk;
+    for (int i = threadIdx.x >> 5; i < items; i += WARPS) {
+        const int r = i / a.nblk;
+        do_block<T, SUMS, VEC>(z, z_ld, a, r0 + r, i - r * a.nblk, lane);
+    }
+    __syncthreads();
+    finish_rows<T, SUMS>(z, z_ld, a, r0, cnt, sh);
+}
+
+template <typename T, int SUMS, bool VEC>
+__global__ void __launch_bounds__(32 * WARPS)
+k_distill_blocks(const T* z, int64_t z_ld, const __grid_constant__ FwdArgs a)
+{
+    const int item = blockIdx.x * WARPS + (threadIdx.x >> 5);
+    if (item >= a.n * a.nblk)
+        return;
+    const int row = item / a.nblk;
+    do_block<T, SUMS, VEC>(z, z_ld, a, row, item - row * a.nblk, threadIdx.x & 31);
+}
+
+template <typename T, int SUMS>
+__global__ void __launch_bounds__(32 * WARPS)
+k_distill_rows(const T* z, int64_t z_ld, const __grid_constant__ FwdArgs a)
+{
+    __shared__ RowShared sh;
+    pdl_wait();
+    const int r0 = blockIdx.x * MAX_ROWS;
+    finish_rows<T, SUMS>(z, z_ld, a, r0, min(MAX_ROWS, a.n - r0), sh);
 }
 
 struct BwdArgs {
     const void* t_idx;
     const void* labels;
     int index_bytes;
-    int64_t V, K, nblk, items;
+    int V, K, nblk, groups, items, per;
     float it, tau, w_kd, w_ce, w_z;
     const float* stats;
     const float* g;
     int64_t g_stride;
 };
 
-// v at block element e, if this lane has it: `slot` and `own` are uniform
-__device__ __forceinline__ void subtract_at(float (&v)[PER], int slot, bool mine, float c)
-{
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (i == slot && mine)
-            v[i] = fadd_ftz(v[i], -c);
-}
-
-template <typename T, int SUMS, bool VEC>
-__global__ void __launch_bounds__(256)
-k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const BwdArgs a)
+// One warp takes `per` consecutive blocks of a row, so that what belongs to the row
+// (statistics, coefficients and their divisions) is done once.  The order of the
+// elements does not matter here: where z and dz start equally far past a 4-element
+// boundary (SHIFT), a row's blocks are cut at those boundaries and all but the
+// row's ends move four elements at a time, whatever the vocabulary's remainder.
+// Block element i of lane: EACH: 32 i + lane; SHIFT: 128 (i / 4) + 4 lane + i mod 4.
+template <typename T, int SUMS, bool SHIFT>
+__global__ void __launch_bounds__(32 * WARPS)
+k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_constant__ BwdArgs a)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int item = blockIdx.x * WARPS + (threadIdx.x >> 5);
     if (item >= a.items)
         return;
-    const int64_t row = item / a.nblk, blk = item - row * a.nblk, lo = blk * BLK;
-    const int len = (int)(a.V - lo < BLK ? a.V - lo : BLK);
-    float x[PER];
-    load_block<T, VEC>(z + row * z_ld + lo, len, lane, x);
-    const float* st = a.stats + row * (STATS + a.K);
+    const int row = item / a.groups, first = (item - row * a.groups) * a.per;
+    const T* zr = z + row * z_ld;
+    T* dr = dz + row * dz_ld;
+    const int shift = SHIFT ? (int)((reinterpret_cast<uintptr_t>(zr) / sizeof(T)) & 3) : 0;
+    const float* st = a.stats + (int64_t)row * (STATS + a.K);
     const float M = st[0], l = st[1], l1 = st[3], lse1 = st[4], P = st[7];
     const float g = flush(a.g[row * a.g_stride]);
-    int64_t lab = -1;
+    int lab = -1;
     if (a.w_ce != 0.0f) {
-        lab = load_index(a.labels, a.index_bytes, row);
-        lab = lab < a.V ? lab : -1;
+        const int64_t t = load_index(a.labels, a.index_bytes, row);
+        lab = t >= 0 && t < a.V ? (int)t : -1;
     }
     const float gk = fmul_flush(fmul_flush(g, a.w_kd), a.tau);
     const float ca = fmul_flush(gk, P);
     const float cb = fmul_flush(g, fadd_ftz(lab >= 0 ? a.w_ce : 0.0f,
                                             fmul_rn(fmul_flush(2.0f, a.w_z), a.w_z != 0.0f ? lse1 : 0.0f)));
     const float qa = flush(__fdiv_rn(SUMS == ONE ? fadd_ftz(ca, cb) : ca, l));
-    const float qb = SUMS == BOTH ? flush(__fdiv_rn(cb, l1)) : 0.0f;
+    const float qb = SUMS >= BOTH ? flush(__fdiv_rn(cb, l1)) : 0.0f;
     const bool none = M == -CUDART_INF_F;
     const float Mu = fmul_flush(M, a.it);
     const u64 zero = dup2(-0.0f), nu = dup2(-Mu), nm = dup2(-M), sc = dup2(a.it), wa = dup2(qa), wb = dup2(qb);
-#pragma unroll
-    for (int i = 0; i < PER; i += 2) {
-        const u64 v = pack2(x[i], x[i + 1]);
-        const u64 u = SUMS == ONE ? v : fmul2_rn(fadd2_ftz(v, zero), sc);
-        u64 d = fadd2_ftz(fmul2_rn(exp_neg2(fadd2_ftz(u, nu)), wa), zero);
-        if (SUMS == BOTH)
-            d = fadd2_ftz(d, fmul2_rn(exp_neg2(fadd2_ftz(v, nm)), wb));
-        unpack2(d, x[i], x[i + 1]);
-    }
-    // the teacher's entries and the label inside this block, entry by entry
-    auto take = [&](int64_t e, float c) {
-        const int el = (int)e;
-        const int slot = VEC ? (el >> 7) * 4 + (el & 3) : el >> 5;
-        const int own = VEC ? (el >> 2) & 31 : el & 31;
-        subtract_at(x, slot, lane == own, c);
-    };
-    if (a.w_kd != 0.0f)
-        for (int64_t k0 = 0; k0 < a.K; k0 += 32) {
-            int64_t e = -1;
-            if (k0 + lane < a.K)
-                e = load_index(a.t_idx, a.index_bytes, row * a.K + k0 + lane) - lo;
-            unsigned hits = __ballot_sync(0xffffffffu, e >= 0 && e < len);
-            if (hits == 0)
-                continue;
-            const float c = e >= 0 && e < len ? fmul_flush(gk, st[STATS + k0 + lane]) : 0.0f;
-            while (hits) {
-                const int src = __ffs(hits) - 1;
-                hits &= hits - 1;
-                take(__shfl_sync(0xffffffffu, (int)e, src), __shfl_sync(0xffffffffu, c, src));
-            }
-        }
-    if (lab >= lo && lab < lo + len)
-        take(lab - lo, fmul_flush(g, a.w_ce));
-    if (none) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            x[i] = 0.0f;
-    }
-    T* out = dz + row * dz_ld + lo;
-    if (VEC) {
+    const int last = min(first + a.per, a.nblk);
+    for (int blk = first; blk < last; ++blk) {
+        const int lo = blk * BLK - shift;
+        if (lo >= a.V)
+            break;
+        float x[PER];
 #pragma unroll
         for (int i = 0; i < PER; i += 4) {
-            const int e = element<true>(i, lane);
-            if (e + 4 <= len) {
-                store4(out + e, make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+            if (SHIFT) {
+                const int e = lo + 32 * i + 4 * lane;
+                if (e >= 0 && e + 4 <= a.V) {
+                    const float4 v = load4(zr + e);
+                    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        x[i + c] = e + c >= 0 && e + c < a.V ? to_f32<T>(zr[e + c]) : -CUDART_INF_F;
+                }
             } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (e + c < len)
-                        out[e + c] = from_f32<T>(x[i + c]);
+                for (int c = 0; c < 4; ++c) {
+                    const int e = lo + 32 * (i + c) + lane;
+                    x[i + c] = e < a.V ? to_f32<T>(zr[e]) : -CUDART_INF_F;
+                }
             }
         }
-    } else {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = element<false>(i, lane);
-            if (e < len)
-                out[e] = from_f32<T>(x[i]);
+        for (int i = 0; i < PER; i += 2) {
+            const u64 v = pack2(x[i], x[i + 1]);
+            const u64 e = exp_neg2(fadd2_ftz(SUMS == ONE ? v : fmul2_rn(v, sc), nu));
+            u64 d = fmul2_rn(e, wa);
+            if (SUMS >= BOTH)
+                d = fadd2_ftz(d, fmul2_rn(SUMS == BOTH ? exp_neg2(fadd2_ftz(v, nm)) : power2<SUMS>(e), wb));
+            else
+                d = fadd2_ftz(d, zero);
+            unpack2(d, x[i], x[i + 1]);
+        }
+        // the teacher's entries and the label inside this block, entry by entry
+        auto take = [&](int e, float c) {
+            const int slot = SHIFT ? (e >> 7) * 4 + (e & 3) : e >> 5;
+            const int own = SHIFT ? (e >> 2) & 31 : e & 31;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (i == slot && lane == own)
+                    x[i] = fadd_ftz(x[i], -c);
+        };
+        if (a.w_kd != 0.0f)
+            for (int k0 = 0; k0 < a.K; k0 += 32) {
+                int e = -1;
+                if (k0 + lane < a.K) {
+                    const int64_t j = load_index(a.t_idx, a.index_bytes, (int64_t)row * a.K + k0 + lane);
+                    e = j >= max(lo, 0) && j < min((int64_t)lo + BLK, (int64_t)a.V) ? (int)j - lo : -1;
+                }
+                unsigned hits = __ballot_sync(0xffffffffu, e >= 0);
+                if (hits == 0)
+                    continue;
+                const float c = e >= 0 ? fmul_flush(gk, st[STATS + k0 + lane]) : 0.0f;
+                while (hits) {
+                    const int src = __ffs(hits) - 1;
+                    hits &= hits - 1;
+                    take(__shfl_sync(0xffffffffu, e, src), __shfl_sync(0xffffffffu, c, src));
+                }
+            }
+        if (lab >= max(lo, 0) && lab < lo + BLK)
+            take(lab - lo, fmul_flush(g, a.w_ce));
+        if (none) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                x[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+            if (SHIFT) {
+                const int e = lo + 32 * i + 4 * lane;
+                if (e >= 0 && e + 4 <= a.V) {
+                    store4(dr + e, make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (e + c >= 0 && e + c < a.V)
+                            dr[e + c] = from_f32<T>(x[i + c]);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int e = lo + 32 * (i + c) + lane;
+                    if (e < a.V)
+                        dr[e] = from_f32<T>(x[i + c]);
+                }
+            }
         }
     }
 }
@@ -474,59 +579,75 @@ int64_t blocks_of(int64_t V) { return (V + BLK - 1) / BLK; }
 
 int sums_of(const DistillArgs& a)
 {
-    return a.tau == 1.0f ? ONE : a.w_ce != 0.0f || a.w_z != 0.0f ? BOTH : SOFT;
+    if (a.tau == 1.0f)
+        return ONE;
+    if (a.w_ce == 0.0f && a.w_z == 0.0f)
+        return SOFT;
+    return a.tau == 2.0f ? SQR1 : a.tau == 4.0f ? SQR2 : BOTH;
 }
 
 // calls f(SUMS) as a compile-time constant
 template <typename F> cudaError_t by_sums(int sums, F f)
 {
-    if (sums == ONE)
-        return f(std::integral_constant<int, ONE>());
-    if (sums == SOFT)
-        return f(std::integral_constant<int, SOFT>());
-    return f(std::integral_constant<int, BOTH>());
+    switch (sums) {
+    case ONE: return f(std::integral_constant<int, ONE>());
+    case SOFT: return f(std::integral_constant<int, SOFT>());
+    case BOTH: return f(std::integral_constant<int, BOTH>());
+    case SQR1: return f(std::integral_constant<int, SQR1>());
+    default: return f(std::integral_constant<int, SQR2>());
+    }
 }
 
 template <typename T> cudaError_t fwd_typed(const DistillArgs& a, void* ws, cudaStream_t st)
 {
     const T* z = static_cast<const T*>(a.z);
     const int64_t nblk = blocks_of(a.V), items = a.n * nblk;
-    const float it = 1.0f / a.tau;
-    float2* ms = static_cast<float2*>(ws);
-    float* s1 = reinterpret_cast<float*>(ms + items);
     const bool vec = rows4<T>(a.z, a.z_ld);
-    RowArgs r;
+    FwdArgs r;
     r.t_idx = a.t_idx;
     r.t_val = a.t_val;
     r.t_type = a.t_type;
     r.labels = a.labels;
     r.index_bytes = a.index_bytes;
-    r.n = a.n;
-    r.V = a.V;
-    r.K = a.K;
-    r.nblk = nblk;
-    r.it = it;
+    r.n = (int)a.n;
+    r.V = (int)a.V;
+    r.K = (int)a.K;
+    r.nblk = (int)nblk;
+    r.it = 1.0f / a.tau;
     r.tau = a.tau;
     r.w_kd = a.w_kd;
     r.w_ce = a.w_ce;
     r.w_z = a.w_z;
     r.logprobs = a.logprobs;
-    r.ms = ms;
-    r.s1 = s1;
+    r.ms = static_cast<float2*>(ws);
+    r.s1 = reinterpret_cast<float*>(r.ms + items);
     r.loss = a.loss;
     r.stats = a.stats;
     r.err = a.err;
+    // rows per CTA: two of at least 8 blocks, more of shorter ones
+    const int rows = nblk >= 8 ? 2 : nblk >= 4 ? 4 : MAX_ROWS;
+    const bool owned = (a.n + rows - 1) / rows >= 4 * num_sms();
     return by_sums(sums_of(a), [&](auto s) {
         constexpr int SUMS = decltype(s)::value;
-        const unsigned grid = (unsigned)((items + 7) / 8);
+        if (owned) {
+            const unsigned grid = (unsigned)((a.n + rows - 1) / rows);
+            if (vec)
+                k_distill_fwd<T, SUMS, true><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, r, rows);
+            else
+                k_distill_fwd<T, SUMS, false><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, r, rows);
+            count_launches(1);
+            return cudaGetLastError();
+        }
+        const unsigned grid = (unsigned)((items + WARPS - 1) / WARPS);
         if (vec)
-            k_distill_blocks<T, SUMS, true><<<grid, 256, 0, st>>>(z, a.z_ld, a.V, nblk, items, it, ms, s1);
+            k_distill_blocks<T, SUMS, true><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, r);
         else
-            k_distill_blocks<T, SUMS, false><<<grid, 256, 0, st>>>(z, a.z_ld, a.V, nblk, items, it, ms, s1);
+            k_distill_blocks<T, SUMS, false><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, r);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess)
             return e;
-        e = launch_pdl(k_distill_rows<T, SUMS>, dim3((unsigned)((a.n + 3) / 4)), dim3(128), 0, st, z, a.z_ld, r);
+        e = launch_pdl(k_distill_rows<T, SUMS>, dim3((unsigned)((a.n + MAX_ROWS - 1) / MAX_ROWS)), dim3(32 * WARPS),
+                       0, st, z, a.z_ld, r);
         count_launches(2);
         return e;
     });
@@ -540,10 +661,8 @@ template <typename T> cudaError_t bwd_typed(const DistillArgs& a, cudaStream_t s
     b.t_idx = a.t_idx;
     b.labels = a.labels;
     b.index_bytes = a.index_bytes;
-    b.V = a.V;
-    b.K = a.K;
-    b.nblk = blocks_of(a.V);
-    b.items = a.n * b.nblk;
+    b.V = (int)a.V;
+    b.K = (int)a.K;
     b.it = 1.0f / a.tau;
     b.tau = a.tau;
     b.w_kd = a.w_kd;
@@ -552,14 +671,21 @@ template <typename T> cudaError_t bwd_typed(const DistillArgs& a, cudaStream_t s
     b.stats = a.stats;
     b.g = a.g;
     b.g_stride = a.g_stride;
-    const bool vec = rows4<T>(a.z, a.z_ld) && rows4<T>(a.dz, a.dz_ld);
+    // whole 4-element groups where both rows start equally far past a boundary
+    const uintptr_t zs = reinterpret_cast<uintptr_t>(a.z) / sizeof(T), ds = reinterpret_cast<uintptr_t>(a.dz) / sizeof(T);
+    const bool shift = zs % 4 == ds % 4 && (a.z_ld - a.dz_ld) % 4 == 0;
+    b.nblk = (int)blocks_of(a.V + (shift ? 3 : 0));
+    // four blocks a warp once that leaves every scheduler several warps
+    b.per = a.n * b.nblk >= (int64_t)num_sms() * 128 ? 4 : 1;
+    b.groups = (b.nblk + b.per - 1) / b.per;
+    b.items = (int)(a.n * b.groups);
     return by_sums(sums_of(a), [&](auto s) {
         constexpr int SUMS = decltype(s)::value;
-        const unsigned grid = (unsigned)((b.items + 7) / 8);
-        if (vec)
-            k_distill_bwd<T, SUMS, true><<<grid, 256, 0, st>>>(z, a.z_ld, dz, a.dz_ld, b);
+        const unsigned grid = (unsigned)((b.items + WARPS - 1) / WARPS);
+        if (shift)
+            k_distill_bwd<T, SUMS, true><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, dz, a.dz_ld, b);
         else
-            k_distill_bwd<T, SUMS, false><<<grid, 256, 0, st>>>(z, a.z_ld, dz, a.dz_ld, b);
+            k_distill_bwd<T, SUMS, false><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, dz, a.dz_ld, b);
         count_launches(1);
         return cudaGetLastError();
     });

@@ -16,7 +16,7 @@
 //      same launch zero the table rows that no token names (each marks its own
 //      rows' tokens in a bitmap first), so the sort hides behind the
 //      part of the write that needs no order.
-//   2. k_embed_sum: one warp per (chunk, 256 columns), left to right from the
+//   2. k_embed_sum: one warp per (chunk, 512 columns), left to right from the
 //      first term; a token's only chunk is scaled and stored, others leave their
 //      partial row in the workspace.
 //   3. k_row_tree (k_rowtree.cu): the pairwise tree over a token's partial rows;
@@ -104,6 +104,7 @@ constexpr int SORT_CTAS = 8;      // CTAs of the sorting cluster
 constexpr int SORT_NT = 1024;
 constexpr int SORT_W = SORT_NT / 32;
 constexpr int DIGITS = 256;
+constexpr int LONG = 8;           // chunks of more positions than this are summed first
 
 struct SortArgs {
     const void* tokens;
@@ -113,8 +114,9 @@ struct SortArgs {
     int64_t pad;
     uint2* a;            // (token, position), written by passes 0, 2, ..
     uint2* b;            // .. and by passes 1, 3
-    int* counts;         // [0] chunks listed, [1] tokens with several chunks
-    int4* chunks;        // {first sorted index, length, token, partial row or -1}
+    int2* seg;           // [V] first and one past the last sorted index of a named token
+    int* counts;         // chunks at the list's front, tokens with several chunks, chunks at its back
+    int4* chunks;        // [n] {first sorted index, length, token, partial row or -1}
     int4* joins;         // {first sorted index, chunks, token, 0}
     float* table;        // rows to zero, or NULL
     int64_t table_ld;
@@ -142,33 +144,6 @@ __device__ __forceinline__ unsigned sort_key(const SortArgs& a, int i, bool repo
 __device__ __forceinline__ uint2 ld_pair(const uint2* p) { return __ldcg(p); }
 __device__ __forceinline__ unsigned ld_tok(const uint2* s, int i) { return __ldcg(&s[i].x); }
 
-// first index in [0, hi] whose token is >= key, given that s[hi] has it
-__device__ int lower_bound(const uint2* s, int hi, unsigned key)
-{
-    int lo = 0;
-    while (lo < hi) {
-        const int m = (lo + hi) >> 1;
-        if (ld_tok(s, m) < key)
-            lo = m + 1;
-        else
-            hi = m;
-    }
-    return lo;
-}
-
-// one past the last index of `key`, given that s[lo] has it
-__device__ int upper_bound(const uint2* s, int lo, int hi, unsigned key)
-{
-    while (lo < hi) {
-        const int m = (lo + hi) >> 1;
-        if (ld_tok(s, m) <= key)
-            lo = m + 1;
-        else
-            hi = m;
-    }
-    return lo;
-}
-
 __device__ void sort_cluster(const SortArgs& a, SortSmem& sm)
 {
     cg::cluster_group cluster = cg::this_cluster();
@@ -177,7 +152,7 @@ __device__ void sort_cluster(const SortArgs& a, SortSmem& sm)
     // each warp owns a run of 32-element rounds, so that (CTA, warp, round, lane) is position order
     const int rounds = (a.n + SORT_CTAS * SORT_NT - 1) / (SORT_CTAS * SORT_NT);
     const int base = (rank * SORT_W + warp) * rounds * 32;
-    if (rank == 0 && tid < 2)
+    if (rank == 0 && tid < 3)
         a.counts[tid] = 0;
     const uint2* src = nullptr;
     uint2* dst = a.a;
@@ -256,29 +231,37 @@ __device__ void sort_cluster(const SortArgs& a, SortSmem& sm)
         src = dst;
         dst = dst == a.a ? a.b : a.a;
     }
-    // the chunks: sorted index i starts one when it is a multiple of 64 past its token's first
+    // where every named token's positions begin and end
     for (int i = rank * SORT_NT + tid; i < a.n; i += SORT_CTAS * SORT_NT) {
         const unsigned key = ld_tok(src, i);
         if (key >= (unsigned)a.V)
             continue;
-        int first = i;
-        if (i > 0 && ld_tok(src, i - 1) == key) {
-            if (i < 64 || ld_tok(src, i - 64) != key)
-                continue;
-            first = lower_bound(src, i, key);
-            if ((i - first) & 63)
-                continue;
-        }
-        const int hi = i + 64 < a.n ? i + 64 : a.n;
-        const int end = ld_tok(src, hi - 1) == key ? hi : upper_bound(src, i, hi, key);
-        const bool several = first != i || (end == i + 64 && end < a.n && ld_tok(src, end) == key);
+        if (i == 0 || ld_tok(src, i - 1) != key)
+            a.seg[key].x = i;
+        if (i == a.n - 1 || ld_tok(src, i + 1) != key)
+            a.seg[key].y = i + 1;
+    }
+    __threadfence();
+    cluster.sync();
+    // the chunks: sorted index i starts one when it is a multiple of 64 past its token's
+    // first.  Long ones are listed from the front, short ones from the back, so that
+    // the sums start with what takes longest.
+    for (int i = rank * SORT_NT + tid; i < a.n; i += SORT_CTAS * SORT_NT) {
+        const unsigned key = ld_tok(src, i);
+        if (key >= (unsigned)a.V)
+            continue;
+        const int2 g = __ldcg(&a.seg[key]);
+        if ((i - g.x) & 63)
+            continue;
+        const bool several = g.y - g.x > 64;
+        const int len = g.y - i < 64 ? g.y - i : 64;
         // a partial row of its own: in a run of 64 sorted indexes at most one chunk of a
         // token with several starts that is its first, and at most one that is not
-        const int slot = several ? 2 * (i >> 6) + (first == i ? 1 : 0) : -1;
-        a.chunks[atomicAdd(&a.counts[0], 1)] = make_int4(i, end - i, (int)key, slot);
-        if (several && first == i)
-            a.joins[atomicAdd(&a.counts[1], 1)] =
-                make_int4(i, (upper_bound(src, i, a.n, key) - i + 63) / 64, (int)key, 0);
+        const int slot = several ? 2 * (i >> 6) + (g.x == i ? 1 : 0) : -1;
+        const int at = len > LONG ? atomicAdd(&a.counts[0], 1) : a.n - 1 - atomicAdd(&a.counts[2], 1);
+        a.chunks[at] = make_int4(i, len, (int)key, slot);
+        if (several && g.x == i)
+            a.joins[atomicAdd(&a.counts[1], 1)] = make_int4(i, (g.y - g.x + 63) / 64, (int)key, 0);
     }
 }
 
@@ -290,10 +273,15 @@ __device__ void zero_rows(const SortArgs& a, unsigned* bits, int v0, int v1)
     for (int i = tid; i < words; i += SORT_NT)
         bits[i] = 0u;
     __syncthreads();
-    for (int i = tid; i < a.n; i += SORT_NT) {
-        const int64_t t = load_index(a.tokens, a.index_bytes, i);
-        if (t >= v0 && t < v1 && t != a.pad)
-            atomicOr(&bits[(t - v0) >> 5], 1u << ((t - v0) & 31));
+    for (int i0 = tid; i0 < a.n; i0 += 8 * SORT_NT) {
+        int64_t t[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            t[u] = i0 + u * SORT_NT < a.n ? load_index(a.tokens, a.index_bytes, i0 + u * SORT_NT) : -1;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (t[u] >= v0 && t[u] < v1 && t[u] != a.pad)
+                atomicOr(&bits[(t[u] - v0) >> 5], 1u << ((t[u] - v0) & 31));
     }
     __syncthreads();
     for (int v = v0 + warp; v < v1; v += SORT_W) {
@@ -327,40 +315,49 @@ k_embed_sort(const SortArgs a)
 
 // ---------------------------------------------------------------- chunk sums
 
-constexpr int ES_G = 2;             // 4-element groups per lane
+constexpr int ES_G = 4;             // 4-element groups per lane
 constexpr int ES_COLS = 32 * 4 * ES_G;
-constexpr int ES_U = 4;             // rows in flight
+constexpr int ES_U = 2;             // rows in flight
 
-template <typename TD>
+// One warp per (chunk, 512 columns).  What a warp needs next (the chunk's entry, then
+// its positions) is fetched while the rows of the one before are on their way:
+// most tokens occur once or twice, so each chunk would otherwise cost three
+// dependent trips to memory.
+template <typename TD, bool VEC>
 __global__ void __launch_bounds__(256)
 k_embed_sum(const TD* __restrict__ dout, int64_t dout_ld, const uint2* __restrict__ sorted,
-            const int* __restrict__ counts, const int4* __restrict__ chunks, int64_t D, float scale,
+            const int* __restrict__ counts, const int4* __restrict__ chunks, int n, int64_t D, float scale,
             float* __restrict__ table, int64_t table_ld, bool accumulate, float* __restrict__ parts,
-            int segs, bool vec_in, bool vec_out)
+            int segs, bool vec_out)
 {
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t items = (int64_t)counts[0] * segs;
+    const int longs = counts[0];
+    const int64_t items = (int64_t)(longs + counts[2]) * segs, step = (int64_t)gridDim.x * 8;
     const float sc = flush(scale);
-    for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < items;
-         item += (int64_t)gridDim.x * 8) {
-        const int64_t ch = item / segs;
-        const int4 c = chunks[ch];
-        const int64_t c0 = (item - ch * segs) * ES_COLS;
-        // positions of the chunk's rows, one or two per lane
-        const unsigned p0 = lane < c.y ? sorted[c.x + lane].y : 0u;
-        const unsigned p1 = lane + 32 < c.y ? sorted[c.x + lane + 32].y : 0u;
-        float acc[ES_G][4];
-        // column of group g, element e: four neighbours, or lane-strided when rows are unaligned
-        auto col = [&](int g, int e) {
-            return c0 + (vec_in ? 4 * (lane + 32 * g) + e : lane + 32 * (4 * g + e));
-        };
+    const int64_t pitch = (D + 3) & ~3LL;
+    int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (item >= items)
+        return;
+    auto entry = [&](int64_t it) {
+        const int ch = (int)(it / segs);
+        return chunks[ch < longs ? ch : n - 1 - (ch - longs)];
+    };
+    auto position = [&](const int4& c, int j) { return j < c.y ? sorted[c.x + j].y : 0u; };
+    int4 c = entry(item), next = c;
+    unsigned p0 = position(c, lane), p1 = c.y > 32 ? position(c, lane + 32) : 0u;
+    if (item + step < items)
+        next = entry(item + step);
+    for (; item < items; item += step) {
+        const int64_t c0 = (item % segs) * ES_COLS;
+        // column of group g, element e: four neighbours, or lane-strided where rows are unaligned
+        auto col = [&](int g, int e) { return c0 + (VEC ? 4 * (lane + 32 * g) + e : lane + 32 * (4 * g + e)); };
         auto row = [&](int j, float (&x)[ES_G][4]) {
             const unsigned pos = __shfl_sync(0xffffffffu, j < 32 ? p0 : p1, j & 31);
             const TD* s = dout + (int64_t)pos * dout_ld;
 #pragma unroll
             for (int g = 0; g < ES_G; ++g) {
-                if (vec_in) {
+                if (VEC) {
                     if (col(g, 0) < D) {
                         const float4 v = load4(s + col(g, 0));
                         x[g][0] = v.x, x[g][1] = v.y, x[g][2] = v.z, x[g][3] = v.w;
@@ -373,13 +370,16 @@ k_embed_sum(const TD* __restrict__ dout, int64_t dout_ld, const uint2* __restric
                 }
             }
         };
-        float x[ES_U][ES_G][4] = {};
-        row(0, x[0]);
+        float acc[ES_G][4] = {}, x[ES_U][ES_G][4] = {};
+        row(0, acc);
+        // the next item's positions and the entry after it, behind the first row's loads
+        const unsigned q0 = position(next, lane), q1 = next.y > 32 ? position(next, lane + 32) : 0u;
+        const int4 after = item + 2 * step < items ? entry(item + 2 * step) : next;
 #pragma unroll
         for (int g = 0; g < ES_G; ++g)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                acc[g][e] = flush(x[0][g][e]);
+                acc[g][e] = flush(acc[g][e]);
         int j = 1;
         for (; j + ES_U <= c.y; j += ES_U) {
 #pragma unroll
@@ -402,43 +402,57 @@ k_embed_sum(const TD* __restrict__ dout, int64_t dout_ld, const uint2* __restric
                     acc[g][e] = fadd_ftz(acc[g][e], x[0][g][e]);
         }
         const bool part = c.w >= 0;
-        float* dst = part ? parts + (int64_t)c.w * ((D + 3) & ~3LL) : table + (int64_t)c.z * table_ld;
+        float* dst = part ? parts + (int64_t)c.w * pitch : table + (int64_t)c.z * table_ld;
+        const bool wide = VEC && (part || vec_out);
 #pragma unroll
         for (int g = 0; g < ES_G; ++g) {
-            if (!part) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    acc[g][e] = fmul_flush(acc[g][e], sc);
-                    if (accumulate && col(g, e) < D)
-                        acc[g][e] = fadd_ftz(dst[col(g, e)], acc[g][e]);
+            if (wide) {
+                if (col(g, 0) >= D)
+                    continue;
+                float4 v = make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
+                if (!part) {
+                    v = make_float4(fmul_flush(v.x, sc), fmul_flush(v.y, sc), fmul_flush(v.z, sc), fmul_flush(v.w, sc));
+                    if (accumulate) {
+                        const float4 o = load4(dst + col(g, 0));
+                        v = make_float4(fadd_ftz(o.x, v.x), fadd_ftz(o.y, v.y), fadd_ftz(o.z, v.z), fadd_ftz(o.w, v.w));
+                    }
                 }
-            }
-            if (vec_in && (part || vec_out)) {
-                if (col(g, 0) < D)
-                    store4(dst + col(g, 0), make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]));
+                store4(dst + col(g, 0), v);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (col(g, e) < D)
-                        dst[col(g, e)] = acc[g][e];
+                    if (col(g, e) < D) {
+                        float v = acc[g][e];
+                        if (!part) {
+                            v = fmul_flush(v, sc);
+                            if (accumulate)
+                                v = fadd_ftz(dst[col(g, e)], v);
+                        }
+                        dst[col(g, e)] = v;
+                    }
             }
         }
+        c = next;
+        next = after;
+        p0 = q0;
+        p1 = q1;
     }
 }
 
 // workspace: sorted pairs twice, chunk and join lists, counters, partial rows
 struct EmbedWs {
-    size_t a, b, chunks, joins, counts, parts, total;
+    size_t a, b, seg, chunks, joins, counts, parts, total;
 };
 
-EmbedWs embed_ws(int64_t n, int64_t D)
+EmbedWs embed_ws(int64_t n, int64_t V, int64_t D)
 {
     EmbedWs w;
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     const int64_t blocks = (n + 63) / 64;
     w.a = 0;
     w.b = w.a + up((size_t)n * 8);
-    w.chunks = w.b + up((size_t)n * 8);
+    w.seg = w.b + up((size_t)n * 8);
+    w.chunks = w.seg + up((size_t)V * 8);
     w.joins = w.chunks + up((size_t)n * 16);
     w.counts = w.joins + up((size_t)blocks * 16);
     w.parts = w.counts + 256;
@@ -479,11 +493,11 @@ cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, cudaStream_t st)
     }
 }
 
-size_t embed_bwd_ws_bytes(int64_t n, int64_t D) { return embed_ws(n, D).total; }
+size_t embed_bwd_ws_bytes(int64_t n, int64_t V, int64_t D) { return embed_ws(n, V, D).total; }
 
 cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
 {
-    const EmbedWs w = embed_ws(a.n, a.D);
+    const EmbedWs w = embed_ws(a.n, a.V, a.D);
     char* p = static_cast<char*>(ws);
     SortArgs s;
     s.tokens = a.tokens;
@@ -493,6 +507,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
     s.pad = a.pad;
     s.a = reinterpret_cast<uint2*>(p + w.a);
     s.b = reinterpret_cast<uint2*>(p + w.b);
+    s.seg = reinterpret_cast<int2*>(p + w.seg);
     s.chunks = reinterpret_cast<int4*>(p + w.chunks);
     s.joins = reinterpret_cast<int4*>(p + w.joins);
     s.counts = reinterpret_cast<int*>(p + w.counts);
@@ -526,14 +541,16 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
     const int64_t most = (a.n * segs + 7) / 8, cap = (int64_t)num_sms() * 8;
     const unsigned grid = (unsigned)(most < cap ? most : cap);
     const bool vec_out = s.vec;
-    auto sum = [&](auto kernel, auto type) {
+    auto sum = [&](auto type) {
         using T = decltype(type);
-        const bool vec_in = a.D % 4 == 0 && rows4<T>(a.dout, a.dout_ld);
-        return launch_pdl(kernel, dim3(grid), dim3(256), 0, st, static_cast<const T*>(a.dout), a.dout_ld,
-                          sorted, (const int*)s.counts, (const int4*)s.chunks, a.D, a.scale, a.table,
-                          a.table_ld, a.accumulate, parts, segs, vec_in, vec_out);
+        auto go = [&](auto kernel) {
+            return launch_pdl(kernel, dim3(grid), dim3(256), 0, st, static_cast<const T*>(a.dout), a.dout_ld,
+                              sorted, (const int*)s.counts, (const int4*)s.chunks, (int)a.n, a.D, a.scale,
+                              a.table, a.table_ld, a.accumulate, parts, segs, vec_out);
+        };
+        return a.D % 4 == 0 && rows4<T>(a.dout, a.dout_ld) ? go(k_embed_sum<T, true>) : go(k_embed_sum<T, false>);
     };
-    e = a.dout_type == 0 ? sum(k_embed_sum<float>, float()) : sum(k_embed_sum<__nv_bfloat16>, __nv_bfloat16());
+    e = a.dout_type == 0 ? sum(float()) : sum(__nv_bfloat16());
     count_launches(1);
     if (e != cudaSuccess || a.n <= 64)
         return e;
@@ -547,7 +564,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
     t.out_ld = a.table_ld;
     t.scale = a.scale;
     t.accumulate = a.accumulate;
-    return launch_row_tree(t, num_sms() * 2, st);
+    return launch_row_tree(t, num_sms() * 8, st);
 }
 
 } // namespace repro

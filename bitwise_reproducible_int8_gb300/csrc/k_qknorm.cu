@@ -23,6 +23,8 @@
 namespace repro {
 namespace {
 
+typedef unsigned long long u64;
+
 constexpr int INTER = 0, HALF = 1, GENERIC = 2;   // how a rotation partner is found
 
 
@@ -62,19 +64,21 @@ __device__ __forceinline__ void store_head(T* p, int d0, int D, const float (&x)
     }
 }
 
-// S of the terms a_e (x) b_e over the head: groups of 4 left to right, then the
-// pairwise tree, first within the lane, then over its LPH lanes.  A term past the
-// width counts as -0, which leaves every sum as it is.
-template <int E, int LPH>
-__device__ __forceinline__ float head_sum(const float (&a)[E], const float (&b)[E], int d0, int D)
+// In-lane part of S of the terms a_e (x) b_e: groups of 4 left to right, then the
+// pairwise tree over the lane's groups.  A term past the width counts as -0, which
+// leaves every sum as it is.
+template <int E>
+__device__ __forceinline__ float lane_sum(const u64 (&a)[E / 2], const u64 (&b)[E / 2], int d0, int D)
 {
     float g[E / 4];
 #pragma unroll
     for (int k = 0; k < E / 4; ++k) {
         float p[4];
+        unpack2(fmul2_rn(a[2 * k], b[2 * k]), p[0], p[1]);
+        unpack2(fmul2_rn(a[2 * k + 1], b[2 * k + 1]), p[2], p[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            p[e] = d0 + 4 * k + e < D ? fmul_rn(a[4 * k + e], b[4 * k + e]) : -0.0f;
+            p[e] = d0 + 4 * k + e < D ? p[e] : -0.0f;
         g[k] = fadd_ftz(fadd_ftz(fadd_ftz(p[0], p[1]), p[2]), p[3]);
     }
 #pragma unroll
@@ -82,83 +86,155 @@ __device__ __forceinline__ float head_sum(const float (&a)[E], const float (&b)[
 #pragma unroll
         for (int k = 0; k + s < E / 4; k += 2 * s)
             g[k] = fadd_ftz(g[k], g[k + s]);
-    float v = g[0];
+    return g[0];
+}
+
+// The tree over the LPH lanes of U rows at once.  At the first log2 U levels a lane
+// keeps half of the rows it still has and hands its partner the others, so 4 rows
+// take 6 exchanges instead of 20, and every row's sum ends up in its own lanes:
+// this lane gets row own_row<U>(lane), and lane_of<U>(u) holds row u.
+template <int U, int LPH> __device__ __forceinline__ float rows_tree(const float (&S)[U], int lane)
+{
+    constexpr unsigned ALL = 0xffffffffu;
+    float v;
+    int s = 1;
+    if (U == 4) {
+        const bool hi = lane & 1, hi2 = lane & 2;
+        const float a = fadd_ftz(hi ? S[2 % U] : S[0], __shfl_xor_sync(ALL, hi ? S[0] : S[2 % U], 1));
+        const float b = fadd_ftz(hi ? S[3 % U] : S[1 % U], __shfl_xor_sync(ALL, hi ? S[1 % U] : S[3 % U], 1));
+        v = fadd_ftz(hi2 ? b : a, __shfl_xor_sync(ALL, hi2 ? a : b, 2));
+        s = 4;
+    } else if (U == 2) {
+        const bool hi = lane & 1;
+        v = fadd_ftz(hi ? S[1 % U] : S[0], __shfl_xor_sync(ALL, hi ? S[0] : S[1 % U], 1));
+        s = 2;
+    } else {
+        v = S[0];
+    }
 #pragma unroll
-    for (int s = 1; s < LPH; s *= 2)
-        v = fadd_ftz(v, __shfl_xor_sync(0xffffffffu, v, s));
+    for (; s < LPH; s *= 2)
+        v = fadd_ftz(v, __shfl_xor_sync(ALL, v, s));
     return v;
 }
 
-// v turned by the position's angle (BACK: turned back), in place.  d0 + e >= R is
-// left alone.  cs: the position's row, R / 2 cosines then R / 2 sines.
-template <int E, int LPH, int MODE, bool BACK>
-__device__ __forceinline__ void rotate(float (&v)[E], const float* __restrict__ cs, int d0, int D, int R,
-                                       bool inter, float* row)
+template <int U> __device__ __forceinline__ int lane_of(int u) { return U == 4 ? (u >> 1) | ((u & 1) << 1) : u; }
+
+// S (/) D; by an exact product where D is a power of two
+__device__ __forceinline__ float over_width(float S, float width, float inv)
+{
+    return inv != 0.0f ? fmul_flush(S, inv) : flush(__fdiv_rn(S, width));
+}
+
+__device__ __forceinline__ float rnorm(float S, float width, float inv, float eps)
+{
+    return flush(__fdiv_rn(1.0f, flush(__fsqrt_rn(fadd_ftz(over_width(S, width, inv), eps)))));
+}
+
+// the turn of a position for this lane's elements: out_e = v_e c_e + w_e s_e, w_e the
+// other member of the pair, s_e with its sign (BACK: the turn undone)
+template <int E, int MODE, bool BACK>
+__device__ __forceinline__ void load_turn(u64 (&c)[E / 2], u64 (&s)[E / 2], const float* __restrict__ cs, int d0,
+                                          int R, bool inter)
 {
     const int half = R >> 1;
-    if (MODE == INTER) {
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            if (d0 + e < R) {
-                const int j = (d0 + e) >> 1;
-                const float c = flush(__ldg(cs + j)), s = flush(__ldg(cs + half + j));
-                const float a = v[e], b = v[e + 1];
-                const float as = fmul_rn(a, s), bs = fmul_rn(b, s);
-                v[e] = fadd_ftz(fmul_rn(a, c), BACK ? bs : -bs);
-                v[e + 1] = fadd_ftz(fmul_rn(b, c), BACK ? -as : as);
-            }
-    } else if (MODE == HALF) {
-        const int lane = threadIdx.x & 31, step = half / E;
-        const bool low = d0 < half, turns = d0 < R;
-        const int other = turns ? (low ? lane + step : lane - step) : lane;
-        float w[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            w[e] = __shfl_sync(0xffffffffu, v[e], other);
-        if (turns) {
+    const u64 z = pack2(-0.0f, -0.0f);
+    if (MODE == HALF) {
+        if (d0 < R) {
+            const bool low = d0 < half;
             const int j0 = low ? d0 : d0 - half;
-            const bool minus = low != BACK;   // a: c y_a - s y_b (turned back: +); b the other way round
+            const bool minus = low != BACK;
 #pragma unroll
             for (int g = 0; g < E; g += 4) {
-                const float4 c4 = __ldg(reinterpret_cast<const float4*>(cs + j0 + g));
-                const float4 s4 = __ldg(reinterpret_cast<const float4*>(cs + half + j0 + g));
-                const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float ws = fmul_rn(w[g + e], flush(s[e]));
-                    v[g + e] = fadd_ftz(fmul_rn(v[g + e], flush(c[e])), minus ? -ws : ws);
-                }
+                const float4 a = __ldg(reinterpret_cast<const float4*>(cs + j0 + g));
+                const float4 b = __ldg(reinterpret_cast<const float4*>(cs + half + j0 + g));
+                c[g / 2] = fadd2_ftz(pack2(a.x, a.y), z);
+                c[g / 2 + 1] = fadd2_ftz(pack2(a.z, a.w), z);
+                s[g / 2] = fadd2_ftz(minus ? pack2(-b.x, -b.y) : pack2(b.x, b.y), z);
+                s[g / 2 + 1] = fadd2_ftz(minus ? pack2(-b.z, -b.w) : pack2(b.z, b.w), z);
             }
         }
     } else {
-        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (d0 + e < D)
-                row[d0 + e] = v[e];
-        __syncwarp();
+        for (int e = 0; e < E; e += 2) {
+            float cc[2] = {0.0f, 0.0f}, ss[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int d = d0 + e;
-            if (d < R) {
-                const bool low = inter ? !(d & 1) : d < half;
-                const int j = inter ? d >> 1 : (low ? d : d - half);
-                const int o = inter ? d ^ 1 : (low ? d + half : d - half);
-                const float ws = fmul_rn(row[o], flush(__ldg(cs + half + j)));
-                v[e] = fadd_ftz(fmul_rn(v[e], flush(__ldg(cs + j))), low != BACK ? -ws : ws);
+            for (int i = 0; i < 2; ++i) {
+                const int d = d0 + e + i;
+                if (d < R) {
+                    const bool pairs = MODE == INTER || inter;
+                    const bool low = pairs ? !(d & 1) : d < half;
+                    const int j = pairs ? d >> 1 : (low ? d : d - half);
+                    cc[i] = __ldg(cs + j);
+                    ss[i] = __ldg(cs + half + j);
+                    ss[i] = low != BACK ? -ss[i] : ss[i];
+                }
             }
+            c[e / 2] = fadd2_ftz(pack2(cc[0], cc[1]), z);
+            s[e / 2] = fadd2_ftz(pack2(ss[0], ss[1]), z);
         }
     }
 }
 
-__device__ __forceinline__ float rnorm(float S, float width, float eps)
+// v turned in place; elements from R on are left alone
+template <int E, int MODE>
+__device__ __forceinline__ void turn(u64 (&v)[E / 2], const u64 (&c)[E / 2], const u64 (&s)[E / 2], int d0, int D,
+                                     int R, bool inter, float* row)
 {
-    const float ms = fadd_ftz(flush(__fdiv_rn(S, width)), eps);
-    return flush(__fdiv_rn(1.0f, flush(__fsqrt_rn(ms))));
+    const int half = R >> 1;
+    u64 w[E / 2];
+    if (MODE == INTER) {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            float a, b;
+            unpack2(v[i], a, b);
+            w[i] = pack2(b, a);
+        }
+    } else if (MODE == HALF) {
+        const int lane = threadIdx.x & 31, step = half / E;
+        const int other = d0 < half ? lane + step : d0 < R ? lane - step : lane;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            float a, b;
+            unpack2(v[i], a, b);
+            w[i] = pack2(__shfl_sync(0xffffffffu, a, other), __shfl_sync(0xffffffffu, b, other));
+        }
+    } else {
+        float x[E], y[E];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < E; i += 2)
+            unpack2(v[i / 2], x[i], x[i + 1]);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (d0 + e < D)
+                row[d0 + e] = x[e];
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int d = d0 + e;
+            y[e] = d < R ? row[inter ? d ^ 1 : d < half ? d + half : d - half] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < E; i += 2)
+            w[i / 2] = pack2(y[i], y[i + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+        const u64 t = fadd2_ftz(fmul2_rn(v[i], c[i]), fmul2_rn(w[i], s[i]));
+        if (MODE == HALF) {   // a lane's elements lie on one side of R
+            if (d0 < R)
+                v[i] = t;
+        } else {
+            float t0, t1, v0, v1;
+            unpack2(t, t0, t1);
+            unpack2(v[i], v0, v1);
+            v[i] = pack2(d0 + 2 * i < R ? t0 : v0, d0 + 2 * i + 1 < R ? t1 : v1);
+        }
+    }
 }
 
-// the row of the table for a token's position, or NULL (and the error word) when
-// there is none
+// the table's row for a token's position; its first row and ok = false (and the
+// error word) when there is none
 __device__ __forceinline__ const float* rope_row(const QkArgs& a, unsigned tok, bool report, bool& ok)
 {
     ok = true;
@@ -171,150 +247,265 @@ __device__ __forceinline__ const float* rope_row(const QkArgs& a, unsigned tok, 
     return a.rope + (ok ? p : 0) * a.R;
 }
 
+// Rows (token, head) of one tensor, U consecutive ones per LPH lanes: where their
+// data lies, and which begin another token than the row before.
+template <int U> struct Rows {
+    unsigned tok[U];
+    bool live[U], turned[U];   // turned: the position differs from the row before
+    int64_t at[U];             // offset of the row in the strided tensor
+
+    __device__ __forceinline__ void locate(unsigned row, unsigned total, unsigned H, int64_t ld, int64_t hs)
+    {
+        unsigned t = row / H, h = row - t * H;
+        int64_t o = (int64_t)t * ld + (int64_t)h * hs;
+        const int64_t wrap = ld - (int64_t)(H - 1) * hs;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            tok[u] = t;
+            live[u] = row + u < total;
+            turned[u] = u == 0 || h == 0;
+            at[u] = o;
+            const bool last = ++h == H;
+            h = last ? 0 : h;
+            t += last;
+            o += last ? wrap : hs;
+        }
+    }
+};
+
+// U rows' values from memory, flushed, as packed pairs (0 for rows past the end)
+template <typename T, int E, bool VEC>
+__device__ __forceinline__ void load_row(const T* p, bool live, int d0, int D, u64 (&v)[E / 2])
+{
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        x[e] = 0.0f;
+    if (live)
+        load_head<T, E, VEC>(p, d0, D, x);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i)
+        v[i] = pack2(x[2 * i], x[2 * i + 1]);
+}
+
+template <typename T, int E, bool VEC>
+__device__ __forceinline__ void store_row(T* p, int d0, int D, const u64 (&v)[E / 2])
+{
+    float x[E];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i)
+        unpack2(v[i], x[2 * i], x[2 * i + 1]);
+    store_head<T, E, VEC>(p, d0, D, x);
+}
+
+template <int N> __device__ __forceinline__ void mul_flush(u64 (&v)[N], const u64 (&w)[N])
+{
+    const u64 z = pack2(-0.0f, -0.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = fadd2_ftz(fmul2_rn(v[i], w[i]), z);
+}
+
+template <int N> __device__ __forceinline__ void mul_flush(u64 (&v)[N], float w)
+{
+    const u64 z = pack2(-0.0f, -0.0f), ww = pack2(w, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = fadd2_ftz(fmul2_rn(v[i], ww), z);
+}
+
+template <int N> __device__ __forceinline__ void flush_row(u64 (&v)[N])
+{
+    const u64 z = pack2(-0.0f, -0.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = fadd2_ftz(v[i], z);
+}
+
+// this lane's gains, flushed
+template <int E> __device__ __forceinline__ void load_gain(const float* gain, int d0, int D, u64 (&g)[E / 2])
+{
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        x[e] = gain && d0 + e < D ? __ldg(gain + d0 + e) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i)
+        g[i] = pack2(x[2 * i], x[2 * i + 1]);
+    flush_row(g);
+}
+
+__host__ __device__ constexpr int fwd_rows(int E) { return E == 4 ? 4 : E == 8 ? 2 : 1; }
+
 template <typename T, int E, int LPH, int MODE>
 __global__ void __launch_bounds__(256)
-k_qk_fwd(const __grid_constant__ QkArgs a)
+k_qk_fwd(const __grid_constant__ QkArgs a, unsigned blocks_q)
 {
-    constexpr int HPW = 32 / LPH;            // heads a warp holds
-    constexpr int U = E >= 16 ? 1 : 16 / E;  // rows in flight per lane
+    constexpr int HPW = 32 / LPH;   // heads a warp holds
+    constexpr int U = fwd_rows(E);
     constexpr bool VEC = MODE != GENERIC;
     __shared__ float rows[MODE == GENERIC ? 8 * HPW * E * LPH : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int D = (int)a.D, R = (int)a.R, d0 = (lane % LPH) * E, sub = lane / LPH;
-    const unsigned H = (unsigned)(a.t[0].H + a.t[1].H), total = (unsigned)a.n * H;
-    const unsigned base = blockIdx.x * (8u * HPW * U) + (unsigned)(warp * HPW + sub);
-    const float width = (float)D, eps = flush(a.eps);
-    float x[U][E];
-    unsigned tok[U], h[U];
+    float* srow = rows + (MODE == GENERIC ? (warp * HPW + sub) * E * LPH : 0);
+    const bool is_q = blockIdx.x < blocks_q;
+    const QkTensor& t = is_q ? a.t[0] : a.t[1];
+    const unsigned block = is_q ? blockIdx.x : blockIdx.x - blocks_q;
+    const unsigned H = (unsigned)t.H, total = (unsigned)a.n * H;
+    const unsigned row0 = ((block * 8 + warp) * HPW + sub) * U;
+    Rows<U> at;
+    at.locate(row0, total, H, t.ld, t.hs);
+    u64 x[U][E / 2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        load_row<T, E, VEC>(static_cast<const T*>(t.x) + at.at[u], at.live[u], d0, D, x[u]);
+    if (__ballot_sync(0xffffffffu, at.live[0]) == 0)
+        return;
+    u64 c[E / 2] = {}, s[E / 2] = {}, g[E / 2];
+    bool ok;
+    const float* cs = rope_row(a, at.live[0] ? at.tok[0] : 0u, at.live[0] && d0 == 0, ok);
+    load_turn<E, MODE, false>(c, s, cs, d0, R, a.interleaved);
+    load_gain<E>(t.gain, d0, D, g);
+    float S[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const unsigned row = base + (unsigned)u * 8u * HPW;
-        tok[u] = row / H;
-        h[u] = row - tok[u] * H;
-        if (row < total) {
-            const bool is_q = h[u] < (unsigned)a.t[0].H;
-            const QkTensor& t = is_q ? a.t[0] : a.t[1];
-            const int64_t head = is_q ? h[u] : h[u] - (unsigned)a.t[0].H;
-            load_head<T, E, VEC>(static_cast<const T*>(t.x) + (int64_t)tok[u] * t.ld + head * t.hs, d0, D, x[u]);
-        }
+        flush_row(x[u]);
+        S[u] = lane_sum<E>(x[u], x[u], d0, D);
     }
+    const float r = rnorm(rows_tree<U, LPH>(S, lane), (float)D, a.inv, flush(a.eps));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const unsigned row = base + (unsigned)u * 8u * HPW;
-        // lanes of one warp may hold rows on both sides of the end: all take part in the shuffles
-        const bool live = row < total;
-        if (__ballot_sync(0xffffffffu, live) == 0)
-            break;
-        const bool is_q = !live || h[u] < (unsigned)a.t[0].H;
-        const QkTensor& t = is_q ? a.t[0] : a.t[1];
-        const int64_t head = !live ? 0 : is_q ? h[u] : h[u] - (unsigned)a.t[0].H;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            x[u][e] = live ? flush(x[u][e]) : 0.0f;
-        const float r = rnorm(head_sum<E, LPH>(x[u], x[u], d0, D), width, eps);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            x[u][e] = fmul_flush(x[u][e], r);
-        if (t.gain) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (d0 + e < D)
-                    x[u][e] = fmul_flush(x[u][e], flush(__ldg(t.gain + d0 + e)));
+        mul_flush(x[u], __shfl_sync(0xffffffffu, r, lane_of<U>(u), LPH));
+        if (t.gain)
+            mul_flush(x[u], g);
+        if (u > 0 && at.turned[u] && at.live[u]) {
+            cs = rope_row(a, at.tok[u], d0 == 0, ok);
+            load_turn<E, MODE, false>(c, s, cs, d0, R, a.interleaved);
         }
-        bool ok;
-        const float* cs = rope_row(a, live ? tok[u] : 0u, live && d0 == 0, ok);
-        rotate<E, LPH, MODE, false>(x[u], cs, d0, D, R, a.interleaved,
-                                    rows + (MODE == GENERIC ? (warp * HPW + sub) * E * LPH : 0));
+        turn<E, MODE>(x[u], c, s, d0, D, R, a.interleaved, srow);
         if (!ok) {
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                x[u][e] = 0.0f;
+            for (int i = 0; i < E / 2; ++i)
+                x[u][i] = 0ull;
         }
-        if (live) {
-            float* o = t.out + ((int64_t)tok[u] * t.H + head) * D;
+        if (at.live[u]) {
+            float* o = t.out + (int64_t)(row0 + u) * D;
             if (D % 4 == 0)
-                store_head<float, E, true>(o, d0, D, x[u]);
+                store_row<float, E, true>(o, d0, D, x[u]);
             else
-                store_head<float, E, false>(o, d0, D, x[u]);
+                store_row<float, E, false>(o, d0, D, x[u]);
         }
     }
 }
 
 constexpr int CHUNK = 64;   // rows of a chunk of the gains' canonical sums
+__host__ __device__ constexpr int bwd_rows(int E, int LPH) { return E == 4 ? (LPH == 8 ? 2 : 4) : E == 8 ? 2 : 1; }
 
 template <typename T, int E, int LPH, int MODE>
 __global__ void __launch_bounds__(256)
 k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict__ parts, int64_t pitch)
 {
     constexpr int HPW = 32 / LPH;
-    constexpr int U = E >= 8 ? 1 : 2;
+    constexpr int U = bwd_rows(E, LPH);
+    constexpr int PER = CHUNK / (8 * HPW);   // consecutive rows of the chunk per LPH lanes
     constexpr bool VEC = MODE != GENERIC;
     __shared__ float rows[MODE == GENERIC ? 8 * HPW * E * LPH : 1];
     extern __shared__ float terms[];   // [CHUNK][D] with a gain
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int D = (int)a.D, R = (int)a.R, d0 = (lane % LPH) * E, sub = lane / LPH;
+    float* srow = rows + (MODE == GENERIC ? (warp * HPW + sub) * E * LPH : 0);
     const bool is_q = blockIdx.x < chunks_q;
     const QkTensor& t = is_q ? a.t[0] : a.t[1];
     const unsigned chunk = is_q ? blockIdx.x : blockIdx.x - chunks_q;
     const unsigned H = (unsigned)t.H, total = (unsigned)a.n * H, first = chunk * CHUNK;
     const float width = (float)D, eps = flush(a.eps);
     const bool gain = t.gain != nullptr;
-    float* srow = rows + (MODE == GENERIC ? (warp * HPW + sub) * E * LPH : 0);
-    for (int k0 = 0; k0 < CHUNK; k0 += 8 * HPW * U) {
-        float x[U][E], dy[U][E];
-        unsigned tok[U], h[U];
+    u64 g[E / 2];
+    load_gain<E>(t.gain, d0, D, g);
+#pragma unroll 1
+    for (int k0 = 0; k0 < PER; k0 += U) {
+        const unsigned row0 = first + (unsigned)((warp * HPW + sub) * PER + k0);
+        Rows<U> at;
+        at.locate(row0, total, H, t.ld, t.hs);
+        if (__ballot_sync(0xffffffffu, at.live[0]) == 0)
+            break;
+        u64 x[U][E / 2], dy[U][E / 2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const unsigned row = first + (unsigned)(k0 + u * 8 * HPW + warp * HPW + sub);
-            tok[u] = row / H;
-            h[u] = row - tok[u] * H;
-            if (row < total) {
-                load_head<T, E, VEC>(static_cast<const T*>(t.x) + (int64_t)tok[u] * t.ld + (int64_t)h[u] * t.hs,
-                                     d0, D, x[u]);
-                const float* g = t.dout + (int64_t)row * D;
-                if (D % 4 == 0)
-                    load_head<float, E, true>(g, d0, D, dy[u]);
-                else
-                    load_head<float, E, false>(g, d0, D, dy[u]);
-            }
+            load_row<T, E, VEC>(static_cast<const T*>(t.x) + at.at[u], at.live[u], d0, D, x[u]);
+            const float* p = t.dout + (int64_t)(row0 + u) * D;
+            if (D % 4 == 0)
+                load_row<float, E, true>(p, at.live[u], d0, D, dy[u]);
+            else
+                load_row<float, E, false>(p, at.live[u], d0, D, dy[u]);
         }
+        u64 c[E / 2] = {}, s[E / 2] = {};
+        bool ok[U];
+        const float* cs = rope_row(a, at.live[0] ? at.tok[0] : 0u, at.live[0] && d0 == 0, ok[0]);
+        load_turn<E, MODE, true>(c, s, cs, d0, R, a.interleaved);
+        float S[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const unsigned row = first + (unsigned)(k0 + u * 8 * HPW + warp * HPW + sub);
-            const bool live = row < total;
-            if (__ballot_sync(0xffffffffu, live) == 0)
-                break;
+            flush_row(x[u]);
+            S[u] = lane_sum<E>(x[u], x[u], d0, D);
+        }
+        const float r = rnorm(rows_tree<U, LPH>(S, lane), width, a.inv, eps);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                x[u][e] = live ? flush(x[u][e]) : 0.0f;
-                dy[u][e] = live ? flush(dy[u][e]) : 0.0f;
+        for (int u = 0; u < U; ++u) {
+            if (u > 0) {
+                ok[u] = ok[u - 1];
+                if (at.turned[u] && at.live[u]) {
+                    cs = rope_row(a, at.tok[u], d0 == 0, ok[u]);
+                    load_turn<E, MODE, true>(c, s, cs, d0, R, a.interleaved);
+                }
             }
-            const float r = rnorm(head_sum<E, LPH>(x[u], x[u], d0, D), width, eps);
-            bool ok;
-            const float* cs = rope_row(a, live ? tok[u] : 0u, live && d0 == 0, ok);
-            rotate<E, LPH, MODE, true>(dy[u], cs, d0, D, R, a.interleaved, srow);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                x[u][e] = fmul_flush(x[u][e], r);   // h
+            flush_row(dy[u]);
+            turn<E, MODE>(dy[u], c, s, d0, D, R, a.interleaved, srow);
+            mul_flush(x[u], __shfl_sync(0xffffffffu, r, lane_of<U>(u), LPH));   // h
             if (gain) {
-                const int at = (int)(row - first) * D;
+                u64 p[E / 2];
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (live && d0 + e < D) {
-                        terms[at + d0 + e] = ok ? fmul_flush(dy[u][e], x[u][e]) : 0.0f;
-                        dy[u][e] = fmul_flush(dy[u][e], flush(__ldg(t.gain + d0 + e)));
-                    }
-            }
-            const float c1 = flush(__fdiv_rn(head_sum<E, LPH>(dy[u], x[u], d0, D), width));
+                for (int i = 0; i < E / 2; ++i)
+                    p[i] = ok[u] ? dy[u][i] : 0ull;
+                mul_flush(p, x[u]);
+                if (!ok[u]) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float v = fadd_ftz(dy[u][e], -fmul_flush(x[u][e], c1));
-                x[u][e] = ok ? fmul_flush(r, v) : 0.0f;
+                    for (int i = 0; i < E / 2; ++i)
+                        p[i] = 0ull;
+                }
+                if (at.live[u]) {
+                    float* o = terms + (row0 + u - first) * D;
+                    if (D % 4 == 0)
+                        store_row<float, E, true>(o, d0, D, p);
+                    else
+                        store_row<float, E, false>(o, d0, D, p);
+                }
+                mul_flush(dy[u], g);
             }
-            if (live)
-                store_head<T, E, VEC>(static_cast<T*>(t.dx) + (int64_t)tok[u] * t.dx_ld + (int64_t)h[u] * t.dx_hs,
-                                      d0, D, x[u]);
+            S[u] = lane_sum<E>(dy[u], x[u], d0, D);
         }
+        const float c1 = over_width(rows_tree<U, LPH>(S, lane), width, a.inv);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float ru = __shfl_sync(0xffffffffu, r, lane_of<U>(u), LPH);
+            const float cu = __shfl_sync(0xffffffffu, c1, lane_of<U>(u), LPH);
+            const u64 nc = pack2(-cu, -cu);
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i)
+                x[u][i] = fadd2_ftz(dy[u][i], fmul2_rn(x[u][i], nc));
+            mul_flush(x[u], ru);
+            if (!ok[u]) {
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i)
+                    x[u][i] = 0ull;
+            }
+        }
+        Rows<U> to;
+        to.locate(row0, total, H, t.dx_ld, t.dx_hs);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (to.live[u])
+                store_row<T, E, VEC>(static_cast<T*>(t.dx) + to.at[u], d0, D, x[u]);
     }
     if (gain) {
         __syncthreads();
@@ -367,16 +558,16 @@ template <typename T> cudaError_t fwd_typed(const QkArgs& a, cudaStream_t st)
 {
     return by_width(a.D, [&](auto e, auto l) {
         constexpr int E = decltype(e)::value, LPH = decltype(l)::value;
-        constexpr int per = 8 * (32 / LPH) * (E >= 16 ? 1 : 16 / E);
-        const int64_t total = a.n * (a.t[0].H + a.t[1].H);
-        const unsigned grid = (unsigned)((total + per - 1) / per);
+        constexpr int per = 8 * (32 / LPH) * fwd_rows(E);
+        const unsigned bq = (unsigned)((a.n * a.t[0].H + per - 1) / per);
+        const unsigned grid = bq + (unsigned)((a.n * a.t[1].H + per - 1) / per);
         const int m = mode_of<T>(a, E, false);
         if (m == INTER)
-            k_qk_fwd<T, E, LPH, INTER><<<grid, 256, 0, st>>>(a);
+            k_qk_fwd<T, E, LPH, INTER><<<grid, 256, 0, st>>>(a, bq);
         else if (m == HALF)
-            k_qk_fwd<T, E, LPH, HALF><<<grid, 256, 0, st>>>(a);
+            k_qk_fwd<T, E, LPH, HALF><<<grid, 256, 0, st>>>(a, bq);
         else
-            k_qk_fwd<T, E, LPH, GENERIC><<<grid, 256, 0, st>>>(a);
+            k_qk_fwd<T, E, LPH, GENERIC><<<grid, 256, 0, st>>>(a, bq);
         count_launches(1);
         return cudaGetLastError();
     });

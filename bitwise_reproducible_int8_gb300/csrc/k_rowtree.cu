@@ -2,10 +2,13 @@
 // (each a row of D floats) combined by the stride-doubling pairwise tree, and
 // the debug scan of strided tensors.
 //
-// t_j += t_{j+s} for j a multiple of 2s: at every stride the pairs are
-// independent, so a CTA gives 8 lanes to 32 columns and spreads the pairs over
-// its 32 groups of lanes, with a barrier between strides.  The partial rows come
-// straight out of L2.
+// t_j += t_{j+s} for j a multiple of 2s.  An aligned group of 16 chunks is a subtree:
+// a worker loads its 16 rows at once and folds them in registers, so a tree over C
+// chunks takes log16 C rounds over memory (out of L2) instead of log2 C, with 16
+// loads in flight.  LANES lanes of 4 columns make a worker: a warp where many joins
+// of few chunks over wide rows are to be done (the table's gradient), two lanes for
+// one long join over a narrow row (the gains' gradients; with 8 lanes and one pair
+// per worker and barrier, 4,096 chunks of 128 took 25 us).
 #include "elem.cuh"
 #include "internal.h"
 #include "launch.cuh"
@@ -13,19 +16,20 @@
 namespace repro {
 namespace {
 
-constexpr int RT_COLS = 32;       // columns per CTA step
-constexpr int RT_WORKERS = 32;    // pairs at a time
+constexpr int FOLD = 16;   // chunks a worker folds at a time
 
+template <int LANES>
 __global__ void __launch_bounds__(256)
 k_row_tree(const RowTree t, int colsegs)
 {
+    constexpr int WORKERS = 256 / LANES;
     pdl_wait();
     const int64_t joins = t.joins ? *t.njoins : 1;
-    const int lane = threadIdx.x & 7, worker = threadIdx.x >> 3;
+    const int lane = threadIdx.x % LANES, worker = threadIdx.x / LANES;
     const float sc = flush(t.scale);
     for (int64_t item = blockIdx.x; item < joins * colsegs; item += gridDim.x) {
         const int64_t jn = item / colsegs;
-        const int64_t c = (item - jn * colsegs) * RT_COLS + 4 * lane;
+        const int64_t c = (item - jn * colsegs) * (4 * LANES) + 4 * lane;
         const int4 j = t.joins ? t.joins[jn] : make_int4(0, (int)t.count, 0, 0);
         const bool live = c < t.D;
         // partial row of chunk k: see the slot rule of the chunk list (k_embed.cu)
@@ -34,13 +38,20 @@ k_row_tree(const RowTree t, int colsegs)
             return t.parts + slot * t.pitch + c;
         };
         const int64_t C = j.y;
-        for (int64_t s = 1; s < C; s *= 2) {
+        for (int64_t s = 1; s < C; s *= FOLD) {
             if (live)
-                for (int64_t k = 2 * s * worker; k + s < C; k += 2 * s * RT_WORKERS) {
-                    float* p = row(k);
-                    const float4 x = load4(p), y = load4(row(k + s));
-                    store4(p, make_float4(fadd_ftz(x.x, y.x), fadd_ftz(x.y, y.y), fadd_ftz(x.z, y.z),
-                                          fadd_ftz(x.w, y.w)));
+                for (int64_t k = (int64_t)worker * FOLD * s; k < C; k += (int64_t)WORKERS * FOLD * s) {
+                    float4 v[FOLD];
+#pragma unroll
+                    for (int i = 0; i < FOLD; ++i)   // -0 in place of a missing chunk leaves a sum as it is
+                        v[i] = k + i * s < C ? load4(row(k + i * s)) : make_float4(-0.0f, -0.0f, -0.0f, -0.0f);
+#pragma unroll
+                    for (int w = 1; w < FOLD; w *= 2)
+#pragma unroll
+                        for (int i = 0; i < FOLD; i += 2 * w)
+                            v[i] = make_float4(fadd_ftz(v[i].x, v[i + w].x), fadd_ftz(v[i].y, v[i + w].y),
+                                               fadd_ftz(v[i].z, v[i + w].z), fadd_ftz(v[i].w, v[i + w].w));
+                    store4(row(k), v[0]);
                 }
             __syncthreads();
         }
@@ -75,9 +86,11 @@ k_check_rows(const T* __restrict__ p, int64_t n, int64_t D, int64_t ld, int* err
 
 cudaError_t launch_row_tree(const RowTree& t, int max_ctas, cudaStream_t st)
 {
-    const int colsegs = (int)((t.D + RT_COLS - 1) / RT_COLS);
+    const int cols = t.joins ? 128 : 8;
+    const int colsegs = (int)((t.D + cols - 1) / cols);
     const int grid = t.joins ? max_ctas : (colsegs < max_ctas ? colsegs : max_ctas);
-    const cudaError_t e = launch_pdl(k_row_tree, dim3((unsigned)grid), dim3(256), 0, st, t, colsegs);
+    const cudaError_t e = t.joins ? launch_pdl(k_row_tree<32>, dim3((unsigned)grid), dim3(256), 0, st, t, colsegs)
+                                  : launch_pdl(k_row_tree<2>, dim3((unsigned)grid), dim3(256), 0, st, t, colsegs);
     count_launches(1);
     return e;
 }

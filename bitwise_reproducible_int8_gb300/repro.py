@@ -158,7 +158,9 @@ def declared_functions() -> list:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle, without the Stream object around it: a call's
+        # host time is a few microseconds and building that object was most of it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -411,13 +413,17 @@ def _index_bytes(name, *ts) -> int:
 def _rows2d(t, name):
     """(rows, width, row stride) of a matrix, or of an array whose leading
     dimensions collapse into one; elements of a row adjacent."""
-    if t.dim() < 2:
+    shape = t.shape
+    if len(shape) < 2:
         raise ValueError(f"{name} must have at least two dimensions")
-    D = t.shape[-1]
-    if D > 1 and t.stride(-1) != 1 and t.numel() > 0:
+    D = shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // D if D else 0), D, D
+    strides = t.stride()
+    if D > 1 and strides[-1] != 1 and t.numel() > 0:
         raise ValueError(f"{name}: the elements of a row must be adjacent")
     n, ld = 1, None
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, stride in zip(shape[-2::-1], strides[-2::-1]):
         if size == 1:
             continue
         if ld is None:
@@ -474,15 +480,21 @@ def repro_embed_bwd(dout: torch.Tensor, tokens: torch.Tensor, dtable: torch.Tens
 
 def _heads(t, name):
     """(tokens, heads, width, token stride, head stride) of [n, H, D] or [B, T, H, D]."""
-    if t.dim() not in (3, 4):
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 3:
+        n, ld = shape[0], strides[0]
+    elif len(shape) == 4:
+        B, T = shape[:2]
+        n = B * T
+        ld = strides[0] if T == 1 else strides[1]
+        if B > 1 and T > 1 and strides[0] != T * ld:
+            raise ValueError(f"{name}: the tokens must lie at one stride")
+    else:
         raise ValueError(f"{name} must be [n, H, D] or [B, T, H, D]")
-    H, D = t.shape[-2:]
-    if D > 1 and t.stride(-1) != 1 and t.numel() > 0:
+    H, D = shape[-2:]
+    if D > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: the elements of a head must be adjacent")
-    n, _, ld = _rows2d(t[..., 0, :], name) if H > 0 else (t.shape[:-2].numel(), D, D)
-    if n <= 1:
-        ld = max(ld, 1)
-    return n, H, D, ld, int(t.stride(-2)) if H > 1 else D
+    return n, H, D, (ld if n > 1 else max(ld, 1)), (strides[-2] if H > 1 else D)
 
 
 def _qk_common(q, k, rope, g_q, g_k, positions):

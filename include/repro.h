@@ -443,13 +443,14 @@ size_t repro_qk_norm_rope_bwd_ws_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64
  * penalty from the same pass.  it = 1 (/) tau, u_j = z_j (x) it:
  *   e(x) = 2^t for x <= 0, t = x (x) RN(1 / ln 2): k = rint(t), f = t (-) k, the
  *     degree-6 polynomial of 2^f (coefficients in k_distill.cu) in Horner form,
- *     times 2^k; 0 below t = -125;
+ *     times 2^k; 0 where k < -125;
  *   blocks of REPRO_DISTILL_BLOCK consecutive logits: the block's maximum M_b
  *     (a zero maximum is +0, a NaN stays) and S_b = sum of e(u_j (-) M_b (x) it) in
  *     128 chains (element j of the block in chain j mod 128, ascending from
  *     +0), the chains by the pairwise tree;
  *   M = max M_b; l = sum over blocks of S_b (x) e((M_b (x) it) (-) (M (x) it)) in 32
- *     chains (block b in chain b mod 32) and the tree; l1 the same with it = 1;
+ *     chains (block b in chain b mod 32) and the tree; l1 the same with it = 1, where
+ *     for tau = 2 and 4 a block's term is the first one's square, its fourth power;
  *   the teacher's weights p_k over the non-empty entries: a_k = t_k (x) it,
  *     m = max a_k, p_k = e(a_k (-) m) (/) lt, lt the sum of the e(.) in 32 chains and
  *     the tree, P = 1; with REPRO_DISTILL_LOGPROBS t_k are the teacher's own
@@ -484,6 +485,7 @@ size_t repro_distill_ws_bytes(int64_t n, int64_t V);
  *   gk = (g (x) w_kd) (x) tau;  a = gk (x) P;  b = g (x) ([label >= 0] w_ce (+) (2 (x) w_z) (x) lse(z))
  *   tau = 1: dz_j = e(u_j (-) M) (x) ((a (+) b) (/) l);
  *   else dz_j = e(u_j (-) M (x) it) (x) (a (/) l), (+) e(z_j (-) M) (x) (b (/) l1) if w_ce or w_z
+ *     (for tau = 2 and 4 the second e(.) is the first's square, its fourth power);
  *   then, entry by entry in ascending k, dz at t_idx_k (-)= gk (x) p_k (w_kd not 0),
  *   and dz at the label (-)= g (x) w_ce.
  * dz in z's type, rows dz_ld apart; it may be z itself (same pointer and

@@ -978,16 +978,16 @@ void oracle_qk_bwd(const float* dout, const float* x, const float* rope, const i
 
 /* 2^t for t <= 0: t = k + f, k = rint(t), and the degree-6 minimax polynomial
  * of 2^f on [-1/2, 1/2] (relative error 2.6e-9, constant term 1; coefficients
- * by the exchange algorithm of Remez, rounded to binary32); 0 below -125 */
+ * by the exchange algorithm of Remez, rounded to binary32); 0 where k < -125 */
 float oracle_exp2_neg(float t)
 {
     static const float c[7] = {1.0f, 0x1.62e432p-1f, 0x1.ebfbe2p-3f, 0x1.c6ae72p-5f, 0x1.3b270ep-7f,
                                0x1.5f7278p-10f, 0x1.470b5p-13f};
-    if (t < -125.0f)
-        return 0.0f;
     if (t != t)
         return t;
     const float k = nearbyintf(t);
+    if (k < -125.0f)
+        return 0.0f;
     const float f = oracle_add(t, -k);
     float p = c[6];
     for (int i = 5; i >= 0; --i)
@@ -1053,8 +1053,16 @@ static double chains_sum_d(const double* t, int64_t n, int chains)
     return s[0];
 }
 
-/* max and sum of e^(it z - it max) over a row, block by block */
-static float row_sum(const float* z, int64_t V, float it, float* mx)
+/* the softmax-of-z term e^(z - m) from the softened one where tau is 2 or 4 */
+static float term_power(float e, float tau)
+{
+    e = oracle_mul(e, e);
+    return tau == 4.0f ? oracle_mul(e, e) : e;
+}
+
+/* max and sum of e^(it z - it max) over a row, block by block; with tau 2 or 4 (and
+ * it = 1 / tau) the blocks' sums are of e^(z - max) as a power of that, joined with it = 1 */
+static float row_sum(const float* z, int64_t V, float it, float tau, float* mx)
 {
     const int64_t C = (V + DISTILL_BLOCK - 1) / DISTILL_BLOCK;
     float* S = (float*)malloc(sizeof(float) * (size_t)C);
@@ -1069,12 +1077,17 @@ static float row_sum(const float* z, int64_t V, float it, float* mx)
         const float Mu = oracle_mul(M[c], it);
         for (int64_t j = 0; j < n; ++j)
             t[j] = exp_neg(oracle_add(oracle_mul(z[lo + j], it), -Mu));
+        if (tau != 0.0f)
+            for (int64_t j = 0; j < n; ++j)
+                t[j] = term_power(t[j], tau);
         S[c] = M[c] == -INFINITY ? 0.0f : chains_sum(t, n, DISTILL_CHAINS);
         m = max_nan(m, M[c]);
     }
     m = m == 0.0f ? 0.0f : m;
     *mx = m;
     float l = 0.0f;
+    if (tau != 0.0f)
+        it = 1.0f;
     if (m != -INFINITY) {
         for (int64_t c = 0; c < C; ++c)
             S[c] = oracle_mul(S[c], exp_neg(oracle_add(oracle_mul(M[c], it), -oracle_mul(m, it))));
@@ -1096,8 +1109,9 @@ void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx
         float* st = stats + r * (DISTILL_STATS + K);
         float* p = st + DISTILL_STATS;
         float mz, m1;
-        const float l = row_sum(zr, V, it, &mz);
-        const float l1 = row_sum(zr, V, 1.0f, &m1);
+        const int power = tau == 2.0f || tau == 4.0f;
+        const float l = row_sum(zr, V, it, 0.0f, &mz);
+        const float l1 = power ? row_sum(zr, V, it, tau, &m1) : row_sum(zr, V, 1.0f, 0.0f, &m1);
         const float Mu = oracle_mul(mz, it);
         /* the teacher's weights */
         float mt = -INFINITY, lt = 0.0f, P = 0.0f;
@@ -1186,9 +1200,11 @@ void oracle_distill_bwd(const float* z, int64_t n, int64_t V, const int64_t* idx
         const float cb = two ? oracle_div(b, st[3]) : 0.0f;
         const float Mu = oracle_mul(st[0], it);
         for (int64_t j = 0; j < V; ++j) {
-            d[j] = oracle_mul(exp_neg(oracle_add(oracle_mul(zr[j], it), -Mu)), ca);
+            const float e = exp_neg(oracle_add(oracle_mul(zr[j], it), -Mu));
+            d[j] = oracle_mul(e, ca);
             if (two)
-                d[j] = oracle_add(d[j], oracle_mul(exp_neg(oracle_add(zr[j], -st[0])), cb));
+                d[j] = oracle_add(d[j], oracle_mul(tau == 2.0f || tau == 4.0f ? term_power(e, tau)
+                                                                              : exp_neg(oracle_add(zr[j], -st[0])), cb));
         }
         if (w_kd != 0.0f)
             for (int64_t k = 0; k < K; ++k) {

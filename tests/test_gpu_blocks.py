@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 import bitwise_reproducible_int8_gb300 as R  # noqa: E402
 import ops64 as F  # noqa: E402
 from gpu_helpers import assert_bits_equal, dev, host  # noqa: E402
-from test_oracle_blocks import case as distill_case, rope_table  # noqa: E402
+from test_oracle_blocks import HP, case as distill_case, rope_table  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -225,10 +225,6 @@ def test_qk_no_tokens():
 
 # ---------------------------------------------------------------- distillation
 
-HP = [dict(), dict(tau=2.0), dict(tau=2.0, w_kd=0.7, w_ce=0.3, w_z=1e-3), dict(w_kd=0.5, w_ce=0.5, w_z=1e-4),
-      dict(w_kd=0.0, w_ce=1.0), dict(tau=0.5, logprobs=True)]
-
-
 def run_distill(z, idx, tl, lab, g, hp, zt, t_dtype=torch.float32, int_t=np.int32, in_place=False):
     """(loss, stats, gradient) from the device."""
     n, V = z.shape
@@ -275,7 +271,26 @@ def test_distill(orc, n, V, K, kind, hp):
     assert R.repro_device_check() == 0
 
 
-@pytest.mark.parametrize("tau", [1.0, 1.5])
+@pytest.mark.parametrize("n,V,K", [(5000, 130, 7), (2500, 3100, 20), (2300, 9001, 20)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("hp", [dict(), dict(tau=2.0, w_kd=0.7, w_ce=0.3), dict(tau=1.5, w_kd=0.7, w_z=1e-3)])
+def test_distill_many_rows(orc, n, V, K, kind, hp):
+    """Rows enough for a CTA to own its rows, and for several blocks a warp."""
+    z, idx, tl, lab = distill_case(V, n, V, K)
+    z = bf(z) if kind == "bf16" else z
+    g = np.float32([0.01])
+    full = dict(tau=1.0, w_kd=1.0, w_ce=0.0, w_z=0.0)
+    full.update(hp)
+    el, es = orc.distill_fwd(z, idx, tl, lab, **full)
+    ez = orc.distill_bwd(z, idx, es, g, lab, **full)
+    zt = strided(z, dtype=BF if kind == "bf16" else torch.float32)
+    loss, stats, dz = run_distill(z, idx, tl, lab, g, hp, zt)
+    same(stats, es, "stats")
+    same(loss, el, "loss")
+    same(dz, bf(ez) if kind == "bf16" else ez, "dz")
+
+
+@pytest.mark.parametrize("tau", [1.0, 1.5, 2.0])
 def test_distill_masked_rows(orc, tau):
     V, K = 3000, 4
     z, idx, tl, lab = distill_case(9, 7, V, K)

@@ -125,7 +125,8 @@ def case(seed, n, V, K):
 
 
 HP = [dict(), dict(tau=2.0), dict(tau=2.0, w_kd=0.7, w_ce=0.3, w_z=1e-3), dict(w_kd=0.5, w_ce=0.5, w_z=1e-4),
-      dict(w_kd=0.0, w_ce=1.0), dict(tau=0.5, logprobs=True)]
+      dict(w_kd=0.0, w_ce=1.0), dict(tau=0.5, logprobs=True), dict(tau=4.0, w_kd=0.5, w_ce=0.5),
+      dict(tau=1.5, w_kd=0.5, w_ce=0.5, w_z=1e-4)]
 
 
 @pytest.mark.parametrize("n,V,K", [(2, 1, 1), (3, 130, 0), (4, 1025, 17), (2, 3000, 70)])
