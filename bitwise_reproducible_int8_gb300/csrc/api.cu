@@ -1229,7 +1229,7 @@ static int check_distill(const void* z, int z_type, int64_t z_ld, const void* t_
     if (!(hp->tau >= 1e-4f && hp->tau <= 1e4f) || !finite_f(hp->w_kd) || !finite_f(hp->w_ce) || !finite_f(hp->w_z))
         return REPRO_ERR_ARG;
     if (n < 0 || V < 1 || K < 0 || z_ld < V || !rows_fit(n, z_ld, V) || K > 65536 || n > INT32_MAX ||
-        n * ((V + REPRO_DISTILL_BLOCK - 1) / REPRO_DISTILL_BLOCK) > INT32_MAX)
+        n * ((V + 574) / 512) > INT32_MAX)
         return REPRO_ERR_SHAPE;
     if (n == 0)
         return REPRO_OK;

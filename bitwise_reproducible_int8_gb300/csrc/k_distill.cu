@@ -60,15 +60,19 @@ __device__ __forceinline__ u64 dup2(float v) { return pack2(v, v); }
 // algorithm of Remez, rounded to binary32) in Horner form, times 2^k; 0 where
 // k < -125, so nothing here is subnormal.  The coefficients below are doubled and
 // the power halved, both exact: 2^(k - 1) then has the bits (k + 126) << 23 down to
-// k = -125, and k = -126, where smaller t are clamped, gives the factor +0.
+// k = -125, and k = -126, where smaller t are clamped, gives the factor +0.  126 is
+// part of the number added for rint, so the shift alone makes the power.
+constexpr float BIG = 0x1.8p23f + 126.0f;
+
 __device__ __forceinline__ u64 exp_neg2(u64 x)
 {
-    float t0, t1, k0, k1, m0, m1;
+    float t0, t1, m0, m1;
     unpack2(fmul2_rn(x, dup2(LOG2E)), t0, t1);   // subnormal t: consumed by flushing sums only
     const u64 t = pack2(max_nan(t0, -126.0f), max_nan(t1, -126.0f));
-    const u64 m = fadd2_ftz(t, dup2(0x1.8p23f));
-    unpack2(fadd2_ftz(m, dup2(-0x1.8p23f)), k0, k1);
-    const u64 f = fadd2_ftz(t, pack2(-k0, -k1));
+    const u64 m = fadd2_ftz(t, dup2(BIG));
+    // -k = BIG - m: the product by -1 and the difference are exact, so nothing is fused here
+    // that rounds; it saves a negation
+    const u64 f = fadd2_ftz(t, ffma2_rn(m, dup2(-1.0f), dup2(BIG)));
     u64 p = dup2(0x1.470b5p-12f);
     p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.5f7278p-9f));
     p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.3b270ep-6f));
@@ -77,10 +81,8 @@ __device__ __forceinline__ u64 exp_neg2(u64 x)
     p = fadd2_ftz(fmul2_rn(p, f), dup2(0x1.62e432p+0f));
     p = fadd2_ftz(fmul2_rn(p, f), dup2(2.0f));
     unpack2(m, m0, m1);
-    // the low bits of 1.5 * 2^23 + k are k
-    const u64 s = pack2(__int_as_float((__float_as_int(m0) << 23) + (126 << 23)),
-                        __int_as_float((__float_as_int(m1) << 23) + (126 << 23)));
-    return fmul2_rn(p, s);
+    // the low bits of m are k + 126
+    return fmul2_rn(p, pack2(__int_as_float(__float_as_int(m0) << 23), __int_as_float(__float_as_int(m1) << 23)));
 }
 
 // the softmax-of-z term from the softened one, e(x)^tau by squaring
@@ -439,21 +441,77 @@ struct BwdArgs {
     const void* t_idx;
     const void* labels;
     int index_bytes;
-    int V, K, nblk, groups, items, per;
+    int V, K, nblk, groups, items, per, mask;
     float it, tau, w_kd, w_ce, w_z;
     const float* stats;
     const float* g;
     int64_t g_stride;
 };
 
-// One warp takes `per` consecutive blocks of a row, so that what belongs to the row
-// (statistics, coefficients and their divisions) is done once.  The order of the
-// elements does not matter here: where z and dz start equally far past a 4-element
-// boundary (SHIFT), a row's blocks are cut at those boundaries and all but the
-// row's ends move four elements at a time, whatever the vocabulary's remainder.
-// Block element i of lane: EACH: 32 i + lane; SHIFT: 128 (i / 4) + 4 lane + i mod 4.
+constexpr int BWD_CTAS = 6;
+constexpr int BPER = 16;           // logits per lane and piece of the backward
+constexpr int BBLK = 32 * BPER;
+
+// A piece of a row as loaded.  The order of the elements does not matter in the
+// backward.  SHIFT, where z and dz start equally far past a 128-byte line (or a
+// 4-element group): a row's pieces are cut there, and all but the row's ends move
+// four elements at a time and whole lines by the warp, whatever the vocabulary's
+// remainder: slot i of a lane is element 128 (i / 4) + 4 lane + i mod 4.  Otherwise element 32 i + lane.  Elements outside
+// [0, V) are -infinity.
+template <typename T, bool SHIFT> __device__ __forceinline__ void load_piece(const T* p, int lo, int V, int lane, float (&x)[BPER])
+{
+#pragma unroll
+    for (int i = 0; i < BPER; i += 4) {
+        if (SHIFT) {
+            const int e = lo + 32 * i + 4 * lane;
+            if (e >= 0 && e + 4 <= V) {
+                const float4 v = load4(p + e);
+                x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    x[i + c] = e + c >= 0 && e + c < V ? to_f32<T>(p[e + c]) : -CUDART_INF_F;
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int e = lo + 32 * (i + c) + lane;
+                x[i + c] = e < V ? to_f32<T>(p[e]) : -CUDART_INF_F;
+            }
+        }
+    }
+}
+
+template <typename T, bool SHIFT> __device__ __forceinline__ void store_piece(T* p, int lo, int V, int lane, const float (&x)[BPER])
+{
+#pragma unroll
+    for (int i = 0; i < BPER; i += 4) {
+        if (SHIFT) {
+            const int e = lo + 32 * i + 4 * lane;
+            if (e >= 0 && e + 4 <= V) {
+                store4(p + e, make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (e + c >= 0 && e + c < V)
+                        p[e + c] = from_f32<T>(x[i + c]);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int e = lo + 32 * (i + c) + lane;
+                if (e < V)
+                    p[e] = from_f32<T>(x[i + c]);
+            }
+        }
+    }
+}
+
+// One warp takes `per` consecutive pieces of a row, so that what belongs to the row
+// (statistics, coefficients and their divisions) is done once.  Pieces of 16 logits a
+// lane leave registers for 40 warps per SM, which is what covers the loads.
 template <typename T, int SUMS, bool SHIFT>
-__global__ void __launch_bounds__(32 * WARPS)
+__global__ void __launch_bounds__(32 * WARPS, BWD_CTAS)
 k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_constant__ BwdArgs a)
 {
     const int lane = threadIdx.x & 31;
@@ -463,7 +521,9 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
     const int row = item / a.groups, first = (item - row * a.groups) * a.per;
     const T* zr = z + row * z_ld;
     T* dr = dz + row * dz_ld;
-    const int shift = SHIFT ? (int)((reinterpret_cast<uintptr_t>(zr) / sizeof(T)) & 3) : 0;
+    const int shift = SHIFT ? (int)((reinterpret_cast<uintptr_t>(zr) / sizeof(T)) & a.mask) : 0;
+    float x[BPER];
+    load_piece<T, SHIFT>(zr, first * BBLK - shift, a.V, lane, x);   // on its way while the row's numbers come
     const float* st = a.stats + (int64_t)row * (STATS + a.K);
     const float M = st[0], l = st[1], l1 = st[3], lse1 = st[4], P = st[7];
     const float g = flush(a.g[row * a.g_stride]);
@@ -472,6 +532,14 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
         const int64_t t = load_index(a.labels, a.index_bytes, row);
         lab = t >= 0 && t < a.V ? (int)t : -1;
     }
+    // the row's first 64 columns stay in registers over the warp's pieces
+    auto column = [&](int k) {
+        int64_t j = -1;
+        if (k < a.K && a.w_kd != 0.0f)
+            j = load_index(a.t_idx, a.index_bytes, (int64_t)row * a.K + k);
+        return j >= 0 && j < a.V ? (int)j : -1;
+    };
+    const int col0 = column(lane), col1 = a.K > 32 ? column(lane + 32) : -1;
     const float gk = fmul_flush(fmul_flush(g, a.w_kd), a.tau);
     const float ca = fmul_flush(gk, P);
     const float cb = fmul_flush(g, fadd_ftz(lab >= 0 ? a.w_ce : 0.0f,
@@ -483,32 +551,13 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
     const u64 zero = dup2(-0.0f), nu = dup2(-Mu), nm = dup2(-M), sc = dup2(a.it), wa = dup2(qa), wb = dup2(qb);
     const int last = min(first + a.per, a.nblk);
     for (int blk = first; blk < last; ++blk) {
-        const int lo = blk * BLK - shift;
+        const int lo = blk * BBLK - shift;
         if (lo >= a.V)
             break;
-        float x[PER];
+        if (blk > first)
+            load_piece<T, SHIFT>(zr, lo, a.V, lane, x);
 #pragma unroll
-        for (int i = 0; i < PER; i += 4) {
-            if (SHIFT) {
-                const int e = lo + 32 * i + 4 * lane;
-                if (e >= 0 && e + 4 <= a.V) {
-                    const float4 v = load4(zr + e);
-                    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        x[i + c] = e + c >= 0 && e + c < a.V ? to_f32<T>(zr[e + c]) : -CUDART_INF_F;
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int e = lo + 32 * (i + c) + lane;
-                    x[i + c] = e < a.V ? to_f32<T>(zr[e]) : -CUDART_INF_F;
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < PER; i += 2) {
+        for (int i = 0; i < BPER; i += 2) {
             const u64 v = pack2(x[i], x[i + 1]);
             const u64 e = exp_neg2(fadd2_ftz(SUMS == ONE ? v : fmul2_rn(v, sc), nu));
             u64 d = fmul2_rn(e, wa);
@@ -518,60 +567,37 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
                 d = fadd2_ftz(d, zero);
             unpack2(d, x[i], x[i + 1]);
         }
-        // the teacher's entries and the label inside this block, entry by entry
+        // the teacher's entries and the label inside this piece, entry by entry
         auto take = [&](int e, float c) {
             const int slot = SHIFT ? (e >> 7) * 4 + (e & 3) : e >> 5;
             const int own = SHIFT ? (e >> 2) & 31 : e & 31;
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
+            for (int i = 0; i < BPER; ++i)
                 if (i == slot && lane == own)
                     x[i] = fadd_ftz(x[i], -c);
         };
         if (a.w_kd != 0.0f)
             for (int k0 = 0; k0 < a.K; k0 += 32) {
-                int e = -1;
-                if (k0 + lane < a.K) {
-                    const int64_t j = load_index(a.t_idx, a.index_bytes, (int64_t)row * a.K + k0 + lane);
-                    e = j >= max(lo, 0) && j < min((int64_t)lo + BLK, (int64_t)a.V) ? (int)j - lo : -1;
-                }
-                unsigned hits = __ballot_sync(0xffffffffu, e >= 0);
+                const int j = k0 == 0 ? col0 : k0 == 32 ? col1 : column(k0 + lane);
+                const bool here = j >= max(lo, 0) && j < lo + BBLK;
+                unsigned hits = __ballot_sync(0xffffffffu, here);
                 if (hits == 0)
                     continue;
-                const float c = e >= 0 ? fmul_flush(gk, st[STATS + k0 + lane]) : 0.0f;
+                const float c = here ? fmul_flush(gk, st[STATS + k0 + lane]) : 0.0f;
                 while (hits) {
                     const int src = __ffs(hits) - 1;
                     hits &= hits - 1;
-                    take(__shfl_sync(0xffffffffu, e, src), __shfl_sync(0xffffffffu, c, src));
+                    take(__shfl_sync(0xffffffffu, j - lo, src), __shfl_sync(0xffffffffu, c, src));
                 }
             }
-        if (lab >= max(lo, 0) && lab < lo + BLK)
+        if (lab >= max(lo, 0) && lab < lo + BBLK)
             take(lab - lo, fmul_flush(g, a.w_ce));
         if (none) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
+            for (int i = 0; i < BPER; ++i)
                 x[i] = 0.0f;
         }
-#pragma unroll
-        for (int i = 0; i < PER; i += 4) {
-            if (SHIFT) {
-                const int e = lo + 32 * i + 4 * lane;
-                if (e >= 0 && e + 4 <= a.V) {
-                    store4(dr + e, make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (e + c >= 0 && e + c < a.V)
-                            dr[e + c] = from_f32<T>(x[i + c]);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int e = lo + 32 * (i + c) + lane;
-                    if (e < a.V)
-                        dr[e] = from_f32<T>(x[i + c]);
-                }
-            }
-        }
+        store_piece<T, SHIFT>(dr, lo, a.V, lane, x);
     }
 }
 
@@ -671,12 +697,17 @@ template <typename T> cudaError_t bwd_typed(const DistillArgs& a, cudaStream_t s
     b.stats = a.stats;
     b.g = a.g;
     b.g_stride = a.g_stride;
-    // whole 4-element groups where both rows start equally far past a boundary
-    const uintptr_t zs = reinterpret_cast<uintptr_t>(a.z) / sizeof(T), ds = reinterpret_cast<uintptr_t>(a.dz) / sizeof(T);
-    const bool shift = zs % 4 == ds % 4 && (a.z_ld - a.dz_ld) % 4 == 0;
-    b.nblk = (int)blocks_of(a.V + (shift ? 3 : 0));
-    // four blocks a warp once that leaves every scheduler several warps
-    b.per = a.n * b.nblk >= (int64_t)num_sms() * 128 ? 4 : 1;
+    // pieces begin on 128 bytes, or else on 4 elements, where z and dz agree on that
+    auto agree = [&](int64_t m) {
+        return (reinterpret_cast<uintptr_t>(a.z) - reinterpret_cast<uintptr_t>(a.dz)) / sizeof(T) % m == 0 &&
+               (a.z_ld - a.dz_ld) % m == 0;
+    };
+    const int64_t line = 128 / sizeof(T);
+    const bool shift = agree(4);
+    b.mask = shift ? (int)(agree(line) ? line : 4) - 1 : 0;
+    b.nblk = (int)((a.V + b.mask + BBLK - 1) / BBLK);
+    // eight pieces a warp once that leaves every scheduler several warps
+    b.per = a.n * b.nblk >= (int64_t)num_sms() * 256 ? 8 : 1;
     b.groups = (b.nblk + b.per - 1) / b.per;
     b.items = (int)(a.n * b.groups);
     return by_sums(sums_of(a), [&](auto s) {

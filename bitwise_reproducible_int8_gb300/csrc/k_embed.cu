@@ -12,16 +12,18 @@
 // (stably, so ascending within a token) and every table element is summed by one
 // thread in the canonical order:
 //   1. k_embed_sort: one cluster of 8 CTAs sorts (token, position) by 8 bits a
-//      pass and lists the chunks of up to 64 positions.  The other clusters of the
-//      same launch zero the table rows that no token names (each marks its own
-//      rows' tokens in a bitmap first), so the sort hides behind the
-//      part of the write that needs no order.
-//   2. k_embed_sum: one warp per (chunk, 512 columns), left to right from the
-//      first term; a token's only chunk is scaled and stored, others leave their
-//      partial row in the workspace.
+//      pass and marks where chunks of up to 64 positions begin.  The other clusters
+//      of the same launch zero the table rows that no token names (each marks its
+//      own rows' tokens in a bitmap first), so the sort hides behind the part of the
+//      write that needs no order.
+//   2. k_embed_sum: the rows in sorted order as one stream per warp and piece of the
+//      columns, left to right from each chunk's first term; a token's only chunk is
+//      scaled and stored, others leave their partial row in the workspace.
 //   3. k_row_tree (k_rowtree.cu): the pairwise tree over a token's partial rows;
 //      only launched when n > 64, below which no token can have two chunks.
 #include <cooperative_groups.h>
+
+#include <atomic>
 
 #include "elem.cuh"
 #include "internal.h"
@@ -104,7 +106,11 @@ constexpr int SORT_CTAS = 8;      // CTAs of the sorting cluster
 constexpr int SORT_NT = 1024;
 constexpr int SORT_W = SORT_NT / 32;
 constexpr int DIGITS = 256;
-constexpr int LONG = 8;           // chunks of more positions than this are summed first
+constexpr int ZERO_BYTES = 16384; // zeroed shared memory that bulk copies read
+constexpr int ZERO_WARPS = 8;     // warps whose first lane issues them
+// what begins at a sorted index: a chunk with a partial row (>= 0), a token's only
+// chunk, nothing (inside a chunk), or no token at all (padding, out of range: the end)
+constexpr int WHOLE = -1, MIDDLE = -2, NOTHING = -3;
 
 struct SortArgs {
     const void* tokens;
@@ -115,8 +121,8 @@ struct SortArgs {
     uint2* a;            // (token, position), written by passes 0, 2, ..
     uint2* b;            // .. and by passes 1, 3
     int2* seg;           // [V] first and one past the last sorted index of a named token
-    int* counts;         // chunks at the list's front, tokens with several chunks, chunks at its back
-    int4* chunks;        // [n] {first sorted index, length, token, partial row or -1}
+    int* counts;         // tokens with several chunks
+    int4* order;         // [n] {position, token, what begins here, 0}
     int4* joins;         // {first sorted index, chunks, token, 0}
     float* table;        // rows to zero, or NULL
     int64_t table_ld;
@@ -152,8 +158,8 @@ __device__ void sort_cluster(const SortArgs& a, SortSmem& sm)
     // each warp owns a run of 32-element rounds, so that (CTA, warp, round, lane) is position order
     const int rounds = (a.n + SORT_CTAS * SORT_NT - 1) / (SORT_CTAS * SORT_NT);
     const int base = (rank * SORT_W + warp) * rounds * 32;
-    if (rank == 0 && tid < 3)
-        a.counts[tid] = 0;
+    if (rank == 0 && tid == 0)
+        a.counts[0] = 0;
     const uint2* src = nullptr;
     uint2* dst = a.a;
     for (int pass = 0; pass < a.passes; ++pass) {
@@ -243,25 +249,22 @@ __device__ void sort_cluster(const SortArgs& a, SortSmem& sm)
     }
     __threadfence();
     cluster.sync();
-    // the chunks: sorted index i starts one when it is a multiple of 64 past its token's
-    // first.  Long ones are listed from the front, short ones from the back, so that
-    // the sums start with what takes longest.
+    // sorted index i begins a chunk when it is a multiple of 64 past its token's first
     for (int i = rank * SORT_NT + tid; i < a.n; i += SORT_CTAS * SORT_NT) {
-        const unsigned key = ld_tok(src, i);
-        if (key >= (unsigned)a.V)
-            continue;
-        const int2 g = __ldcg(&a.seg[key]);
-        if ((i - g.x) & 63)
-            continue;
-        const bool several = g.y - g.x > 64;
-        const int len = g.y - i < 64 ? g.y - i : 64;
-        // a partial row of its own: in a run of 64 sorted indexes at most one chunk of a
-        // token with several starts that is its first, and at most one that is not
-        const int slot = several ? 2 * (i >> 6) + (g.x == i ? 1 : 0) : -1;
-        const int at = len > LONG ? atomicAdd(&a.counts[0], 1) : a.n - 1 - atomicAdd(&a.counts[2], 1);
-        a.chunks[at] = make_int4(i, len, (int)key, slot);
-        if (several && g.x == i)
-            a.joins[atomicAdd(&a.counts[1], 1)] = make_int4(i, (g.y - g.x + 63) / 64, (int)key, 0);
+        const uint2 kv = ld_pair(src + i);
+        int what = NOTHING;
+        if (kv.x < (unsigned)a.V) {
+            const int2 g = __ldcg(&a.seg[kv.x]);
+            const bool several = g.y - g.x > 64;
+            what = MIDDLE;
+            // a partial row of its own: in a run of 64 sorted indexes at most one chunk of a
+            // token with several starts that is its first, and at most one that is not
+            if (((i - g.x) & 63) == 0)
+                what = several ? 2 * (i >> 6) + (g.x == i ? 1 : 0) : WHOLE;
+            if (several && g.x == i)
+                a.joins[atomicAdd(&a.counts[0], 1)] = make_int4(i, (g.y - g.x + 63) / 64, (int)kv.x, 0);
+        }
+        a.order[i] = make_int4((int)kv.y, (int)kv.x, what, 0);
     }
 }
 
@@ -284,24 +287,45 @@ __device__ void zero_rows(const SortArgs& a, unsigned* bits, int v0, int v1)
                 atomicOr(&bits[(t[u] - v0) >> 5], 1u << ((t[u] - v0) & 31));
     }
     __syncthreads();
+    if (a.vec) {
+        // rows on 16 bytes: bulk copies of a zeroed piece of shared memory, one thread's
+        // instruction each, so that a row is written in one go (a warp's store per row
+        // kept thousands of rows open at once: 268 MB took 64 us)
+        float4* zero = reinterpret_cast<float4*>(bits + ((words + 31) & ~31));
+        for (int i = tid; i < ZERO_BYTES / 16; i += SORT_NT)
+            zero[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        const unsigned src = (unsigned)__cvta_generic_to_shared(zero);
+        if (warp < ZERO_WARPS && lane == 0) {
+            for (int v = v0 + warp; v < v1; v += ZERO_WARPS) {
+                if (bits[(v - v0) >> 5] >> ((v - v0) & 31) & 1u)
+                    continue;
+                char* row = reinterpret_cast<char*>(a.table + (int64_t)v * a.table_ld);
+                for (int64_t o = 0; o < a.D * 4; o += ZERO_BYTES) {
+                    const unsigned len = (unsigned)(a.D * 4 - o < ZERO_BYTES ? a.D * 4 - o : ZERO_BYTES);
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                                 :: "l"(row + o), "r"(src), "r"(len) : "memory");
+                }
+            }
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // shared memory is read until then
+        }
+        return;
+    }
     for (int v = v0 + warp; v < v1; v += SORT_W) {
         if (bits[(v - v0) >> 5] >> ((v - v0) & 31) & 1u)
             continue;
         float* row = a.table + (int64_t)v * a.table_ld;
-        if (a.vec) {
-            for (int64_t c = 4 * lane; c < a.D; c += 128)
-                store4(row + c, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
-        } else {
-            for (int64_t c = lane; c < a.D; c += 32)
-                row[c] = 0.0f;
-        }
+        for (int64_t c = lane; c < a.D; c += 32)
+            row[c] = 0.0f;
     }
 }
 
 __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_NT, 1)
 k_embed_sort(const SortArgs a)
 {
-    extern __shared__ unsigned dyn[];
+    extern __shared__ __align__(128) unsigned dyn[];
     if (blockIdx.x < SORT_CTAS) {
         sort_cluster(a, *reinterpret_cast<SortSmem*>(dyn));
     } else {
@@ -315,133 +339,179 @@ k_embed_sort(const SortArgs a)
 
 // ---------------------------------------------------------------- chunk sums
 
-constexpr int ES_G = 4;             // 4-element groups per lane
+constexpr int ES_G = 2;             // 4-element groups per lane
+constexpr int ES_U = 8;             // rows in flight
 constexpr int ES_COLS = 32 * 4 * ES_G;
-constexpr int ES_U = 2;             // rows in flight
+constexpr int ES_CTAS = 2;          // per SM
 
-// One warp per (chunk, 512 columns).  What a warp needs next (the chunk's entry, then
-// its positions) is fetched while the rows of the one before are on their way:
-// most tokens occur once or twice, so each chunk would otherwise cost three
-// dependent trips to memory.
+// columns of group g of this lane, from c0 on: four neighbours, or lane-strided single
+// elements where rows are unaligned
+template <bool VEC> __device__ __forceinline__ int64_t sum_col(int64_t c0, int lane, int g, int e)
+{
+    return c0 + (VEC ? 4 * (lane + 32 * g) + e : lane + 32 * (4 * g + e));
+}
+
 template <typename TD, bool VEC>
-__global__ void __launch_bounds__(256)
-k_embed_sum(const TD* __restrict__ dout, int64_t dout_ld, const uint2* __restrict__ sorted,
-            const int* __restrict__ counts, const int4* __restrict__ chunks, int n, int64_t D, float scale,
-            float* __restrict__ table, int64_t table_ld, bool accumulate, float* __restrict__ parts,
-            int segs, bool vec_out)
+__device__ __forceinline__ void sum_load(const TD* s, int64_t c0, int64_t D, int lane, float (&x)[ES_G][4])
+{
+#pragma unroll
+    for (int g = 0; g < ES_G; ++g) {
+        if (VEC) {
+            if (sum_col<VEC>(c0, lane, g, 0) < D) {
+                const float4 v = load4(s + sum_col<VEC>(c0, lane, g, 0));
+                x[g][0] = v.x, x[g][1] = v.y, x[g][2] = v.z, x[g][3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (sum_col<VEC>(c0, lane, g, e) < D)
+                    x[g][e] = to_f32<TD>(s[sum_col<VEC>(c0, lane, g, e)]);
+        }
+    }
+}
+
+// table (+) v where this is the only addition the element gets: the memory's own binary32
+// addition rounds to nearest and flushes subnormals like fadd_ftz, and the warp does not
+// wait for the old value (reading it first made the accumulating call 1.3 times as long)
+__device__ __forceinline__ void add_once(float* p, float4 v)
+{
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};"
+                 :: "l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+// a finished chunk: a partial row as it is, a token's only chunk scaled into the table
+template <bool VEC>
+__device__ __forceinline__ void sum_store(float* dst, bool part, bool wide, bool accumulate, float sc, int64_t c0,
+                                          int64_t D, int lane, const float (&acc)[ES_G][4])
+{
+#pragma unroll
+    for (int g = 0; g < ES_G; ++g) {
+        const int64_t c = sum_col<VEC>(c0, lane, g, 0);
+        if (VEC && wide) {
+            if (c >= D)
+                continue;
+            float4 v = make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
+            if (!part) {
+                v = make_float4(fmul_flush(v.x, sc), fmul_flush(v.y, sc), fmul_flush(v.z, sc), fmul_flush(v.w, sc));
+            }
+            if (!part && accumulate)
+                add_once(dst + c, v);
+            else
+                store4(dst + c, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t ce = sum_col<VEC>(c0, lane, g, e);
+                if (ce < D) {
+                    const float v = part ? acc[g][e] : fmul_flush(acc[g][e], sc);
+                    if (!part && accumulate)
+                        atomicAdd(dst + ce, v);
+                    else
+                        dst[ce] = v;
+                }
+            }
+        }
+    }
+}
+
+// A warp takes the chunks that begin among `span` sorted indexes, for one piece of the
+// columns, as one stream of rows: 8 rows are on their way at any time, across the chunks'
+// ends (most tokens occur once or twice; chunk by chunk every one cost a trip to
+// memory).  `span` leaves one stream to a warp, two where few rows meet many pieces.
+template <typename TD, bool VEC>
+__global__ void __launch_bounds__(256, ES_CTAS)
+k_embed_sum(const TD* __restrict__ dout, int64_t dout_ld, const int4* __restrict__ order, int n, int span,
+            int64_t D, float scale, float* __restrict__ table, int64_t table_ld, bool accumulate,
+            float* __restrict__ parts, int pieces, bool vec_out)
 {
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int longs = counts[0];
-    const int64_t items = (int64_t)(longs + counts[2]) * segs, step = (int64_t)gridDim.x * 8;
     const float sc = flush(scale);
     const int64_t pitch = (D + 3) & ~3LL;
-    int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (item >= items)
-        return;
-    auto entry = [&](int64_t it) {
-        const int ch = (int)(it / segs);
-        return chunks[ch < longs ? ch : n - 1 - (ch - longs)];
-    };
-    auto position = [&](const int4& c, int j) { return j < c.y ? sorted[c.x + j].y : 0u; };
-    int4 c = entry(item), next = c;
-    unsigned p0 = position(c, lane), p1 = c.y > 32 ? position(c, lane + 32) : 0u;
-    if (item + step < items)
-        next = entry(item + step);
-    for (; item < items; item += step) {
-        const int64_t c0 = (item % segs) * ES_COLS;
-        // column of group g, element e: four neighbours, or lane-strided where rows are unaligned
-        auto col = [&](int g, int e) { return c0 + (VEC ? 4 * (lane + 32 * g) + e : lane + 32 * (4 * g + e)); };
-        auto row = [&](int j, float (&x)[ES_G][4]) {
-            const unsigned pos = __shfl_sync(0xffffffffu, j < 32 ? p0 : p1, j & 31);
-            const TD* s = dout + (int64_t)pos * dout_ld;
+    const int64_t items = (int64_t)((n + span - 1) / span) * pieces;
+    for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < items; item += (int64_t)gridDim.x * 8) {
+        const int range = (int)(item / pieces);
+        const int64_t c0 = (item - (int64_t)range * pieces) * ES_COLS;
+        const int lo = range * span, hi = min(n, lo + span);
+        // the first index of the range at which a chunk begins
+        int at = hi;
+        for (int i = lo; i < hi && at == hi; i += 32) {
+            const unsigned m = __ballot_sync(0xffffffffu, i + lane < hi && order[i + lane].z >= WHOLE);
+            if (m)
+                at = i + __ffs(m) - 1;
+        }
+        if (at >= hi)
+            continue;
+        // 32 entries of the order at a time, the next 32 fetched ahead; {0, 0, NOTHING} past the end
+        const int4 none = make_int4(0, 0, NOTHING, 0);
+        int4 cur = at + lane < n ? order[at + lane] : none;
+        int4 ahead = at + 32 + lane < n ? order[at + 32 + lane] : none;
+        bool beyond = false;   // a chunk that begins past the range belongs to the next one
+        auto entry = [&](int k, int& pos, int& tok, int& what) {   // k < 64 from the window's start
+            pos = __shfl_sync(0xffffffffu, k < 32 ? cur.x : ahead.x, k & 31);
+            tok = __shfl_sync(0xffffffffu, k < 32 ? cur.y : ahead.y, k & 31);
+            what = __shfl_sync(0xffffffffu, k < 32 ? cur.z : ahead.z, k & 31);
+            beyond = beyond || (at + k >= hi && what != MIDDLE);
+            what = beyond ? NOTHING : what;
+        };
+        float x[ES_U][ES_G][4] = {}, acc[ES_G][4] = {};
+        int tok_of[ES_U], what_of[ES_U];
 #pragma unroll
-            for (int g = 0; g < ES_G; ++g) {
-                if (VEC) {
-                    if (col(g, 0) < D) {
-                        const float4 v = load4(s + col(g, 0));
-                        x[g][0] = v.x, x[g][1] = v.y, x[g][2] = v.z, x[g][3] = v.w;
-                    }
+        for (int u = 0; u < ES_U; ++u) {
+            int pos;
+            entry(u, pos, tok_of[u], what_of[u]);
+            if (what_of[u] != NOTHING)
+                sum_load<TD, VEC>(dout + (int64_t)pos * dout_ld, c0, D, lane, x[u]);
+        }
+        int slot = 0, row = 0;      // the open chunk: partial row or WHOLE, token
+        bool open = false;
+        int k = 0;                  // window index of the row in x[0]
+        for (;;) {
+            bool done = false;
+#pragma unroll
+            for (int u = 0; u < ES_U; ++u) {
+                const int what = what_of[u];
+                if (!done && what != MIDDLE) {
+                    if (open)
+                        sum_store<VEC>(slot >= 0 ? parts + (int64_t)slot * pitch : table + (int64_t)row * table_ld,
+                                       slot >= 0, slot >= 0 || vec_out, accumulate, sc, c0, D, lane, acc);
+                    done = what == NOTHING;
+                    open = true;
+                    slot = what;
+                    row = tok_of[u];
+#pragma unroll
+                    for (int g = 0; g < ES_G; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[g][e] = flush(x[u][g][e]);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (col(g, e) < D)
-                            x[g][e] = to_f32<TD>(s[col(g, e)]);
+                    for (int g = 0; g < ES_G; ++g)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[g][e] = fadd_ftz(acc[g][e], x[u][g][e]);
                 }
+                int pos;
+                entry(k + ES_U + u, pos, tok_of[u], what_of[u]);
+                if (what_of[u] != NOTHING)
+                    sum_load<TD, VEC>(dout + (int64_t)pos * dout_ld, c0, D, lane, x[u]);
             }
-        };
-        float acc[ES_G][4] = {}, x[ES_U][ES_G][4] = {};
-        row(0, acc);
-        // the next item's positions and the entry after it, behind the first row's loads
-        const unsigned q0 = position(next, lane), q1 = next.y > 32 ? position(next, lane + 32) : 0u;
-        const int4 after = item + 2 * step < items ? entry(item + 2 * step) : next;
-#pragma unroll
-        for (int g = 0; g < ES_G; ++g)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[g][e] = flush(acc[g][e]);
-        int j = 1;
-        for (; j + ES_U <= c.y; j += ES_U) {
-#pragma unroll
-            for (int u = 0; u < ES_U; ++u)
-                row(j + u, x[u]);
-#pragma unroll
-            for (int u = 0; u < ES_U; ++u)
-#pragma unroll
-                for (int g = 0; g < ES_G; ++g)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[g][e] = fadd_ftz(acc[g][e], x[u][g][e]);
-        }
-        for (; j < c.y; ++j) {
-            row(j, x[0]);
-#pragma unroll
-            for (int g = 0; g < ES_G; ++g)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[g][e] = fadd_ftz(acc[g][e], x[0][g][e]);
-        }
-        const bool part = c.w >= 0;
-        float* dst = part ? parts + (int64_t)c.w * pitch : table + (int64_t)c.z * table_ld;
-        const bool wide = VEC && (part || vec_out);
-#pragma unroll
-        for (int g = 0; g < ES_G; ++g) {
-            if (wide) {
-                if (col(g, 0) >= D)
-                    continue;
-                float4 v = make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
-                if (!part) {
-                    v = make_float4(fmul_flush(v.x, sc), fmul_flush(v.y, sc), fmul_flush(v.z, sc), fmul_flush(v.w, sc));
-                    if (accumulate) {
-                        const float4 o = load4(dst + col(g, 0));
-                        v = make_float4(fadd_ftz(o.x, v.x), fadd_ftz(o.y, v.y), fadd_ftz(o.z, v.z), fadd_ftz(o.w, v.w));
-                    }
-                }
-                store4(dst + col(g, 0), v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (col(g, e) < D) {
-                        float v = acc[g][e];
-                        if (!part) {
-                            v = fmul_flush(v, sc);
-                            if (accumulate)
-                                v = fadd_ftz(dst[col(g, e)], v);
-                        }
-                        dst[col(g, e)] = v;
-                    }
+            if (done)
+                break;
+            k += ES_U;
+            if (k == 32) {
+                at += 32;
+                k = 0;
+                cur = ahead;
+                ahead = at + 32 + lane < n ? order[at + 32 + lane] : none;
             }
         }
-        c = next;
-        next = after;
-        p0 = q0;
-        p1 = q1;
     }
 }
 
 // workspace: sorted pairs twice, chunk and join lists, counters, partial rows
 struct EmbedWs {
-    size_t a, b, seg, chunks, joins, counts, parts, total;
+    size_t a, b, seg, order, joins, counts, parts, total;
 };
 
 EmbedWs embed_ws(int64_t n, int64_t V, int64_t D)
@@ -452,13 +522,36 @@ EmbedWs embed_ws(int64_t n, int64_t V, int64_t D)
     w.a = 0;
     w.b = w.a + up((size_t)n * 8);
     w.seg = w.b + up((size_t)n * 8);
-    w.chunks = w.seg + up((size_t)V * 8);
-    w.joins = w.chunks + up((size_t)n * 16);
+    w.order = w.seg + up((size_t)V * 8);
+    w.joins = w.order + up((size_t)n * 16);
     w.counts = w.joins + up((size_t)blocks * 16);
     w.parts = w.counts + 256;
     // a token with several chunks has more than 64 positions
     w.total = w.parts + (n > 64 ? (size_t)(2 * blocks) * (size_t)((D + 3) & ~3LL) * 4 : 0);
     return w;
+}
+
+// CTAs that may zero rows beside the sorting cluster: a cluster's CTAs share a GPC,
+// so fewer clusters than SMs / 8 run at a time, and one more would start when the
+// others are done (all 18 of them: 57 us for 268 MB instead of 43)
+int fill_ctas()
+{
+    static std::atomic<int> known{0};
+    int v = known.load(std::memory_order_relaxed);
+    if (v == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(SORT_CTAS);
+        cfg.blockDim = dim3(SORT_NT);
+        cfg.dynamicSmemBytes = sizeof(SortSmem);
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, k_embed_sort, &cfg) != cudaSuccess || clusters < 2) {
+            cudaGetLastError();
+            clusters = 8;
+        }
+        v = (clusters - 1) * SORT_CTAS;
+        known.store(v, std::memory_order_relaxed);
+    }
+    return v;
 }
 
 template <typename TT, typename TO>
@@ -508,7 +601,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
     s.a = reinterpret_cast<uint2*>(p + w.a);
     s.b = reinterpret_cast<uint2*>(p + w.b);
     s.seg = reinterpret_cast<int2*>(p + w.seg);
-    s.chunks = reinterpret_cast<int4*>(p + w.chunks);
+    s.order = reinterpret_cast<int4*>(p + w.order);
     s.joins = reinterpret_cast<int4*>(p + w.joins);
     s.counts = reinterpret_cast<int*>(p + w.counts);
     s.table = a.table;
@@ -519,12 +612,12 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
     s.passes = 1;
     while (((int64_t)1 << (8 * s.passes)) <= a.V)   // keys 0 .. V
         ++s.passes;
-    const uint2* sorted = (s.passes & 1) ? s.a : s.b;
-    const int fill = a.accumulate ? 0 : (num_sms() / SORT_CTAS - 1) * SORT_CTAS;
+    const int fill = a.accumulate ? 0 : fill_ctas();
     const int per = fill > 0 ? (int)((a.V + fill - 1) / fill) : 0;
     size_t smem = sizeof(SortSmem);
-    if ((size_t)(per + 31) / 32 * 4 > smem)
-        smem = (size_t)(per + 31) / 32 * 4;
+    const size_t fill_smem = (size_t)(per + 31) / 32 * 4 + 128 + ZERO_BYTES;   // a bitmap and the zeros
+    if (fill_smem > smem)
+        smem = fill_smem;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)smem);
@@ -537,16 +630,18 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
     if (e != cudaSuccess || a.n == 0)
         return e;
     float* parts = reinterpret_cast<float*>(p + w.parts);
-    const int segs = (int)((a.D + ES_COLS - 1) / ES_COLS);
-    const int64_t most = (a.n * segs + 7) / 8, cap = (int64_t)num_sms() * 8;
+    const int pieces = (int)((a.D + ES_COLS - 1) / ES_COLS);
+    const int64_t warps = (int64_t)num_sms() * ES_CTAS * 8;
+    const int span = (int)((a.n * pieces + warps - 1) / warps);
+    const int64_t most = ((a.n + span - 1) / span * pieces + 7) / 8, cap = warps / 8;
     const unsigned grid = (unsigned)(most < cap ? most : cap);
     const bool vec_out = s.vec;
     auto sum = [&](auto type) {
         using T = decltype(type);
         auto go = [&](auto kernel) {
             return launch_pdl(kernel, dim3(grid), dim3(256), 0, st, static_cast<const T*>(a.dout), a.dout_ld,
-                              sorted, (const int*)s.counts, (const int4*)s.chunks, (int)a.n, a.D, a.scale,
-                              a.table, a.table_ld, a.accumulate, parts, segs, vec_out);
+                              (const int4*)s.order, (int)a.n, span, a.D, a.scale, a.table, a.table_ld,
+                              a.accumulate, parts, pieces, vec_out);
         };
         return a.D % 4 == 0 && rows4<T>(a.dout, a.dout_ld) ? go(k_embed_sum<T, true>) : go(k_embed_sum<T, false>);
     };
@@ -558,7 +653,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
     t.parts = parts;
     t.pitch = (a.D + 3) & ~3LL;
     t.joins = s.joins;
-    t.njoins = s.counts + 1;
+    t.njoins = s.counts;
     t.D = a.D;
     t.out = a.table;
     t.out_ld = a.table_ld;

@@ -5,13 +5,12 @@
 //   (a, b) turned by the position's angle.  Backward: turn the gradient back, then
 //   dx_d = r (x) (u_d (-) (h_d (x) c1)) with h = x r, u = dy gain, c1 = S'(u h) / D.
 //
-// One read and one write of the heads (and the gradient): bound by HBM.  A head
-// lies in the registers of 8, 16 or 32 lanes, 4, 8 or 16 consecutive elements
-// each, so the norm's order (groups of 4, then the pairwise tree) is a chain in a
-// lane and a butterfly over lanes, and no shared memory stands between the load
-// and the store.  A pair's other half is in the same lane (neighbour pairs), at a
-// fixed lane distance (halves, R / 2 a multiple of the lane's elements), or else
-// fetched through shared memory (every other width or alignment).
+// One read and one write of the heads (and the gradient): bound by HBM, and close
+// behind by the instructions issued.  A head lies in the registers of 8, 16 or 32
+// lanes, so the norm's order (groups of 4, then the pairwise tree) is a chain in a
+// lane and an exchange over lanes, and no shared memory stands between the load
+// and the store.  Two rows a lane share the exchanges and the root and division of
+// the norm; the arithmetic is on packed pairs.
 //
 // The gains' gradients are sums over all rows (token, head): a CTA of the backward
 // owns one 64-row chunk, leaves dy (x) h of each row in shared memory and adds the
@@ -25,50 +24,67 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int INTER = 0, HALF = 1, GENERIC = 2;   // how a rotation partner is found
+// How a rotation partner is found, and what a lane holds.  SPLIT: heads of 64, 128 or
+// 256 elements turned whole, by halves: a lane holds 4 elements of each half, both
+// members of its pairs and one set of cosines and sines for them.  Otherwise a lane
+// holds E consecutive elements: INTER, neighbour pairs (or no turn): in the lane;
+// HALF, by halves, R / 2 a multiple of E: at a fixed lane distance; GENERIC, anything
+// else, and rows off 4-element boundaries: through shared memory.
+constexpr int INTER = 0, HALF = 1, GENERIC = 2, SPLIT = 3;
 
 
-// the head's values in this lane: E elements from d0 on (0 past the width)
-template <typename T, int E, bool VEC>
-__device__ __forceinline__ void load_head(const T* p, int d0, int D, float (&x)[E])
+// first element of group g of 4 in this lane: l is the lane's place in the head
+template <int E, int MODE> __device__ __forceinline__ int group(int l, int g, int D)
 {
-    if (VEC) {
+    return MODE == SPLIT ? 4 * l + (g ? D >> 1 : 0) : E * l + 4 * g;
+}
+
+// the head's values in this lane (0 past the width)
+template <typename T, int E, int MODE, bool VEC>
+__device__ __forceinline__ void load_head(const T* p, int l, int D, float (&x)[E])
+{
 #pragma unroll
-        for (int g = 0; g < E; g += 4)
-            if (d0 + g < D) {
-                const float4 v = load4(p + d0 + g);
-                x[g] = v.x, x[g + 1] = v.y, x[g + 2] = v.z, x[g + 3] = v.w;
+    for (int g = 0; g < E / 4; ++g) {
+        const int d = group<E, MODE>(l, g, D);
+        if (VEC) {
+            if (MODE == SPLIT || d < D) {
+                const float4 v = load4(p + d);
+                x[4 * g] = v.x, x[4 * g + 1] = v.y, x[4 * g + 2] = v.z, x[4 * g + 3] = v.w;
             } else {
-                x[g] = x[g + 1] = x[g + 2] = x[g + 3] = 0.0f;
+                x[4 * g] = x[4 * g + 1] = x[4 * g + 2] = x[4 * g + 3] = 0.0f;
             }
-    } else {
+        } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            x[e] = d0 + e < D ? to_f32<T>(p[d0 + e]) : 0.0f;
+            for (int e = 0; e < 4; ++e)
+                x[4 * g + e] = d + e < D ? to_f32<T>(p[d + e]) : 0.0f;
+        }
     }
 }
 
-template <typename T, int E, bool VEC>
-__device__ __forceinline__ void store_head(T* p, int d0, int D, const float (&x)[E])
+template <typename T, int E, int MODE, bool VEC>
+__device__ __forceinline__ void store_head(T* p, int l, int D, const float (&x)[E])
 {
-    if (VEC) {
 #pragma unroll
-        for (int g = 0; g < E; g += 4)
-            if (d0 + g < D)
-                store4(p + d0 + g, make_float4(x[g], x[g + 1], x[g + 2], x[g + 3]));
-    } else {
+    for (int g = 0; g < E / 4; ++g) {
+        const int d = group<E, MODE>(l, g, D);
+        if (VEC) {
+            if (MODE == SPLIT || d < D)
+                store4(p + d, make_float4(x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]));
+        } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (d0 + e < D)
-                p[d0 + e] = from_f32<T>(x[e]);
+            for (int e = 0; e < 4; ++e)
+                if (d + e < D)
+                    p[d + e] = from_f32<T>(x[4 * g + e]);
+        }
     }
 }
 
 // In-lane part of S of the terms a_e (x) b_e: groups of 4 left to right, then the
-// pairwise tree over the lane's groups.  A term past the width counts as -0, which
-// leaves every sum as it is.
-template <int E>
-__device__ __forceinline__ float lane_sum(const u64 (&a)[E / 2], const u64 (&b)[E / 2], int d0, int D)
+// pairwise tree over the lane's groups (SPLIT: the two halves' groups stay apart
+// until the lanes are done).  A term past the width counts as -0, which leaves
+// every sum as it is.
+template <int E, int MODE>
+__device__ __forceinline__ void lane_sum(const u64 (&a)[E / 2], const u64 (&b)[E / 2], int l, int D, float* out)
 {
     float g[E / 4];
 #pragma unroll
@@ -76,37 +92,48 @@ __device__ __forceinline__ float lane_sum(const u64 (&a)[E / 2], const u64 (&b)[
         float p[4];
         unpack2(fmul2_rn(a[2 * k], b[2 * k]), p[0], p[1]);
         unpack2(fmul2_rn(a[2 * k + 1], b[2 * k + 1]), p[2], p[3]);
+        const int d = group<E, MODE>(l, k, D);
+        if (MODE == GENERIC) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            p[e] = d0 + 4 * k + e < D ? p[e] : -0.0f;
+            for (int e = 0; e < 4; ++e)
+                p[e] = d + e < D ? p[e] : -0.0f;
+        }
         g[k] = fadd_ftz(fadd_ftz(fadd_ftz(p[0], p[1]), p[2]), p[3]);
+        if (MODE == INTER || MODE == HALF)
+            g[k] = d < D ? g[k] : -0.0f;
+    }
+    if (MODE == SPLIT) {
+        out[0] = g[0];
+        out[1] = g[E / 4 - 1];
+        return;
     }
 #pragma unroll
     for (int s = 1; s < E / 4; s *= 2)
 #pragma unroll
         for (int k = 0; k + s < E / 4; k += 2 * s)
             g[k] = fadd_ftz(g[k], g[k + s]);
-    return g[0];
+    out[0] = g[0];
 }
 
-// The tree over the LPH lanes of U rows at once.  At the first log2 U levels a lane
-// keeps half of the rows it still has and hands its partner the others, so 4 rows
-// take 6 exchanges instead of 20, and every row's sum ends up in its own lanes:
-// this lane gets row own_row<U>(lane), and lane_of<U>(u) holds row u.
-template <int U, int LPH> __device__ __forceinline__ float rows_tree(const float (&S)[U], int lane)
+// The tree over the LPH lanes of U rows at once.  At the first levels a lane keeps
+// half of the sums it still has and hands its partner the others, so 4 sums take 6
+// exchanges instead of 20, and every row's sum ends up in lanes of its own:
+// lane_of<U, MODE>(u) holds row u.  SPLIT has two sums a row, a half each, joined last.
+template <int U, int LPH, int MODE> __device__ __forceinline__ float rows_tree(const float* S, int lane)
 {
     constexpr unsigned ALL = 0xffffffffu;
+    constexpr int N = MODE == SPLIT ? 2 * U : U;
     float v;
     int s = 1;
-    if (U == 4) {
+    if (N == 4) {
         const bool hi = lane & 1, hi2 = lane & 2;
-        const float a = fadd_ftz(hi ? S[2 % U] : S[0], __shfl_xor_sync(ALL, hi ? S[0] : S[2 % U], 1));
-        const float b = fadd_ftz(hi ? S[3 % U] : S[1 % U], __shfl_xor_sync(ALL, hi ? S[1 % U] : S[3 % U], 1));
+        const float a = fadd_ftz(hi ? S[2] : S[0], __shfl_xor_sync(ALL, hi ? S[0] : S[2], 1));
+        const float b = fadd_ftz(hi ? S[3] : S[1], __shfl_xor_sync(ALL, hi ? S[1] : S[3], 1));
         v = fadd_ftz(hi2 ? b : a, __shfl_xor_sync(ALL, hi2 ? a : b, 2));
         s = 4;
-    } else if (U == 2) {
+    } else if (N == 2) {
         const bool hi = lane & 1;
-        v = fadd_ftz(hi ? S[1 % U] : S[0], __shfl_xor_sync(ALL, hi ? S[0] : S[1 % U], 1));
+        v = fadd_ftz(hi ? S[1] : S[0], __shfl_xor_sync(ALL, hi ? S[0] : S[1], 1));
         s = 2;
     } else {
         v = S[0];
@@ -114,10 +141,15 @@ template <int U, int LPH> __device__ __forceinline__ float rows_tree(const float
 #pragma unroll
     for (; s < LPH; s *= 2)
         v = fadd_ftz(v, __shfl_xor_sync(ALL, v, s));
+    if (MODE == SPLIT)   // rows in lane bit 0, halves in bit 1
+        v = fadd_ftz(v, __shfl_xor_sync(ALL, v, 2));
     return v;
 }
 
-template <int U> __device__ __forceinline__ int lane_of(int u) { return U == 4 ? (u >> 1) | ((u & 1) << 1) : u; }
+template <int U, int MODE> __device__ __forceinline__ int lane_of(int u)
+{
+    return U == 4 ? (u >> 1) | ((u & 1) << 1) : u;
+}
 
 // S (/) D; by an exact product where D is a power of two
 __device__ __forceinline__ float over_width(float S, float width, float inv)
@@ -131,26 +163,33 @@ __device__ __forceinline__ float rnorm(float S, float width, float inv, float ep
 }
 
 // the turn of a position for this lane's elements: out_e = v_e c_e + w_e s_e, w_e the
-// other member of the pair, s_e with its sign (BACK: the turn undone)
+// other member of the pair, s_e with its sign (BACK: the turn undone).  SPLIT: of the
+// lower half's elements; the upper half's s is the negative.
 template <int E, int MODE, bool BACK>
-__device__ __forceinline__ void load_turn(u64 (&c)[E / 2], u64 (&s)[E / 2], const float* __restrict__ cs, int d0,
-                                          int R, bool inter)
+__device__ __forceinline__ void load_turn(u64 (&c)[E / 2], u64 (&s)[E / 2], const float* __restrict__ cs, int l,
+                                          int D, int R, bool inter)
 {
     const int half = R >> 1;
     const u64 z = pack2(-0.0f, -0.0f);
-    if (MODE == HALF) {
-        if (d0 < R) {
-            const bool low = d0 < half;
-            const int j0 = low ? d0 : d0 - half;
+    if (MODE == HALF || MODE == SPLIT) {
+        const int d0 = E * l;
+        if (MODE == SPLIT || d0 < R) {
+            const bool low = MODE == SPLIT || d0 < half;
+            const int j0 = MODE == SPLIT ? 4 * l : low ? d0 : d0 - half;
             const bool minus = low != BACK;
 #pragma unroll
-            for (int g = 0; g < E; g += 4) {
+            for (int g = 0; g < (MODE == SPLIT ? 4 : E); g += 4) {
                 const float4 a = __ldg(reinterpret_cast<const float4*>(cs + j0 + g));
                 const float4 b = __ldg(reinterpret_cast<const float4*>(cs + half + j0 + g));
                 c[g / 2] = fadd2_ftz(pack2(a.x, a.y), z);
                 c[g / 2 + 1] = fadd2_ftz(pack2(a.z, a.w), z);
                 s[g / 2] = fadd2_ftz(minus ? pack2(-b.x, -b.y) : pack2(b.x, b.y), z);
                 s[g / 2 + 1] = fadd2_ftz(minus ? pack2(-b.z, -b.w) : pack2(b.z, b.w), z);
+            }
+            if (MODE == SPLIT) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    s[E / 4 + i] = fmul2_rn(s[i], pack2(-1.0f, -1.0f));
             }
         }
     } else {
@@ -159,7 +198,7 @@ __device__ __forceinline__ void load_turn(u64 (&c)[E / 2], u64 (&s)[E / 2], cons
             float cc[2] = {0.0f, 0.0f}, ss[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int d = d0 + e + i;
+                const int d = E * l + e + i;
                 if (d < R) {
                     const bool pairs = MODE == INTER || inter;
                     const bool low = pairs ? !(d & 1) : d < half;
@@ -177,10 +216,19 @@ __device__ __forceinline__ void load_turn(u64 (&c)[E / 2], u64 (&s)[E / 2], cons
 
 // v turned in place; elements from R on are left alone
 template <int E, int MODE>
-__device__ __forceinline__ void turn(u64 (&v)[E / 2], const u64 (&c)[E / 2], const u64 (&s)[E / 2], int d0, int D,
+__device__ __forceinline__ void turn(u64 (&v)[E / 2], const u64 (&c)[E / 2], const u64 (&s)[E / 2], int l, int D,
                                      int R, bool inter, float* row)
 {
-    const int half = R >> 1;
+    if (MODE == SPLIT) {   // E = 8: pairs 0, 1 of the lower half, 2, 3 of the upper
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            const u64 a = v[i], b = v[E / 4 + i];
+            v[i] = fadd2_ftz(fmul2_rn(a, c[i]), fmul2_rn(b, s[i]));
+            v[E / 4 + i] = fadd2_ftz(fmul2_rn(b, c[i]), fmul2_rn(a, s[E / 4 + i]));
+        }
+        return;
+    }
+    const int half = R >> 1, d0 = E * l;
     u64 w[E / 2];
     if (MODE == INTER) {
 #pragma unroll
@@ -273,29 +321,29 @@ template <int U> struct Rows {
     }
 };
 
-// U rows' values from memory, flushed, as packed pairs (0 for rows past the end)
-template <typename T, int E, bool VEC>
-__device__ __forceinline__ void load_row(const T* p, bool live, int d0, int D, u64 (&v)[E / 2])
+// a row's values from memory as packed pairs (0 for rows past the end)
+template <typename T, int E, int MODE, bool VEC>
+__device__ __forceinline__ void load_row(const T* p, bool live, int l, int D, u64 (&v)[E / 2])
 {
     float x[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
         x[e] = 0.0f;
     if (live)
-        load_head<T, E, VEC>(p, d0, D, x);
+        load_head<T, E, MODE, VEC>(p, l, D, x);
 #pragma unroll
     for (int i = 0; i < E / 2; ++i)
         v[i] = pack2(x[2 * i], x[2 * i + 1]);
 }
 
-template <typename T, int E, bool VEC>
-__device__ __forceinline__ void store_row(T* p, int d0, int D, const u64 (&v)[E / 2])
+template <typename T, int E, int MODE, bool VEC>
+__device__ __forceinline__ void store_row(T* p, int l, int D, const u64 (&v)[E / 2])
 {
     float x[E];
 #pragma unroll
     for (int i = 0; i < E / 2; ++i)
         unpack2(v[i], x[2 * i], x[2 * i + 1]);
-    store_head<T, E, VEC>(p, d0, D, x);
+    store_head<T, E, MODE, VEC>(p, l, D, x);
 }
 
 template <int N> __device__ __forceinline__ void mul_flush(u64 (&v)[N], const u64 (&w)[N])
@@ -323,12 +371,14 @@ template <int N> __device__ __forceinline__ void flush_row(u64 (&v)[N])
 }
 
 // this lane's gains, flushed
-template <int E> __device__ __forceinline__ void load_gain(const float* gain, int d0, int D, u64 (&g)[E / 2])
+template <int E, int MODE> __device__ __forceinline__ void load_gain(const float* gain, int l, int D, u64 (&g)[E / 2])
 {
     float x[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        x[e] = gain && d0 + e < D ? __ldg(gain + d0 + e) : 0.0f;
+    for (int e = 0; e < E; ++e) {
+        const int d = group<E, MODE>(l, e / 4, D) + e % 4;
+        x[e] = gain && d < D ? __ldg(gain + d) : 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < E / 2; ++i)
         g[i] = pack2(x[2 * i], x[2 * i + 1]);
@@ -343,10 +393,11 @@ k_qk_fwd(const __grid_constant__ QkArgs a, unsigned blocks_q)
 {
     constexpr int HPW = 32 / LPH;   // heads a warp holds
     constexpr int U = fwd_rows(E);
+    constexpr int N = MODE == SPLIT ? 2 : 1;
     constexpr bool VEC = MODE != GENERIC;
     __shared__ float rows[MODE == GENERIC ? 8 * HPW * E * LPH : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int D = (int)a.D, R = (int)a.R, d0 = (lane % LPH) * E, sub = lane / LPH;
+    const int D = (int)a.D, R = (int)a.R, l = lane % LPH, sub = lane / LPH;
     float* srow = rows + (MODE == GENERIC ? (warp * HPW + sub) * E * LPH : 0);
     const bool is_q = blockIdx.x < blocks_q;
     const QkTensor& t = is_q ? a.t[0] : a.t[1];
@@ -358,31 +409,31 @@ k_qk_fwd(const __grid_constant__ QkArgs a, unsigned blocks_q)
     u64 x[U][E / 2];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        load_row<T, E, VEC>(static_cast<const T*>(t.x) + at.at[u], at.live[u], d0, D, x[u]);
+        load_row<T, E, MODE, VEC>(static_cast<const T*>(t.x) + at.at[u], at.live[u], l, D, x[u]);
     if (__ballot_sync(0xffffffffu, at.live[0]) == 0)
         return;
     u64 c[E / 2] = {}, s[E / 2] = {}, g[E / 2];
     bool ok;
-    const float* cs = rope_row(a, at.live[0] ? at.tok[0] : 0u, at.live[0] && d0 == 0, ok);
-    load_turn<E, MODE, false>(c, s, cs, d0, R, a.interleaved);
-    load_gain<E>(t.gain, d0, D, g);
-    float S[U];
+    const float* cs = rope_row(a, at.live[0] ? at.tok[0] : 0u, at.live[0] && l == 0, ok);
+    load_turn<E, MODE, false>(c, s, cs, l, D, R, a.interleaved);
+    load_gain<E, MODE>(t.gain, l, D, g);
+    float S[N * U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         flush_row(x[u]);
-        S[u] = lane_sum<E>(x[u], x[u], d0, D);
+        lane_sum<E, MODE>(x[u], x[u], l, D, S + N * u);
     }
-    const float r = rnorm(rows_tree<U, LPH>(S, lane), (float)D, a.inv, flush(a.eps));
+    const float r = rnorm(rows_tree<U, LPH, MODE>(S, lane), (float)D, a.inv, flush(a.eps));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        mul_flush(x[u], __shfl_sync(0xffffffffu, r, lane_of<U>(u), LPH));
+        mul_flush(x[u], __shfl_sync(0xffffffffu, r, lane_of<U, MODE>(u), LPH));
         if (t.gain)
             mul_flush(x[u], g);
         if (u > 0 && at.turned[u] && at.live[u]) {
-            cs = rope_row(a, at.tok[u], d0 == 0, ok);
-            load_turn<E, MODE, false>(c, s, cs, d0, R, a.interleaved);
+            cs = rope_row(a, at.tok[u], l == 0, ok);
+            load_turn<E, MODE, false>(c, s, cs, l, D, R, a.interleaved);
         }
-        turn<E, MODE>(x[u], c, s, d0, D, R, a.interleaved, srow);
+        turn<E, MODE>(x[u], c, s, l, D, R, a.interleaved, srow);
         if (!ok) {
 #pragma unroll
             for (int i = 0; i < E / 2; ++i)
@@ -390,29 +441,30 @@ k_qk_fwd(const __grid_constant__ QkArgs a, unsigned blocks_q)
         }
         if (at.live[u]) {
             float* o = t.out + (int64_t)(row0 + u) * D;
-            if (D % 4 == 0)
-                store_row<float, E, true>(o, d0, D, x[u]);
+            if (VEC || D % 4 == 0)
+                store_row<float, E, MODE, true>(o, l, D, x[u]);
             else
-                store_row<float, E, false>(o, d0, D, x[u]);
+                store_row<float, E, MODE, false>(o, l, D, x[u]);
         }
     }
 }
 
 constexpr int CHUNK = 64;   // rows of a chunk of the gains' canonical sums
-__host__ __device__ constexpr int bwd_rows(int E, int LPH) { return E == 4 ? (LPH == 8 ? 2 : 4) : E == 8 ? 2 : 1; }
+__host__ __device__ constexpr int bwd_rows(int E, int LPH) { return E == 16 ? 1 : 2; }
 
 template <typename T, int E, int LPH, int MODE>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, E == 16 ? 2 : 3)
 k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict__ parts, int64_t pitch)
 {
     constexpr int HPW = 32 / LPH;
     constexpr int U = bwd_rows(E, LPH);
+    constexpr int N = MODE == SPLIT ? 2 : 1;
     constexpr int PER = CHUNK / (8 * HPW);   // consecutive rows of the chunk per LPH lanes
     constexpr bool VEC = MODE != GENERIC;
     __shared__ float rows[MODE == GENERIC ? 8 * HPW * E * LPH : 1];
     extern __shared__ float terms[];   // [CHUNK][D] with a gain
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int D = (int)a.D, R = (int)a.R, d0 = (lane % LPH) * E, sub = lane / LPH;
+    const int D = (int)a.D, R = (int)a.R, l = lane % LPH, sub = lane / LPH;
     float* srow = rows + (MODE == GENERIC ? (warp * HPW + sub) * E * LPH : 0);
     const bool is_q = blockIdx.x < chunks_q;
     const QkTensor& t = is_q ? a.t[0] : a.t[1];
@@ -421,7 +473,7 @@ k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict_
     const float width = (float)D, eps = flush(a.eps);
     const bool gain = t.gain != nullptr;
     u64 g[E / 2];
-    load_gain<E>(t.gain, d0, D, g);
+    load_gain<E, MODE>(t.gain, l, D, g);
 #pragma unroll 1
     for (int k0 = 0; k0 < PER; k0 += U) {
         const unsigned row0 = first + (unsigned)((warp * HPW + sub) * PER + k0);
@@ -432,41 +484,41 @@ k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict_
         u64 x[U][E / 2], dy[U][E / 2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            load_row<T, E, VEC>(static_cast<const T*>(t.x) + at.at[u], at.live[u], d0, D, x[u]);
+            load_row<T, E, MODE, VEC>(static_cast<const T*>(t.x) + at.at[u], at.live[u], l, D, x[u]);
             const float* p = t.dout + (int64_t)(row0 + u) * D;
-            if (D % 4 == 0)
-                load_row<float, E, true>(p, at.live[u], d0, D, dy[u]);
+            if (VEC || D % 4 == 0)
+                load_row<float, E, MODE, true>(p, at.live[u], l, D, dy[u]);
             else
-                load_row<float, E, false>(p, at.live[u], d0, D, dy[u]);
+                load_row<float, E, MODE, false>(p, at.live[u], l, D, dy[u]);
         }
         u64 c[E / 2] = {}, s[E / 2] = {};
         bool ok[U];
-        const float* cs = rope_row(a, at.live[0] ? at.tok[0] : 0u, at.live[0] && d0 == 0, ok[0]);
-        load_turn<E, MODE, true>(c, s, cs, d0, R, a.interleaved);
-        float S[U];
+        const float* cs = rope_row(a, at.live[0] ? at.tok[0] : 0u, at.live[0] && l == 0, ok[0]);
+        load_turn<E, MODE, true>(c, s, cs, l, D, R, a.interleaved);
+        float S[N * U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             flush_row(x[u]);
-            S[u] = lane_sum<E>(x[u], x[u], d0, D);
+            lane_sum<E, MODE>(x[u], x[u], l, D, S + N * u);
         }
-        const float r = rnorm(rows_tree<U, LPH>(S, lane), width, a.inv, eps);
+        const float r = rnorm(rows_tree<U, LPH, MODE>(S, lane), width, a.inv, eps);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (u > 0) {
                 ok[u] = ok[u - 1];
                 if (at.turned[u] && at.live[u]) {
-                    cs = rope_row(a, at.tok[u], d0 == 0, ok[u]);
-                    load_turn<E, MODE, true>(c, s, cs, d0, R, a.interleaved);
+                    cs = rope_row(a, at.tok[u], l == 0, ok[u]);
+                    load_turn<E, MODE, true>(c, s, cs, l, D, R, a.interleaved);
                 }
             }
             flush_row(dy[u]);
-            turn<E, MODE>(dy[u], c, s, d0, D, R, a.interleaved, srow);
-            mul_flush(x[u], __shfl_sync(0xffffffffu, r, lane_of<U>(u), LPH));   // h
+            turn<E, MODE>(dy[u], c, s, l, D, R, a.interleaved, srow);
+            mul_flush(x[u], __shfl_sync(0xffffffffu, r, lane_of<U, MODE>(u), LPH));   // h
             if (gain) {
                 u64 p[E / 2];
 #pragma unroll
                 for (int i = 0; i < E / 2; ++i)
-                    p[i] = ok[u] ? dy[u][i] : 0ull;
+                    p[i] = dy[u][i];
                 mul_flush(p, x[u]);
                 if (!ok[u]) {
 #pragma unroll
@@ -475,20 +527,20 @@ k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict_
                 }
                 if (at.live[u]) {
                     float* o = terms + (row0 + u - first) * D;
-                    if (D % 4 == 0)
-                        store_row<float, E, true>(o, d0, D, p);
+                    if (VEC || D % 4 == 0)
+                        store_row<float, E, MODE, true>(o, l, D, p);
                     else
-                        store_row<float, E, false>(o, d0, D, p);
+                        store_row<float, E, MODE, false>(o, l, D, p);
                 }
                 mul_flush(dy[u], g);
             }
-            S[u] = lane_sum<E>(dy[u], x[u], d0, D);
+            lane_sum<E, MODE>(dy[u], x[u], l, D, S + N * u);
         }
-        const float c1 = over_width(rows_tree<U, LPH>(S, lane), width, a.inv);
+        const float c1 = over_width(rows_tree<U, LPH, MODE>(S, lane), width, a.inv);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float ru = __shfl_sync(0xffffffffu, r, lane_of<U>(u), LPH);
-            const float cu = __shfl_sync(0xffffffffu, c1, lane_of<U>(u), LPH);
+            const float ru = __shfl_sync(0xffffffffu, r, lane_of<U, MODE>(u), LPH);
+            const float cu = __shfl_sync(0xffffffffu, c1, lane_of<U, MODE>(u), LPH);
             const u64 nc = pack2(-cu, -cu);
 #pragma unroll
             for (int i = 0; i < E / 2; ++i)
@@ -505,7 +557,7 @@ k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict_
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (to.live[u])
-                store_row<T, E, VEC>(static_cast<T*>(t.dx) + to.at[u], d0, D, x[u]);
+                store_row<T, E, MODE, VEC>(static_cast<T*>(t.dx) + to.at[u], l, D, x[u]);
     }
     if (gain) {
         __syncthreads();
@@ -536,19 +588,20 @@ template <typename T> int mode_of(const QkArgs& a, int E, bool back)
         return GENERIC;
     if (a.interleaved || a.R == 0)
         return INTER;
+    if (a.R == a.D && (a.D == 64 || a.D == 128 || a.D == 256))
+        return SPLIT;
     return (a.R / 2) % E == 0 ? HALF : GENERIC;
 }
 
-// calls f(E, LPH) as compile-time constants for the head width: up to 128
-// elements 4 per lane in 8, 16 or 32 lanes, wider ones 8 or 16 per lane
+// calls f(E, LPH) as compile-time constants for the head width
 template <typename F> cudaError_t by_width(int64_t D, F f)
 {
     if (D <= 32)
         return f(std::integral_constant<int, 4>(), std::integral_constant<int, 8>());
     if (D <= 64)
-        return f(std::integral_constant<int, 4>(), std::integral_constant<int, 16>());
+        return f(std::integral_constant<int, 8>(), std::integral_constant<int, 8>());
     if (D <= 128)
-        return f(std::integral_constant<int, 4>(), std::integral_constant<int, 32>());
+        return f(std::integral_constant<int, 8>(), std::integral_constant<int, 16>());
     if (D <= 256)
         return f(std::integral_constant<int, 8>(), std::integral_constant<int, 32>());
     return f(std::integral_constant<int, 16>(), std::integral_constant<int, 32>());
@@ -566,8 +619,10 @@ template <typename T> cudaError_t fwd_typed(const QkArgs& a, cudaStream_t st)
             k_qk_fwd<T, E, LPH, INTER><<<grid, 256, 0, st>>>(a, bq);
         else if (m == HALF)
             k_qk_fwd<T, E, LPH, HALF><<<grid, 256, 0, st>>>(a, bq);
-        else
+        else if (m == GENERIC)
             k_qk_fwd<T, E, LPH, GENERIC><<<grid, 256, 0, st>>>(a, bq);
+        else if constexpr (E == 8)
+            k_qk_fwd<T, E, LPH, SPLIT><<<grid, 256, 0, st>>>(a, bq);
         count_launches(1);
         return cudaGetLastError();
     });
@@ -592,8 +647,14 @@ template <typename T> cudaError_t bwd_typed(const QkArgs& a, float* parts, int64
             count_launches(1);
             return cudaGetLastError();
         };
-        return m == INTER ? go(k_qk_bwd<T, E, LPH, INTER>)
-               : m == HALF ? go(k_qk_bwd<T, E, LPH, HALF>) : go(k_qk_bwd<T, E, LPH, GENERIC>);
+        if (m == INTER)
+            return go(k_qk_bwd<T, E, LPH, INTER>);
+        if (m == HALF)
+            return go(k_qk_bwd<T, E, LPH, HALF>);
+        if constexpr (E == 8)
+            if (m == SPLIT)
+                return go(k_qk_bwd<T, E, LPH, SPLIT>);
+        return go(k_qk_bwd<T, E, LPH, GENERIC>);
     });
 }
 

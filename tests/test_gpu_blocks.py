@@ -97,6 +97,24 @@ def test_embed_bwd(orc, n, V, D, kind, accumulate):
         assert np.all(np.abs(host(dW) - e64) <= bound)
 
 
+@pytest.mark.parametrize("D", [8, 5])
+def test_embed_bwd_subnormals(orc, D):
+    """Old values, sums and results below the smallest normal are flushed, however
+    the addition into the table is done."""
+    tiny = np.float32(2.0 ** -126)
+    d = np.tile(np.float32([1.5 * tiny, -1.25 * tiny, 0.5 * tiny, 3.0]), (6, 2))[:, :D]
+    tok = np.array([0, 1, 1, 2, 3, 4])
+    acc = np.zeros((6, D), dtype=np.float32)
+    acc[0] = -1.25 * tiny
+    acc[1] = 0.75 * tiny
+    acc[2] = 1.0
+    acc[3] = -1.5 * tiny
+    for scale in (1.0, 0.25):
+        dW = dev(acc.copy())
+        R.repro_embed_bwd(dev(d), dev(tok), dW, scale=scale, accumulate=True)
+        same(host(dW), orc.embed_bwd(d, tok, 6, scale, -1, acc))
+
+
 def test_embed_out_of_range_tokens(orc):
     g = rng(1)
     W, d = g.standard_normal((10, 36)).astype(np.float32), g.standard_normal((5, 36)).astype(np.float32)
