@@ -41,6 +41,35 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v)
     *reinterpret_cast<uint2*>(p) = o;
 }
 
+// 16 bytes: four binary32 or eight bf16 neighbours, widened
+__device__ __forceinline__ void load16(const float* p, float* x)
+{
+    const float4 v = load4(p);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* x)
+{
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ void store16(float* p, const float* x) { store4(p, make_float4(x[0], x[1], x[2], x[3])); }
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float* x)
+{
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const unsigned*>(&v);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // index i of a list of int32 (bytes 4) or int64 (bytes 8)
 __device__ __forceinline__ int64_t load_index(const void* p, int bytes, int64_t i)
 {

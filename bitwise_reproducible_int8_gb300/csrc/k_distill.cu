@@ -159,26 +159,25 @@ template <bool VEC> __device__ __forceinline__ int element(int i, int lane)
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_block(const T* p, int len, int lane, float (&x)[PER])
 {
-    if (VEC) {
-        // rows on 4-element boundaries may still end inside a group
+    if (len == BLK) {   // all but a row's last block: no bounds
+        const T* q = p + (VEC ? 4 * lane : lane);
 #pragma unroll
         for (int i = 0; i < PER; i += 4) {
-            const int e = element<true>(i, lane);
-            if (e + 4 <= len) {
-                const float4 v = load4(p + e);
+            if (VEC) {
+                const float4 v = load4(q + 32 * i);
                 x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
             } else {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    x[i + c] = e + c < len ? to_f32<T>(p[e + c]) : -CUDART_INF_F;
+                    x[i + c] = to_f32<T>(q[32 * (i + c)]);
             }
         }
-    } else {
+        return;
+    }
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = element<false>(i, lane);
-            x[i] = e < len ? to_f32<T>(p[e]) : -CUDART_INF_F;
-        }
+    for (int i = 0; i < PER; ++i) {
+        const int e = element<VEC>(i, lane);
+        x[i] = e < len ? to_f32<T>(p[e]) : -CUDART_INF_F;
     }
 }
 
@@ -262,6 +261,7 @@ __device__ __forceinline__ void do_block(const T* z, int64_t z_ld, const FwdArgs
 }
 
 constexpr int WARPS = 8;
+constexpr int FWD_CTAS = 5;
 constexpr int MAX_ROWS = 8;   // rows a CTA joins at a time
 
 struct RowShared {
@@ -402,7 +402,7 @@ __device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, 
 
 // a CTA owns `rows` rows: their blocks, then their losses
 template <typename T, int SUMS, bool VEC>
-__global__ void __launch_bounds__(32 * WARPS)
+__global__ void __launch_bounds__(32 * WARPS, FWD_CTAS)
 k_distill_fwd(const T* z, int64_t z_ld, const __grid_constant__ FwdArgs a, int rows)
 {
     __shared__ RowShared sh;
@@ -448,69 +448,63 @@ struct BwdArgs {
     int64_t g_stride;
 };
 
-constexpr int BWD_CTAS = 6;
+constexpr int BWD_CTAS = 5;
 constexpr int BPER = 16;           // logits per lane and piece of the backward
 constexpr int BBLK = 32 * BPER;
 
-// A piece of a row as loaded.  The order of the elements does not matter in the
-// backward.  SHIFT, where z and dz start equally far past a 128-byte line (or a
-// 4-element group): a row's pieces are cut there, and all but the row's ends move
-// four elements at a time and whole lines by the warp, whatever the vocabulary's
-// remainder: slot i of a lane is element 128 (i / 4) + 4 lane + i mod 4.  Otherwise element 32 i + lane.  Elements outside
-// [0, V) are -infinity.
-template <typename T, bool SHIFT> __device__ __forceinline__ void load_piece(const T* p, int lo, int V, int lane, float (&x)[BPER])
+// A piece of a row.  The order of the elements does not matter in the backward.  LINES,
+// where z and dz start equally far past a 128-byte line: a row's pieces are cut at
+// lines, and all but the row's ends move 16 bytes a lane and whole lines by the warp,
+// whatever the vocabulary's remainder: with W = 16 / sizeof(T), slot i of a lane is
+// element 32 W (i / W) + W lane + i mod W.  Otherwise element 32 i + lane.  Elements
+// outside [0, V) are -infinity.
+template <typename T, bool LINES> __device__ __forceinline__ int piece_element(int i, int lane)
 {
+    constexpr int W = 16 / sizeof(T);
+    return LINES ? 32 * W * (i / W) + W * lane + i % W : 32 * i + lane;
+}
+
+template <typename T, bool LINES>
+__device__ __forceinline__ void load_piece(const T* p, int lo, int V, int lane, float (&x)[BPER])
+{
+    constexpr int W = 16 / sizeof(T);
+    if (LINES && lo >= 0 && lo + BBLK <= V) {
+        const T* q = p + lo + W * lane;
 #pragma unroll
-    for (int i = 0; i < BPER; i += 4) {
-        if (SHIFT) {
-            const int e = lo + 32 * i + 4 * lane;
-            if (e >= 0 && e + 4 <= V) {
-                const float4 v = load4(p + e);
-                x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-            } else {
+        for (int i = 0; i < BPER; i += W)
+            load16(q + 32 * i, x + i);
+        return;
+    }
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    x[i + c] = e + c >= 0 && e + c < V ? to_f32<T>(p[e + c]) : -CUDART_INF_F;
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int e = lo + 32 * (i + c) + lane;
-                x[i + c] = e < V ? to_f32<T>(p[e]) : -CUDART_INF_F;
-            }
-        }
+    for (int i = 0; i < BPER; ++i) {
+        const int e = lo + piece_element<T, LINES>(i, lane);
+        x[i] = e >= 0 && e < V ? to_f32<T>(p[e]) : -CUDART_INF_F;
     }
 }
 
-template <typename T, bool SHIFT> __device__ __forceinline__ void store_piece(T* p, int lo, int V, int lane, const float (&x)[BPER])
+template <typename T, bool LINES>
+__device__ __forceinline__ void store_piece(T* p, int lo, int V, int lane, const float (&x)[BPER])
 {
+    constexpr int W = 16 / sizeof(T);
+    if (LINES && lo >= 0 && lo + BBLK <= V) {
+        T* q = p + lo + W * lane;
 #pragma unroll
-    for (int i = 0; i < BPER; i += 4) {
-        if (SHIFT) {
-            const int e = lo + 32 * i + 4 * lane;
-            if (e >= 0 && e + 4 <= V) {
-                store4(p + e, make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
-            } else {
+        for (int i = 0; i < BPER; i += W)
+            store16(q + 32 * i, x + i);
+        return;
+    }
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (e + c >= 0 && e + c < V)
-                        p[e + c] = from_f32<T>(x[i + c]);
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int e = lo + 32 * (i + c) + lane;
-                if (e < V)
-                    p[e] = from_f32<T>(x[i + c]);
-            }
-        }
+    for (int i = 0; i < BPER; ++i) {
+        const int e = lo + piece_element<T, LINES>(i, lane);
+        if (e >= 0 && e < V)
+            p[e] = from_f32<T>(x[i]);
     }
 }
 
 // One warp takes `per` consecutive pieces of a row, so that what belongs to the row
 // (statistics, coefficients and their divisions) is done once.  Pieces of 16 logits a
 // lane leave registers for 40 warps per SM, which is what covers the loads.
-template <typename T, int SUMS, bool SHIFT>
+template <typename T, int SUMS, bool LINES>
 __global__ void __launch_bounds__(32 * WARPS, BWD_CTAS)
 k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_constant__ BwdArgs a)
 {
@@ -521,9 +515,9 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
     const int row = item / a.groups, first = (item - row * a.groups) * a.per;
     const T* zr = z + row * z_ld;
     T* dr = dz + row * dz_ld;
-    const int shift = SHIFT ? (int)((reinterpret_cast<uintptr_t>(zr) / sizeof(T)) & a.mask) : 0;
+    const int shift = LINES ? (int)((reinterpret_cast<uintptr_t>(zr) / sizeof(T)) & a.mask) : 0;
     float x[BPER];
-    load_piece<T, SHIFT>(zr, first * BBLK - shift, a.V, lane, x);   // on its way while the row's numbers come
+    load_piece<T, LINES>(zr, first * BBLK - shift, a.V, lane, x);   // on its way while the row's numbers come
     const float* st = a.stats + (int64_t)row * (STATS + a.K);
     const float M = st[0], l = st[1], l1 = st[3], lse1 = st[4], P = st[7];
     const float g = flush(a.g[row * a.g_stride]);
@@ -546,16 +540,25 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
                                             fmul_rn(fmul_flush(2.0f, a.w_z), a.w_z != 0.0f ? lse1 : 0.0f)));
     const float qa = flush(__fdiv_rn(SUMS == ONE ? fadd_ftz(ca, cb) : ca, l));
     const float qb = SUMS >= BOTH ? flush(__fdiv_rn(cb, l1)) : 0.0f;
-    const bool none = M == -CUDART_INF_F;
     const float Mu = fmul_flush(M, a.it);
     const u64 zero = dup2(-0.0f), nu = dup2(-Mu), nm = dup2(-M), sc = dup2(a.it), wa = dup2(qa), wb = dup2(qb);
     const int last = min(first + a.per, a.nblk);
+    if (M == -CUDART_INF_F) {   // nothing in the row: no gradient
+#pragma unroll
+        for (int i = 0; i < BPER; ++i)
+            x[i] = 0.0f;
+        for (int blk = first; blk < last; ++blk)
+            store_piece<T, LINES>(dr, blk * BBLK - shift, a.V, lane, x);
+        return;
+    }
+    const bool kd = a.w_kd != 0.0f;
+    const float cl = lab >= 0 ? fmul_flush(g, a.w_ce) : 0.0f;
     for (int blk = first; blk < last; ++blk) {
         const int lo = blk * BBLK - shift;
         if (lo >= a.V)
             break;
         if (blk > first)
-            load_piece<T, SHIFT>(zr, lo, a.V, lane, x);
+            load_piece<T, LINES>(zr, lo, a.V, lane, x);
 #pragma unroll
         for (int i = 0; i < BPER; i += 2) {
             const u64 v = pack2(x[i], x[i + 1]);
@@ -568,18 +571,21 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
             unpack2(d, x[i], x[i + 1]);
         }
         // the teacher's entries and the label inside this piece, entry by entry
-        auto take = [&](int e, float c) {
-            const int slot = SHIFT ? (e >> 7) * 4 + (e & 3) : e >> 5;
-            const int own = SHIFT ? (e >> 2) & 31 : e & 31;
+        const int lo0 = max(lo, 0), end = lo + BBLK;
+        const bool in0 = col0 >= lo0 && col0 < end, in1 = col1 >= lo0 && col1 < end, inl = lab >= lo0 && lab < end;
+        if (__any_sync(0xffffffffu, in0 || in1 || inl || (kd && a.K > 64))) {
+            auto take = [&](int e, float c) {
+                constexpr int W = 16 / sizeof(T);
+                const int slot = LINES ? e / (32 * W) * W + e % W : e >> 5;
+                const int own = LINES ? e / W & 31 : e & 31;
 #pragma unroll
-            for (int i = 0; i < BPER; ++i)
-                if (i == slot && lane == own)
-                    x[i] = fadd_ftz(x[i], -c);
-        };
-        if (a.w_kd != 0.0f)
-            for (int k0 = 0; k0 < a.K; k0 += 32) {
+                for (int i = 0; i < BPER; ++i)
+                    if (i == slot && lane == own)
+                        x[i] = fadd_ftz(x[i], -c);
+            };
+            for (int k0 = 0; kd && k0 < a.K; k0 += 32) {
                 const int j = k0 == 0 ? col0 : k0 == 32 ? col1 : column(k0 + lane);
-                const bool here = j >= max(lo, 0) && j < lo + BBLK;
+                const bool here = j >= lo0 && j < end;
                 unsigned hits = __ballot_sync(0xffffffffu, here);
                 if (hits == 0)
                     continue;
@@ -590,14 +596,10 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
                     take(__shfl_sync(0xffffffffu, j - lo, src), __shfl_sync(0xffffffffu, c, src));
                 }
             }
-        if (lab >= max(lo, 0) && lab < lo + BBLK)
-            take(lab - lo, fmul_flush(g, a.w_ce));
-        if (none) {
-#pragma unroll
-            for (int i = 0; i < BPER; ++i)
-                x[i] = 0.0f;
+            if (inl)
+                take(lab - lo, cl);
         }
-        store_piece<T, SHIFT>(dr, lo, a.V, lane, x);
+        store_piece<T, LINES>(dr, lo, a.V, lane, x);
     }
 }
 
@@ -697,14 +699,11 @@ template <typename T> cudaError_t bwd_typed(const DistillArgs& a, cudaStream_t s
     b.stats = a.stats;
     b.g = a.g;
     b.g_stride = a.g_stride;
-    // pieces begin on 128 bytes, or else on 4 elements, where z and dz agree on that
-    auto agree = [&](int64_t m) {
-        return (reinterpret_cast<uintptr_t>(a.z) - reinterpret_cast<uintptr_t>(a.dz)) / sizeof(T) % m == 0 &&
-               (a.z_ld - a.dz_ld) % m == 0;
-    };
+    // pieces begin on 128-byte lines where z and dz agree on them
     const int64_t line = 128 / sizeof(T);
-    const bool shift = agree(4);
-    b.mask = shift ? (int)(agree(line) ? line : 4) - 1 : 0;
+    const bool lines = (reinterpret_cast<uintptr_t>(a.z) - reinterpret_cast<uintptr_t>(a.dz)) % 128 == 0 &&
+                       (a.z_ld - a.dz_ld) % line == 0;
+    b.mask = lines ? (int)line - 1 : 0;
     b.nblk = (int)((a.V + b.mask + BBLK - 1) / BBLK);
     // eight pieces a warp once that leaves every scheduler several warps
     b.per = a.n * b.nblk >= (int64_t)num_sms() * 256 ? 8 : 1;
@@ -713,7 +712,7 @@ template <typename T> cudaError_t bwd_typed(const DistillArgs& a, cudaStream_t s
     return by_sums(sums_of(a), [&](auto s) {
         constexpr int SUMS = decltype(s)::value;
         const unsigned grid = (unsigned)((b.items + WARPS - 1) / WARPS);
-        if (shift)
+        if (lines)
             k_distill_bwd<T, SUMS, true><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, dz, a.dz_ld, b);
         else
             k_distill_bwd<T, SUMS, false><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, dz, a.dz_ld, b);
