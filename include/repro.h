@@ -441,9 +441,9 @@ size_t repro_qk_norm_rope_bwd_ws_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64
  * top logits: t_idx [n][K] (index_bytes; negative: an empty entry) and t_val
  * [n][K] (fp32 or bf16), with the label's cross entropy and the log-partition
  * penalty from the same pass.  it = 1 (/) tau, u_j = z_j (x) it:
- *   e(x) = 2^t for x <= 0, t = x (x) RN(1 / ln 2): k = rint(t), f = t (-) k, the
- *     degree-6 polynomial of 2^f (coefficients in k_distill.cu) in Horner form,
- *     times 2^k; 0 where k < -125;
+ *   e(x) = 2^t for x <= 0, t = x (x) RN(1 / ln 2): k = rint(32 t), f = t (-) k / 32, the
+ *     degree-2 polynomial of 2^f (coefficients in k_distill.cu) in Horner form,
+ *     times RN(2^((k mod 32) / 32)) 2^floor(k / 32); 0 where floor(k / 32) < -125;
  *   blocks of REPRO_DISTILL_BLOCK consecutive logits: the block's maximum M_b
  *     (a zero maximum is +0, a NaN stays) and S_b = sum of e(u_j (-) M_b (x) it) in
  *     128 chains (element j of the block in chain j mod 128, ascending from

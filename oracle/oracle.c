@@ -976,23 +976,26 @@ void oracle_qk_bwd(const float* dout, const float* x, const float* rope, const i
 #define DISTILL_CHAINS 128
 #define DISTILL_STATS 8
 
-/* 2^t for t <= 0: t = k + f, k = rint(t), and the degree-6 minimax polynomial
- * of 2^f on [-1/2, 1/2] (relative error 2.6e-9, constant term 1; coefficients
- * by the exchange algorithm of Remez, rounded to binary32); 0 where k < -125 */
+/* 2^t for t <= 0: t = k / 32 + f, k = rint(32 t); the degree-2 minimax polynomial
+ * of 2^f on [-1/64, 1/64] (relative error 5.4e-8, constant term 1; coefficients by
+ * the exchange algorithm of Remez, rounded to binary32) times RN(2^((k mod 32) / 32))
+ * 2^floor(k / 32); 0 where floor(k / 32) < -125 */
 float oracle_exp2_neg(float t)
 {
-    static const float c[7] = {1.0f, 0x1.62e432p-1f, 0x1.ebfbe2p-3f, 0x1.c6ae72p-5f, 0x1.3b270ep-7f,
-                               0x1.5f7278p-10f, 0x1.470b5p-13f};
+    static const float c[3] = {1.0f, 0x1.62e586p-1f, 0x1.ebfeacp-3f};
     if (t != t)
         return t;
-    const float k = nearbyintf(t);
-    if (k < -125.0f)
+    if (t < -126.0f)
         return 0.0f;
-    const float f = oracle_add(t, -k);
-    float p = c[6];
-    for (int i = 5; i >= 0; --i)
+    const float k32 = nearbyintf(oracle_mul(32.0f, t));
+    const int k = (int)floorf(k32 / 32.0f), j = (int)k32 - 32 * k;
+    if (k < -125)
+        return 0.0f;
+    const float f = oracle_add(t, -(k32 / 32.0f));
+    float p = c[2];
+    for (int i = 1; i >= 0; --i)
         p = oracle_add(oracle_mul(p, f), c[i]);
-    return oracle_mul(p, ldexpf(1.0f, (int)k));
+    return oracle_mul(p, ldexpf((float)exp2((double)j / 32.0), k));
 }
 
 /* e^x for x <= 0 */
