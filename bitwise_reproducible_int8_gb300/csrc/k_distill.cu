@@ -277,6 +277,12 @@ __device__ __forceinline__ void block_stats(const T* p, int len, int lane, unsig
         s1 = chains_tree<VEC>(a1, b1);
 }
 
+// a row's teacher: maximum, sum, P, ln of the sum, the sums of p_k (a_k - u_k) and of p_k
+struct Teacher {
+    double ln_lt, sum, weight;
+    float mt, lt, P, unused;
+};
+
 struct FwdArgs {
     const void* t_idx;
     const void* t_val;
@@ -288,6 +294,7 @@ struct FwdArgs {
     bool logprobs;
     float2* ms;      // [n][nblk] block maxima and sums
     float* s1;       // [n][nblk]
+    Teacher* teachers;   // [n], where a CTA does not own its rows
     float* loss;
     float* stats;
     int* err;
@@ -313,8 +320,10 @@ constexpr int FWD_CTAS = 5;
 constexpr int MAX_ROWS = 8;   // rows a CTA joins at a time
 
 struct RowShared {
-    float M[MAX_ROWS], l[MAX_ROWS], l1[MAX_ROWS], mt[MAX_ROWS], lt[MAX_ROWS], P[MAX_ROWS];
-    double ln[3][MAX_ROWS];
+    Teacher t[MAX_ROWS];
+    float M[MAX_ROWS], l[MAX_ROWS], l1[MAX_ROWS];
+    double ln[2][MAX_ROWS];
+    int next;   // block handed out
 };
 
 // a_k of an entry, and its column (-1: empty)
@@ -331,12 +340,64 @@ __device__ __forceinline__ float teacher(const FwdArgs& a, int64_t at, int& j)
     return a.logprobs ? t : fmul_flush(t, a.it);
 }
 
-// joins the blocks of rows [r0, r0 + cnt), forms the teacher's weights and the
-// losses.  A warp per row, but the logarithms: binary64 runs at 1/64 of the
-// binary32 rate here whether one lane needs it or 32, so one warp takes all of the
-// CTA's logarithms, a lane each.
+// What a row's loss needs of the teacher, by one warp: the weights p_k, and in binary64
+// the sums of p_k (a_k - u_k) and of p_k.  None of it waits for the row's blocks:
+//   sum p_k (ln p_k - ln q_k) = sum p_k (a_k - u_k) + (lse(u) - (m + ln lt)) sum p_k.
+template <typename T>
+__device__ void teacher_row(const T* zr, const FwdArgs& a, int64_t row, Teacher* out)
+{
+    const int lane = threadIdx.x & 31;
+    float* p = a.stats + row * (STATS + a.K) + STATS;
+    float mt = a.logprobs ? 0.0f : -CUDART_INF_F, lt = 0.0f, P = 0.0f;
+    double sum = 0.0, weight = 0.0, ln_lt = 0.0;
+    int j;
+    if (!a.logprobs) {
+        for (int k = lane; k < a.K; k += 32)
+            mt = max_nan(mt, teacher(a, row * a.K + k, j));
+        mt = warp_max(mt);
+        mt = mt == 0.0f ? 0.0f : mt;
+    }
+    if (mt == -CUDART_INF_F) {
+        for (int k = lane; k < a.K; k += 32)
+            p[k] = 0.0f;
+    } else {
+        for (int k = lane; k < a.K; k += 32) {
+            const float e = exp_neg(fadd_ftz(teacher(a, row * a.K + k, j), -mt));
+            lt = fadd_ftz(lt, e);
+            p[k] = e;
+        }
+        lt = warp_tree(lt);
+        P = a.logprobs ? lt : lt == lt ? 1.0f : lt;
+        lt = a.logprobs ? 1.0f : lt;
+        for (int k = lane; k < a.K; k += 32) {
+            float w = p[k];
+            if (!a.logprobs) {
+                w = flush(__fdiv_rn(w, lt));
+                p[k] = w;
+            }
+            if (w != 0.0f && a.w_kd != 0.0f) {
+                const float ak = teacher(a, row * a.K + k, j);
+                const float u = fmul_flush(flush(to_f32<T>(zr[j])), a.it);
+                sum = sum + (double)w * ((double)ak - (double)u);
+                weight = weight + (double)w;
+            }
+        }
+        if (a.w_kd != 0.0f) {
+            sum = warp_tree(sum);
+            weight = warp_tree(weight);
+            ln_lt = ln_d(lt);
+        }
+    }
+    if (lane == 0)
+        *out = {ln_lt, sum, weight, mt, lt, P, 0.0f};
+}
+
+// joins the blocks of rows [r0, r0 + cnt) and forms the losses.  A warp per row, but the
+// logarithms: binary64 runs at 1/64 of the binary32 rate here whether one lane needs
+// it or 32, so one warp takes all of the CTA's, a lane each.
 template <typename T, int SUMS>
-__device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, int cnt, RowShared& sh)
+__device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, int cnt, const Teacher* teachers,
+                            RowShared& sh)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int r = warp; r < cnt; r += WARPS) {
@@ -359,117 +420,99 @@ __device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, 
             l = warp_tree(l);
             l1 = SUMS >= BOTH ? warp_tree(l1) : SUMS == ONE ? l : 0.0f;
         }
-        float* p = a.stats + row * (STATS + a.K) + STATS;
-        float mt = a.logprobs ? 0.0f : -CUDART_INF_F, lt = 0.0f, P = 0.0f;
-        int j;
-        if (!a.logprobs) {
-            for (int k = lane; k < a.K; k += 32)
-                mt = max_nan(mt, teacher(a, row * a.K + k, j));
-            mt = warp_max(mt);
-            mt = mt == 0.0f ? 0.0f : mt;
-        }
-        if (mt == -CUDART_INF_F) {
-            for (int k = lane; k < a.K; k += 32)
-                p[k] = 0.0f;
-        } else {
-            for (int k = lane; k < a.K; k += 32) {
-                const float e = exp_neg(fadd_ftz(teacher(a, row * a.K + k, j), -mt));
-                lt = fadd_ftz(lt, e);
-                p[k] = e;
-            }
-            lt = warp_tree(lt);
-            P = a.logprobs ? lt : lt == lt ? 1.0f : lt;
-            lt = a.logprobs ? 1.0f : lt;
-        }
         if (lane == 0) {
             sh.M[r] = M;
             sh.l[r] = l;
             sh.l1[r] = l1;
-            sh.mt[r] = mt;
-            sh.lt[r] = lt;
-            sh.P[r] = P;
         }
     }
     __syncthreads();
-    if (threadIdx.x < 3 * MAX_ROWS) {
-        const int which = threadIdx.x / MAX_ROWS, r = threadIdx.x % MAX_ROWS;
+    if (threadIdx.x >= 32)
+        return;
+    if (lane < 2 * MAX_ROWS) {
+        const int which = lane / MAX_ROWS, r = lane % MAX_ROWS;
         if (r < cnt)
-            sh.ln[which][r] = ln_d(which == 0 ? sh.l[r] : which == 1 ? sh.lt[r] : sh.l1[r]);
+            sh.ln[which][r] = ln_d(which == 0 ? sh.l[r] : sh.l1[r]);
     }
-    __syncthreads();
-    for (int r = warp; r < cnt; r += WARPS) {
-        const int64_t row = r0 + r;
-        const float M = sh.M[r], mt = sh.mt[r], lt = sh.lt[r];
-        const bool none = M == -CUDART_INF_F;
-        const double lse_t = none ? 0.0 : (double)fmul_flush(M, a.it) + sh.ln[0][r];
-        const double lse1 = none || SUMS == SOFT ? 0.0 : (double)M + sh.ln[2][r];
-        float* st = a.stats + row * (STATS + a.K);
-        float* p = st + STATS;
-        double v = 0.0;
-        if (mt != -CUDART_INF_F) {
-            const double cst = none ? 0.0 : lse_t - ((double)mt + sh.ln[1][r]);
-            double sum = 0.0;
-            for (int k = lane; k < a.K; k += 32) {
-                float w = p[k];
-                if (!a.logprobs) {
-                    w = flush(__fdiv_rn(w, lt));
-                    p[k] = w;
-                }
-                if (w != 0.0f && !none && a.w_kd != 0.0f) {
-                    int j;
-                    const float ak = teacher(a, row * a.K + k, j);
-                    const float u = fmul_flush(flush(to_f32<T>(z[row * z_ld + j])), a.it);
-                    sum = sum + (double)w * (((double)ak - (double)u) + cst);
-                }
-            }
-            if (!none && a.w_kd != 0.0f)
-                v = ((double)a.w_kd * ((double)a.tau * (double)a.tau)) * warp_tree(sum);
-        }
-        if (lane == 0) {
-            if (a.w_ce != 0.0f) {
-                const int64_t lab = load_index(a.labels, a.index_bytes, row);
-                if (lab >= a.V)
-                    atomicOr(a.err, kErrIndexBit);
-                else if (lab >= 0 && !none)
-                    v = v + (double)a.w_ce * (lse1 - (double)flush(to_f32<T>(z[row * z_ld + lab])));
-            }
-            if (a.w_z != 0.0f && !none)
-                v = v + (double)a.w_z * (lse1 * lse1);
-            a.loss[row] = flush(__double2float_rn(v));
-            st[0] = M;
-            st[1] = sh.l[r];
-            st[2] = none ? M : flush(__double2float_rn(lse_t));
-            st[3] = sh.l1[r];
-            st[4] = SUMS == SOFT ? 0.0f : none ? M : flush(__double2float_rn(lse1));
-            st[5] = mt;
-            st[6] = lt;
-            st[7] = sh.P[r];
-        }
+    __syncwarp();
+    if (lane >= cnt)
+        return;
+    const int r = lane;
+    const int64_t row = r0 + r;
+    const T* zr = z + row * z_ld;
+    const float M = sh.M[r];
+    const Teacher t = teachers[r];
+    const bool none = M == -CUDART_INF_F;
+    const double lse_t = none ? 0.0 : (double)fmul_flush(M, a.it) + sh.ln[0][r];
+    const double lse1 = none || SUMS == SOFT ? 0.0 : (double)M + sh.ln[1][r];
+    double v = 0.0;
+    if (!none && a.w_kd != 0.0f && t.mt != -CUDART_INF_F)
+        v = ((double)a.w_kd * ((double)a.tau * (double)a.tau)) *
+            (t.sum + (lse_t - ((double)t.mt + t.ln_lt)) * t.weight);
+    if (a.w_ce != 0.0f) {
+        const int64_t lab = load_index(a.labels, a.index_bytes, row);
+        if (lab >= a.V)
+            atomicOr(a.err, kErrIndexBit);
+        else if (lab >= 0 && !none)
+            v = v + (double)a.w_ce * (lse1 - (double)flush(to_f32<T>(zr[lab])));
     }
+    if (a.w_z != 0.0f && !none)
+        v = v + (double)a.w_z * (lse1 * lse1);
+    float* st = a.stats + row * (STATS + a.K);
+    a.loss[row] = flush(__double2float_rn(v));
+    st[0] = M;
+    st[1] = sh.l[r];
+    st[2] = none ? M : flush(__double2float_rn(lse_t));
+    st[3] = sh.l1[r];
+    st[4] = SUMS == SOFT ? 0.0f : none ? M : flush(__double2float_rn(lse1));
+    st[5] = t.mt;
+    st[6] = t.lt;
+    st[7] = t.P;
 }
 
-// a CTA owns `rows` rows: their blocks, then their losses
+// a CTA owns `rows` rows: the teacher's part by a warp each, the rows' blocks by all
+// warps as they come free, then the losses
 template <typename T, int SUMS, bool VEC>
 __global__ void __launch_bounds__(32 * WARPS, FWD_CTAS)
 k_distill_fwd(const T* z, int64_t z_ld, const __grid_constant__ FwdArgs a, int rows)
 {
     __shared__ RowShared sh;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned pow = lane_pow();
     const int r0 = blockIdx.x * rows, cnt = min(rows, a.n - r0), items = cnt * a.nblk;
-    for (int i = threadIdx.x >> 5; i < items; i += WARPS) {
+    if (threadIdx.x == 0)
+        sh.next = 0;
+    __syncthreads();
+    if (warp < cnt)
+        teacher_row(z + (int64_t)(r0 + warp) * z_ld, a, r0 + warp, &sh.t[warp]);
+    for (;;) {
+        int i = 0;
+        if (lane == 0)
+            i = atomicAdd(&sh.next, 1);
+        i = __shfl_sync(0xffffffffu, i, 0);
+        if (i >= items)
+            break;
         const int r = i / a.nblk;
         do_block<T, SUMS, VEC>(z, z_ld, a, r0 + r, i - r * a.nblk, lane, pow);
     }
     __syncthreads();
-    finish_rows<T, SUMS>(z, z_ld, a, r0, cnt, sh);
+    finish_rows<T, SUMS>(z, z_ld, a, r0, cnt, sh.t, sh);
 }
 
+// the same work spread over the card: the first `tctas` CTAs take the teacher's part of a
+// row per warp, the others a block per warp; k_distill_rows joins them
 template <typename T, int SUMS, bool VEC>
 __global__ void __launch_bounds__(32 * WARPS)
-k_distill_blocks(const T* z, int64_t z_ld, const __grid_constant__ FwdArgs a)
+k_distill_blocks(const T* z, int64_t z_ld, const __grid_constant__ FwdArgs a, int tctas)
 {
-    const int item = blockIdx.x * WARPS + (threadIdx.x >> 5);
+    const int warp = threadIdx.x >> 5;
+    if (blockIdx.x < tctas) {
+        const int row = blockIdx.x * WARPS + warp;
+        if (row < a.n)
+            teacher_row(z + (int64_t)row * z_ld, a, row, a.teachers + row);
+        return;
+    }
+    const int item = (blockIdx.x - tctas) * WARPS + warp;
     if (item >= a.n * a.nblk)
         return;
     const int row = item / a.nblk;
@@ -483,7 +526,7 @@ k_distill_rows(const T* z, int64_t z_ld, const __grid_constant__ FwdArgs a)
     __shared__ RowShared sh;
     pdl_wait();
     const int r0 = blockIdx.x * MAX_ROWS;
-    finish_rows<T, SUMS>(z, z_ld, a, r0, min(MAX_ROWS, a.n - r0), sh);
+    finish_rows<T, SUMS>(z, z_ld, a, r0, min(MAX_ROWS, a.n - r0), a.teachers + r0, sh);
 }
 
 struct BwdArgs {
@@ -697,7 +740,8 @@ template <typename T> cudaError_t fwd_typed(const DistillArgs& a, void* ws, cuda
     r.w_ce = a.w_ce;
     r.w_z = a.w_z;
     r.logprobs = a.logprobs;
-    r.ms = static_cast<float2*>(ws);
+    r.teachers = static_cast<Teacher*>(ws);
+    r.ms = reinterpret_cast<float2*>(r.teachers + a.n);
     r.s1 = reinterpret_cast<float*>(r.ms + items);
     r.loss = a.loss;
     r.stats = a.stats;
@@ -716,11 +760,12 @@ template <typename T> cudaError_t fwd_typed(const DistillArgs& a, void* ws, cuda
             count_launches(1);
             return cudaGetLastError();
         }
-        const unsigned grid = (unsigned)((items + WARPS - 1) / WARPS);
+        const int tctas = (int)((a.n + WARPS - 1) / WARPS);
+        const unsigned grid = (unsigned)((items + WARPS - 1) / WARPS) + tctas;
         if (vec)
-            k_distill_blocks<T, SUMS, true><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, r);
+            k_distill_blocks<T, SUMS, true><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, r, tctas);
         else
-            k_distill_blocks<T, SUMS, false><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, r);
+            k_distill_blocks<T, SUMS, false><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, r, tctas);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess)
             return e;
@@ -773,7 +818,7 @@ template <typename T> cudaError_t bwd_typed(const DistillArgs& a, cudaStream_t s
 
 } // namespace
 
-size_t distill_ws_bytes(int64_t n, int64_t V) { return (size_t)(n * blocks_of(V)) * 12; }
+size_t distill_ws_bytes(int64_t n, int64_t V) { return (size_t)(n * blocks_of(V)) * 12 + (size_t)n * sizeof(Teacher); }
 
 cudaError_t launch_distill_fwd(const DistillArgs& a, void* ws, cudaStream_t st)
 {

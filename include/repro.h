@@ -457,8 +457,9 @@ size_t repro_qk_norm_rope_bwd_ws_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64
  *     log-probabilities: a_k = t_k, p_k = e(a_k), P their sum in that order.  No
  *     entry (or only -infinities): every p_k and P are 0.
  *   loss = w_kd tau^2 sum_k p_k (ln p_k - ln softmax(u)_k) + w_ce (lse(z) - z_label)
- *     + w_z lse(z)^2, its row terms in binary64, unfused, rounded once; ln of a
- *     sum by its atanh series, the terms over k in 32 chains and the tree.
+ *     + w_z lse(z)^2, its row terms in binary64, unfused, rounded once: the sum over k
+ *     as sum p_k (a_k - u_k) + (lse(u) - (m + ln lt)) sum p_k, both in 32 chains and the
+ *     tree, ln of a sum by its atanh series.
  * p_k = 0 adds nothing.  A negative label adds no cross entropy.  An index or a
  * label >= V is passed over and sets the error word.  A row with no logit above
  * -infinity has loss 0 and gradient 0.  A NaN among a row's logits makes its

@@ -1154,9 +1154,11 @@ void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx
                 const double cst = lse_t - ((double)mt + oracle_ln(lt));
                 for (int64_t k = 0; k < K; ++k)
                     term[k] = p[k] == 0.0f ? 0.0
-                                           : (double)p[k] * (((double)a[k] -
-                                                              (double)oracle_mul(zr[idx[r * K + k]], it)) + cst);
-                v = ((double)w_kd * ((double)tau * (double)tau)) * chains_sum_d(term, K, 32);
+                                           : (double)p[k] * ((double)a[k] - (double)oracle_mul(zr[idx[r * K + k]], it));
+                const double sum = chains_sum_d(term, K, 32);
+                for (int64_t k = 0; k < K; ++k)
+                    term[k] = (double)p[k];
+                v = ((double)w_kd * ((double)tau * (double)tau)) * (sum + cst * chains_sum_d(term, K, 32));
             }
             if (w_ce != 0.0f && label[r] >= 0 && label[r] < V)
                 v = v + (double)w_ce * (lse1 - (double)oracle_flush(zr[label[r]]));
