@@ -158,14 +158,15 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st);
 
 // ---- pairwise tree over partial rows (k_rowtree.cu), shared by the table's and the gains' gradients
 struct RowTree {
-    float* parts;        // partial rows, `pitch` floats apart (used as scratch)
+    float* parts[2];     // partial rows, `pitch` floats apart (used as scratch)
     int64_t pitch;
-    const int4* joins;   // {first sorted index, chunks, output row, 0}, or NULL: one join over
-                         // `count` consecutive partial rows
+    const int4* joins;   // {first sorted index, chunks, output row, 0}, or NULL: `jobs` joins, job i
+                         // over the count[i] consecutive partial rows of parts[i], into out[i]
     const int* njoins;   // device count of joins
-    int64_t count;
+    int jobs;
+    int64_t count[2];
     int64_t D;
-    float* out;
+    float* out[2];
     int64_t out_ld;
     float scale;         // applied to the sum (1: leaves it)
     bool accumulate;     // out (+) the scaled sum

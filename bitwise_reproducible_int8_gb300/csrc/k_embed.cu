@@ -326,6 +326,7 @@ __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_NT, 1)
 k_embed_sort(const SortArgs a)
 {
     extern __shared__ __align__(128) unsigned dyn[];
+    pdl_trigger();   // the sums may be launched; they wait for this grid
     if (blockIdx.x < SORT_CTAS) {
         sort_cluster(a, *reinterpret_cast<SortSmem*>(dyn));
     } else {
@@ -425,6 +426,7 @@ k_embed_sum(const TD* __restrict__ dout, int64_t dout_ld, const int4* __restrict
             float* __restrict__ parts, int pieces, bool vec_out)
 {
     pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x & 31;
     const float sc = flush(scale);
     const int64_t pitch = (D + 3) & ~3LL;
@@ -649,13 +651,13 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
     count_launches(1);
     if (e != cudaSuccess || a.n <= 64)
         return e;
-    RowTree t;
-    t.parts = parts;
+    RowTree t = {};
+    t.parts[0] = parts;
     t.pitch = (a.D + 3) & ~3LL;
     t.joins = s.joins;
     t.njoins = s.counts;
     t.D = a.D;
-    t.out = a.table;
+    t.out[0] = a.table;
     t.out_ld = a.table_ld;
     t.scale = a.scale;
     t.accumulate = a.accumulate;

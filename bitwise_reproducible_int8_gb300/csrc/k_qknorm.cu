@@ -472,6 +472,7 @@ k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict_
     const unsigned H = (unsigned)t.H, total = (unsigned)a.n * H, first = chunk * CHUNK;
     const float width = (float)D, eps = flush(a.eps);
     const bool gain = t.gain != nullptr;
+    pdl_trigger();   // the gains' tree may be launched; it waits for this grid
     u64 g[E / 2];
     load_gain<E, MODE>(t.gain, l, D, g);
 #pragma unroll 1
@@ -675,26 +676,23 @@ cudaError_t launch_qk_bwd(const QkArgs& a, void* ws, cudaStream_t st)
     const int64_t pitch = (a.D + 3) & ~3LL;
     float* parts = static_cast<float*>(ws);
     cudaError_t e = a.type == 0 ? bwd_typed<float>(a, parts, pitch, st) : bwd_typed<__nv_bfloat16>(a, parts, pitch, st);
-    for (int x = 0; x < 2 && e == cudaSuccess; ++x) {
+    RowTree r = {};
+    for (int x = 0; x < 2; ++x) {
         const QkTensor& t = a.t[x];
         if (!t.gain || t.H == 0)
             continue;
-        RowTree r;
-        r.parts = parts;
-        r.pitch = pitch;
-        r.joins = nullptr;
-        r.njoins = nullptr;
-        r.count = chunks_of(a.n * t.H);
-        r.D = a.D;
-        r.out = t.dgain;
-        r.out_ld = a.D;
-        r.scale = 1.0f;
-        r.accumulate = a.accumulate;
-        if (x == 1)
-            r.parts += (int64_t)chunks_of(a.n * a.t[0].H) * pitch;
-        e = launch_row_tree(r, num_sms(), st);
+        r.parts[r.jobs] = parts + (x == 1 ? (int64_t)chunks_of(a.n * a.t[0].H) * pitch : 0);
+        r.count[r.jobs] = chunks_of(a.n * t.H);
+        r.out[r.jobs++] = t.dgain;
     }
-    return e;
+    if (e != cudaSuccess || r.jobs == 0)
+        return e;
+    r.pitch = pitch;
+    r.D = a.D;
+    r.out_ld = a.D;
+    r.scale = 1.0f;
+    r.accumulate = a.accumulate;
+    return launch_row_tree(r, num_sms(), st);
 }
 
 } // namespace repro

@@ -20,22 +20,24 @@ constexpr int FOLD = 16;   // chunks a worker folds at a time
 
 template <int LANES>
 __global__ void __launch_bounds__(256)
-k_row_tree(const RowTree t, int colsegs)
+k_row_tree(const __grid_constant__ RowTree t, int colsegs)
 {
     constexpr int WORKERS = 256 / LANES;
     pdl_wait();
-    const int64_t joins = t.joins ? *t.njoins : 1;
+    const int64_t joins = t.joins ? *t.njoins : t.jobs;
     const int lane = threadIdx.x % LANES, worker = threadIdx.x / LANES;
     const float sc = flush(t.scale);
     for (int64_t item = blockIdx.x; item < joins * colsegs; item += gridDim.x) {
         const int64_t jn = item / colsegs;
         const int64_t c = (item - jn * colsegs) * (4 * LANES) + 4 * lane;
-        const int4 j = t.joins ? t.joins[jn] : make_int4(0, (int)t.count, 0, 0);
+        const int4 j = t.joins ? t.joins[jn] : make_int4(0, (int)t.count[jn != 0], 0, 0);
+        float* parts = t.joins || jn == 0 ? t.parts[0] : t.parts[1];
+        float* out = t.joins || jn == 0 ? t.out[0] : t.out[1];
         const bool live = c < t.D;
         // partial row of chunk k: see the slot rule of the chunk list (k_embed.cu)
         auto row = [&](int64_t k) {
             const int64_t slot = t.joins ? (k == 0 ? 2 * (int64_t)(j.x >> 6) + 1 : 2 * ((j.x + 64 * k) >> 6)) : k;
-            return t.parts + slot * t.pitch + c;
+            return parts + slot * t.pitch + c;
         };
         const int64_t C = j.y;
         for (int64_t s = 1; s < C; s *= FOLD) {
@@ -58,7 +60,7 @@ k_row_tree(const RowTree t, int colsegs)
         if (live && worker == 0) {
             const float4 x = load4(row(0));
             const float v[4] = {x.x, x.y, x.z, x.w};
-            float* o = t.out + (int64_t)j.z * t.out_ld + c;
+            float* o = out + (int64_t)j.z * t.out_ld + c;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (c + e < t.D) {
@@ -88,7 +90,7 @@ cudaError_t launch_row_tree(const RowTree& t, int max_ctas, cudaStream_t st)
 {
     const int cols = t.joins ? 128 : 8;
     const int colsegs = (int)((t.D + cols - 1) / cols);
-    const int grid = t.joins ? max_ctas : (colsegs < max_ctas ? colsegs : max_ctas);
+    const int grid = t.joins ? max_ctas : (colsegs * t.jobs < max_ctas ? colsegs * t.jobs : max_ctas);
     const cudaError_t e = t.joins ? launch_pdl(k_row_tree<32>, dim3((unsigned)grid), dim3(256), 0, st, t, colsegs)
                                   : launch_pdl(k_row_tree<2>, dim3((unsigned)grid), dim3(256), 0, st, t, colsegs);
     count_launches(1);
