@@ -345,13 +345,17 @@ constexpr int ES_U = 8;             // rows in flight
 constexpr int ES_COLS = 32 * 4 * ES_G;
 constexpr int ES_CTAS = 2;          // per SM
 
-// columns of group g of this lane, from c0 on: four neighbours, or lane-strided single
-// elements where rows are unaligned
+// A row's piece in a lane: ES_G groups of four columns.  Group g begins
+// at column c0 + 4 (lane + 32 g); where rows are not on 4-element boundaries its elements
+// are c0 + lane + 32 (4 g + e) instead.
+typedef unsigned long long u64;
+
 template <bool VEC> __device__ __forceinline__ int64_t sum_col(int64_t c0, int lane, int g, int e)
 {
     return c0 + (VEC ? 4 * (lane + 32 * g) + e : lane + 32 * (4 * g + e));
 }
 
+// left as single floats until they are added: packing them here would wait for the load
 template <typename TD, bool VEC>
 __device__ __forceinline__ void sum_load(const TD* s, int64_t c0, int64_t D, int lane, float (&x)[ES_G][4])
 {
@@ -383,32 +387,35 @@ __device__ __forceinline__ void add_once(float* p, float4 v)
 // a finished chunk: a partial row as it is, a token's only chunk scaled into the table
 template <bool VEC>
 __device__ __forceinline__ void sum_store(float* dst, bool part, bool wide, bool accumulate, float sc, int64_t c0,
-                                          int64_t D, int lane, const float (&acc)[ES_G][4])
+                                          int64_t D, int lane, const u64 (&acc)[ES_G][2])
 {
 #pragma unroll
     for (int g = 0; g < ES_G; ++g) {
+        float v[4];
+        unpack2(acc[g][0], v[0], v[1]);
+        unpack2(acc[g][1], v[2], v[3]);
+        if (!part) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = fmul_flush(v[e], sc);
+        }
         const int64_t c = sum_col<VEC>(c0, lane, g, 0);
         if (VEC && wide) {
             if (c >= D)
                 continue;
-            float4 v = make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
-            if (!part) {
-                v = make_float4(fmul_flush(v.x, sc), fmul_flush(v.y, sc), fmul_flush(v.z, sc), fmul_flush(v.w, sc));
-            }
             if (!part && accumulate)
-                add_once(dst + c, v);
+                add_once(dst + c, make_float4(v[0], v[1], v[2], v[3]));
             else
-                store4(dst + c, v);
+                store4(dst + c, make_float4(v[0], v[1], v[2], v[3]));
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int64_t ce = sum_col<VEC>(c0, lane, g, e);
                 if (ce < D) {
-                    const float v = part ? acc[g][e] : fmul_flush(acc[g][e], sc);
                     if (!part && accumulate)
-                        atomicAdd(dst + ce, v);
+                        atomicAdd(dst + ce, v[e]);
                     else
-                        dst[ce] = v;
+                        dst[ce] = v[e];
                 }
             }
         }
@@ -418,7 +425,8 @@ __device__ __forceinline__ void sum_store(float* dst, bool part, bool wide, bool
 // A warp takes the chunks that begin among `span` sorted indexes, for one piece of the
 // columns, as one stream of rows: 8 rows are on their way at any time, across the chunks'
 // ends (most tokens occur once or twice; chunk by chunk every one cost a trip to
-// memory).  `span` leaves one stream to a warp, two where few rows meet many pieces.
+// memory).  `span` leaves one stream to a warp.  What a row needs of the order is its
+// position and one bit; the rest is looked up where a chunk begins.
 template <typename TD, bool VEC>
 __global__ void __launch_bounds__(256, ES_CTAS)
 k_embed_sum(const TD* __restrict__ dout, int64_t dout_ld, const int4* __restrict__ order, int n, int span,
@@ -427,9 +435,11 @@ k_embed_sum(const TD* __restrict__ dout, int64_t dout_ld, const int4* __restrict
 {
     pdl_wait();
     pdl_trigger();
+    constexpr unsigned ALL = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     const float sc = flush(scale);
     const int64_t pitch = (D + 3) & ~3LL;
+    const u64 zero = pack2(-0.0f, -0.0f);
     const int64_t items = (int64_t)((n + span - 1) / span) * pieces;
     for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < items; item += (int64_t)gridDim.x * 8) {
         const int range = (int)(item / pieces);
@@ -438,74 +448,74 @@ k_embed_sum(const TD* __restrict__ dout, int64_t dout_ld, const int4* __restrict
         // the first index of the range at which a chunk begins
         int at = hi;
         for (int i = lo; i < hi && at == hi; i += 32) {
-            const unsigned m = __ballot_sync(0xffffffffu, i + lane < hi && order[i + lane].z >= WHOLE);
+            const unsigned m = __ballot_sync(ALL, i + lane < hi && order[i + lane].z >= WHOLE);
             if (m)
                 at = i + __ffs(m) - 1;
         }
         if (at >= hi)
             continue;
-        // 32 entries of the order at a time, the next 32 fetched ahead; {0, 0, NOTHING} past the end
+        // 32 entries of the order at a time, the next 32 fetched ahead; the stream ends at
+        // `end`: the first chunk past the range, the first index without a token, or n
         const int4 none = make_int4(0, 0, NOTHING, 0);
-        int4 cur = at + lane < n ? order[at + lane] : none;
-        int4 ahead = at + 32 + lane < n ? order[at + 32 + lane] : none;
-        bool beyond = false;   // a chunk that begins past the range belongs to the next one
-        auto entry = [&](int k, int& pos, int& tok, int& what) {   // k < 64 from the window's start
-            pos = __shfl_sync(0xffffffffu, k < 32 ? cur.x : ahead.x, k & 31);
-            tok = __shfl_sync(0xffffffffu, k < 32 ? cur.y : ahead.y, k & 31);
-            what = __shfl_sync(0xffffffffu, k < 32 ? cur.z : ahead.z, k & 31);
-            beyond = beyond || (at + k >= hi && what != MIDDLE);
-            what = beyond ? NOTHING : what;
+        int end = n;
+        auto window = [&](int from, int4& v, unsigned& starts) {
+            v = from + lane < n ? order[from + lane] : none;
+            starts = __ballot_sync(ALL, v.z != MIDDLE);
+            const unsigned stop = __ballot_sync(ALL, v.z == NOTHING || (v.z != MIDDLE && from + lane >= hi));
+            if (stop)
+                end = min(end, from + __ffs(stop) - 1);
         };
-        float x[ES_U][ES_G][4] = {}, acc[ES_G][4] = {};
-        int tok_of[ES_U], what_of[ES_U];
+        int4 cur, ahead;
+        unsigned starts, starts_ahead;
+        window(at, cur, starts);
+        window(at + 32, ahead, starts_ahead);
+        float x[ES_U][ES_G][4] = {};
+        u64 acc[ES_G][2] = {};
+        auto fetch = [&](int k, float (&v)[ES_G][4]) {   // row k < 64 of the window
+            const int pos = __shfl_sync(ALL, k < 32 ? cur.x : ahead.x, k & 31);
+            if (at + k < end)
+                sum_load<TD, VEC>(dout + (int64_t)pos * dout_ld, c0, D, lane, v);
+        };
 #pragma unroll
-        for (int u = 0; u < ES_U; ++u) {
-            int pos;
-            entry(u, pos, tok_of[u], what_of[u]);
-            if (what_of[u] != NOTHING)
-                sum_load<TD, VEC>(dout + (int64_t)pos * dout_ld, c0, D, lane, x[u]);
-        }
-        int slot = 0, row = 0;      // the open chunk: partial row or WHOLE, token
-        bool open = false;
-        int k = 0;                  // window index of the row in x[0]
-        for (;;) {
-            bool done = false;
+        for (int u = 0; u < ES_U; ++u)
+            fetch(u, x[u]);
+        int slot = 0, row = -1;   // the open chunk: partial row or WHOLE, token
+        int k = 0;                // window index of the row in x[0]
+        for (bool done = false; !done;) {
 #pragma unroll
             for (int u = 0; u < ES_U; ++u) {
-                const int what = what_of[u];
-                if (!done && what != MIDDLE) {
-                    if (open)
+                // (one place for both ends of a chunk: the loop is unrolled and has to stay in
+                // the instruction cache; two took the call from 86 to 133 us)
+                const bool over = at + k + u >= end;
+                if (over || (starts >> (k + u) & 1u)) {
+                    if (row >= 0)
                         sum_store<VEC>(slot >= 0 ? parts + (int64_t)slot * pitch : table + (int64_t)row * table_ld,
                                        slot >= 0, slot >= 0 || vec_out, accumulate, sc, c0, D, lane, acc);
-                    done = what == NOTHING;
-                    open = true;
-                    slot = what;
-                    row = tok_of[u];
+                    slot = __shfl_sync(ALL, cur.z, k + u);
+                    row = __shfl_sync(ALL, cur.y, k + u);
+                    row = over ? -1 : row;
+                    done = over;
 #pragma unroll
                     for (int g = 0; g < ES_G; ++g)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[g][e] = flush(x[u][g][e]);
+                        for (int e = 0; e < 2; ++e)
+                            acc[g][e] = fadd2_ftz(pack2(x[u][g][2 * e], x[u][g][2 * e + 1]), zero);
                 } else {
 #pragma unroll
                     for (int g = 0; g < ES_G; ++g)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[g][e] = fadd_ftz(acc[g][e], x[u][g][e]);
+                        for (int e = 0; e < 2; ++e)
+                            acc[g][e] = fadd2_ftz(acc[g][e], pack2(x[u][g][2 * e], x[u][g][2 * e + 1]));
                 }
-                int pos;
-                entry(k + ES_U + u, pos, tok_of[u], what_of[u]);
-                if (what_of[u] != NOTHING)
-                    sum_load<TD, VEC>(dout + (int64_t)pos * dout_ld, c0, D, lane, x[u]);
+                fetch(k + ES_U + u, x[u]);
             }
-            if (done)
-                break;
             k += ES_U;
             if (k == 32) {
                 at += 32;
                 k = 0;
                 cur = ahead;
-                ahead = at + 32 + lane < n ? order[at + 32 + lane] : none;
+                starts = starts_ahead;
+                window(at + 32, ahead, starts_ahead);
             }
         }
     }
