@@ -954,7 +954,7 @@ int repro_embed_fwd(const void* table, int table_type, int64_t table_ld, const f
         (table_type == REPRO_I8) != (s_w != nullptr))
         return REPRO_ERR_ARG;
     if (n < 0 || V < 1 || D < 1 || table_ld < D || out_ld < D || !rows_fit(V, table_ld, D) ||
-        !rows_fit(n, out_ld, D) || n > INT32_MAX)
+        !rows_fit(n, out_ld, D) || n > INT32_MAX || n * ((D + 511) / 512) > 8 * (int64_t)INT32_MAX)
         return REPRO_ERR_SHAPE;
     if (n == 0)
         return REPRO_OK;
@@ -994,7 +994,7 @@ int repro_embed_bwd(const void* dout, int dout_type, int64_t dout_ld, const void
         (flags & ~REPRO_BWD_DW_ACCUMULATE) || !dtable)
         return REPRO_ERR_ARG;
     if (n < 0 || n > INT32_MAX || V < 1 || V > REPRO_EMBED_MAX_V || D < 1 || dout_ld < D || dtable_ld < D ||
-        !rows_fit(n, dout_ld, D) || !rows_fit(V, dtable_ld, D))
+        !rows_fit(n, dout_ld, D) || !rows_fit(V, dtable_ld, D) || n * ((D + 255) / 256) > 256 * (int64_t)INT32_MAX)
         return REPRO_ERR_SHAPE;
     const bool accumulate = (flags & REPRO_BWD_DW_ACCUMULATE) != 0;
     if (n == 0 && accumulate)

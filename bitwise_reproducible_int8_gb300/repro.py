@@ -397,6 +397,16 @@ def _dev_ptr(t, name, contiguous=True):
     return t.data_ptr()
 
 
+def _call_workspace(nbytes, device, stream):
+    """A workspace for one call: memory that is not handed out again before the
+    call's stream is done with it, whichever stream is current."""
+    ws = _workspace(nbytes, device)
+    if stream is not None:
+        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                         else torch.cuda.ExternalStream(int(stream), device=device))
+    return ws
+
+
 def _float_type(t, name) -> int:
     if t.dtype not in _FLOAT_TYPES:
         raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
@@ -470,7 +480,7 @@ def repro_embed_bwd(dout: torch.Tensor, tokens: torch.Tensor, dtable: torch.Tens
     if dtable.dtype != torch.float32:
         raise ValueError(f"dtable must be {torch.float32}, got {dtable.dtype}")
     if ws is None:
-        ws = _workspace(repro_embed_bwd_ws_bytes(n, V, D), dtable.device)
+        ws = _call_workspace(repro_embed_bwd_ws_bytes(n, V, D), dtable.device, stream)
     _check("repro_embed_bwd", lib().repro_embed_bwd(
         _dev_ptr(dout, "dout", False), _float_type(dout, "dout"), dout_ld, _dev_ptr(tokens, "tokens"),
         _index_bytes("tokens", tokens), n, V, D, float(scale), int(pad), _dev_ptr(dtable, "dtable", False),
@@ -562,7 +572,7 @@ def repro_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out, q: torch.Tensor, k, rop
         if g is not None and g.numel() != D:
             raise ValueError(f"{name} must have D elements")
     if ws is None and (g_q is not None or g_k is not None):
-        ws = _workspace(repro_qk_norm_rope_bwd_ws_bytes(n, Hq, Hkv, D), q.device)
+        ws = _call_workspace(repro_qk_norm_rope_bwd_ws_bytes(n, Hq, Hkv, D), q.device, stream)
     flags = (REPRO_QK_INTERLEAVED if interleaved else 0) | (REPRO_BWD_DW_ACCUMULATE if accumulate else 0)
     has_k = k is not None
     _check("repro_qk_norm_rope_bwd", lib().repro_qk_norm_rope_bwd(
@@ -604,7 +614,7 @@ def repro_distill_fwd(logits: torch.Tensor, t_idx: torch.Tensor, t_logits: torch
     if loss.numel() != n or stats.numel() != n * (REPRO_DISTILL_STATS + K):
         raise ValueError("loss must be [n], stats [n, REPRO_DISTILL_STATS + K]")
     if ws is None:
-        ws = _workspace(repro_distill_ws_bytes(n, V), logits.device)
+        ws = _call_workspace(repro_distill_ws_bytes(n, V), logits.device, stream)
     _check("repro_distill_fwd", lib().repro_distill_fwd(
         _dev_ptr(logits, "logits", False), _float_type(logits, "logits"), ld, _dev_ptr(t_idx, "t_idx"),
         _dev_ptr(t_logits, "t_logits"), _float_type(t_logits, "t_logits"), _dev_ptr(labels, "labels"), ib,

@@ -386,6 +386,55 @@ def test_side_stream_and_debug():
         R.repro_set_debug(0)
 
 
+def test_nan_in_masked_places(orc):
+    """What padding, empty entries and strides leave out is never read into a result."""
+    g = rng(2)
+    d = g.standard_normal((300, 40)).astype(np.float32)
+    tok = g.integers(0, 9, 300)
+    d[tok == 4] = np.nan
+    dW = torch.full((9, 40), 5.0, device="cuda")
+    R.repro_embed_bwd(dev(d), dev(tok), dW, pad=4)
+    same(host(dW), orc.embed_bwd(np.nan_to_num(d), tok, 9, 1.0, 4))
+    assert not torch.isnan(dW).any()
+    W = g.standard_normal((9, 40)).astype(np.float32)
+    W[4] = np.nan
+    out = torch.empty(300, 40, device="cuda")
+    R.repro_embed_fwd(dev(W), dev(tok), out, pad=4)
+    assert not torch.isnan(out).any()
+    z, idx, tl, lab = distill_case(3, 4, 700, 9)
+    idx[:, 5:] = -1
+    bad = tl.copy()
+    bad[:, 5:] = np.nan
+    hp = dict(tau=2.0, w_kd=0.5, w_ce=0.5)
+    gr = np.ones(1, dtype=np.float32)
+    exp = run_distill(z, idx, tl, lab, gr, hp, dev(z))
+    got = run_distill(z, idx, bad, lab, gr, hp, dev(z))
+    for a, b in zip(got, exp):
+        same(a, b)
+
+
+def test_workspace_of_another_stream():
+    """A call that makes its own workspace on a stream that is not current: memory freed
+    on return is not handed to the current stream's work while the call runs."""
+    s = torch.cuda.Stream()
+    z = torch.randn(2000, 20000, device="cuda")
+    idx = torch.randint(0, 20000, (2000, 8), device="cuda")
+    tl = torch.randn(2000, 8, device="cuda")
+    loss, stats = torch.empty(2000, device="cuda"), torch.empty(2000, R.REPRO_DISTILL_STATS + 8, device="cuda")
+    R.repro_distill_fwd(z, idx, tl, loss, stats)
+    want = loss.clone()
+    torch.cuda.synchronize()
+    nbytes = R.repro_distill_ws_bytes(2000, 20000)
+    for _ in range(5):
+        loss.zero_()
+        torch.cuda.synchronize()
+        R.repro_distill_fwd(z, idx, tl, loss, stats, stream=s)
+        junk = torch.full((nbytes,), 0xff, dtype=torch.uint8, device="cuda")
+        s.synchronize()
+        del junk
+        assert torch.equal(loss, want)
+
+
 def test_runs_repeat():
     """The same bits from run to run at a size with many chunks per token."""
     g = torch.Generator(device="cuda").manual_seed(0)
