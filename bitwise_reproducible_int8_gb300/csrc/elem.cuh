@@ -31,6 +31,16 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p)
                        __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
 }
 
+// the same for data that is read once and that no thread writes during the kernel
+__device__ __forceinline__ float4 stream4(const float* p) { return ld_stream(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 stream4(const __nv_bfloat16* p)
+{
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+}
+
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v)
 {

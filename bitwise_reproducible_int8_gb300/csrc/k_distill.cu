@@ -210,7 +210,7 @@ __device__ __forceinline__ void load_block(const T* p, int len, int lane, float 
 #pragma unroll
         for (int i = 0; i < PER; i += 4) {
             if (VEC) {
-                const float4 v = load4(q + 32 * i);
+                const float4 v = stream4(q + 32 * i);
                 x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
             } else {
 #pragma unroll
@@ -318,6 +318,14 @@ __device__ __forceinline__ void do_block(const T* z, int64_t z_ld, const FwdArgs
 constexpr int WARPS = 8;
 constexpr int FWD_CTAS = 5;
 constexpr int MAX_ROWS = 8;   // rows a CTA joins at a time
+
+// asks L2 for `count` elements from p on, a 128-byte line a lane
+template <typename T> __device__ __forceinline__ void fetch_ahead(const T* p, int count, int lane)
+{
+    const int e = lane * (128 / (int)sizeof(T));
+    if (e < count)
+        asm volatile("prefetch.global.L2 [%0];" :: "l"(p + e));
+}
 
 struct RowShared {
     Teacher t[MAX_ROWS];
@@ -652,6 +660,8 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
             break;
         if (blk > first)
             load_piece<T, LINES>(zr, lo, a.V, lane, x);
+        if (blk + 1 < last)
+            fetch_ahead(zr + lo + BBLK, min(a.V - lo - BBLK, BBLK), lane);
 #pragma unroll
         for (int i = 0; i < BPER; i += 2) {
             const u64 v = pack2(x[i], x[i + 1]);

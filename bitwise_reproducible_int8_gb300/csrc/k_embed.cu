@@ -34,6 +34,8 @@ namespace cg = cooperative_groups;
 namespace repro {
 namespace {
 
+typedef unsigned long long u64;
+
 // ---------------------------------------------------------------- forward
 
 constexpr int EF_U = 4;            // 4-element groups per lane
@@ -106,6 +108,7 @@ constexpr int SORT_CTAS = 8;      // CTAs of the sorting cluster
 constexpr int SORT_NT = 1024;
 constexpr int SORT_W = SORT_NT / 32;
 constexpr int DIGITS = 256;
+constexpr int COUNTED = 1024;     // up to this many positions are sorted by counting
 constexpr int ZERO_BYTES = 16384; // zeroed shared memory that bulk copies read
 constexpr int ZERO_WARPS = 8;     // warps whose first lane issues them
 // what begins at a sorted index: a chunk with a partial row (>= 0), a token's only
@@ -162,7 +165,27 @@ __device__ void sort_cluster(const SortArgs& a, SortSmem& sm)
         a.counts[0] = 0;
     const uint2* src = nullptr;
     uint2* dst = a.a;
-    for (int pass = 0; pass < a.passes; ++pass) {
+    if (a.n <= COUNTED) {
+        // few positions: every CTA holds all of them, and eight lanes count how many are
+        // smaller than one.  One trip through memory instead of two passes.
+        u64* keys = reinterpret_cast<u64*>(&sm.hist[0][0]);
+        if (tid < a.n)
+            keys[tid] = (u64)sort_key(a, tid, rank == 0) << 32 | (unsigned)tid;
+        __syncthreads();
+        const int i = rank * (COUNTED / SORT_CTAS) + (tid >> 3);
+        const u64 own = i < a.n ? keys[i] : 0ull;
+        int below = 0;
+        for (int j = tid & 7; j < a.n; j += 8)
+            below += keys[j] < own;
+        for (int o = 1; o < 8; o <<= 1)
+            below += __shfl_xor_sync(0xffffffffu, below, o);
+        if (i < a.n && (tid & 7) == 0)
+            dst[below] = make_uint2((unsigned)(own >> 32), (unsigned)own);
+        __threadfence();
+        cluster.sync();
+        src = dst;
+    }
+    for (int pass = 0; a.n > COUNTED && pass < a.passes; ++pass) {
         const int shift = 8 * pass;
         for (int i = tid; i < SORT_W * DIGITS; i += SORT_NT)
             (&sm.hist[0][0])[i] = 0;
@@ -348,8 +371,6 @@ constexpr int ES_CTAS = 2;          // per SM
 // A row's piece in a lane: ES_G groups of four columns.  Group g begins
 // at column c0 + 4 (lane + 32 g); where rows are not on 4-element boundaries its elements
 // are c0 + lane + 32 (4 g + e) instead.
-typedef unsigned long long u64;
-
 template <bool VEC> __device__ __forceinline__ int64_t sum_col(int64_t c0, int lane, int g, int e)
 {
     return c0 + (VEC ? 4 * (lane + 32 * g) + e : lane + 32 * (4 * g + e));
@@ -363,7 +384,7 @@ __device__ __forceinline__ void sum_load(const TD* s, int64_t c0, int64_t D, int
     for (int g = 0; g < ES_G; ++g) {
         if (VEC) {
             if (sum_col<VEC>(c0, lane, g, 0) < D) {
-                const float4 v = load4(s + sum_col<VEC>(c0, lane, g, 0));
+                const float4 v = stream4(s + sum_col<VEC>(c0, lane, g, 0));
                 x[g][0] = v.x, x[g][1] = v.y, x[g][2] = v.z, x[g][3] = v.w;
             }
         } else {

@@ -48,7 +48,7 @@ __device__ __forceinline__ void load_head(const T* p, int l, int D, float (&x)[E
         const int d = group<E, MODE>(l, g, D);
         if (VEC) {
             if (MODE == SPLIT || d < D) {
-                const float4 v = load4(p + d);
+                const float4 v = stream4(p + d);
                 x[4 * g] = v.x, x[4 * g + 1] = v.y, x[4 * g + 2] = v.z, x[4 * g + 3] = v.w;
             } else {
                 x[4 * g] = x[4 * g + 1] = x[4 * g + 2] = x[4 * g + 3] = 0.0f;
