@@ -311,9 +311,9 @@ __device__ void zero_rows(const SortArgs& a, unsigned* bits, int v0, int v1)
     }
     __syncthreads();
     if (a.vec) {
-        // rows on 16 bytes: bulk copies of a zeroed piece of shared memory, one thread's
-        // instruction each, so that a row is written in one go (a warp's store per row
-        // kept thousands of rows open at once: 268 MB took 64 us)
+        // rows on 16 bytes: bulk copies of a zeroed piece of shared memory, one instruction a
+        // row (268 MB at 6.2 TB/s, as plain stores from all threads).  Leaving part of this
+        // to the sums' kernel made the call longer: 84 -> 94 us with 96 MB written here, 89 with 140.
         float4* zero = reinterpret_cast<float4*>(bits + ((words + 31) & ~31));
         for (int i = tid; i < ZERO_BYTES / 16; i += SORT_NT)
             zero[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
