@@ -21,7 +21,12 @@
 // neighbours.  The blocks' (maximum, sum) pairs of a row are joined once all are
 // there, in the same CTA when there are rows enough for a CTA to own its rows
 // (k_distill_fwd), else by a second kernel, so that few rows over a long
-// vocabulary still spread over the card (k_distill_blocks, k_distill_rows).
+// vocabulary still spread over the card (k_distill_blocks, k_distill_rows).  What a row
+// needs of the teacher does not wait for its blocks and is done beside them.
+//
+// 8192 x 32768 fp32 with 64 entries a row: forward 174 us at tau 1 (6.2 TB/s, 0.92 of a
+// copy's), 187 us at tau 2 with labels; backward 313 us (6.9 TB/s).  bf16: forward 165 us,
+// backward 209 us, bound by the FP32 pipe.
 #include <math_constants.h>
 
 #include "elem.cuh"
@@ -756,7 +761,8 @@ template <typename T> cudaError_t fwd_typed(const DistillArgs& a, void* ws, cuda
     r.loss = a.loss;
     r.stats = a.stats;
     r.err = a.err;
-    // rows per CTA: two of at least 8 blocks, more of shorter ones
+    // rows per CTA: two of at least 8 blocks (8192 x 32768: one row 205 us, two 193, four 200),
+    // more of shorter ones; from four CTAs per SM on a CTA owns its rows (the other way 217 us)
     const int rows = nblk >= 8 ? 2 : nblk >= 4 ? 4 : MAX_ROWS;
     const bool owned = (a.n + rows - 1) / rows >= 4 * num_sms();
     return by_sums(sums_of(a), [&](auto s) {
@@ -810,7 +816,8 @@ template <typename T> cudaError_t bwd_typed(const DistillArgs& a, cudaStream_t s
                        (a.z_ld - a.dz_ld) % line == 0;
     b.mask = lines ? (int)line - 1 : 0;
     b.nblk = (int)((a.V + b.mask + BBLK - 1) / BBLK);
-    // eight pieces a warp once that leaves every scheduler several warps
+    // eight pieces a warp once that leaves every scheduler several warps (1021 x 130001 bf16 with
+    // pieces of 1024: one a warp 264 us, two 251, four 240)
     b.per = a.n * b.nblk >= (int64_t)num_sms() * 256 ? 8 : 1;
     b.groups = (b.nblk + b.per - 1) / b.per;
     b.items = (int)(a.n * b.groups);
