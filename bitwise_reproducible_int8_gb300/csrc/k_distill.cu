@@ -190,14 +190,6 @@ __device__ __forceinline__ float warp_tree(float v)
     return v;
 }
 
-__device__ __forceinline__ double warp_tree(double v)
-{
-#pragma unroll
-    for (int s = 1; s < 32; s *= 2)
-        v = v + __shfl_xor_sync(0xffffffffu, v, s);
-    return v;
-}
-
 // Element of the block in slot i of this lane.  Rows on 4-element boundaries:
 // four neighbours per load; else single elements.  Either way slots i, i + 4, ..
 // of a lane are one chain (element mod 128), ascending.
@@ -282,9 +274,9 @@ __device__ __forceinline__ void block_stats(const T* p, int len, int lane, unsig
         s1 = chains_tree<VEC>(a1, b1);
 }
 
-// a row's teacher: maximum, sum, P, ln of the sum, the sums of p_k (a_k - u_k) and of p_k
+// a row's teacher: the sums of p_k (a_k - u_k) and of p_k, maximum, sum and P
 struct Teacher {
-    double ln_lt, sum, weight;
+    double sum, weight;
     float mt, lt, P, unused;
 };
 
@@ -335,7 +327,7 @@ template <typename T> __device__ __forceinline__ void fetch_ahead(const T* p, in
 struct RowShared {
     Teacher t[MAX_ROWS];
     float M[MAX_ROWS], l[MAX_ROWS], l1[MAX_ROWS];
-    double ln[2][MAX_ROWS];
+    double ln[3][MAX_ROWS];
     int next;   // block handed out
 };
 
@@ -362,7 +354,7 @@ __device__ void teacher_row(const T* zr, const FwdArgs& a, int64_t row, Teacher*
     const int lane = threadIdx.x & 31;
     float* p = a.stats + row * (STATS + a.K) + STATS;
     float mt = a.logprobs ? 0.0f : -CUDART_INF_F, lt = 0.0f, P = 0.0f;
-    double sum = 0.0, weight = 0.0, ln_lt = 0.0;
+    double sum = 0.0, weight = 0.0;
     int j;
     if (!a.logprobs) {
         for (int k = lane; k < a.K; k += 32)
@@ -396,13 +388,19 @@ __device__ void teacher_row(const T* zr, const FwdArgs& a, int64_t row, Teacher*
             }
         }
         if (a.w_kd != 0.0f) {
-            sum = warp_tree(sum);
-            weight = warp_tree(weight);
-            ln_lt = ln_d(lt);
+            // both trees at once: after the first level the even lanes have the one, the odd
+            // lanes the other (6 binary64 additions instead of 10)
+            const bool odd = lane & 1;
+            double v = (odd ? weight : sum) + __shfl_xor_sync(0xffffffffu, odd ? sum : weight, 1);
+#pragma unroll
+            for (int s = 2; s < 32; s *= 2)
+                v = v + __shfl_xor_sync(0xffffffffu, v, s);
+            sum = __shfl_sync(0xffffffffu, v, 0);
+            weight = __shfl_sync(0xffffffffu, v, 1);
         }
     }
     if (lane == 0)
-        *out = {ln_lt, sum, weight, mt, lt, P, 0.0f};
+        *out = {sum, weight, mt, lt, P, 0.0f};
 }
 
 // joins the blocks of rows [r0, r0 + cnt) and forms the losses.  A warp per row, but the
@@ -442,10 +440,10 @@ __device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, 
     __syncthreads();
     if (threadIdx.x >= 32)
         return;
-    if (lane < 2 * MAX_ROWS) {
+    if (lane < 3 * MAX_ROWS) {
         const int which = lane / MAX_ROWS, r = lane % MAX_ROWS;
         if (r < cnt)
-            sh.ln[which][r] = ln_d(which == 0 ? sh.l[r] : sh.l1[r]);
+            sh.ln[which][r] = ln_d(which == 0 ? sh.l[r] : which == 1 ? sh.l1[r] : teachers[r].lt);
     }
     __syncwarp();
     if (lane >= cnt)
@@ -461,7 +459,7 @@ __device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, 
     double v = 0.0;
     if (!none && a.w_kd != 0.0f && t.mt != -CUDART_INF_F)
         v = ((double)a.w_kd * ((double)a.tau * (double)a.tau)) *
-            (t.sum + (lse_t - ((double)t.mt + t.ln_lt)) * t.weight);
+            (t.sum + (lse_t - ((double)t.mt + sh.ln[2][r])) * t.weight);
     if (a.w_ce != 0.0f) {
         const int64_t lab = load_index(a.labels, a.index_bytes, row);
         if (lab >= a.V)

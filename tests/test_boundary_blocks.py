@@ -125,7 +125,7 @@ DISTILL_BAD = [(dict(z=None), -1), (dict(t_idx=None), -1), (dict(z_type=2), -1),
 
 def test_distill(L):
     ws = repro.repro_distill_ws_bytes(40, 5000)
-    assert ws == 40 * (5 * 12 + 40)
+    assert ws == 40 * (5 * 12 + 32)
     ok = dict(z=B, z_type=0, z_ld=5000, t_idx=2 * B, t_val=3 * B, t_type=0, labels=4 * B, index_bytes=4, n=40,
               V=5000, K=16, hp=hp(), flags=0, loss=5 * B, stats=6 * B, ws=7 * B, ws_bytes=ws, stream=None)
     f = lambda **kw: call(L.repro_distill_fwd, ok, **kw)  # noqa: E731
