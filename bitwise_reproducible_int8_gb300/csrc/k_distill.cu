@@ -551,7 +551,9 @@ struct BwdArgs {
     int64_t g_stride;
 };
 
-constexpr int BWD_CTAS = 5;
+constexpr int BWD_CTAS = 4;
+constexpr int LIST = 128;          // teacher entries in its pieces that a warp of the backward lists
+constexpr int FEW = 3;             // entries in a piece that are taken one by one
 constexpr int BPER = 16;           // logits per lane and piece of the backward
 constexpr int BBLK = 32 * BPER;
 
@@ -607,12 +609,14 @@ __device__ __forceinline__ void store_piece(T* p, int lo, int V, int lane, const
 // One warp takes `per` consecutive pieces of a row, so that what belongs to the row
 // (statistics, coefficients and their divisions) is done once.  Pieces of 16 logits a
 // lane leave registers for 40 warps per SM, which is what covers the loads.
-template <typename T, int SUMS, bool LINES>
+template <typename T, int SUMS, bool LINES, bool LONG>
 __global__ void __launch_bounds__(32 * WARPS, BWD_CTAS)
 k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_constant__ BwdArgs a)
 {
-    const int lane = threadIdx.x & 31;
-    const int item = blockIdx.x * WARPS + (threadIdx.x >> 5);
+    __shared__ float pieces[WARPS][BBLK], weights[WARPS][LONG ? LIST : 1];
+    __shared__ int columns[WARPS][LONG ? LIST : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int item = blockIdx.x * WARPS + warp;
     if (item >= a.items)
         return;
     const int row = item / a.groups, first = (item - row * a.groups) * a.per;
@@ -630,14 +634,17 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
         const int64_t t = load_index(a.labels, a.index_bytes, row);
         lab = t >= 0 && t < a.V ? (int)t : -1;
     }
-    // the row's first 64 columns stay in registers over the warp's pieces
+    const int K = a.w_kd != 0.0f ? a.K : 0;
     auto column = [&](int k) {
-        int64_t j = -1;
-        if (k < a.K && a.w_kd != 0.0f)
-            j = load_index(a.t_idx, a.index_bytes, (int64_t)row * a.K + k);
+        const int64_t j = k < K ? load_index(a.t_idx, a.index_bytes, (int64_t)row * a.K + k) : -1;
         return j >= 0 && j < a.V ? (int)j : -1;
     };
-    const int col0 = column(lane), col1 = a.K > 32 ? column(lane + 32) : -1;
+    int col0 = column(lane), col1 = K > 32 ? column(lane + 32) : -1;   // on their way, too
+    float p0 = 0.0f, p1 = 0.0f;
+    if (!LONG) {
+        p0 = col0 >= 0 ? st[STATS + lane] : 0.0f;
+        p1 = col1 >= 0 ? st[STATS + lane + 32] : 0.0f;
+    }
     const float gk = fmul_flush(fmul_flush(g, a.w_kd), a.tau);
     const float ca = fmul_flush(gk, P);
     const float cb = fmul_flush(g, fadd_ftz(lab >= 0 ? a.w_ce : 0.0f,
@@ -647,6 +654,7 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
     const float Mu = fmul_flush(M, a.it);
     const u64 zero = dup2(-0.0f), nu = dup2(-Mu), nm = dup2(-M), sc = dup2(a.it), wa = dup2(qa), wb = dup2(qb);
     const int last = min(first + a.per, a.nblk);
+    int listed = 0;
     if (M == -CUDART_INF_F) {   // nothing in the row: no gradient
 #pragma unroll
         for (int i = 0; i < BPER; ++i)
@@ -655,7 +663,6 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
             store_piece<T, LINES>(dr, blk * BBLK - shift, a.V, lane, x);
         return;
     }
-    const bool kd = a.w_kd != 0.0f;
     const float cl = lab >= 0 ? fmul_flush(g, a.w_ce) : 0.0f;
     for (int blk = first; blk < last; ++blk) {
         const int lo = blk * BBLK - shift;
@@ -678,9 +685,82 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
         }
         // the teacher's entries and the label inside this piece, entry by entry
         const int lo0 = max(lo, 0), end = lo + BBLK;
-        const bool in0 = col0 >= lo0 && col0 < end, in1 = col1 >= lo0 && col1 < end, inl = lab >= lo0 && lab < end;
-        if (__any_sync(0xffffffffu, in0 || in1 || inl || (kd && a.K > 64))) {
-            auto take = [&](int e, float c) {
+        const bool inl = lab >= lo0 && lab < end;
+        if (LONG && blk == first) {
+            // the teacher's entries in the warp's pieces, in order: most pieces have few or none
+            const int from = max(lo, 0), to = min(a.V, (last * BBLK) - shift);
+            for (int k0 = 0; k0 < K; k0 += 32) {
+                const int j = k0 == 0 ? col0 : k0 == 32 ? col1 : column(k0 + lane);
+                const bool in = j >= from && j < to;
+                const unsigned m = __ballot_sync(0xffffffffu, in);
+                const int at = listed + __popc(m & ((1u << lane) - 1u));
+                if (in && at < LIST) {
+                    columns[warp][at] = j;
+                    weights[warp][at] = st[STATS + k0 + lane];
+                }
+                listed += __popc(m);
+            }
+            __syncwarp();
+            col0 = lane < min(listed, LIST) ? columns[warp][lane] : -1;
+            p0 = col0 >= 0 ? weights[warp][lane] : 0.0f;
+        }
+        auto within = [&](int j) { return j >= lo0 && j < end; };
+        // entry k0 + lane: of the row, or of the list where that has all of them
+        const int entries = !LONG || listed > LIST ? K : listed;
+        auto entry = [&](int k0, int& j, float& p) {
+            j = k0 == 0 ? col0 : col1;
+            p = k0 == 0 ? p0 : p1;
+            if (LONG && listed > LIST) {
+                j = column(k0 + lane);
+                p = within(j) ? st[STATS + k0 + lane] : 0.0f;
+            } else if (LONG && k0 > 0) {
+                j = k0 + lane < listed ? columns[warp][k0 + lane] : -1;
+                p = j >= 0 ? weights[warp][k0 + lane] : 0.0f;
+            }
+        };
+        int hits = 0;
+        for (int k0 = 0; k0 < entries; k0 += 32) {
+            int j;
+            float p;
+            entry(k0, j, p);
+            hits += __popc(__ballot_sync(0xffffffffu, within(j)));
+        }
+        if (hits > FEW) {
+            // through shared memory, 32 entries at a time, those of one column after one another
+            float* piece = pieces[warp];
+            auto place = [&](int e) {
+                constexpr int W = 16 / sizeof(T);
+                return LINES ? 32 * (e / (32 * W) * W + e % W) + (e / W & 31) : e;
+            };
+#pragma unroll
+            for (int i = 0; i < BPER; ++i)
+                piece[32 * i + lane] = x[i];
+            __syncwarp();
+            for (int k0 = 0; k0 < entries; k0 += 32) {
+                int j;
+                float p;
+                entry(k0, j, p);
+                if (__ballot_sync(0xffffffffu, within(j)) == 0)
+                    continue;
+                const int at = within(j) ? place(j - lo) : -1 - lane;
+                const unsigned same = __match_any_sync(0xffffffffu, at);
+                const int turn = __popc(same & ((1u << lane) - 1u));
+                const int turns = __reduce_max_sync(0xffffffffu, turn);
+                for (int t = 0; t <= turns; ++t) {
+                    if (within(j) && turn == t)
+                        piece[at] = fadd_ftz(piece[at], -fmul_flush(gk, p));
+                    __syncwarp();
+                }
+            }
+            if (inl && lane == 0)
+                piece[place(lab - lo)] = fadd_ftz(piece[place(lab - lo)], -cl);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < BPER; ++i)
+                x[i] = piece[32 * i + lane];
+            __syncwarp();
+        } else if (hits > 0 || inl) {
+            auto take = [&](int e, float c) {   // (a branch on the slot would put x in local memory)
                 constexpr int W = 16 / sizeof(T);
                 const int slot = LINES ? e / (32 * W) * W + e % W : e >> 5;
                 const int own = LINES ? e / W & 31 : e & 31;
@@ -689,17 +769,16 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
                     if (i == slot && lane == own)
                         x[i] = fadd_ftz(x[i], -c);
             };
-            for (int k0 = 0; kd && k0 < a.K; k0 += 32) {
-                const int j = k0 == 0 ? col0 : k0 == 32 ? col1 : column(k0 + lane);
-                const bool here = j >= lo0 && j < end;
-                unsigned hits = __ballot_sync(0xffffffffu, here);
-                if (hits == 0)
-                    continue;
-                const float c = here ? fmul_flush(gk, st[STATS + k0 + lane]) : 0.0f;
-                while (hits) {
-                    const int src = __ffs(hits) - 1;
-                    hits &= hits - 1;
-                    take(__shfl_sync(0xffffffffu, j - lo, src), __shfl_sync(0xffffffffu, c, src));
+            for (int k0 = 0; hits > 0; k0 += 32) {
+                int j;
+                float p;
+                entry(k0, j, p);
+                unsigned in = __ballot_sync(0xffffffffu, within(j));
+                hits -= __popc(in);
+                while (in) {
+                    const int src = __ffs(in) - 1;
+                    in &= in - 1;
+                    take(__shfl_sync(0xffffffffu, j - lo, src), fmul_flush(gk, __shfl_sync(0xffffffffu, p, src)));
                 }
             }
             if (inl)
@@ -822,10 +901,11 @@ template <typename T> cudaError_t bwd_typed(const DistillArgs& a, cudaStream_t s
     return by_sums(sums_of(a), [&](auto s) {
         constexpr int SUMS = decltype(s)::value;
         const unsigned grid = (unsigned)((b.items + WARPS - 1) / WARPS);
+        auto go = [&](auto kernel) { kernel<<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, dz, a.dz_ld, b); };
         if (lines)
-            k_distill_bwd<T, SUMS, true><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, dz, a.dz_ld, b);
+            a.K > 64 ? go(k_distill_bwd<T, SUMS, true, true>) : go(k_distill_bwd<T, SUMS, true, false>);
         else
-            k_distill_bwd<T, SUMS, false><<<grid, 32 * WARPS, 0, st>>>(z, a.z_ld, dz, a.dz_ld, b);
+            a.K > 64 ? go(k_distill_bwd<T, SUMS, false, true>) : go(k_distill_bwd<T, SUMS, false, false>);
         count_launches(1);
         return cudaGetLastError();
     });
