@@ -256,7 +256,7 @@ def run_distill(z, idx, tl, lab, g, hp, zt, t_dtype=torch.float32, int_t=np.int3
 
 
 @pytest.mark.parametrize("n,V,K", [(1, 1, 1), (3, 31, 0), (5, 130, 7), (2, 1023, 33), (4, 1024, 40), (3, 1025, 64),
-                                   (7, 5001, 100), (2, 70000, 64)])
+                                   (7, 5001, 100), (2, 70000, 64), (3, 300, 200), (2, 9000, 300)])
 @pytest.mark.parametrize("kind", ["f32", "bf16", "odd", "odd16"])
 @pytest.mark.parametrize("hp", HP)
 def test_distill(orc, n, V, K, kind, hp):
@@ -455,3 +455,74 @@ def test_runs_repeat():
         if first is None:
             first = outs
         assert all(torch.equal(a, b) for a, b in zip(first, outs))
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+
+def test_embed_offsets_past_32_bits():
+    """1.1 M rows of 2048: the output's and the gradient's offsets pass 2^31 elements."""
+    n, V, D = 1100000, 3000, 2048
+    g = torch.Generator(device="cuda").manual_seed(1)
+    table = torch.randn(V, D, device="cuda", generator=g)
+    tok = torch.randint(0, V, (n,), device="cuda", generator=g)
+    out = torch.empty(n, D, device="cuda")
+    R.repro_embed_fwd(table, tok, out, scale=2.0)
+    part = torch.empty(1000, D, device="cuda")
+    R.repro_embed_fwd(table, tok[-1000:].contiguous(), part, scale=2.0)
+    assert torch.equal(out[-1000:], part)
+    # a token that only the last rows have: its gradient is the sum of those rows alone
+    tok[tok == 7] = 8
+    tok[-130:] = 7
+    dW, few = torch.empty(V, D, device="cuda"), torch.empty(V, D, device="cuda")
+    R.repro_embed_bwd(out, tok, dW)
+    R.repro_embed_bwd(out[-130:], tok[-130:].contiguous(), few)
+    assert torch.equal(dW[7], few[7])
+    assert R.repro_device_check() == 0
+
+
+def test_qk_offsets_past_32_bits():
+    n, Hq, Hkv, D = 900000, 16, 4, 128
+    g = torch.Generator(device="cuda").manual_seed(2)
+    qkv = torch.empty(n, (Hq + 2 * Hkv) * D, device="cuda", dtype=BF).normal_(generator=g)
+    heads = lambda t: (t.view(-1, Hq + 2 * Hkv, D)[:, :Hq], t.view(-1, Hq + 2 * Hkv, D)[:, Hq:Hq + Hkv])  # noqa: E731
+    rope = dev(rope_table(64, D))
+    pos = torch.arange(n, device="cuda", dtype=torch.int32) % 64
+    q, k = heads(qkv)
+    qo, ko = torch.empty(n, Hq, D, device="cuda"), torch.empty(n, Hkv, D, device="cuda")
+    R.repro_qk_norm_rope_fwd(q, k, rope, qo, ko, positions=pos)
+    m = 500
+    qs, ks = heads(qkv[-m:])
+    qp, kp = torch.empty(m, Hq, D, device="cuda"), torch.empty(m, Hkv, D, device="cuda")
+    R.repro_qk_norm_rope_fwd(qs, ks, rope, qp, kp, positions=pos[-m:].contiguous())
+    assert torch.equal(qo[-m:], qp) and torch.equal(ko[-m:], kp)
+    dqkv = torch.empty_like(qkv)
+    dq, dk = heads(dqkv)
+    R.repro_qk_norm_rope_bwd(qo, ko, q, k, rope, dq, dk, positions=pos)
+    part = torch.empty_like(qkv[-m:])
+    dqs, dks = heads(part)
+    R.repro_qk_norm_rope_bwd(qp, kp, qs, ks, rope, dqs, dks, positions=pos[-m:].contiguous())
+    assert torch.equal(dq[-m:], dqs) and torch.equal(dk[-m:], dks)
+    assert R.repro_device_check() == 0
+
+
+def test_distill_offsets_past_32_bits():
+    n, V, K = 70000, 33001, 5
+    g = torch.Generator(device="cuda").manual_seed(3)
+    z = torch.empty(n, V, device="cuda", dtype=BF).normal_(generator=g)
+    idx = torch.randint(0, V, (n, K), device="cuda", generator=g)
+    tl = torch.randn(n, K, device="cuda", generator=g)
+    one = torch.ones(1, device="cuda")
+
+    def run(z, idx, tl):
+        loss = torch.empty(z.shape[0], device="cuda")
+        stats = torch.empty(z.shape[0], R.REPRO_DISTILL_STATS + K, device="cuda")
+        R.repro_distill_fwd(z, idx, tl, loss, stats, tau=2.0)
+        dz = torch.empty_like(z)
+        R.repro_distill_bwd(z, idx, stats, one, dz, tau=2.0)
+        return loss, stats, dz
+
+    m = 300
+    whole, part = run(z, idx, tl), run(z[-m:].clone(), idx[-m:].contiguous(), tl[-m:].contiguous())
+    for a, b in zip(whole, part):
+        assert torch.equal(a[-m:], b)
+    assert R.repro_device_check() == 0
