@@ -24,9 +24,9 @@
 // vocabulary still spread over the card (k_distill_blocks, k_distill_rows).  What a row
 // needs of the teacher does not wait for its blocks and is done beside them.
 //
-// 8192 x 32768 fp32 with 64 entries a row: forward 174 us at tau 1 (6.2 TB/s, 0.92 of a
-// copy's), 187 us at tau 2 with labels; backward 313 us (6.9 TB/s).  bf16: forward 165 us,
-// backward 209 us, bound by the FP32 pipe.
+// 8192 x 32768 fp32 with 64 entries a row: forward 170 us at tau 1 (6.3 TB/s, 0.94 of a
+// copy's), 186 us at tau 2 with labels; backward 312 us (6.9 TB/s).  4096 x 32768 bf16:
+// forward 91 us, backward 118 us (98 with one entry a row), bound by the FP32 pipe.
 #include <math_constants.h>
 
 #include "elem.cuh"
