@@ -17,7 +17,7 @@ from .repro import (  # noqa: F401
     REPRO_HASH_LEAF_BYTES, REPRO_DEBUG_CHECK_FINITE, REPRO_ERR_NONFINITE, REPRO_ERR_TIMEOUT,
     repro_set_debug,
     REPRO_BF16, REPRO_DISTILL_BLOCK, REPRO_DISTILL_LOGPROBS, REPRO_DISTILL_STATS,
-    REPRO_DISTILL_STAT_LSE, REPRO_EMBED_MAX_V, REPRO_ERR_INDEX, REPRO_F32, REPRO_I8,
+    REPRO_DISTILL_STAT_LSE, REPRO_EMBED_MAX_N, REPRO_EMBED_MAX_V, REPRO_ERR_INDEX, REPRO_F32, REPRO_I8,
     REPRO_QK_INTERLEAVED, REPRO_QK_MAX_D, repro_distill_bwd, repro_distill_fwd,
     repro_distill_ws_bytes, repro_embed_bwd, repro_embed_bwd_ws_bytes, repro_embed_fwd,
     repro_qk_norm_rope_bwd, repro_qk_norm_rope_bwd_ws_bytes, repro_qk_norm_rope_fwd,

@@ -981,7 +981,7 @@ int repro_embed_fwd(const void* table, int table_type, int64_t table_ld, const f
 
 size_t repro_embed_bwd_ws_bytes(int64_t n, int64_t V, int64_t D)
 {
-    if (n < 0 || n > INT32_MAX || V < 1 || V > REPRO_EMBED_MAX_V || D < 1 || D > (int64_t)1 << 28)
+    if (n < 0 || n > REPRO_EMBED_MAX_N || V < 1 || V > REPRO_EMBED_MAX_V || D < 1 || D > (int64_t)1 << 28)
         return 0;
     return embed_bwd_ws_bytes(n, V, D);
 }
@@ -993,7 +993,7 @@ int repro_embed_bwd(const void* dout, int dout_type, int64_t dout_ld, const void
     if (!float_type(dout_type) || (index_bytes != 4 && index_bytes != 8) || !finite_f(scale) ||
         (flags & ~REPRO_BWD_DW_ACCUMULATE) || !dtable)
         return REPRO_ERR_ARG;
-    if (n < 0 || n > INT32_MAX || V < 1 || V > REPRO_EMBED_MAX_V || D < 1 || dout_ld < D || dtable_ld < D ||
+    if (n < 0 || n > REPRO_EMBED_MAX_N || V < 1 || V > REPRO_EMBED_MAX_V || D < 1 || dout_ld < D || dtable_ld < D ||
         !rows_fit(n, dout_ld, D) || !rows_fit(V, dtable_ld, D) || n * ((D + 255) / 256) > 256 * (int64_t)INT32_MAX)
         return REPRO_ERR_SHAPE;
     const bool accumulate = (flags & REPRO_BWD_DW_ACCUMULATE) != 0;
@@ -1229,7 +1229,7 @@ static int check_distill(const void* z, int z_type, int64_t z_ld, const void* t_
     if (!(hp->tau >= 1e-4f && hp->tau <= 1e4f) || !finite_f(hp->w_kd) || !finite_f(hp->w_ce) || !finite_f(hp->w_z))
         return REPRO_ERR_ARG;
     if (n < 0 || V < 1 || K < 0 || z_ld < V || !rows_fit(n, z_ld, V) || K > 65536 || n > INT32_MAX ||
-        n * ((V + 574) / 512) > INT32_MAX)
+        n * ((V + 574) / 512) > (int64_t)1 << 30)   // block numbers, with room past the last one
         return REPRO_ERR_SHAPE;
     if (n == 0)
         return REPRO_OK;

@@ -33,6 +33,7 @@ REPRO_QMAX = 127
 REPRO_MAX_REPLICAS = 64
 REPRO_F32, REPRO_BF16, REPRO_I8 = 0, 1, 2
 REPRO_EMBED_MAX_V = 16777215
+REPRO_EMBED_MAX_N = 1 << 30
 REPRO_QK_INTERLEAVED = 2
 REPRO_QK_MAX_D = 512
 REPRO_DISTILL_BLOCK = 1024

@@ -380,10 +380,11 @@ int repro_embed_fwd(const void* table, int table_type, int64_t table_ld, const f
  * tok_i = v, ascending, of dout_id, (x) scale; +0 for a row without tokens.  With
  * REPRO_BWD_DW_ACCUMULATE in flags: dtable (+) that, rows without tokens left
  * alone.  Padding and out-of-range tokens contribute nothing.  dtable [V][D]
- * fp32, rows dtable_ld apart.  V <= REPRO_EMBED_MAX_V, n < 2^31.  ws:
+ * fp32, rows dtable_ld apart.  V <= REPRO_EMBED_MAX_V, n <= REPRO_EMBED_MAX_N.  ws:
  * repro_embed_bwd_ws_bytes(n, V, D) bytes: the sorted positions and the partial
  * sums of tokens that occur more than 64 times. */
 #define REPRO_EMBED_MAX_V 16777215
+#define REPRO_EMBED_MAX_N 1073741824
 int repro_embed_bwd(const void* dout, int dout_type, int64_t dout_ld, const void* tokens,
                     int index_bytes, int64_t n, int64_t V, int64_t D, float scale, int64_t pad,
                     float* dtable, int64_t dtable_ld, int flags, void* ws, size_t ws_bytes,
@@ -467,7 +468,9 @@ size_t repro_qk_norm_rope_bwd_ws_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64
  * stats [n][REPRO_DISTILL_STATS + K] fp32 (dense): M, l, lse(u), l1, lse(z), m, lt, P,
  * then the p_k; the backward's input.  (l1 and lse(z) are 0 when tau != 1 and
  * both w_ce and w_z are 0.)  loss [n] fp32.  hp: HOST struct, tau > 0 finite.
- * labels may be NULL when w_ce is 0.  ws: repro_distill_ws_bytes(n, V) bytes. */
+ * labels may be NULL when w_ce is 0.  n ceil((V + 63) / 512) <= 2^30, K <= 65536.  ws:
+ * repro_distill_ws_bytes(n, V) bytes.  (Debug mode scans z, not t_val, where -infinity
+ * is an ordinary value.) */
 #define REPRO_DISTILL_BLOCK 1024
 #define REPRO_DISTILL_STATS 8
 #define REPRO_DISTILL_STAT_LSE 2

@@ -53,6 +53,7 @@ def test_embed_bwd(L):
                dict(index_bytes=1), dict(scale=-INF)):
         assert f(**kw) == -1, kw
     for kw in (dict(n=-1), dict(V=0), dict(V=repro.REPRO_EMBED_MAX_V + 1), dict(D=0), dict(dout_ld=1),
+               dict(n=repro.REPRO_EMBED_MAX_N + 1),
                dict(dtable_ld=63)):
         assert f(**kw) == -2, kw
     assert f(ws=None) == -7 and f(ws_bytes=ws - 1) == -7
