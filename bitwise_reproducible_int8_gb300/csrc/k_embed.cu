@@ -16,7 +16,8 @@
 //      pass and marks where chunks of up to 64 positions begin.  The other clusters
 //      of the same launch zero the table rows that no token names (each marks its
 //      own rows' tokens in a bitmap first), so the sort hides behind the part of the
-//      write that needs no order.
+//      write that needs no order.  Few tokens: k_embed_rank, every token's place by
+//      counting, over the whole card and without passes.
 //   2. k_embed_sum: the rows in sorted order as one stream per warp and piece of the
 //      columns, left to right from each chunk's first term; a token's only chunk is
 //      scaled and stored, others leave their partial row in the workspace.
@@ -24,7 +25,7 @@
 //      only launched when n > 64, below which no token can have two chunks.
 // 16,384 tokens (text-like frequencies) into 32768 x 2048: 83 to 86 us, 4.8 TB/s: 41 us
 // zeroing beside the sort, 36 summing (rows read in sorted order, 4.9 TB/s), 7 the tree;
-// added into an existing gradient 55 us.
+// added into an existing gradient 55 us (301 tokens 10 us).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -112,7 +113,6 @@ constexpr int SORT_CTAS = 8;      // CTAs of the sorting cluster
 constexpr int SORT_NT = 1024;
 constexpr int SORT_W = SORT_NT / 32;
 constexpr int DIGITS = 256;
-constexpr int COUNTED = 1024;     // up to this many positions are sorted by counting
 constexpr int ZERO_BYTES = 16384; // zeroed shared memory that bulk copies read
 constexpr int ZERO_WARPS = 8;     // warps whose first lane issues them
 // what begins at a sorted index: a chunk with a partial row (>= 0), a token's only
@@ -129,8 +129,7 @@ struct SortArgs {
     uint2* b;            // .. and by passes 1, 3
     int2* seg;           // [V] first and one past the last sorted index of a named token
     int* counts;         // tokens with several chunks
-    int4* order;         // [n] {position, token, what begins here, 0}
-    int4* joins;         // {first sorted index, chunks, token, 0}
+    int4* order;         // [n] {position, token, what begins here, the token's positions}
     float* table;        // rows to zero, or NULL
     int64_t table_ld;
     int64_t D;
@@ -169,27 +168,7 @@ __device__ void sort_cluster(const SortArgs& a, SortSmem& sm)
         a.counts[0] = 0;
     const uint2* src = nullptr;
     uint2* dst = a.a;
-    if (a.n <= COUNTED) {
-        // few positions: every CTA holds all of them, and eight lanes count how many are
-        // smaller than one.  One trip through memory instead of two passes.
-        u64* keys = reinterpret_cast<u64*>(&sm.hist[0][0]);
-        if (tid < a.n)
-            keys[tid] = (u64)sort_key(a, tid, rank == 0) << 32 | (unsigned)tid;
-        __syncthreads();
-        const int i = rank * (COUNTED / SORT_CTAS) + (tid >> 3);
-        const u64 own = i < a.n ? keys[i] : 0ull;
-        int below = 0;
-        for (int j = tid & 7; j < a.n; j += 8)
-            below += keys[j] < own;
-        for (int o = 1; o < 8; o <<= 1)
-            below += __shfl_xor_sync(0xffffffffu, below, o);
-        if (i < a.n && (tid & 7) == 0)
-            dst[below] = make_uint2((unsigned)(own >> 32), (unsigned)own);
-        __threadfence();
-        cluster.sync();
-        src = dst;
-    }
-    for (int pass = 0; a.n > COUNTED && pass < a.passes; ++pass) {
+    for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = 8 * pass;
         for (int i = tid; i < SORT_W * DIGITS; i += SORT_NT)
             (&sm.hist[0][0])[i] = 0;
@@ -279,7 +258,7 @@ __device__ void sort_cluster(const SortArgs& a, SortSmem& sm)
     // sorted index i begins a chunk when it is a multiple of 64 past its token's first
     for (int i = rank * SORT_NT + tid; i < a.n; i += SORT_CTAS * SORT_NT) {
         const uint2 kv = ld_pair(src + i);
-        int what = NOTHING;
+        int what = NOTHING, length = 0;
         if (kv.x < (unsigned)a.V) {
             const int2 g = __ldcg(&a.seg[kv.x]);
             const bool several = g.y - g.x > 64;
@@ -288,17 +267,57 @@ __device__ void sort_cluster(const SortArgs& a, SortSmem& sm)
             // token with several starts that is its first, and at most one that is not
             if (((i - g.x) & 63) == 0)
                 what = several ? 2 * (i >> 6) + (g.x == i ? 1 : 0) : WHOLE;
-            if (several && g.x == i)
-                a.joins[atomicAdd(&a.counts[0], 1)] = make_int4(i, (g.y - g.x + 63) / 64, (int)kv.x, 0);
+            length = g.y - g.x;
         }
-        a.order[i] = make_int4((int)kv.y, (int)kv.x, what, 0);
+        a.order[i] = make_int4((int)kv.y, (int)kv.x, what, length);
     }
 }
 
-// zero the table rows in [v0, v1) that no token names
+// zeroes the table rows in [v0, v1) whose bit is not set, by all of the CTA's threads; `zero`
+// is ZERO_BYTES of shared memory.  Where rows lie on 16 bytes the copy engine writes them
+// out of zeroed shared memory, one instruction a row (268 MB at 6.2 TB/s, as plain stores from
+// all threads); zero_wait() is due before the CTA ends.  Leaving part of this to the
+// sums' kernel made the call longer: 84 -> 94 us with 96 MB written here, 89 with 140.
+__device__ void zero_unnamed(const SortArgs& a, const unsigned* bits, float4* zero, int v0, int v1)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+    if (!a.vec) {
+        for (int v = v0 + warp; v < v1; v += threads / 32) {
+            if (bits[(v - v0) >> 5] >> ((v - v0) & 31) & 1u)
+                continue;
+            float* row = a.table + (int64_t)v * a.table_ld;
+            for (int64_t c = lane; c < a.D; c += 32)
+                row[c] = 0.0f;
+        }
+        return;
+    }
+    for (int i = tid; i < ZERO_BYTES / 16; i += threads)
+        zero[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    const unsigned src = (unsigned)__cvta_generic_to_shared(zero);
+    if (warp < ZERO_WARPS && lane == 0) {
+        for (int v = v0 + warp; v < v1; v += ZERO_WARPS) {
+            if (bits[(v - v0) >> 5] >> ((v - v0) & 31) & 1u)
+                continue;
+            char* row = reinterpret_cast<char*>(a.table + (int64_t)v * a.table_ld);
+            for (int64_t o = 0; o < a.D * 4; o += ZERO_BYTES) {
+                const unsigned len = (unsigned)(a.D * 4 - o < ZERO_BYTES ? a.D * 4 - o : ZERO_BYTES);
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                             :: "l"(row + o), "r"(src), "r"(len) : "memory");
+            }
+        }
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+}
+
+// until this thread's copies have read shared memory and written their rows
+__device__ __forceinline__ void zero_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// zeroes the table rows in [v0, v1) that no token names
 __device__ void zero_rows(const SortArgs& a, unsigned* bits, int v0, int v1)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     const int words = (v1 - v0 + 31) / 32;
     for (int i = tid; i < words; i += SORT_NT)
         bits[i] = 0u;
@@ -314,39 +333,8 @@ __device__ void zero_rows(const SortArgs& a, unsigned* bits, int v0, int v1)
                 atomicOr(&bits[(t[u] - v0) >> 5], 1u << ((t[u] - v0) & 31));
     }
     __syncthreads();
-    if (a.vec) {
-        // rows on 16 bytes: bulk copies of a zeroed piece of shared memory, one instruction a
-        // row (268 MB at 6.2 TB/s, as plain stores from all threads).  Leaving part of this
-        // to the sums' kernel made the call longer: 84 -> 94 us with 96 MB written here, 89 with 140.
-        float4* zero = reinterpret_cast<float4*>(bits + ((words + 31) & ~31));
-        for (int i = tid; i < ZERO_BYTES / 16; i += SORT_NT)
-            zero[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncthreads();
-        const unsigned src = (unsigned)__cvta_generic_to_shared(zero);
-        if (warp < ZERO_WARPS && lane == 0) {
-            for (int v = v0 + warp; v < v1; v += ZERO_WARPS) {
-                if (bits[(v - v0) >> 5] >> ((v - v0) & 31) & 1u)
-                    continue;
-                char* row = reinterpret_cast<char*>(a.table + (int64_t)v * a.table_ld);
-                for (int64_t o = 0; o < a.D * 4; o += ZERO_BYTES) {
-                    const unsigned len = (unsigned)(a.D * 4 - o < ZERO_BYTES ? a.D * 4 - o : ZERO_BYTES);
-                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
-                                 :: "l"(row + o), "r"(src), "r"(len) : "memory");
-                }
-            }
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // shared memory is read until then
-        }
-        return;
-    }
-    for (int v = v0 + warp; v < v1; v += SORT_W) {
-        if (bits[(v - v0) >> 5] >> ((v - v0) & 31) & 1u)
-            continue;
-        float* row = a.table + (int64_t)v * a.table_ld;
-        for (int64_t c = lane; c < a.D; c += 32)
-            row[c] = 0.0f;
-    }
+    zero_unnamed(a, bits, reinterpret_cast<float4*>(bits + ((words + 31) & ~31)), v0, v1);
+    zero_wait();
 }
 
 __global__ void __cluster_dims__(SORT_CTAS, 1, 1) __launch_bounds__(SORT_NT, 1)
@@ -363,6 +351,92 @@ k_embed_sort(const SortArgs a)
         if (v0 < v1)
             zero_rows(a, dyn, (int)v0, (int)v1);
     }
+}
+
+// ---------------------------------------------------------------- order of few tokens
+
+constexpr int RANK_NT = 512;
+constexpr int RANK_W = RANK_NT / 32;
+// Up to this many tokens are put in order by counting, alone and beside the zeroing of a
+// table (by counting against by passes, 32768 x 2048, us: added into a gradient 301 tokens
+// 10 and 19, 4096 31 and 36, 8192 51 and 40; into a new one 2048 63 and 63, 4096 70 and 66)
+constexpr int RANKED = 4096, RANKED_NEW = 2048;
+
+// A CTA takes 32 tokens, a lane each, and counts against all n how many are smaller and
+// how many equal, before it and in all; its warps share the n.  That is the token's
+// place, its chunk and its segment's length at once, with nothing to wait for.  Every CTA
+// also has its share of the table rows to zero, which the copy engine does meanwhile.
+__global__ void __launch_bounds__(RANK_NT)
+k_embed_rank(const SortArgs a, int ranks, int per)
+{
+    extern __shared__ __align__(128) unsigned dyn[];
+    __shared__ int sums[RANK_W][3][32];
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x == 0 && tid == 0)
+        a.counts[0] = 0;
+    const int padded = (a.n + 127) & ~127, words = (per + 31) / 32;
+    unsigned* bits = dyn + padded;
+    for (int i = tid; i < padded; i += RANK_NT)   // past the end: larger than every key
+        dyn[i] = i < a.n ? sort_key(a, i, blockIdx.x == 0) : 0xffffffffu;
+    for (int i = tid; i < words; i += RANK_NT)
+        bits[i] = 0u;
+    __syncthreads();
+    const int64_t first = (int64_t)blockIdx.x * per;
+    const int v0 = (int)(first < a.V ? first : a.V), v1 = (int)(first + per < a.V ? first + per : a.V);
+    if (v0 < v1) {
+        for (int i = tid; i < a.n; i += RANK_NT)
+            if ((int)dyn[i] >= v0 && (int)dyn[i] < v1)
+                atomicOr(&bits[((int)dyn[i] - v0) >> 5], 1u << (((int)dyn[i] - v0) & 31));
+        __syncthreads();
+        zero_unnamed(a, bits, reinterpret_cast<float4*>(bits + ((words + 31) & ~31)), v0, v1);
+    }
+    if (blockIdx.x >= ranks) {
+        zero_wait();
+        return;
+    }
+    const int i0 = blockIdx.x * 32, i = i0 + lane;
+    const unsigned own = i < a.n ? dyn[i] : 0u;
+    int less = 0, upto = 0, before = 0;   // smaller; smaller or equal; equal and earlier
+    for (int j = 4 * warp; j < padded; j += 4 * RANK_W) {
+        const uint4 k = *reinterpret_cast<const uint4*>(dyn + j);
+        const unsigned q[4] = {k.x, k.y, k.z, k.w};
+        int l = 0, u = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            l += q[e] < own;
+            u += q[e] <= own;
+        }
+        less += l;
+        upto += u;
+        if (j < i0) {
+            before += u - l;
+        } else if (j < i0 + 32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                before += q[e] == own && j + e < i;
+        }
+    }
+    sums[warp][0][lane] = less;
+    sums[warp][1][lane] = upto;
+    sums[warp][2][lane] = before;
+    __syncthreads();
+    zero_wait();
+    if (warp > 0 || i >= a.n)
+        return;
+    for (int w = 1; w < RANK_W; ++w) {
+        less += sums[w][0][lane];
+        upto += sums[w][1][lane];
+        before += sums[w][2][lane];
+    }
+    const int at = less + before, length = upto - less;
+    int what = NOTHING;
+    if (own < (unsigned)a.V) {
+        what = MIDDLE;
+        if ((before & 63) == 0)
+            what = length > 64 ? 2 * (at >> 6) + (before == 0 ? 1 : 0) : WHOLE;
+    }
+    a.order[at] = make_int4(i, (int)own, what, length);
 }
 
 // ---------------------------------------------------------------- chunk sums
@@ -456,7 +530,7 @@ template <typename TD, bool VEC>
 __global__ void __launch_bounds__(256, ES_CTAS)
 k_embed_sum(const TD* __restrict__ dout, int64_t dout_ld, const int4* __restrict__ order, int n, int span,
             int64_t D, float scale, float* __restrict__ table, int64_t table_ld, bool accumulate,
-            float* __restrict__ parts, int pieces, bool vec_out)
+            float* __restrict__ parts, int pieces, bool vec_out, int4* __restrict__ joins, int* njoins)
 {
     pdl_wait();
     pdl_trigger();
@@ -520,6 +594,8 @@ k_embed_sum(const TD* __restrict__ dout, int64_t dout_ld, const int4* __restrict
                     row = __shfl_sync(ALL, cur.y, k + u);
                     row = over ? -1 : row;
                     done = over;
+                    if (c0 == 0 && !over && slot >= 0 && (slot & 1) && lane == k + u)   // a token's first of several
+                        joins[atomicAdd(njoins, 1)] = make_int4(at + k + u, (cur.w + 63) / 64, row, 0);
 #pragma unroll
                     for (int g = 0; g < ES_G; ++g)
 #pragma unroll
@@ -639,7 +715,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
     s.b = reinterpret_cast<uint2*>(p + w.b);
     s.seg = reinterpret_cast<int2*>(p + w.seg);
     s.order = reinterpret_cast<int4*>(p + w.order);
-    s.joins = reinterpret_cast<int4*>(p + w.joins);
+    int4* joins = reinterpret_cast<int4*>(p + w.joins);   // {first sorted index, chunks, token, 0}
     s.counts = reinterpret_cast<int*>(p + w.counts);
     s.table = a.table;
     s.table_ld = a.table_ld;
@@ -649,21 +725,30 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
     s.passes = 1;
     while (((int64_t)1 << (8 * s.passes)) <= a.V)   // keys 0 .. V
         ++s.passes;
-    const int fill = a.accumulate ? 0 : fill_ctas();
+    const bool ranked = a.n <= (a.accumulate ? RANKED : RANKED_NEW);
+    // zeroing: beside the cluster, or a share for every CTA, two per SM
+    const int ranks = (int)((a.n + 31) / 32);
+    const int fill = a.accumulate ? 0 : ranked ? 2 * num_sms() : fill_ctas();
     const int per = fill > 0 ? (int)((a.V + fill - 1) / fill) : 0;
-    size_t smem = sizeof(SortSmem);
-    const size_t fill_smem = (size_t)(per + 31) / 32 * 4 + 128 + ZERO_BYTES;   // a bitmap and the zeros
-    if (fill_smem > smem)
-        smem = fill_smem;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)smem);
-        if (e != cudaSuccess)
-            return e;
-    }
-    k_embed_sort<<<SORT_CTAS + fill, SORT_NT, smem, st>>>(s);
-    count_launches(1);
-    cudaError_t e = cudaGetLastError();
+    const size_t fill_smem = fill > 0 ? (size_t)(per + 31) / 32 * 4 + 128 + ZERO_BYTES : 0;   // a bitmap and the zeros
+    const size_t smem = ranked ? (size_t)((a.n + 127) & ~127LL) * 4 + fill_smem
+                               : fill_smem > sizeof(SortSmem) ? fill_smem : sizeof(SortSmem);
+    const int ctas = ranks > fill ? ranks : fill;
+    auto first = [&](auto kernel, auto launch) {
+        if (smem > 40 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess)
+                return e;
+        }
+        launch();
+        count_launches(1);
+        return cudaGetLastError();
+    };
+    cudaError_t e = cudaSuccess;
+    if (!ranked)
+        e = first(k_embed_sort, [&] { k_embed_sort<<<SORT_CTAS + fill, SORT_NT, smem, st>>>(s); });
+    else if (ctas > 0)
+        e = first(k_embed_rank, [&] { k_embed_rank<<<ctas, RANK_NT, smem, st>>>(s, ranks, per); });
     if (e != cudaSuccess || a.n == 0)
         return e;
     float* parts = reinterpret_cast<float*>(p + w.parts);
@@ -678,7 +763,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
         auto go = [&](auto kernel) {
             return launch_pdl(kernel, dim3(grid), dim3(256), 0, st, static_cast<const T*>(a.dout), a.dout_ld,
                               (const int4*)s.order, (int)a.n, span, a.D, a.scale, a.table, a.table_ld,
-                              a.accumulate, parts, pieces, vec_out);
+                              a.accumulate, parts, pieces, vec_out, joins, s.counts);
         };
         return a.D % 4 == 0 && rows4<T>(a.dout, a.dout_ld) ? go(k_embed_sum<T, true>) : go(k_embed_sum<T, false>);
     };
@@ -689,7 +774,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
     RowTree t = {};
     t.parts[0] = parts;
     t.pitch = (a.D + 3) & ~3LL;
-    t.joins = s.joins;
+    t.joins = joins;
     t.njoins = s.counts;
     t.D = a.D;
     t.out[0] = a.table;
