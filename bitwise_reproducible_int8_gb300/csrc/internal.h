@@ -196,6 +196,7 @@ struct QkArgs {
     int64_t n, D, R;
     bool interleaved, accumulate;
     float inv;           // 1 / D where D is a power of two, else 0
+    int w;               // elements loaded at a time (set by the launchers)
     int* err;
 };
 cudaError_t launch_qk_fwd(const QkArgs& a, cudaStream_t st);

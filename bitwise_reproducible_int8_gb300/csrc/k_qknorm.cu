@@ -8,9 +8,9 @@
 // One read and one write of the heads (and the gradient): bound by HBM, and close
 // behind by the instructions issued.  A head lies in the registers of 8, 16 or 32
 // lanes, so the norm's order (groups of 4, then the pairwise tree) is a chain in a
-// lane and an exchange over lanes, and no shared memory stands between the load
-// and the store.  Two rows a lane share the exchanges and the root and division of
-// the norm; the arithmetic is on packed pairs.  16,384 tokens of 16 + 4 heads of 128,
+// lane, an exchange over lanes and a few sums in a lane; only partners that lie in
+// other lanes pass through shared memory.  Two rows a lane share the exchanges and the
+// root and division of the norm; the arithmetic is on packed pairs.  16,384 tokens of 16 + 4 heads of 128,
 // fp32: forward 52.7 us, 6.4 TB/s (0.96 of a copy's); backward with gains 88.5 us, 5.7 TB/s
 // (0.85; 5 us of it the gains' tree).  With 4 elements a lane, a row at a time, these were
 // 108 and 213 us: 265 warp instructions a row in the forward, now 101.
@@ -27,52 +27,76 @@ namespace {
 
 typedef unsigned long long u64;
 
-// How a rotation partner is found, and what a lane holds.  SPLIT: heads of 64, 128 or
-// 256 elements turned whole, by halves: a lane holds 4 elements of each half, both
-// members of its pairs and one set of cosines and sines for them.  Otherwise a lane
-// holds E consecutive elements: INTER, neighbour pairs (or no turn): in the lane;
-// HALF, by halves, R / 2 a multiple of E: at a fixed lane distance; GENERIC, anything
-// else, and rows off 4-element boundaries: through shared memory.
+// How a rotation partner is found.  SPLIT: heads of 64, 128, 256 or 512 elements turned
+// whole, by halves: both members of a pair lie in one lane, with one set of cosines and
+// sines for them.  INTER: neighbour pairs (or no turn): in the lane.  HALF: by halves,
+// R / 2 a multiple of 4: groups of 4 through shared memory.  GENERIC: any other R by
+// halves, and rows off 4-element boundaries: single elements through shared memory.
 constexpr int INTER = 0, HALF = 1, GENERIC = 2, SPLIT = 3;
 
+// First element of group g of 4 in lane l of a head's LPH: neighbouring lanes hold
+// neighbouring groups, so a load of 16 bytes a lane takes whole lines.  (With E
+// consecutive elements in a lane each of its loads took half or a quarter of every
+// sector: 321 us against 126 for 16 + 4 heads
+// of 512, 8,192 tokens.)
+template <int LPH> __device__ __forceinline__ int group(int l, int g) { return 4 * (l + g * LPH); }
 
-// first element of group g of 4 in this lane: l is the lane's place in the head
-template <int E, int MODE> __device__ __forceinline__ int group(int l, int g, int D)
+// two neighbours on a two-element boundary
+__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p)
 {
-    return MODE == SPLIT ? 4 * l + (g ? D >> 1 : 0) : E * l + 4 * g;
+    const unsigned v = *reinterpret_cast<const unsigned*>(p);
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ void store2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b)
+{
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
 }
 
-// the head's values in this lane (0 past the width)
-template <typename T, int E, int MODE, bool VEC>
-__device__ __forceinline__ void load_head(const T* p, int l, int D, float (&x)[E])
+// the head's values in this lane (0 past the width), w elements at a time: 4, or in GENERIC
+// 4, 2 or 1, whatever width, strides and start allow
+template <typename T, int E, int LPH, int MODE>
+__device__ __forceinline__ void load_head(const T* p, int l, int D, int w, float (&x)[E])
 {
 #pragma unroll
     for (int g = 0; g < E / 4; ++g) {
-        const int d = group<E, MODE>(l, g, D);
-        if (VEC) {
+        const int d = group<LPH>(l, g);
+        if (MODE != GENERIC || w == 4) {
             if (MODE == SPLIT || d < D) {
                 const float4 v = stream4(p + d);
                 x[4 * g] = v.x, x[4 * g + 1] = v.y, x[4 * g + 2] = v.z, x[4 * g + 3] = v.w;
-            } else {
-                x[4 * g] = x[4 * g + 1] = x[4 * g + 2] = x[4 * g + 3] = 0.0f;
             }
+        } else if (w == 2) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)
+                if (d + e < D) {
+                    const float2 v = load2(p + d + e);
+                    x[4 * g + e] = v.x, x[4 * g + e + 1] = v.y;
+                }
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                x[4 * g + e] = d + e < D ? to_f32<T>(p[d + e]) : 0.0f;
+                if (d + e < D)
+                    x[4 * g + e] = to_f32<T>(p[d + e]);
         }
     }
 }
 
-template <typename T, int E, int MODE, bool VEC>
-__device__ __forceinline__ void store_head(T* p, int l, int D, const float (&x)[E])
+template <typename T, int E, int LPH, int MODE>
+__device__ __forceinline__ void store_head(T* p, int l, int D, int w, const float (&x)[E])
 {
 #pragma unroll
     for (int g = 0; g < E / 4; ++g) {
-        const int d = group<E, MODE>(l, g, D);
-        if (VEC) {
+        const int d = group<LPH>(l, g);
+        if (MODE != GENERIC || w == 4) {
             if (MODE == SPLIT || d < D)
                 store4(p + d, make_float4(x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]));
+        } else if (w == 2) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)
+                if (d + e < D)
+                    store2(p + d + e, x[4 * g + e], x[4 * g + e + 1]);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -82,50 +106,37 @@ __device__ __forceinline__ void store_head(T* p, int l, int D, const float (&x)[
     }
 }
 
-// In-lane part of S of the terms a_e (x) b_e: groups of 4 left to right, then the
-// pairwise tree over the lane's groups (SPLIT: the two halves' groups stay apart
-// until the lanes are done).  A term past the width counts as -0, which leaves
-// every sum as it is.
-template <int E, int MODE>
+// In-lane part of S of the terms a_e (x) b_e: each group of 4 left to right.  A term
+// past the width counts as -0, which leaves every sum as it is.
+template <int E, int LPH, int MODE>
 __device__ __forceinline__ void lane_sum(const u64 (&a)[E / 2], const u64 (&b)[E / 2], int l, int D, float* out)
 {
-    float g[E / 4];
 #pragma unroll
     for (int k = 0; k < E / 4; ++k) {
         float p[4];
         unpack2(fmul2_rn(a[2 * k], b[2 * k]), p[0], p[1]);
         unpack2(fmul2_rn(a[2 * k + 1], b[2 * k + 1]), p[2], p[3]);
-        const int d = group<E, MODE>(l, k, D);
+        const int d = group<LPH>(l, k);
         if (MODE == GENERIC) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 p[e] = d + e < D ? p[e] : -0.0f;
         }
-        g[k] = fadd_ftz(fadd_ftz(fadd_ftz(p[0], p[1]), p[2]), p[3]);
+        out[k] = fadd_ftz(fadd_ftz(fadd_ftz(p[0], p[1]), p[2]), p[3]);
         if (MODE == INTER || MODE == HALF)
-            g[k] = d < D ? g[k] : -0.0f;
+            out[k] = d < D ? out[k] : -0.0f;
     }
-    if (MODE == SPLIT) {
-        out[0] = g[0];
-        out[1] = g[E / 4 - 1];
-        return;
-    }
-#pragma unroll
-    for (int s = 1; s < E / 4; s *= 2)
-#pragma unroll
-        for (int k = 0; k + s < E / 4; k += 2 * s)
-            g[k] = fadd_ftz(g[k], g[k + s]);
-    out[0] = g[0];
 }
 
-// The tree over the LPH lanes of U rows at once.  At the first levels a lane keeps
-// half of the sums it still has and hands its partner the others, so 4 sums take 6
-// exchanges instead of 20, and every row's sum ends up in lanes of its own:
-// lane_of<U, MODE>(u) holds row u.  SPLIT has two sums a row, a half each, joined last.
-template <int U, int LPH, int MODE> __device__ __forceinline__ float rows_tree(const float* S, int lane)
+// The pairwise tree over the groups of U rows at once, G sums a row in a lane: over the
+// lanes first, then over a row's sums, as the groups' order has it.  At the first levels
+// a lane keeps half of the sums it still has and hands its partner the others, so 4 sums
+// take 6 exchanges instead of 20, and every row's sum ends up in lanes of its own:
+// lane_of<U>(u) holds row u.
+template <int U, int LPH, int G> __device__ __forceinline__ float rows_tree(const float* S, int lane)
 {
     constexpr unsigned ALL = 0xffffffffu;
-    constexpr int N = MODE == SPLIT ? 2 * U : U;
+    constexpr int N = U * G;
     float v;
     int s = 1;
     if (N == 4) {
@@ -144,12 +155,15 @@ template <int U, int LPH, int MODE> __device__ __forceinline__ float rows_tree(c
 #pragma unroll
     for (; s < LPH; s *= 2)
         v = fadd_ftz(v, __shfl_xor_sync(ALL, v, s));
-    if (MODE == SPLIT)   // rows in lane bit 0, halves in bit 1
+    static_assert(G == 1 || N == 4, "sum 2 b0 + b1 is in lanes with bits b0 and b1");
+    if (G >= 2)
         v = fadd_ftz(v, __shfl_xor_sync(ALL, v, 2));
+    if (G == 4)
+        v = fadd_ftz(v, __shfl_xor_sync(ALL, v, 1));
     return v;
 }
 
-template <int U, int MODE> __device__ __forceinline__ int lane_of(int u)
+template <int U> __device__ __forceinline__ int lane_of(int u)
 {
     return U == 4 ? (u >> 1) | ((u & 1) << 1) : u;
 }
@@ -168,61 +182,66 @@ __device__ __forceinline__ float rnorm(float S, float width, float inv, float ep
 // the turn of a position for this lane's elements: out_e = v_e c_e + w_e s_e, w_e the
 // other member of the pair, s_e with its sign (BACK: the turn undone).  SPLIT: of the
 // lower half's elements; the upper half's s is the negative.
-template <int E, int MODE, bool BACK>
+template <int E, int LPH, int MODE, bool BACK>
 __device__ __forceinline__ void load_turn(u64 (&c)[E / 2], u64 (&s)[E / 2], const float* __restrict__ cs, int l,
-                                          int D, int R, bool inter)
+                                          int R, bool inter)
 {
     const int half = R >> 1;
     const u64 z = pack2(-0.0f, -0.0f);
-    if (MODE == HALF || MODE == SPLIT) {
-        const int d0 = E * l;
-        if (MODE == SPLIT || d0 < R) {
-            const bool low = MODE == SPLIT || d0 < half;
-            const int j0 = MODE == SPLIT ? 4 * l : low ? d0 : d0 - half;
-            const bool minus = low != BACK;
 #pragma unroll
-            for (int g = 0; g < (MODE == SPLIT ? 4 : E); g += 4) {
-                const float4 a = __ldg(reinterpret_cast<const float4*>(cs + j0 + g));
-                const float4 b = __ldg(reinterpret_cast<const float4*>(cs + half + j0 + g));
-                c[g / 2] = fadd2_ftz(pack2(a.x, a.y), z);
-                c[g / 2 + 1] = fadd2_ftz(pack2(a.z, a.w), z);
-                s[g / 2] = fadd2_ftz(minus ? pack2(-b.x, -b.y) : pack2(b.x, b.y), z);
-                s[g / 2 + 1] = fadd2_ftz(minus ? pack2(-b.z, -b.w) : pack2(b.z, b.w), z);
-            }
+    for (int g = 0; g < (MODE == SPLIT ? E / 8 : E / 4); ++g) {
+        const int d = group<LPH>(l, g);
+        if (MODE == SPLIT || (MODE == HALF && d < R)) {
+            const bool low = MODE == SPLIT || d < half, minus = low != BACK;
+            const int j = low ? d : d - half;
+            const float4 a = __ldg(reinterpret_cast<const float4*>(cs + j));
+            const float4 b = __ldg(reinterpret_cast<const float4*>(cs + half + j));
+            c[2 * g] = fadd2_ftz(pack2(a.x, a.y), z);
+            c[2 * g + 1] = fadd2_ftz(pack2(a.z, a.w), z);
+            s[2 * g] = fadd2_ftz(minus ? pack2(-b.x, -b.y) : pack2(b.x, b.y), z);
+            s[2 * g + 1] = fadd2_ftz(minus ? pack2(-b.z, -b.w) : pack2(b.z, b.w), z);
             if (MODE == SPLIT) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    s[E / 4 + i] = fmul2_rn(s[i], pack2(-1.0f, -1.0f));
+                s[E / 4 + 2 * g] = fmul2_rn(s[2 * g], pack2(-1.0f, -1.0f));
+                s[E / 4 + 2 * g + 1] = fmul2_rn(s[2 * g + 1], pack2(-1.0f, -1.0f));
             }
         }
-    } else {
+        if (MODE == INTER) {
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            float cc[2] = {0.0f, 0.0f}, ss[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int d = E * l + e + i;
-                if (d < R) {
-                    const bool pairs = MODE == INTER || inter;
-                    const bool low = pairs ? !(d & 1) : d < half;
-                    const int j = pairs ? d >> 1 : (low ? d : d - half);
-                    cc[i] = __ldg(cs + j);
-                    ss[i] = __ldg(cs + half + j);
-                    ss[i] = low != BACK ? -ss[i] : ss[i];
+            for (int i = 0; i < 2; ++i)
+                if (d + 2 * i < R) {
+                    const float a = __ldg(cs + d / 2 + i), b = __ldg(cs + half + d / 2 + i);
+                    c[2 * g + i] = fadd2_ftz(pack2(a, a), z);
+                    s[2 * g + i] = fadd2_ftz(BACK ? pack2(b, -b) : pack2(-b, b), z);
                 }
+        }
+        if (MODE == GENERIC) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                float cc[2] = {0.0f, 0.0f}, ss[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int k = d + e + i;
+                    if (k < R) {
+                        const bool low = inter ? i == 0 : k < half;
+                        const int j = inter ? k >> 1 : (low ? k : k - half);
+                        cc[i] = __ldg(cs + j);
+                        ss[i] = __ldg(cs + half + j);
+                        ss[i] = low != BACK ? -ss[i] : ss[i];
+                    }
+                }
+                c[2 * g + e / 2] = fadd2_ftz(pack2(cc[0], cc[1]), z);
+                s[2 * g + e / 2] = fadd2_ftz(pack2(ss[0], ss[1]), z);
             }
-            c[e / 2] = fadd2_ftz(pack2(cc[0], cc[1]), z);
-            s[e / 2] = fadd2_ftz(pack2(ss[0], ss[1]), z);
         }
     }
 }
 
 // v turned in place; elements from R on are left alone
-template <int E, int MODE>
+template <int E, int LPH, int MODE>
 __device__ __forceinline__ void turn(u64 (&v)[E / 2], const u64 (&c)[E / 2], const u64 (&s)[E / 2], int l, int D,
                                      int R, bool inter, float* row)
 {
-    if (MODE == SPLIT) {   // E = 8: pairs 0, 1 of the lower half, 2, 3 of the upper
+    if (MODE == SPLIT) {   // the first half of the lane's pairs is of the lower half
 #pragma unroll
         for (int i = 0; i < E / 4; ++i) {
             const u64 a = v[i], b = v[E / 4 + i];
@@ -231,56 +250,52 @@ __device__ __forceinline__ void turn(u64 (&v)[E / 2], const u64 (&c)[E / 2], con
         }
         return;
     }
-    const int half = R >> 1, d0 = E * l;
-    u64 w[E / 2];
+    const int half = R >> 1;
+    float x[E], y[E];
+#pragma unroll
+    for (int i = 0; i < E; i += 2)
+        unpack2(v[i / 2], x[i], x[i + 1]);
     if (MODE == INTER) {
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            float a, b;
-            unpack2(v[i], a, b);
-            w[i] = pack2(b, a);
-        }
+        for (int i = 0; i < E; ++i)
+            y[i] = x[i ^ 1];
     } else if (MODE == HALF) {
-        const int lane = threadIdx.x & 31, step = half / E;
-        const int other = d0 < half ? lane + step : d0 < R ? lane - step : lane;
-#pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-            float a, b;
-            unpack2(v[i], a, b);
-            w[i] = pack2(__shfl_sync(0xffffffffu, a, other), __shfl_sync(0xffffffffu, b, other));
-        }
-    } else {
-        float x[E], y[E];
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < E; i += 2)
-            unpack2(v[i / 2], x[i], x[i + 1]);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (d0 + e < D)
-                row[d0 + e] = x[e];
+        for (int g = 0; g < E / 4; ++g) {
+            const int d = group<LPH>(l, g);
+            if (d < R)
+                *reinterpret_cast<float4*>(row + d) = make_float4(x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]);
+        }
         __syncwarp();
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int d = d0 + e;
-            y[e] = d < R ? row[inter ? d ^ 1 : d < half ? d + half : d - half] : 0.0f;
+        for (int g = 0; g < E / 4; ++g) {
+            const int d = group<LPH>(l, g);
+            float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (d < R)
+                w = *reinterpret_cast<const float4*>(row + (d < half ? d + half : d - half));
+            y[4 * g] = w.x, y[4 * g + 1] = w.y, y[4 * g + 2] = w.z, y[4 * g + 3] = w.w;
         }
+    } else {   // element d at (d mod 4) E LPH / 4 + d / 4: lanes side by side at any distance
+        constexpr unsigned Q = E * LPH / 4;
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < E; i += 2)
-            w[i / 2] = pack2(y[i], y[i + 1]);
+        for (int i = 0; i < E; ++i)
+            if (group<LPH>(l, i / 4) + i % 4 < R)
+                row[i % 4 * Q + l + i / 4 * LPH] = x[i];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int d = group<LPH>(l, i / 4) + i % 4;
+            const unsigned o = inter ? d ^ 1 : d < half ? d + half : d - half;
+            y[i] = d < R ? row[o % 4 * Q + o / 4] : 0.0f;
+        }
     }
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) {
-        const u64 t = fadd2_ftz(fmul2_rn(v[i], c[i]), fmul2_rn(w[i], s[i]));
-        if (MODE == HALF) {   // a lane's elements lie on one side of R
-            if (d0 < R)
-                v[i] = t;
-        } else {
-            float t0, t1, v0, v1;
-            unpack2(t, t0, t1);
-            unpack2(v[i], v0, v1);
-            v[i] = pack2(d0 + 2 * i < R ? t0 : v0, d0 + 2 * i + 1 < R ? t1 : v1);
-        }
+        const int d = group<LPH>(l, i / 2) + i % 2 * 2;
+        const u64 t = fadd2_ftz(fmul2_rn(v[i], c[i]), fmul2_rn(pack2(y[2 * i], y[2 * i + 1]), s[i]));
+        v[i] = d < R ? t : v[i];   // R is even
     }
 }
 
@@ -325,28 +340,28 @@ template <int U> struct Rows {
 };
 
 // a row's values from memory as packed pairs (0 for rows past the end)
-template <typename T, int E, int MODE, bool VEC>
-__device__ __forceinline__ void load_row(const T* p, bool live, int l, int D, u64 (&v)[E / 2])
+template <typename T, int E, int LPH, int MODE>
+__device__ __forceinline__ void load_row(const T* p, bool live, int l, int D, int w, u64 (&v)[E / 2])
 {
     float x[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
         x[e] = 0.0f;
     if (live)
-        load_head<T, E, MODE, VEC>(p, l, D, x);
+        load_head<T, E, LPH, MODE>(p, l, D, w, x);
 #pragma unroll
     for (int i = 0; i < E / 2; ++i)
         v[i] = pack2(x[2 * i], x[2 * i + 1]);
 }
 
-template <typename T, int E, int MODE, bool VEC>
-__device__ __forceinline__ void store_row(T* p, int l, int D, const u64 (&v)[E / 2])
+template <typename T, int E, int LPH, int MODE>
+__device__ __forceinline__ void store_row(T* p, int l, int D, int w, const u64 (&v)[E / 2])
 {
     float x[E];
 #pragma unroll
     for (int i = 0; i < E / 2; ++i)
         unpack2(v[i], x[2 * i], x[2 * i + 1]);
-    store_head<T, E, MODE, VEC>(p, l, D, x);
+    store_head<T, E, LPH, MODE>(p, l, D, w, x);
 }
 
 template <int N> __device__ __forceinline__ void mul_flush(u64 (&v)[N], const u64 (&w)[N])
@@ -374,12 +389,12 @@ template <int N> __device__ __forceinline__ void flush_row(u64 (&v)[N])
 }
 
 // this lane's gains, flushed
-template <int E, int MODE> __device__ __forceinline__ void load_gain(const float* gain, int l, int D, u64 (&g)[E / 2])
+template <int E, int LPH> __device__ __forceinline__ void load_gain(const float* gain, int l, int D, u64 (&g)[E / 2])
 {
     float x[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const int d = group<E, MODE>(l, e / 4, D) + e % 4;
+        const int d = group<LPH>(l, e / 4) + e % 4;
         x[e] = gain && d < D ? __ldg(gain + d) : 0.0f;
     }
 #pragma unroll
@@ -396,12 +411,13 @@ k_qk_fwd(const __grid_constant__ QkArgs a, unsigned blocks_q)
 {
     constexpr int HPW = 32 / LPH;   // heads a warp holds
     constexpr int U = fwd_rows(E);
-    constexpr int N = MODE == SPLIT ? 2 : 1;
-    constexpr bool VEC = MODE != GENERIC;
-    __shared__ float rows[MODE == GENERIC ? 8 * HPW * E * LPH : 1];
+    constexpr int G = E / 4;        // groups of 4 a lane holds of a row
+    constexpr int ROW = MODE == HALF || MODE == GENERIC ? E * LPH + (HPW > 1 ? LPH : 0) : 0;   // of a head, shared
+    __shared__ __align__(16) float rows[ROW ? 8 * HPW * ROW : 4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int D = (int)a.D, R = (int)a.R, l = lane % LPH, sub = lane / LPH;
-    float* srow = rows + (MODE == GENERIC ? (warp * HPW + sub) * E * LPH : 0);
+    float* srow = rows + (warp * HPW + sub) * ROW;
+    const int dense = D % 4 == 0 ? 4 : D % 2 == 0 ? 2 : 1;   // of rows without gaps
     const bool is_q = blockIdx.x < blocks_q;
     const QkTensor& t = is_q ? a.t[0] : a.t[1];
     const unsigned block = is_q ? blockIdx.x : blockIdx.x - blocks_q;
@@ -412,31 +428,31 @@ k_qk_fwd(const __grid_constant__ QkArgs a, unsigned blocks_q)
     u64 x[U][E / 2];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        load_row<T, E, MODE, VEC>(static_cast<const T*>(t.x) + at.at[u], at.live[u], l, D, x[u]);
+        load_row<T, E, LPH, MODE>(static_cast<const T*>(t.x) + at.at[u], at.live[u], l, D, a.w, x[u]);
     if (__ballot_sync(0xffffffffu, at.live[0]) == 0)
         return;
     u64 c[E / 2] = {}, s[E / 2] = {}, g[E / 2];
     bool ok;
     const float* cs = rope_row(a, at.live[0] ? at.tok[0] : 0u, at.live[0] && l == 0, ok);
-    load_turn<E, MODE, false>(c, s, cs, l, D, R, a.interleaved);
-    load_gain<E, MODE>(t.gain, l, D, g);
-    float S[N * U];
+    load_turn<E, LPH, MODE, false>(c, s, cs, l, R, a.interleaved);
+    load_gain<E, LPH>(t.gain, l, D, g);
+    float S[G * U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         flush_row(x[u]);
-        lane_sum<E, MODE>(x[u], x[u], l, D, S + N * u);
+        lane_sum<E, LPH, MODE>(x[u], x[u], l, D, S + G * u);
     }
-    const float r = rnorm(rows_tree<U, LPH, MODE>(S, lane), (float)D, a.inv, flush(a.eps));
+    const float r = rnorm(rows_tree<U, LPH, G>(S, lane), (float)D, a.inv, flush(a.eps));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        mul_flush(x[u], __shfl_sync(0xffffffffu, r, lane_of<U, MODE>(u), LPH));
+        mul_flush(x[u], __shfl_sync(0xffffffffu, r, lane_of<U>(u), LPH));
         if (t.gain)
             mul_flush(x[u], g);
         if (u > 0 && at.turned[u] && at.live[u]) {
             cs = rope_row(a, at.tok[u], l == 0, ok);
-            load_turn<E, MODE, false>(c, s, cs, l, D, R, a.interleaved);
+            load_turn<E, LPH, MODE, false>(c, s, cs, l, R, a.interleaved);
         }
-        turn<E, MODE>(x[u], c, s, l, D, R, a.interleaved, srow);
+        turn<E, LPH, MODE>(x[u], c, s, l, D, R, a.interleaved, srow);
         if (!ok) {
 #pragma unroll
             for (int i = 0; i < E / 2; ++i)
@@ -444,10 +460,7 @@ k_qk_fwd(const __grid_constant__ QkArgs a, unsigned blocks_q)
         }
         if (at.live[u]) {
             float* o = t.out + (int64_t)(row0 + u) * D;
-            if (VEC || D % 4 == 0)
-                store_row<float, E, MODE, true>(o, l, D, x[u]);
-            else
-                store_row<float, E, MODE, false>(o, l, D, x[u]);
+            store_row<float, E, LPH, MODE>(o, l, D, dense, x[u]);
         }
     }
 }
@@ -461,14 +474,15 @@ k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict_
 {
     constexpr int HPW = 32 / LPH;
     constexpr int U = bwd_rows(E, LPH);
-    constexpr int N = MODE == SPLIT ? 2 : 1;
+    constexpr int G = E / 4;        // groups of 4 a lane holds of a row
     constexpr int PER = CHUNK / (8 * HPW);   // consecutive rows of the chunk per LPH lanes
-    constexpr bool VEC = MODE != GENERIC;
-    __shared__ float rows[MODE == GENERIC ? 8 * HPW * E * LPH : 1];
+    constexpr int ROW = MODE == HALF || MODE == GENERIC ? E * LPH + (HPW > 1 ? LPH : 0) : 0;   // of a head, shared
+    __shared__ __align__(16) float rows[ROW ? 8 * HPW * ROW : 4];
     extern __shared__ float terms[];   // [CHUNK][D] with a gain
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int D = (int)a.D, R = (int)a.R, l = lane % LPH, sub = lane / LPH;
-    float* srow = rows + (MODE == GENERIC ? (warp * HPW + sub) * E * LPH : 0);
+    float* srow = rows + (warp * HPW + sub) * ROW;
+    const int dense = D % 4 == 0 ? 4 : D % 2 == 0 ? 2 : 1;   // of rows without gaps
     const bool is_q = blockIdx.x < chunks_q;
     const QkTensor& t = is_q ? a.t[0] : a.t[1];
     const unsigned chunk = is_q ? blockIdx.x : blockIdx.x - chunks_q;
@@ -477,7 +491,7 @@ k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict_
     const bool gain = t.gain != nullptr;
     pdl_trigger();   // the gains' tree may be launched; it waits for this grid
     u64 g[E / 2];
-    load_gain<E, MODE>(t.gain, l, D, g);
+    load_gain<E, LPH>(t.gain, l, D, g);
 #pragma unroll 1
     for (int k0 = 0; k0 < PER; k0 += U) {
         const unsigned row0 = first + (unsigned)((warp * HPW + sub) * PER + k0);
@@ -488,36 +502,33 @@ k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict_
         u64 x[U][E / 2], dy[U][E / 2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            load_row<T, E, MODE, VEC>(static_cast<const T*>(t.x) + at.at[u], at.live[u], l, D, x[u]);
+            load_row<T, E, LPH, MODE>(static_cast<const T*>(t.x) + at.at[u], at.live[u], l, D, a.w, x[u]);
             const float* p = t.dout + (int64_t)(row0 + u) * D;
-            if (VEC || D % 4 == 0)
-                load_row<float, E, MODE, true>(p, at.live[u], l, D, dy[u]);
-            else
-                load_row<float, E, MODE, false>(p, at.live[u], l, D, dy[u]);
+            load_row<float, E, LPH, MODE>(p, at.live[u], l, D, dense, dy[u]);
         }
         u64 c[E / 2] = {}, s[E / 2] = {};
         bool ok[U];
         const float* cs = rope_row(a, at.live[0] ? at.tok[0] : 0u, at.live[0] && l == 0, ok[0]);
-        load_turn<E, MODE, true>(c, s, cs, l, D, R, a.interleaved);
-        float S[N * U];
+        load_turn<E, LPH, MODE, true>(c, s, cs, l, R, a.interleaved);
+        float S[G * U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             flush_row(x[u]);
-            lane_sum<E, MODE>(x[u], x[u], l, D, S + N * u);
+            lane_sum<E, LPH, MODE>(x[u], x[u], l, D, S + G * u);
         }
-        const float r = rnorm(rows_tree<U, LPH, MODE>(S, lane), width, a.inv, eps);
+        const float r = rnorm(rows_tree<U, LPH, G>(S, lane), width, a.inv, eps);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (u > 0) {
                 ok[u] = ok[u - 1];
                 if (at.turned[u] && at.live[u]) {
                     cs = rope_row(a, at.tok[u], l == 0, ok[u]);
-                    load_turn<E, MODE, true>(c, s, cs, l, D, R, a.interleaved);
+                    load_turn<E, LPH, MODE, true>(c, s, cs, l, R, a.interleaved);
                 }
             }
             flush_row(dy[u]);
-            turn<E, MODE>(dy[u], c, s, l, D, R, a.interleaved, srow);
-            mul_flush(x[u], __shfl_sync(0xffffffffu, r, lane_of<U, MODE>(u), LPH));   // h
+            turn<E, LPH, MODE>(dy[u], c, s, l, D, R, a.interleaved, srow);
+            mul_flush(x[u], __shfl_sync(0xffffffffu, r, lane_of<U>(u), LPH));   // h
             if (gain) {
                 u64 p[E / 2];
 #pragma unroll
@@ -531,20 +542,17 @@ k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict_
                 }
                 if (at.live[u]) {
                     float* o = terms + (row0 + u - first) * D;
-                    if (VEC || D % 4 == 0)
-                        store_row<float, E, MODE, true>(o, l, D, p);
-                    else
-                        store_row<float, E, MODE, false>(o, l, D, p);
+                    store_row<float, E, LPH, MODE>(o, l, D, dense, p);
                 }
                 mul_flush(dy[u], g);
             }
-            lane_sum<E, MODE>(dy[u], x[u], l, D, S + N * u);
+            lane_sum<E, LPH, MODE>(dy[u], x[u], l, D, S + G * u);
         }
-        const float c1 = over_width(rows_tree<U, LPH, MODE>(S, lane), width, a.inv);
+        const float c1 = over_width(rows_tree<U, LPH, G>(S, lane), width, a.inv);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float ru = __shfl_sync(0xffffffffu, r, lane_of<U, MODE>(u), LPH);
-            const float cu = __shfl_sync(0xffffffffu, c1, lane_of<U, MODE>(u), LPH);
+            const float ru = __shfl_sync(0xffffffffu, r, lane_of<U>(u), LPH);
+            const float cu = __shfl_sync(0xffffffffu, c1, lane_of<U>(u), LPH);
             const u64 nc = pack2(-cu, -cu);
 #pragma unroll
             for (int i = 0; i < E / 2; ++i)
@@ -561,7 +569,7 @@ k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict_
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (to.live[u])
-                store_row<T, E, MODE, VEC>(static_cast<T*>(t.dx) + to.at[u], l, D, x[u]);
+                store_row<T, E, LPH, MODE>(static_cast<T*>(t.dx) + to.at[u], l, D, a.w, x[u]);
     }
     if (gain) {
         __syncthreads();
@@ -578,23 +586,33 @@ k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict_
 
 unsigned chunks_of(int64_t rows) { return (unsigned)((rows + CHUNK - 1) / CHUNK); }
 
-// how partners are found, given everything that is loaded four at a time
-template <typename T> int mode_of(const QkArgs& a, int E, bool back)
+// elements that may be loaded and stored at a time: 4, 2 or 1
+template <typename T> int width_of(const QkArgs& a, bool back)
 {
-    bool vec = a.D % 4 == 0;
-    for (const QkTensor& t : a.t)
-        if (t.H > 0) {
-            vec = vec && rows4<T>(t.x, t.ld) && t.hs % 4 == 0;
-            if (back)
-                vec = vec && rows4<T>(t.dx, t.dx_ld) && t.dx_hs % 4 == 0;
-        }
-    if (!vec)
+    auto whole = [&](int64_t w) {
+        bool ok = a.D % w == 0;
+        for (const QkTensor& t : a.t)
+            if (t.H > 0) {
+                ok = ok && reinterpret_cast<uintptr_t>(t.x) % (w * sizeof(T)) == 0 && t.ld % w == 0 && t.hs % w == 0;
+                if (back)
+                    ok = ok && reinterpret_cast<uintptr_t>(t.dx) % (w * sizeof(T)) == 0 && t.dx_ld % w == 0 &&
+                         t.dx_hs % w == 0;
+            }
+        return ok;
+    };
+    return whole(4) ? 4 : whole(2) ? 2 : 1;
+}
+
+// how partners are found
+int mode_of(const QkArgs& a, int E, int LPH)
+{
+    if (a.w != 4)
         return GENERIC;
     if (a.interleaved || a.R == 0)
         return INTER;
-    if (a.R == a.D && (a.D == 64 || a.D == 128 || a.D == 256))
+    if (E >= 8 && a.R == a.D && a.D == E * LPH)
         return SPLIT;
-    return (a.R / 2) % E == 0 ? HALF : GENERIC;
+    return a.R % 8 == 0 ? HALF : GENERIC;
 }
 
 // calls f(E, LPH) as compile-time constants for the head width
@@ -611,35 +629,37 @@ template <typename F> cudaError_t by_width(int64_t D, F f)
     return f(std::integral_constant<int, 16>(), std::integral_constant<int, 32>());
 }
 
-template <typename T> cudaError_t fwd_typed(const QkArgs& a, cudaStream_t st)
+template <typename T> cudaError_t fwd_typed(QkArgs a, cudaStream_t st)
 {
+    a.w = width_of<T>(a, false);
     return by_width(a.D, [&](auto e, auto l) {
         constexpr int E = decltype(e)::value, LPH = decltype(l)::value;
         constexpr int per = 8 * (32 / LPH) * fwd_rows(E);
         const unsigned bq = (unsigned)((a.n * a.t[0].H + per - 1) / per);
         const unsigned grid = bq + (unsigned)((a.n * a.t[1].H + per - 1) / per);
-        const int m = mode_of<T>(a, E, false);
+        const int m = mode_of(a, E, LPH);
         if (m == INTER)
             k_qk_fwd<T, E, LPH, INTER><<<grid, 256, 0, st>>>(a, bq);
         else if (m == HALF)
             k_qk_fwd<T, E, LPH, HALF><<<grid, 256, 0, st>>>(a, bq);
         else if (m == GENERIC)
             k_qk_fwd<T, E, LPH, GENERIC><<<grid, 256, 0, st>>>(a, bq);
-        else if constexpr (E == 8)
+        else if constexpr (E >= 8)
             k_qk_fwd<T, E, LPH, SPLIT><<<grid, 256, 0, st>>>(a, bq);
         count_launches(1);
         return cudaGetLastError();
     });
 }
 
-template <typename T> cudaError_t bwd_typed(const QkArgs& a, float* parts, int64_t pitch, cudaStream_t st)
+template <typename T> cudaError_t bwd_typed(QkArgs a, float* parts, int64_t pitch, cudaStream_t st)
 {
+    a.w = width_of<T>(a, true);
     return by_width(a.D, [&](auto e, auto l) {
         constexpr int E = decltype(e)::value, LPH = decltype(l)::value;
         const unsigned cq = chunks_of(a.n * a.t[0].H), ck = chunks_of(a.n * a.t[1].H);
         const bool gain = a.t[0].gain || a.t[1].gain;
         const size_t smem = gain ? (size_t)CHUNK * a.D * 4 : 0;
-        const int m = mode_of<T>(a, E, true);
+        const int m = mode_of(a, E, LPH);
         auto go = [&](auto kernel) {
             if (smem > 32 * 1024) {
                 const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -655,7 +675,7 @@ template <typename T> cudaError_t bwd_typed(const QkArgs& a, float* parts, int64
             return go(k_qk_bwd<T, E, LPH, INTER>);
         if (m == HALF)
             return go(k_qk_bwd<T, E, LPH, HALF>);
-        if constexpr (E == 8)
+        if constexpr (E >= 8)
             if (m == SPLIT)
                 return go(k_qk_bwd<T, E, LPH, SPLIT>);
         return go(k_qk_bwd<T, E, LPH, GENERIC>);
