@@ -466,18 +466,21 @@ k_qk_fwd(const __grid_constant__ QkArgs a, unsigned blocks_q)
 }
 
 constexpr int CHUNK = 64;   // rows of a chunk of the gains' canonical sums
-__host__ __device__ constexpr int bwd_rows(int E, int LPH) { return E == 16 ? 1 : 2; }
+__host__ __device__ constexpr int bwd_rows(int E) { return E == 16 ? 1 : 2; }
+// warps of a CTA: the terms of heads past 256 leave room for one CTA or two an SM (16 + 4
+// heads of 512, 8,192 tokens: 262 us with 8 warps, 192 with 16)
+__host__ __device__ constexpr int bwd_warps(int E) { return E == 16 ? 16 : 8; }
 
 template <typename T, int E, int LPH, int MODE>
-__global__ void __launch_bounds__(256, E == 16 ? 2 : 3)
+__global__ void __launch_bounds__(32 * bwd_warps(E), E == 16 ? 1 : 3)
 k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict__ parts, int64_t pitch)
 {
     constexpr int HPW = 32 / LPH;
-    constexpr int U = bwd_rows(E, LPH);
+    constexpr int U = bwd_rows(E), W = bwd_warps(E);
     constexpr int G = E / 4;        // groups of 4 a lane holds of a row
-    constexpr int PER = CHUNK / (8 * HPW);   // consecutive rows of the chunk per LPH lanes
+    constexpr int PER = CHUNK / (W * HPW);   // consecutive rows of the chunk per LPH lanes
     constexpr int ROW = MODE == HALF || MODE == GENERIC ? E * LPH + (HPW > 1 ? LPH : 0) : 0;   // of a head, shared
-    __shared__ __align__(16) float rows[ROW ? 8 * HPW * ROW : 4];
+    __shared__ __align__(16) float rows[ROW ? W * HPW * ROW : 4];
     extern __shared__ float terms[];   // [CHUNK][D] with a gain
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int D = (int)a.D, R = (int)a.R, l = lane % LPH, sub = lane / LPH;
@@ -574,7 +577,7 @@ k_qk_bwd(const __grid_constant__ QkArgs a, unsigned chunks_q, float* __restrict_
     if (gain) {
         __syncthreads();
         const int L = total - first < CHUNK ? (int)(total - first) : CHUNK;
-        for (int d = threadIdx.x; d < D; d += 256) {
+        for (int d = threadIdx.x; d < D; d += 32 * W) {
             float s = terms[d];
 #pragma unroll 8
             for (int k = 1; k < L; ++k)
@@ -667,7 +670,7 @@ template <typename T> cudaError_t bwd_typed(QkArgs a, float* parts, int64_t pitc
                 if (r != cudaSuccess)
                     return r;
             }
-            kernel<<<cq + ck, 256, smem, st>>>(a, cq, parts, pitch);
+            kernel<<<cq + ck, 32 * bwd_warps(E), smem, st>>>(a, cq, parts, pitch);
             count_launches(1);
             return cudaGetLastError();
         };
