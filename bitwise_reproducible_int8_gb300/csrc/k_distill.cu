@@ -367,7 +367,8 @@ __device__ void teacher_row(const T* zr, const FwdArgs& a, int64_t row, Teacher*
             p[k] = 0.0f;
     } else {
         for (int k = lane; k < a.K; k += 32) {
-            const float e = exp_neg(fadd_ftz(teacher(a, row * a.K + k, j), -mt));
+            float e = exp_neg(fadd_ftz(teacher(a, row * a.K + k, j), -mt));
+            e = j >= 0 ? e : 0.0f;   // an empty entry weighs nothing, whatever the maximum is
             lt = fadd_ftz(lt, e);
             p[k] = e;
         }
@@ -375,13 +376,15 @@ __device__ void teacher_row(const T* zr, const FwdArgs& a, int64_t row, Teacher*
         P = a.logprobs ? lt : lt == lt ? 1.0f : lt;
         lt = a.logprobs ? 1.0f : lt;
         for (int k = lane; k < a.K; k += 32) {
+            const float ak = teacher(a, row * a.K + k, j);
+            if (j < 0)   // its +0 stays: over a sum that is no number it would be one no more
+                continue;
             float w = p[k];
             if (!a.logprobs) {
                 w = flush(__fdiv_rn(w, lt));
                 p[k] = w;
             }
             if (w != 0.0f && a.w_kd != 0.0f) {
-                const float ak = teacher(a, row * a.K + k, j);
                 const float u = fmul_flush(flush(to_f32<T>(zr[j])), a.it);
                 sum = sum + (double)w * ((double)ak - (double)u);
                 weight = weight + (double)w;

@@ -1101,6 +1101,9 @@ static float row_sum(const float* z, int64_t V, float it, float tau, float* mx)
     return l;
 }
 
+/* whether entry j names a logit of the row */
+static int in_row(int64_t j, int64_t V) { return j >= 0 && j < V; }
+
 void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx, const float* tl,
                         int64_t K, const int64_t* label, float tau, float w_kd, float w_ce, float w_z,
                         int logprobs, float* loss, float* stats)
@@ -1119,9 +1122,8 @@ void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx
         /* the teacher's weights */
         float mt = -INFINITY, lt = 0.0f, P = 0.0f;
         for (int64_t k = 0; k < K; ++k) {
-            const int64_t j = idx[r * K + k];
             p[k] = -INFINITY;
-            if (j >= 0 && j < V)
+            if (in_row(idx[r * K + k], V))
                 p[k] = logprobs ? oracle_flush(tl[r * K + k]) : oracle_mul(tl[r * K + k], it);
             mt = max_nan(mt, p[k]);
         }
@@ -1136,14 +1138,15 @@ void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx
                 p[k] = 0.0f;
         } else {
             for (int64_t k = 0; k < K; ++k)
-                p[k] = exp_neg(oracle_add(a[k], -mt));
+                p[k] = in_row(idx[r * K + k], V) ? exp_neg(oracle_add(a[k], -mt)) : 0.0f;
             lt = chains_sum(p, K, 32);
             if (logprobs) {
                 P = lt;
                 lt = 1.0f;
             } else {
                 for (int64_t k = 0; k < K; ++k)
-                    p[k] = oracle_div(p[k], lt);
+                    if (in_row(idx[r * K + k], V)) /* an empty entry's weight stays +0 */
+                        p[k] = oracle_div(p[k], lt);
                 P = lt == lt ? 1.0f : lt;
             }
         }
