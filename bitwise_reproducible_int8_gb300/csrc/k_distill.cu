@@ -224,6 +224,17 @@ __device__ __forceinline__ void load_block(const T* p, int len, int lane, float 
     }
 }
 
+// Whether differences from m are taken before they are scaled: m (x) it is infinite although m
+// is not (tau below 1 and a row, block or list masked by the type's lowest value), so that
+// the difference of the products would be a NaN.
+__device__ __forceinline__ bool overflows(float m, float mu)
+{
+    return fabsf(mu) == CUDART_INF_F && fabsf(m) < CUDART_INF_F;
+}
+
+// which sums' products can do that
+template <int SUMS> constexpr bool SCALED = SUMS == SOFT || SUMS == BOTH;
+
 // the tree over a block's 128 chains: this lane's four, in slots i mod 4
 template <bool VEC> __device__ __forceinline__ float chains_tree(u64 a, u64 b)
 {
@@ -306,7 +317,9 @@ __device__ __forceinline__ void do_block(const T* z, int64_t z_ld, const FwdArgs
     block_stats<T, SUMS, VEC>(z + (int64_t)row * z_ld + lo, min(a.V - lo, BLK), lane, pow, a.it, m, s, s1);
     if (lane == 0) {
         const int64_t at = (int64_t)row * a.nblk + blk;
-        a.ms[at] = make_float2(m, s);
+        // where m (x) it overflows the sum is a NaN: +0 under a row's finite maximum, which
+        // such a block adds nothing to; else join_apart forms it again
+        a.ms[at] = make_float2(m, SCALED<SUMS> && fabsf(m) < CUDART_INF_F && s != s ? 0.0f : s);
         if (SUMS >= BOTH)
             a.s1[at] = s1;
     }
@@ -331,7 +344,7 @@ struct RowShared {
     int next;   // block handed out
 };
 
-// a_k of an entry, and its column (-1: empty)
+// t_k of an entry, and its column (-1, and -infinity: empty)
 __device__ __forceinline__ float teacher(const FwdArgs& a, int64_t at, int& j)
 {
     const int64_t c = load_index(a.t_idx, a.index_bytes, at);
@@ -340,10 +353,12 @@ __device__ __forceinline__ float teacher(const FwdArgs& a, int64_t at, int& j)
     j = c < 0 || c >= a.V ? -1 : (int)c;
     if (j < 0)
         return -CUDART_INF_F;
-    const float t = flush(a.t_type == 0 ? static_cast<const float*>(a.t_val)[at]
-                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(a.t_val)[at]));
-    return a.logprobs ? t : fmul_flush(t, a.it);
+    return flush(a.t_type == 0 ? static_cast<const float*>(a.t_val)[at]
+                               : __bfloat162float(static_cast<const __nv_bfloat16*>(a.t_val)[at]));
 }
+
+// a_k from t_k
+__device__ __forceinline__ float weighed(const FwdArgs& a, float t) { return a.logprobs ? t : fmul_flush(t, a.it); }
 
 // What a row's loss needs of the teacher, by one warp: the weights p_k, and in binary64
 // the sums of p_k (a_k - u_k) and of p_k.  None of it waits for the row's blocks:
@@ -358,16 +373,25 @@ __device__ void teacher_row(const T* zr, const FwdArgs& a, int64_t row, Teacher*
     int j;
     if (!a.logprobs) {
         for (int k = lane; k < a.K; k += 32)
-            mt = max_nan(mt, teacher(a, row * a.K + k, j));
+            mt = max_nan(mt, weighed(a, teacher(a, row * a.K + k, j)));
         mt = warp_max(mt);
         mt = mt == 0.0f ? 0.0f : mt;
     }
-    if (mt == -CUDART_INF_F) {
+    float most = 0.0f;   // the largest t_k, where its product by it may have overflowed
+    if (fabsf(mt) == CUDART_INF_F) {
+        most = -CUDART_INF_F;
+        for (int k = lane; k < a.K; k += 32)
+            most = max_nan(most, teacher(a, row * a.K + k, j));
+        most = warp_max(most);
+    }
+    const bool apart = overflows(most, mt);
+    if (mt == -CUDART_INF_F && !apart) {
         for (int k = lane; k < a.K; k += 32)
             p[k] = 0.0f;
     } else {
         for (int k = lane; k < a.K; k += 32) {
-            float e = exp_neg(fadd_ftz(teacher(a, row * a.K + k, j), -mt));
+            const float t = teacher(a, row * a.K + k, j);
+            float e = exp_neg(apart ? fmul_flush(fadd_ftz(t, -most), a.it) : fadd_ftz(weighed(a, t), -mt));
             e = j >= 0 ? e : 0.0f;   // an empty entry weighs nothing, whatever the maximum is
             lt = fadd_ftz(lt, e);
             p[k] = e;
@@ -376,7 +400,7 @@ __device__ void teacher_row(const T* zr, const FwdArgs& a, int64_t row, Teacher*
         P = a.logprobs ? lt : lt == lt ? 1.0f : lt;
         lt = a.logprobs ? 1.0f : lt;
         for (int k = lane; k < a.K; k += 32) {
-            const float ak = teacher(a, row * a.K + k, j);
+            const float ak = weighed(a, teacher(a, row * a.K + k, j));
             if (j < 0)   // its +0 stays: over a sum that is no number it would be one no more
                 continue;
             float w = p[k];
@@ -406,6 +430,49 @@ __device__ void teacher_row(const T* zr, const FwdArgs& a, int64_t row, Teacher*
         *out = {sum, weight, mt, lt, P, 0.0f};
 }
 
+// A block's sum of e((z_i (-) m) (x) it), for rows whose maximum overflows when scaled: they
+// are rare, so the block is read again (ahead of block_stats's own sums this cost those
+// registers: 8192 x 32768 fp32 at tau 1.5 with labels 278 us instead of 267).  The order is
+// block_stats's for either way of loading.
+template <typename T> __device__ float block_apart(const T* p, int len, float it, float m)
+{
+    const int lane = threadIdx.x & 31;
+    const unsigned pow = lane_pow();
+    u64 s[2] = {dup2(0.0f), dup2(0.0f)};
+#pragma unroll 1
+    for (int i = 0; i < PER; i += 4) {
+        float d[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int e = element<false>(i + c, lane);
+            d[c] = e < len ? fadd_ftz(to_f32<T>(p[e]), -m) : -CUDART_INF_F;
+        }
+        s[0] = add2_plain(s[0], exp_neg2(fmul2_rn(pack2(d[0], d[1]), dup2(it)), pow));
+        s[1] = add2_plain(s[1], exp_neg2(fmul2_rn(pack2(d[2], d[3]), dup2(it)), pow));
+    }
+    return chains_tree<false>(s[0], s[1]);
+}
+
+// lane's chain of the sum over the blocks of such a row, M its maximum (in line 276 us for the
+// bf16 rows of those sizes, out of line 273)
+template <typename T>
+__device__ __noinline__ float join_apart(const T* zr, const float2* ms, int nblk, int V, float it, float M)
+{
+    const int lane = threadIdx.x & 31;
+    float l = 0.0f;
+#pragma unroll 1
+    for (int b = 0; b < nblk; ++b) {
+        const float2 v = ms[b];
+        const float f = exp_neg(fmul_rn(fadd_ftz(v.x, -M), it));
+        float s = v.y;
+        if (f != 0.0f && overflows(v.x, fmul_flush(v.x, it)))
+            s = block_apart<T>(zr + b * BLK, min(V - b * BLK, BLK), it, v.x);
+        if (lane == (b & 31))
+            l = fadd_ftz(l, fmul_rn(s, f));
+    }
+    return l;
+}
+
 // joins the blocks of rows [r0, r0 + cnt) and forms the losses.  A warp per row, but the
 // logarithms: binary64 runs at 1/64 of the binary32 rate here whether one lane needs
 // it or 32, so one warp takes all of the CTA's, a lane each.
@@ -431,6 +498,8 @@ __device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, 
                 if (SUMS >= BOTH)
                     l1 = fadd_ftz(l1, fmul_rn(a.s1[row * a.nblk + b], exp_neg(fadd_ftz(v.x, -M))));
             }
+            if (SCALED<SUMS> && overflows(M, Mu))
+                l = join_apart(z + row * z_ld, ms, a.nblk, a.V, a.it, M);
             l = warp_tree(l);
             l1 = SUMS >= BOTH ? warp_tree(l1) : SUMS == ONE ? l : 0.0f;
         }
@@ -460,7 +529,7 @@ __device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, 
     const double lse_t = none ? 0.0 : (double)fmul_flush(M, a.it) + sh.ln[0][r];
     const double lse1 = none || SUMS == SOFT ? 0.0 : (double)M + sh.ln[1][r];
     double v = 0.0;
-    if (!none && a.w_kd != 0.0f && t.mt != -CUDART_INF_F)
+    if (!none && a.w_kd != 0.0f && t.lt != 0.0f)   // 0: no teacher
         v = ((double)a.w_kd * ((double)a.tau * (double)a.tau)) *
             (t.sum + (lse_t - ((double)t.mt + sh.ln[2][r])) * t.weight);
     if (a.w_ce != 0.0f) {
@@ -655,7 +724,9 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
     const float qa = flush(__fdiv_rn(SUMS == ONE ? fadd_ftz(ca, cb) : ca, l));
     const float qb = SUMS >= BOTH ? flush(__fdiv_rn(cb, l1)) : 0.0f;
     const float Mu = fmul_flush(M, a.it);
-    const u64 zero = dup2(-0.0f), nu = dup2(-Mu), nm = dup2(-M), sc = dup2(a.it), wa = dup2(qa), wb = dup2(qb);
+    const bool apart = SCALED<SUMS> && overflows(M, Mu);
+    const u64 zero = dup2(-0.0f), nu = dup2(apart ? -0.0f : -Mu), nm = dup2(apart ? -0.0f : -M), sc = dup2(a.it),
+              wa = dup2(qa), wb = dup2(qb);
     const int last = min(first + a.per, a.nblk);
     int listed = 0;
     if (M == -CUDART_INF_F) {   // nothing in the row: no gradient
@@ -675,6 +746,11 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
             load_piece<T, LINES>(zr, lo, a.V, lane, x);
         if (blk + 1 < last)
             fetch_ahead(zr + lo + BBLK, min(a.V - lo - BBLK, BBLK), lane);
+        if (apart) {
+#pragma unroll
+            for (int i = 0; i < BPER; ++i)
+                x[i] = fadd_ftz(x[i], -M);
+        }
 #pragma unroll
         for (int i = 0; i < BPER; i += 2) {
             const u64 v = pack2(x[i], x[i + 1]);

@@ -445,18 +445,20 @@ size_t repro_qk_norm_rope_bwd_ws_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64
  *   e(x) = 2^t for x <= 0, t = x (x) RN(1 / ln 2): k = rint(32 t), f = t (-) k / 32, the
  *     degree-2 polynomial of 2^f (coefficients in k_distill.cu) in Horner form,
  *     times RN(2^((k mod 32) / 32)) 2^floor(k / 32); 0 where floor(k / 32) < -125;
+ *   d(v, m) = (v (x) it) (-) (m (x) it), or where m (x) it is infinite although m is not
+ *     (tau < 1 and a mask of the type's lowest value), (v (-) m) (x) it;
  *   blocks of REPRO_DISTILL_BLOCK consecutive logits: the block's maximum M_b
- *     (a zero maximum is +0, a NaN stays) and S_b = sum of e(u_j (-) M_b (x) it) in
+ *     (a zero maximum is +0, a NaN stays) and S_b = sum of e(d(z_j, M_b)) in
  *     128 chains (element j of the block in chain j mod 128, ascending from
  *     +0), the chains by the pairwise tree;
- *   M = max M_b; l = sum over blocks of S_b (x) e((M_b (x) it) (-) (M (x) it)) in 32
+ *   M = max M_b; l = sum over blocks of S_b (x) e(d(M_b, M)) in 32
  *     chains (block b in chain b mod 32) and the tree; l1 the same with it = 1, where
  *     for tau = 2 and 4 a block's term is the first one's square, its fourth power;
  *   the teacher's weights p_k over the non-empty entries: a_k = t_k (x) it,
- *     m = max a_k, p_k = e(a_k (-) m) (/) lt, lt the sum of the e(.) in 32 chains and
+ *     m = max a_k, p_k = e(d(t_k, max t)) (/) lt, lt the sum of the e(.) in 32 chains and
  *     the tree, P = 1; with REPRO_DISTILL_LOGPROBS t_k are the teacher's own
  *     log-probabilities: a_k = t_k, p_k = e(a_k), P their sum in that order.  No
- *     entry (or only -infinities): every p_k and P are 0.  The p_k of an empty entry is +0
+ *     entry (or only t_k of -infinity): every p_k and P are 0.  The p_k of an empty entry is +0
  *     whatever the others are; a NaN (or +infinity) among them makes the others' NaN.
  *   loss = w_kd tau^2 sum_k p_k (ln p_k - ln softmax(u)_k) + w_ce (lse(z) - z_label)
  *     + w_z lse(z)^2, its row terms in binary64, unfused, rounded once: the sum over k
@@ -489,7 +491,7 @@ size_t repro_distill_ws_bytes(int64_t n, int64_t V);
  * floats, or g_n = 1: one for every row), from the forward's inputs and stats:
  *   gk = (g (x) w_kd) (x) tau;  a = gk (x) P;  b = g (x) ([label >= 0] w_ce (+) (2 (x) w_z) (x) lse(z))
  *   tau = 1: dz_j = e(u_j (-) M) (x) ((a (+) b) (/) l);
- *   else dz_j = e(u_j (-) M (x) it) (x) (a (/) l), (+) e(z_j (-) M) (x) (b (/) l1) if w_ce or w_z
+ *   else dz_j = e(d(z_j, M)) (x) (a (/) l), (+) e(z_j (-) M) (x) (b (/) l1) if w_ce or w_z
  *     (for tau = 2 and 4 the second e(.) is the first's square, its fourth power);
  *   then, entry by entry in ascending k, dz at t_idx_k (-)= gk (x) p_k (w_kd not 0),
  *   and dz at the label (-)= g (x) w_ce.

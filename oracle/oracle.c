@@ -1056,6 +1056,15 @@ static double chains_sum_d(const double* t, int64_t n, int chains)
     return s[0];
 }
 
+/* x (x) it (-) m (x) it, the argument of e(.); the difference first where m (x) it overflows */
+static float scaled_diff(float x, float m, float it)
+{
+    const float mu = oracle_mul(m, it);
+    if (isinf(mu) && !isinf(m))
+        return oracle_mul(oracle_add(x, -m), it);
+    return oracle_add(oracle_mul(x, it), -mu);
+}
+
 /* the softmax-of-z term e^(z - m) from the softened one where tau is 2 or 4 */
 static float term_power(float e, float tau)
 {
@@ -1077,9 +1086,8 @@ static float row_sum(const float* z, int64_t V, float it, float tau, float* mx)
         for (int64_t j = 0; j < n; ++j)
             M[c] = max_nan(M[c], oracle_flush(z[lo + j]));
         M[c] = M[c] == 0.0f ? 0.0f : M[c]; /* a zero maximum is +0 */
-        const float Mu = oracle_mul(M[c], it);
         for (int64_t j = 0; j < n; ++j)
-            t[j] = exp_neg(oracle_add(oracle_mul(z[lo + j], it), -Mu));
+            t[j] = exp_neg(scaled_diff(z[lo + j], M[c], it));
         if (tau != 0.0f)
             for (int64_t j = 0; j < n; ++j)
                 t[j] = term_power(t[j], tau);
@@ -1093,7 +1101,7 @@ static float row_sum(const float* z, int64_t V, float it, float tau, float* mx)
         it = 1.0f;
     if (m != -INFINITY) {
         for (int64_t c = 0; c < C; ++c)
-            S[c] = oracle_mul(S[c], exp_neg(oracle_add(oracle_mul(M[c], it), -oracle_mul(m, it))));
+            S[c] = oracle_mul(S[c], exp_neg(scaled_diff(M[c], m, it)));
         l = chains_sum(S, C, 32);
     }
     free(S);
@@ -1119,26 +1127,25 @@ void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx
         const float l = row_sum(zr, V, it, 0.0f, &mz);
         const float l1 = power ? row_sum(zr, V, it, tau, &m1) : row_sum(zr, V, 1.0f, 0.0f, &m1);
         const float Mu = oracle_mul(mz, it);
-        /* the teacher's weights */
-        float mt = -INFINITY, lt = 0.0f, P = 0.0f;
+        /* the teacher's weights; t_k, or a_k = t_k (x) it */
+        const float ta = logprobs ? 1.0f : it;
+        float most = -INFINITY, mt, lt = 0.0f, P = 0.0f;
+        float* t = (float*)malloc(sizeof(float) * (size_t)(K + 1));
         for (int64_t k = 0; k < K; ++k) {
-            p[k] = -INFINITY;
-            if (in_row(idx[r * K + k], V))
-                p[k] = logprobs ? oracle_flush(tl[r * K + k]) : oracle_mul(tl[r * K + k], it);
-            mt = max_nan(mt, p[k]);
+            t[k] = in_row(idx[r * K + k], V) ? oracle_flush(tl[r * K + k]) : -INFINITY;
+            most = max_nan(most, t[k]);
         }
-        mt = mt == 0.0f ? 0.0f : mt;
-        float* a = (float*)malloc(sizeof(float) * (size_t)(K + 1));
-        double* term = (double*)malloc(sizeof(double) * (size_t)(K + 1));
-        memcpy(a, p, sizeof(float) * (size_t)K);
         if (logprobs)
-            mt = 0.0f;
-        if (mt == -INFINITY) {
+            most = 0.0f;
+        mt = oracle_mul(most, ta);
+        mt = mt == 0.0f ? 0.0f : mt;
+        double* term = (double*)malloc(sizeof(double) * (size_t)(K + 1));
+        if (most == -INFINITY) {
             for (int64_t k = 0; k < K; ++k)
                 p[k] = 0.0f;
         } else {
             for (int64_t k = 0; k < K; ++k)
-                p[k] = in_row(idx[r * K + k], V) ? exp_neg(oracle_add(a[k], -mt)) : 0.0f;
+                p[k] = in_row(idx[r * K + k], V) ? exp_neg(scaled_diff(t[k], most, ta)) : 0.0f;
             lt = chains_sum(p, K, 32);
             if (logprobs) {
                 P = lt;
@@ -1153,11 +1160,11 @@ void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx
         const double lse_t = (double)Mu + oracle_ln(l), lse1 = (double)mz + oracle_ln(l1);
         double v = 0.0;
         if (mz != -INFINITY) {
-            if (w_kd != 0.0f && mt != -INFINITY) {
+            if (w_kd != 0.0f && most != -INFINITY) {
                 const double cst = lse_t - ((double)mt + oracle_ln(lt));
                 for (int64_t k = 0; k < K; ++k)
                     term[k] = p[k] == 0.0f ? 0.0
-                                           : (double)p[k] * ((double)a[k] - (double)oracle_mul(zr[idx[r * K + k]], it));
+                                           : (double)p[k] * ((double)oracle_mul(t[k], ta) - (double)oracle_mul(zr[idx[r * K + k]], it));
                 const double sum = chains_sum_d(term, K, 32);
                 for (int64_t k = 0; k < K; ++k)
                     term[k] = (double)p[k];
@@ -1178,7 +1185,7 @@ void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx
         st[5] = mt;
         st[6] = lt;
         st[7] = P;
-        free(a);
+        free(t);
         free(term);
     }
 }
@@ -1206,9 +1213,8 @@ void oracle_distill_bwd(const float* z, int64_t n, int64_t V, const int64_t* idx
         const int two = tau != 1.0f && (w_ce != 0.0f || w_z != 0.0f);
         const float ca = tau == 1.0f ? oracle_div(oracle_add(a, b), st[1]) : oracle_div(a, st[1]);
         const float cb = two ? oracle_div(b, st[3]) : 0.0f;
-        const float Mu = oracle_mul(st[0], it);
         for (int64_t j = 0; j < V; ++j) {
-            const float e = exp_neg(oracle_add(oracle_mul(zr[j], it), -Mu));
+            const float e = exp_neg(scaled_diff(zr[j], st[0], it));
             d[j] = oracle_mul(e, ca);
             if (two)
                 d[j] = oracle_add(d[j], oracle_mul(tau == 2.0f || tau == 4.0f ? term_power(e, tau)
