@@ -285,10 +285,11 @@ __device__ __forceinline__ void block_stats(const T* p, int len, int lane, unsig
         s1 = chains_tree<VEC>(a1, b1);
 }
 
-// a row's teacher: the sums of p_k (a_k - u_k) and of p_k, maximum, sum and P
+// a row's teacher: the sums of p_k (a_k - u_k) and of p_k, maximum, sum and P; `ref` not
+// infinite: the first sum is of differences from the maximum and from that logit's u
 struct Teacher {
     double sum, weight;
-    float mt, lt, P, unused;
+    float mt, lt, P, ref;
 };
 
 struct FwdArgs {
@@ -360,9 +361,24 @@ __device__ __forceinline__ float teacher(const FwdArgs& a, int64_t at, int& j)
 // a_k from t_k
 __device__ __forceinline__ float weighed(const FwdArgs& a, float t) { return a.logprobs ? t : fmul_flush(t, a.it); }
 
+// From here on a value is far from zero: binary64 holds its sum with a logarithm no better
+// than to 2^-23, and the loss takes differences first.
+constexpr float FAR = 0x1p30f;
+
+// |v| < FAR (by its bits: a binary64 comparison costs the SM 16 cycles a warp)
+__device__ __forceinline__ bool below_far(double v) { return (__double2hiint(v) & 0x7fffffff) < 0x41d00000; }
+
+// v (x) it for the loss's binary64 terms: in binary64 itself where binary32 overflows
+__device__ __forceinline__ double wide_mul(float v, float it)
+{
+    const float p = fmul_flush(v, it);
+    return overflows(v, p) ? (double)v * (double)it : (double)p;
+}
+
 // What a row's loss needs of the teacher, by one warp: the weights p_k, and in binary64
 // the sums of p_k (a_k - u_k) and of p_k.  None of it waits for the row's blocks:
-//   sum p_k (ln p_k - ln q_k) = sum p_k (a_k - u_k) + (lse(u) - (m + ln lt)) sum p_k.
+//   sum p_k (ln p_k - ln q_k) = sum p_k (a_k - u_k) + (lse(u) - (m + ln lt)) sum p_k,
+// and far from zero sum p_k ((a_k - m) - (u_k - u_ref)) + ((lse(u) - u_ref) - ln lt) sum p_k.
 template <typename T>
 __device__ void teacher_row(const T* zr, const FwdArgs& a, int64_t row, Teacher* out)
 {
@@ -427,7 +443,7 @@ __device__ void teacher_row(const T* zr, const FwdArgs& a, int64_t row, Teacher*
         }
     }
     if (lane == 0)
-        *out = {sum, weight, mt, lt, P, 0.0f};
+        *out = {sum, weight, mt, lt, P, CUDART_INF_F};
 }
 
 // A block's sum of e((z_i (-) m) (x) it), for rows whose maximum overflows when scaled: they
@@ -473,11 +489,45 @@ __device__ __noinline__ float join_apart(const T* zr, const float2* ms, int nblk
     return l;
 }
 
+// A row far from zero (masked by the type's lowest value throughout): its teacher's sum anew, of
+// p_k ((a_k - m) - (u_k - u_ref)), ref the largest logit that has weight.
+template <typename T> __device__ __noinline__ void far_row(const T* zr, const FwdArgs& a, int64_t row, Teacher* out)
+{
+    const int lane = threadIdx.x & 31;
+    const float ta = a.logprobs ? 1.0f : a.it;
+    const float* p = a.stats + row * (STATS + a.K) + STATS;
+    int j;
+    float ref = -CUDART_INF_F, most = a.logprobs ? 0.0f : -CUDART_INF_F;
+    for (int k = lane; k < a.K; k += 32) {
+        const float t = teacher(a, row * a.K + k, j);
+        most = a.logprobs ? most : max_nan(most, t);
+        if (j >= 0 && p[k] != 0.0f)
+            ref = max_nan(ref, flush(to_f32<T>(zr[j])));
+    }
+    ref = warp_max(ref);
+    if (!(fabsf(ref) < CUDART_INF_F))
+        return;
+    const double m = wide_mul(warp_max(most), ta), c = wide_mul(ref, a.it);
+    double sum = 0.0;
+    for (int k = lane; k < a.K; k += 32) {
+        const float t = teacher(a, row * a.K + k, j);
+        if (j >= 0 && p[k] != 0.0f)
+            sum = sum + (double)p[k] * ((wide_mul(t, ta) - m) - (wide_mul(flush(to_f32<T>(zr[j])), a.it) - c));
+    }
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2)
+        sum = sum + __shfl_xor_sync(0xffffffffu, sum, s);
+    if (lane == 0) {
+        out->sum = sum;
+        out->ref = ref;
+    }
+}
+
 // joins the blocks of rows [r0, r0 + cnt) and forms the losses.  A warp per row, but the
 // logarithms: binary64 runs at 1/64 of the binary32 rate here whether one lane needs
 // it or 32, so one warp takes all of the CTA's, a lane each.
 template <typename T, int SUMS>
-__device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, int cnt, const Teacher* teachers,
+__device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, int cnt, Teacher* teachers,
                             RowShared& sh)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -503,6 +553,9 @@ __device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, 
             l = warp_tree(l);
             l1 = SUMS >= BOTH ? warp_tree(l1) : SUMS == ONE ? l : 0.0f;
         }
+        const Teacher* t = teachers + r;
+        if (a.w_kd != 0.0f && t->lt != 0.0f && !(fabsf(t->mt) < FAR && below_far(t->sum)))
+            far_row(z + row * z_ld, a, row, teachers + r);
         if (lane == 0) {
             sh.M[r] = M;
             sh.l[r] = l;
@@ -526,18 +579,24 @@ __device__ void finish_rows(const T* z, int64_t z_ld, const FwdArgs& a, int r0, 
     const float M = sh.M[r];
     const Teacher t = teachers[r];
     const bool none = M == -CUDART_INF_F;
-    const double lse_t = none ? 0.0 : (double)fmul_flush(M, a.it) + sh.ln[0][r];
+    const double Mu = SCALED<SUMS> ? wide_mul(M, a.it) : (double)fmul_flush(M, a.it);
+    const double lse_t = none ? 0.0 : Mu + sh.ln[0][r];
     const double lse1 = none || SUMS == SOFT ? 0.0 : (double)M + sh.ln[1][r];
     double v = 0.0;
-    if (!none && a.w_kd != 0.0f && t.lt != 0.0f)   // 0: no teacher
-        v = ((double)a.w_kd * ((double)a.tau * (double)a.tau)) *
-            (t.sum + (lse_t - ((double)t.mt + sh.ln[2][r])) * t.weight);
+    if (!none && a.w_kd != 0.0f && t.lt != 0.0f) {   // 0: no teacher
+        double rest = lse_t - ((double)t.mt + sh.ln[2][r]);
+        if (t.ref != CUDART_INF_F)
+            rest = ((Mu - wide_mul(t.ref, a.it)) + sh.ln[0][r]) - sh.ln[2][r];
+        v = ((double)a.w_kd * ((double)a.tau * (double)a.tau)) * (t.sum + rest * t.weight);
+    }
     if (a.w_ce != 0.0f) {
         const int64_t lab = load_index(a.labels, a.index_bytes, row);
         if (lab >= a.V)
             atomicOr(a.err, kErrIndexBit);
-        else if (lab >= 0 && !none)
-            v = v + (double)a.w_ce * (lse1 - (double)flush(to_f32<T>(zr[lab])));
+        else if (lab >= 0 && !none) {
+            const double zl = (double)flush(to_f32<T>(zr[lab]));
+            v = v + (double)a.w_ce * (fabsf(M) < FAR ? lse1 - zl : ((double)M - zl) + sh.ln[1][r]);
+        }
     }
     if (a.w_z != 0.0f && !none)
         v = v + (double)a.w_z * (lse1 * lse1);

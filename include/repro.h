@@ -462,8 +462,12 @@ size_t repro_qk_norm_rope_bwd_ws_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64
  *     whatever the others are; a NaN (or +infinity) among them makes the others' NaN.
  *   loss = w_kd tau^2 sum_k p_k (ln p_k - ln softmax(u)_k) + w_ce (lse(z) - z_label)
  *     + w_z lse(z)^2, its row terms in binary64, unfused, rounded once: the sum over k
- *     as sum p_k (a_k - u_k) + (lse(u) - (m + ln lt)) sum p_k, both in 32 chains and the
- *     tree, ln of a sum by its atanh series.
+ *     as sum p_k (a_k - u_k) + ((M (x) it + ln l) - (m + ln lt)) sum p_k, both in 32 chains
+ *     and the tree, ln of a sum by its atanh series.  Rows far from zero (like one that is the
+ *     type's lowest value throughout): where |m| or that first sum is not below 2^30 and
+ *     c, the largest u_k with p_k not 0, is finite, sum p_k ((a_k - m) - (u_k - c)) +
+ *     (((M (x) it - c) + ln l) - ln lt) sum p_k, a product by it that overflows binary32 taken
+ *     in binary64; where |M| is not, (M - z_label) + ln l1.
  * p_k = 0 adds nothing.  A negative label adds no cross entropy.  An index or a
  * label >= V is passed over and sets the error word.  A row with no logit above
  * -infinity has loss 0 and gradient 0.  A NaN among a row's logits makes its

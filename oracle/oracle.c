@@ -1109,6 +1109,13 @@ static float row_sum(const float* z, int64_t V, float it, float tau, float* mx)
     return l;
 }
 
+/* v (x) it for the loss's binary64 terms: in binary64 itself where binary32 overflows */
+static double wide_mul(float v, float it)
+{
+    const float p = oracle_mul(v, it);
+    return isinf(p) && !isinf(v) ? (double)v * (double)it : (double)p;
+}
+
 /* whether entry j names a logit of the row */
 static int in_row(int64_t j, int64_t V) { return j >= 0 && j < V; }
 
@@ -1126,7 +1133,6 @@ void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx
         const int power = tau == 2.0f || tau == 4.0f;
         const float l = row_sum(zr, V, it, 0.0f, &mz);
         const float l1 = power ? row_sum(zr, V, it, tau, &m1) : row_sum(zr, V, 1.0f, 0.0f, &m1);
-        const float Mu = oracle_mul(mz, it);
         /* the teacher's weights; t_k, or a_k = t_k (x) it */
         const float ta = logprobs ? 1.0f : it;
         float most = -INFINITY, mt, lt = 0.0f, P = 0.0f;
@@ -1157,21 +1163,38 @@ void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx
                 P = lt == lt ? 1.0f : lt;
             }
         }
-        const double lse_t = (double)Mu + oracle_ln(l), lse1 = (double)mz + oracle_ln(l1);
+        const double Mu = wide_mul(mz, it), ln_l = oracle_ln(l), ln_l1 = oracle_ln(l1);
+        const double lse_t = Mu + ln_l, lse1 = (double)mz + ln_l1;
         double v = 0.0;
         if (mz != -INFINITY) {
             if (w_kd != 0.0f && most != -INFINITY) {
-                const double cst = lse_t - ((double)mt + oracle_ln(lt));
-                for (int64_t k = 0; k < K; ++k)
-                    term[k] = p[k] == 0.0f ? 0.0
-                                           : (double)p[k] * ((double)oracle_mul(t[k], ta) - (double)oracle_mul(zr[idx[r * K + k]], it));
-                const double sum = chains_sum_d(term, K, 32);
+                float ref = -INFINITY; /* the largest logit that has weight */
+                for (int64_t k = 0; k < K; ++k) {
+                    term[k] = 0.0;
+                    if (p[k] != 0.0f) {
+                        const float zk = oracle_flush(zr[idx[r * K + k]]);
+                        term[k] = (double)p[k] * ((double)oracle_mul(t[k], ta) - (double)oracle_mul(zk, it));
+                        ref = max_nan(ref, zk);
+                    }
+                }
+                double sum = chains_sum_d(term, K, 32), rest = lse_t - ((double)mt + oracle_ln(lt));
+                if (isfinite(ref) && !(fabsf(mt) < 0x1p30f && fabs(sum) < 0x1p30)) {
+                    /* far from zero: differences from the largest on both sides */
+                    for (int64_t k = 0; k < K; ++k)
+                        if (p[k] != 0.0f)
+                            term[k] = (double)p[k] * ((wide_mul(t[k], ta) - wide_mul(most, ta)) -
+                                                      (wide_mul(zr[idx[r * K + k]], it) - wide_mul(ref, it)));
+                    sum = chains_sum_d(term, K, 32);
+                    rest = ((Mu - wide_mul(ref, it)) + ln_l) - oracle_ln(lt);
+                }
                 for (int64_t k = 0; k < K; ++k)
                     term[k] = (double)p[k];
-                v = ((double)w_kd * ((double)tau * (double)tau)) * (sum + cst * chains_sum_d(term, K, 32));
+                v = ((double)w_kd * ((double)tau * (double)tau)) * (sum + rest * chains_sum_d(term, K, 32));
             }
-            if (w_ce != 0.0f && label[r] >= 0 && label[r] < V)
-                v = v + (double)w_ce * (lse1 - (double)oracle_flush(zr[label[r]]));
+            if (w_ce != 0.0f && in_row(label[r], V)) {
+                const double zl = (double)oracle_flush(zr[label[r]]);
+                v = v + (double)w_ce * (fabsf(mz) < 0x1p30f ? lse1 - zl : ((double)mz - zl) + ln_l1);
+            }
             if (w_z != 0.0f)
                 v = v + (double)w_z * (lse1 * lse1);
         }

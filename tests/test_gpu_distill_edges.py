@@ -8,7 +8,8 @@ torch = pytest.importorskip("torch")
 import bitwise_reproducible_int8_gb300 as R  # noqa: E402
 from gpu_helpers import dev  # noqa: E402
 from test_gpu_blocks import BF, bf, run_distill, same  # noqa: E402
-from test_oracle_distill_edges import MIXES, both, masked_rows, nonfinite_teachers, overflowing_rows  # noqa: E402
+from test_oracle_blocks import case  # noqa: E402
+from test_oracle_distill_edges import LOWEST, MIXES, both, far_rows, masked_rows, nonfinite_teachers, overflowing_rows  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +59,28 @@ def test_lowest_value_masks(orc, tau, mix, copies, wide):
 def test_overflowing_products(orc, tau, mix, copies, wide):
     (z, tl), _, idx, lab = overflowing_rows()
     check(orc, z, idx, tl, lab, 0, copies, wide, tau=tau, **mix)
+
+
+@pytest.mark.parametrize("tau", [0.01, 0.5, 0.9, 1.0, 1.5, 2.0, 4.0])
+@pytest.mark.parametrize("mix", [dict(), dict(w_kd=0.0, w_ce=1.0), dict(w_kd=0.7, w_ce=0.3)])
+@pytest.mark.parametrize("copies,wide", [(1, True), (1, False), (250, True)])
+def test_loss_of_rows_far_from_zero(orc, tau, mix, copies, wide):
+    (z, tl), _, idx, lab = far_rows()
+    loss, _, dz = check(orc, z, idx, tl, lab, 0, copies, wide, tau=tau, **mix)
+    if wide:                                   # (bf16 has -infinity for the lowest value)
+        assert np.isfinite(loss).all() and np.isfinite(dz).all()
+
+
+def test_loss_of_masked_row_with_logprobs(orc):
+    (z, _), (_, tl), idx, lab = far_rows()
+    check(orc, z, idx, (tl - 12).astype(np.float32), lab, logprobs=True)
+
+
+@pytest.mark.parametrize("tau", [0.5, 1.0, 2.0])
+def test_loss_of_infinite_columns(orc, tau):
+    z, idx, tl, lab = case(15, 4, 300, 40)
+    idx[:] = np.arange(40) + 1
+    tl[:] = 0.0
+    z[0, 2], z[1, 1:41], z[2, 2], z[3, 1:41] = -np.inf, -np.inf, LOWEST, LOWEST
+    loss, _, _ = check(orc, z, idx, tl, lab, tau=tau)
+    assert np.all(loss[:2] == np.inf)

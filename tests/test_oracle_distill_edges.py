@@ -112,3 +112,63 @@ def test_overflowing_products(orc, tau, mix):
     assert np.array_equal(s[:, [1, 3]], es[:, [1, 3]])                       # the sums
     assert np.array_equal(s[:, orc.DISTILL_STATS:], es[:, orc.DISTILL_STATS:])
     assert np.isfinite(dz).all() and np.array_equal(dz, ez)
+
+
+def far_rows():
+    """(rows, the same moved to zero): logits and teacher values so far from zero that 64 bits
+    cannot hold their sums with a logarithm.  Softmax depends on differences, so each pair has
+    one loss; the differences here are exact."""
+    V, K = 2100, 6
+    z, idx, tl, lab = case(14, 7, V, K)
+    idx[:] = np.arange(K) * 301
+    idx[1::2, 2] = -1
+    lab[:] = 2 * 301
+    tl = np.round(tl * 4).astype(np.float32)
+    plain_z, plain_t = z.copy(), tl.copy()
+    z[0], plain_z[0] = LOWEST, 0                # a row that its mask leaves nothing of
+    z[1], plain_z[1] = -(2.0 - 2.0 ** -7) * 2.0 ** 127, 0
+    plain_z[2] = np.where(np.arange(V) % 301 == 0, 2.0 ** 20, 0) - 2.0 ** 20
+    z[2] = plain_z[2] + 2.0 ** 40
+    tl[3], plain_t[3] = LOWEST, 0               # a teacher that its mask leaves nothing of
+    tl[4], plain_t[4] = 2.0 ** 100, 0
+    z[4], plain_z[4] = 2.0 ** 100, 0
+    z[5], plain_z[5] = LOWEST, 0
+    tl[5], plain_t[5] = LOWEST, 0
+    return (z, tl), (plain_z, plain_t), idx, lab
+
+
+@pytest.mark.parametrize("tau", [0.01, 0.5, 0.9, 1.0, 1.5, 2.0, 4.0])
+@pytest.mark.parametrize("mix", [dict(), dict(w_kd=0.0, w_ce=1.0), dict(w_kd=0.7, w_ce=0.3)])
+def test_loss_of_rows_far_from_zero(orc, tau, mix):
+    """A row masked by the lowest value throughout is uniform: its cross entropy is ln V."""
+    (z, tl), (plain_z, plain_t), idx, lab = far_rows()
+    loss, _, dz = both(orc, z, idx, tl, lab, tau=tau, **mix)
+    el, bound, ez, zb = F.distill_rows(plain_z, idx, plain_t, lab, **{**FULL, "tau": tau, **mix})
+    assert np.all(np.abs(loss - el) <= bound)
+    assert np.all(np.abs(dz - ez) <= zb)
+
+
+def test_loss_of_masked_row_with_logprobs(orc):
+    (z, tl), (plain_z, plain_t), idx, lab = far_rows()
+    lp = (plain_t - 12).astype(np.float32)
+    loss = both(orc, z, idx, lp, lab, logprobs=True)[0]
+    el, bound, _, _ = F.distill_rows(plain_z, idx, lp, lab, **{**FULL, "logprobs": True})
+    assert np.all(np.abs(loss - el) <= bound)
+
+
+def test_loss_of_infinite_columns(orc):
+    """Teacher weight on a masked logit costs without end; a mask that is large and finite costs
+    its weight."""
+    z, idx, tl, lab = case(15, 4, 300, 3)
+    idx[:] = (1, 2, 3)
+    tl[:] = 0.0
+    z[0, 2] = -np.inf
+    z[1, 1:4] = -np.inf
+    z[2, 2] = LOWEST
+    z[3, 1:4] = LOWEST
+    for tau in (0.5, 1.0, 2.0):
+        loss = both(orc, z, idx, tl, lab, tau=tau)[0]
+        assert np.all(loss[:2] == np.inf)
+        exp = tau * np.float64(-LOWEST) * np.float64([1 / 3, 1])
+        rows = 2 if tau < 1 else 1                          # (the other's loss is past binary32)
+        assert np.all(np.abs(loss[2:2 + rows] / exp[:rows] - 1) < 4 * F.U)
