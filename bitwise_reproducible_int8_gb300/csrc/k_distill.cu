@@ -777,7 +777,7 @@ k_distill_bwd(const T* z, int64_t z_ld, T* dz, int64_t dz_ld, const __grid_const
         p1 = col1 >= 0 ? st[STATS + lane + 32] : 0.0f;
     }
     const float gk = fmul_flush(fmul_flush(g, a.w_kd), a.tau);
-    const float ca = fmul_flush(gk, P);
+    const float ca = a.w_kd != 0.0f ? fmul_flush(gk, P) : gk;   // P may be a NaN that no one asked for
     const float cb = fmul_flush(g, fadd_ftz(lab >= 0 ? a.w_ce : 0.0f,
                                             fmul_rn(fmul_flush(2.0f, a.w_z), a.w_z != 0.0f ? lse1 : 0.0f)));
     const float qa = flush(__fdiv_rn(SUMS == ONE ? fadd_ftz(ca, cb) : ca, l));

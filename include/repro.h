@@ -493,7 +493,8 @@ size_t repro_distill_ws_bytes(int64_t n, int64_t V);
 
 /* The logits' gradient for upstream gradients g of the row losses (g_n = n
  * floats, or g_n = 1: one for every row), from the forward's inputs and stats:
- *   gk = (g (x) w_kd) (x) tau;  a = gk (x) P;  b = g (x) ([label >= 0] w_ce (+) (2 (x) w_z) (x) lse(z))
+ *   gk = (g (x) w_kd) (x) tau;  a = gk (x) P, or gk where w_kd is 0 (what the teacher holds does
+ *     not matter then);  b = g (x) ([label >= 0] w_ce (+) (2 (x) w_z) (x) lse(z))
  *   tau = 1: dz_j = e(u_j (-) M) (x) ((a (+) b) (/) l);
  *   else dz_j = e(d(z_j, M)) (x) (a (/) l), (+) e(z_j (-) M) (x) (b (/) l1) if w_ce or w_z
  *     (for tau = 2 and 4 the second e(.) is the first's square, its fourth power);

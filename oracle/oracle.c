@@ -1230,7 +1230,7 @@ void oracle_distill_bwd(const float* z, int64_t n, int64_t V, const int64_t* idx
         const float gr = g[r * g_stride];
         const int lab = w_ce != 0.0f && label[r] >= 0 && label[r] < V;
         const float gk = oracle_mul(oracle_mul(gr, w_kd), tau);
-        const float a = oracle_mul(gk, st[7]);
+        const float a = w_kd != 0.0f ? oracle_mul(gk, st[7]) : gk;
         const float b = oracle_mul(gr, oracle_add(lab ? w_ce : 0.0f,
                                                   oracle_mul(oracle_mul(2.0f, w_z), w_z != 0.0f ? st[4] : 0.0f)));
         const int two = tau != 1.0f && (w_ce != 0.0f || w_z != 0.0f);

@@ -84,3 +84,15 @@ def test_loss_of_infinite_columns(orc, tau):
     z[0, 2], z[1, 1:41], z[2, 2], z[3, 1:41] = -np.inf, -np.inf, LOWEST, LOWEST
     loss, _, _ = check(orc, z, idx, tl, lab, tau=tau)
     assert np.all(loss[:2] == np.inf)
+
+
+@pytest.mark.parametrize("tau", [1.0, 1.5, 2.0])
+@pytest.mark.parametrize("K", [5, 80])
+@pytest.mark.parametrize("wide", [True, False])
+def test_teacher_without_weight_is_not_looked_at(orc, tau, K, wide):
+    z, idx, tl, lab = case(16, 4, 300, K)
+    idx[:, 0] = 7
+    lab[:] = (3, -1, 7, 299)
+    tl[0, 0], tl[1, 0], tl[2, 0] = np.nan, np.inf, -np.inf
+    loss, _, dz = check(orc, z, idx, tl, lab, wide=wide, tau=tau, w_kd=0.0, w_ce=1.0)
+    assert np.isfinite(loss).all() and np.isfinite(dz).all()

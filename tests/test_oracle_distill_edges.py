@@ -172,3 +172,19 @@ def test_loss_of_infinite_columns(orc):
         exp = tau * np.float64(-LOWEST) * np.float64([1 / 3, 1])
         rows = 2 if tau < 1 else 1                          # (the other's loss is past binary32)
         assert np.all(np.abs(loss[2:2 + rows] / exp[:rows] - 1) < 4 * F.U)
+
+
+@pytest.mark.parametrize("tau", [1.0, 1.5, 2.0])
+def test_teacher_without_weight_is_not_looked_at(orc, tau):
+    """w_kd 0: whatever the teacher's values are, loss and gradient are those of an ordinary one."""
+    z, idx, tl, lab = case(16, 4, 300, 5)
+    idx[:, 0] = 7
+    lab[:] = (3, -1, 7, 299)
+    bad = tl.copy()
+    bad[0, 0], bad[1, 0], bad[2, 0] = np.nan, np.inf, -np.inf
+    for g in (1.0, -0.5):
+        hp = dict(tau=tau, w_kd=0.0, w_ce=1.0)
+        got, exp = (orc.distill_fwd(z, idx, t, lab, **hp) for t in (bad, tl))
+        assert np.array_equal(got[0], exp[0]) and np.isfinite(got[0]).all()
+        got, exp = (orc.distill_bwd(z, idx, s, np.float32([g]), lab, **hp) for s in (got[1], exp[1]))
+        assert np.isfinite(got).all() and np.array_equal(got.view(np.uint32), exp.view(np.uint32))
