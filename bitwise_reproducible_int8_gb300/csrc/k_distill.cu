@@ -407,7 +407,9 @@ __device__ void teacher_row(const T* zr, const FwdArgs& a, int64_t row, Teacher*
     } else {
         for (int k = lane; k < a.K; k += 32) {
             const float t = teacher(a, row * a.K + k, j);
-            float e = exp_neg(apart ? fmul_flush(fadd_ftz(t, -most), a.it) : fadd_ftz(weighed(a, t), -mt));
+            const float x = apart ? fmul_flush(fadd_ftz(t, -most), a.it) : fadd_ftz(weighed(a, t), -mt);
+            // a log-probability may be anything the caller has; e(.) has no powers from 2^128 on
+            float e = x > 88.0f ? CUDART_INF_F : exp_neg(x);
             e = j >= 0 ? e : 0.0f;   // an empty entry weighs nothing, whatever the maximum is
             lt = fadd_ftz(lt, e);
             p[k] = e;

@@ -457,9 +457,10 @@ size_t repro_qk_norm_rope_bwd_ws_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64
  *   the teacher's weights p_k over the non-empty entries: a_k = t_k (x) it,
  *     m = max a_k, p_k = e(d(t_k, max t)) (/) lt, lt the sum of the e(.) in 32 chains and
  *     the tree, P = 1; with REPRO_DISTILL_LOGPROBS t_k are the teacher's own
- *     log-probabilities: a_k = t_k, p_k = e(a_k), P their sum in that order.  No
- *     entry (or only t_k of -infinity): every p_k and P are 0.  The p_k of an empty entry is +0
- *     whatever the others are; a NaN (or +infinity) among them makes the others' NaN.
+ *     log-probabilities (at most 0, up to their rounding): a_k = t_k, p_k = e(a_k), +infinity
+ *     where a_k > 88, P their sum in that order.  No entry (or only t_k of -infinity): every
+ *     p_k and P are 0.  The p_k of an empty entry is +0 whatever the others are; a NaN (or, of
+ *     logits, +infinity) among them makes the others' NaN.
  *   loss = w_kd tau^2 sum_k p_k (ln p_k - ln softmax(u)_k) + w_ce (lse(z) - z_label)
  *     + w_z lse(z)^2, its row terms in binary64, unfused, rounded once: the sum over k
  *     as sum p_k (a_k - u_k) + ((M (x) it + ln l) - (m + ln lt)) sum p_k, both in 32 chains

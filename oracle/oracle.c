@@ -1150,8 +1150,10 @@ void oracle_distill_fwd(const float* z, int64_t n, int64_t V, const int64_t* idx
             for (int64_t k = 0; k < K; ++k)
                 p[k] = 0.0f;
         } else {
-            for (int64_t k = 0; k < K; ++k)
-                p[k] = in_row(idx[r * K + k], V) ? exp_neg(scaled_diff(t[k], most, ta)) : 0.0f;
+            for (int64_t k = 0; k < K; ++k) {
+                const float x = scaled_diff(t[k], most, ta);
+                p[k] = !in_row(idx[r * K + k], V) ? 0.0f : x > 88.0f ? INFINITY : exp_neg(x);
+            }
             lt = chains_sum(p, K, 32);
             if (logprobs) {
                 P = lt;

@@ -9,7 +9,8 @@ import bitwise_reproducible_int8_gb300 as R  # noqa: E402
 from gpu_helpers import dev  # noqa: E402
 from test_gpu_blocks import BF, bf, run_distill, same  # noqa: E402
 from test_oracle_blocks import case  # noqa: E402
-from test_oracle_distill_edges import LOWEST, MIXES, both, far_rows, masked_rows, nonfinite_teachers, overflowing_rows  # noqa: E402
+from test_oracle_distill_edges import (LOWEST, MIXES, both, far_rows, masked_rows, nonfinite_teachers,  # noqa: E402
+                                       overflowing_rows, positive_logprobs)
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +97,9 @@ def test_teacher_without_weight_is_not_looked_at(orc, tau, K, wide):
     tl[0, 0], tl[1, 0], tl[2, 0] = np.nan, np.inf, -np.inf
     loss, _, dz = check(orc, z, idx, tl, lab, wide=wide, tau=tau, w_kd=0.0, w_ce=1.0)
     assert np.isfinite(loss).all() and np.isfinite(dz).all()
+
+
+@pytest.mark.parametrize("copies,wide", [(1, True), (1, False), (500, True)])
+@pytest.mark.parametrize("tau", [1.0, 2.0])
+def test_logprobs_above_zero(orc, copies, wide, tau):
+    check(orc, *positive_logprobs(), 0, copies, wide, tau=tau, logprobs=True)

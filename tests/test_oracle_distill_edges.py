@@ -188,3 +188,26 @@ def test_teacher_without_weight_is_not_looked_at(orc, tau):
         assert np.array_equal(got[0], exp[0]) and np.isfinite(got[0]).all()
         got, exp = (orc.distill_bwd(z, idx, s, np.float32([g]), lab, **hp) for s in (got[1], exp[1]))
         assert np.isfinite(got).all() and np.array_equal(got.view(np.uint32), exp.view(np.uint32))
+
+
+def positive_logprobs():
+    """Values that are no log-probabilities: one a row, beside ordinary ones."""
+    big = [0.0, 1e-6, 0.02, 20.0, 88.0, 88.5, 89.5, 100.0, 1e4, 1e30, np.inf]
+    z, idx, tl, lab = case(17, len(big), 300, 4)
+    idx[:] = (5, 60, 7, 8)
+    tl = (tl - 9).astype(np.float32)
+    tl[:, 1] = big
+    return z, idx, tl, lab
+
+
+def test_logprobs_above_zero(orc):
+    """Rounding may leave a log-probability above 0; from 88 on the weight is infinite instead of
+    some number that binary32 exponents wrap around to."""
+    z, idx, tl, lab = positive_logprobs()
+    loss, stats, dz = both(orc, z, idx, tl, lab, logprobs=True)
+    p = stats[:, orc.DISTILL_STATS + 1]
+    exp = np.exp(tl[:5, 1].astype(np.float64))
+    assert np.all(np.abs(p[:5] / exp - 1) <= (2 * tl[:5, 1] + 5) * F.U)   # t's two roundings, e's four
+    assert np.all(p[5:] == np.inf) and np.all(stats[5:, 7] == np.inf)
+    assert np.isfinite(loss[:4]).all() and not np.isfinite(loss[5:]).any()
+    assert not np.isfinite(dz[5:]).all(1).any()
