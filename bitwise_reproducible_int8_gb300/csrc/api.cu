@@ -1056,6 +1056,12 @@ static size_t head_span(int64_t n, int64_t ld, int64_t hs, int64_t H, int64_t D,
     return n > 0 && H > 0 ? (size_t)((n - 1) * ld + (H - 1) * hs + D) * type_bytes(type) : 0;
 }
 
+// whether n tokens of H strided heads lie apart: token after token, or head after head
+static bool heads_apart(int64_t n, int64_t ld, int64_t hs, int64_t H, int64_t D)
+{
+    return n <= 1 || H < 1 || ld >= (H - 1) * hs + D || (ld >= D && hs >= (n - 1) * ld + D);
+}
+
 // debug mode: the scan of n tokens of H strided heads, head by head
 static int scan_heads(void* stream, const void* p, int type, int64_t n, int64_t ld, int64_t hs, int64_t H, int64_t D)
 {
@@ -1161,6 +1167,8 @@ int repro_qk_norm_rope_bwd(const float* dq_out, const float* dk_out, const void*
         return REPRO_ERR_WORKSPACE;
     if (need > 0 && !al16(ws))
         return REPRO_ERR_ALIGN;
+    if (!heads_apart(n, dq_ld, dq_hs, Hq, D) || !heads_apart(n, dk_ld, dk_hs, Hkv, D))
+        return REPRO_ERR_ALIAS;
     // dq and dk may lie between one another, as in the gradient of the fused output; each is
     // checked against everything else, and they must not share a row range head by head
     const Span sq = {dq, head_span(n, dq_ld, dq_hs, Hq, D, type)}, sk = {dk, head_span(n, dk_ld, dk_hs, Hkv, D, type)};

@@ -1,0 +1,30 @@
+"""More refusals and admissions of the embedding, the per-head norm with rotation and the
+distillation loss, through the C ABI on invented addresses: nothing is launched."""
+import pytest
+
+from bitwise_reproducible_int8_gb300 import repro
+from test_boundary_blocks import B, BAD, QK, L, call  # noqa: F401
+
+
+@pytest.fixture
+def qk_bwd(L):  # noqa: F811
+    """The head norm's backward of 20 tokens of 16 and 4 heads of 64, some arguments replaced."""
+    need = repro.repro_qk_norm_rope_bwd_ws_bytes(20, 16, 4, 64)
+    ok = dict(dq_out=5 * B, dk_out=6 * B, **dict(QK, gain_q=7 * B, gain_k=8 * B), dq=9 * B, dq_ld=1024, dq_hs=64,
+              dk=10 * B, dk_ld=256, dk_hs=64, dgain_q=11 * B, dgain_k=12 * B, ws=13 * B, ws_bytes=need, stream=None)
+    return lambda **kw: call(L.repro_qk_norm_rope_bwd, ok, **kw)
+
+
+def test_gradients_over_themselves(qk_bwd):
+    """Strides that put two heads or tokens of dq (dk) in one place are refused: the writes race."""
+    f = qk_bwd
+    for kw in (dict(dq_ld=64), dict(dq_ld=1023), dict(dk_ld=255), dict(dq_ld=1), dict(dq_hs=128),
+               dict(dk_hs=20 * 64 - 1, dk_ld=64), dict(dk_hs=20 * 64, dk_ld=63),
+               dict(Hkv=1, dk_ld=63), dict(dq_hs=65, dq_ld=1024 + 14)):
+        assert f(**kw) == -8, kw
+    # token after token, head after head, with room between; a single token's or head's other stride
+    for kw in (dict(dq_hs=65, dq_ld=1024 + 15), dict(dq_hs=20 * 64, dq_ld=64), dict(dk_hs=20 * 70, dk_ld=70),
+               dict(Hkv=1, dk_ld=64), dict(n=1, dq_ld=1, dk_ld=3)):
+        assert f(**kw) not in BAD, kw
+    # inputs may share what they like
+    assert f(q_ld=64, k_ld=1) not in BAD
