@@ -1062,6 +1062,17 @@ static bool heads_apart(int64_t n, int64_t ld, int64_t hs, int64_t H, int64_t D)
     return n <= 1 || H < 1 || ld >= (H - 1) * hs + D || (ld >= D && hs >= (n - 1) * ld + D);
 }
 
+// whether two such tensors, the second's first element `off` past the first's, take different
+// parts of slots at one stride: every position of either is that of its first element modulo it
+static bool heads_side_by_side(int64_t n, int64_t ld, int64_t ld2, int64_t hs, int64_t hs2, int64_t off, int64_t D)
+{
+    if (hs != hs2 || (n > 1 && ld != ld2))
+        return false;
+    const int64_t slot = n > 1 && ld < hs ? ld : hs;
+    const int64_t at = ((off % slot) + slot) % slot;
+    return hs % slot == 0 && (n <= 1 || ld % slot == 0) && at >= D && at + D <= slot;
+}
+
 // debug mode: the scan of n tokens of H strided heads, head by head
 static int scan_heads(void* stream, const void* p, int type, int64_t n, int64_t ld, int64_t hs, int64_t H, int64_t D)
 {
@@ -1184,12 +1195,12 @@ int repro_qk_norm_rope_bwd(const float* dq_out, const float* dk_out, const void*
     if (any_overlap({dg[0], dg[1], wss}, {sq, sk}))
         return REPRO_ERR_ALIAS;
     if (overlap(sq.p, sq.bytes, sk.p, sk.bytes)) {
-        // interleaved in one buffer: allowed when the token strides agree and a token's
-        // heads of q and k are disjoint
+        // interleaved in one buffer: allowed when the token strides agree and a token's heads of
+        // q and k are disjoint, or q and k of each head lie side by side at equal strides
         const int64_t off = ((const char*)dk - (const char*)dq) / (int64_t)b;
         const int64_t wq = (Hq - 1) * dq_hs + D, wk = (Hkv - 1) * dk_hs + D;
         const bool ok = dq_ld == dk_ld && (off >= 0 ? off >= wq && off + wk <= dq_ld : -off >= wk && -off + wq <= dq_ld);
-        if (!ok)
+        if (!ok && !heads_side_by_side(n, dq_ld, dk_ld, dq_hs, dk_hs, off, D))
             return REPRO_ERR_ALIAS;
     }
     st = check_arch();

@@ -425,7 +425,8 @@ int repro_qk_norm_rope_fwd(const void* q, int64_t q_ld, int64_t q_hs, const void
  *   dx_d = r (x) (u_d (-) (h_d (x) c1)), written to dq (dk) in q's type with the
  *     strides dq_ld, dq_hs, which set the heads one after another in a token (dq_ld at least
  *     (Hq - 1) dq_hs + D) or the tokens in a head (dq_hs at least (n - 1) dq_ld + D), else
- *     REPRO_ERR_ALIAS;
+ *     REPRO_ERR_ALIAS; dq and dk may lie in one buffer, a token's heads of q beside its heads
+ *     of k, or each head of q beside one of k at equal strides;
  *   dgain_d = canonical sum of dy_d (x) h_d over the rows (token, head), token
  *     major (a row of an out-of-range position gives a +0 term), (+) into
  *     dgain with REPRO_BWD_DW_ACCUMULATE.

@@ -28,3 +28,23 @@ def test_gradients_over_themselves(qk_bwd):
         assert f(**kw) not in BAD, kw
     # inputs may share what they like
     assert f(q_ld=64, k_ld=1) not in BAD
+
+
+def test_gradients_between_one_another(qk_bwd):
+    """A fused gradient with q, k (and v) of each head side by side, tokens or heads outermost."""
+    def f(slots, k_slot, n=20, heads_first=False, **kw):
+        s = slots * 64
+        ld, hs = (s, n * s) if heads_first else (4 * s, s)
+        return qk_bwd(**{**dict(n=n, Hq=4, Hkv=4, dq_ld=ld, dq_hs=hs, dk=9 * B + k_slot * 64 * 4, dk_ld=ld, dk_hs=hs), **kw})
+
+    for heads_first in (False, True):
+        for slots, k_slot in ((2, 1), (3, 1), (3, 2), (3, -1)):
+            assert f(slots, k_slot, heads_first=heads_first) not in BAD
+        assert f(3, 0, heads_first=heads_first) == -8
+        for off in (-4, 4):                                   # an element into the neighbour
+            assert f(2, 1, heads_first=heads_first, dk=9 * B + 64 * 4 + off) == -8
+        assert f(3, 1, heads_first=heads_first, dk=9 * B + 64 * 4 - 4) == -8
+        assert f(3, 1, heads_first=heads_first, Hkv=2) not in BAD
+    assert f(3, 1, dk_ld=4 * 3 * 64 + 64) == -8               # tokens at another distance
+    assert f(3, 1, dq_ld=4 * 3 * 64 + 64, dk_ld=4 * 3 * 64 + 64) == -8    # no whole number of heads
+    assert f(3, 1, n=1, dq_ld=1, dk_ld=5) not in BAD

@@ -1,0 +1,41 @@
+"""GPU: layouts, streams and reports of the embedding, the per-head norm with rotation
+and the distillation loss that are not the usual ones."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import bitwise_reproducible_int8_gb300 as R  # noqa: E402
+from gpu_helpers import dev  # noqa: E402
+from test_oracle_blocks import rope_table  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("heads_first", [False, True])
+@pytest.mark.parametrize("D", [64, 33])
+def test_heads_side_by_side(heads_first, D):
+    """q, k and v of each head next to one another, in the inputs and in their gradient: the
+    bits of tensors of their own."""
+    n, H = 37, 4
+    g = torch.Generator(device="cuda").manual_seed(4)
+    shape = (H, n, 3, D) if heads_first else (n, H, 3, D)
+    x = torch.randn(shape, device="cuda", generator=g)
+    dx = torch.full(shape, 9.0, device="cuda")
+    part = lambda t, i: (t.transpose(0, 1) if heads_first else t)[:, :, i]  # noqa: E731
+    do = [torch.randn(n, H, D, device="cuda", generator=g) for _ in range(2)]
+    gains = [torch.rand(D, device="cuda", generator=g) + 0.5 for _ in range(2)]
+    rope = dev(rope_table(n, D - D % 2))
+
+    def run(q, k, dq, dk):
+        out = [torch.empty(n, H, D, device="cuda") for _ in range(2)]
+        dg = [torch.empty(D, device="cuda") for _ in range(2)]
+        R.repro_qk_norm_rope_fwd(q, k, rope, *out, g_q=gains[0], g_k=gains[1])
+        R.repro_qk_norm_rope_bwd(*do, q, k, rope, dq, dk, g_q=gains[0], g_k=gains[1], dg_q=dg[0], dg_k=dg[1])
+        return [*out, dq, dk, *dg]
+
+    got = run(part(x, 0), part(x, 1), part(dx, 0), part(dx, 1))
+    own = [part(x, i).contiguous() for i in range(2)]
+    exp = run(*own, *(torch.empty_like(t) for t in own))
+    for a, b in zip(got, exp):
+        assert torch.equal(a, b)
+    assert torch.all(part(dx, 2) == 9.0)
