@@ -644,6 +644,11 @@ EmbedWs embed_ws(int64_t n, int64_t V, int64_t D)
     return w;
 }
 
+// Shared memory that the first launch may ask for: a bitmap of REPRO_EMBED_MAX_V / 56 rows and
+// the zeros (a constant: what one call sets is every host thread's limit)
+constexpr int FIRST_SMEM = 54 * 1024;
+static_assert((16777215 / 56 + 32) / 32 * 4 + 128 + ZERO_BYTES <= FIRST_SMEM, "fill_ctas() is 56 at least");
+
 // CTAs that may zero rows beside the sorting cluster: a cluster's CTAs share a GPC,
 // so fewer clusters than SMs / 8 run at a time, and one more would start when the
 // others are done (all 18 of them: 57 us for 268 MB instead of 43)
@@ -657,11 +662,9 @@ int fill_ctas()
         cfg.blockDim = dim3(SORT_NT);
         cfg.dynamicSmemBytes = sizeof(SortSmem);
         int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, k_embed_sort, &cfg) != cudaSuccess || clusters < 2) {
+        if (cudaOccupancyMaxActiveClusters(&clusters, k_embed_sort, &cfg) != cudaSuccess)
             cudaGetLastError();
-            clusters = 8;
-        }
-        v = (clusters - 1) * SORT_CTAS;
+        v = (clusters < 8 ? 7 : clusters - 1) * SORT_CTAS;
         known.store(v, std::memory_order_relaxed);
     }
     return v;
@@ -736,7 +739,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st)
     const int ctas = ranks > fill ? ranks : fill;
     auto first = [&](auto kernel, auto launch) {
         if (smem > 40 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FIRST_SMEM);
             if (e != cudaSuccess)
                 return e;
         }

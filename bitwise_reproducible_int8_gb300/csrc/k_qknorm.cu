@@ -663,10 +663,12 @@ template <typename T> cudaError_t bwd_typed(QkArgs a, float* parts, int64_t pitc
         const bool gain = a.t[0].gain || a.t[1].gain;
         const size_t smem = gain ? (size_t)CHUNK * a.D * 4 : 0;
         const int m = mode_of(a, E, LPH);
+        // the limit is the variant's widest head's, so that calls of other widths in other host
+        // threads set the same
+        constexpr int most = CHUNK * E * LPH * 4;
         auto go = [&](auto kernel) {
-            if (smem > 32 * 1024) {
-                const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                           (int)smem);
+            if (gain && most > 32 * 1024) {
+                const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
                 if (r != cudaSuccess)
                     return r;
             }

@@ -1,5 +1,7 @@
 """GPU: layouts, streams and reports of the embedding, the per-head norm with rotation
 and the distillation loss that are not the usual ones."""
+import threading
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -39,3 +41,32 @@ def test_heads_side_by_side(heads_first, D):
     for a, b in zip(got, exp):
         assert torch.equal(a, b)
     assert torch.all(part(dx, 2) == 9.0)
+
+
+def test_widths_in_two_threads():
+    """Two host threads in one variant of the backward with different widths: neither's
+    shared-memory size gets in the other's way."""
+    n, H = 8, 2
+
+    def work(D, seed, failures):
+        try:
+            g = torch.Generator(device="cuda").manual_seed(seed)
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                x, do = (torch.randn(n, H, D, device="cuda", generator=g) for _ in range(2))
+                gain, dx, dg = torch.ones(D, device="cuda"), torch.empty_like(x), torch.empty(D, device="cuda")
+                ws = torch.empty(R.repro_qk_norm_rope_bwd_ws_bytes(n, H, 0, D), dtype=torch.uint8, device="cuda")
+                for _ in range(3000):
+                    R.repro_qk_norm_rope_bwd(do, None, x, None, None, dx, None, g_q=gain, dg_q=dg, ws=ws)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failures.append((D, e))
+
+    for widths in ((132, 256), (260, 512)):
+        failures = []
+        threads = [threading.Thread(target=work, args=(D, D, failures)) for D in widths]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not failures, failures
