@@ -300,12 +300,14 @@ int repro_device_check(void* stream)
     if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int)) != cudaSuccess)
         return REPRO_ERR_LAUNCH;
     if (v != 0) {
-        const int zero = 0;
-        if (cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int)) != cudaSuccess)
+        // an index report leaves what the debug scan found to the next call
+        const bool index = !(v & kErrTimeoutBit) && (v & kErrIndexBit);
+        const int left = index ? v & ~kErrIndexBit : 0;
+        if (cudaMemcpyToSymbol(g_device_error, &left, sizeof(int)) != cudaSuccess)
             return REPRO_ERR_LAUNCH;
-        if (v & kErrTimeoutBit)
-            return REPRO_ERR_TIMEOUT;
-        return v & kErrIndexBit ? REPRO_ERR_INDEX : v & kErrNonfiniteBit ? REPRO_ERR_NONFINITE : REPRO_ERR_TIMEOUT;
+        if (index)
+            return REPRO_ERR_INDEX;
+        return (v & kErrTimeoutBit) || !(v & kErrNonfiniteBit) ? REPRO_ERR_TIMEOUT : REPRO_ERR_NONFINITE;
     }
     const int dev = current_device();
     if (dev >= 0 && dev < kMaxDevices && g_tc_notice[dev].exchange(0) != 0)

@@ -543,7 +543,8 @@ size_t repro_state_hash_ws_bytes(const int64_t* nbytes, int nbuf);
  * repro_device_check: synchronises `stream`, then reads and clears the
  *   device error word set by bounded device-side waits (and by out-of-range
  *   tokens, positions, indexes and labels); returns REPRO_OK,
- *   REPRO_ERR_TIMEOUT, REPRO_ERR_INDEX, or REPRO_ERR_SELFTEST once after the forward's
+ *   REPRO_ERR_TIMEOUT, REPRO_ERR_INDEX (a finding of the debug scan made along
+ *   with it is left to the next call), REPRO_ERR_NONFINITE, or REPRO_ERR_SELFTEST once after the forward's
  *   exactness check failed on the current device (REPRO_ERR_LAUNCH if the
  *   stream reported an error).
  * repro_launch_count: number of kernels this library has enqueued in this

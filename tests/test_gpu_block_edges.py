@@ -70,3 +70,22 @@ def test_widths_in_two_threads():
         for t in threads:
             t.join()
         assert not failures, failures
+
+
+def test_index_and_nonfinite_reports_both_arrive():
+    """A token out of range does not hide what the debug scan found."""
+    assert R.repro_device_check() == R.REPRO_OK
+    table, out = torch.randn(10, 8, device="cuda"), torch.empty(3, 8, device="cuda")
+    table[4, 5] = float("nan")
+    tok = torch.tensor([1, 10, 2], device="cuda")
+    R.repro_set_debug(R.REPRO_DEBUG_CHECK_FINITE)
+    try:
+        R.repro_embed_fwd(table, tok, out)
+        assert [R.repro_device_check() for _ in range(3)] == [R.REPRO_ERR_INDEX, R.REPRO_ERR_NONFINITE, R.REPRO_OK]
+        R.repro_embed_fwd(table, tok[:1], out[:1])
+        assert [R.repro_device_check() for _ in range(2)] == [R.REPRO_ERR_NONFINITE, R.REPRO_OK]
+    finally:
+        R.repro_set_debug(0)
+        R.repro_device_check()
+    R.repro_embed_fwd(table, tok, out)
+    assert [R.repro_device_check() for _ in range(2)] == [R.REPRO_ERR_INDEX, R.REPRO_OK]
