@@ -607,7 +607,7 @@ def repro_distill_fwd(logits: torch.Tensor, t_idx: torch.Tensor, t_logits: torch
     """loss [n] <- w_kd tau^2 KL(teacher, student) over the teacher's K entries a
     row (t_idx [n, K], negative: empty; t_logits [n, K], or its log-probabilities
     with logprobs) + w_ce cross entropy of labels (negative: none) + w_z lse^2.
-    logits [n, V] float32 or bfloat16, rows at any stride; stats
+    logits [n, V] float32 or bfloat16, rows at any stride; tau from 1e-4 to 1e4; stats
     [n, REPRO_DISTILL_STATS + K] float32 is the backward's input."""
     n, V, ld, K, ib, hp = _distill_common(logits, t_idx, labels, tau, w_kd, w_ce, w_z)
     if t_logits.shape != t_idx.shape:

@@ -478,7 +478,8 @@ size_t repro_qk_norm_rope_bwd_ws_bytes(int64_t n, int64_t Hq, int64_t Hkv, int64
  * loss and gradient NaN.
  * stats [n][REPRO_DISTILL_STATS + K] fp32 (dense): M, l, lse(u), l1, lse(z), m, lt, P,
  * then the p_k; the backward's input.  (l1 and lse(z) are 0 when tau != 1 and
- * both w_ce and w_z are 0.)  loss [n] fp32.  hp: HOST struct, tau > 0 finite.
+ * both w_ce and w_z are 0.)  loss [n] fp32.  hp: HOST struct, tau from 1e-4 to 1e4
+ * (REPRO_ERR_ARG outside), weights finite.
  * labels may be NULL when w_ce is 0.  n ceil((V + 63) / 512) <= 2^30, K <= 65536.  ws:
  * repro_distill_ws_bytes(n, V) bytes.  (Debug mode scans z, not t_val, where -infinity
  * is an ordinary value.) */

@@ -3,7 +3,7 @@ distillation loss, through the C ABI on invented addresses: nothing is launched.
 import pytest
 
 from bitwise_reproducible_int8_gb300 import repro
-from test_boundary_blocks import B, BAD, QK, L, call  # noqa: F401
+from test_boundary_blocks import B, BAD, QK, L, call, hp  # noqa: F401
 
 
 @pytest.fixture
@@ -48,3 +48,18 @@ def test_gradients_between_one_another(qk_bwd):
     assert f(3, 1, dk_ld=4 * 3 * 64 + 64) == -8               # tokens at another distance
     assert f(3, 1, dq_ld=4 * 3 * 64 + 64, dk_ld=4 * 3 * 64 + 64) == -8    # no whole number of heads
     assert f(3, 1, n=1, dq_ld=1, dk_ld=5) not in BAD
+
+
+def test_temperature_range(L):  # noqa: F811
+    """The header's range of tau, both calls."""
+    ws = repro.repro_distill_ws_bytes(40, 5000)
+    common = dict(z=B, z_type=0, z_ld=5000, t_idx=2 * B)
+    fwd = dict(common, t_val=3 * B, t_type=0, labels=None, index_bytes=4, n=40, V=5000, K=16, hp=hp(), flags=0,
+               loss=5 * B, stats=6 * B, ws=7 * B, ws_bytes=ws, stream=None)
+    bwd = dict(common, labels=None, index_bytes=4, n=40, V=5000, K=16, hp=hp(), stats=6 * B, g=8 * B, g_n=1,
+               dz=9 * B, dz_ld=5000, stream=None)
+    for fn, base in ((L.repro_distill_fwd, fwd), (L.repro_distill_bwd, bwd)):
+        for tau in (1e-4, 0.5, 1e4):
+            assert call(fn, base, hp=hp(tau=tau)) not in BAD, tau
+        for tau in (9.9e-5, 1e-30, 1.01e4, 1e30):
+            assert call(fn, base, hp=hp(tau=tau)) == -1, tau
