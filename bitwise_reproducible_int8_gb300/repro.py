@@ -5,6 +5,7 @@ built, or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -186,8 +187,14 @@ def _check(fn: str, status: int) -> None:
         raise ReproError(fn, status)
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
-    return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+def _workspace(nbytes: int, device, stream=None) -> torch.Tensor:
+    """A workspace for one call on `stream`: memory of that stream, whichever is current,
+    so that its owners before and after this call are in the stream's order."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) \
+            else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
 # ------------------------------------------------------------------ the calls
@@ -201,7 +208,7 @@ def repro_wscale(x: torch.Tensor, mode: int, scale_out: torch.Tensor, ws=None,
     """scale_out[0] <- weight (mode 0) or activation (mode 1) scale of x."""
     n = x.numel()
     if ws is None:
-        ws = _workspace(repro_wscale_ws_bytes(n), x.device)
+        ws = _workspace(repro_wscale_ws_bytes(n), x.device, stream)
     _check("repro_wscale", lib().repro_wscale(
         _ptr(x, torch.float32, "x"), n, int(mode), int(qmax),
         _ptr(scale_out, torch.float32, "scale_out"), _ptr(ws, None, "ws"),
@@ -247,7 +254,7 @@ def repro_wscale_multi(xs, mode: int, scales_out: torch.Tensor, ws=None,
     if scales_out.numel() < len(xs):
         raise ValueError("scales_out needs one float per tensor")
     if ws is None:
-        ws = _workspace(repro_wscale_multi_ws_bytes([x.numel() for x in xs]), xs[0].device)
+        ws = _workspace(repro_wscale_multi_ws_bytes([x.numel() for x in xs]), xs[0].device, stream)
     _check("repro_wscale_multi", lib().repro_wscale_multi(
         ptrs, sizes, len(xs), int(mode), int(qmax), _ptr(scales_out, torch.float32, "scales_out"),
         _ptr(ws, None, "ws"), ws.numel() * ws.element_size(), _stream(stream)))
@@ -277,7 +284,7 @@ def repro_linear_fwd(xq: torch.Tensor, wq: torch.Tensor, s_x: torch.Tensor, s_w:
         raise ValueError("shape mismatch: xq [M,K], wq [N,K], y [M,N]")
     if ws is None:
         need = repro_linear_fwd_ws_bytes(M, N, K)
-        ws = _workspace(need, y.device) if need > 0 else None
+        ws = _workspace(need, y.device, stream) if need > 0 else None
     ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
     _check("repro_linear_fwd", lib().repro_linear_fwd(
         _ptr(xq, torch.int8, "xq"), _ptr(wq, torch.int8, "wq"), _ptr(s_x, torch.float32, "s_x"),
@@ -299,7 +306,7 @@ def repro_linear_bwd(dy: torch.Tensor, xq, wq, s_x, s_w, dx=None, dw=None,
         raise ValueError("dw must be [N,K]")
     if ws is None:
         need = repro_linear_bwd_ws_bytes(M, N, K)
-        ws = _workspace(need, dy.device) if need > 0 else None
+        ws = _workspace(need, dy.device, stream) if need > 0 else None
     ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
     _check("repro_linear_bwd", lib().repro_linear_bwd(
         _ptr(dy, torch.float32, "dy"), _ptr(xq, torch.int8, "xq"), _ptr(wq, torch.int8, "wq"),
@@ -374,7 +381,7 @@ def repro_attn_bwd(q, k, vq, s_v, o, dout, m, l, dq, dk, dv, W: int = 0, ws=None
     Hkv = k.shape[2]
     if ws is None:
         ws = _workspace(repro_attn_bwd_ws_bytes(B, T, Hq, int(W) if fwd_ws is not None else -1),
-                        q.device)
+                        q.device, stream)
     f32 = torch.float32
     _check("repro_attn_bwd", lib().repro_attn_bwd(
         _ptr(q, f32, "q"), _ptr(k, f32, "k"), _ptr(vq, torch.int8, "vq"), _ptr(s_v, f32, "s_v"),
@@ -396,16 +403,6 @@ def _dev_ptr(t, name, contiguous=True):
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
-
-
-def _call_workspace(nbytes, device, stream):
-    """A workspace for one call: memory that is not handed out again before the
-    call's stream is done with it, whichever stream is current."""
-    ws = _workspace(nbytes, device)
-    if stream is not None:
-        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                         else torch.cuda.ExternalStream(int(stream), device=device))
-    return ws
 
 
 def _float_type(t, name) -> int:
@@ -481,7 +478,7 @@ def repro_embed_bwd(dout: torch.Tensor, tokens: torch.Tensor, dtable: torch.Tens
     if dtable.dtype != torch.float32:
         raise ValueError(f"dtable must be {torch.float32}, got {dtable.dtype}")
     if ws is None:
-        ws = _call_workspace(repro_embed_bwd_ws_bytes(n, V, D), dtable.device, stream)
+        ws = _workspace(repro_embed_bwd_ws_bytes(n, V, D), dtable.device, stream)
     _check("repro_embed_bwd", lib().repro_embed_bwd(
         _dev_ptr(dout, "dout", False), _float_type(dout, "dout"), dout_ld, _dev_ptr(tokens, "tokens"),
         _index_bytes("tokens", tokens), n, V, D, float(scale), int(pad), _dev_ptr(dtable, "dtable", False),
@@ -573,7 +570,7 @@ def repro_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out, q: torch.Tensor, k, rop
         if g is not None and g.numel() != D:
             raise ValueError(f"{name} must have D elements")
     if ws is None and (g_q is not None or g_k is not None):
-        ws = _call_workspace(repro_qk_norm_rope_bwd_ws_bytes(n, Hq, Hkv, D), q.device, stream)
+        ws = _workspace(repro_qk_norm_rope_bwd_ws_bytes(n, Hq, Hkv, D), q.device, stream)
     flags = (REPRO_QK_INTERLEAVED if interleaved else 0) | (REPRO_BWD_DW_ACCUMULATE if accumulate else 0)
     has_k = k is not None
     _check("repro_qk_norm_rope_bwd", lib().repro_qk_norm_rope_bwd(
@@ -615,7 +612,7 @@ def repro_distill_fwd(logits: torch.Tensor, t_idx: torch.Tensor, t_logits: torch
     if loss.numel() != n or stats.numel() != n * (REPRO_DISTILL_STATS + K):
         raise ValueError("loss must be [n], stats [n, REPRO_DISTILL_STATS + K]")
     if ws is None:
-        ws = _call_workspace(repro_distill_ws_bytes(n, V), logits.device, stream)
+        ws = _workspace(repro_distill_ws_bytes(n, V), logits.device, stream)
     _check("repro_distill_fwd", lib().repro_distill_fwd(
         _dev_ptr(logits, "logits", False), _float_type(logits, "logits"), ld, _dev_ptr(t_idx, "t_idx"),
         _dev_ptr(t_logits, "t_logits"), _float_type(t_logits, "t_logits"), _dev_ptr(labels, "labels"), ib,
@@ -647,7 +644,7 @@ def repro_selftest(device=None, stream=None) -> int:
     """Runs the tensor-core forward's exactness self-test; returns the status
     (REPRO_OK when every output matches the exact CUDA-core path)."""
     dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
-    ws = _workspace(int(lib().repro_selftest_ws_bytes()), dev)
+    ws = _workspace(int(lib().repro_selftest_ws_bytes()), dev, stream)
     return int(lib().repro_selftest(_ptr(ws, None, "ws"), ws.numel(), _stream(stream)))
 
 
@@ -676,7 +673,7 @@ def repro_state_hash(buffers, digest: torch.Tensor, ws=None, stream=None) -> Non
     if digest.numel() != 32 or digest.dtype != torch.uint8:
         raise ValueError("digest must be 32 uint8")
     if ws is None:
-        ws = _workspace(int(lib().repro_state_hash_ws_bytes(sizes, nb)), digest.device)
+        ws = _workspace(int(lib().repro_state_hash_ws_bytes(sizes, nb)), digest.device, stream)
     _check("repro_state_hash", lib().repro_state_hash(
         ptrs, sizes, nb, _ptr(digest, torch.uint8, "digest"), _ptr(ws, None, "ws"),
         ws.numel() * ws.element_size(), _stream(stream)))
@@ -690,7 +687,7 @@ def repro_sumsq(g: torch.Tensor, out: torch.Tensor, ws=None, stream=None) -> Non
     """out[0] <- canonical sum of g_i (x) g_i."""
     n = g.numel()
     if ws is None:
-        ws = _workspace(repro_sumsq_ws_bytes(n), g.device)
+        ws = _workspace(repro_sumsq_ws_bytes(n), g.device, stream)
     _check("repro_sumsq", lib().repro_sumsq(
         _ptr(g, torch.float32, "g"), n, _ptr(out, torch.float32, "out"), _ptr(ws, None, "ws"),
         ws.numel() * ws.element_size(), _stream(stream)))

@@ -89,3 +89,34 @@ def test_index_and_nonfinite_reports_both_arrive():
         R.repro_device_check()
     R.repro_embed_fwd(table, tok, out)
     assert [R.repro_device_check() for _ in range(2)] == [R.REPRO_ERR_INDEX, R.REPRO_OK]
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_workspace_beside_the_current_streams_work(handle):
+    """A call on another stream makes its workspace while the current stream has yet to write
+    memory it has already let go of."""
+    n, V = 2000, 20000
+    s = torch.cuda.Stream()
+    z, tl = torch.randn(n, V, device="cuda"), torch.randn(n, 8, device="cuda")
+    idx, tok = torch.randint(0, V, (n, 8), device="cuda"), torch.randint(0, 50, (n,), device="cuda")
+    loss, stats = torch.empty(n, device="cuda"), torch.empty(n, R.REPRO_DISTILL_STATS + 8, device="cuda")
+    dW = torch.empty(50, V, device="cuda")
+    where = s.cuda_stream if handle else s
+
+    def calls(**kw):
+        R.repro_distill_fwd(z, idx, tl, loss, stats, **kw)
+        R.repro_embed_bwd(z, tok, dW, **kw)
+
+    calls()
+    want = loss.clone(), dW.clone()
+    sizes = R.repro_distill_ws_bytes(n, V), R.repro_embed_bwd_ws_bytes(n, 50, V)
+    for _ in range(3):
+        loss.zero_()
+        dW.zero_()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(1000000)
+        for b in sizes:
+            torch.empty(b, dtype=torch.uint8, device="cuda").fill_(0xff)
+        calls(stream=where)
+        torch.cuda.synchronize()
+        assert torch.equal(loss, want[0]) and torch.equal(dW, want[1])
