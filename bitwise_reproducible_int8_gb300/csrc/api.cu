@@ -915,10 +915,10 @@ bool finite_f(float v) { return v - v == 0.0f; }
 
 // elements from the first to one past the last of `rows` rows of D, ld apart
 size_t row_span(int64_t rows, int64_t ld, int64_t D) { return (size_t)((rows - 1) * ld + D); }
-// whether that count fits comfortably in 63 bits of bytes
+// whether that count fits comfortably in 63 bits of bytes (one row has no next)
 bool rows_fit(int64_t rows, int64_t ld, int64_t D)
 {
-    return rows <= (int64_t)1 << 31 && ld <= (int64_t)1 << 28 && D <= (int64_t)1 << 28;
+    return rows <= (int64_t)1 << 31 && (rows <= 1 || ld <= (int64_t)1 << 28) && D <= (int64_t)1 << 28;
 }
 
 bool any_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins)

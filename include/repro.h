@@ -355,7 +355,8 @@ size_t repro_attn_bwd_ws_bytes(int64_t B, int64_t T, int64_t Hq, int64_t W);
  *
  * Types: REPRO_F32, or REPRO_BF16 (read exactly; a result written as bf16 is
  * the binary32 result rounded once more, to nearest even), or REPRO_I8 codes
- * for an embedding table.  Strides are in elements and may exceed the row;
+ * for an embedding table.  Strides are in elements, at most 2^28 where there is
+ * more than one row (REPRO_ERR_SHAPE), and may exceed the row;
  * rows whose strides or widths are not multiples of 4 elements are taken
  * element by element.  Tokens, teacher indexes and labels are int32 or int64
  * (index_bytes 4 or 8); one that is out of range is passed over as stated and

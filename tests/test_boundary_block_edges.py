@@ -63,3 +63,18 @@ def test_temperature_range(L):  # noqa: F811
             assert call(fn, base, hp=hp(tau=tau)) not in BAD, tau
         for tau in (9.9e-5, 1e-30, 1.01e4, 1e30):
             assert call(fn, base, hp=hp(tau=tau)) == -1, tau
+
+
+def test_stride_of_a_single_row(L, qk_bwd):  # noqa: F811
+    """The distance to a next row that is not there may be anything (a slice of a long cache)."""
+    far = 1 << 40
+    assert qk_bwd(n=1, q_ld=far, k_ld=far, dq_ld=far, dk_ld=far) not in BAD
+    for kw in (dict(q_ld=far), dict(dk_ld=far)):
+        assert qk_bwd(**kw) == -2, kw
+    embed = dict(table=B, table_type=0, table_ld=far, s_w=None, tokens=2 * B, index_bytes=8, n=1, V=1, D=64, scale=1.0,
+                 pad=-1, out=3 * B, out_type=0, out_ld=far, stream=None)
+    assert call(L.repro_embed_fwd, embed) not in BAD
+    assert call(L.repro_embed_fwd, embed, V=2) == -2 and call(L.repro_embed_fwd, embed, n=2) == -2
+    loss = dict(z=B, z_type=0, z_ld=far, t_idx=None, labels=None, index_bytes=4, n=1, V=5000, K=0, hp=hp(), stats=6 * B,
+                g=8 * B, g_n=1, dz=9 * B, dz_ld=far, stream=None)
+    assert call(L.repro_distill_bwd, loss) not in BAD and call(L.repro_distill_bwd, loss, n=2) == -2

@@ -120,3 +120,22 @@ def test_workspace_beside_the_current_streams_work(handle):
         calls(stream=where)
         torch.cuda.synchronize()
         assert torch.equal(loss, want[0]) and torch.equal(dW, want[1])
+
+
+def test_single_token_of_a_long_sequence():
+    """The last token of [1, T, H, D] whose sequence is longer than any token stride may be."""
+    T, H, D = 140000, 16, 128
+    whole = torch.zeros(1, T, H, D, device="cuda", dtype=torch.bfloat16)
+    q = whole[:, -1:]
+    q.normal_()
+    assert q.stride(0) > 1 << 28
+    rope = dev(rope_table(4, D))
+    got, exp = torch.empty(1, 1, H, D, device="cuda"), torch.empty(1, 1, H, D, device="cuda")
+    R.repro_qk_norm_rope_fwd(q, None, rope, got, None)
+    R.repro_qk_norm_rope_fwd(q.clone(), None, rope, exp, None)
+    assert torch.equal(got, exp)
+    dq = torch.empty_like(whole)[:, -1:]
+    own = torch.empty(1, 1, H, D, device="cuda", dtype=torch.bfloat16)
+    R.repro_qk_norm_rope_bwd(got, None, q, None, rope, dq, None)
+    R.repro_qk_norm_rope_bwd(got, None, q.clone(), None, rope, own, None)
+    assert torch.equal(dq, own)
