@@ -139,3 +139,28 @@ def test_single_token_of_a_long_sequence():
     R.repro_qk_norm_rope_bwd(got, None, q, None, rope, dq, None)
     R.repro_qk_norm_rope_bwd(got, None, q.clone(), None, rope, own, None)
     assert torch.equal(dq, own)
+
+
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gain_of_one_side(which, accumulate):
+    """Gains of the queries or of the keys alone: the bits of each side by itself."""
+    n, D, heads = 200, 128, {"q": 5, "k": 2}
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, do = ({nm: torch.randn(n, h, D, device="cuda", generator=g) for nm, h in heads.items()} for _ in range(2))
+    gain, acc = torch.rand(D, device="cuda", generator=g) + 0.5, torch.randn(D, device="cuda", generator=g)
+    rope = dev(rope_table(n, D))
+    kw = {"g_" + which: gain}
+    out = {nm: torch.empty(n, h, D, device="cuda") for nm, h in heads.items()}
+    dx, dg = {nm: torch.empty_like(t) for nm, t in x.items()}, acc.clone()
+    R.repro_qk_norm_rope_fwd(x["q"], x["k"], rope, out["q"], out["k"], **kw)
+    R.repro_qk_norm_rope_bwd(do["q"], do["k"], x["q"], x["k"], rope, dx["q"], dx["k"], accumulate=accumulate,
+                             **kw, **{"dg_" + which: dg})
+    for nm in heads:
+        has = nm == which
+        o, d, e = torch.empty_like(out[nm]), torch.empty_like(x[nm]), acc.clone()
+        R.repro_qk_norm_rope_fwd(x[nm], None, rope, o, None, g_q=gain if has else None)
+        R.repro_qk_norm_rope_bwd(do[nm], None, x[nm], None, rope, d, None, g_q=gain if has else None,
+                                 dg_q=e if has else None, accumulate=accumulate)
+        assert torch.equal(out[nm], o) and torch.equal(dx[nm], d)
+        assert not has or torch.equal(dg, e)
