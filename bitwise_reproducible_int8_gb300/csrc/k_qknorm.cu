@@ -10,10 +10,12 @@
 // lanes, so the norm's order (groups of 4, then the pairwise tree) is a chain in a
 // lane, an exchange over lanes and a few sums in a lane; only partners that lie in
 // other lanes pass through shared memory.  Two rows a lane share the exchanges and the
-// root and division of the norm; the arithmetic is on packed pairs.  16,384 tokens of 16 + 4 heads of 128,
-// fp32: forward 52.7 us, 6.4 TB/s (0.96 of a copy's); backward with gains 88.5 us, 5.7 TB/s
-// (0.85; 5 us of it the gains' tree).  With 4 elements a lane, a row at a time, these were
-// 108 and 213 us: 265 warp instructions a row in the forward, now 101.
+// root and division of the norm; the arithmetic is on packed pairs.  16,384 tokens of 16 + 4
+// heads of 128, fp32: forward 52.4 us, 6.4 TB/s (0.96 of a copy's); backward with gains 88 us,
+// 5.7 TB/s (0.86; 5 us of it the gains' tree).  With 4 elements a lane, a row at a time, these were
+// 108 and 213 us: 265 warp instructions a row in the forward, now 101.  bf16 heads, 8,192 tokens:
+// 30 us forward, 46 us backward with gains, 37 without (fp32 31 and 49 with gains): as many
+// instructions over fewer bytes, 0.63 and 0.54 of a copy's rate.
 //
 // The gains' gradients are sums over all rows (token, head): a CTA of the backward
 // owns one 64-row chunk, leaves dy (x) h of each row in shared memory and adds the

@@ -552,7 +552,8 @@ def repro_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out, q: torch.Tensor, k, rop
                            g_q=None, g_k=None, dg_q=None, dg_k=None, positions=None, eps: float = 1e-6,
                            interleaved: bool = False, accumulate: bool = False, ws=None,
                            stream=None) -> None:
-    """dq, dk (q's type, any token and head strides) and the gains' gradients
+    """dq, dk (q's type, any token and head strides that keep their heads apart;
+    both may lie in one buffer) and the gains' gradients
     dg_q, dg_k [D] (added to with accumulate) from the gradients dq_out, dk_out
     of the forward's outputs (dense float32) and the forward's inputs."""
     f32 = torch.float32
@@ -604,6 +605,7 @@ def repro_distill_fwd(logits: torch.Tensor, t_idx: torch.Tensor, t_logits: torch
     """loss [n] <- w_kd tau^2 KL(teacher, student) over the teacher's K entries a
     row (t_idx [n, K], negative: empty; t_logits [n, K], or its log-probabilities
     with logprobs) + w_ce cross entropy of labels (negative: none) + w_z lse^2.
+    Without a teacher (w_kd 0) t_idx and t_logits may have K = 0 columns.
     logits [n, V] float32 or bfloat16, rows at any stride; tau from 1e-4 to 1e4; stats
     [n, REPRO_DISTILL_STATS + K] float32 is the backward's input."""
     n, V, ld, K, ib, hp = _distill_common(logits, t_idx, labels, tau, w_kd, w_ce, w_z)
