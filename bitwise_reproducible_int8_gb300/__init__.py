@@ -21,4 +21,9 @@ from .repro import (  # noqa: F401
     REPRO_QK_INTERLEAVED, REPRO_QK_MAX_D, repro_distill_bwd, repro_distill_fwd,
     repro_distill_ws_bytes, repro_embed_bwd, repro_embed_bwd_ws_bytes, repro_embed_fwd,
     repro_qk_norm_rope_bwd, repro_qk_norm_rope_bwd_ws_bytes, repro_qk_norm_rope_fwd,
+    REPRO_MM_A_T, REPRO_MM_B_T, REPRO_MM_MAX_ROWS, REPRO_NORM_CHUNK, REPRO_NORM_GATE_ROWS,
+    REPRO_NORM_MAX_D, REPRO_NORM_POST, REPRO_QUANT_COLUMNS, REPRO_SWIGLU_GROUP,
+    repro_block_norm_bwd, repro_block_norm_bwd_ws_bytes, repro_block_norm_fwd, repro_matmul_i8,
+    repro_matmul_i8_ws_bytes, repro_quant_rows_i8, repro_quant_rows_i8_ws_bytes, repro_swiglu_bwd,
+    repro_swiglu_fwd,
 )

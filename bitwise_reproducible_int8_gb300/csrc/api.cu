@@ -1366,6 +1366,313 @@ int repro_distill_bwd(const void* z, int z_type, int64_t z_ld, const void* t_idx
     return status_of(launch_distill_bwd(a, as_stream(stream)));
 }
 
+// ---------------------------------------------------------------- the feed-forward half
+
+// arguments that the block norm's forward and backward share
+static int check_norm(bool has_y, int type, int u_type, const void* gate, int64_t gate_ld, const float* gain_post,
+                      float alpha, float beta, int64_t n, int64_t D, int flags, int allowed)
+{
+    if (!float_type(type) || !float_type(u_type) || (flags & ~allowed) || !finite_f(alpha) || !finite_f(beta))
+        return REPRO_ERR_ARG;
+    if ((!has_y && (gate || gain_post || (flags & (REPRO_NORM_POST | REPRO_NORM_GATE_ROWS)))) ||
+        (gain_post && !(flags & REPRO_NORM_POST)) || (!gate && (flags & REPRO_NORM_GATE_ROWS)))
+        return REPRO_ERR_ARG;
+    if (n < 0 || D < 1 || D > REPRO_NORM_MAX_D || ((flags & REPRO_NORM_GATE_ROWS) && (gate_ld < D || !rows_fit(n, gate_ld, D))))
+        return REPRO_ERR_SHAPE;
+    return REPRO_OK;
+}
+
+// bytes of n strided rows, 0 for a missing tensor
+static size_t rows_bytes(const void* p, int64_t n, int64_t ld, int64_t D, int type)
+{
+    return p && n > 0 ? row_span(n, ld, D) * type_bytes(type) : 0;
+}
+
+static bool bad_rows(const void* p, int64_t n, int64_t ld, int64_t D) { return p && (ld < D || !rows_fit(n, ld, D)); }
+
+int repro_block_norm_fwd(const void* x, int64_t x_ld, const void* y, int64_t y_ld, int type, const void* gate,
+                         int64_t gate_ld, const float* gain_post, const float* gain_pre, float alpha, float beta,
+                         float eps, int64_t n, int64_t D, int flags, void* h, int64_t h_ld, void* u, int u_type,
+                         int64_t u_ld, float* stats, void* stream)
+{
+    int st = check_norm(y, type, u_type, gate, gate_ld, gain_post, alpha, beta, n, D, flags,
+                        REPRO_NORM_POST | REPRO_NORM_GATE_ROWS);
+    if (st != REPRO_OK)
+        return st;
+    if (!(eps >= 0.0f) || !finite_f(eps) || (y != nullptr) != (h != nullptr) || (!y && !u && n > 0) || (!u && gain_pre))
+        return REPRO_ERR_ARG;
+    if (x_ld < D || !rows_fit(n, x_ld, D) || bad_rows(y, n, y_ld, D) || bad_rows(h, n, h_ld, D) || bad_rows(u, n, u_ld, D))
+        return REPRO_ERR_SHAPE;
+    if (n == 0)
+        return REPRO_OK;
+    if (!x)
+        return REPRO_ERR_ARG;
+    const bool rows = (flags & REPRO_NORM_GATE_ROWS) != 0;
+    const size_t b = type_bytes(type);
+    if (!aligned_to(x, b) || !aligned_to(y, b) || !aligned_to(h, b) || !aligned_to(gate, rows ? b : 4) ||
+        !aligned_to(u, type_bytes(u_type)) || !al4(gain_post) || !al4(gain_pre) || !al4(stats))
+        return REPRO_ERR_ALIGN;
+    const bool in_place = h == x && (n == 1 || h_ld == x_ld);
+    const Span sx = {x, in_place ? 0 : rows_bytes(x, n, x_ld, D, type)};
+    if (any_overlap({{h, rows_bytes(h, n, h_ld, D, type)}, {u, rows_bytes(u, n, u_ld, D, u_type)}, {stats, (size_t)n * 8}},
+                    {sx, {y, rows_bytes(y, n, y_ld, D, type)},
+                     {gate, rows ? rows_bytes(gate, n, gate_ld, D, type) : (size_t)D * 4}, {gain_post, (size_t)D * 4},
+                     {gain_pre, (size_t)D * 4}}))
+        return REPRO_ERR_ALIAS;
+    if ((st = check_arch()) != REPRO_OK)
+        return st;
+    if ((st = scan_rows(stream, x, type, n, D, x_ld)) != REPRO_OK || (st = scan_rows(stream, y, type, n, D, y_ld)) != REPRO_OK ||
+        (rows && (st = scan_rows(stream, gate, type, n, D, gate_ld)) != REPRO_OK) ||
+        (st = scan_inputs(stream, {{rows ? nullptr : static_cast<const float*>(gate), D}, {gain_post, D}, {gain_pre, D}})) != REPRO_OK)
+        return st;
+    NormArgs a = {};
+    a.x = x, a.x_ld = x_ld, a.y = y, a.y_ld = y_ld, a.type = type, a.u_type = u_type;
+    a.gate = gate, a.gate_ld = gate_ld, a.gate_rows = rows, a.post = (flags & REPRO_NORM_POST) != 0;
+    a.gain_post = gain_post, a.gain_pre = gain_pre;
+    a.alpha = alpha, a.beta = beta, a.eps = eps, a.n = n, a.D = D;
+    a.h = h, a.h_ld = h_ld, a.u = u, a.u_ld = u_ld, a.stats = stats;
+    return status_of(launch_norm_fwd(a, as_stream(stream)));
+}
+
+size_t repro_block_norm_bwd_ws_bytes(int64_t n, int64_t D)
+{
+    if (n <= 0 || n > (int64_t)1 << 31 || D < 1 || D > REPRO_NORM_MAX_D)
+        return 0;
+    return norm_bwd_ws_bytes(n, D);
+}
+
+int repro_block_norm_bwd(const void* dh, int64_t dh_ld, const void* du, int u_type, int64_t du_ld, const void* h,
+                         int64_t h_ld, const void* y, int64_t y_ld, int type, const void* gate, int64_t gate_ld,
+                         const float* gain_post, const float* gain_pre, const float* stats, float alpha, float beta,
+                         int64_t n, int64_t D, int flags, void* dx, int64_t dx_ld, void* dy, int64_t dy_ld, void* dgate,
+                         int64_t dgate_ld, float* dgain_post, float* dgain_pre, void* ws, size_t ws_bytes, void* stream)
+{
+    int st = check_norm(y, type, u_type, gate, gate_ld, gain_post, alpha, beta, n, D, flags,
+                        REPRO_NORM_POST | REPRO_NORM_GATE_ROWS | REPRO_BWD_DW_ACCUMULATE);
+    if (st != REPRO_OK)
+        return st;
+    const bool rows = (flags & REPRO_NORM_GATE_ROWS) != 0, accumulate = (flags & REPRO_BWD_DW_ACCUMULATE) != 0;
+    if ((gate != nullptr) != (dgate != nullptr) || (gain_post != nullptr) != (dgain_post != nullptr) ||
+        (gain_pre != nullptr) != (dgain_pre != nullptr) || (y != nullptr) != (dy != nullptr) ||
+        (n > 0 && ((!dh && !du) || !dx || !stats)) || (n > 0 && (du != nullptr) != (h != nullptr)) ||
+        (n > 0 && !du && gain_pre))
+        return REPRO_ERR_ARG;
+    if (bad_rows(dh, n, dh_ld, D) || bad_rows(du, n, du_ld, D) || bad_rows(h, n, h_ld, D) || bad_rows(y, n, y_ld, D) ||
+        bad_rows(dx, n, dx_ld, D) || bad_rows(dy, n, dy_ld, D) || (rows && bad_rows(dgate, n, dgate_ld, D)))
+        return REPRO_ERR_SHAPE;
+    const size_t b = type_bytes(type);
+    if (!aligned_to(dh, b) || !aligned_to(h, b) || !aligned_to(y, b) || !aligned_to(dx, b) || !aligned_to(dy, b) ||
+        !aligned_to(gate, rows ? b : 4) || !aligned_to(dgate, rows ? b : 4) || !aligned_to(du, type_bytes(u_type)) ||
+        !al4(gain_post) || !al4(gain_pre) || !al4(stats) || !al4(dgain_post) || !al4(dgain_pre))
+        return REPRO_ERR_ALIGN;
+    float* sums[3] = {rows ? nullptr : static_cast<float*>(dgate), dgain_post, dgain_pre};
+    if (n == 0) {   // sums over no tokens are +0
+        if (accumulate || (!sums[0] && !sums[1] && !sums[2]))
+            return REPRO_OK;
+        if ((st = check_arch()) != REPRO_OK)
+            return st;
+        for (float* s : sums)
+            if (s && cudaMemsetAsync(s, 0, (size_t)D * 4, as_stream(stream)) != cudaSuccess)
+                return REPRO_ERR_LAUNCH;
+        return REPRO_OK;
+    }
+    const size_t need = sums[0] || sums[1] || sums[2] ? norm_bwd_ws_bytes(n, D) : 0, col = (size_t)D * 4;
+    if (need > 0 && (!ws || ws_bytes < need))
+        return REPRO_ERR_WORKSPACE;
+    if (need > 0 && !al16(ws))
+        return REPRO_ERR_ALIGN;
+    const bool in_place = dx == dh && (n == 1 || dx_ld == dh_ld);
+    if (any_overlap({{dx, rows_bytes(dx, n, dx_ld, D, type)}, {dy, rows_bytes(dy, n, dy_ld, D, type)},
+                     {dgate, rows ? rows_bytes(dgate, n, dgate_ld, D, type) : col}, {dgain_post, col}, {dgain_pre, col},
+                     {ws, need}},
+                    {{dh, in_place ? 0 : rows_bytes(dh, n, dh_ld, D, type)}, {du, rows_bytes(du, n, du_ld, D, u_type)},
+                     {h, rows_bytes(h, n, h_ld, D, type)}, {y, rows_bytes(y, n, y_ld, D, type)},
+                     {gate, rows ? rows_bytes(gate, n, gate_ld, D, type) : col}, {gain_post, col}, {gain_pre, col},
+                     {stats, (size_t)n * 8}}))
+        return REPRO_ERR_ALIAS;
+    if ((st = check_arch()) != REPRO_OK)
+        return st;
+    if ((st = scan_rows(stream, dh, type, n, D, dh_ld)) != REPRO_OK || (st = scan_rows(stream, du, u_type, n, D, du_ld)) != REPRO_OK ||
+        (st = scan_rows(stream, h, type, n, D, h_ld)) != REPRO_OK || (st = scan_rows(stream, y, type, n, D, y_ld)) != REPRO_OK ||
+        (rows && (st = scan_rows(stream, gate, type, n, D, gate_ld)) != REPRO_OK) ||
+        (st = scan_inputs(stream, {{rows ? nullptr : static_cast<const float*>(gate), D}, {gain_post, D}, {gain_pre, D}, {stats, 2 * n}})) !=
+            REPRO_OK)
+        return st;
+    NormArgs a = {};
+    a.y = y, a.y_ld = y_ld, a.type = type, a.u_type = u_type;
+    a.gate = gate, a.gate_ld = gate_ld, a.gate_rows = rows, a.post = (flags & REPRO_NORM_POST) != 0;
+    a.accumulate = accumulate, a.gain_post = gain_post, a.gain_pre = gain_pre;
+    a.alpha = alpha, a.beta = beta, a.n = n, a.D = D, a.stats = const_cast<float*>(stats);
+    a.dh = dh, a.dh_ld = dh_ld, a.du = du, a.du_ld = du_ld, a.hs = h, a.hs_ld = h_ld;
+    a.dx = dx, a.dx_ld = dx_ld, a.dy = dy, a.dy_ld = dy_ld, a.dgate = dgate, a.dgate_ld = dgate_ld;
+    a.dgain_post = dgain_post, a.dgain_pre = dgain_pre;
+    return status_of(launch_norm_bwd(a, ws, as_stream(stream)));
+}
+
+size_t repro_quant_rows_i8_ws_bytes(int64_t n, int64_t D, int flags)
+{
+    if (n < 0 || D < 1 || D > (int64_t)1 << 28)
+        return 0;
+    return quant_rows_ws_bytes(n, D, (flags & REPRO_QUANT_COLUMNS) != 0);
+}
+
+int repro_quant_rows_i8(const void* x, int type, int64_t x_ld, const float* mul, int64_t n, int64_t D, int flags,
+                        int8_t* q, int64_t q_ld, float* scales, void* ws, size_t ws_bytes, void* stream)
+{
+    if (!float_type(type) || (flags & ~REPRO_QUANT_COLUMNS))
+        return REPRO_ERR_ARG;
+    if (n < 0 || D < 1 || x_ld < D || q_ld < D || !rows_fit(n, x_ld, D) || !rows_fit(n, q_ld, D))
+        return REPRO_ERR_SHAPE;
+    const bool columns = (flags & REPRO_QUANT_COLUMNS) != 0;
+    if (n == 0 && !columns)
+        return REPRO_OK;
+    if (!scales || (n > 0 && (!x || !q)))
+        return REPRO_ERR_ARG;
+    const size_t need = n > 0 ? quant_rows_ws_bytes(n, D, columns) : 0;
+    if (!aligned_to(x, type_bytes(type)) || !al4(mul) || !al4(scales))
+        return REPRO_ERR_ALIGN;
+    if (need > 0 && (!ws || ws_bytes < need))
+        return REPRO_ERR_WORKSPACE;
+    if (need > 0 && !al16(ws))
+        return REPRO_ERR_ALIGN;
+    const size_t sbytes = (size_t)(columns ? D : n) * 4, mbytes = (size_t)(columns ? n : D) * 4;
+    if (any_overlap({{q, n > 0 ? row_span(n, q_ld, D) : 0}, {scales, sbytes}, {ws, need}},
+                    {{x, rows_bytes(x, n, x_ld, D, type)}, {mul, mbytes}}))
+        return REPRO_ERR_ALIAS;
+    int st = check_arch();
+    if (st != REPRO_OK)
+        return st;
+    if (n == 0)   // columns of no rows
+        return cudaMemsetAsync(scales, 0, sbytes, as_stream(stream)) == cudaSuccess ? REPRO_OK : REPRO_ERR_LAUNCH;
+    if ((st = scan_rows(stream, x, type, n, D, x_ld)) != REPRO_OK ||
+        (st = scan_inputs(stream, {{mul, columns ? n : D}})) != REPRO_OK)
+        return st;
+    return status_of(launch_quant_rows({x, type, x_ld, mul, n, D, columns, q, q_ld, scales}, ws, as_stream(stream)));
+}
+
+static size_t matmul_ws_need(int64_t M, int64_t N, int64_t K, int flags)
+{
+    const size_t need = matmul_i8_ws_bytes(M, N, K, flags & REPRO_MM_A_T, flags & REPRO_MM_B_T);
+    return need == 0 || need > selftest_ws_bytes() ? need : selftest_ws_bytes();   // the first call's check runs there
+}
+
+size_t repro_matmul_i8_ws_bytes(int64_t M, int64_t N, int64_t K, int flags)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || M > REPRO_MM_MAX_ROWS || N > REPRO_MM_MAX_ROWS || K > 133144)
+        return 0;
+    return matmul_ws_need(M, N, K, flags);
+}
+
+int repro_matmul_i8(const int8_t* a, int64_t a_ld, const int8_t* b, int64_t b_ld, const float* s_a, const float* s_b,
+                    int64_t M, int64_t N, int64_t K, int flags, void* y, int y_type, int64_t y_ld, void* ws,
+                    size_t ws_bytes, void* stream)
+{
+    const bool accumulate = (flags & REPRO_BWD_DW_ACCUMULATE) != 0, a_t = (flags & REPRO_MM_A_T) != 0, b_t = (flags & REPRO_MM_B_T) != 0;
+    if (!float_type(y_type) || (flags & ~(REPRO_BWD_DW_ACCUMULATE | REPRO_MM_A_T | REPRO_MM_B_T)) || (accumulate && y_type != REPRO_F32))
+        return REPRO_ERR_ARG;
+    if (M < 0 || N < 0 || K < 0 || M > REPRO_MM_MAX_ROWS || N > REPRO_MM_MAX_ROWS || K > 133144)
+        return REPRO_ERR_SHAPE;
+    const int64_t ar = a_t ? K : M, ac = a_t ? M : K, br = b_t ? K : N, bc = b_t ? N : K;
+    if (a_ld < ac || b_ld < bc || y_ld < N || !rows_fit(ar, a_ld, ac) || !rows_fit(br, b_ld, bc) || !rows_fit(M, y_ld, N))
+        return REPRO_ERR_SHAPE;
+    if (M == 0 || N == 0 || (K == 0 && accumulate))
+        return REPRO_OK;
+    if (!y || (K > 0 && (!a || !b)))
+        return REPRO_ERR_ARG;
+    if (!aligned_to(y, type_bytes(y_type)) || !al4(s_a) || !al4(s_b))
+        return REPRO_ERR_ALIGN;
+    const size_t need = K > 0 ? matmul_ws_need(M, N, K, flags) : 0;
+    if (need > 0 && (!ws || ws_bytes < need))
+        return REPRO_ERR_WORKSPACE;
+    if (need > 0 && !al16(ws))
+        return REPRO_ERR_ALIGN;
+    if (any_overlap({{y, row_span(M, y_ld, N) * type_bytes(y_type)}, {ws, need}},
+                    {{a, K > 0 ? row_span(ar, a_ld, ac) : 0}, {b, K > 0 ? row_span(br, b_ld, bc) : 0},
+                     {s_a, (size_t)M * 4}, {s_b, (size_t)N * 4}}))
+        return REPRO_ERR_ALIAS;
+    int st = check_arch();
+    if (st != REPRO_OK)
+        return st;
+    if ((st = scan_inputs(stream, {{s_a, M}, {s_b, N}})) != REPRO_OK ||
+        (accumulate && (st = scan_rows(stream, y, y_type, M, N, y_ld)) != REPRO_OK))
+        return st;
+    bool tc = need > 0 && g_cfg.fwd_path != 0;
+    if (tc && g_cfg.fwd_path < 1) {
+        const int gate = tc_gate(ws, as_stream(stream));
+        if (gate < 0)
+            return REPRO_ERR_LAUNCH;
+        tc = gate == 1;
+    }
+    return status_of(launch_matmul_i8({a, b, a_ld, b_ld, a_t, b_t, s_a, s_b, M, N, K, y, y_type, y_ld, accumulate}, ws, tc,
+                                      as_stream(stream)));
+}
+
+// what the activation's forward and backward share
+static int check_swiglu(int type, int a_type, int64_t n, int64_t F, const void* gu, int64_t gu_ld, const void* a, int64_t a_ld,
+                        const int8_t* codes, const float* scales)
+{
+    if (!float_type(type) || !float_type(a_type) || (codes != nullptr) != (scales != nullptr))
+        return REPRO_ERR_ARG;
+    if (n < 0 || F < 1 || F > (int64_t)1 << 27 || bad_rows(gu, n, gu_ld, 2 * F) || bad_rows(a, n, a_ld, F) ||
+        n > (int64_t)1 << 31)
+        return REPRO_ERR_SHAPE;
+    if (!aligned_to(gu, type_bytes(type)) || !aligned_to(a, type_bytes(a_type)) || !al16(codes) || !al4(scales))
+        return REPRO_ERR_ALIGN;
+    return REPRO_OK;
+}
+
+static int64_t swiglu_groups(int64_t F) { return (F + REPRO_SWIGLU_GROUP - 1) / REPRO_SWIGLU_GROUP; }
+
+int repro_swiglu_fwd(const void* gu, int type, int64_t gu_ld, int64_t n, int64_t F, void* a, int a_type, int64_t a_ld,
+                     int8_t* codes, float* scales, void* stream)
+{
+    int st = check_swiglu(type, a_type, n, F, gu, gu_ld, a, a_ld, codes, scales);
+    if (st != REPRO_OK || n == 0)
+        return st;
+    if (!gu || !a)
+        return REPRO_ERR_ARG;
+    const size_t groups = (size_t)(2 * n * swiglu_groups(F));
+    if (any_overlap({{a, rows_bytes(a, n, a_ld, F, a_type)}, {codes, groups * REPRO_SWIGLU_GROUP}, {scales, groups * 4}},
+                    {{gu, rows_bytes(gu, n, gu_ld, 2 * F, type)}}))
+        return REPRO_ERR_ALIAS;
+    if ((st = check_arch()) != REPRO_OK || (st = scan_rows(stream, gu, type, n, 2 * F, gu_ld)) != REPRO_OK)
+        return st;
+    SwigluArgs s = {};
+    s.gu = gu, s.type = type, s.gu_ld = gu_ld, s.a_type = a_type, s.a_ld = a_ld, s.codes = codes, s.scales = scales;
+    s.n = n, s.F = F, s.a = a;
+    return status_of(launch_swiglu_fwd(s, as_stream(stream)));
+}
+
+int repro_swiglu_bwd(const void* da, int a_type, int64_t da_ld, const void* gu, int64_t gu_ld, const int8_t* codes,
+                     const float* scales, int64_t n, int64_t F, void* dgu, int type, int64_t dgu_ld, void* stream)
+{
+    int st = check_swiglu(type, a_type, n, F, gu, gu_ld, da, da_ld, codes, scales);
+    if (st != REPRO_OK)
+        return st;
+    if (bad_rows(dgu, n, dgu_ld, 2 * F))
+        return REPRO_ERR_SHAPE;
+    if (n == 0)
+        return REPRO_OK;
+    if (!da || !dgu || (gu != nullptr) == (codes != nullptr))
+        return REPRO_ERR_ARG;
+    if (!aligned_to(dgu, type_bytes(type)))
+        return REPRO_ERR_ALIGN;
+    const size_t groups = (size_t)(2 * n * swiglu_groups(F));
+    if (any_overlap({{dgu, rows_bytes(dgu, n, dgu_ld, 2 * F, type)}},
+                    {{gu, rows_bytes(gu, n, gu_ld, 2 * F, type)}, {da, rows_bytes(da, n, da_ld, F, a_type)},
+                     {codes, groups * REPRO_SWIGLU_GROUP}, {scales, groups * 4}}))
+        return REPRO_ERR_ALIAS;
+    if ((st = check_arch()) != REPRO_OK || (st = scan_rows(stream, da, a_type, n, F, da_ld)) != REPRO_OK ||
+        (st = scan_rows(stream, gu, type, n, 2 * F, gu_ld)) != REPRO_OK ||
+        (st = scan_inputs(stream, {{scales, (int64_t)groups}})) != REPRO_OK)
+        return st;
+    SwigluArgs s = {};
+    s.gu = gu, s.type = type, s.gu_ld = gu_ld, s.da = da, s.a_type = a_type, s.a_ld = da_ld;
+    s.codes = const_cast<int8_t*>(codes), s.scales = const_cast<float*>(scales);
+    s.n = n, s.F = F, s.dgu = dgu, s.dgu_ld = dgu_ld;
+    return status_of(launch_swiglu_bwd(s, as_stream(stream)));
+}
+
 size_t repro_state_hash_ws_bytes(const int64_t* nbytes, int nbuf)
 {
     if (nbuf < 0 || nbuf > REPRO_HASH_MAX_BUFFERS || (nbuf > 0 && !nbytes))

@@ -156,17 +156,17 @@ struct EmbedBwdArgs {
 size_t embed_bwd_ws_bytes(int64_t n, int64_t V, int64_t D);
 cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, void* ws, cudaStream_t st);
 
-// ---- pairwise tree over partial rows (k_rowtree.cu), shared by the table's and the gains' gradients
+// ---- pairwise tree over partial rows (k_rowtree.cu), shared by the gradients of the table, of gains and of a gate
 struct RowTree {
-    float* parts[2];     // partial rows, `pitch` floats apart (used as scratch)
+    float* parts[3];     // partial rows, `pitch` floats apart (used as scratch)
     int64_t pitch;
     const int4* joins;   // {first sorted index, chunks, output row, 0}, or NULL: `jobs` joins, job i
                          // over the count[i] consecutive partial rows of parts[i], into out[i]
     const int* njoins;   // device count of joins
-    int jobs;
-    int64_t count[2];
+    int jobs;            // at most 3
+    int64_t count[3];
     int64_t D;
-    float* out[2];
+    float* out[3];
     int64_t out_ld;
     float scale;         // applied to the sum (1: leaves it)
     bool accumulate;     // out (+) the scaled sum
@@ -227,6 +227,96 @@ struct DistillArgs {
 size_t distill_ws_bytes(int64_t n, int64_t V);
 cudaError_t launch_distill_fwd(const DistillArgs& a, void* ws, cudaStream_t st);
 cudaError_t launch_distill_bwd(const DistillArgs& a, cudaStream_t st);
+
+// ---- norms around a block (k_blocknorm.cu)
+struct NormArgs {
+    const void* x;       // forward: the stream; y: the block's output (both directions)
+    int64_t x_ld;
+    const void* y;
+    int64_t y_ld;
+    int type, u_type;
+    const void* gate;
+    int64_t gate_ld;
+    bool gate_rows, post, accumulate;
+    const float *gain_post, *gain_pre;
+    float alpha, beta, eps;
+    int64_t n, D;
+    void* h;             // forward's outputs
+    int64_t h_ld;
+    void* u;
+    int64_t u_ld;
+    float* stats;        // forward: written or NULL; backward: read
+    const void* dh;      // backward: gradients of the stream and of u, the stream as stored
+    int64_t dh_ld;
+    const void* du;
+    int64_t du_ld;
+    const void* hs;
+    int64_t hs_ld;
+    void* dx;
+    int64_t dx_ld;
+    void* dy;
+    int64_t dy_ld;
+    void* dgate;
+    int64_t dgate_ld;
+    float *dgain_post, *dgain_pre;
+    float* parts[3];     // set by the launchers: partial sums of gain_pre, gain_post and a gate that is one row
+    int64_t pitch;
+    int tpr;             // threads of a row
+    float inv;           // 1 / D where D is a power of two, else 0
+    bool vec;            // every row on 4-element boundaries
+};
+cudaError_t launch_norm_fwd(NormArgs a, cudaStream_t st);
+size_t norm_bwd_ws_bytes(int64_t n, int64_t D);
+cudaError_t launch_norm_bwd(NormArgs a, void* ws, cudaStream_t st);
+
+// ---- codes by row or column (k_quant_rows.cu)
+struct QuantRowsArgs {
+    const void* x;
+    int type;
+    int64_t x_ld;
+    const float* mul;
+    int64_t n, D;
+    bool columns;
+    int8_t* q;
+    int64_t q_ld;
+    float* scales;
+};
+size_t quant_rows_ws_bytes(int64_t n, int64_t D, bool columns);
+cudaError_t launch_quant_rows(const QuantRowsArgs& a, void* ws, cudaStream_t st);
+
+// ---- product of codes with scales by row of either side (k_matmul_i8.cu)
+struct MatmulI8Args {
+    const int8_t *a, *b;
+    int64_t a_ld, b_ld;
+    bool a_t, b_t;
+    const float *s_a, *s_b;
+    int64_t M, N, K;
+    void* y;
+    int y_type;
+    int64_t y_ld;
+    bool accumulate;
+};
+bool matmul_i8_small(int64_t M, bool a_t, bool b_t);   // few tokens: without a workspace, on the CUDA cores
+size_t matmul_i8_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_t, bool b_t);
+cudaError_t launch_matmul_i8(const MatmulI8Args& a, void* ws, bool tc, cudaStream_t st);
+
+// ---- gated activation (k_swiglu.cu)
+struct SwigluArgs {
+    const void* gu;
+    int type;            // of gu and dgu
+    int64_t gu_ld;
+    const void* da;
+    int a_type;          // of a and da
+    int64_t a_ld;        // of a or da
+    int8_t* codes;
+    float* scales;
+    int64_t n, F;
+    void* a;
+    void* dgu;
+    int64_t dgu_ld;
+};
+cudaError_t launch_swiglu_fwd(const SwigluArgs& a, cudaStream_t st);
+cudaError_t launch_swiglu_bwd(const SwigluArgs& a, cudaStream_t st);
 
 // ---- debug scan of strided rows (k_rowtree.cu): n rows of D elements of `type`, ld apart
 cudaError_t launch_check_finite_rows(const void* p, int type, int64_t n, int64_t D, int64_t ld, int* err,

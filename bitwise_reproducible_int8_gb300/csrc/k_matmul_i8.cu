@@ -1,0 +1,745 @@
+// k_matmul_i8.cu -- product of 8-bit codes with a scale for each row of both sides, in the three
+// layouts of a linear's training step.
+//
+//   y_mn = (i2f(sum_k A(m, k) B(n, k)) (x) s_a[m]) (x) s_b[n], the integer sum exact
+//
+// As in k_fwd_tc.cu the codes go to tcgen05.mma kind::f16 as bf16 (exact), fp32 accumulators over
+// slices of 512 terms (integers below 2^23, exact), the slices added up in int32.  What differs:
+//   * the widening pass also transposes (a reduction over tokens has its operands the other way
+//     round) and pads the rows, so any K, stride and layout reaches the tensor cores;
+//   * two SMs work on one 256 x 256 tile (cta_group::2): each loads its 128 rows of A and half of B,
+//     32 KB for 64 terms of K instead of 48 KB, because with one SM a tile of 128 x 256 the operands'
+//     way from L2 bound the product, not the tensor pipe;
+//   * the epilogue has a scale for each of its rows and columns.
+// Products of few tokens are bound by the weights' bytes and run on the CUDA cores (k_mm_rows).
+//
+// Roles in a CTA of the pair, as in k_fwd_tc.cu: warp 0 loads, warp 1 of the leading CTA issues the
+// MMAs for both (warp 1 of the other holds its tensor memory), warps 2 .. 9 are the epilogue.  The
+// leader's full barriers count both CTAs' bytes; an MMA's commit frees its stage, and hands over its
+// accumulator, in both; both epilogues free the accumulator on the leader's barrier.  Every wait is
+// bounded as there.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "common.cuh"
+#include "elem.cuh"
+#include "internal.h"
+#include "launch.cuh"
+#include "pipeline.cuh"
+#include "umma.cuh"
+
+namespace repro {
+namespace {
+
+// ---------------------------------------------------------------- operands to bf16
+
+inline int64_t pad8(int64_t k) { return (k + 7) / 8 * 8; }
+inline int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
+
+// four codes to two words of bf16 pairs: 128 + low seven bits less 128 or 256, all exact
+__device__ __forceinline__ uint2 widen4(uint32_t c)
+{
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t b = __byte_perm(c, 0, i == 0 ? 0x4140 : 0x4342);      // code, 0, code, 0
+        const uint32_t hi = (b & 0x007f007fu) | 0x43004300u, lo = (b & 0x00800080u) | 0x43004300u;
+        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&hi),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&lo));
+        w[i] = *reinterpret_cast<const uint32_t*>(&d);
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+struct Widen {
+    const int8_t* q;
+    int64_t ld, rows, K, Kp;    // source rows of K (or, transposed, K rows of `rows`); pitch of the copy
+    __nv_bfloat16* out;
+    bool vec;                   // source rows on 8-byte boundaries
+};
+
+// rows of K codes to rows of Kp bf16, zeros behind K; 8 at a time
+__global__ void __launch_bounds__(256)
+k_mm_widen(const __grid_constant__ Widen w)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int64_t per = w.Kp / 8, total = w.rows * per, step = (int64_t)gridDim.x * blockDim.x;
+    const bool flat = w.vec && w.K == w.Kp && w.ld == w.K;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += step) {
+        uint2 c;
+        if (flat) {
+            c = __ldg(reinterpret_cast<const uint2*>(w.q) + i);
+        } else {
+            const int64_t r = i / per, k = 8 * (i - r * per);
+            const int8_t* p = w.q + r * w.ld + k;
+            if (w.vec && k + 8 <= w.K) {
+                c = __ldg(reinterpret_cast<const uint2*>(p));
+            } else {
+                uint32_t v[2] = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (k + e < w.K)
+                        v[e >> 2] |= (uint32_t)(uint8_t)p[e] << (8 * (e & 3));
+                c = make_uint2(v[0], v[1]);
+            }
+        }
+        const uint2 a = widen4(c.x), b = widen4(c.y);
+        reinterpret_cast<uint4*>(w.out)[i] = make_uint4(a.x, a.y, b.x, b.y);
+    }
+}
+
+// K rows of codes to `rows` rows of Kp bf16, through tiles of 64 terms x 128 rows in shared memory
+__global__ void __launch_bounds__(256)
+k_mm_widen_t(const __grid_constant__ Widen w, int tiles_r)
+{
+    __shared__ uint32_t tile[64][33];
+    const int tr = blockIdx.x % tiles_r;
+    const int64_t k0 = (int64_t)(blockIdx.x / tiles_r) * 64, r0 = (int64_t)tr * 128;
+    pdl_wait();
+    pdl_trigger();
+    for (int e = threadIdx.x; e < 64 * 32; e += 256) {
+        const int k = e >> 5, c = e & 31;
+        const int64_t r = r0 + 4 * c;
+        uint32_t v = 0;
+        if (k0 + k < w.K) {
+            const int8_t* p = w.q + (k0 + k) * w.ld + r;
+            if (w.vec && r + 4 <= w.rows) {
+                v = __ldg(reinterpret_cast<const uint32_t*>(p));
+            } else {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (r + b < w.rows)
+                        v |= (uint32_t)(uint8_t)p[b] << (8 * b);
+            }
+        }
+        tile[k][c] = v;
+    }
+    __syncthreads();
+    // 8 terms of 4 rows a step: neighbouring threads take neighbouring terms of the same rows
+    for (int e = threadIdx.x; e < 8 * 32; e += 256) {
+        const int kk = 8 * (e & 7), c = e >> 3;
+        if (k0 + kk >= w.Kp)
+            continue;
+        uint32_t in[8], t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            in[i] = tile[kk + i][c];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // 4 x 4 bytes transposed
+            const uint32_t a = __byte_perm(in[4 * h], in[4 * h + 1], 0x5140), b = __byte_perm(in[4 * h], in[4 * h + 1], 0x7362);
+            const uint32_t c2 = __byte_perm(in[4 * h + 2], in[4 * h + 3], 0x5140), d = __byte_perm(in[4 * h + 2], in[4 * h + 3], 0x7362);
+            t[h] = __byte_perm(a, c2, 0x5410);
+            t[2 + h] = __byte_perm(a, c2, 0x7632);
+            t[4 + h] = __byte_perm(b, d, 0x5410);
+            t[6 + h] = __byte_perm(b, d, 0x7632);
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int64_t r = r0 + 4 * c + b;
+            if (r < w.rows) {
+                const uint2 x = widen4(t[2 * b]), y = widen4(t[2 * b + 1]);
+                *reinterpret_cast<uint4*>(w.out + r * w.Kp + k0 + kk) = make_uint4(x.x, x.y, y.x, y.y);
+            }
+        }
+    }
+}
+
+cudaError_t widen(const int8_t* q, int64_t ld, int64_t rows, int64_t K, bool t, __nv_bfloat16* out, cudaStream_t st)
+{
+    const size_t b = t ? 4 : 8;
+    Widen w = {q, ld, rows, K, pad8(K), out, reinterpret_cast<uintptr_t>(q) % b == 0 && ld % (int64_t)b == 0};
+    count_launches(1);
+    if (t) {
+        const int tiles_r = (int)((rows + 127) / 128);
+        return launch_pdl(k_mm_widen_t, dim3((unsigned)(tiles_r * ((K + 63) / 64))), dim3(256), 0, st, w, tiles_r);
+    }
+    const int64_t want = (rows * (w.Kp / 8) + 255) / 256, most = (int64_t)num_sms() * 8;
+    return launch_pdl(k_mm_widen, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, w);
+}
+
+// ---------------------------------------------------------------- what every path ends with
+
+template <typename Y> __device__ __forceinline__ void put(Y* p, float v, bool accumulate)
+{
+    if (accumulate)
+        v = fadd_ftz(to_f32<Y>(*p), v);
+    *p = from_f32<Y>(v);
+}
+
+__device__ __forceinline__ float scaled(int acc, bool has_a, float sa, bool has_b, float sb)
+{
+    float v = __int2float_rn(acc);
+    if (has_a)
+        v = fmul_flush(v, sa);
+    return has_b ? fmul_flush(v, sb) : v;
+}
+
+// ---------------------------------------------------------------- any shape on the CUDA cores
+
+constexpr int FT = 64, KW = 16;
+
+__device__ __forceinline__ int word_of(const int8_t* p, int64_t ld, bool t, int64_t row, int64_t rows, int64_t k, int64_t K)
+{
+    uint32_t w = 0;
+    if (row < rows)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (k + i < K)
+                w |= (uint32_t)(uint8_t)p[t ? (k + i) * ld + row : row * ld + k + i] << (8 * i);
+    return (int)w;
+}
+
+template <typename Y>
+__global__ void __launch_bounds__(256)
+k_mm_any(const __grid_constant__ MatmulI8Args g, int64_t tiles_n)
+{
+    __shared__ __align__(16) int As[KW][FT + 4];
+    __shared__ __align__(16) int Bs[KW][FT + 4];
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * FT, n0 = (int64_t)(blockIdx.x % tiles_n) * FT;
+    int acc[4][4] = {};
+    pdl_wait();
+    for (int64_t k0 = 0; k0 < g.K; k0 += 4 * KW) {
+        for (int e = tid; e < FT * KW; e += 256) {
+            const int ra = g.a_t ? e % FT : e / KW, wa = g.a_t ? e / FT : e % KW;
+            const int rb = g.b_t ? e % FT : e / KW, wb = g.b_t ? e / FT : e % KW;
+            As[wa][ra] = word_of(g.a, g.a_ld, g.a_t, m0 + ra, g.M, k0 + 4 * wa, g.K);
+            Bs[wb][rb] = word_of(g.b, g.b_ld, g.b_t, n0 + rb, g.N, k0 + 4 * wb, g.K);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+            const int4 a = *reinterpret_cast<const int4*>(&As[w][4 * ty]), b = *reinterpret_cast<const int4*>(&Bs[w][4 * tx]);
+            const int av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] = __dp4a(av[i], bv[j], acc[i][j]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t m = m0 + 4 * ty + i, n = n0 + 4 * tx + j;
+            if (m < g.M && n < g.N)
+                put(static_cast<Y*>(g.y) + m * g.y_ld + n,
+                    scaled(acc[i][j], g.s_a, g.s_a ? flush(__ldg(g.s_a + m)) : 0.0f, g.s_b, g.s_b ? flush(__ldg(g.s_b + n)) : 0.0f),
+                    g.accumulate);
+        }
+}
+
+// ---------------------------------------------------------------- few rows of A: the weights' bytes
+
+constexpr int RM = 8;    // rows of A a pass
+
+// codes k .. k + 15 of a row of K, 0 past its end
+template <bool VEC> __device__ __forceinline__ int4 codes16(const int8_t* p, int64_t k, int64_t K)
+{
+    if (VEC)
+        return __ldg(reinterpret_cast<const int4*>(p + k));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (k + e < K)
+            w[e >> 2] |= (uint32_t)(uint8_t)__ldg(p + k + e) << (8 * (e & 3));
+    return make_int4((int)w[0], (int)w[1], (int)w[2], (int)w[3]);
+}
+
+// A warp takes a row of B at a time, 16 codes a lane, against up to R rows of A (out of L1).
+// VEC: rows of both on 16-byte boundaries and K a multiple of 16.
+template <typename Y, int R, bool VEC>
+__global__ void __launch_bounds__(128)
+k_mm_rows(const __grid_constant__ MatmulI8Args g)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), m0 = (int64_t)blockIdx.y * R;
+    pdl_wait();
+    if (n >= g.N)
+        return;
+    int acc[R] = {};
+    const int8_t* b = g.b + n * g.b_ld;
+    const int8_t* a = g.a + m0 * g.a_ld;
+#pragma unroll 4
+    for (int64_t k = 16 * lane; k < g.K; k += 512) {
+        const int4 v = codes16<VEC>(b, k, g.K);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (R > 1 && m0 + r >= g.M)
+                break;
+            const int4 x = codes16<VEC>(a + r * g.a_ld, k, g.K);
+            acc[r] = __dp4a(x.x, v.x, __dp4a(x.y, v.y, __dp4a(x.z, v.z, __dp4a(x.w, v.w, acc[r]))));
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        acc[r] = __reduce_add_sync(0xffffffffu, acc[r]);
+    int mine = acc[0];
+#pragma unroll
+    for (int r = 1; r < R; ++r)
+        mine = lane == r ? acc[r] : mine;
+    if (lane < R && m0 + lane < g.M)
+        put(static_cast<Y*>(g.y) + (m0 + lane) * g.y_ld + n,
+            scaled(mine, g.s_a, g.s_a ? flush(__ldg(g.s_a + m0 + lane)) : 0.0f, g.s_b, g.s_b ? flush(__ldg(g.s_b + n)) : 0.0f),
+            g.accumulate);
+}
+
+template <typename Y> cudaError_t run_rows(const MatmulI8Args& g, cudaStream_t st)
+{
+    const bool vec = reinterpret_cast<uintptr_t>(g.a) % 16 == 0 && reinterpret_cast<uintptr_t>(g.b) % 16 == 0 &&
+                     (g.M == 1 || g.a_ld % 16 == 0) && (g.N == 1 || g.b_ld % 16 == 0) && g.K % 16 == 0;
+    const dim3 grid((unsigned)((g.N + 3) / 4), (unsigned)(g.M == 1 ? 1 : (g.M + RM - 1) / RM));
+    count_launches(1);
+    if (g.M == 1)
+        return vec ? launch_pdl(k_mm_rows<Y, 1, true>, grid, dim3(128), 0, st, g)
+                   : launch_pdl(k_mm_rows<Y, 1, false>, grid, dim3(128), 0, st, g);
+    return vec ? launch_pdl(k_mm_rows<Y, RM, true>, grid, dim3(128), 0, st, g)
+               : launch_pdl(k_mm_rows<Y, RM, false>, grid, dim3(128), 0, st, g);
+}
+
+// ---------------------------------------------------------------- tensor cores, two SMs a tile
+
+constexpr int HM = 128;                   // rows of a tile that one CTA of the pair holds
+constexpr int TN = 256;
+constexpr int TK = 64;                    // terms a stage: one 128-byte swizzle row of bf16
+constexpr int SLICE_KB = 8;               // stages an exact slice: 8 * 64 = 512 terms
+constexpr int STAGES = 6;
+constexpr int HALF_BYTES = HM * TK * 2;   // 16 KB: a CTA's rows of A, and as much of B
+constexpr int STAGE_BYTES = 2 * HALF_BYTES;
+constexpr int NBUF = 2;                   // accumulators of 256 columns
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int EPI_WARPS = 8;
+constexpr int STG_BYTES = 4096;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+
+struct Smem {
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t dfull[NBUF];
+    uint64_t dempty[NBUF];
+    uint64_t done;
+    uint32_t tmem_base;
+    int failed;
+};
+constexpr size_t SMEM_BYTES = 1024 + (size_t)STAGES * STAGE_BYTES + EPI_WARPS * STG_BYTES + 256;
+static_assert(sizeof(Smem) <= 256 && SMEM_BYTES <= 227 * 1024, "fits one SM's shared memory");
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// the address of this CTA's variable in CTA `rank` of the pair
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(su32(p)), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void arrive_at(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// mbar_wait with the other CTA's arrivals among those that are waited for
+__device__ __forceinline__ bool wait_pair(uint64_t* b, uint32_t parity)
+{
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(su32(b)), "r"(parity)
+            : "memory");
+        if (ok)
+            return true;
+        if (clock64() - t0 > WAIT_CYCLES)
+            return false;
+    }
+}
+
+// a tile into this CTA's shared memory, its bytes counted on a barrier of either CTA of the pair
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(su32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t dtmem, uint64_t a, uint64_t b, uint32_t acc)
+{
+    // kind::f16: fp32 accumulator, bf16 A and B, both K-major, M = 256, N = 256
+    constexpr uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(2 * HM >> 4) << 24);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtmem),
+        "l"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+}
+
+// arrives on the barrier at this place in both CTAs once the MMAs issued so far are done
+__device__ __forceinline__ void commit_pair(uint64_t* bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(su32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, const void* src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(su32(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+struct PairArgs {
+    MatmulI8Args g;
+    int K, tiles_n, tiles, y_tma;
+    int* err;
+};
+
+__device__ __forceinline__ void origin(const PairArgs& p, int t, int& m0, int& n0)
+{
+    m0 = (t / p.tiles_n) * 2 * HM;
+    n0 = (t % p.tiles_n) * TN;
+}
+
+template <typename Y>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+          const __grid_constant__ CUtensorMap map_y, const __grid_constant__ PairArgs p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = smem_raw + ((1024u - (su32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* A = base;                                   // STAGES x 16 KB
+    uint8_t* B = base + STAGES * HALF_BYTES;             // STAGES x 16 KB
+    uint8_t* STG = base + STAGES * STAGE_BYTES;          // EPI_WARPS x 4 KB
+    Smem* sm = reinterpret_cast<Smem*>(STG + EPI_WARPS * STG_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int KB = (p.K + TK - 1) / TK, NS = (KB + SLICE_KB - 1) / SLICE_KB;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&sm->full[s], 1);
+            mbar_init(&sm->empty[s], 1);
+        }
+        for (int d = 0; d < NBUF; ++d) {
+            mbar_init(&sm->dfull[d], 1);
+            mbar_init(&sm->dempty[d], 2 * EPI_WARPS);
+        }
+        mbar_init(&sm->done, 1);
+        sm->failed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_a)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_b)) : "memory");
+    }
+    __syncwarp();
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&sm->tmem_base)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+    fence_after();
+    const uint32_t tmem = sm->tmem_base;
+    pdl_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int g = 0;   // stages filled over all of this pair's tiles
+            for (int t = pair; t < p.tiles && !*(volatile int*)&sm->failed; t += pairs) {
+                int m0, n0;
+                origin(p, t, m0, n0);
+                for (int kb = 0; kb < KB; ++kb, ++g) {
+                    const int s = g % STAGES;
+                    if (g >= STAGES && !wait_pair(&sm->empty[s], ((g / STAGES) - 1) & 1)) {
+                        sm->failed = 1;
+                        break;
+                    }
+                    if (rank == 0)
+                        mbar_expect_tx(&sm->full[s], 2 * STAGE_BYTES);
+                    const uint32_t bar = peer_addr(&sm->full[s], 0);
+                    tma_load_pair(A + s * HALF_BYTES, &map_a, kb * TK, m0 + (int)rank * HM, bar);
+                    tma_load_pair(B + s * HALF_BYTES, &map_b, kb * TK, n0 + (int)rank * HM, bar);
+                }
+                if (*(volatile int*)&sm->failed)
+                    break;
+            }
+            // the leader sees both CTAs' last copies land before either can exit (cluster_sync below)
+            if (rank == 0)
+                for (int h = g - 1; h >= 0 && h >= g - STAGES; --h)
+                    if (!wait_pair(&sm->full[h % STAGES], (h / STAGES) & 1))
+                        sm->failed = 1;
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            bool ok = true;
+            int g = 0, sg = 0;   // stages and slices consumed over all tiles
+            for (int t = pair; t < p.tiles && ok; t += pairs) {
+                for (int kb = 0; kb < KB; ++kb, ++g) {
+                    const int s = g % STAGES, d = sg % NBUF;
+                    if (kb % SLICE_KB == 0 && sg >= NBUF && !wait_pair(&sm->dempty[d], ((sg / NBUF) - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!wait_pair(&sm->full[s], (g / STAGES) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint64_t a0 = sdesc(su32(A + s * HALF_BYTES)), b0 = sdesc(su32(B + s * HALF_BYTES));
+#pragma unroll
+                    for (int k = 0; k < TK / 16; ++k)
+                        mma_pair(tmem + (uint32_t)(d * TN), a0 + 2 * k, b0 + 2 * k, (kb % SLICE_KB != 0 || k != 0) ? 1u : 0u);
+                    commit_pair(&sm->empty[s]);
+                    if (kb % SLICE_KB == SLICE_KB - 1 || kb == KB - 1) {
+                        commit_pair(&sm->dfull[d]);
+                        ++sg;
+                    }
+                }
+            }
+            if (!ok)
+                sm->failed = 1;
+            // every MMA issued here has completed once `done` fires (in both CTAs)
+            commit_pair(&sm->done);
+            if (!wait_pair(&sm->done, 0))
+                sm->failed = 1;
+        }
+    } else {
+        // epilogue: rows m0 + 128 rank + 32 q + lane, columns n0 + 128 h .. + 127
+        const int q = warp & 3, ew = warp - 2, h = ew >> 2;
+        const MatmulI8Args& g = p.g;
+        uint8_t* stg = STG + ew * STG_BYTES;
+        const uint32_t lead[NBUF] = {peer_addr(&sm->dempty[0], 0), peer_addr(&sm->dempty[1], 0)};
+        bool ok = true;
+        int sg = 0;
+        for (int t = pair; t < p.tiles && ok; t += pairs) {
+            int m0, n0;
+            origin(p, t, m0, n0);
+            const int nc = n0 + 128 * h, r0 = m0 + (int)rank * HM + 32 * q;
+            int acc[128];
+#pragma unroll
+            for (int j = 0; j < 128; ++j)
+                acc[j] = 0;
+            for (int sl = 0; sl < NS; ++sl, ++sg) {
+                const int d = sg % NBUF;
+                if (!wait_pair(&sm->dfull[d], (sg / NBUF) & 1)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t v[16];
+                    tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(d * TN + 128 * h + 16 * c), v);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        acc[16 * c + e] += __float2int_rn(__uint_as_float(v[e]));
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    arrive_at(lead[d]);
+            }
+            if (!ok)
+                break;
+            const float sa = g.s_a && r0 + lane < g.M ? flush(__ldg(g.s_a + r0 + lane)) : 0.0f;
+            constexpr int W = 128 / (int)sizeof(Y);   // columns of a 128-byte staging row
+#pragma unroll
+            for (int c = 0; c < 128 / W; ++c) {
+                const int nb = nc + W * c;
+                if (r0 >= g.M || nb >= g.N)   // warp-uniform
+                    continue;
+                // the old values of this row: a reduction in L2 would not flush subnormals
+                float old[sizeof(Y) == 4 ? W : 1];
+                if (sizeof(Y) == 4 && p.y_tma && g.accumulate && r0 + lane < g.M) {
+                    const float* src = static_cast<const float*>(g.y) + (int64_t)(r0 + lane) * g.y_ld + nb;
+                    if (nb + W <= g.N) {
+#pragma unroll
+                        for (int k = 0; k < W / 4; ++k) {
+                            const float4 v = load4(src + 4 * k);
+                            old[4 * k] = v.x, old[4 * k + 1] = v.y, old[4 * k + 2] = v.z, old[4 * k + 3] = v.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < W; ++j)
+                            old[j] = nb + j < g.N ? src[j] : 0.0f;
+                    }
+                }
+                if (p.y_tma) {
+                    if (lane == 0)
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {   // 16 bytes a step
+                    float o[W / 8];
+#pragma unroll
+                    for (int e = 0; e < W / 8; ++e) {
+                        const int j = W / 8 * k + e;
+                        const float sb = g.s_b && nb + j < g.N ? flush(__ldg(g.s_b + nb + j)) : 0.0f;
+                        o[e] = scaled(acc[W * c + j], g.s_a, sa, g.s_b, sb);
+                    }
+                    if (p.y_tma) {
+                        if (sizeof(Y) == 4 && g.accumulate) {
+#pragma unroll
+                            for (int e = 0; e < W / 8; ++e)
+                                o[e] = fadd_ftz(old[W / 8 * k + e], o[e]);
+                        }
+                        store16(reinterpret_cast<Y*>(stg + lane * 128 + 16 * (k ^ (lane & 7))), o);
+                    } else if (r0 + lane < g.M) {
+#pragma unroll
+                        for (int e = 0; e < W / 8; ++e)
+                            if (nb + W / 8 * k + e < g.N)
+                                put(static_cast<Y*>(g.y) + (int64_t)(r0 + lane) * g.y_ld + nb + W / 8 * k + e, o[e], g.accumulate);
+                    }
+                }
+                if (p.y_tma) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)
+                        store_tile(&map_y, stg, nb, r0);
+                }
+            }
+        }
+        if (!ok && lane == 0)
+            sm->failed = 1;
+        if (lane == 0)
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    cluster_sync();   // no barrier, tile or tensor memory of either CTA is used past here
+    if (warp == 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+    if (threadIdx.x == 0 && sm->failed)
+        atomicOr(p.err, kErrTimeoutBit);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult qr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
+            qr != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+// rows of `cols` elements, `ld` apart; boxes of 128 bytes x box_rows, 128-byte swizzle
+bool make_map(CUtensorMap* map, const void* p, CUtensorMapDataType type, int size, int64_t rows, int64_t cols, int64_t ld,
+              int box_rows)
+{
+    const auto fn = encode_fn();
+    if (!fn)
+        return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * size};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, type, 2, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename Y> cudaError_t run_pair(const MatmulI8Args& g, const __nv_bfloat16* xa, const __nv_bfloat16* xb, cudaStream_t st)
+{
+    PairArgs p = {};
+    p.g = g;
+    p.K = (int)g.K;
+    p.tiles_n = (int)((g.N + TN - 1) / TN);
+    p.tiles = (int)((g.M + 2 * HM - 1) / (2 * HM)) * p.tiles_n;
+    p.err = device_error_word();
+    if (!p.err)
+        return cudaErrorInvalidValue;
+    CUtensorMap ma, mb, my;
+    memset(&my, 0, sizeof(my));
+    const int64_t Kp = pad8(g.K);
+    if (!make_map(&ma, xa, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.M, Kp, Kp, HM) ||
+        !make_map(&mb, xb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.N, Kp, Kp, HM))
+        return cudaErrorInvalidValue;
+    // tensor stores need rows on 16-byte boundaries
+    p.y_tma = reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && (g.M == 1 || g.y_ld * (int64_t)sizeof(Y) % 16 == 0);
+    const int64_t y_pitch = g.M == 1 ? (g.N + 7) / 8 * 8 : g.y_ld;
+    if (p.y_tma && !make_map(&my, g.y, sizeof(Y) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                             (int)sizeof(Y), g.M, g.N, y_pitch, 32))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(k_mm_pair<Y>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    if (e != cudaSuccess)
+        return e;
+    const int pairs = std::min(p.tiles, num_sms() / 2);
+    e = launch_pdl(k_mm_pair<Y>, dim3((unsigned)(2 * pairs)), dim3(THREADS), SMEM_BYTES, st, ma, mb, my, p);
+    count_launches(1);
+    return e;
+}
+
+template <typename Y> cudaError_t launch(const MatmulI8Args& g, void* ws, bool tc, cudaStream_t st)
+{
+    if (matmul_i8_small(g.M, g.a_t, g.b_t))
+        return run_rows<Y>(g, st);
+    if (!tc || g.K == 0) {
+        const int64_t tiles_n = (g.N + FT - 1) / FT, tiles = tiles_n * ((g.M + FT - 1) / FT);
+        count_launches(1);
+        return launch_pdl(k_mm_any<Y>, dim3((unsigned)tiles), dim3(256), 0, st, g, tiles_n);
+    }
+    __nv_bfloat16* xa = static_cast<__nv_bfloat16*>(ws);
+    __nv_bfloat16* xb = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(ws) + align256(2 * g.M * pad8(g.K)));
+    cudaError_t e = widen(g.a, g.a_ld, g.M, g.K, g.a_t, xa, st);
+    if (e == cudaSuccess)
+        e = widen(g.b, g.b_ld, g.N, g.K, g.b_t, xb, st);
+    return e == cudaSuccess ? run_pair<Y>(g, xa, xb, st) : e;
+}
+
+} // namespace
+
+bool matmul_i8_small(int64_t M, bool a_t, bool b_t) { return M <= 16 && !a_t && !b_t; }
+
+size_t matmul_i8_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_t, bool b_t)
+{
+    if (matmul_i8_small(M, a_t, b_t))
+        return 0;
+    return (size_t)(align256(2 * M * pad8(K)) + align256(2 * N * pad8(K)));
+}
+
+cudaError_t launch_matmul_i8(const MatmulI8Args& g, void* ws, bool tc, cudaStream_t st)
+{
+    return g.y_type == 0 ? launch<float>(g, ws, tc, st) : launch<__nv_bfloat16>(g, ws, tc, st);
+}
+
+} // namespace repro

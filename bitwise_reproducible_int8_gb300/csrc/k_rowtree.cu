@@ -30,9 +30,9 @@ k_row_tree(const __grid_constant__ RowTree t, int colsegs)
     for (int64_t item = blockIdx.x; item < joins * colsegs; item += gridDim.x) {
         const int64_t jn = item / colsegs;
         const int64_t c = (item - jn * colsegs) * (4 * LANES) + 4 * lane;
-        const int4 j = t.joins ? t.joins[jn] : make_int4(0, (int)t.count[jn != 0], 0, 0);
-        float* parts = t.joins || jn == 0 ? t.parts[0] : t.parts[1];
-        float* out = t.joins || jn == 0 ? t.out[0] : t.out[1];
+        const int4 j = t.joins ? t.joins[jn] : make_int4(0, (int)t.count[jn], 0, 0);
+        float* parts = t.parts[t.joins ? 0 : jn];
+        float* out = t.out[t.joins ? 0 : jn];
         const bool live = c < t.D;
         // partial row of chunk k: see the slot rule of the chunk list (k_embed.cu)
         auto row = [&](int64_t k) {

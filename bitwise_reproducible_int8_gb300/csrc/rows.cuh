@@ -1,0 +1,161 @@
+// rows.cuh -- rows held in the registers of a group of threads, 16 elements each.
+//
+// A row of D <= 16384 elements belongs to TPR threads, TPR the smallest power of two from
+// 32 on with 16 TPR >= D: thread t holds the groups of 4 neighbours t, t + TPR, t + 2 TPR
+// and t + 3 TPR, so that neighbouring threads load neighbouring 16 bytes, and the row's sum
+// has the order that these threads can add in: a thread's groups are one chain of S, the
+// tree over the chains is five exchanges inside a warp, one trip through shared memory and
+// up to five exchanges over the warps.
+#pragma once
+
+#include "elem.cuh"
+
+namespace repro {
+
+typedef unsigned long long u64;
+
+constexpr int ROW_E = 16;    // elements a thread holds of a row
+
+// threads of a row's group
+inline int row_threads(int64_t D)
+{
+    int t = 32;
+    while (ROW_E * (int64_t)t < D)
+        t *= 2;
+    return t;
+}
+
+// Where a thread stands in its row's group
+struct RowLane {
+    int t, tpr, D;      // thread in the group, threads of the group, width
+    int bar;            // named barrier of the group
+    bool vec;           // rows and strides on 4-element boundaries
+    __device__ __forceinline__ int at(int k) const { return 4 * (t + k * tpr); }   // first element of group k
+};
+
+__device__ __forceinline__ void group_barrier(const RowLane& r)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(r.bar), "r"(r.tpr) : "memory");
+}
+
+// FULL: D = 16 TPR and vec, nothing to check.  What lies past D reads as 0.
+template <bool FULL, bool STREAM, typename T>
+__device__ __forceinline__ void load_row16(const T* p, const RowLane& r, u64 (&v)[8])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int d = r.at(k);
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (FULL || (r.vec && d + 4 <= r.D)) {
+            x = STREAM ? stream4(p + d) : load4(p + d);
+        } else if (d < r.D) {
+            x.x = to_f32<T>(p[d]);
+            x.y = d + 1 < r.D ? to_f32<T>(p[d + 1]) : 0.0f;
+            x.z = d + 2 < r.D ? to_f32<T>(p[d + 2]) : 0.0f;
+            x.w = d + 3 < r.D ? to_f32<T>(p[d + 3]) : 0.0f;
+        }
+        v[2 * k] = pack2(x.x, x.y);
+        v[2 * k + 1] = pack2(x.z, x.w);
+    }
+}
+
+template <bool FULL, typename T>
+__device__ __forceinline__ void store_row16(T* p, const RowLane& r, const u64 (&v)[8])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int d = r.at(k);
+        float4 x;
+        unpack2(v[2 * k], x.x, x.y);
+        unpack2(v[2 * k + 1], x.z, x.w);
+        if (FULL || (r.vec && d + 4 <= r.D)) {
+            store4(p + d, x);
+        } else if (d < r.D) {
+            p[d] = from_f32<T>(x.x);
+            if (d + 1 < r.D)
+                p[d + 1] = from_f32<T>(x.y);
+            if (d + 2 < r.D)
+                p[d + 2] = from_f32<T>(x.z);
+            if (d + 3 < r.D)
+                p[d + 3] = from_f32<T>(x.w);
+        }
+    }
+}
+
+__device__ __forceinline__ void flush16(u64 (&v)[8])
+{
+    const u64 z = pack2(-0.0f, -0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = fadd2_ftz(v[i], z);
+}
+
+// v (x) w, flushed (both operands flushed already)
+__device__ __forceinline__ void mul16(u64 (&v)[8], const u64 (&w)[8])
+{
+    const u64 z = pack2(-0.0f, -0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = fadd2_ftz(fmul2_rn(v[i], w[i]), z);
+}
+
+__device__ __forceinline__ void mul16(u64 (&v)[8], float w)
+{
+    const u64 z = pack2(-0.0f, -0.0f), ww = pack2(w, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = fadd2_ftz(fmul2_rn(v[i], ww), z);
+}
+
+// this thread's chain of S(a (x) b); terms past the width count as -0, which leaves a sum alone
+template <bool FULL>
+__device__ __forceinline__ float chain16(const u64 (&a)[8], const u64 (&b)[8], const RowLane& r)
+{
+    float s = -0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float p[4];
+        unpack2(fmul2_rn(a[2 * k], b[2 * k]), p[0], p[1]);
+        unpack2(fmul2_rn(a[2 * k + 1], b[2 * k + 1]), p[2], p[3]);
+        if (!FULL) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                p[e] = r.at(k) + e < r.D ? p[e] : -0.0f;
+        }
+        const float g = fadd_ftz(fadd_ftz(fadd_ftz(p[0], p[1]), p[2]), p[3]);
+        s = k == 0 ? g : fadd_ftz(s, g);
+    }
+    return s;
+}
+
+// the tree over the group's chains, the same bits in every thread.  red: 64 floats of the
+// group in shared memory, used in halves by turns (phase), so that one barrier a sum is enough
+__device__ __forceinline__ float tree_of_chains(float v, const RowLane& r, float* red, int& phase)
+{
+    constexpr unsigned ALL = 0xffffffffu;
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2)
+        v = fadd_ftz(v, __shfl_xor_sync(ALL, v, s));
+    if (r.tpr == 32)
+        return v;
+    const int lane = r.t & 31, warps = r.tpr >> 5;
+    float* half = red + 32 * phase;
+    phase ^= 1;
+    if (lane == 0)
+        half[r.t >> 5] = v;
+    group_barrier(r);
+    v = lane < warps ? half[lane] : -0.0f;
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2)
+        if (s < warps)
+            v = fadd_ftz(v, __shfl_xor_sync(ALL, v, s));
+    return __shfl_sync(ALL, v, 0);
+}
+
+// S (/) D; by an exact product where D is a power of two (inv = 1 / D, else 0)
+__device__ __forceinline__ float mean_of(float S, float width, float inv)
+{
+    return inv != 0.0f ? fmul_flush(S, inv) : flush(__fdiv_rn(S, width));
+}
+
+} // namespace repro

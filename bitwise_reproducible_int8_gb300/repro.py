@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 import re
 
@@ -41,6 +42,13 @@ REPRO_DISTILL_BLOCK = 1024
 REPRO_DISTILL_STATS = 8
 REPRO_DISTILL_STAT_LSE = 2
 REPRO_DISTILL_LOGPROBS = 1
+REPRO_NORM_POST, REPRO_NORM_GATE_ROWS = 4, 8
+REPRO_NORM_MAX_D = 16384
+REPRO_NORM_CHUNK = 16
+REPRO_QUANT_COLUMNS = 1
+REPRO_MM_A_T, REPRO_MM_B_T = 2, 4
+REPRO_MM_MAX_ROWS = 4194240
+REPRO_SWIGLU_GROUP = 128
 
 
 class ReproError(RuntimeError):
@@ -117,6 +125,18 @@ _SIGNATURES = {
     "repro_distill_ws_bytes": (_sz, [_i64, _i64]),
     "repro_distill_bwd": (_int, [_vp, _int, _i64, _vp, _vp, _int, _i64, _i64, _i64,
                                  ctypes.POINTER(DistillHparams), _vp, _vp, _i64, _vp, _i64, _vp]),
+    "repro_block_norm_fwd": (_int, [_vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _vp, *[ctypes.c_float] * 3, _i64, _i64,
+                                    _int, _vp, _i64, _vp, _int, _i64, _vp, _vp]),
+    "repro_block_norm_bwd": (_int, [_vp, _i64, _vp, _int, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _vp, _vp,
+                                    ctypes.c_float, ctypes.c_float, _i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _i64,
+                                    _vp, _vp, _vp, _sz, _vp]),
+    "repro_block_norm_bwd_ws_bytes": (_sz, [_i64, _i64]),
+    "repro_quant_rows_i8": (_int, [_vp, _int, _i64, _vp, _i64, _i64, _int, _vp, _i64, _vp, _vp, _sz, _vp]),
+    "repro_quant_rows_i8_ws_bytes": (_sz, [_i64, _i64, _int]),
+    "repro_matmul_i8": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _vp, _int, _i64, _vp, _sz, _vp]),
+    "repro_matmul_i8_ws_bytes": (_sz, [_i64, _i64, _i64, _int]),
+    "repro_swiglu_fwd": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _int, _i64, _vp, _vp, _vp]),
+    "repro_swiglu_bwd": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _int, _i64, _vp]),
     "repro_selftest": (_int, [_vp, _sz, _vp]),
     "repro_selftest_ws_bytes": (_sz, []),
     "repro_status_str": (ctypes.c_char_p, [_int]),
@@ -640,6 +660,198 @@ def repro_distill_bwd(logits: torch.Tensor, t_idx: torch.Tensor, stats: torch.Te
         _dev_ptr(logits, "logits", False), _float_type(logits, "logits"), ld, _dev_ptr(t_idx, "t_idx"),
         _dev_ptr(labels, "labels"), ib, n, V, K, ctypes.byref(hp), _ptr(stats, torch.float32, "stats"),
         _ptr(g, torch.float32, "g"), g.numel(), _dev_ptr(dlogits, "dlogits", False), dld, _stream(stream)))
+
+
+def _like(t, shape, name):
+    """Strided rows of t, which has to have this shape: (pointer, row stride)."""
+    if t is None:
+        return None, shape[-1]
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _dev_ptr(t, name, False), _rows2d(t, name)[2]
+
+
+def _one_type(kind, name, *ts):
+    if any(t is not None and t.dtype != kind for t in ts):
+        raise ValueError(f"{name} must be of one type")
+
+
+def _gate(gate, shape, dtype, name):
+    """(pointer, row stride, flag) of a gate [D] float32, or of the stream's shape and type."""
+    if gate is None:
+        return None, shape[-1], 0
+    if gate.dim() == 1 and len(shape) > 1:
+        if gate.numel() != shape[-1]:
+            raise ValueError(f"{name} must be [D] or have the stream's shape")
+        return _ptr(gate, torch.float32, name), shape[-1], 0
+    _one_type(dtype, f"{name} and the stream", gate)
+    return *_like(gate, shape, name), REPRO_NORM_GATE_ROWS
+
+
+def _gain(t, D, name):
+    if t is not None and t.numel() != D:
+        raise ValueError(f"{name} must have D elements")
+    return _ptr(t, torch.float32, name)
+
+
+def repro_block_norm_fwd(x: torch.Tensor, y, h, u, stats=None, gate=None, g_post=None, g_pre=None,
+                         post: bool = False, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6,
+                         stream=None) -> None:
+    """h <- x alpha + beta gate post(y), u <- the RMS norm of h with gain g_pre [D]; post(y)
+    is the RMS norm of y with gain g_post [D] (with post), else y.  x, y, h [..., D] float32
+    or bfloat16 (h may be x); u [..., D] of either type, or None; gate [D] float32, or of x's
+    shape and type.  y and h None: the norm of x alone.  stats [n, 2] float32 (or None) is the
+    backward's input.  Rows at any stride; gains None: none."""
+    n, D, x_ld = _rows2d(x, "x")
+    kind = _float_type(x, "x")
+    _one_type(x.dtype, "x, y and h", y, h)
+    yp, y_ld = _like(y, x.shape, "y")
+    hp, h_ld = _like(h, x.shape, "h")
+    up, u_ld = _like(u, x.shape, "u")
+    gp, gate_ld, rows = _gate(gate, x.shape, x.dtype, "gate")
+    if stats is not None and stats.numel() != 2 * n:
+        raise ValueError("stats must be [n, 2]")
+    _check("repro_block_norm_fwd", lib().repro_block_norm_fwd(
+        _dev_ptr(x, "x", False), x_ld, yp, y_ld, kind, gp, gate_ld, _gain(g_post, D, "g_post"),
+        _gain(g_pre, D, "g_pre"), alpha, beta, eps, n, D, (REPRO_NORM_POST if post else 0) | rows, hp, h_ld, up,
+        REPRO_F32 if u is None else _float_type(u, "u"), u_ld, _ptr(stats, torch.float32, "stats"), _stream(stream)))
+
+
+def repro_block_norm_bwd_ws_bytes(n: int, D: int) -> int:
+    return int(lib().repro_block_norm_bwd_ws_bytes(int(n), int(D)))
+
+
+def repro_block_norm_bwd(dh, du, h, y, stats: torch.Tensor, dx: torch.Tensor, dy, gate=None, dgate=None, g_post=None,
+                         g_pre=None, dg_post=None, dg_pre=None, post: bool = False, alpha: float = 1.0,
+                         beta: float = 1.0, accumulate: bool = False, ws=None, stream=None) -> None:
+    """dx, dy and the gradients of gate and gains from dh (of the stream, or None), du (of u,
+    or None; h, the stream as the forward wrote it, goes with it), y and the forward's stats.
+    dx may be dh.  accumulate: the sums over tokens (gains, a gate [D]) are added to."""
+    n, D, dx_ld = _rows2d(dx, "dx")
+    kind = _float_type(dx, "dx")
+    _one_type(dx.dtype, "dh, h, y, dx and dy", dh, h, y, dy)
+    dhp, dh_ld = _like(dh, dx.shape, "dh")
+    dup, du_ld = _like(du, dx.shape, "du")
+    hp, h_ld = _like(h, dx.shape, "h")
+    yp, y_ld = _like(y, dx.shape, "y")
+    dyp, dy_ld = _like(dy, dx.shape, "dy")
+    gp, gate_ld, rows = _gate(gate, dx.shape, dx.dtype, "gate")
+    dgp, dgate_ld, drows = _gate(dgate, dx.shape, dx.dtype, "dgate")
+    if gate is not None and dgate is not None and rows != drows:
+        raise ValueError("dgate must have the gate's shape")
+    if stats.numel() != 2 * n:
+        raise ValueError("stats must be [n, 2]")
+    if ws is None and (dg_post is not None or dg_pre is not None or (dgate is not None and not drows)):
+        ws = _workspace(repro_block_norm_bwd_ws_bytes(n, D), dx.device, stream)
+    flags = (REPRO_NORM_POST if post else 0) | rows | (REPRO_BWD_DW_ACCUMULATE if accumulate else 0)
+    _check("repro_block_norm_bwd", lib().repro_block_norm_bwd(
+        dhp, dh_ld, dup, REPRO_F32 if du is None else _float_type(du, "du"), du_ld, hp, h_ld, yp, y_ld, kind, gp, gate_ld,
+        _gain(g_post, D, "g_post"), _gain(g_pre, D, "g_pre"), _ptr(stats, torch.float32, "stats"), alpha, beta, n, D,
+        flags, _dev_ptr(dx, "dx", False), dx_ld, dyp, dy_ld, dgp, dgate_ld, _gain(dg_post, D, "dg_post"),
+        _gain(dg_pre, D, "dg_pre"), _dev_ptr(ws, "ws"), ws.numel() * ws.element_size() if ws is not None else 0,
+        _stream(stream)))
+
+
+def repro_quant_rows_i8_ws_bytes(n: int, D: int, columns: bool = False) -> int:
+    return int(lib().repro_quant_rows_i8_ws_bytes(int(n), int(D), REPRO_QUANT_COLUMNS if columns else 0))
+
+
+def repro_quant_rows_i8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, mul=None, columns: bool = False, ws=None,
+                        stream=None) -> None:
+    """q <- int8 codes of x [..., D] with a scale for each row (scales [n]) or, with columns,
+    for each column (scales [D]); with mul, of x (x) mul, mul [D] (columns: [n])."""
+    n, D, x_ld = _rows2d(x, "x")
+    qp, q_ld = _like(q, x.shape, "q")
+    if q.dtype != torch.int8:
+        raise ValueError(f"q must be {torch.int8}, got {q.dtype}")
+    if scales.numel() != (D if columns else n) or (mul is not None and mul.numel() != (n if columns else D)):
+        raise ValueError("scales must have an entry per row (column), mul one per column (row)")
+    if ws is None and columns:
+        ws = _workspace(repro_quant_rows_i8_ws_bytes(n, D, True), x.device, stream)
+    _check("repro_quant_rows_i8", lib().repro_quant_rows_i8(
+        _dev_ptr(x, "x", False), _float_type(x, "x"), x_ld, _ptr(mul, torch.float32, "mul"), n, D,
+        REPRO_QUANT_COLUMNS if columns else 0, qp, q_ld, _ptr(scales, torch.float32, "scales"), _dev_ptr(ws, "ws"),
+        ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
+
+
+def _codes2d(t, name):
+    """_rows2d that keeps the rows of a matrix without columns."""
+    n, D, ld = _rows2d(t, name)
+    return (n if D else math.prod(t.shape[:-1])), D, ld
+
+
+def _mm_flags(trans_a, trans_b, accumulate=False) -> int:
+    return (REPRO_MM_A_T if trans_a else 0) | (REPRO_MM_B_T if trans_b else 0) | \
+        (REPRO_BWD_DW_ACCUMULATE if accumulate else 0)
+
+
+def repro_matmul_i8_ws_bytes(M: int, N: int, K: int, trans_a: bool = False, trans_b: bool = False) -> int:
+    return int(lib().repro_matmul_i8_ws_bytes(int(M), int(N), int(K), _mm_flags(trans_a, trans_b)))
+
+
+def repro_matmul_i8(a: torch.Tensor, b: torch.Tensor, y: torch.Tensor, s_a=None, s_b=None, trans_a: bool = False,
+                    trans_b: bool = False, accumulate: bool = False, ws=None, stream=None) -> None:
+    """y [M, N] <- (or (+)=) the exact product of int8 codes a [M, K] (trans_a: [K, M]) and b
+    [N, K] (trans_b: [K, N]), times the scales s_a [M] and s_b [N] (None: left out).  y float32,
+    or bfloat16 without accumulate; rows at any stride."""
+    ar, ac, a_ld = _codes2d(a, "a")
+    br, bc, b_ld = _codes2d(b, "b")
+    My, Ny, y_ld = _rows2d(y, "y")
+    M, K = (ac, ar) if trans_a else (ar, ac)
+    N, K2 = (bc, br) if trans_b else (br, bc)
+    if K != K2 or (My, Ny) != (M, N):
+        raise ValueError("shape mismatch: a [M, K] or [K, M], b [N, K] or [K, N], y [M, N]")
+    if a.dtype != torch.int8 or b.dtype != torch.int8:
+        raise ValueError("a and b must be int8 codes")
+    kind = _float_type(y, "y")
+    if (s_a is not None and s_a.numel() != M) or (s_b is not None and s_b.numel() != N):
+        raise ValueError("s_a must be [M], s_b [N]")
+    if ws is None:
+        need = repro_matmul_i8_ws_bytes(M, N, K, trans_a, trans_b)
+        ws = _workspace(need, y.device, stream) if need > 0 else None
+    f32 = torch.float32
+    _check("repro_matmul_i8", lib().repro_matmul_i8(
+        _dev_ptr(a, "a", False), a_ld, _dev_ptr(b, "b", False), b_ld, _ptr(s_a, f32, "s_a"), _ptr(s_b, f32, "s_b"), M, N, K,
+        _mm_flags(trans_a, trans_b, accumulate), _dev_ptr(y, "y", False), kind, y_ld, _dev_ptr(ws, "ws"),
+        ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
+
+
+def _kept(codes, scales, n, F):
+    if codes is None and scales is None:
+        return None, None
+    G = -(-F // REPRO_SWIGLU_GROUP)
+    if codes is None or scales is None or codes.numel() != 2 * n * G * REPRO_SWIGLU_GROUP or scales.numel() != 2 * n * G:
+        raise ValueError("codes must be [n, 2, G, 128] and scales [n, 2, G], G = ceil(F / 128)")
+    return _ptr(codes, torch.int8, "codes"), _ptr(scales, torch.float32, "scales")
+
+
+def repro_swiglu_fwd(gu: torch.Tensor, a: torch.Tensor, codes=None, scales=None, stream=None) -> None:
+    """a [..., F] <- silu(gate) up of gu [..., 2 F] (gate, then up); with codes [n, 2, G, 128]
+    int8 and scales [n, 2, G] float32 (G = ceil(F / 128)) also the 8-bit copy of gate and up,
+    groups of 128 neighbours to a scale.  gu, a float32 or bfloat16, rows at any stride."""
+    n, F2, gu_ld = _rows2d(gu, "gu")
+    na, F, a_ld = _rows2d(a, "a")
+    if F2 != 2 * F or na != n:
+        raise ValueError("shape mismatch: gu [..., 2 F], a [..., F]")
+    cp, sp = _kept(codes, scales, n, F)
+    _check("repro_swiglu_fwd", lib().repro_swiglu_fwd(
+        _dev_ptr(gu, "gu", False), _float_type(gu, "gu"), gu_ld, n, F, _dev_ptr(a, "a", False), _float_type(a, "a"), a_ld,
+        cp, sp, _stream(stream)))
+
+
+def repro_swiglu_bwd(da: torch.Tensor, dgu: torch.Tensor, gu=None, codes=None, scales=None, stream=None) -> None:
+    """dgu [..., 2 F] from da [..., F] and the forward's gu, or its 8-bit copy (codes, scales)."""
+    n, F, da_ld = _rows2d(da, "da")
+    nd, F2, dgu_ld = _rows2d(dgu, "dgu")
+    if F2 != 2 * F or nd != n:
+        raise ValueError("shape mismatch: da [..., F], dgu [..., 2 F]")
+    if gu is not None:
+        _one_type(dgu.dtype, "gu and dgu", gu)
+    gp, gu_ld = _like(gu, dgu.shape, "gu")
+    cp, sp = _kept(codes, scales, n, F)
+    _check("repro_swiglu_bwd", lib().repro_swiglu_bwd(
+        _dev_ptr(da, "da", False), _float_type(da, "da"), da_ld, gp, gu_ld, cp, sp, n, F, _dev_ptr(dgu, "dgu", False),
+        _float_type(dgu, "dgu"), dgu_ld, _stream(stream)))
 
 
 def repro_selftest(device=None, stream=None) -> int:

@@ -514,6 +514,123 @@ int repro_distill_bwd(const void* z, int z_type, int64_t z_ld, const void* t_idx
                       int64_t g_n, void* dz, int64_t dz_ld, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The feed-forward half of a decoder block around its 8-bit products, and the norms
+ * between the halves.  The pages name the model's RMS norms and its gated activation
+ * (neither quantised there) and quantise every linear with one scale a tensor; scales
+ * for each token and each output channel, and the 8-bit copy of the activation's inputs,
+ * are the library's.  Types, strides, alignment and arithmetic as above.
+ * ------------------------------------------------------------------------ */
+
+/* Norms behind and before a block, with its gate and the residual scales.  For token i,
+ * x the residual stream, y the block's output:
+ *   S(t) of D terms: groups of 4 consecutive terms left to right; with C the smallest power of
+ *     two from 32 on that has 16 C >= D, group g in chain g mod C, each chain ascending, the
+ *     chains by the stride-doubling pairwise tree;
+ *   rms(v) = 1 (/) sqrt((S(v_d (x) v_d) (/) D) (+) eps);
+ *   p_d = (y_d (x) r1) (x) gain_post_d, r1 = rms(y), with REPRO_NORM_POST (gain_post may be NULL),
+ *     else p_d = y_d;  then p_d (x) gate_d where a gate is given;
+ *   h_d = (x_d (x) alpha) (+) (p_d (x) beta), rounded once more where it is bf16;
+ *   u_d = (h_d (x) r2) (x) gain_pre_d, r2 = rms(h), of h as it is stored (gain_pre may be NULL).
+ * y NULL: h is x (h, gate and gain_post NULL, flags 0; alpha and beta are not looked at), the
+ * norm before a block alone.  u NULL: no norm of h (gain_pre NULL).  One of y and u is given.
+ * gate: with REPRO_NORM_GATE_ROWS a row for each token, gate_ld apart, in x's type; else one row
+ * [D] fp32 for all.  x, y, h: `type`; u: u_type.  h may be x itself (same pointer and stride).
+ * stats [n][2] fp32 (dense; NULL: not wanted): r1 (0 without a post norm) and r2 (0 without u).
+ * 1 <= D <= REPRO_NORM_MAX_D, eps >= 0, alpha and beta finite. */
+#define REPRO_NORM_POST 4
+#define REPRO_NORM_GATE_ROWS 8
+#define REPRO_NORM_MAX_D 16384
+#define REPRO_NORM_CHUNK 16
+int repro_block_norm_fwd(const void* x, int64_t x_ld, const void* y, int64_t y_ld, int type,
+                         const void* gate, int64_t gate_ld, const float* gain_post,
+                         const float* gain_pre, float alpha, float beta, float eps, int64_t n,
+                         int64_t D, int flags, void* h, int64_t h_ld, void* u, int u_type,
+                         int64_t u_ld, float* stats, void* stream);
+
+/* Its backward, from the gradients dh of the stream (NULL: none) and du of u (NULL: none; h,
+ * gain_pre and dgain_pre are then NULL), the stream h as the forward wrote it (x without y), y,
+ * and the forward's stats:
+ *   hn_d = h_d (x) r2;  v_d = du_d (x) gain_pre_d;  c = S(v_d (x) hn_d) (/) D;
+ *   g_d = dh_d (+) (r2 (x) (v_d (-) (hn_d (x) c)))  (without dh, or without du, the other alone);
+ *   dx_d = g_d (x) alpha (g_d without y);  b_d = g_d (x) beta;
+ *   yn_d = y_d (x) r1 and p_d = yn_d (x) gain_post_d with REPRO_NORM_POST, else p_d = y_d;
+ *   dgate_d = b_d (x) p_d;  q_d = b_d (x) gate_d (b_d without a gate);
+ *   dy_d = q_d, or with REPRO_NORM_POST, w_d = q_d (x) gain_post_d and c' = S(w_d (x) yn_d) (/) D,
+ *     dy_d = r1 (x) (w_d (-) (yn_d (x) c'));
+ *   dgain_pre_d = sum over tokens of du_d (x) hn_d;  dgain_post_d of q_d (x) yn_d;  the gradient of
+ *     a gate that is one row, of dgate_d: tokens in chunks of REPRO_NORM_CHUNK consecutive ones,
+ *     each left to right, the chunks by the stride-doubling pairwise tree; +0 for no tokens, and
+ *     (+) into the old value with REPRO_BWD_DW_ACCUMULATE.
+ * A gradient is required for each gain and gate given, else NULL; a gate's has the gate's type
+ * and form (rows dgate_ld apart).  dx may be dh itself (same pointer and stride).  dy NULL without
+ * y.  ws: repro_block_norm_bwd_ws_bytes(n, D) bytes, needed when a sum over tokens is. */
+int repro_block_norm_bwd(const void* dh, int64_t dh_ld, const void* du, int u_type, int64_t du_ld,
+                         const void* h, int64_t h_ld, const void* y, int64_t y_ld, int type,
+                         const void* gate, int64_t gate_ld, const float* gain_post,
+                         const float* gain_pre, const float* stats, float alpha, float beta,
+                         int64_t n, int64_t D, int flags, void* dx, int64_t dx_ld, void* dy,
+                         int64_t dy_ld, void* dgate, int64_t dgate_ld, float* dgain_post,
+                         float* dgain_pre, void* ws, size_t ws_bytes, void* stream);
+size_t repro_block_norm_bwd_ws_bytes(int64_t n, int64_t D);
+
+/* 8-bit codes with a scale for each row of x [n][D] (a token, an output channel of a weight), or
+ * with REPRO_QUANT_COLUMNS for each column:
+ *   v_id = x_id, or x_id (x) mul_d with mul [D] (columns: x_id (x) mul_i, mul [n]);
+ *   s = (max |v|) (/) 127 over the row (column), as REPRO_SCALE_ACT_AMAX (a NaN is passed over);
+ *   q = clamp(round_half_even(v (/) s), -127, 127), as repro_quant_i8 (s = 0: q = 0).
+ * mul folds the other side's scales into a gradient before it becomes codes: dX = dY (s_w W) and
+ * dW = (dY s_x)^T X are then products of codes (repro_matmul_i8).  x: `type`, rows x_ld apart; q
+ * rows q_ld apart; scales [n] (columns: [D]) fp32.  ws: repro_quant_rows_i8_ws_bytes bytes, 0
+ * without REPRO_QUANT_COLUMNS.  n >= 0, D >= 1; columns of no rows have scale 0. */
+#define REPRO_QUANT_COLUMNS 1
+int repro_quant_rows_i8(const void* x, int type, int64_t x_ld, const float* mul, int64_t n, int64_t D,
+                        int flags, int8_t* q, int64_t q_ld, float* scales, void* ws, size_t ws_bytes,
+                        void* stream);
+size_t repro_quant_rows_i8_ws_bytes(int64_t n, int64_t D, int flags);
+
+/* Product of 8-bit codes with a scale for each row of both sides:
+ *   y_mn = (i2f(sum_k A(m, k) B(n, k)) (x) s_a[m]) (x) s_b[n], the integer sum exact; a NULL scale
+ *   is left out; with REPRO_BWD_DW_ACCUMULATE y (+) that (y_type REPRO_F32).
+ * A(m, k) = a[m][k], or a[k][m] with REPRO_MM_A_T; B(n, k) = b[n][k], or b[k][n] with REPRO_MM_B_T;
+ * rows a_ld, b_ld apart.  The three products of a linear's step, for codes X [T][K], W [N][K]:
+ *   Y  = X W^T               a = X, b = W;
+ *   dX = G W                 a = G [T][N], b = W, REPRO_MM_B_T;
+ *   dW = H^T X               a = H [T][N], b = X, REPRO_MM_A_T | REPRO_MM_B_T.
+ * y: y_type (REPRO_F32 or REPRO_BF16), rows y_ld apart.  K <= 133144 (any code of int8 but -128 is
+ * within the exact sums; -128 is not checked for: K <= 131071 then), M, N <= REPRO_MM_MAX_ROWS.
+ * K = 0 gives +0 times the scales.  ws: repro_matmul_i8_ws_bytes bytes.  Runs on the tensor cores
+ * under the exactness check of repro_linear_fwd (the first such call on a device runs it in ws and
+ * synchronises); small products, and every product before the check in a capture or after it
+ * failed, on the CUDA cores.  The integer sum, and so every bit, is the same. */
+#define REPRO_MM_A_T 2
+#define REPRO_MM_B_T 4
+#define REPRO_MM_MAX_ROWS 4194240
+int repro_matmul_i8(const int8_t* a, int64_t a_ld, const int8_t* b, int64_t b_ld, const float* s_a,
+                    const float* s_b, int64_t M, int64_t N, int64_t K, int flags, void* y, int y_type,
+                    int64_t y_ld, void* ws, size_t ws_bytes, void* stream);
+size_t repro_matmul_i8_ws_bytes(int64_t M, int64_t N, int64_t K, int flags);
+
+/* Gated activation of gu [n][2 F] (gate, then up, as the fused linear writes them):
+ *   e = exp_r(-|g|) (repro_attn_fwd's), w = 1 (/) (1 (+) e), sig(g) = w for g >= 0, else e (x) w;
+ *   a = (g (x) sig(g)) (x) up.
+ * codes, scales (both NULL: not wanted): the 8-bit copy of gate and up for the backward, in groups
+ * of REPRO_SWIGLU_GROUP consecutive elements of either: scales [n][2][G], G = ceil(F / group),
+ * s = max |v| (/) 127; codes [n][2][G][group], code = clamp(round_half_even(v (/) s), -127, 127) as
+ * repro_quant_i8 (0 past F): about 2.06 bytes a pair in place of 8 (fp32) or 4 (bf16).  Both dense,
+ * codes 16-byte aligned.  gu: `type`, rows gu_ld apart; a: a_type, rows a_ld apart.  1 <= F <= 2^27. */
+#define REPRO_SWIGLU_GROUP 128
+int repro_swiglu_fwd(const void* gu, int type, int64_t gu_ld, int64_t n, int64_t F, void* a, int a_type,
+                     int64_t a_ld, int8_t* codes, float* scales, void* stream);
+
+/* Its backward, from the gradient da of a and either gu or its 8-bit copy (then gu is NULL and
+ * g = i2f(code) (x) s, up alike): with sig(g) and t = sig(-g), the other of w and e (x) w,
+ *   dg = ((da (x) up) (x) sig(g)) (x) (1 (+) (g (x) t));  dup = da (x) (g (x) sig(g)),
+ * to dgu [n][2 F] in `type` (gu's too), rows dgu_ld apart; da: a_type, rows da_ld apart. */
+int repro_swiglu_bwd(const void* da, int a_type, int64_t da_ld, const void* gu, int64_t gu_ld,
+                     const int8_t* codes, const float* scales, int64_t n, int64_t F, void* dgu, int type,
+                     int64_t dgu_ld, void* stream);
+
+/* ------------------------------------------------------------------------
  * Per-step state hash ([rit] paragraph 4, [limits]: a hash of the state is
  * recorded after every step and a replay must reproduce it; the pages hash on
  * the host and name on-device hashing as future work).  The pages fix no

@@ -141,6 +141,18 @@ def load(path: str) -> ctypes.CDLL:
                                       *[ctypes.c_float] * 4, ctypes.c_int, _f32p, _f32p]),
         "oracle_distill_bwd": (None, [_f32p, _i64, _i64, _i64p, _i64, _i64p, _f32p, _f32p, _i64,
                                       *[ctypes.c_float] * 4, _f32p]),
+        "oracle_bf16": (ctypes.c_float, [ctypes.c_float]),
+        "oracle_block_norm_fwd": (None, [_f32p, _f32p, _f32p, ctypes.c_int, _f32p, _f32p,
+                                         *[ctypes.c_float] * 3, _i64, _i64, *[ctypes.c_int] * 3,
+                                         _f32p, _f32p, _f32p]),
+        "oracle_block_norm_bwd": (None, [_f32p, _f32p, _f32p, _f32p, _f32p, ctypes.c_int, _f32p, _f32p,
+                                         _f32p, *[ctypes.c_float] * 2, _i64, _i64, *[ctypes.c_int] * 2,
+                                         *[_f32p] * 5]),
+        "oracle_quant_rows": (None, [_f32p, _f32p, _i64, _i64, ctypes.c_int, _i8p, _f32p]),
+        "oracle_matmul_i8": (None, [_i8p, _i8p, _f32p, _f32p, _i64, _i64, _i64, *[ctypes.c_int] * 3,
+                                    _f32p]),
+        "oracle_swiglu_fwd": (None, [_f32p, _i64, _i64, _f32p, _i8p, _f32p]),
+        "oracle_swiglu_bwd": (None, [_f32p, _f32p, _i8p, _f32p, _i64, _i64, _f32p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -546,3 +558,91 @@ def distill_bwd(z, idx, stats, g, label=None, tau=1.0, w_kd=1.0, w_ce=0.0, w_z=0
                              _p(stats, _f32p), _p(g, _f32p), 0 if g.size == 1 else 1, float(tau),
                              float(w_kd), float(w_ce), float(w_z), _p(dz, _f32p))
     return dz
+
+
+# ---------------------------------------------------------------- the feed-forward half
+
+NORM_CHUNK, SWIGLU_GROUP = 16, 128
+
+
+def bf16(x: float) -> np.float32:
+    return np.float32(lib().oracle_bf16(float(x)))
+
+
+def _f32o(a):
+    return None if a is None else _f32(a)
+
+
+def block_norm_fwd(x, y=None, gate=None, g_post=None, g_pre=None, alpha=1.0, beta=1.0, eps=1e-6,
+                   post=False, want_u=True, h_bf16=False):
+    """(h, u, stats) of x, y [n, D]; gate [D] or [n, D].  h is None without y, u without want_u."""
+    x, y, gate, g_post, g_pre = (_f32o(a) for a in (x, y, gate, g_post, g_pre))
+    n, D = x.shape
+    h = None if y is None else np.empty((n, D), dtype=np.float32)
+    u = np.empty((n, D), dtype=np.float32) if want_u else None
+    stats = np.empty((n, 2), dtype=np.float32)
+    lib().oracle_block_norm_fwd(_p(x, _f32p), _opt(y, _f32p), _opt(gate, _f32p),
+                                int(gate is not None and gate.ndim == 2), _opt(g_post, _f32p),
+                                _opt(g_pre, _f32p), float(alpha), float(beta), float(eps), n, D, int(post),
+                                int(want_u), int(h_bf16), _opt(h, _f32p), _opt(u, _f32p), _p(stats, _f32p))
+    return h, u, stats
+
+
+def block_norm_bwd(dh, du, h, y, stats, gate=None, g_post=None, g_pre=None, alpha=1.0, beta=1.0,
+                   post=False, acc=None):
+    """(dx, dy, dgate, dg_post, dg_pre), each None where it has no input; acc: the old values of the
+    last three's sums over tokens."""
+    dh, du, h, y, stats, gate, g_post, g_pre = (_f32o(a) for a in (dh, du, h, y, stats, gate, g_post, g_pre))
+    n, D = (dh if dh is not None else du).shape
+    rows = gate is not None and gate.ndim == 2
+    new = lambda *s: np.empty(s, dtype=np.float32)  # noqa: E731
+    old = lambda i: new(D) if acc is None else _f32(acc[i]).copy()  # noqa: E731
+    dx, dy = new(n, D), None if y is None else new(n, D)
+    dgate = None if gate is None else new(n, D) if rows else old(0)
+    dgp = None if g_post is None else old(1)
+    dgn = None if g_pre is None or du is None else old(2)
+    lib().oracle_block_norm_bwd(*(_opt(a, _f32p) for a in (dh, du, h, y, gate)), int(rows),
+                                *(_opt(a, _f32p) for a in (g_post, g_pre, stats)), float(alpha), float(beta),
+                                n, D, int(post), int(acc is not None),
+                                *(_opt(a, _f32p) for a in (dx, dy, dgate, dgp, dgn)))
+    return dx, dy, dgate, dgp, dgn
+
+
+def quant_rows(x, mul=None, columns: bool = False):
+    """(codes [n, D], scales [n] or, by columns, [D])."""
+    x, mul = _f32(x), _f32o(mul)
+    n, D = x.shape
+    q, s = np.empty((n, D), dtype=np.int8), np.empty(D if columns else n, dtype=np.float32)
+    lib().oracle_quant_rows(_p(x, _f32p), _opt(mul, _f32p), n, D, int(columns), _p(q, _i8p), _p(s, _f32p))
+    return q, s
+
+
+def matmul_i8(a, b, s_a=None, s_b=None, a_t: bool = False, b_t: bool = False, acc=None) -> np.ndarray:
+    a, b, s_a, s_b = _i8(a), _i8(b), _f32o(s_a), _f32o(s_b)
+    M, K = a.shape[::-1] if a_t else a.shape
+    N = b.shape[1] if b_t else b.shape[0]
+    y = np.empty((M, N), dtype=np.float32) if acc is None else _f32(acc).copy()
+    lib().oracle_matmul_i8(_p(a, _i8p), _p(b, _i8p), _opt(s_a, _f32p), _opt(s_b, _f32p), M, N, K, int(a_t),
+                           int(b_t), int(acc is not None), _p(y, _f32p))
+    return y
+
+
+def swiglu_fwd(gu):
+    """(a [n, F], codes [n, 2, G, 128], scales [n, 2, G]) of gu [n, 2 F]."""
+    gu = _f32(gu)
+    n, F = gu.shape[0], gu.shape[1] // 2
+    G = -(-F // SWIGLU_GROUP)
+    a = np.empty((n, F), dtype=np.float32)
+    codes, scales = np.empty((n, 2, G, SWIGLU_GROUP), dtype=np.int8), np.empty((n, 2, G), dtype=np.float32)
+    lib().oracle_swiglu_fwd(_p(gu, _f32p), n, F, _p(a, _f32p), _p(codes, _i8p), _p(scales, _f32p))
+    return a, codes, scales
+
+
+def swiglu_bwd(da, gu=None, codes=None, scales=None) -> np.ndarray:
+    da, gu, scales = _f32(da), _f32o(gu), _f32o(scales)
+    codes = None if codes is None else _i8(codes)
+    n, F = da.shape
+    dgu = np.empty((n, 2 * F), dtype=np.float32)
+    lib().oracle_swiglu_bwd(_p(da, _f32p), _opt(gu, _f32p), _opt(codes, _i8p), _opt(scales, _f32p), n, F,
+                            _p(dgu, _f32p))
+    return dgu

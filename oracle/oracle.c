@@ -1255,3 +1255,288 @@ void oracle_distill_bwd(const float* z, int64_t n, int64_t V, const int64_t* idx
             d[label[r]] = oracle_add(d[label[r]], -oracle_mul(gr, w_ce));
     }
 }
+
+/* ------------------------------------------------------------------------ */
+/* Norms around a block, codes by row or column, their product, the gated     */
+/* activation (definitions and orders: include/repro.h).                      */
+/* ------------------------------------------------------------------------ */
+
+#define NORM_CHUNK 16
+#define SWIGLU_GROUP 128
+
+/* to bf16 and back: nearest, ties to even; a NaN stays one */
+float oracle_bf16(float x)
+{
+    uint32_t b;
+    if (x != x)
+        return x;
+    memcpy(&b, &x, 4);
+    b = (b + 0x7fffu + ((b >> 16) & 1u)) & 0xffff0000u;
+    memcpy(&x, &b, 4);
+    return x;
+}
+
+/* S(t): groups of 4 left to right into C ascending chains, the chains by the tree */
+static float norm_sum(const float* t, int64_t D)
+{
+    int64_t C = 32;
+    while (16 * C < D)
+        C *= 2;
+    const int64_t G = (D + 3) / 4, used = G < C ? G : C;
+    float* s = (float*)malloc((size_t)used * sizeof(float));
+    for (int64_t g = 0; g < G; ++g) {
+        float a = t[4 * g];
+        for (int64_t d = 4 * g + 1; d < 4 * g + 4 && d < D; ++d)
+            a = oracle_add(a, t[d]);
+        s[g % C] = g < C ? a : oracle_add(s[g % C], a);
+    }
+    for (int64_t w = 1; w < used; w *= 2)
+        for (int64_t j = 0; j + w < used; j += 2 * w)
+            s[j] = oracle_add(s[j], s[j + w]);
+    const float r = s[0];
+    free(s);
+    return r;
+}
+
+static float norm_rms(const float* v, int64_t D, float eps, float* tmp)
+{
+    for (int64_t d = 0; d < D; ++d)
+        tmp[d] = oracle_mul(v[d], v[d]);
+    return oracle_div(1.0f, oracle_sqrt(oracle_add(oracle_div(norm_sum(tmp, D), (float)D), eps)));
+}
+
+void oracle_block_norm_fwd(const float* x, const float* y, const float* gate, int gate_rows,
+                           const float* gp, const float* gn, float alpha, float beta, float eps,
+                           int64_t n, int64_t D, int post, int want_u, int h_bf16, float* h, float* u,
+                           float* stats)
+{
+#pragma omp parallel for schedule(static)
+    for (int64_t i = 0; i < n; ++i) {
+        float* tmp = (float*)malloc((size_t)D * sizeof(float));
+        float* row = (float*)malloc((size_t)D * sizeof(float));
+        float r1 = 0.0f, r2 = 0.0f;
+        if (y && post)
+            r1 = norm_rms(y + i * D, D, eps, tmp);
+        for (int64_t d = 0; d < D; ++d) {
+            float v = x[i * D + d];
+            if (y) {
+                float p = y[i * D + d];
+                if (post)
+                    p = oracle_mul(p, r1);
+                if (post && gp)
+                    p = oracle_mul(p, gp[d]);
+                if (gate)
+                    p = oracle_mul(p, gate[gate_rows ? i * D + d : d]);
+                v = oracle_add(oracle_mul(v, alpha), oracle_mul(p, beta));
+                if (h_bf16)
+                    v = oracle_bf16(v);
+                h[i * D + d] = v;
+            }
+            row[d] = v;
+        }
+        if (want_u) {
+            r2 = norm_rms(row, D, eps, tmp);
+            for (int64_t d = 0; d < D; ++d) {
+                const float v = oracle_mul(row[d], r2);
+                u[i * D + d] = gn ? oracle_mul(v, gn[d]) : v;
+            }
+        }
+        stats[2 * i] = r1;
+        stats[2 * i + 1] = r2;
+        free(tmp);
+        free(row);
+    }
+}
+
+/* sum over the rows of terms [n][D], chunk by chunk, into out (or added to it) */
+static void norm_columns(const float* terms, int64_t n, int64_t D, int accumulate, float* out)
+{
+    const int64_t C = (n + NORM_CHUNK - 1) / NORM_CHUNK;
+#pragma omp parallel for schedule(static)
+    for (int64_t d = 0; d < D; ++d) {
+        float* t = (float*)malloc((size_t)(C > 0 ? C : 1) * sizeof(float));
+        t[0] = 0.0f;
+        for (int64_t i = 0; i < n; ++i) {
+            const float v = terms[i * D + d];
+            t[i / NORM_CHUNK] = i % NORM_CHUNK == 0 ? v : oracle_add(t[i / NORM_CHUNK], v);
+        }
+        for (int64_t w = 1; w < C; w *= 2)
+            for (int64_t j = 0; j + w < C; j += 2 * w)
+                t[j] = oracle_add(t[j], t[j + w]);
+        out[d] = accumulate ? oracle_add(out[d], t[0]) : t[0];
+        free(t);
+    }
+}
+
+/* r (x) (v (-) (unit (x) (S(v (x) unit) (/) D))) of one row */
+static void norm_back(const float* v, const float* unit, float r, int64_t D, float* tmp, float* out)
+{
+    for (int64_t d = 0; d < D; ++d)
+        tmp[d] = oracle_mul(v[d], unit[d]);
+    const float c = oracle_div(norm_sum(tmp, D), (float)D);
+    for (int64_t d = 0; d < D; ++d)
+        out[d] = oracle_mul(r, oracle_add(v[d], -oracle_mul(unit[d], c)));
+}
+
+void oracle_block_norm_bwd(const float* dh, const float* du, const float* h, const float* y,
+                           const float* gate, int gate_rows, const float* gp, const float* gn,
+                           const float* stats, float alpha, float beta, int64_t n, int64_t D, int post,
+                           int accumulate, float* dx, float* dy, float* dgate, float* dgp, float* dgn)
+{
+    const size_t bytes = (size_t)(n * D > 0 ? n * D : 1) * sizeof(float);
+    float *tn = (float*)malloc(bytes), *tp = (float*)malloc(bytes), *tg = (float*)malloc(bytes);
+#pragma omp parallel for schedule(static)
+    for (int64_t i = 0; i < n; ++i) {
+        const size_t rb = (size_t)D * sizeof(float);
+        float *tmp = (float*)malloc(rb), *v = (float*)malloc(rb), *unit = (float*)malloc(rb), *g = (float*)malloc(rb);
+        const float r1 = stats[2 * i], r2 = stats[2 * i + 1];
+        for (int64_t d = 0; d < D; ++d)
+            g[d] = dh ? oracle_flush(dh[i * D + d]) : 0.0f;
+        if (du) {
+            for (int64_t d = 0; d < D; ++d) {
+                const float u = du[i * D + d];
+                unit[d] = oracle_mul(h[i * D + d], r2);
+                v[d] = gn ? oracle_mul(u, gn[d]) : oracle_flush(u);
+                tn[i * D + d] = oracle_mul(u, unit[d]);
+            }
+            norm_back(v, unit, r2, D, tmp, v);
+            for (int64_t d = 0; d < D; ++d)
+                g[d] = dh ? oracle_add(g[d], v[d]) : v[d];
+        }
+        for (int64_t d = 0; d < D; ++d)
+            dx[i * D + d] = y ? oracle_mul(g[d], alpha) : g[d];
+        if (y) {
+            for (int64_t d = 0; d < D; ++d) {
+                const float yv = oracle_flush(y[i * D + d]);
+                unit[d] = post ? oracle_mul(yv, r1) : yv;
+                const float p = post && gp ? oracle_mul(unit[d], gp[d]) : unit[d];
+                const float b = oracle_mul(g[d], beta);
+                if (gate) {
+                    (gate_rows ? dgate : tg)[i * D + d] = oracle_mul(b, p);
+                    v[d] = oracle_mul(b, gate[gate_rows ? i * D + d : d]);
+                } else {
+                    v[d] = b;
+                }
+            }
+            if (post) {
+                for (int64_t d = 0; d < D; ++d) {
+                    tp[i * D + d] = oracle_mul(v[d], unit[d]);
+                    if (gp)
+                        v[d] = oracle_mul(v[d], gp[d]);
+                }
+                norm_back(v, unit, r1, D, tmp, dy + i * D);
+            } else {
+                memcpy(dy + i * D, v, rb);
+            }
+        }
+        free(tmp);
+        free(v);
+        free(unit);
+        free(g);
+    }
+    if (dgn)
+        norm_columns(tn, n, D, accumulate, dgn);
+    if (dgp)
+        norm_columns(tp, n, D, accumulate, dgp);
+    if (gate && !gate_rows)
+        norm_columns(tg, n, D, accumulate, dgate);
+    free(tn);
+    free(tp);
+    free(tg);
+}
+
+void oracle_quant_rows(const float* x, const float* mul, int64_t n, int64_t D, int columns, int8_t* q,
+                       float* scales)
+{
+    const int64_t R = columns ? D : n, L = columns ? n : D;
+#pragma omp parallel for schedule(static)
+    for (int64_t r = 0; r < R; ++r) {
+        float m = 0.0f;
+        for (int pass = 0; pass < 2; ++pass) {
+            for (int64_t j = 0; j < L; ++j) {
+                const int64_t at = columns ? j * D + r : r * D + j;
+                const float v = mul ? oracle_mul(x[at], mul[j]) : oracle_flush(x[at]);
+                if (pass)
+                    q[at] = (int8_t)oracle_quant_one(v, scales[r], 127);
+                else if (fabsf(v) > m)
+                    m = fabsf(v);
+            }
+            if (!pass)
+                scales[r] = oracle_div(m, oracle_i2f(127));
+        }
+    }
+}
+
+void oracle_matmul_i8(const int8_t* a, const int8_t* b, const float* s_a, const float* s_b, int64_t M,
+                      int64_t N, int64_t K, int a_t, int b_t, int accumulate, float* y)
+{
+#pragma omp parallel for schedule(static)
+    for (int64_t m = 0; m < M; ++m)
+        for (int64_t j = 0; j < N; ++j) {
+            int64_t acc = 0;
+            for (int64_t k = 0; k < K; ++k)
+                acc += (int64_t)a[a_t ? k * M + m : m * K + k] * b[b_t ? k * N + j : j * K + k];
+            float v = oracle_i2f(acc);
+            if (s_a)
+                v = oracle_mul(v, s_a[m]);
+            if (s_b)
+                v = oracle_mul(v, s_b[j]);
+            y[m * N + j] = accumulate ? oracle_add(y[m * N + j], v) : v;
+        }
+}
+
+/* sig(g) and sig(-g) from one e^-|g| and one reciprocal */
+static void sigmoids(float g, float* sig, float* rest)
+{
+    const float e = oracle_exp(-fabsf(oracle_flush(g)));
+    const float w = oracle_div(1.0f, oracle_add(1.0f, e)), ew = oracle_mul(e, w);
+    *sig = g >= 0.0f ? w : ew;
+    *rest = g >= 0.0f ? ew : w;
+}
+
+void oracle_swiglu_fwd(const float* gu, int64_t n, int64_t F, float* a, int8_t* codes, float* scales)
+{
+    const int64_t G = (F + SWIGLU_GROUP - 1) / SWIGLU_GROUP;
+#pragma omp parallel for schedule(static)
+    for (int64_t i = 0; i < n; ++i) {
+        for (int64_t j = 0; j < F; ++j) {
+            const float g = gu[2 * i * F + j], up = gu[(2 * i + 1) * F + j];
+            float sig, rest;
+            sigmoids(g, &sig, &rest);
+            a[i * F + j] = oracle_mul(oracle_mul(g, sig), up);
+        }
+        for (int64_t h = 0; codes && h < 2 * G; ++h) {
+            const float* v = gu + (2 * i + h / G) * F;
+            const int64_t lo = h % G * SWIGLU_GROUP, hi = lo + SWIGLU_GROUP < F ? lo + SWIGLU_GROUP : F;
+            float m = 0.0f;
+            for (int64_t j = lo; j < hi; ++j)
+                if (fabsf(oracle_flush(v[j])) > m)
+                    m = fabsf(oracle_flush(v[j]));
+            const float s = scales[2 * G * i + h] = oracle_div(m, oracle_i2f(127));
+            int8_t* c = codes + (2 * G * i + h) * SWIGLU_GROUP;
+            for (int64_t j = 0; j < SWIGLU_GROUP; ++j)
+                c[j] = lo + j < hi ? (int8_t)oracle_quant_one(v[lo + j], s, 127) : 0;
+        }
+    }
+}
+
+void oracle_swiglu_bwd(const float* da, const float* gu, const int8_t* codes, const float* scales,
+                       int64_t n, int64_t F, float* dgu)
+{
+    const int64_t G = (F + SWIGLU_GROUP - 1) / SWIGLU_GROUP;
+#pragma omp parallel for schedule(static)
+    for (int64_t i = 0; i < n; ++i)
+        for (int64_t j = 0; j < F; ++j) {
+            float v[2], sig, rest;
+            for (int h = 0; h < 2; ++h) {
+                const int64_t at = (2 * i + h) * G + j / SWIGLU_GROUP;
+                v[h] = gu ? gu[(2 * i + h) * F + j]
+                          : oracle_mul(oracle_i2f(codes[at * SWIGLU_GROUP + j % SWIGLU_GROUP]), scales[at]);
+            }
+            sigmoids(v[0], &sig, &rest);
+            const float d = da[i * F + j];
+            dgu[2 * i * F + j] = oracle_mul(oracle_mul(oracle_mul(d, v[1]), sig),
+                                            oracle_add(1.0f, oracle_mul(v[0], rest)));
+            dgu[(2 * i + 1) * F + j] = oracle_mul(d, oracle_mul(v[0], sig));
+        }
+}

@@ -174,6 +174,27 @@ void oracle_distill_bwd(const float* z, int64_t n, int64_t V, const int64_t* idx
                         const int64_t* label, const float* stats, const float* g, int64_t g_stride,
                         float tau, float w_kd, float w_ce, float w_z, float* dz);
 
+/* Norms around a block, codes by row or column, their product, the gated activation
+ * (definitions in include/repro.h).  Tensors dense and widened to binary32; h_bf16:
+ * the stream is rounded to bf16 before the norm reads it; gate_rows: a gate row per
+ * token, else one. */
+float oracle_bf16(float x);
+void oracle_block_norm_fwd(const float* x, const float* y, const float* gate, int gate_rows,
+                           const float* gp, const float* gn, float alpha, float beta, float eps,
+                           int64_t n, int64_t D, int post, int want_u, int h_bf16, float* h, float* u,
+                           float* stats);
+void oracle_block_norm_bwd(const float* dh, const float* du, const float* h, const float* y,
+                           const float* gate, int gate_rows, const float* gp, const float* gn,
+                           const float* stats, float alpha, float beta, int64_t n, int64_t D, int post,
+                           int accumulate, float* dx, float* dy, float* dgate, float* dgp, float* dgn);
+void oracle_quant_rows(const float* x, const float* mul, int64_t n, int64_t D, int columns, int8_t* q,
+                       float* scales);
+void oracle_matmul_i8(const int8_t* a, const int8_t* b, const float* s_a, const float* s_b, int64_t M,
+                      int64_t N, int64_t K, int a_t, int b_t, int accumulate, float* y);
+void oracle_swiglu_fwd(const float* gu, int64_t n, int64_t F, float* a, int8_t* codes, float* scales);
+void oracle_swiglu_bwd(const float* da, const float* gu, const int8_t* codes, const float* scales,
+                       int64_t n, int64_t F, float* dgu);
+
 int oracle_threads(void);
 void oracle_set_threads(int n);
 
