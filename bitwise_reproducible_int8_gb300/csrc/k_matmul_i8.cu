@@ -14,7 +14,7 @@
 // Products of few tokens are bound by the weights' bytes and run on the CUDA cores (k_mm_rows).
 //
 // Roles in a CTA of the pair, as in k_fwd_tc.cu: warp 0 loads, warp 1 of the leading CTA issues the
-// MMAs for both (warp 1 of the other holds its tensor memory), warps 2 .. 9 are the epilogue.  The
+// MMAs for both (warp 1 of the other holds its tensor memory), the others are the epilogue.  The
 // leader's full barriers count both CTAs' bytes; an MMA's commit frees its stage, and hands over its
 // accumulator, in both; both epilogues free the accumulator on the leader's barrier.  Every wait is
 // bounded as there.
@@ -34,6 +34,8 @@
 
 namespace repro {
 namespace {
+
+typedef unsigned long long u64;
 
 // ---------------------------------------------------------------- operands to bf16
 
@@ -59,7 +61,7 @@ struct Widen {
     const int8_t* q;
     int64_t ld, rows, K, Kp;    // source rows of K (or, transposed, K rows of `rows`); pitch of the copy
     __nv_bfloat16* out;
-    bool vec;                   // source rows on 8-byte boundaries
+    bool vec;                   // source rows on 8-byte (transposed: 16-byte) boundaries
 };
 
 // rows of K codes to rows of Kp bf16, zeros behind K; 8 at a time
@@ -93,57 +95,74 @@ k_mm_widen(const __grid_constant__ Widen w)
     }
 }
 
-// K rows of codes to `rows` rows of Kp bf16, through tiles of 64 terms x 128 rows in shared memory
+// where word c (4 rows) of term k lies in a tile of 128 x 32 words: rotated so that neither the 4
+// terms of a warp's stores nor the 8 octets of terms of its loads meet in a bank
+__device__ __forceinline__ int tile_word(int k, int c) { return 32 * k + ((c + 4 * (k >> 3) + (k & 3)) & 31); }
+
+// K rows of codes to `rows` rows of Kp bf16, through tiles of 128 terms x 128 rows in shared memory
 __global__ void __launch_bounds__(256)
 k_mm_widen_t(const __grid_constant__ Widen w, int tiles_r)
 {
-    __shared__ uint32_t tile[64][33];
+    __shared__ uint32_t tile[128 * 32];
     const int tr = blockIdx.x % tiles_r;
-    const int64_t k0 = (int64_t)(blockIdx.x / tiles_r) * 64, r0 = (int64_t)tr * 128;
+    const int64_t k0 = (int64_t)(blockIdx.x / tiles_r) * 128, r0 = (int64_t)tr * 128;
     pdl_wait();
     pdl_trigger();
-    for (int e = threadIdx.x; e < 64 * 32; e += 256) {
-        const int k = e >> 5, c = e & 31;
-        const int64_t r = r0 + 4 * c;
-        uint32_t v = 0;
-        if (k0 + k < w.K) {
-            const int8_t* p = w.q + (k0 + k) * w.ld + r;
-            if (w.vec && r + 4 <= w.rows) {
-                v = __ldg(reinterpret_cast<const uint32_t*>(p));
-            } else {
+    const int c16 = threadIdx.x & 7;                 // 16 rows of a term
+    const int64_t r = r0 + 16 * c16;
+    const bool whole = w.vec && r + 16 <= w.rows && k0 + 128 <= w.K;
+    uint4 v[4];
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    if (r + b < w.rows)
-                        v |= (uint32_t)(uint8_t)p[b] << (8 * b);
-            }
+    for (int i = 0; i < 4; ++i) {
+        const int64_t k = k0 + (threadIdx.x >> 3) + 32 * i;
+        const int8_t* p = w.q + k * w.ld + r;
+        if (whole) {
+            asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                         : "l"(p));
+        } else {
+            uint32_t x[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (k < w.K && r + e < w.rows)
+                    x[e >> 2] |= (uint32_t)(uint8_t)p[e] << (8 * (e & 3));
+            v[i] = make_uint4(x[0], x[1], x[2], x[3]);
         }
-        tile[k][c] = v;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int k = (threadIdx.x >> 3) + 32 * i;
+        tile[tile_word(k, 4 * c16)] = v[i].x;
+        tile[tile_word(k, 4 * c16 + 1)] = v[i].y;
+        tile[tile_word(k, 4 * c16 + 2)] = v[i].z;
+        tile[tile_word(k, 4 * c16 + 3)] = v[i].w;
     }
     __syncthreads();
-    // 8 terms of 4 rows a step: neighbouring threads take neighbouring terms of the same rows
-    for (int e = threadIdx.x; e < 8 * 32; e += 256) {
-        const int kk = 8 * (e & 7), c = e >> 3;
+    // 8 terms of 4 rows a step: 8 neighbouring threads write 128 bytes of each of the rows
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int kk = 8 * (threadIdx.x & 7) + 64 * h, c = threadIdx.x >> 3;
         if (k0 + kk >= w.Kp)
-            continue;
+            break;
         uint32_t in[8], t[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            in[i] = tile[kk + i][c];
+            in[i] = tile[tile_word(kk + i, c)];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {   // 4 x 4 bytes transposed
-            const uint32_t a = __byte_perm(in[4 * h], in[4 * h + 1], 0x5140), b = __byte_perm(in[4 * h], in[4 * h + 1], 0x7362);
-            const uint32_t c2 = __byte_perm(in[4 * h + 2], in[4 * h + 3], 0x5140), d = __byte_perm(in[4 * h + 2], in[4 * h + 3], 0x7362);
-            t[h] = __byte_perm(a, c2, 0x5410);
-            t[2 + h] = __byte_perm(a, c2, 0x7632);
-            t[4 + h] = __byte_perm(b, d, 0x5410);
-            t[6 + h] = __byte_perm(b, d, 0x7632);
+        for (int q = 0; q < 2; ++q) {   // 4 x 4 bytes transposed
+            const uint32_t a = __byte_perm(in[4 * q], in[4 * q + 1], 0x5140), b = __byte_perm(in[4 * q], in[4 * q + 1], 0x7362);
+            const uint32_t c2 = __byte_perm(in[4 * q + 2], in[4 * q + 3], 0x5140), d = __byte_perm(in[4 * q + 2], in[4 * q + 3], 0x7362);
+            t[q] = __byte_perm(a, c2, 0x5410);
+            t[2 + q] = __byte_perm(a, c2, 0x7632);
+            t[4 + q] = __byte_perm(b, d, 0x5410);
+            t[6 + q] = __byte_perm(b, d, 0x7632);
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int64_t r = r0 + 4 * c + b;
-            if (r < w.rows) {
+            const int64_t row = r0 + 4 * c + b;
+            if (row < w.rows) {
                 const uint2 x = widen4(t[2 * b]), y = widen4(t[2 * b + 1]);
-                *reinterpret_cast<uint4*>(w.out + r * w.Kp + k0 + kk) = make_uint4(x.x, x.y, y.x, y.y);
+                *reinterpret_cast<uint4*>(w.out + row * w.Kp + k0 + kk) = make_uint4(x.x, x.y, y.x, y.y);
             }
         }
     }
@@ -151,12 +170,12 @@ k_mm_widen_t(const __grid_constant__ Widen w, int tiles_r)
 
 cudaError_t widen(const int8_t* q, int64_t ld, int64_t rows, int64_t K, bool t, __nv_bfloat16* out, cudaStream_t st)
 {
-    const size_t b = t ? 4 : 8;
+    const size_t b = t ? 16 : 8;
     Widen w = {q, ld, rows, K, pad8(K), out, reinterpret_cast<uintptr_t>(q) % b == 0 && ld % (int64_t)b == 0};
     count_launches(1);
     if (t) {
         const int tiles_r = (int)((rows + 127) / 128);
-        return launch_pdl(k_mm_widen_t, dim3((unsigned)(tiles_r * ((K + 63) / 64))), dim3(256), 0, st, w, tiles_r);
+        return launch_pdl(k_mm_widen_t, dim3((unsigned)(tiles_r * ((K + 127) / 128))), dim3(256), 0, st, w, tiles_r);
     }
     const int64_t want = (rows * (w.Kp / 8) + 255) / 256, most = (int64_t)num_sms() * 8;
     return launch_pdl(k_mm_widen, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, w);
@@ -310,13 +329,14 @@ constexpr int HM = 128;                   // rows of a tile that one CTA of the 
 constexpr int TN = 256;
 constexpr int TK = 64;                    // terms a stage: one 128-byte swizzle row of bf16
 constexpr int SLICE_KB = 8;               // stages an exact slice: 8 * 64 = 512 terms
-constexpr int STAGES = 6;
+constexpr int STAGES = 5;
 constexpr int HALF_BYTES = HM * TK * 2;   // 16 KB: a CTA's rows of A, and as much of B
 constexpr int STAGE_BYTES = 2 * HALF_BYTES;
 constexpr int NBUF = 2;                   // accumulators of 256 columns
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int EPI_WARPS = 8;
-constexpr int STG_BYTES = 4096;
+constexpr int EPI_WARPS = 16;
+constexpr int EW = TN / (EPI_WARPS / 4);  // columns of a tile that an epilogue warp holds of 32 rows
+constexpr int STG_BYTES = 4096;          // an epilogue warp's 32 rows x 128 bytes on their way out
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 
 struct Smem {
@@ -338,6 +358,14 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
+// true in one lane of a whole warp
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // the address of this CTA's variable in CTA `rank` of the pair
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank)
 {
@@ -352,29 +380,12 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// an arrival on a barrier of either CTA.  What it orders are tensor memory's reads, which the
+// tcgen05 fences around it order; waits and arrivals of cluster scope (this one's release, every
+// wait's acquire) cost the pipeline half of its rate
 __device__ __forceinline__ void arrive_at(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// mbar_wait with the other CTA's arrivals among those that are waited for
-__device__ __forceinline__ bool wait_pair(uint64_t* b, uint32_t parity)
-{
-    const long long t0 = clock64();
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(su32(b)), "r"(parity)
-            : "memory");
-        if (ok)
-            return true;
-        if (clock64() - t0 > WAIT_CYCLES)
-            return false;
-    }
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // a tile into this CTA's shared memory, its bytes counted on a barrier of either CTA of the pair
@@ -408,7 +419,29 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar)
         : "memory");
 }
 
-__device__ __forceinline__ void store_tile(const CUtensorMap* map, const void* src, int x, int y)
+// 16 accumulator columns into registers, not waited for
+__device__ __forceinline__ void tmem_ask16(uint32_t taddr, uint32_t* v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+// waits for what was asked for; it names the registers, so that no use of them comes before it
+__device__ __forceinline__ void tmem_got16(uint32_t* v)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+
+// 32 rows x 128 bytes from shared memory (128-byte swizzle) to y; the tensor map clips what lies outside
+__device__ __forceinline__ void store_block(const CUtensorMap* map, const void* src, int x, int y)
 {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
@@ -417,16 +450,193 @@ __device__ __forceinline__ void store_tile(const CUtensorMap* map, const void* s
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
+}
+
+// whether a scale's products with whole numbers below 2^31, and with another such scale, need no
+// flush: they are zero, or not below 2^-120
+__device__ __forceinline__ bool ample(float s) { return !(fabsf(s) < 0x1p-60f) || s == 0.0f; }
+
+// How a product is cut: whole tiles in rounds over the pairs of SMs; the tiles of a last round that
+// would leave most pairs idle are cut along K instead (the integer sums are exact, so any cut gives
+// the same bits) and their parts added up by k_mm_join.  A cut has to save four slices, what the
+// parts' way through memory costs.
+struct Plan {
+    int tiles_m, tiles_n, pairs;
+    int whole, split, items;    // tiles 0 .. whole - 1, then the rest in `split` parts each
+};
+
+Plan plan_of(int64_t M, int64_t N, int64_t K)
+{
+    Plan p;
+    p.tiles_m = (int)((M + 2 * HM - 1) / (2 * HM));
+    p.tiles_n = (int)((N + TN - 1) / TN);
+    p.pairs = std::max(1, num_sms() / 2);
+    const int tiles = p.tiles_m * p.tiles_n, rest = tiles % p.pairs, slices = (int)((K + TK * SLICE_KB - 1) / (TK * SLICE_KB));
+    p.split = rest > 0 ? std::min(p.pairs / rest, slices) : 1;
+    if (slices - (slices + p.split - 1) / p.split < 4)
+        p.split = 1;
+    p.whole = p.split > 1 ? tiles - rest : tiles;
+    p.items = p.whole + (tiles - p.whole) * p.split;
+    return p;
+}
+
+constexpr int64_t PART_BYTES = 2 * HM * TN * 4;
+
 struct PairArgs {
     MatmulI8Args g;
-    int K, tiles_n, tiles, y_tma;
+    Plan p;
+    int K;
+    bool y_tma;          // rows of y on 16-byte boundaries
+    int* parts;          // the cut tiles' sums, [part][256][256]
     int* err;
 };
 
-__device__ __forceinline__ void origin(const PairArgs& p, int t, int& m0, int& n0)
+// Tiles in groups of 8 rows of tiles, column by column within a group: the 76 tiles of a round then
+// share 8 blocks of A and about 10 of B, which stay in L2 beside the output that streams through it
+__host__ __device__ __forceinline__ void tile_at(const Plan& p, int tile, int& m0, int& n0)
 {
-    m0 = (t / p.tiles_n) * 2 * HM;
-    n0 = (t % p.tiles_n) * TN;
+    const int per = 8 * p.tiles_n, group = tile / per, in = tile - group * per;
+    const int rows = p.tiles_m - 8 * group < 8 ? p.tiles_m - 8 * group : 8;
+    n0 = (in / rows) * TN;
+    m0 = (8 * group + in % rows) * 2 * HM;
+}
+
+// An item: its tile, its part (-1: a whole tile) and its stages of K
+struct Item {
+    int m0, n0, part, kb0, kb1;
+};
+
+__device__ __forceinline__ Item item_at(const PairArgs& a, int i)
+{
+    const int KB = (a.K + TK - 1) / TK;
+    Item t;
+    t.part = -1, t.kb0 = 0, t.kb1 = KB;
+    int tile = i;
+    if (i >= a.p.whole) {
+        const int j = i - a.p.whole, q = j / a.p.split, s = j - q * a.p.split, NS = (KB + SLICE_KB - 1) / SLICE_KB;
+        tile = a.p.whole + q;
+        if (a.p.split > 1) {
+            t.part = j;
+            t.kb0 = SLICE_KB * (int)((int64_t)NS * s / a.p.split);
+            t.kb1 = min(KB, SLICE_KB * (int)((int64_t)NS * (s + 1) / a.p.split));
+        }
+    }
+    tile_at(a.p, tile, t.m0, t.n0);
+    return t;
+}
+
+// A warp's 32 rows x EW columns: scaled, added to what is there, stored.  own: the columns' scales,
+// two a lane.  Rows on 16-byte boundaries go through the warp's buffer in blocks of 128 bytes (chunk
+// k of row r at k ^ (r mod 8)), one tensor store each.  (Straight to memory, 4 lanes to a row's line
+// after a turn by shuffles, 16384 x 11264 x 2048 took 87 us longer, although the operands' ring then
+// has two stages more; a lane's own 32 bytes at a time took 41 us longer still.)
+template <typename Y>
+__device__ __forceinline__ void finish(const PairArgs& p, const CUtensorMap* map, const uint32_t (&acc)[EW], uint8_t* stg, int lane,
+                                       float sa, const float (&own)[2], int r0, int n)
+{
+    constexpr int W = 128 / (int)sizeof(Y), E = W / 8;
+    const MatmulI8Args& g = p.g;
+    Y* row = static_cast<Y*>(g.y) + (int64_t)(r0 + lane) * g.y_ld;
+    const bool live = r0 + lane < g.M;
+    const bool fast = __all_sync(0xffffffffu, ample(sa) && ample(own[0]) && ample(own[1]));
+    const u64 sa2 = pack2(sa, sa), z = pack2(-0.0f, -0.0f);
+#pragma unroll
+    for (int b = 0; b < EW; b += W) {
+        if (n + b >= g.N)   // warp-uniform
+            break;
+        float o[W];
+#pragma unroll
+        for (int e = 0; e < W; e += 2) {
+            const int c = b + e, from = c >> 1;
+            u64 v = pack2(__int2float_rn((int)acc[c]), __int2float_rn((int)acc[c + 1]));
+            if (g.s_a)
+                v = fmul2_rn(v, sa2);
+            if (!fast)
+                v = fadd2_ftz(v, z);
+            if (g.s_b)
+                v = fmul2_rn(v, pack2(__shfl_sync(0xffffffffu, own[0], from), __shfl_sync(0xffffffffu, own[1], from)));
+            if (!fast)
+                v = fadd2_ftz(v, z);
+            unpack2(v, o[e], o[e + 1]);
+        }
+        if (!p.y_tma) {
+            if (live)
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    if (n + b + e < g.N)
+                        put(row + n + b + e, o[e], g.accumulate);
+            continue;
+        }
+        // added to the old values here: a reduction in L2 would not flush subnormals
+        if (sizeof(Y) == 4 && g.accumulate && live) {
+#pragma unroll
+            for (int e = 0; e < W; e += 4) {
+                const int c = n + b + e;
+                if (c + 4 <= g.N) {
+                    const float4 old = load4(reinterpret_cast<const float*>(row) + c);
+                    o[e] = fadd_ftz(old.x, o[e]), o[e + 1] = fadd_ftz(old.y, o[e + 1]);
+                    o[e + 2] = fadd_ftz(old.z, o[e + 2]), o[e + 3] = fadd_ftz(old.w, o[e + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c + i < g.N)
+                            o[e + i] = fadd_ftz(to_f32<Y>(row[c + i]), o[e + i]);
+                }
+            }
+        }
+        if (lane == 0)   // the buffer's last store has read it
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)   // 16 bytes a step
+            store16(reinterpret_cast<Y*>(stg + lane * 128 + 16 * (k ^ (lane & 7))), o + E * k);
+        {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0)
+                store_block(map, stg, n + b, r0);
+        }
+    }
+}
+
+// hands an accumulator back to the leader's MMA thread
+__device__ __forceinline__ void release(uint32_t bar, int lane)
+{
+    fence_before();
+    __syncwarp();
+    if (lane == 0)
+        arrive_at(bar);
+}
+
+__device__ __forceinline__ void turn_buffer(int& d, uint32_t& ph)
+{
+    d ^= 1;
+    ph ^= d == 0;
+}
+static_assert(NBUF == 2, "turn_buffer");
+
+// a slice's columns on top of what a warp holds, as floats or as int32; the next 16 come while
+// these are added
+template <bool FLOAT> __device__ __forceinline__ void add_slice(uint32_t (&acc)[EW], uint32_t at)
+{
+    uint32_t v[2][16];
+    tmem_ask16(at, v[0]);
+#pragma unroll
+    for (int c = 0; c < EW / 16; ++c) {
+        tmem_got16(v[c & 1]);
+        if (c < EW / 16 - 1)
+            tmem_ask16(at + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float x = __uint_as_float(v[c & 1][e]);
+            uint32_t& y = acc[16 * c + e];
+            y = FLOAT ? __float_as_uint(__fadd_rn(__uint_as_float(y), x)) : y + (uint32_t)__float2int_rn(x);
+        }
+    }
 }
 
 template <typename Y>
@@ -443,7 +653,6 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int KB = (p.K + TK - 1) / TK, NS = (KB + SLICE_KB - 1) / SLICE_KB;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -474,162 +683,157 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
     const uint32_t tmem = sm->tmem_base;
     pdl_wait();
 
+    // Warps 0 and 1 go through their loops whole and one lane issues: addresses and descriptors stay in
+    // uniform registers.  With one lane in the loops the issuing thread took 620 cycles for a stage
+    // whose MMAs take 512
     if (warp == 0) {
-        if (lane == 0) {
-            int g = 0;   // stages filled over all of this pair's tiles
-            for (int t = pair; t < p.tiles && !*(volatile int*)&sm->failed; t += pairs) {
-                int m0, n0;
-                origin(p, t, m0, n0);
-                for (int kb = 0; kb < KB; ++kb, ++g) {
-                    const int s = g % STAGES;
-                    if (g >= STAGES && !wait_pair(&sm->empty[s], ((g / STAGES) - 1) & 1)) {
-                        sm->failed = 1;
-                        break;
-                    }
-                    if (rank == 0)
-                        mbar_expect_tx(&sm->full[s], 2 * STAGE_BYTES);
-                    const uint32_t bar = peer_addr(&sm->full[s], 0);
-                    tma_load_pair(A + s * HALF_BYTES, &map_a, kb * TK, m0 + (int)rank * HM, bar);
-                    tma_load_pair(B + s * HALF_BYTES, &map_b, kb * TK, n0 + (int)rank * HM, bar);
-                }
-                if (*(volatile int*)&sm->failed)
-                    break;
-            }
-            // the leader sees both CTAs' last copies land before either can exit (cluster_sync below)
-            if (rank == 0)
-                for (int h = g - 1; h >= 0 && h >= g - STAGES; --h)
-                    if (!wait_pair(&sm->full[h % STAGES], (h / STAGES) & 1))
-                        sm->failed = 1;
-        }
-    } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
-            bool ok = true;
-            int g = 0, sg = 0;   // stages and slices consumed over all tiles
-            for (int t = pair; t < p.tiles && ok; t += pairs) {
-                for (int kb = 0; kb < KB; ++kb, ++g) {
-                    const int s = g % STAGES, d = sg % NBUF;
-                    if (kb % SLICE_KB == 0 && sg >= NBUF && !wait_pair(&sm->dempty[d], ((sg / NBUF) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!wait_pair(&sm->full[s], (g / STAGES) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    fence_after();
-                    const uint64_t a0 = sdesc(su32(A + s * HALF_BYTES)), b0 = sdesc(su32(B + s * HALF_BYTES));
-#pragma unroll
-                    for (int k = 0; k < TK / 16; ++k)
-                        mma_pair(tmem + (uint32_t)(d * TN), a0 + 2 * k, b0 + 2 * k, (kb % SLICE_KB != 0 || k != 0) ? 1u : 0u);
-                    commit_pair(&sm->empty[s]);
-                    if (kb % SLICE_KB == SLICE_KB - 1 || kb == KB - 1) {
-                        commit_pair(&sm->dfull[d]);
-                        ++sg;
-                    }
-                }
-            }
-            if (!ok)
-                sm->failed = 1;
-            // every MMA issued here has completed once `done` fires (in both CTAs)
-            commit_pair(&sm->done);
-            if (!wait_pair(&sm->done, 0))
-                sm->failed = 1;
-        }
-    } else {
-        // epilogue: rows m0 + 128 rank + 32 q + lane, columns n0 + 128 h .. + 127
-        const int q = warp & 3, ew = warp - 2, h = ew >> 2;
-        const MatmulI8Args& g = p.g;
-        uint8_t* stg = STG + ew * STG_BYTES;
-        const uint32_t lead[NBUF] = {peer_addr(&sm->dempty[0], 0), peer_addr(&sm->dempty[1], 0)};
+        const uint32_t bar0 = peer_addr(&sm->full[0], 0);
         bool ok = true;
-        int sg = 0;
-        for (int t = pair; t < p.tiles && ok; t += pairs) {
-            int m0, n0;
-            origin(p, t, m0, n0);
-            const int nc = n0 + 128 * h, r0 = m0 + (int)rank * HM + 32 * q;
-            int acc[128];
-#pragma unroll
-            for (int j = 0; j < 128; ++j)
-                acc[j] = 0;
-            for (int sl = 0; sl < NS; ++sl, ++sg) {
-                const int d = sg % NBUF;
-                if (!wait_pair(&sm->dfull[d], (sg / NBUF) & 1)) {
+        int s = 0, ph = 1;   // stage, and the parity whose end frees it (of a fresh barrier: at once)
+        int filled = 0;
+        for (int i = pair; i < p.p.items && ok && !*(volatile int*)&sm->failed; i += pairs) {
+            const Item t = item_at(p, i);
+            const int ya = t.m0 + (int)rank * HM, yb = t.n0 + (int)rank * HM;
+            for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                if (!mbar_wait(&sm->empty[s], (uint32_t)ph)) {
                     ok = false;
                     break;
                 }
-                fence_after();
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t v[16];
-                    tmem_ld16(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(d * TN + 128 * h + 16 * c), v);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        acc[16 * c + e] += __float2int_rn(__uint_as_float(v[e]));
+                if (elect_one()) {
+                    if (rank == 0)
+                        mbar_expect_tx(&sm->full[s], 2 * STAGE_BYTES);
+                    tma_load_pair(A + s * HALF_BYTES, &map_a, kb * TK, ya, bar0 + 8 * s);
+                    tma_load_pair(B + s * HALF_BYTES, &map_b, kb * TK, yb, bar0 + 8 * s);
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    arrive_at(lead[d]);
+                filled = min(filled + 1, STAGES);
+                if (++s == STAGES)
+                    s = 0, ph ^= 1;
+            }
+        }
+        // the leader sees both CTAs' last copies land before either can exit (cluster_sync below):
+        // of the last `filled` stages, the newest first
+        if (rank == 0)
+            for (; filled > 0; --filled) {
+                if (--s < 0)
+                    s = STAGES - 1, ph ^= 1;
+                if (!mbar_wait(&sm->full[s], (uint32_t)(ph ^ 1)))
+                    ok = false;
+            }
+        if (!ok && lane == 0)
+            sm->failed = 1;
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const uint64_t a0 = sdesc(su32(A)), b0 = sdesc(su32(B));
+            bool ok = true;
+            int s = 0, ph = 0, d = 0, dph = 1;   // stage and accumulator, and the parities to wait for
+            for (int i = pair; i < p.p.items && ok; i += pairs) {
+                const Item t = item_at(p, i);
+                for (int kb = t.kb0; kb < t.kb1 && ok; kb += SLICE_KB) {   // a slice; a part starts with one
+                    const int end = min(kb + SLICE_KB, t.kb1);
+                    ok = mbar_wait(&sm->dempty[d], (uint32_t)dph);
+                    for (int j = kb; j < end && ok; ++j) {
+                        ok = mbar_wait(&sm->full[s], (uint32_t)ph);
+                        if (!ok)
+                            break;
+                        fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < TK / 16; ++k)
+                                mma_pair(tmem + (uint32_t)(d * TN), a0 + (uint32_t)(s * (HALF_BYTES >> 4) + 2 * k),
+                                         b0 + (uint32_t)(s * (HALF_BYTES >> 4) + 2 * k), (j != kb || k != 0) ? 1u : 0u);
+                            commit_pair(&sm->empty[s]);
+                            if (j == end - 1)
+                                commit_pair(&sm->dfull[d]);
+                        }
+                        __syncwarp();
+                        if (++s == STAGES)
+                            s = 0, ph ^= 1;
+                    }
+                    if (++d == NBUF)
+                        d = 0, dph ^= 1;
+                }
+            }
+            // every MMA issued here has completed once `done` fires (in both CTAs)
+            if (elect_one())
+                commit_pair(&sm->done);
+            __syncwarp();
+            if (!mbar_wait(&sm->done, 0))
+                ok = false;
+            if (!ok && lane == 0)
+                sm->failed = 1;
+        }
+    } else {
+        // epilogue: rows m0 + 128 rank + 32 q + lane, columns n0 + EW h .. on.  The tensor core runs at
+        // most two slices ahead, so a tile's way out has to be short: 16 warps
+        const int q = warp & 3, h = (warp - 2) >> 2;
+        const MatmulI8Args& g = p.g;
+        const uint32_t lead = peer_addr(&sm->dempty[0], 0);
+        const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(EW * h);
+        bool ok = true;
+        int d = 0;
+        uint32_t ph = 0;   // accumulator, and the parity whose end fills it
+        for (int i = pair; i < p.p.items && ok; i += pairs) {
+            const Item t = item_at(p, i);
+            const int nc = t.n0 + EW * h, r0 = t.m0 + (int)rank * HM + 32 * q;
+            const int NS = (t.kb1 - t.kb0 + SLICE_KB - 1) / SLICE_KB;
+            float sa = 0.0f, own[2] = {0.0f, 0.0f};
+            if (g.s_a && r0 + lane < g.M)
+                sa = flush(__ldg(g.s_a + r0 + lane));
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (g.s_b && nc + 2 * lane + e < g.N)
+                    own[e] = flush(__ldg(g.s_b + nc + 2 * lane + e));
+            // The first slice stays as it comes, the second is added as floats (together at most 2^24,
+            // exact) and both become int32 once the accumulator is free: what stands between a tile's
+            // way out and the next tile's third slice is then the loads alone
+            uint32_t acc[EW];
+            ok = mbar_wait(&sm->dfull[d], ph);
+            if (!ok)
+                break;
+            fence_after();
+#pragma unroll
+            for (int c = 0; c < EW; c += 16)
+                tmem_ask16(at + (uint32_t)(d * TN + c), acc + c);
+#pragma unroll
+            for (int c = 0; c < EW; c += 16)
+                tmem_got16(acc + c);
+            release(lead + 8 * d, lane);
+            turn_buffer(d, ph);
+            if (NS > 1) {
+                ok = mbar_wait(&sm->dfull[d], ph);
+                if (!ok)
+                    break;
+                fence_after();
+                add_slice<true>(acc, at + (uint32_t)(d * TN));
+                release(lead + 8 * d, lane);
+                turn_buffer(d, ph);
+            }
+#pragma unroll
+            for (int j = 0; j < EW; ++j)
+                acc[j] = (uint32_t)__float2int_rn(__uint_as_float(acc[j]));
+            for (int sl = 2; sl < NS && ok; ++sl) {
+                ok = mbar_wait(&sm->dfull[d], ph);
+                if (!ok)
+                    break;
+                fence_after();
+                add_slice<false>(acc, at + (uint32_t)(d * TN));
+                release(lead + 8 * d, lane);
+                turn_buffer(d, ph);
             }
             if (!ok)
                 break;
-            const float sa = g.s_a && r0 + lane < g.M ? flush(__ldg(g.s_a + r0 + lane)) : 0.0f;
-            constexpr int W = 128 / (int)sizeof(Y);   // columns of a 128-byte staging row
+            if (t.part >= 0) {
+                int* out = p.parts + (int64_t)t.part * (2 * HM * TN) + (int64_t)((int)rank * HM + 32 * q + lane) * TN + EW * h;
 #pragma unroll
-            for (int c = 0; c < 128 / W; ++c) {
-                const int nb = nc + W * c;
-                if (r0 >= g.M || nb >= g.N)   // warp-uniform
-                    continue;
-                // the old values of this row: a reduction in L2 would not flush subnormals
-                float old[sizeof(Y) == 4 ? W : 1];
-                if (sizeof(Y) == 4 && p.y_tma && g.accumulate && r0 + lane < g.M) {
-                    const float* src = static_cast<const float*>(g.y) + (int64_t)(r0 + lane) * g.y_ld + nb;
-                    if (nb + W <= g.N) {
+                for (int c = 0; c < EW; c += 8) {
+                    uint32_t w[8];
 #pragma unroll
-                        for (int k = 0; k < W / 4; ++k) {
-                            const float4 v = load4(src + 4 * k);
-                            old[4 * k] = v.x, old[4 * k + 1] = v.y, old[4 * k + 2] = v.z, old[4 * k + 3] = v.w;
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < W; ++j)
-                            old[j] = nb + j < g.N ? src[j] : 0.0f;
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = acc[c + e];
+                    store32(out + c, w);
                 }
-                if (p.y_tma) {
-                    if (lane == 0)
-                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {   // 16 bytes a step
-                    float o[W / 8];
-#pragma unroll
-                    for (int e = 0; e < W / 8; ++e) {
-                        const int j = W / 8 * k + e;
-                        const float sb = g.s_b && nb + j < g.N ? flush(__ldg(g.s_b + nb + j)) : 0.0f;
-                        o[e] = scaled(acc[W * c + j], g.s_a, sa, g.s_b, sb);
-                    }
-                    if (p.y_tma) {
-                        if (sizeof(Y) == 4 && g.accumulate) {
-#pragma unroll
-                            for (int e = 0; e < W / 8; ++e)
-                                o[e] = fadd_ftz(old[W / 8 * k + e], o[e]);
-                        }
-                        store16(reinterpret_cast<Y*>(stg + lane * 128 + 16 * (k ^ (lane & 7))), o);
-                    } else if (r0 + lane < g.M) {
-#pragma unroll
-                        for (int e = 0; e < W / 8; ++e)
-                            if (nb + W / 8 * k + e < g.N)
-                                put(static_cast<Y*>(g.y) + (int64_t)(r0 + lane) * g.y_ld + nb + W / 8 * k + e, o[e], g.accumulate);
-                    }
-                }
-                if (p.y_tma) {
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0)
-                        store_tile(&map_y, stg, nb, r0);
-                }
+            } else if (r0 < g.M) {   // warp-uniform
+                finish<Y>(p, &map_y, acc, STG + (warp - 2) * STG_BYTES, lane, sa, own, r0, nc);
             }
         }
         if (!ok && lane == 0)
@@ -648,6 +852,35 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
     }
     if (threadIdx.x == 0 && sm->failed)
         atomicOr(p.err, kErrTimeoutBit);
+}
+
+// the cut tiles: the sum of a tile's parts, scaled.  A thread takes 4 columns of a row
+template <typename Y>
+__global__ void __launch_bounds__(256)
+k_mm_join(const __grid_constant__ PairArgs p)
+{
+    pdl_wait();
+    const MatmulI8Args& g = p.g;
+    const int tile = blockIdx.x >> 6, e = (blockIdx.x & 63) * 256 + threadIdx.x;   // 64 CTAs a tile
+    int m0, n0;
+    tile_at(p.p, p.p.whole + tile, m0, n0);
+    const int r = e >> 6, c = 4 * (e & 63);
+    const int64_t m = m0 + r, n = n0 + c;
+    if (m >= g.M || n >= g.N)
+        return;
+    const int* part = p.parts + (int64_t)tile * p.p.split * (2 * HM * TN) + r * TN + c;
+    int4 s = *reinterpret_cast<const int4*>(part);
+    for (int k = 1; k < p.p.split; ++k) {
+        const int4 v = *reinterpret_cast<const int4*>(part + (int64_t)k * (2 * HM * TN));
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    const int acc[4] = {s.x, s.y, s.z, s.w};
+    const float sa = g.s_a ? flush(__ldg(g.s_a + m)) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < g.N)
+            put(static_cast<Y*>(g.y) + m * g.y_ld + n + i,
+                scaled(acc[i], g.s_a, sa, g.s_b, g.s_b ? flush(__ldg(g.s_b + n + i)) : 0.0f), g.accumulate);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
@@ -678,34 +911,37 @@ bool make_map(CUtensorMap* map, const void* p, CUtensorMapDataType type, int siz
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename Y> cudaError_t run_pair(const MatmulI8Args& g, const __nv_bfloat16* xa, const __nv_bfloat16* xb, cudaStream_t st)
+template <typename Y>
+cudaError_t run_pair(const MatmulI8Args& g, const __nv_bfloat16* xa, const __nv_bfloat16* xb, int* parts, cudaStream_t st)
 {
     PairArgs p = {};
     p.g = g;
+    p.p = plan_of(g.M, g.N, g.K);
     p.K = (int)g.K;
-    p.tiles_n = (int)((g.N + TN - 1) / TN);
-    p.tiles = (int)((g.M + 2 * HM - 1) / (2 * HM)) * p.tiles_n;
+    p.parts = parts;
     p.err = device_error_word();
     if (!p.err)
         return cudaErrorInvalidValue;
+    const int64_t Kp = pad8(g.K), y_ld = g.M == 1 ? (g.N + 7) / 8 * 8 : g.y_ld;
+    p.y_tma = reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && y_ld * (int64_t)sizeof(Y) % 16 == 0;
     CUtensorMap ma, mb, my;
     memset(&my, 0, sizeof(my));
-    const int64_t Kp = pad8(g.K);
     if (!make_map(&ma, xa, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.M, Kp, Kp, HM) ||
-        !make_map(&mb, xb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.N, Kp, Kp, HM))
-        return cudaErrorInvalidValue;
-    // tensor stores need rows on 16-byte boundaries
-    p.y_tma = reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && (g.M == 1 || g.y_ld * (int64_t)sizeof(Y) % 16 == 0);
-    const int64_t y_pitch = g.M == 1 ? (g.N + 7) / 8 * 8 : g.y_ld;
-    if (p.y_tma && !make_map(&my, g.y, sizeof(Y) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                             (int)sizeof(Y), g.M, g.N, y_pitch, 32))
+        !make_map(&mb, xb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.N, Kp, Kp, HM) ||
+        (p.y_tma && !make_map(&my, g.y, sizeof(Y) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                              (int)sizeof(Y), g.M, g.N, y_ld, 32)))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(k_mm_pair<Y>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
     if (e != cudaSuccess)
         return e;
-    const int pairs = std::min(p.tiles, num_sms() / 2);
+    const int pairs = std::min(p.p.items, p.p.pairs);
     e = launch_pdl(k_mm_pair<Y>, dim3((unsigned)(2 * pairs)), dim3(THREADS), SMEM_BYTES, st, ma, mb, my, p);
     count_launches(1);
+    if (e == cudaSuccess && p.p.split > 1) {
+        const int cut = (p.p.items - p.p.whole) / p.p.split;
+        e = launch_pdl(k_mm_join<Y>, dim3((unsigned)(64 * cut)), dim3(256), 0, st, p);
+        count_launches(1);
+    }
     return e;
 }
 
@@ -723,7 +959,8 @@ template <typename Y> cudaError_t launch(const MatmulI8Args& g, void* ws, bool t
     cudaError_t e = widen(g.a, g.a_ld, g.M, g.K, g.a_t, xa, st);
     if (e == cudaSuccess)
         e = widen(g.b, g.b_ld, g.N, g.K, g.b_t, xb, st);
-    return e == cudaSuccess ? run_pair<Y>(g, xa, xb, st) : e;
+    int* parts = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(xb) + align256(2 * g.N * pad8(g.K)));
+    return e == cudaSuccess ? run_pair<Y>(g, xa, xb, parts, st) : e;
 }
 
 } // namespace
@@ -734,7 +971,9 @@ size_t matmul_i8_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_t, bool b_t)
 {
     if (matmul_i8_small(M, a_t, b_t))
         return 0;
-    return (size_t)(align256(2 * M * pad8(K)) + align256(2 * N * pad8(K)));
+    const Plan p = plan_of(M, N, K);
+    const int64_t parts = p.split > 1 ? p.items - p.whole : 0;
+    return (size_t)(align256(2 * M * pad8(K)) + align256(2 * N * pad8(K)) + parts * PART_BYTES);
 }
 
 cudaError_t launch_matmul_i8(const MatmulI8Args& g, void* ws, bool tc, cudaStream_t st)

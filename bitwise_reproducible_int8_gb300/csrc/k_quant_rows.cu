@@ -73,7 +73,10 @@ __device__ __forceinline__ void values4(const Kernel& k, const T* p, int64_t d, 
     }
 }
 
-template <typename T>
+// VEC: rows of x and q on 4-element boundaries, whole groups of 4 (and mul on 16 bytes): every load is
+// issued before the first value is looked at.  (With a branch around each load, one was in flight at a
+// time: 198 us against 81 for 16384 x 5632 fp32.)
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(512)
 k_quant_tokens(const __grid_constant__ Kernel k)
 {
@@ -82,27 +85,61 @@ k_quant_tokens(const __grid_constant__ Kernel k)
     const int64_t D = k.a.D;
     int phase = 0;
     pdl_wait();
+    pdl_trigger();
     for (int64_t i0 = (int64_t)blockIdx.x * per; i0 < k.a.n; i0 += (int64_t)gridDim.x * per) {
         const int64_t i = i0 + sub;
         const bool live = i < k.a.n;
         const T* row = static_cast<const T*>(k.a.x) + i * k.a.x_ld;
         float v[4][4];
         unsigned m = 0;
-        if (live) {
+        if (VEC) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const int64_t d = 4 * ((int64_t)t + g * tpr);
-                if (d < D) {
-                    values4<T, true>(k, row, d, v[g]);
-                    m = max(max(max(m, magnitude(v[g][0])), max(magnitude(v[g][1]), magnitude(v[g][2]))), magnitude(v[g][3]));
-                }
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (live && d < D)
+                    x = stream4(row + d);
+                v[g][0] = x.x, v[g][1] = x.y, v[g][2] = x.z, v[g][3] = x.w;
             }
+            if (k.a.mul) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int64_t d = 4 * ((int64_t)t + g * tpr);
+                    float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (d < D)
+                        f = load4(k.a.mul + d);
+                    v[g][0] = fmul_flush(flush(v[g][0]), flush(f.x)), v[g][1] = fmul_flush(flush(v[g][1]), flush(f.y));
+                    v[g][2] = fmul_flush(flush(v[g][2]), flush(f.z)), v[g][3] = fmul_flush(flush(v[g][3]), flush(f.w));
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[g][e] = flush(v[g][e]);
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int64_t d = 4 * ((int64_t)t + g * tpr);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[g][e] = 0.0f;
+                if (live && d < D)
+                    values4<T, true>(k, row, d, v[g]);
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                m = max(m, magnitude(v[g][e]));
+        if (live)
             for (int64_t d = 4 * ((int64_t)t + 4 * tpr); d < D; d += 4 * tpr) {
                 float w[4];
                 values4<T, false>(k, row, d, w);
                 m = max(max(max(m, magnitude(w[0])), max(magnitude(w[1]), magnitude(w[2]))), magnitude(w[3]));
             }
-        }
         m = __reduce_max_sync(0xffffffffu, m);
         if (tpr > 32) {   // one row a CTA
             if ((t & 31) == 0)
@@ -120,7 +157,7 @@ k_quant_tokens(const __grid_constant__ Kernel k)
         for (int g = 0; g < 4; ++g) {
             const int64_t d = 4 * ((int64_t)t + g * tpr);
             if (d < D)
-                put4(q, d, D, k.qvec, codes4(v[g], c));
+                put4(q, d, D, VEC || k.qvec, codes4(v[g], c));
         }
         for (int64_t d = 4 * ((int64_t)t + 4 * tpr); d < D; d += 4 * tpr) {
             float w[4];
@@ -132,8 +169,40 @@ k_quant_tokens(const __grid_constant__ Kernel k)
     }
 }
 
+constexpr int RUN = 8;   // tokens whose loads a warp has in flight by columns
+
+// four columns of RUN tokens, `step` apart, times their multipliers; 0 past the last
+template <typename T, bool VEC>
+__device__ __forceinline__ void take_run(const Kernel& k, int64_t i, int64_t hi, int step, int64_t d, float (&v)[RUN][4])
+{
+    const T* x = static_cast<const T*>(k.a.x);
+    float f[RUN];
+#pragma unroll
+    for (int u = 0; u < RUN; ++u) {
+        const int64_t r = i + u * step;
+        f[u] = 1.0f;
+        if (VEC) {
+            float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r < hi)
+                w = load4(x + r * k.a.x_ld + d);
+            v[u][0] = w.x, v[u][1] = w.y, v[u][2] = w.z, v[u][3] = w.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[u][e] = r < hi && d + e < k.a.D ? to_f32<T>(x[r * k.a.x_ld + d + e]) : 0.0f;
+        }
+        if (k.a.mul && r < hi)
+            f[u] = __ldg(k.a.mul + r);
+    }
+#pragma unroll
+    for (int u = 0; u < RUN; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[u][e] = fmul_flush(flush(v[u][e]), flush(f[u]));
+}
+
 // a CTA: 32 x 4 columns of a slab of tokens, 8 warps taking every eighth token
-template <typename T>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
 k_column_max(const __grid_constant__ Kernel k)
 {
@@ -146,14 +215,14 @@ k_column_max(const __grid_constant__ Kernel k)
     pdl_trigger();
     unsigned m[4] = {0, 0, 0, 0};
     if (d < k.a.D)
-#pragma unroll 4
-        for (int64_t i = lo + warp; i < hi; i += 8) {
-            float v[4];
-            take4<T, false>(static_cast<const T*>(k.a.x) + i * k.a.x_ld, d, k.a.D, k.vec, v);
-            const float f = k.a.mul ? flush(__ldg(k.a.mul + i)) : 1.0f;
+        for (int64_t i = lo + warp; i < hi; i += 8 * RUN) {
+            float v[RUN][4];
+            take_run<T, VEC>(k, i, hi, 8, d, v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                m[e] = max(m[e], magnitude(fmul_flush(flush(v[e]), f)));
+            for (int u = 0; u < RUN; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    m[e] = max(m[e], magnitude(v[u][e]));
         }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -170,7 +239,7 @@ k_column_max(const __grid_constant__ Kernel k)
     }
 }
 
-template <typename T>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
 k_quant_columns(const __grid_constant__ Kernel k)
 {
@@ -190,14 +259,15 @@ k_quant_columns(const __grid_constant__ Kernel k)
         if (slab == 0 && warp == 0 && d + e < k.a.D)
             k.a.scales[d + e] = c[e].s;
     }
-    for (int64_t i = lo + warp; i < hi; i += 8) {
-        float v[4];
-        take4<T, false>(static_cast<const T*>(k.a.x) + i * k.a.x_ld, d, k.a.D, k.vec, v);
-        const float f = k.a.mul ? flush(__ldg(k.a.mul + i)) : 1.0f;
+    for (int64_t i = lo + warp; i < hi; i += 8 * RUN) {
+        float v[RUN][4];
+        take_run<T, VEC>(k, i, hi, 8, d, v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            v[e] = fmul_flush(flush(v[e]), f);
-        put4(k.a.q + i * k.a.q_ld, d, k.a.D, k.qvec, codes4_by(v, c));
+        for (int u = 0; u < RUN; ++u) {
+            const int64_t r = i + 8 * u;
+            if (r < hi)
+                put4(k.a.q + r * k.a.q_ld, d, k.a.D, k.qvec, codes4_by(v[u], c));
+        }
     }
 }
 
@@ -210,19 +280,25 @@ template <typename T> cudaError_t launch(Kernel& k, cudaStream_t st)
         const int threads = k.tpr == 32 ? 128 : k.tpr, per = threads / k.tpr;
         const int64_t ctas = (a.n + per - 1) / per, most = (int64_t)num_sms() * 64;
         count_launches(1);
-        return launch_pdl(k_quant_tokens<T>, dim3((unsigned)(ctas < most ? ctas : most)), dim3(threads), 0, st, k);
+        const dim3 grid((unsigned)(ctas < most ? ctas : most));
+        return k.vec && k.qvec && a.D % 4 == 0 && (!a.mul || k.mvec)
+                   ? launch_pdl(k_quant_tokens<T, true>, grid, dim3(threads), 0, st, k)
+                   : launch_pdl(k_quant_tokens<T, false>, grid, dim3(threads), 0, st, k);
     }
     k.tiles = (int)((a.D + 127) / 128);
-    // slabs of a multiple of 32 tokens, about eight CTAs on every SM
+    // slabs of a multiple of 64 tokens, about eight CTAs on every SM
     const int64_t want = (8 * (int64_t)num_sms() + k.tiles - 1) / k.tiles, tokens = (a.n + want - 1) / want;
-    k.slab = tokens < 32 ? 32 : (tokens + 31) / 32 * 32;
+    k.slab = tokens < 64 ? 64 : (tokens + 63) / 64 * 64;
     const int64_t slabs = (a.n + k.slab - 1) / k.slab;
     const dim3 grid((unsigned)(k.tiles * slabs));
     cudaError_t e = cudaMemsetAsync(k.top, 0, (size_t)a.D * 4, st);
+    const bool vec = k.vec && a.D % 4 == 0;
     if (e == cudaSuccess)
-        e = launch_pdl(k_column_max<T>, grid, dim3(256), 0, st, k);
+        e = vec ? launch_pdl(k_column_max<T, true>, grid, dim3(256), 0, st, k)
+                : launch_pdl(k_column_max<T, false>, grid, dim3(256), 0, st, k);
     if (e == cudaSuccess)
-        e = launch_pdl(k_quant_columns<T>, grid, dim3(256), 0, st, k);
+        e = vec ? launch_pdl(k_quant_columns<T, true>, grid, dim3(256), 0, st, k)
+                : launch_pdl(k_quant_columns<T, false>, grid, dim3(256), 0, st, k);
     count_launches(2);
     return e;
 }

@@ -19,29 +19,34 @@ namespace repro {
 namespace {
 
 constexpr int GROUP = 128;
+constexpr int RUN = 2;       // groups whose loads a warp has in flight
 
 struct Kernel {
     SwigluArgs s;
     int64_t G, items;      // groups of a row, of all rows
-    bool vec, avec;        // gu (dgu) and a (da) on 4-element boundaries, F too
+    int64_t rows, groups;  // how far a warp steps: so many rows and groups
 };
 
-template <typename T> __device__ __forceinline__ void take4(const T* p, int64_t d, int64_t F, bool vec, float (&v)[4])
+// four neighbours from element d of F; VEC: on a boundary of 4 elements, F a multiple of 4
+template <bool VEC, typename T> __device__ __forceinline__ void take4(const T* p, int64_t d, int64_t F, bool live, float (&v)[4])
 {
-    if (vec && d + 4 <= F) {
-        const float4 x = stream4(p + d);
+    if (VEC) {
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (live && d < F)
+            x = stream4(p + d);
         v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            v[e] = d + e < F ? to_f32<T>(p[d + e]) : 0.0f;
+            v[e] = live && d + e < F ? to_f32<T>(p[d + e]) : 0.0f;
     }
 }
 
-template <typename T> __device__ __forceinline__ void put4(T* p, int64_t d, int64_t F, bool vec, const float (&v)[4])
+template <bool VEC, typename T> __device__ __forceinline__ void put4(T* p, int64_t d, int64_t F, const float (&v)[4])
 {
-    if (vec && d + 4 <= F) {
-        store4(p + d, make_float4(v[0], v[1], v[2], v[3]));
+    if (VEC) {
+        if (d < F)
+            store4(p + d, make_float4(v[0], v[1], v[2], v[3]));
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -81,77 +86,136 @@ __device__ __forceinline__ void keep(const float (&v)[4], int8_t* codes, float* 
         *scale = c.s;
 }
 
-template <typename T, typename A, bool KEEP>
+// The groups a warp takes: every so many, without a division for each
+struct Walk {
+    int64_t it, i, gr;   // group of all, row, group of the row
+
+    __device__ __forceinline__ Walk(const Kernel& k)
+    {
+        it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+        i = it / k.G;
+        gr = it - i * k.G;
+    }
+    __device__ __forceinline__ void next(const Kernel& k)
+    {
+        it += (int64_t)gridDim.x * 8;
+        i += k.rows;
+        gr += k.groups;
+        if (gr >= k.G) {
+            gr -= k.G;
+            ++i;
+        }
+    }
+};
+
+template <typename T, typename A, bool KEEP, bool VEC>
 __global__ void __launch_bounds__(256)
 k_swiglu_fwd(const __grid_constant__ Kernel k)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t F = k.s.F, step = (int64_t)gridDim.x * 8;
+    const int64_t F = k.s.F;
     pdl_wait();
-    for (int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); it < k.items; it += step) {
-        const int64_t i = it / k.G, gr = it - i * k.G, d = gr * GROUP + 4 * lane;
-        const T* row = static_cast<const T*>(k.s.gu) + i * k.s.gu_ld;
-        float g[4], u[4], sig[4], rest[4];
-        take4<T>(row, d, F, k.vec, g);
-        take4<T>(row + F, d, F, k.vec, u);
+    pdl_trigger();
+    for (Walk w(k); w.it < k.items;) {
+        float g[RUN][4], u[RUN][4];
+        int64_t i[RUN], gr[RUN];
+        bool live[RUN];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            g[e] = flush(g[e]), u[e] = flush(u[e]);
-        if (KEEP) {
-            const int64_t at = 2 * i * k.G + gr;
-            keep(g, k.s.codes + at * GROUP, k.s.scales + at, lane);
-            keep(u, k.s.codes + (at + k.G) * GROUP, k.s.scales + at + k.G, lane);
+        for (int r = 0; r < RUN; ++r) {
+            live[r] = w.it < k.items;
+            i[r] = w.i, gr[r] = w.gr;
+            const T* row = static_cast<const T*>(k.s.gu) + i[r] * k.s.gu_ld;
+            take4<VEC>(row, gr[r] * GROUP + 4 * lane, F, live[r], g[r]);
+            take4<VEC>(row + F, gr[r] * GROUP + 4 * lane, F, live[r], u[r]);
+            w.next(k);
         }
-        sigmoids(g, sig, rest);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            g[e] = fmul_flush(fmul_flush(g[e], sig[e]), u[e]);
-        put4<A>(static_cast<A*>(k.s.a) + i * k.s.a_ld, d, F, k.avec, g);
+        for (int r = 0; r < RUN; ++r) {
+            if (!live[r])
+                break;
+            float sig[4], rest[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                g[r][e] = flush(g[r][e]), u[r][e] = flush(u[r][e]);
+            if (KEEP) {
+                const int64_t at = 2 * i[r] * k.G + gr[r];
+                keep(g[r], k.s.codes + at * GROUP, k.s.scales + at, lane);
+                keep(u[r], k.s.codes + (at + k.G) * GROUP, k.s.scales + at + k.G, lane);
+            }
+            sigmoids(g[r], sig, rest);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                g[r][e] = fmul_flush(fmul_flush(g[r][e], sig[e]), u[r][e]);
+            put4<VEC>(static_cast<A*>(k.s.a) + i[r] * k.s.a_ld, gr[r] * GROUP + 4 * lane, F, g[r]);
+        }
     }
 }
 
-__device__ __forceinline__ void decode(const int8_t* codes, float s, int lane, float (&v)[4])
+__device__ __forceinline__ void decode(uint32_t c, float s, float (&v)[4])
 {
-    const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(codes) + lane);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         v[e] = dequant((int)(int8_t)(c >> (8 * e)), s);
 }
 
-template <typename T, typename A, bool KEPT>
+template <typename T, typename A, bool KEPT, bool VEC>
 __global__ void __launch_bounds__(256)
 k_swiglu_bwd(const __grid_constant__ Kernel k)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t F = k.s.F, step = (int64_t)gridDim.x * 8;
+    const int64_t F = k.s.F;
     pdl_wait();
-    for (int64_t it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); it < k.items; it += step) {
-        const int64_t i = it / k.G, gr = it - i * k.G, d = gr * GROUP + 4 * lane;
-        float g[4], u[4], da[4], sig[4], rest[4];
-        take4<A>(static_cast<const A*>(k.s.da) + i * k.s.a_ld, d, F, k.avec, da);
-        if (KEPT) {
-            const int64_t at = 2 * i * k.G + gr;
-            decode(k.s.codes + at * GROUP, flush(__ldg(k.s.scales + at)), lane, g);
-            decode(k.s.codes + (at + k.G) * GROUP, flush(__ldg(k.s.scales + at + k.G)), lane, u);
-        } else {
-            const T* row = static_cast<const T*>(k.s.gu) + i * k.s.gu_ld;
-            take4<T>(row, d, F, k.vec, g);
-            take4<T>(row + F, d, F, k.vec, u);
+    pdl_trigger();
+    for (Walk w(k); w.it < k.items;) {
+        float g[RUN][4], u[RUN][4], da[RUN][4], s[RUN][2];
+        uint32_t c[RUN][2];
+        int64_t i[RUN], gr[RUN];
+        bool live[RUN];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                g[e] = flush(g[e]), u[e] = flush(u[e]);
-        }
-        sigmoids(g, sig, rest);
+        for (int r = 0; r < RUN; ++r) {
+            live[r] = w.it < k.items;
+            i[r] = w.i, gr[r] = w.gr;
+            const int64_t d = gr[r] * GROUP + 4 * lane;
+            take4<VEC>(static_cast<const A*>(k.s.da) + i[r] * k.s.a_ld, d, F, live[r], da[r]);
+            if (KEPT) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float x = flush(da[e]);
-            const float dg = fmul_flush(fmul_flush(fmul_flush(x, u[e]), sig[e]), fadd_ftz(1.0f, fmul_rn(g[e], rest[e])));
-            u[e] = fmul_flush(x, fmul_flush(g[e], sig[e]));
-            g[e] = dg;
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t at = (2 * i[r] + h) * k.G + gr[r];
+                    c[r][h] = live[r] ? __ldg(reinterpret_cast<const uint32_t*>(k.s.codes + at * GROUP) + lane) : 0u;
+                    s[r][h] = live[r] ? __ldg(k.s.scales + at) : 0.0f;
+                }
+            } else {
+                const T* row = static_cast<const T*>(k.s.gu) + i[r] * k.s.gu_ld;
+                take4<VEC>(row, d, F, live[r], g[r]);
+                take4<VEC>(row + F, d, F, live[r], u[r]);
+            }
+            w.next(k);
         }
-        T* out = static_cast<T*>(k.s.dgu) + i * k.s.dgu_ld;
-        put4<T>(out, d, F, k.vec, g);
-        put4<T>(out + F, d, F, k.vec, u);
+#pragma unroll
+        for (int r = 0; r < RUN; ++r) {
+            if (!live[r])
+                break;
+            float sig[4], rest[4];
+            if (KEPT) {
+                decode(c[r][0], flush(s[r][0]), g[r]);
+                decode(c[r][1], flush(s[r][1]), u[r]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    g[r][e] = flush(g[r][e]), u[r][e] = flush(u[r][e]);
+            }
+            sigmoids(g[r], sig, rest);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = flush(da[r][e]);
+                const float dg = fmul_flush(fmul_flush(fmul_flush(x, u[r][e]), sig[e]), fadd_ftz(1.0f, fmul_rn(g[r][e], rest[e])));
+                u[r][e] = fmul_flush(x, fmul_flush(g[r][e], sig[e]));
+                g[r][e] = dg;
+            }
+            T* out = static_cast<T*>(k.s.dgu) + i[r] * k.s.dgu_ld;
+            put4<VEC>(out, gr[r] * GROUP + 4 * lane, F, g[r]);
+            put4<VEC>(out + F, gr[r] * GROUP + 4 * lane, F, u[r]);
+        }
     }
 }
 
@@ -163,16 +227,19 @@ template <typename T> bool vec_of(const void* p, int64_t ld, int64_t F)
 template <typename T, typename A> cudaError_t launch(Kernel& k, bool fwd, cudaStream_t st)
 {
     const SwigluArgs& s = k.s;
-    k.vec = vec_of<T>(s.gu, s.gu_ld, s.F) && vec_of<T>(s.dgu, s.dgu_ld, s.F);
-    k.avec = vec_of<A>(fwd ? s.a : s.da, s.a_ld, s.F);
+    const bool vec = vec_of<T>(s.gu, s.gu_ld, s.F) && vec_of<T>(s.dgu, s.dgu_ld, s.F) && vec_of<A>(fwd ? s.a : s.da, s.a_ld, s.F);
     const int64_t ctas = (k.items + 7) / 8, most = (int64_t)num_sms() * 32;
     const dim3 grid((unsigned)(ctas < most ? ctas : most));
+    const int64_t step = 8 * (int64_t)grid.x;
+    k.rows = step / k.G;
+    k.groups = step - k.rows * k.G;
     count_launches(1);
-    if (fwd)
-        return s.codes ? launch_pdl(k_swiglu_fwd<T, A, true>, grid, dim3(256), 0, st, k)
-                       : launch_pdl(k_swiglu_fwd<T, A, false>, grid, dim3(256), 0, st, k);
-    return s.codes ? launch_pdl(k_swiglu_bwd<T, A, true>, grid, dim3(256), 0, st, k)
-                   : launch_pdl(k_swiglu_bwd<T, A, false>, grid, dim3(256), 0, st, k);
+#define GO(F) (s.codes ? (vec ? launch_pdl(F<T, A, true, true>, grid, dim3(256), 0, st, k) \
+                              : launch_pdl(F<T, A, true, false>, grid, dim3(256), 0, st, k)) \
+                       : (vec ? launch_pdl(F<T, A, false, true>, grid, dim3(256), 0, st, k) \
+                              : launch_pdl(F<T, A, false, false>, grid, dim3(256), 0, st, k)))
+    return fwd ? GO(k_swiglu_fwd) : GO(k_swiglu_bwd);
+#undef GO
 }
 
 cudaError_t dispatch(const SwigluArgs& a, bool fwd, cudaStream_t st)
