@@ -76,4 +76,34 @@ __device__ __forceinline__ unsigned long long exp_r2(unsigned long long x)
     return pack2(exp_scale(p0, k0), exp_scale(p1, k1));
 }
 
+// exp_r of two lanes whose arguments are not above 0 (a NaN counts as far below: 0), in fewer
+// operations and with the same bits: 2^k is an addition to the exponent, k the low bits of
+// x log2 e + 1.5 2^23; below e^-100 nothing is left, so the argument may stop there; and the
+// flushes that can change nothing are left out (k and its products are 0 or normal)
+__device__ __forceinline__ unsigned long long exp_r2_neg(float x0, float x1)
+{
+    const unsigned long long M = pack2(12582912.0f, 12582912.0f);
+    const unsigned long long x = pack2(fmaxf(x0, -100.0f), fmaxf(x1, -100.0f));
+    const unsigned long long t = fadd2_ftz(fmul2_rn(x, pack2(0x1.715476p+0f, 0x1.715476p+0f)), M);
+    const unsigned long long kf = fadd2_ftz(t, pack2(-12582912.0f, -12582912.0f));
+    const unsigned long long r = fadd2_ftz(fadd2_ftz(x, fmul2_rn(kf, pack2(-0x1.63p-1f, -0x1.63p-1f))),
+                                           fmul2_rn(kf, pack2(0x1.bd0106p-13f, 0x1.bd0106p-13f)));
+    unsigned long long p = pack2(0x1.a01a02p-13f, 0x1.a01a02p-13f);
+    p = fadd2_ftz(fmul2_rn(p, r), pack2(0x1.6c16c2p-10f, 0x1.6c16c2p-10f));
+    p = fadd2_ftz(fmul2_rn(p, r), pack2(0x1.111112p-7f, 0x1.111112p-7f));
+    p = fadd2_ftz(fmul2_rn(p, r), pack2(0x1.555556p-5f, 0x1.555556p-5f));
+    p = fadd2_ftz(fmul2_rn(p, r), pack2(0x1.555556p-3f, 0x1.555556p-3f));
+    p = fadd2_ftz(fmul2_rn(p, r), pack2(0.5f, 0.5f));
+    p = fadd2_ftz(fmul2_rn(p, r), pack2(1.0f, 1.0f));
+    p = fadd2_ftz(fmul2_rn(p, r), pack2(1.0f, 1.0f));
+    float p0, p1, t0, t1, k0, k1;
+    unpack2(p, p0, p1);
+    unpack2(t, t0, t1);
+    unpack2(kf, k0, k1);
+    // k = -126 with a factor below 1 is subnormal, and below -126 all is
+    p0 = k0 >= -126.0f ? __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23)) : 0.0f;
+    p1 = k1 >= -126.0f ? __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23)) : 0.0f;
+    return fadd2_ftz(pack2(p0, p1), pack2(-0.0f, -0.0f));
+}
+
 } // namespace repro

@@ -18,6 +18,8 @@
 namespace repro {
 namespace {
 
+typedef unsigned long long u64;
+
 constexpr int GROUP = 128;
 constexpr int RUN = 2;       // groups whose loads a warp has in flight
 
@@ -55,32 +57,43 @@ template <bool VEC, typename T> __device__ __forceinline__ void put4(T* p, int64
     }
 }
 
-// sig(g) and sig(-g) of four
-__device__ __forceinline__ void sigmoids(const float (&g)[4], float (&sig)[4], float (&rest)[4])
+__device__ __forceinline__ u64 mul_flush2(u64 a, u64 b) { return fadd2_ftz(fmul2_rn(a, b), pack2(-0.0f, -0.0f)); }
+__device__ __forceinline__ u64 flush2(u64 a) { return fadd2_ftz(a, pack2(-0.0f, -0.0f)); }
+
+// RN(1 / d) for d in [1, 2]: the hardware's reciprocal (within 2^-23) and one Newton step, which is
+// correctly rounded by Markstein's theorem (P. Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990) but for a significand of all ones; equal to the division for
+// every float of the interval, that one included (all 2^23 + 1 compared)
+__device__ __forceinline__ float reciprocal(float d)
 {
-    float e[4];
-#pragma unroll
-    for (int i = 0; i < 4; i += 2)
-        unpack2(exp_r2(pack2(-fabsf(g[i]), -fabsf(g[i + 1]))), e[i], e[i + 1]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float w = __frcp_rn(fadd_ftz(1.0f, e[i])), ew = fmul_flush(e[i], w);
-        sig[i] = g[i] >= 0.0f ? w : ew;
-        rest[i] = g[i] >= 0.0f ? ew : w;
-    }
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    return __fmaf_rn(r, __fmaf_rn(-d, r, 1.0f), r);
 }
 
-__device__ __forceinline__ unsigned magnitude(float v)
+// sig(g), and with REST sig(-g), of two
+template <bool REST> __device__ __forceinline__ u64 sigmoids(u64 g, u64& rest)
 {
-    const unsigned m = __float_as_uint(v) & 0x7fffffffu;
-    return m > 0x7f800000u ? 0u : m;   // a NaN is passed over
+    float g0, g1, d0, d1;
+    unpack2(g, g0, g1);
+    const u64 e = exp_r2_neg(-fabsf(g0), -fabsf(g1));
+    unpack2(fadd2_ftz(e, pack2(1.0f, 1.0f)), d0, d1);
+    const float w0 = reciprocal(d0), w1 = reciprocal(d1);
+    float s0, s1;
+    unpack2(mul_flush2(e, pack2(w0, w1)), s0, s1);
+    const bool up0 = g0 >= 0.0f, up1 = g1 >= 0.0f;
+    if (REST)
+        rest = pack2(up0 ? s0 : w0, up1 ? s1 : w1);
+    return pack2(up0 ? w0 : s0, up1 ? w1 : s1);
 }
 
-// the group's codes and scale
+// the group's codes and scale.  Subnormals are not flushed one by one: the maximum is, and beside a
+// scale of 2^-100 or more they are nothing
 __device__ __forceinline__ void keep(const float (&v)[4], int8_t* codes, float* scale, int lane)
 {
-    const unsigned m = max(max(magnitude(v[0]), magnitude(v[1])), max(magnitude(v[2]), magnitude(v[3])));
-    const CodeScale c = code_scale_of_max(__uint_as_float(__reduce_max_sync(0xffffffffu, m)));
+    const float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));   // passes over NaN
+    const unsigned top = __reduce_max_sync(0xffffffffu, m != m ? 0u : __float_as_uint(m));
+    const CodeScale c = code_scale_of_max(__uint_as_float(top));
     reinterpret_cast<uint32_t*>(codes)[lane] = codes4(v, c);
     if (lane == 0)
         *scale = c.s;
@@ -133,29 +146,27 @@ k_swiglu_fwd(const __grid_constant__ Kernel k)
         for (int r = 0; r < RUN; ++r) {
             if (!live[r])
                 break;
-            float sig[4], rest[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                g[r][e] = flush(g[r][e]), u[r][e] = flush(u[r][e]);
             if (KEEP) {
                 const int64_t at = 2 * i[r] * k.G + gr[r];
                 keep(g[r], k.s.codes + at * GROUP, k.s.scales + at, lane);
                 keep(u[r], k.s.codes + (at + k.G) * GROUP, k.s.scales + at + k.G, lane);
             }
-            sigmoids(g[r], sig, rest);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                g[r][e] = fmul_flush(fmul_flush(g[r][e], sig[e]), u[r][e]);
+            for (int e = 0; e < 4; e += 2) {   // a subnormal g is flushed with its product, sig being at most 1
+                const u64 gg = pack2(g[r][e], g[r][e + 1]);
+                u64 none;
+                const u64 a = mul_flush2(mul_flush2(gg, sigmoids<false>(gg, none)), flush2(pack2(u[r][e], u[r][e + 1])));
+                unpack2(a, g[r][e], g[r][e + 1]);
+            }
             put4<VEC>(static_cast<A*>(k.s.a) + i[r] * k.s.a_ld, gr[r] * GROUP + 4 * lane, F, g[r]);
         }
     }
 }
 
-__device__ __forceinline__ void decode(uint32_t c, float s, float (&v)[4])
+// two neighbours of a group: from its codes, or as they are
+__device__ __forceinline__ u64 decode(uint32_t c, int e, float s)
 {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        v[e] = dequant((int)(int8_t)(c >> (8 * e)), s);
+    return mul_flush2(pack2(__int2float_rn((int)(int8_t)(c >> (8 * e))), __int2float_rn((int)(int8_t)(c >> (8 * e + 8)))), pack2(s, s));
 }
 
 template <typename T, typename A, bool KEPT, bool VEC>
@@ -195,22 +206,17 @@ k_swiglu_bwd(const __grid_constant__ Kernel k)
         for (int r = 0; r < RUN; ++r) {
             if (!live[r])
                 break;
-            float sig[4], rest[4];
-            if (KEPT) {
-                decode(c[r][0], flush(s[r][0]), g[r]);
-                decode(c[r][1], flush(s[r][1]), u[r]);
-            } else {
+            const float sg = KEPT ? flush(s[r][0]) : 0.0f, su = KEPT ? flush(s[r][1]) : 0.0f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    g[r][e] = flush(g[r][e]), u[r][e] = flush(u[r][e]);
-            }
-            sigmoids(g[r], sig, rest);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = flush(da[r][e]);
-                const float dg = fmul_flush(fmul_flush(fmul_flush(x, u[r][e]), sig[e]), fadd_ftz(1.0f, fmul_rn(g[r][e], rest[e])));
-                u[r][e] = fmul_flush(x, fmul_flush(g[r][e], sig[e]));
-                g[r][e] = dg;
+            for (int e = 0; e < 4; e += 2) {
+                const u64 gg = KEPT ? decode(c[r][0], e, sg) : flush2(pack2(g[r][e], g[r][e + 1]));
+                const u64 uu = KEPT ? decode(c[r][1], e, su) : flush2(pack2(u[r][e], u[r][e + 1]));
+                const u64 x = flush2(pack2(da[r][e], da[r][e + 1]));
+                u64 rest;
+                const u64 sig = sigmoids<true>(gg, rest);
+                const u64 slope = fadd2_ftz(fmul2_rn(gg, rest), pack2(1.0f, 1.0f));
+                unpack2(mul_flush2(mul_flush2(mul_flush2(x, uu), sig), slope), g[r][e], g[r][e + 1]);
+                unpack2(mul_flush2(x, mul_flush2(gg, sig)), u[r][e], u[r][e + 1]);
             }
             T* out = static_cast<T*>(k.s.dgu) + i[r] * k.s.dgu_ld;
             put4<VEC>(out, gr[r] * GROUP + 4 * lane, F, g[r]);

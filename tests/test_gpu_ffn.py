@@ -364,3 +364,17 @@ def test_matmul_paths_agree(hook):
         R.repro_set_launch_cfg(reset=True)
     same(out[0], out[1])
     R.repro_device_check()                                  # takes the forced failure's report
+
+
+def test_swiglu_reciprocals(orc):
+    """sig(g) over 4 million gates of every size: e^-|g| takes values all over (0, 1], and with it the
+    reciprocal of 1 + e."""
+    g = rng(21)
+    gate = np.concatenate([g.uniform(-20, 20, 1 << 21), g.uniform(-1, 1, 1 << 20),
+                           10.0 ** g.uniform(-12, 2, 1 << 20) * g.choice([-1, 1], 1 << 20)]).astype(f32)
+    gu = np.stack([gate.reshape(-1, 1024), np.ones((gate.size // 1024, 1024), f32)], 1).reshape(-1, 2048)
+    a, dgu = torch.empty((gu.shape[0], 1024), device="cuda"), torch.empty(gu.shape, device="cuda")
+    R.repro_swiglu_fwd(dev(gu), a)
+    same(host(a), orc.swiglu_fwd(gu)[0])
+    R.repro_swiglu_bwd(torch.ones_like(a), dgu, gu=dev(gu))
+    same(host(dgu), orc.swiglu_bwd(np.ones(a.shape, f32), gu=gu))
