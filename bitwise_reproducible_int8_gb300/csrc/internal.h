@@ -261,6 +261,7 @@ struct NormArgs {
     float *dgain_post, *dgain_pre;
     float* parts[3];     // set by the launchers: partial sums of gain_pre, gain_post and a gate that is one row
     int64_t pitch;
+    int chunk;           // tokens whose terms a group of the backward sums
     int tpr;             // threads of a row
     float inv;           // 1 / D where D is a power of two, else 0
     bool vec;            // every row on 4-element boundaries

@@ -11,6 +11,9 @@
 // The gradients that are sums over tokens: a group of the backward takes 16 consecutive tokens one
 // after another and keeps its columns' sums in registers, so a chunk's order costs nothing, and
 // writes one row of partial sums (1/16 of a stream of the pass, out of L2); k_rowtree.cu joins them.
+// A few tokens would leave most of the card idle that way, and 16 rows one after another are all
+// latency: then a group takes one token and writes its terms, and k_norm_fold adds the chunks up
+// (1023 x 1001 bf16: 79 us in chunks).
 #include "internal.h"
 #include "launch.cuh"
 #include "rows.cuh"
@@ -18,7 +21,7 @@
 namespace repro {
 namespace {
 
-constexpr int CHUNK = 16;        // tokens a group of the backward sums: REPRO_NORM_CHUNK
+constexpr int CHUNK = 16;        // tokens of a chunk of the sums over tokens: REPRO_NORM_CHUNK
 
 __device__ __forceinline__ float rms_of(float S, const NormArgs& a)
 {
@@ -145,31 +148,81 @@ __device__ __forceinline__ void store_parts(float* parts, int64_t chunk, int64_t
     }
 }
 
-template <typename T, typename U, int THREADS, bool FULL>
-__global__ void __launch_bounds__(THREADS)
+// AHEAD: the next token's row is asked for as soon as this one's is taken, through shared memory (a
+// row of each stream on its way for every group on an SM); else loads where values are needed.
+// CHANNEL: a gate that is one row, whose sums take 16 more registers.  Three groups of 128 threads an
+// SM at 168 registers; with four at 128 the kernel spills.
+template <typename T, int THREADS, bool AHEAD, bool FULL, bool CHANNEL>
+__global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 384 / THREADS : 1)
 k_norm_bwd(const __grid_constant__ NormArgs a)
 {
+    extern __shared__ __align__(16) uint8_t slots[];
     __shared__ float red[4][64];
     int sub, phase = 0;
     const RowLane r = lane_of(a, sub);
     const int per = blockDim.x / a.tpr;
     const float alpha = flush(a.alpha), beta = flush(a.beta);
+    // slots of du, h, dh, y and the gate's rows
+    const size_t st = 4 * sizeof(Four<T>) * blockDim.x;
+    Four<T>* const s_h = reinterpret_cast<Four<T>*>(slots);
+    Four<T>* const s_dh = reinterpret_cast<Four<T>*>(slots + st);
+    Four<T>* const s_y = reinterpret_cast<Four<T>*>(slots + 2 * st);
+    Four<T>* const s_gate = reinterpret_cast<Four<T>*>(slots + 3 * st);
+    void* const s_du = slots + (a.gate_rows ? 4 : 3) * st;
+    const bool gates = !CHANNEL && a.gate;
+    auto row_t = [&](const void* p, int64_t ld, int64_t i) { return static_cast<const T*>(p) + i * ld; };
+    auto ask_norm = [&](int64_t i) {      // what the norm before the block needs of token i
+        if (a.du) {
+            if (a.u_type == 0)
+                ask_row16<FULL>(static_cast<Four<float>*>(s_du), static_cast<const float*>(a.du) + i * a.du_ld, r);
+            else
+                ask_row16<FULL>(static_cast<Four<__nv_bfloat16>*>(s_du), static_cast<const __nv_bfloat16*>(a.du) + i * a.du_ld, r);
+            ask_row16<FULL>(s_h, row_t(a.hs, a.hs_ld, i), r);
+        }
+        asked();
+    };
+    auto ask_rest = [&](int64_t i) {
+        if (a.dh)
+            ask_row16<FULL>(s_dh, row_t(a.dh, a.dh_ld, i), r);
+        if (a.y)
+            ask_row16<FULL>(s_y, row_t(a.y, a.y_ld, i), r);
+        if (gates)
+            ask_row16<FULL>(s_gate, row_t(a.gate, a.gate_ld, i), r);
+        asked();
+    };
     pdl_wait();
     pdl_trigger();
-    const int64_t chunks = (a.n + CHUNK - 1) / CHUNK;
+    const int64_t chunks = (a.n + a.chunk - 1) / a.chunk;
     for (int64_t ch = (int64_t)blockIdx.x * per + sub; ch < chunks; ch += (int64_t)gridDim.x * per) {
-        u64 s_pre[8], s_post[8], s_gate[8];
-        const int64_t lo = ch * CHUNK, hi = lo + CHUNK < a.n ? lo + CHUNK : a.n;
+        u64 s_pre[8], s_post[8], s_chan[8];
+        const int64_t lo = ch * a.chunk, hi = lo + a.chunk < a.n ? lo + a.chunk : a.n;
+        if (AHEAD) {
+            ask_norm(lo);
+            ask_rest(lo);
+        }
+        float2 next = *reinterpret_cast<const float2*>(a.stats + 2 * lo);
         for (int64_t i = lo; i < hi; ++i) {
             const bool first = i == lo;
-            u64 g[8], unit[8], w[8];
-            if (a.dh)
-                load_row16<FULL, false>(static_cast<const T*>(a.dh) + i * a.dh_ld, r, g);
+            const float r1 = flush(next.x), r2 = flush(next.y);
+            if (i + 1 < hi)
+                next = *reinterpret_cast<const float2*>(a.stats + 2 * (i + 1));
+            u64 g[8], v[8], unit[8], w[8];
+            if (AHEAD)
+                wait_asked<1>();
             if (a.du) {
-                u64 v[8];
-                load_row16<FULL, true>(static_cast<const U*>(a.du) + i * a.du_ld, r, v);
-                load_row16<FULL, true>(static_cast<const T*>(a.hs) + i * a.hs_ld, r, unit);
-                const float r2 = flush(a.stats[2 * i + 1]);
+                if (!AHEAD) {
+                    if (a.u_type == 0)
+                        load_row16<FULL, true>(static_cast<const float*>(a.du) + i * a.du_ld, r, v);
+                    else
+                        load_row16<FULL, true>(static_cast<const __nv_bfloat16*>(a.du) + i * a.du_ld, r, v);
+                    load_row16<FULL, true>(row_t(a.hs, a.hs_ld, i), r, unit);
+                } else {
+                    if (a.u_type == 0)
+                        take_row16<FULL>(static_cast<const Four<float>*>(s_du), r, v);
+                    else
+                        take_row16<FULL>(static_cast<const Four<__nv_bfloat16>*>(s_du), r, v);
+                    take_row16<FULL>(s_h, r, unit);
+                }
                 flush16(v);
                 flush16(unit);
                 mul16(unit, r2);
@@ -179,50 +232,82 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
                     gain16<FULL>(a.gain_pre, r, w);
                     mul16(v, w);
                 }
+            }
+            if (AHEAD) {
+                if (i + 1 < hi)
+                    ask_norm(i + 1);
+                else
+                    asked();
+            }
+            if (a.du)
                 norm_back<FULL>(v, unit, r2, a, r, red[sub], phase);
-                if (a.dh) {
+            if (AHEAD)
+                wait_asked<1>();
+            if (a.dh) {
+                if (!AHEAD)
+                    load_row16<FULL, false>(row_t(a.dh, a.dh_ld, i), r, g);
+                else
+                    take_row16<FULL>(s_dh, r, g);
+                flush16(g);
+                if (a.du)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         g[e] = fadd2_ftz(g[e], v[e]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        g[e] = v[e];
-                }
             } else {
-                flush16(g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    g[e] = v[e];
             }
             if (!a.y) {
                 store_row16<FULL>(static_cast<T*>(a.dx) + i * a.dx_ld, r, g);
+                if (AHEAD) {
+                    if (i + 1 < hi)
+                        ask_rest(i + 1);
+                    else
+                        asked();
+                }
                 continue;
             }
-            u64 o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                o[e] = g[e];
-            mul16(o, alpha);
-            store_row16<FULL>(static_cast<T*>(a.dx) + i * a.dx_ld, r, o);
+                v[e] = g[e];
+            mul16(v, alpha);
+            store_row16<FULL>(static_cast<T*>(a.dx) + i * a.dx_ld, r, v);
             mul16(g, beta);
-            load_row16<FULL, true>(static_cast<const T*>(a.y) + i * a.y_ld, r, unit);
-            const float r1 = flush(a.stats[2 * i]);
+            if (!AHEAD)
+                load_row16<FULL, true>(row_t(a.y, a.y_ld, i), r, unit);
+            else
+                take_row16<FULL>(s_y, r, unit);
+            if (gates) {
+                if (!AHEAD)
+                    load_row16<FULL, true>(row_t(a.gate, a.gate_ld, i), r, w);
+                else
+                    take_row16<FULL>(s_gate, r, w);
+                flush16(w);
+            }
+            if (AHEAD) {
+                if (i + 1 < hi)
+                    ask_rest(i + 1);
+                else
+                    asked();
+            }
             flush16(unit);
             if (a.post)
                 mul16(unit, r1);
-            if (a.gate) {
+            if (CHANNEL || gates) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    o[e] = unit[e];
+                    v[e] = unit[e];
                 if (a.post && a.gain_post) {
-                    gain16<FULL>(a.gain_post, r, w);
-                    mul16(o, w);
+                    u64 gp[8];
+                    gain16<FULL>(a.gain_post, r, gp);
+                    mul16(v, gp);
                 }
-                if (a.gate_rows) {
-                    mul16(o, g);
-                    store_row16<FULL>(static_cast<T*>(a.dgate) + i * a.dgate_ld, r, o);
-                    load_row16<FULL, true>(static_cast<const T*>(a.gate) + i * a.gate_ld, r, w);
-                    flush16(w);
+                if (gates) {
+                    mul16(v, g);
+                    store_row16<FULL>(static_cast<T*>(a.dgate) + i * a.dgate_ld, r, v);
                 } else {
-                    column_sum(s_gate, g, o, first);
+                    column_sum(s_chan, g, v, first);
                     gain16<FULL>(static_cast<const float*>(a.gate), r, w);
                 }
                 mul16(g, w);
@@ -242,10 +327,42 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
             store_parts<FULL>(a.parts[0], ch, a.pitch, r, s_pre);
         if (a.dgain_post)
             store_parts<FULL>(a.parts[1], ch, a.pitch, r, s_post);
-        if (a.gate && !a.gate_rows)
-            store_parts<FULL>(a.parts[2], ch, a.pitch, r, s_gate);
+        if (CHANNEL)
+            store_parts<FULL>(a.parts[2], ch, a.pitch, r, s_chan);
     }
 }
+
+// chunks of terms, one row a token, to rows of partial sums; a thread has 4 columns of a chunk
+struct Fold {
+    const float* terms[3];
+    float* parts[3];
+    int64_t n, chunks, pitch;
+    int segs;            // CTAs of a chunk
+};
+
+__global__ void __launch_bounds__(128)
+k_norm_fold(const __grid_constant__ Fold f)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int64_t per = f.chunks * f.segs, job = blockIdx.x / per, in = blockIdx.x - job * per, ch = in / f.segs;
+    const int64_t c = 4 * ((in - ch * f.segs) * 128 + threadIdx.x), lo = ch * CHUNK;
+    if (c >= f.pitch)
+        return;
+    const float* t = f.terms[job] + lo * f.pitch + c;
+    float4 v[CHUNK];
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i)   // -0 in place of a missing token leaves a sum as it is
+        v[i] = lo + i < f.n ? load4(t + i * f.pitch) : make_float4(-0.0f, -0.0f, -0.0f, -0.0f);
+#pragma unroll
+    for (int i = 1; i < CHUNK; ++i)
+        v[0] = make_float4(fadd_ftz(v[0].x, v[i].x), fadd_ftz(v[0].y, v[i].y), fadd_ftz(v[0].z, v[i].z), fadd_ftz(v[0].w, v[i].w));
+    store4(f.parts[job] + ch * f.pitch + c, v[0]);
+}
+
+// Few tokens: 2^21 elements, where the terms' way through L2 (16 MB for two sums) takes less than the
+// 16 rows of a chunk one after another on the 3 x 152 groups that run at once.
+inline bool by_tokens(int64_t n, int64_t D) { return n > 1 && n <= (int64_t)1 << 21 && n * D <= (int64_t)1 << 21; }
 
 inline int64_t pitch_of(int64_t D) { return (D + 3) / 4 * 4; }
 
@@ -267,29 +384,49 @@ void set_up(NormArgs& a)
             rows4_or_none(a.gain_post, 0, 4) && rows4_or_none(a.gain_pre, 0, 4);
 }
 
-template <typename T, typename U, bool BWD> cudaError_t launch(const NormArgs& a, cudaStream_t st)
+template <typename T, typename U> cudaError_t launch_fwd(const NormArgs& a, int threads, dim3 grid, cudaStream_t st)
 {
     const bool full = a.vec && a.D == (int64_t)ROW_E * a.tpr;
-    const int threads = a.tpr < 128 ? 128 : a.tpr;
-    const int64_t items = BWD ? (a.n + CHUNK - 1) / CHUNK : a.n, per = threads / a.tpr;
-    const int64_t ctas = (items + per - 1) / per, most = (int64_t)num_sms() * 64;
-    const dim3 grid((unsigned)(ctas < most ? ctas : most));
-    count_launches(1);
-#define GO(N, F) (BWD ? launch_pdl(k_norm_bwd<T, U, N, F>, grid, dim3(threads), 0, st, a) \
-                      : launch_pdl(k_norm_fwd<T, U, N, F>, grid, dim3(threads), 0, st, a))
-    if (threads <= 256)
-        return full ? GO(256, true) : GO(256, false);
-    if (threads == 512)
-        return full ? GO(512, true) : GO(512, false);
-    return full ? GO(1024, true) : GO(1024, false);
+#define GO(N) (full ? launch_pdl(k_norm_fwd<T, U, N, true>, grid, dim3(threads), 0, st, a) \
+                    : launch_pdl(k_norm_fwd<T, U, N, false>, grid, dim3(threads), 0, st, a))
+    return threads <= 256 ? GO(256) : threads == 512 ? GO(512) : GO(1024);
 #undef GO
 }
 
-template <bool BWD> cudaError_t dispatch(const NormArgs& a, cudaStream_t st)
+template <typename T, int N, bool AHEAD, bool FULL> cudaError_t run_bwd(const NormArgs& a, dim3 grid, cudaStream_t st)
 {
-    if (a.type == 0)
-        return a.u_type == 0 ? launch<float, float, BWD>(a, st) : launch<float, __nv_bfloat16, BWD>(a, st);
-    return a.u_type == 0 ? launch<__nv_bfloat16, float, BWD>(a, st) : launch<__nv_bfloat16, __nv_bfloat16, BWD>(a, st);
+    const auto k = a.gate && !a.gate_rows ? k_norm_bwd<T, N, AHEAD, FULL, true> : k_norm_bwd<T, N, AHEAD, FULL, false>;
+    const size_t smem = AHEAD ? (size_t)N * ROW_E * ((a.gate_rows ? 4 : 3) * sizeof(T) + (a.u_type == 0 ? 4 : 2)) : 0;
+    if (smem > 40 * 1024) {   // static shared memory counts too
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return launch_pdl(k, grid, dim3(N), smem, st, a);
+}
+
+template <typename T, int N> cudaError_t pick_bwd(const NormArgs& a, dim3 grid, cudaStream_t st)
+{
+    if (!a.vec || a.D % 4 != 0)
+        return run_bwd<T, N, false, false>(a, grid, st);
+    return a.D == (int64_t)ROW_E * a.tpr ? run_bwd<T, N, true, true>(a, grid, st) : run_bwd<T, N, true, false>(a, grid, st);
+}
+
+template <typename T> cudaError_t launch_bwd(const NormArgs& a, int threads, dim3 grid, cudaStream_t st)
+{
+    return threads == 128   ? pick_bwd<T, 128>(a, grid, st)
+           : threads == 256 ? pick_bwd<T, 256>(a, grid, st)
+           : threads == 512 ? pick_bwd<T, 512>(a, grid, st)
+                            : run_bwd<T, 1024, false, false>(a, grid, st);   // the slots of 1,024 threads would not fit
+}
+
+// threads of a CTA and CTAs of a grid for so many rows or chunks
+dim3 grid_of(const NormArgs& a, int64_t items, int& threads)
+{
+    threads = a.tpr < 128 ? 128 : a.tpr;
+    const int64_t per = threads / a.tpr, ctas = (items + per - 1) / per, most = (int64_t)num_sms() * 64;
+    count_launches(1);
+    return dim3((unsigned)(ctas < most ? ctas : most));
 }
 
 } // namespace
@@ -297,12 +434,17 @@ template <bool BWD> cudaError_t dispatch(const NormArgs& a, cudaStream_t st)
 cudaError_t launch_norm_fwd(NormArgs a, cudaStream_t st)
 {
     set_up(a);
-    return dispatch<false>(a, st);
+    int threads;
+    const dim3 grid = grid_of(a, a.n, threads);
+    if (a.type == 0)
+        return a.u_type == 0 ? launch_fwd<float, float>(a, threads, grid, st) : launch_fwd<float, __nv_bfloat16>(a, threads, grid, st);
+    return a.u_type == 0 ? launch_fwd<__nv_bfloat16, float>(a, threads, grid, st)
+                         : launch_fwd<__nv_bfloat16, __nv_bfloat16>(a, threads, grid, st);
 }
 
 size_t norm_bwd_ws_bytes(int64_t n, int64_t D)
 {
-    return (size_t)((n + CHUNK - 1) / CHUNK) * (size_t)pitch_of(D) * 4 * 3;
+    return (size_t)((n + CHUNK - 1) / CHUNK + (by_tokens(n, D) ? n : 0)) * (size_t)pitch_of(D) * 4 * 3;
 }
 
 cudaError_t launch_norm_bwd(NormArgs a, void* ws, cudaStream_t st)
@@ -310,23 +452,40 @@ cudaError_t launch_norm_bwd(NormArgs a, void* ws, cudaStream_t st)
     set_up(a);
     const int64_t chunks = (a.n + CHUNK - 1) / CHUNK;
     a.pitch = pitch_of(a.D);
+    float* const out[3] = {a.dgain_pre, a.dgain_post, a.gate && !a.gate_rows ? static_cast<float*>(a.dgate) : nullptr};
+    const bool sums = out[0] || out[1] || out[2], single = !sums || by_tokens(a.n, a.D);
+    a.chunk = single ? 1 : CHUNK;
+    float* const parts = static_cast<float*>(ws);
     RowTree t = {};
     t.pitch = a.pitch;
     t.D = a.D;
     t.scale = 1.0f;
     t.accumulate = a.accumulate;
-    float* out[3] = {a.dgain_pre, a.dgain_post, a.gate && !a.gate_rows ? static_cast<float*>(a.dgate) : nullptr};
-    for (int k = 0; k < 3; ++k) {
-        a.parts[k] = static_cast<float*>(ws) + k * chunks * a.pitch;
+    Fold f = {};
+    f.n = a.n;
+    f.chunks = chunks;
+    f.pitch = a.pitch;
+    f.segs = (int)((a.pitch + 511) / 512);
+    for (int k = 0; k < 3; ++k)
         if (out[k]) {
-            t.parts[t.jobs] = a.parts[k];
+            t.parts[t.jobs] = f.parts[t.jobs] = parts + t.jobs * chunks * a.pitch;
             t.count[t.jobs] = chunks;
             t.out[t.jobs] = out[k];
+            a.parts[k] = t.parts[t.jobs];
+            if (single) {
+                a.parts[k] = parts + (3 * chunks + t.jobs * a.n) * a.pitch;
+                f.terms[t.jobs] = a.parts[k];
+            }
             ++t.jobs;
         }
+    int threads;
+    const dim3 grid = grid_of(a, single ? a.n : chunks, threads);
+    cudaError_t e = a.type == 0 ? launch_bwd<float>(a, threads, grid, st) : launch_bwd<__nv_bfloat16>(a, threads, grid, st);
+    if (e == cudaSuccess && sums && single) {
+        e = launch_pdl(k_norm_fold, dim3((unsigned)(t.jobs * chunks * f.segs)), dim3(128), 0, st, f);
+        count_launches(1);
     }
-    cudaError_t e = dispatch<true>(a, st);
-    if (e == cudaSuccess && t.jobs > 0)
+    if (e == cudaSuccess && sums)
         e = launch_row_tree(t, num_sms() * 4, st);
     return e;
 }

@@ -7,7 +7,7 @@
 // chunks takes log16 C rounds over memory (out of L2) instead of log2 C, with 16
 // loads in flight.  LANES lanes of 4 columns make a worker: a warp where many joins
 // of few chunks over wide rows are to be done (the table's gradient), two lanes for
-// one long join over a narrow row (the gains' gradients; with 8 lanes and one pair
+// one long join over a narrow row (the head norm's gains; with 8 lanes and one pair
 // per worker and barrier, 4,096 chunks of 128 took 25 us).
 #include "elem.cuh"
 #include "internal.h"
@@ -88,11 +88,15 @@ k_check_rows(const T* __restrict__ p, int64_t n, int64_t D, int64_t ld, int* err
 
 cudaError_t launch_row_tree(const RowTree& t, int max_ctas, cudaStream_t st)
 {
-    const int cols = t.joins ? 128 : 8;
+    // one long join over a wide row (a block's gains): 16 columns a worker's turn, so that a round of
+    // CTAs covers the row
+    const bool wide = !t.joins && t.D >= 512;
+    const int cols = t.joins ? 128 : wide ? 16 : 8;
     const int colsegs = (int)((t.D + cols - 1) / cols);
     const int grid = t.joins ? max_ctas : (colsegs * t.jobs < max_ctas ? colsegs * t.jobs : max_ctas);
     const cudaError_t e = t.joins ? launch_pdl(k_row_tree<32>, dim3((unsigned)grid), dim3(256), 0, st, t, colsegs)
-                                  : launch_pdl(k_row_tree<2>, dim3((unsigned)grid), dim3(256), 0, st, t, colsegs);
+                        : wide ? launch_pdl(k_row_tree<4>, dim3((unsigned)grid), dim3(256), 0, st, t, colsegs)
+                               : launch_pdl(k_row_tree<2>, dim3((unsigned)grid), dim3(256), 0, st, t, colsegs);
     count_launches(1);
     return e;
 }

@@ -82,6 +82,42 @@ __device__ __forceinline__ void store_row16(T* p, const RowLane& r, const u64 (&
     }
 }
 
+// A thread's share of a row on its way through shared memory: asked for early, taken when it is needed.
+// Each thread copies and reads its own 16 elements only, so no barrier stands between; group k of
+// thread t lies at k threads + t.  Rows on 4-element boundaries, D a multiple of 4.
+template <typename T> struct alignas(4 * sizeof(T)) Four {
+    T v[4];
+};
+
+template <bool FULL, typename T>
+__device__ __forceinline__ void ask_row16(Four<T>* slot, const T* p, const RowLane& r)
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (FULL || r.at(k) < r.D) {
+            const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot + k * blockDim.x + threadIdx.x);
+            if (sizeof(T) == 4)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p + r.at(k)) : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(p + r.at(k)) : "memory");
+        }
+}
+
+template <bool FULL, typename T> __device__ __forceinline__ void take_row16(const Four<T>* slot, const RowLane& r, u64 (&v)[8])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (FULL || r.at(k) < r.D)
+            x = load4(slot[k * blockDim.x + threadIdx.x].v);
+        v[2 * k] = pack2(x.x, x.y);
+        v[2 * k + 1] = pack2(x.z, x.w);
+    }
+}
+
+__device__ __forceinline__ void asked() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void wait_asked() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
 __device__ __forceinline__ void flush16(u64 (&v)[8])
 {
     const u64 z = pack2(-0.0f, -0.0f);

@@ -157,6 +157,21 @@ NORM = [(1, 1), (2, 3), (5, 4), (3, 37), (17, 128), (33, 512), (4, 513), (2, 100
 @pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("kind,u_kind", [(F32, F32), (BF, F32), (F32, BF), (BF, BF)])
 def test_block_norm(orc, n, D, gate, post, gains, layout, kind, u_kind):
+    norm_check(orc, n, D, gate, post, gains, layout, kind, u_kind)
+
+
+# more than 2^21 elements: the backward takes chunks of tokens, not single ones
+LONG = [(1030, 2048), (2100, 1001), (70000, 32), (4200, 512), (2000, 1060), (517, 4096), (300, 8192), (129, 16384)]
+
+
+@pytest.mark.parametrize("n,D", LONG)
+@pytest.mark.parametrize("gate,post", [(None, True), ("channel", False), ("channel", True), ("token", True)])
+@pytest.mark.parametrize("kind,u_kind", [(F32, F32), (BF, F32), (F32, BF)])
+def test_block_norm_chunks(orc, n, D, gate, post, kind, u_kind):
+    norm_check(orc, n, D, gate, post, True, "strided", kind, u_kind)
+
+
+def norm_check(orc, n, D, gate, post, gains, layout, kind, u_kind):
     c = norm_case(n, D, gate, post, gains)
     narrow = ("x", "y", "dh") + (("gate",) if gate == "token" else ())
     if kind == BF:
