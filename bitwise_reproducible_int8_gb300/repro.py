@@ -668,12 +668,15 @@ def _like(t, shape, name):
         return None, shape[-1]
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _dev_ptr(t, name, False), _rows2d(t, name)[2]
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.data_ptr(), (shape[-1] if t.is_contiguous() else _rows2d(t, name)[2])
 
 
 def _one_type(kind, name, *ts):
-    if any(t is not None and t.dtype != kind for t in ts):
-        raise ValueError(f"{name} must be of one type")
+    for t in ts:
+        if t is not None and t.dtype is not kind:
+            raise ValueError(f"{name} must be of one type")
 
 
 def _gate(gate, shape, dtype, name):
@@ -681,17 +684,27 @@ def _gate(gate, shape, dtype, name):
     if gate is None:
         return None, shape[-1], 0
     if gate.dim() == 1 and len(shape) > 1:
-        if gate.numel() != shape[-1]:
-            raise ValueError(f"{name} must be [D] or have the stream's shape")
-        return _ptr(gate, torch.float32, name), shape[-1], 0
+        return _floats(gate, shape[-1], f"{name} [D], if it has not the stream's shape,"), shape[-1], 0
     _one_type(dtype, f"{name} and the stream", gate)
     return *_like(gate, shape, name), REPRO_NORM_GATE_ROWS
 
 
-def _gain(t, D, name):
-    if t is not None and t.numel() != D:
-        raise ValueError(f"{name} must have D elements")
-    return _ptr(t, torch.float32, name)
+def _floats(t, count, name):
+    """Pointer of `count` dense float32 (None: NULL)."""
+    if t is None:
+        return None
+    if t.numel() != count or t.dtype is not torch.float32:
+        raise ValueError(f"{name} must have {count} float32 elements")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def _space(ws):
+    """(pointer, bytes) of a workspace (None: none)."""
+    if ws is None:
+        return None, 0
+    return _dev_ptr(ws, "ws"), ws.numel() * ws.element_size()
 
 
 def repro_block_norm_fwd(x: torch.Tensor, y, h, u, stats=None, gate=None, g_post=None, g_pre=None,
@@ -703,18 +716,19 @@ def repro_block_norm_fwd(x: torch.Tensor, y, h, u, stats=None, gate=None, g_post
     shape and type.  y and h None: the norm of x alone.  stats [n, 2] float32 (or None) is the
     backward's input.  Rows at any stride; gains None: none."""
     n, D, x_ld = _rows2d(x, "x")
-    kind = _float_type(x, "x")
+    kind, shape = _float_type(x, "x"), x.shape
     _one_type(x.dtype, "x, y and h", y, h)
-    yp, y_ld = _like(y, x.shape, "y")
-    hp, h_ld = _like(h, x.shape, "h")
-    up, u_ld = _like(u, x.shape, "u")
-    gp, gate_ld, rows = _gate(gate, x.shape, x.dtype, "gate")
-    if stats is not None and stats.numel() != 2 * n:
-        raise ValueError("stats must be [n, 2]")
+    yp, y_ld = _like(y, shape, "y")
+    hp, h_ld = _like(h, shape, "h")
+    up, u_ld = _like(u, shape, "u")
+    gp, gate_ld, flags = _gate(gate, shape, x.dtype, "gate")
+    if post:
+        flags |= REPRO_NORM_POST
+    u_kind = REPRO_F32 if u is None else _float_type(u, "u")
+    post_p, pre_p, stats_p = _floats(g_post, D, "g_post"), _floats(g_pre, D, "g_pre"), _floats(stats, 2 * n, "stats [n, 2]")
     _check("repro_block_norm_fwd", lib().repro_block_norm_fwd(
-        _dev_ptr(x, "x", False), x_ld, yp, y_ld, kind, gp, gate_ld, _gain(g_post, D, "g_post"),
-        _gain(g_pre, D, "g_pre"), alpha, beta, eps, n, D, (REPRO_NORM_POST if post else 0) | rows, hp, h_ld, up,
-        REPRO_F32 if u is None else _float_type(u, "u"), u_ld, _ptr(stats, torch.float32, "stats"), _stream(stream)))
+        _dev_ptr(x, "x", False), x_ld, yp, y_ld, kind, gp, gate_ld, post_p, pre_p, alpha, beta, eps, n, D, flags, hp, h_ld,
+        up, u_kind, u_ld, stats_p, _stream(stream)))
 
 
 def repro_block_norm_bwd_ws_bytes(n: int, D: int) -> int:
@@ -728,28 +742,26 @@ def repro_block_norm_bwd(dh, du, h, y, stats: torch.Tensor, dx: torch.Tensor, dy
     or None; h, the stream as the forward wrote it, goes with it), y and the forward's stats.
     dx may be dh.  accumulate: the sums over tokens (gains, a gate [D]) are added to."""
     n, D, dx_ld = _rows2d(dx, "dx")
-    kind = _float_type(dx, "dx")
+    kind, shape = _float_type(dx, "dx"), dx.shape
     _one_type(dx.dtype, "dh, h, y, dx and dy", dh, h, y, dy)
-    dhp, dh_ld = _like(dh, dx.shape, "dh")
-    dup, du_ld = _like(du, dx.shape, "du")
-    hp, h_ld = _like(h, dx.shape, "h")
-    yp, y_ld = _like(y, dx.shape, "y")
-    dyp, dy_ld = _like(dy, dx.shape, "dy")
-    gp, gate_ld, rows = _gate(gate, dx.shape, dx.dtype, "gate")
-    dgp, dgate_ld, drows = _gate(dgate, dx.shape, dx.dtype, "dgate")
+    dhp, dh_ld = _like(dh, shape, "dh")
+    dup, du_ld = _like(du, shape, "du")
+    hp, h_ld = _like(h, shape, "h")
+    yp, y_ld = _like(y, shape, "y")
+    dyp, dy_ld = _like(dy, shape, "dy")
+    gp, gate_ld, rows = _gate(gate, shape, dx.dtype, "gate")
+    dgp, dgate_ld, drows = _gate(dgate, shape, dx.dtype, "dgate")
     if gate is not None and dgate is not None and rows != drows:
         raise ValueError("dgate must have the gate's shape")
-    if stats.numel() != 2 * n:
-        raise ValueError("stats must be [n, 2]")
+    u_kind = REPRO_F32 if du is None else _float_type(du, "du")
+    post_p, pre_p, stats_p = _floats(g_post, D, "g_post"), _floats(g_pre, D, "g_pre"), _floats(stats, 2 * n, "stats [n, 2]")
+    dpost_p, dpre_p = _floats(dg_post, D, "dg_post"), _floats(dg_pre, D, "dg_pre")
     if ws is None and (dg_post is not None or dg_pre is not None or (dgate is not None and not drows)):
         ws = _workspace(repro_block_norm_bwd_ws_bytes(n, D), dx.device, stream)
     flags = (REPRO_NORM_POST if post else 0) | rows | (REPRO_BWD_DW_ACCUMULATE if accumulate else 0)
     _check("repro_block_norm_bwd", lib().repro_block_norm_bwd(
-        dhp, dh_ld, dup, REPRO_F32 if du is None else _float_type(du, "du"), du_ld, hp, h_ld, yp, y_ld, kind, gp, gate_ld,
-        _gain(g_post, D, "g_post"), _gain(g_pre, D, "g_pre"), _ptr(stats, torch.float32, "stats"), alpha, beta, n, D,
-        flags, _dev_ptr(dx, "dx", False), dx_ld, dyp, dy_ld, dgp, dgate_ld, _gain(dg_post, D, "dg_post"),
-        _gain(dg_pre, D, "dg_pre"), _dev_ptr(ws, "ws"), ws.numel() * ws.element_size() if ws is not None else 0,
-        _stream(stream)))
+        dhp, dh_ld, dup, u_kind, du_ld, hp, h_ld, yp, y_ld, kind, gp, gate_ld, post_p, pre_p, stats_p, alpha, beta, n, D,
+        flags, _dev_ptr(dx, "dx", False), dx_ld, dyp, dy_ld, dgp, dgate_ld, dpost_p, dpre_p, *_space(ws), _stream(stream)))
 
 
 def repro_quant_rows_i8_ws_bytes(n: int, D: int, columns: bool = False) -> int:
@@ -762,16 +774,15 @@ def repro_quant_rows_i8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, 
     for each column (scales [D]); with mul, of x (x) mul, mul [D] (columns: [n])."""
     n, D, x_ld = _rows2d(x, "x")
     qp, q_ld = _like(q, x.shape, "q")
-    if q.dtype != torch.int8:
+    if q.dtype is not torch.int8:
         raise ValueError(f"q must be {torch.int8}, got {q.dtype}")
-    if scales.numel() != (D if columns else n) or (mul is not None and mul.numel() != (n if columns else D)):
-        raise ValueError("scales must have an entry per row (column), mul one per column (row)")
+    rows, cols = (D, n) if columns else (n, D)
+    kind, sp, mp = _float_type(x, "x"), _floats(scales, rows, "scales"), _floats(mul, cols, "mul")
     if ws is None and columns:
         ws = _workspace(repro_quant_rows_i8_ws_bytes(n, D, True), x.device, stream)
     _check("repro_quant_rows_i8", lib().repro_quant_rows_i8(
-        _dev_ptr(x, "x", False), _float_type(x, "x"), x_ld, _ptr(mul, torch.float32, "mul"), n, D,
-        REPRO_QUANT_COLUMNS if columns else 0, qp, q_ld, _ptr(scales, torch.float32, "scales"), _dev_ptr(ws, "ws"),
-        ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
+        _dev_ptr(x, "x", False), kind, x_ld, mp, n, D, REPRO_QUANT_COLUMNS if columns else 0, qp, q_ld, sp, *_space(ws),
+        _stream(stream)))
 
 
 def _codes2d(t, name):
@@ -801,28 +812,24 @@ def repro_matmul_i8(a: torch.Tensor, b: torch.Tensor, y: torch.Tensor, s_a=None,
     N, K2 = (bc, br) if trans_b else (br, bc)
     if K != K2 or (My, Ny) != (M, N):
         raise ValueError("shape mismatch: a [M, K] or [K, M], b [N, K] or [K, N], y [M, N]")
-    if a.dtype != torch.int8 or b.dtype != torch.int8:
+    if a.dtype is not torch.int8 or b.dtype is not torch.int8:
         raise ValueError("a and b must be int8 codes")
-    kind = _float_type(y, "y")
-    if (s_a is not None and s_a.numel() != M) or (s_b is not None and s_b.numel() != N):
-        raise ValueError("s_a must be [M], s_b [N]")
+    kind, sap, sbp = _float_type(y, "y"), _floats(s_a, M, "s_a"), _floats(s_b, N, "s_b")
     if ws is None:
         need = repro_matmul_i8_ws_bytes(M, N, K, trans_a, trans_b)
         ws = _workspace(need, y.device, stream) if need > 0 else None
-    f32 = torch.float32
     _check("repro_matmul_i8", lib().repro_matmul_i8(
-        _dev_ptr(a, "a", False), a_ld, _dev_ptr(b, "b", False), b_ld, _ptr(s_a, f32, "s_a"), _ptr(s_b, f32, "s_b"), M, N, K,
-        _mm_flags(trans_a, trans_b, accumulate), _dev_ptr(y, "y", False), kind, y_ld, _dev_ptr(ws, "ws"),
-        ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
+        _dev_ptr(a, "a", False), a_ld, _dev_ptr(b, "b", False), b_ld, sap, sbp, M, N, K,
+        _mm_flags(trans_a, trans_b, accumulate), _dev_ptr(y, "y", False), kind, y_ld, *_space(ws), _stream(stream)))
 
 
 def _kept(codes, scales, n, F):
     if codes is None and scales is None:
         return None, None
     G = -(-F // REPRO_SWIGLU_GROUP)
-    if codes is None or scales is None or codes.numel() != 2 * n * G * REPRO_SWIGLU_GROUP or scales.numel() != 2 * n * G:
+    if codes is None or scales is None or codes.numel() != 2 * n * G * REPRO_SWIGLU_GROUP:
         raise ValueError("codes must be [n, 2, G, 128] and scales [n, 2, G], G = ceil(F / 128)")
-    return _ptr(codes, torch.int8, "codes"), _ptr(scales, torch.float32, "scales")
+    return _ptr(codes, torch.int8, "codes"), _floats(scales, 2 * n * G, "scales")
 
 
 def repro_swiglu_fwd(gu: torch.Tensor, a: torch.Tensor, codes=None, scales=None, stream=None) -> None:

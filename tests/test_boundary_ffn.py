@@ -159,10 +159,11 @@ def test_binding_checks(monkeypatch):
                 raise AssertionError("not refused")
             return call
 
+    class Device(torch.Tensor):              # host memory that passes for a device's
+        is_cuda = property(lambda self: True)
+
     monkeypatch.setattr(repro, "lib", Reached)
-    monkeypatch.setattr(repro, "_dev_ptr", lambda t, name, contiguous=True: None if t is None else 1)
-    monkeypatch.setattr(repro, "_ptr", lambda t, dtype=None, name="": None if t is None else 1)
-    t = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt)  # noqa: E731
+    t = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt).as_subclass(Device)  # noqa: E731
     i8, bf = torch.int8, torch.bfloat16
     x = t(3, 8)
     bad = [
@@ -192,5 +193,6 @@ def test_binding_checks(monkeypatch):
         lambda: repro.repro_swiglu_bwd(t(3, 4), t(4, 8)),
     ]
     for f in bad:
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError) as e:
             f()
+        assert "CUDA" not in str(e.value), e.value
