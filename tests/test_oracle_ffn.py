@@ -230,3 +230,35 @@ def test_swiglu_gradient_against_differences(orc):
         lo = total(x)
         x[i] = old
         assert abs((hi - lo) / (2 * t) - got[i]) < 2e-6 * (1 + abs(got[i]))
+
+
+@pytest.mark.parametrize("T,N,K", [(40, 12, 9), (7, 33, 20)])
+def test_gradient_products(orc, T, N, K):
+    """The gradients of Y = X W^T as products of codes, against those of the dequantised product: a code
+    is at most half a step from its value (and two roundings of the value, its scale and its product),
+    so dX is off by half a step times the sum of the codes that it meets, and dW alike."""
+    g = rng(T)
+    X, W, dY = (g.standard_normal(s).astype(f32) for s in ((T, K), (N, K), (T, N)))
+    xq, sx = orc.quant_rows(X)
+    wq, sw = orc.quant_rows(W)
+    Xd, Wd = xq * sx[:, None].astype(np.float64), wq * sw[:, None].astype(np.float64)
+    q, qs = orc.quant_rows(dY, sw)
+    dX = orc.matmul_i8(q, wq, qs, None, False, True)
+    bound = 0.5 * qs[:, None] * np.abs(wq).sum(0)[None].astype(np.float64)
+    assert np.all(np.abs(dX - dY @ Wd) <= bound * (1 + 1e-4) + 1e-5 * np.abs(dY) @ np.abs(Wd))
+    q, qs = orc.quant_rows(dY, sx, True)
+    dW = orc.matmul_i8(q, xq, qs, None, True, True)
+    bound = 0.5 * qs[:, None] * np.abs(xq).sum(0)[None].astype(np.float64)
+    assert np.all(np.abs(dW - dY.T @ Xd) <= bound * (1 + 1e-4) + 1e-5 * np.abs(dY.T) @ np.abs(Xd))
+    # and against differences of the dequantised product, weighted by dY (linear: exact but for 2^-52 / t)
+    t = 1e-3
+    for i in ((0, 0), (T - 1, K - 1)):
+        hi, lo = Xd.copy(), Xd.copy()
+        hi[i] += t
+        lo[i] -= t
+        d = ((hi @ Wd.T * dY).sum() - (lo @ Wd.T * dY).sum()) / (2 * t)
+        assert abs(d - dX[i]) <= 0.5 * qs_of(orc, dY, sw)[i[0]] * np.abs(wq[:, i[1]]).sum() * (1 + 1e-4) + 1e-6
+
+
+def qs_of(orc, dY, mul):
+    return orc.quant_rows(dY, mul)[1]
