@@ -4,7 +4,8 @@
 // the fp32 accumulator holding every partial sum over a 512-term K-slice
 // exactly (each is an integer below 2^23).  The hardware documentation does
 // not promise how the tensor core adds inside a slice, so this check runs the
-// tensor-core path (both tile widths, 128 x 256 and 128 x 128) and the
+// tensor-core paths (both tile widths of the forward, 128 x 256 and 128 x 128, and the product
+// of codes on pairs of SMs) and the
 // CUDA-core dp4a path (exact by construction) on
 // adversarial codes -- every code at the clamp, alternating signs, a sign flip
 // at the slice boundary, one small term among large ones, a slice whose
@@ -13,6 +14,8 @@
 // of its range), hashed codes -- and compares the outputs bit for bit.  With
 // unit scales and K = 1024 every output is an integer below 2^24, exact in
 // fp32, so a wrong integer shows.
+#include <algorithm>
+
 #include "internal.h"
 
 namespace repro {
@@ -83,7 +86,8 @@ inline size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 size_t selftest_ws_bytes()
 {
     return align256(ST_M * ST_K) + align256(ST_N * ST_K) + align256(16) +
-           2 * align256((size_t)ST_M * ST_N * 4) + align256(fwd_tc_ws_bytes(ST_M, ST_N, ST_K));
+           2 * align256((size_t)ST_M * ST_N * 4) +
+           align256(std::max(fwd_tc_ws_bytes(ST_M, ST_N, ST_K), matmul_i8_ws_bytes(ST_M, ST_N, ST_K, false, false)));
 }
 
 // 0: identical, 1: a mismatch, negative: a CUDA error
@@ -118,6 +122,12 @@ int run_selftest(void* ws, cudaStream_t st)
         k_selftest_compare<<<(ST_M * ST_N + 255) / 256, 256, 0, st>>>(y_tc, y_cc, ST_M * ST_N, flag);
         count_launches(1);
     }
+    // and the product of codes with a tile on two SMs (k_matmul_i8.cu)
+    if (launch_matmul_i8({xq, wq, ST_K, ST_K, false, false, nullptr, nullptr, ST_M, ST_N, ST_K, y_tc, 0, ST_N, false}, tc_ws,
+                         true, st) != cudaSuccess)
+        return -1;
+    k_selftest_compare<<<(ST_M * ST_N + 255) / 256, 256, 0, st>>>(y_tc, y_cc, ST_M * ST_N, flag);
+    count_launches(1);
     int h = 0;
     if (cudaMemcpyAsync(&h, flag, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)
