@@ -297,9 +297,12 @@ struct MatmulI8Args {
     int64_t y_ld;
     bool accumulate;
 };
-bool matmul_i8_small(int64_t M, bool a_t, bool b_t);   // few tokens: without a workspace, on the CUDA cores
 size_t matmul_i8_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_t, bool b_t);
 cudaError_t launch_matmul_i8(const MatmulI8Args& a, void* ws, bool tc, cudaStream_t st);
+cudaError_t launch_matmul_pair(const MatmulI8Args& a, void* ws, cudaStream_t st);   // on pairs of SMs
+// ---- the same for few tokens (k_matmul_few.cu)
+size_t matmul_few_ws_bytes(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_matmul_few(const MatmulI8Args& a, void* ws, cudaStream_t st);
 
 // ---- gated activation (k_swiglu.cu)
 struct SwigluArgs {

@@ -29,6 +29,7 @@
 #include "elem.cuh"
 #include "internal.h"
 #include "launch.cuh"
+#include "mm.cuh"
 #include "pipeline.cuh"
 #include "umma.cuh"
 
@@ -41,21 +42,6 @@ typedef unsigned long long u64;
 
 inline int64_t pad8(int64_t k) { return (k + 7) / 8 * 8; }
 inline int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
-
-// four codes to two words of bf16 pairs: 128 + low seven bits less 128 or 256, all exact
-__device__ __forceinline__ uint2 widen4(uint32_t c)
-{
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t b = __byte_perm(c, 0, i == 0 ? 0x4140 : 0x4342);      // code, 0, code, 0
-        const uint32_t hi = (b & 0x007f007fu) | 0x43004300u, lo = (b & 0x00800080u) | 0x43004300u;
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&hi),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&lo));
-        w[i] = *reinterpret_cast<const uint32_t*>(&d);
-    }
-    return make_uint2(w[0], w[1]);
-}
 
 struct Widen {
     const int8_t* q;
@@ -179,23 +165,6 @@ cudaError_t widen(const int8_t* q, int64_t ld, int64_t rows, int64_t K, bool t, 
     }
     const int64_t want = (rows * (w.Kp / 8) + 255) / 256, most = (int64_t)num_sms() * 8;
     return launch_pdl(k_mm_widen, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, w);
-}
-
-// ---------------------------------------------------------------- what every path ends with
-
-template <typename Y> __device__ __forceinline__ void put(Y* p, float v, bool accumulate)
-{
-    if (accumulate)
-        v = fadd_ftz(to_f32<Y>(*p), v);
-    *p = from_f32<Y>(v);
-}
-
-__device__ __forceinline__ float scaled(int acc, bool has_a, float sa, bool has_b, float sb)
-{
-    float v = __int2float_rn(acc);
-    if (has_a)
-        v = fmul_flush(v, sa);
-    return has_b ? fmul_flush(v, sb) : v;
 }
 
 // ---------------------------------------------------------------- any shape on the CUDA cores
@@ -945,40 +914,65 @@ cudaError_t run_pair(const MatmulI8Args& g, const __nv_bfloat16* xa, const __nv_
     return e;
 }
 
-template <typename Y> cudaError_t launch(const MatmulI8Args& g, void* ws, bool tc, cudaStream_t st)
+template <typename Y> cudaError_t run_any(const MatmulI8Args& g, cudaStream_t st)
 {
-    if (matmul_i8_small(g.M, g.a_t, g.b_t))
-        return run_rows<Y>(g, st);
-    if (!tc || g.K == 0) {
-        const int64_t tiles_n = (g.N + FT - 1) / FT, tiles = tiles_n * ((g.M + FT - 1) / FT);
-        count_launches(1);
-        return launch_pdl(k_mm_any<Y>, dim3((unsigned)tiles), dim3(256), 0, st, g, tiles_n);
-    }
-    __nv_bfloat16* xa = static_cast<__nv_bfloat16*>(ws);
-    __nv_bfloat16* xb = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(ws) + align256(2 * g.M * pad8(g.K)));
-    cudaError_t e = widen(g.a, g.a_ld, g.M, g.K, g.a_t, xa, st);
-    if (e == cudaSuccess)
-        e = widen(g.b, g.b_ld, g.N, g.K, g.b_t, xb, st);
-    int* parts = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(xb) + align256(2 * g.N * pad8(g.K)));
-    return e == cudaSuccess ? run_pair<Y>(g, xa, xb, parts, st) : e;
+    const int64_t tiles_n = (g.N + FT - 1) / FT, tiles = tiles_n * ((g.M + FT - 1) / FT);
+    count_launches(1);
+    return launch_pdl(k_mm_any<Y>, dim3((unsigned)tiles), dim3(256), 0, st, g, tiles_n);
 }
 
-} // namespace
-
-bool matmul_i8_small(int64_t M, bool a_t, bool b_t) { return M <= 16 && !a_t && !b_t; }
-
-size_t matmul_i8_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_t, bool b_t)
+bool aligned16(const MatmulI8Args& g)
 {
-    if (matmul_i8_small(M, a_t, b_t))
-        return 0;
+    return reinterpret_cast<uintptr_t>(g.a) % 16 == 0 && reinterpret_cast<uintptr_t>(g.b) % 16 == 0 &&
+           (g.M == 1 || g.a_ld % 16 == 0) && (g.N == 1 || g.b_ld % 16 == 0);
+}
+
+// Which kernel, for a = [M][K], b = [N][K] (times for N 11264, K 2048 out of HBM): up to 4 tokens the
+// weights' bytes against each of them on the CUDA cores (4 tokens 12 us, 16 tokens 20); up to 128 the
+// weights widened on their way (k_matmul_few.cu: 5 tokens 12 us, 16 tokens 13, 64 tokens 20, 128 tokens
+// 30, or 18 for N 2048 and K 5632); else a widened copy and pairs of SMs (27 us up to 256 tokens, 23 for
+// N 2048, K 5632).  The CUDA cores also take up to 16 tokens where the tensor cores may not be used or
+// rows are not aligned.
+bool small_of(int64_t M, bool a_t, bool b_t) { return M <= 16 && !a_t && !b_t; }
+bool few_of(int64_t M, int64_t K, bool a_t, bool b_t) { return M > 4 && M <= 128 && !a_t && !b_t && K % 16 == 0 && K > 0; }
+
+size_t pair_ws_bytes(int64_t M, int64_t N, int64_t K)
+{
     const Plan p = plan_of(M, N, K);
     const int64_t parts = p.split > 1 ? p.items - p.whole : 0;
     return (size_t)(align256(2 * M * pad8(K)) + align256(2 * N * pad8(K)) + parts * PART_BYTES);
 }
 
+} // namespace
+
+size_t matmul_i8_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_t, bool b_t)
+{
+    const size_t few = few_of(M, K, a_t, b_t) ? std::max<size_t>(matmul_few_ws_bytes(M, N, K), 16) : 0;
+    return small_of(M, a_t, b_t) ? few : std::max(few, pair_ws_bytes(M, N, K));
+}
+
+cudaError_t launch_matmul_pair(const MatmulI8Args& g, void* ws, cudaStream_t st)
+{
+    __nv_bfloat16* xa = static_cast<__nv_bfloat16*>(ws);
+    __nv_bfloat16* xb = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(ws) + align256(2 * g.M * pad8(g.K)));
+    int* parts = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(xb) + align256(2 * g.N * pad8(g.K)));
+    cudaError_t e = widen(g.a, g.a_ld, g.M, g.K, g.a_t, xa, st);
+    if (e == cudaSuccess)
+        e = widen(g.b, g.b_ld, g.N, g.K, g.b_t, xb, st);
+    if (e != cudaSuccess)
+        return e;
+    return g.y_type == 0 ? run_pair<float>(g, xa, xb, parts, st) : run_pair<__nv_bfloat16>(g, xa, xb, parts, st);
+}
+
 cudaError_t launch_matmul_i8(const MatmulI8Args& g, void* ws, bool tc, cudaStream_t st)
 {
-    return g.y_type == 0 ? launch<float>(g, ws, tc, st) : launch<__nv_bfloat16>(g, ws, tc, st);
+    if (tc && few_of(g.M, g.K, g.a_t, g.b_t) && aligned16(g))
+        return launch_matmul_few(g, ws, st);
+    if (small_of(g.M, g.a_t, g.b_t) && g.K > 0)
+        return g.y_type == 0 ? run_rows<float>(g, st) : run_rows<__nv_bfloat16>(g, st);
+    if (!tc || g.K == 0)
+        return g.y_type == 0 ? run_any<float>(g, st) : run_any<__nv_bfloat16>(g, st);
+    return launch_matmul_pair(g, ws, st);
 }
 
 } // namespace repro

@@ -4,8 +4,8 @@
 // the fp32 accumulator holding every partial sum over a 512-term K-slice
 // exactly (each is an integer below 2^23).  The hardware documentation does
 // not promise how the tensor core adds inside a slice, so this check runs the
-// tensor-core paths (both tile widths of the forward, 128 x 256 and 128 x 128, and the product
-// of codes on pairs of SMs) and the
+// tensor-core paths (both tile widths of the forward, 128 x 256 and 128 x 128, and the products
+// of codes on pairs of SMs and for few tokens) and the
 // CUDA-core dp4a path (exact by construction) on
 // adversarial codes -- every code at the clamp, alternating signs, a sign flip
 // at the slice boundary, one small term among large ones, a slice whose
@@ -122,12 +122,14 @@ int run_selftest(void* ws, cudaStream_t st)
         k_selftest_compare<<<(ST_M * ST_N + 255) / 256, 256, 0, st>>>(y_tc, y_cc, ST_M * ST_N, flag);
         count_launches(1);
     }
-    // and the product of codes with a tile on two SMs (k_matmul_i8.cu)
-    if (launch_matmul_i8({xq, wq, ST_K, ST_K, false, false, nullptr, nullptr, ST_M, ST_N, ST_K, y_tc, 0, ST_N, false}, tc_ws,
-                         true, st) != cudaSuccess)
-        return -1;
-    k_selftest_compare<<<(ST_M * ST_N + 255) / 256, 256, 0, st>>>(y_tc, y_cc, ST_M * ST_N, flag);
-    count_launches(1);
+    // and the products of codes on pairs of SMs and for few tokens (k_matmul_i8.cu, k_matmul_few.cu)
+    const MatmulI8Args mm = {xq, wq, ST_K, ST_K, false, false, nullptr, nullptr, ST_M, ST_N, ST_K, y_tc, 0, ST_N, false};
+    for (int few = 0; few < 2; ++few) {
+        if ((few ? launch_matmul_few(mm, tc_ws, st) : launch_matmul_pair(mm, tc_ws, st)) != cudaSuccess)
+            return -1;
+        k_selftest_compare<<<(ST_M * ST_N + 255) / 256, 256, 0, st>>>(y_tc, y_cc, ST_M * ST_N, flag);
+        count_launches(1);
+    }
     int h = 0;
     if (cudaMemcpyAsync(&h, flag, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)

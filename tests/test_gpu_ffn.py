@@ -269,7 +269,8 @@ def test_block_norm_no_rows():
 # ---------------------------------------------------------------- product of codes
 
 MM = [(1, 1, 1), (1, 5, 16), (1, 130, 5632), (3, 7, 100), (8, 64, 512), (9, 33, 513), (16, 100, 1000), (17, 5, 8), (64, 64, 64),
-      (65, 300, 77), (128, 256, 512), (129, 257, 520), (200, 70, 2049), (256, 256, 1024), (300, 520, 640), (700, 260, 96)]
+      (65, 300, 77), (128, 256, 512), (129, 257, 520), (200, 70, 2049), (256, 256, 1024), (300, 520, 640), (700, 260, 96), (5, 130, 528), (33, 300, 1040),
+      (100, 129, 2064), (64, 128, 16), (128, 1000, 5632)]
 
 
 def codes(g, *shape):
@@ -326,7 +327,7 @@ def test_matmul_no_terms():
 def test_matmul_accumulates_subnormals(orc):
     """Old values and sums below the smallest normal are flushed, however the addition is done."""
     tiny = f32(2.0) ** -126
-    for M in (4, 64):
+    for M in (4, 64, 200):
         a, b = np.ones((M, 8), np.int8), np.ones((64, 8), np.int8)
         sa = np.full(M, tiny / 8 * f32(1.5), f32)
         sa[1], sa[2] = -tiny, tiny
@@ -341,7 +342,11 @@ def test_matmul_accumulates_subnormals(orc):
 @pytest.mark.parametrize("K", [512, 1024, 4096, 133144])
 def test_matmul_at_the_clamp(K):
     """Sums at the ends of the range, in every column of two tiles, against exact integers."""
-    M, N = 257, 520
+    for M, N in ((257, 520), (100, 260)):
+        clamp_check(M, N, K)
+
+
+def clamp_check(M, N, K):
     g = rng(K)
     a, b = codes(g, M, K), codes(g, N, K)
     a[::5], a[1::5] = 127, -127
