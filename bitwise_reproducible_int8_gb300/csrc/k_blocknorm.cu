@@ -8,12 +8,13 @@
 // Bound by HBM: x and y in, h and u out (16 bytes an element in fp32); backward du, dh, h, y in,
 // dx, dy out (24).  A row stays in the registers of its threads between its sums (rows.cuh).
 //
-// The gradients that are sums over tokens: a group of the backward takes 16 consecutive tokens one
+// The gradients that are sums over tokens: a group of the backward takes 8 consecutive tokens one
 // after another and keeps its columns' sums in registers, so a chunk's order costs nothing, and
-// writes one row of partial sums (1/16 of a stream of the pass, out of L2); k_rowtree.cu joins them.
-// A few tokens would leave most of the card idle that way, and 16 rows one after another are all
+// writes one row of partial sums (1/8 of a stream of the pass, most of it in L2; with chunks of 16, 2.25
+// rounds over the card, 142 us against 135); k_rowtree.cu joins them.
+// A few tokens would leave most of the card idle that way, and 8 rows one after another are all
 // latency: then a group takes one token and writes its terms, and k_norm_fold adds the chunks up
-// (1023 x 1001 bf16: 79 us in chunks).
+// (1023 x 1001 bf16 with a gate per channel: 22 us, 79 in chunks of 16).
 #include "internal.h"
 #include "launch.cuh"
 #include "rows.cuh"
@@ -21,7 +22,7 @@
 namespace repro {
 namespace {
 
-constexpr int CHUNK = 16;        // tokens of a chunk of the sums over tokens: REPRO_NORM_CHUNK
+constexpr int CHUNK = 8;        // tokens of a chunk of the sums over tokens: REPRO_NORM_CHUNK
 
 __device__ __forceinline__ float rms_of(float S, const NormArgs& a)
 {
@@ -200,12 +201,14 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
             ask_norm(lo);
             ask_rest(lo);
         }
-        float2 next = *reinterpret_cast<const float2*>(a.stats + 2 * lo);
+        float next1 = __ldg(a.stats + 2 * lo), next2 = __ldg(a.stats + 2 * lo + 1);
         for (int64_t i = lo; i < hi; ++i) {
             const bool first = i == lo;
-            const float r1 = flush(next.x), r2 = flush(next.y);
-            if (i + 1 < hi)
-                next = *reinterpret_cast<const float2*>(a.stats + 2 * (i + 1));
+            const float r1 = flush(next1), r2 = flush(next2);
+            if (i + 1 < hi) {
+                next1 = __ldg(a.stats + 2 * (i + 1));
+                next2 = __ldg(a.stats + 2 * (i + 1) + 1);
+            }
             u64 g[8], v[8], unit[8], w[8];
             if (AHEAD)
                 wait_asked<1>();
@@ -361,7 +364,7 @@ k_norm_fold(const __grid_constant__ Fold f)
 }
 
 // Few tokens: 2^21 elements, where the terms' way through L2 (16 MB for two sums) takes less than the
-// 16 rows of a chunk one after another on the 3 x 152 groups that run at once.
+// rows of a chunk one after another on the 3 x 152 groups that run at once.
 inline bool by_tokens(int64_t n, int64_t D) { return n > 1 && n <= (int64_t)1 << 21 && n * D <= (int64_t)1 << 21; }
 
 inline int64_t pitch_of(int64_t D) { return (D + 3) / 4 * 4; }

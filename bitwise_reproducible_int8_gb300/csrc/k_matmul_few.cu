@@ -3,7 +3,7 @@
 //
 // A CTA takes 128 weights' rows (output channels) and one exact slice of K (512 terms).  The weights
 // are the M side of tcgen05.mma (128 rows), the tokens the N side (32, 64 or 128), so that few tokens
-// cost few MMAs; both go from memory through registers, widened to bf16 there, into swizzled shared
+// cost few MMAs; both go from memory through registers, widened there, into swizzled shared
 // memory.  A block of 64 terms of a row is 4 threads' 16 bytes; each thread has four blocks on their
 // way at a time, so a CTA keeps 32 KB of weights in flight, and three CTAs (of up to 64 tokens) an SM.
 //

@@ -44,7 +44,7 @@ REPRO_DISTILL_STAT_LSE = 2
 REPRO_DISTILL_LOGPROBS = 1
 REPRO_NORM_POST, REPRO_NORM_GATE_ROWS = 4, 8
 REPRO_NORM_MAX_D = 16384
-REPRO_NORM_CHUNK = 16
+REPRO_NORM_CHUNK = 8
 REPRO_QUANT_COLUMNS = 1
 REPRO_MM_A_T, REPRO_MM_B_T = 2, 4
 REPRO_MM_MAX_ROWS = 4194240

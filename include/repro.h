@@ -540,7 +540,7 @@ int repro_distill_bwd(const void* z, int z_type, int64_t z_ld, const void* t_idx
 #define REPRO_NORM_POST 4
 #define REPRO_NORM_GATE_ROWS 8
 #define REPRO_NORM_MAX_D 16384
-#define REPRO_NORM_CHUNK 16
+#define REPRO_NORM_CHUNK 8
 int repro_block_norm_fwd(const void* x, int64_t x_ld, const void* y, int64_t y_ld, int type,
                          const void* gate, int64_t gate_ld, const float* gain_post,
                          const float* gain_pre, float alpha, float beta, float eps, int64_t n,

@@ -562,7 +562,7 @@ def distill_bwd(z, idx, stats, g, label=None, tau=1.0, w_kd=1.0, w_ce=0.0, w_z=0
 
 # ---------------------------------------------------------------- the feed-forward half
 
-NORM_CHUNK, SWIGLU_GROUP = 16, 128
+NORM_CHUNK, SWIGLU_GROUP = 8, 128
 
 
 def bf16(x: float) -> np.float32:

@@ -1261,7 +1261,7 @@ void oracle_distill_bwd(const float* z, int64_t n, int64_t V, const int64_t* idx
 /* activation (definitions and orders: include/repro.h).                      */
 /* ------------------------------------------------------------------------ */
 
-#define NORM_CHUNK 16
+#define NORM_CHUNK 8
 #define SWIGLU_GROUP 128
 
 /* to bf16 and back: nearest, ties to even; a NaN stays one */

@@ -52,9 +52,9 @@ class V:
         return self._sum(-1, 6 + int(math.log2(C)))
 
     def token_sum(self):
-        """Sum over the first axis: chunks of 16, the tree."""
+        """Sum over the first axis: chunks of 8, the tree."""
         n = self.v.shape[0]
-        return self._sum(0, 15 + math.ceil(math.log2(max(1, -(-n // 16)))))
+        return self._sum(0, 7 + math.ceil(math.log2(max(1, -(-n // 8)))))
 
     def _sum(self, axis, roundings):
         a = (np.abs(self.v) + self.e).sum(axis)

@@ -398,3 +398,119 @@ def test_swiglu_reciprocals(orc):
     same(host(a), orc.swiglu_fwd(gu)[0])
     R.repro_swiglu_bwd(torch.ones_like(a), dgu, gu=dev(gu))
     same(host(dgu), orc.swiglu_bwd(np.ones(a.shape, f32), gu=gu))
+
+
+# ---------------------------------------------------------------- alignment and far offsets
+
+def test_floats_on_four_bytes(orc):
+    """Statistics, gains, gates and scales need their own type's alignment only."""
+    n, D = 9, 64
+    c = norm_case(n, D, "channel", True, True)
+    off = lambda a: strided(np.asarray(a, f32).reshape(1, -1), 0, 1)[0] if a.ndim == 1 else strided(a, 0, 1)  # noqa: E731
+    kw = dict(gate=off(c["gate"]), g_post=off(c["g_post"]), g_pre=off(c["g_pre"]), post=True)
+    okw = dict(gate=c["gate"], g_post=c["g_post"], g_pre=c["g_pre"], post=True)
+    h, u, st = (off(np.zeros((n, k), f32)) for k in (D, D, 2))
+    R.repro_block_norm_fwd(dev(c["x"]), dev(c["y"]), h, u, stats=st, **kw)
+    eh, eu, es = orc.block_norm_fwd(c["x"], c["y"], **okw)
+    for t, e in ((h, eh), (u, eu), (st, es)):
+        same(host(t), e)
+    out = [off(np.zeros((n, D), f32)) for _ in range(2)] + [off(np.zeros(D, f32)) for _ in range(3)]
+    R.repro_block_norm_bwd(dev(c["dh"]), dev(c["du"]), dev(eh), dev(c["y"]), st, out[0], out[1], dgate=out[2], dg_post=out[3],
+                           dg_pre=out[4], **kw)
+    for t, e in zip(out, orc.block_norm_bwd(c["dh"], c["du"], eh, c["y"], es, **okw)):
+        same(host(t), e)
+    a, b, sa, sb = mm_case(40, 96, 128)
+    for M in (3, 40):
+        y = off(np.zeros((M, 96), f32))
+        R.repro_matmul_i8(dev(a[:M]), dev(b), y, off(sa[:M]), off(sb))
+        same(host(y), orc.matmul_i8(a[:M], b, sa[:M], sb))
+    gu = rng(1).standard_normal((5, 256)).astype(f32)
+    ea, codes_, scales = orc.swiglu_fwd(gu)
+    av, ct, sv = off(np.zeros((5, 128), f32)), torch.empty((5, 2, 1, 128), dtype=torch.int8, device="cuda"), off(np.zeros(10, f32))
+    R.repro_swiglu_fwd(off(gu), av, ct, sv)
+    same(host(av), ea)
+    same(host(sv), scales.ravel())
+    dgu = off(np.zeros((5, 256), f32))
+    R.repro_swiglu_bwd(av, dgu, codes=ct, scales=sv)
+    same(host(dgu), orc.swiglu_bwd(ea, codes=codes_, scales=scales))
+
+
+def test_lowest_codes(orc):
+    """-128, which no quantiser gives: its sums are exact too."""
+    for M, N, K in ((3, 70, 1024), (40, 200, 1536), (300, 260, 2048)):
+        a, b = np.full((M, K), -128, np.int8), np.full((N, K), -128, np.int8)
+        a[1], b[1] = 127, 127
+        b[2, ::3] = 1
+        y = torch.empty((M, N), device="cuda")
+        R.repro_matmul_i8(dev(a), dev(b), y)
+        same(host(y), (a.astype(np.int64) @ b.astype(np.int64).T).astype(f32))
+
+
+def far(rows, width, dtype, seed):
+    """[rows, width] of more than 2^31 elements: one block of rows over and over, the last ones new."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    t = torch.empty((rows, width), dtype=dtype, device="cuda")
+    head = torch.randn((1000, width), generator=g, device="cuda").to(dtype)
+    for lo in range(0, rows, 1000):
+        t[lo:lo + 1000] = head[:min(1000, rows - lo)]
+    t[-7:] = torch.randn((7, width), generator=g, device="cuda").to(dtype)
+    return t
+
+
+def test_offsets_past_32_bits():
+    """The last rows of tensors of more than 2^31 elements, against the same rows by themselves."""
+    n, D = 270000, 8192
+    x, y = far(n, D, BF, 1), far(n, D, BF, 2)
+    h, u, st = torch.empty_like(x), torch.empty_like(x), torch.empty((n, 2), device="cuda")
+    gain = torch.linspace(0.5, 1.5, D, device="cuda")
+    R.repro_block_norm_fwd(x, y, h, u, stats=st, g_post=gain, g_pre=gain, post=True)
+    t = slice(n - 9, n)
+    h2, u2, st2 = torch.empty((9, D), dtype=BF, device="cuda"), torch.empty((9, D), dtype=BF, device="cuda"), torch.empty((9, 2), device="cuda")
+    R.repro_block_norm_fwd(x[t], y[t], h2, u2, stats=st2, g_post=gain, g_pre=gain, post=True)
+    assert torch.equal(h[t], h2) and torch.equal(u[t], u2) and torch.equal(st[t], st2)
+    dx, dy, dg = x, torch.empty_like(x), torch.empty(D, device="cuda")   # x is done with
+    R.repro_block_norm_bwd(None, u, h, y, st, dx, dy, g_post=gain, g_pre=gain, dg_post=dg, dg_pre=torch.empty_like(dg), post=True)
+    dx2, dy2 = torch.empty_like(h2), torch.empty_like(h2)
+    R.repro_block_norm_bwd(None, u[t], h2, y[t], st2, dx2, dy2, g_post=gain, g_pre=gain, dg_post=dg, dg_pre=torch.empty_like(dg),
+                           post=True)
+    assert torch.equal(dx[t], dx2) and torch.equal(dy[t], dy2)
+    del x, y, u, dx, dy
+    q, s = torch.empty((n, D), dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda")
+    R.repro_quant_rows_i8(h, q, s)
+    q2, s2 = torch.empty((9, D), dtype=torch.int8, device="cuda"), torch.empty(9, device="cuda")
+    R.repro_quant_rows_i8(h[t], q2, s2)
+    assert torch.equal(q[t], q2) and torch.equal(s[t], s2)
+    c = torch.empty(D, device="cuda")
+    R.repro_quant_rows_i8(h, q, c, columns=True)
+    assert torch.equal(c, h.abs().amax(0).float() / torch.full((1,), 127.0, device="cuda"))
+    assert int((q[-7:].float() - (h[-7:].float() / c).round()).abs().max()) == 0
+    a, codes_, sc = torch.empty((n, D // 2), dtype=BF, device="cuda"), q.view(n, 2, D // 256, 128), torch.empty((n, 2, D // 256), device="cuda")
+    R.repro_swiglu_fwd(h, a, codes_, sc)
+    a2, codes2, sc2 = torch.empty((9, D // 2), dtype=BF, device="cuda"), torch.empty((9, 2, D // 256, 128), dtype=torch.int8, device="cuda"), torch.empty((9, 2, D // 256), device="cuda")
+    R.repro_swiglu_fwd(h[t], a2, codes2, sc2)
+    assert torch.equal(a[t], a2) and torch.equal(codes_[t], codes2) and torch.equal(sc[t], sc2)
+    dgu, dgu2 = torch.empty_like(h), torch.empty_like(h2)
+    R.repro_swiglu_bwd(a, dgu, codes=codes_, scales=sc)
+    R.repro_swiglu_bwd(a2, dgu2, codes=codes2, scales=sc2)
+    assert torch.equal(dgu[t], dgu2)
+    del a, codes_, sc, dgu, q, h
+    M, N, K = 60000, 40000, 96
+    g = torch.Generator(device="cuda").manual_seed(5)
+    am, bm = (torch.randint(-127, 128, (r, K), generator=g, device="cuda", dtype=torch.int8) for r in (M, N))
+    ym = torch.empty((M, N), device="cuda")
+    R.repro_matmul_i8(am, bm, ym)
+    assert torch.equal(ym[-300:], (am[-300:].double() @ bm.double().T).float())
+    assert R.repro_device_check() == R.REPRO_OK
+
+
+def test_wide_rows_and_many_columns(orc):
+    """Codes of rows past what a thread keeps, and of a wide matrix by columns, in odd widths."""
+    g = rng(9)
+    for n, D in ((2, 40001), (3, 65536), (900, 5001)):
+        x = g.standard_normal((n, D)).astype(f32)
+        for columns in (False, True):
+            q, s = torch.empty((n, D), dtype=torch.int8, device="cuda"), torch.empty(D if columns else n, device="cuda")
+            R.repro_quant_rows_i8(dev(x), q, s, columns=columns)
+            eq, es = orc.quant_rows(x, None, columns)
+            same(host(s), es)
+            assert np.array_equal(host(q), eq)
