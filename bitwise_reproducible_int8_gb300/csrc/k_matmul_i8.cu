@@ -47,8 +47,29 @@ struct Widen {
     const int8_t* q;
     int64_t ld, rows, K, Kp;    // source rows of K (or, transposed, K rows of `rows`); pitch of the copy
     __nv_bfloat16* out;
+    const int8_t* end;          // behind the last code
     bool vec;                   // source rows on 8-byte (transposed: 16-byte) boundaries
 };
+
+// the `left` (at most 8) codes from p on, wherever p lies, 0 behind them: three words that cover them,
+// shifted, where these lie within [lo, hi), else one by one
+__device__ __forceinline__ uint2 codes8(const int8_t* p, int64_t left, const int8_t* lo, const int8_t* hi)
+{
+    uint32_t v[2] = {0, 0};
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3;
+    if (left >= 8 && at >= reinterpret_cast<uintptr_t>(lo) && at + 12 <= reinterpret_cast<uintptr_t>(hi)) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(at);
+        const uint32_t a = __ldg(q), b = __ldg(q + 1), c = __ldg(q + 2), s = 8 * (uint32_t)(reinterpret_cast<uintptr_t>(p) & 3);
+        v[0] = __funnelshift_r(a, b, s);
+        v[1] = __funnelshift_r(b, c, s);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < left)
+                v[e >> 2] |= (uint32_t)(uint8_t)p[e] << (8 * (e & 3));
+    }
+    return make_uint2(v[0], v[1]);
+}
 
 // rows of K codes to rows of Kp bf16, zeros behind K; 8 at a time
 __global__ void __launch_bounds__(256)
@@ -68,12 +89,7 @@ k_mm_widen(const __grid_constant__ Widen w)
             if (w.vec && k + 8 <= w.K) {
                 c = __ldg(reinterpret_cast<const uint2*>(p));
             } else {
-                uint32_t v[2] = {0, 0};
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (k + e < w.K)
-                        v[e >> 2] |= (uint32_t)(uint8_t)p[e] << (8 * (e & 3));
-                c = make_uint2(v[0], v[1]);
+                c = codes8(p, w.K - k, w.q, w.end);
             }
         }
         const uint2 a = widen4(c.x), b = widen4(c.y);
@@ -157,7 +173,7 @@ k_mm_widen_t(const __grid_constant__ Widen w, int tiles_r)
 cudaError_t widen(const int8_t* q, int64_t ld, int64_t rows, int64_t K, bool t, __nv_bfloat16* out, cudaStream_t st)
 {
     const size_t b = t ? 16 : 8;
-    Widen w = {q, ld, rows, K, pad8(K), out, reinterpret_cast<uintptr_t>(q) % b == 0 && ld % (int64_t)b == 0};
+    Widen w = {q, ld, rows, K, pad8(K), out, q + (t ? (K - 1) * ld + rows : (rows - 1) * ld + K), reinterpret_cast<uintptr_t>(q) % b == 0 && ld % (int64_t)b == 0};
     count_launches(1);
     if (t) {
         const int tiles_r = (int)((rows + 127) / 128);
@@ -499,8 +515,8 @@ __device__ __forceinline__ Item item_at(const PairArgs& a, int i)
 }
 
 // A warp's 32 rows x EW columns: scaled, added to what is there, stored.  own: the columns' scales,
-// two a lane.  Rows on 16-byte boundaries go through the warp's buffer in blocks of 128 bytes (chunk
-// k of row r at k ^ (r mod 8)), one tensor store each.  (Straight to memory, 4 lanes to a row's line
+// two a lane.  They go through the warp's buffer in blocks of 128 bytes a row (chunk k of row r at
+// k ^ (r mod 8)): rows on 16-byte boundaries by one tensor store a block, others row by row.  (Straight to memory, 4 lanes to a row's line
 // after a turn by shuffles, 16384 x 11264 x 2048 took 87 us longer, although the operands' ring then
 // has two stages more; a lane's own 32 bytes at a time took 41 us longer still.)
 template <typename Y>
@@ -532,16 +548,8 @@ __device__ __forceinline__ void finish(const PairArgs& p, const CUtensorMap* map
                 v = fadd2_ftz(v, z);
             unpack2(v, o[e], o[e + 1]);
         }
-        if (!p.y_tma) {
-            if (live)
-#pragma unroll
-                for (int e = 0; e < W; ++e)
-                    if (n + b + e < g.N)
-                        put(row + n + b + e, o[e], g.accumulate);
-            continue;
-        }
         // added to the old values here: a reduction in L2 would not flush subnormals
-        if (sizeof(Y) == 4 && g.accumulate && live) {
+        if (sizeof(Y) == 4 && g.accumulate && live && p.y_tma) {
 #pragma unroll
             for (int e = 0; e < W; e += 4) {
                 const int c = n + b + e;
@@ -563,12 +571,24 @@ __device__ __forceinline__ void finish(const PairArgs& p, const CUtensorMap* map
 #pragma unroll
         for (int k = 0; k < 8; ++k)   // 16 bytes a step
             store16(reinterpret_cast<Y*>(stg + lane * 128 + 16 * (k ^ (lane & 7))), o + E * k);
-        {
+        if (p.y_tma) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0)
                 store_block(map, stg, n + b, r0);
+            continue;
         }
+        // rows off 16-byte boundaries: row by row, neighbouring lanes neighbouring elements
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < 32 && r0 + i < g.M; ++i)
+#pragma unroll
+            for (int e = lane; e < W; e += 32)
+                if (n + b + e < g.N)
+                    put(static_cast<Y*>(g.y) + (int64_t)(r0 + i) * g.y_ld + n + b + e,
+                        to_f32<Y>(*reinterpret_cast<const Y*>(stg + i * 128 + 16 * ((e / E) ^ (i & 7)) + e % E * sizeof(Y))),
+                        g.accumulate);
+        __syncwarp();
     }
 }
 
