@@ -261,6 +261,7 @@ struct NormArgs {
     float *dgain_post, *dgain_pre;
     float* parts[3];     // set by the launchers: partial sums of gain_pre, gain_post and a gate that is one row
     int64_t pitch;
+    int piece, piece_u;  // elements that rows of the stream's type, and of u's, are copied by (0: not)
     int chunk;           // tokens whose terms a group of the backward sums
     int tpr;             // threads of a row
     float inv;           // 1 / D where D is a power of two, else 0

@@ -37,18 +37,19 @@ __device__ __forceinline__ RowLane lane_of(const NormArgs& a, int& sub)
     r.t = threadIdx.x - sub * a.tpr;
     r.D = (int)a.D;
     r.bar = 1 + sub;
-    r.vec = a.vec;
     return r;
 }
 
-template <bool FULL> __device__ __forceinline__ void gain16(const float* g, const RowLane& r, u64 (&v)[8])
+template <int W> __device__ __forceinline__ void gain16(const float* g, const RowLane& r, u64 (&v)[8])
 {
-    load_row16<FULL, false>(g, r, v);
+    load_row16<W, false>(g, r, v);
     flush16(v);
 }
 
-template <typename T, typename U, int THREADS, bool FULL>
-__global__ void __launch_bounds__(THREADS)
+// 64 registers a thread: with 94, five rows of 2048 on an SM instead of eight, 8192 x 4096 fp32 took
+// 93 us against 80
+template <typename T, typename U, int THREADS, int W>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 k_norm_fwd(const __grid_constant__ NormArgs a)
 {
     __shared__ float red[4][64];
@@ -62,23 +63,23 @@ k_norm_fwd(const __grid_constant__ NormArgs a)
         float r1 = 0.0f, r2 = 0.0f;
         if (a.y) {
             u64 y[8];
-            load_row16<FULL, true>(static_cast<const T*>(a.y) + i * a.y_ld, r, y);
-            load_row16<FULL, false>(static_cast<const T*>(a.x) + i * a.x_ld, r, x);
+            load_row16<W, true>(static_cast<const T*>(a.y) + i * a.y_ld, r, y);
+            load_row16<W, false>(static_cast<const T*>(a.x) + i * a.x_ld, r, x);
             flush16(y);
             if (a.post) {
-                r1 = rms_of(tree_of_chains(chain16<FULL>(y, y, r), r, red[sub], phase), a);
+                r1 = rms_of(tree_of_chains(chain16<W>(y, y, r), r, red[sub], phase), a);
                 mul16(y, r1);
                 if (a.gain_post) {
-                    gain16<FULL>(a.gain_post, r, w);
+                    gain16<W>(a.gain_post, r, w);
                     mul16(y, w);
                 }
             }
             if (a.gate) {
                 if (a.gate_rows) {
-                    load_row16<FULL, true>(static_cast<const T*>(a.gate) + i * a.gate_ld, r, w);
+                    load_row16<W, true>(static_cast<const T*>(a.gate) + i * a.gate_ld, r, w);
                     flush16(w);
                 } else {
-                    gain16<FULL>(static_cast<const float*>(a.gate), r, w);
+                    gain16<W>(static_cast<const float*>(a.gate), r, w);
                 }
                 mul16(y, w);
             }
@@ -93,19 +94,19 @@ k_norm_fwd(const __grid_constant__ NormArgs a)
                     x[e] = pack2(to_f32<T>(from_f32<T>(p)), to_f32<T>(from_f32<T>(q)));
                 }
             }
-            store_row16<FULL>(static_cast<T*>(a.h) + i * a.h_ld, r, x);
+            store_row16<W>(static_cast<T*>(a.h) + i * a.h_ld, r, x);
         } else {
-            load_row16<FULL, true>(static_cast<const T*>(a.x) + i * a.x_ld, r, x);
+            load_row16<W, true>(static_cast<const T*>(a.x) + i * a.x_ld, r, x);
         }
         if (a.u) {
             flush16(x);
-            r2 = rms_of(tree_of_chains(chain16<FULL>(x, x, r), r, red[sub], phase), a);
+            r2 = rms_of(tree_of_chains(chain16<W>(x, x, r), r, red[sub], phase), a);
             mul16(x, r2);
             if (a.gain_pre) {
-                gain16<FULL>(a.gain_pre, r, w);
+                gain16<W>(a.gain_pre, r, w);
                 mul16(x, w);
             }
-            store_row16<FULL>(static_cast<U*>(a.u) + i * a.u_ld, r, x);
+            store_row16<W>(static_cast<U*>(a.u) + i * a.u_ld, r, x);
         }
         if (a.stats && r.t == 0) {
             a.stats[2 * i] = r1;
@@ -115,11 +116,11 @@ k_norm_fwd(const __grid_constant__ NormArgs a)
 }
 
 // v <- scale (x) (v (-) (unit (x) c)), c = S(v (x) unit) (/) D
-template <bool FULL>
+template <int W>
 __device__ __forceinline__ void norm_back(u64 (&v)[8], const u64 (&unit)[8], float scale, const NormArgs& a,
                                           const RowLane& r, float* red, int& phase)
 {
-    const float c = mean_of(tree_of_chains(chain16<FULL>(v, unit, r), r, red, phase), (float)a.D, a.inv);
+    const float c = mean_of(tree_of_chains(chain16<W>(v, unit, r), r, red, phase), (float)a.D, a.inv);
     const u64 cc = pack2(-c, -c), sc = pack2(scale, scale), z = pack2(-0.0f, -0.0f);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -135,7 +136,7 @@ __device__ __forceinline__ void column_sum(u64 (&s)[8], const u64 (&a)[8], const
         s[e] = fadd2_ftz(fmul2_rn(a[e], b[e]), first ? z : s[e]);
 }
 
-template <bool FULL>
+template <int W>
 __device__ __forceinline__ void store_parts(float* parts, int64_t chunk, int64_t pitch, const RowLane& r, const u64 (&s)[8])
 {
 #pragma unroll
@@ -144,7 +145,7 @@ __device__ __forceinline__ void store_parts(float* parts, int64_t chunk, int64_t
         float4 v;
         unpack2(s[2 * k], v.x, v.y);
         unpack2(s[2 * k + 1], v.z, v.w);
-        if (FULL || d < r.D)   // the pitch is a multiple of 4
+        if (W == WHOLE || d < r.D)   // the pitch is a multiple of 4
             store4(parts + chunk * pitch + d, v);
     }
 }
@@ -153,7 +154,7 @@ __device__ __forceinline__ void store_parts(float* parts, int64_t chunk, int64_t
 // row of each stream on its way for every group on an SM); else loads where values are needed.
 // CHANNEL: a gate that is one row, whose sums take 16 more registers.  Three groups of 128 threads an
 // SM at 168 registers; with four at 128 the kernel spills.
-template <typename T, int THREADS, bool AHEAD, bool FULL, bool CHANNEL>
+template <typename T, int THREADS, bool AHEAD, int W, bool CHANNEL>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 384 / THREADS : 1)
 k_norm_bwd(const __grid_constant__ NormArgs a)
 {
@@ -175,20 +176,20 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
     auto ask_norm = [&](int64_t i) {      // what the norm before the block needs of token i
         if (a.du) {
             if (a.u_type == 0)
-                ask_row16<FULL>(static_cast<Four<float>*>(s_du), static_cast<const float*>(a.du) + i * a.du_ld, r);
+                ask_row16<W>(static_cast<Four<float>*>(s_du), static_cast<const float*>(a.du) + i * a.du_ld, r, a.piece_u);
             else
-                ask_row16<FULL>(static_cast<Four<__nv_bfloat16>*>(s_du), static_cast<const __nv_bfloat16*>(a.du) + i * a.du_ld, r);
-            ask_row16<FULL>(s_h, row_t(a.hs, a.hs_ld, i), r);
+                ask_row16<W>(static_cast<Four<__nv_bfloat16>*>(s_du), static_cast<const __nv_bfloat16*>(a.du) + i * a.du_ld, r, a.piece_u);
+            ask_row16<W>(s_h, row_t(a.hs, a.hs_ld, i), r, a.piece);
         }
         asked();
     };
     auto ask_rest = [&](int64_t i) {
         if (a.dh)
-            ask_row16<FULL>(s_dh, row_t(a.dh, a.dh_ld, i), r);
+            ask_row16<W>(s_dh, row_t(a.dh, a.dh_ld, i), r, a.piece);
         if (a.y)
-            ask_row16<FULL>(s_y, row_t(a.y, a.y_ld, i), r);
+            ask_row16<W>(s_y, row_t(a.y, a.y_ld, i), r, a.piece);
         if (gates)
-            ask_row16<FULL>(s_gate, row_t(a.gate, a.gate_ld, i), r);
+            ask_row16<W>(s_gate, row_t(a.gate, a.gate_ld, i), r, a.piece);
         asked();
     };
     pdl_wait();
@@ -215,16 +216,16 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
             if (a.du) {
                 if (!AHEAD) {
                     if (a.u_type == 0)
-                        load_row16<FULL, true>(static_cast<const float*>(a.du) + i * a.du_ld, r, v);
+                        load_row16<W, true>(static_cast<const float*>(a.du) + i * a.du_ld, r, v);
                     else
-                        load_row16<FULL, true>(static_cast<const __nv_bfloat16*>(a.du) + i * a.du_ld, r, v);
-                    load_row16<FULL, true>(row_t(a.hs, a.hs_ld, i), r, unit);
+                        load_row16<W, true>(static_cast<const __nv_bfloat16*>(a.du) + i * a.du_ld, r, v);
+                    load_row16<W, true>(row_t(a.hs, a.hs_ld, i), r, unit);
                 } else {
                     if (a.u_type == 0)
-                        take_row16<FULL>(static_cast<const Four<float>*>(s_du), r, v);
+                        take_row16<W>(static_cast<const Four<float>*>(s_du), r, v);
                     else
-                        take_row16<FULL>(static_cast<const Four<__nv_bfloat16>*>(s_du), r, v);
-                    take_row16<FULL>(s_h, r, unit);
+                        take_row16<W>(static_cast<const Four<__nv_bfloat16>*>(s_du), r, v);
+                    take_row16<W>(s_h, r, unit);
                 }
                 flush16(v);
                 flush16(unit);
@@ -232,7 +233,7 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
                 if (a.dgain_pre)
                     column_sum(s_pre, v, unit, first);
                 if (a.gain_pre) {
-                    gain16<FULL>(a.gain_pre, r, w);
+                    gain16<W>(a.gain_pre, r, w);
                     mul16(v, w);
                 }
             }
@@ -243,14 +244,14 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
                     asked();
             }
             if (a.du)
-                norm_back<FULL>(v, unit, r2, a, r, red[sub], phase);
+                norm_back<W>(v, unit, r2, a, r, red[sub], phase);
             if (AHEAD)
                 wait_asked<1>();
             if (a.dh) {
                 if (!AHEAD)
-                    load_row16<FULL, false>(row_t(a.dh, a.dh_ld, i), r, g);
+                    load_row16<W, false>(row_t(a.dh, a.dh_ld, i), r, g);
                 else
-                    take_row16<FULL>(s_dh, r, g);
+                    take_row16<W>(s_dh, r, g);
                 flush16(g);
                 if (a.du)
 #pragma unroll
@@ -262,7 +263,7 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
                     g[e] = v[e];
             }
             if (!a.y) {
-                store_row16<FULL>(static_cast<T*>(a.dx) + i * a.dx_ld, r, g);
+                store_row16<W>(static_cast<T*>(a.dx) + i * a.dx_ld, r, g);
                 if (AHEAD) {
                     if (i + 1 < hi)
                         ask_rest(i + 1);
@@ -275,17 +276,17 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
             for (int e = 0; e < 8; ++e)
                 v[e] = g[e];
             mul16(v, alpha);
-            store_row16<FULL>(static_cast<T*>(a.dx) + i * a.dx_ld, r, v);
+            store_row16<W>(static_cast<T*>(a.dx) + i * a.dx_ld, r, v);
             mul16(g, beta);
             if (!AHEAD)
-                load_row16<FULL, true>(row_t(a.y, a.y_ld, i), r, unit);
+                load_row16<W, true>(row_t(a.y, a.y_ld, i), r, unit);
             else
-                take_row16<FULL>(s_y, r, unit);
+                take_row16<W>(s_y, r, unit);
             if (gates) {
                 if (!AHEAD)
-                    load_row16<FULL, true>(row_t(a.gate, a.gate_ld, i), r, w);
+                    load_row16<W, true>(row_t(a.gate, a.gate_ld, i), r, w);
                 else
-                    take_row16<FULL>(s_gate, r, w);
+                    take_row16<W>(s_gate, r, w);
                 flush16(w);
             }
             if (AHEAD) {
@@ -303,15 +304,15 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
                     v[e] = unit[e];
                 if (a.post && a.gain_post) {
                     u64 gp[8];
-                    gain16<FULL>(a.gain_post, r, gp);
+                    gain16<W>(a.gain_post, r, gp);
                     mul16(v, gp);
                 }
                 if (gates) {
                     mul16(v, g);
-                    store_row16<FULL>(static_cast<T*>(a.dgate) + i * a.dgate_ld, r, v);
+                    store_row16<W>(static_cast<T*>(a.dgate) + i * a.dgate_ld, r, v);
                 } else {
                     column_sum(s_chan, g, v, first);
-                    gain16<FULL>(static_cast<const float*>(a.gate), r, w);
+                    gain16<W>(static_cast<const float*>(a.gate), r, w);
                 }
                 mul16(g, w);
             }
@@ -319,19 +320,19 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
                 if (a.dgain_post)
                     column_sum(s_post, g, unit, first);
                 if (a.gain_post) {
-                    gain16<FULL>(a.gain_post, r, w);
+                    gain16<W>(a.gain_post, r, w);
                     mul16(g, w);
                 }
-                norm_back<FULL>(g, unit, r1, a, r, red[sub], phase);
+                norm_back<W>(g, unit, r1, a, r, red[sub], phase);
             }
-            store_row16<FULL>(static_cast<T*>(a.dy) + i * a.dy_ld, r, g);
+            store_row16<W>(static_cast<T*>(a.dy) + i * a.dy_ld, r, g);
         }
         if (a.dgain_pre)
-            store_parts<FULL>(a.parts[0], ch, a.pitch, r, s_pre);
+            store_parts<W>(a.parts[0], ch, a.pitch, r, s_pre);
         if (a.dgain_post)
-            store_parts<FULL>(a.parts[1], ch, a.pitch, r, s_post);
+            store_parts<W>(a.parts[1], ch, a.pitch, r, s_post);
         if (CHANNEL)
-            store_parts<FULL>(a.parts[2], ch, a.pitch, r, s_chan);
+            store_parts<W>(a.parts[2], ch, a.pitch, r, s_chan);
     }
 }
 
@@ -363,9 +364,15 @@ k_norm_fold(const __grid_constant__ Fold f)
     store4(f.parts[job] + ch * f.pitch + c, v[0]);
 }
 
-// Few tokens: 2^21 elements, where the terms' way through L2 (16 MB for two sums) takes less than the
-// rows of a chunk one after another on the 3 x 152 groups that run at once.
-inline bool by_tokens(int64_t n, int64_t D) { return n > 1 && n <= (int64_t)1 << 21 && n * D <= (int64_t)1 << 21; }
+// Few tokens: up to 2^21 elements, where the terms' way through L2 (16 MB for two sums) takes less than
+// the rows of a chunk one after another, or chunks for less than half of the groups that run at once
+// (three CTAs of 128 threads on an SM, one of more).
+inline bool by_tokens(int64_t n, int64_t D)
+{
+    const int tpr = row_threads(D);
+    const int64_t at_once = (int64_t)num_sms() * (tpr <= 128 ? 3 * (128 / tpr) : 1);
+    return n > 1 && n <= (int64_t)1 << 21 && (n * D <= (int64_t)1 << 21 || 2 * ((n + CHUNK - 1) / CHUNK) < at_once);
+}
 
 inline int64_t pitch_of(int64_t D) { return (D + 3) / 4 * 4; }
 
@@ -387,18 +394,41 @@ void set_up(NormArgs& a)
             rows4_or_none(a.gain_post, 0, 4) && rows4_or_none(a.gain_pre, 0, 4);
 }
 
+int check_of(const NormArgs& a)
+{
+    return !a.vec || a.D % 4 != 0 ? ELEMENTS : a.D == (int64_t)ROW_E * a.tpr ? WHOLE : GROUPS;
+}
+
+// the pieces that every row of the backward can be copied by
+void set_pieces(NormArgs& a)
+{
+    const int t = a.type == 0 ? 4 : 2, u = a.u_type == 0 ? 4 : 2;
+    a.piece = 4;
+    const struct {
+        const void* p;
+        int64_t ld;
+    } rows[4] = {{a.hs, a.hs_ld}, {a.dh, a.dh_ld}, {a.y, a.y_ld}, {a.gate_rows ? a.gate : nullptr, a.gate_ld}};
+    for (const auto& r : rows)
+        if (r.p) {
+            const int e = piece_of(r.p, r.ld, a.D, t);
+            a.piece = e < a.piece ? e : a.piece;
+        }
+    a.piece_u = a.du ? piece_of(a.du, a.du_ld, a.D, u) : 4;
+}
+
 template <typename T, typename U> cudaError_t launch_fwd(const NormArgs& a, int threads, dim3 grid, cudaStream_t st)
 {
-    const bool full = a.vec && a.D == (int64_t)ROW_E * a.tpr;
-#define GO(N) (full ? launch_pdl(k_norm_fwd<T, U, N, true>, grid, dim3(threads), 0, st, a) \
-                    : launch_pdl(k_norm_fwd<T, U, N, false>, grid, dim3(threads), 0, st, a))
-    return threads <= 256 ? GO(256) : threads == 512 ? GO(512) : GO(1024);
+    const int w = check_of(a);
+#define GO(N) (w == WHOLE    ? launch_pdl(k_norm_fwd<T, U, N, WHOLE>, grid, dim3(threads), 0, st, a) \
+               : w == GROUPS ? launch_pdl(k_norm_fwd<T, U, N, GROUPS>, grid, dim3(threads), 0, st, a) \
+                             : launch_pdl(k_norm_fwd<T, U, N, ELEMENTS>, grid, dim3(threads), 0, st, a))
+    return threads == 128 ? GO(128) : threads == 256 ? GO(256) : threads == 512 ? GO(512) : GO(1024);
 #undef GO
 }
 
-template <typename T, int N, bool AHEAD, bool FULL> cudaError_t run_bwd(const NormArgs& a, dim3 grid, cudaStream_t st)
+template <typename T, int N, bool AHEAD, int W> cudaError_t run_bwd(const NormArgs& a, dim3 grid, cudaStream_t st)
 {
-    const auto k = a.gate && !a.gate_rows ? k_norm_bwd<T, N, AHEAD, FULL, true> : k_norm_bwd<T, N, AHEAD, FULL, false>;
+    const auto k = a.gate && !a.gate_rows ? k_norm_bwd<T, N, AHEAD, W, true> : k_norm_bwd<T, N, AHEAD, W, false>;
     const size_t smem = AHEAD ? (size_t)N * ROW_E * ((a.gate_rows ? 4 : 3) * sizeof(T) + (a.u_type == 0 ? 4 : 2)) : 0;
     if (smem > 40 * 1024) {   // static shared memory counts too
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -410,9 +440,11 @@ template <typename T, int N, bool AHEAD, bool FULL> cudaError_t run_bwd(const No
 
 template <typename T, int N> cudaError_t pick_bwd(const NormArgs& a, dim3 grid, cudaStream_t st)
 {
-    if (!a.vec || a.D % 4 != 0)
-        return run_bwd<T, N, false, false>(a, grid, st);
-    return a.D == (int64_t)ROW_E * a.tpr ? run_bwd<T, N, true, true>(a, grid, st) : run_bwd<T, N, true, false>(a, grid, st);
+    if (a.piece == 0 || a.piece_u == 0)
+        return run_bwd<T, N, false, ELEMENTS>(a, grid, st);
+    const int w = check_of(a);
+    return w == WHOLE ? run_bwd<T, N, true, WHOLE>(a, grid, st) : w == GROUPS ? run_bwd<T, N, true, GROUPS>(a, grid, st)
+                                                                              : run_bwd<T, N, true, ELEMENTS>(a, grid, st);
 }
 
 template <typename T> cudaError_t launch_bwd(const NormArgs& a, int threads, dim3 grid, cudaStream_t st)
@@ -420,7 +452,8 @@ template <typename T> cudaError_t launch_bwd(const NormArgs& a, int threads, dim
     return threads == 128   ? pick_bwd<T, 128>(a, grid, st)
            : threads == 256 ? pick_bwd<T, 256>(a, grid, st)
            : threads == 512 ? pick_bwd<T, 512>(a, grid, st)
-                            : run_bwd<T, 1024, false, false>(a, grid, st);   // the slots of 1,024 threads would not fit
+           : check_of(a) == ELEMENTS ? run_bwd<T, 1024, false, ELEMENTS>(a, grid, st)   // the slots of 1,024 threads would not fit
+                                     : run_bwd<T, 1024, false, GROUPS>(a, grid, st);
 }
 
 // threads of a CTA and CTAs of a grid for so many rows or chunks
@@ -458,6 +491,7 @@ cudaError_t launch_norm_bwd(NormArgs a, void* ws, cudaStream_t st)
     float* const out[3] = {a.dgain_pre, a.dgain_post, a.gate && !a.gate_rows ? static_cast<float*>(a.dgate) : nullptr};
     const bool sums = out[0] || out[1] || out[2], single = !sums || by_tokens(a.n, a.D);
     a.chunk = single ? 1 : CHUNK;
+    set_pieces(a);
     float* const parts = static_cast<float*>(ws);
     RowTree t = {};
     t.pitch = a.pitch;

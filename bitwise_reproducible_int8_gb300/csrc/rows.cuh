@@ -29,7 +29,6 @@ inline int row_threads(int64_t D)
 struct RowLane {
     int t, tpr, D;      // thread in the group, threads of the group, width
     int bar;            // named barrier of the group
-    bool vec;           // rows and strides on 4-element boundaries
     __device__ __forceinline__ int at(int k) const { return 4 * (t + k * tpr); }   // first element of group k
 };
 
@@ -38,18 +37,23 @@ __device__ __forceinline__ void group_barrier(const RowLane& r)
     asm volatile("bar.sync %0, %1;" ::"r"(r.bar), "r"(r.tpr) : "memory");
 }
 
-// FULL: D = 16 TPR and vec, nothing to check.  What lies past D reads as 0.
-template <bool FULL, bool STREAM, typename T>
+// What a row's width leaves to check.  WHOLE: D = 16 TPR, rows on 4-element boundaries: nothing.
+// GROUPS: the boundaries and D a multiple of 4: whether a group is there.  ELEMENTS: each element.
+constexpr int ELEMENTS = 0, GROUPS = 1, WHOLE = 2;
+
+// What lies past D reads as 0.
+template <int W, bool STREAM, typename T>
 __device__ __forceinline__ void load_row16(const T* p, const RowLane& r, u64 (&v)[8])
 {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int d = r.at(k);
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (FULL || (r.vec && d + 4 <= r.D)) {
-            x = STREAM ? stream4(p + d) : load4(p + d);
-        } else if (d < r.D) {
-            x.x = to_f32<T>(p[d]);
+        if (W != ELEMENTS) {
+            if (W == WHOLE || d < r.D)
+                x = STREAM ? stream4(p + d) : load4(p + d);
+        } else {
+            x.x = d < r.D ? to_f32<T>(p[d]) : 0.0f;
             x.y = d + 1 < r.D ? to_f32<T>(p[d + 1]) : 0.0f;
             x.z = d + 2 < r.D ? to_f32<T>(p[d + 2]) : 0.0f;
             x.w = d + 3 < r.D ? to_f32<T>(p[d + 3]) : 0.0f;
@@ -59,7 +63,7 @@ __device__ __forceinline__ void load_row16(const T* p, const RowLane& r, u64 (&v
     }
 }
 
-template <bool FULL, typename T>
+template <int W, typename T>
 __device__ __forceinline__ void store_row16(T* p, const RowLane& r, const u64 (&v)[8])
 {
 #pragma unroll
@@ -68,10 +72,12 @@ __device__ __forceinline__ void store_row16(T* p, const RowLane& r, const u64 (&
         float4 x;
         unpack2(v[2 * k], x.x, x.y);
         unpack2(v[2 * k + 1], x.z, x.w);
-        if (FULL || (r.vec && d + 4 <= r.D)) {
-            store4(p + d, x);
-        } else if (d < r.D) {
-            p[d] = from_f32<T>(x.x);
+        if (W != ELEMENTS) {
+            if (W == WHOLE || d < r.D)
+                store4(p + d, x);
+        } else {
+            if (d < r.D)
+                p[d] = from_f32<T>(x.x);
             if (d + 1 < r.D)
                 p[d + 1] = from_f32<T>(x.y);
             if (d + 2 < r.D)
@@ -84,35 +90,72 @@ __device__ __forceinline__ void store_row16(T* p, const RowLane& r, const u64 (&
 
 // A thread's share of a row on its way through shared memory: asked for early, taken when it is needed.
 // Each thread copies and reads its own 16 elements only, so no barrier stands between; group k of
-// thread t lies at k threads + t.  Rows on 4-element boundaries, D a multiple of 4.
+// thread t lies at k threads + t.  piece (ELEMENTS): elements copied at a time, 4, 2 or 1, whatever the
+// rows' boundaries and width allow (a copy has 4 bytes at least).
 template <typename T> struct alignas(4 * sizeof(T)) Four {
     T v[4];
 };
 
-template <bool FULL, typename T>
-__device__ __forceinline__ void ask_row16(Four<T>* slot, const T* p, const RowLane& r)
+template <int BYTES> __device__ __forceinline__ void copy_async(void* to, const void* from)
 {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (FULL || r.at(k) < r.D) {
-            const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot + k * blockDim.x + threadIdx.x);
-            if (sizeof(T) == 4)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p + r.at(k)) : "memory");
-            else
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(p + r.at(k)) : "memory");
-        }
+    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(from), "n"(BYTES) : "memory");
 }
 
-template <bool FULL, typename T> __device__ __forceinline__ void take_row16(const Four<T>* slot, const RowLane& r, u64 (&v)[8])
+template <int W, typename T>
+__device__ __forceinline__ void ask_row16(Four<T>* slot, const T* p, const RowLane& r, int piece)
+{
+    constexpr int SZ = (int)sizeof(T);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int d = r.at(k);
+        T* to = slot[k * blockDim.x + threadIdx.x].v;
+        if (W != ELEMENTS) {
+            if (W == WHOLE || d < r.D)
+                copy_async<4 * SZ>(to, p + d);
+        } else if (piece == 4) {
+            if (d < r.D)
+                copy_async<4 * SZ>(to, p + d);
+        } else if (SZ == 2 || piece == 2) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2)
+                if (d + e < r.D)
+                    copy_async<2 * SZ>(to + e, p + d + e);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (d + e < r.D)
+                    copy_async<SZ == 4 ? 4 : 8>(to + e, p + d + e);   // fp32 alone comes here
+        }
+    }
+}
+
+template <int W, typename T> __device__ __forceinline__ void take_row16(const Four<T>* slot, const RowLane& r, u64 (&v)[8])
 {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (FULL || r.at(k) < r.D)
+        if (W != GROUPS || r.at(k) < r.D)
             x = load4(slot[k * blockDim.x + threadIdx.x].v);
+        if (W == ELEMENTS) {
+            const int left = r.D - r.at(k);
+            x.x = left > 0 ? x.x : 0.0f, x.y = left > 1 ? x.y : 0.0f, x.z = left > 2 ? x.z : 0.0f, x.w = left > 3 ? x.w : 0.0f;
+        }
         v[2 * k] = pack2(x.x, x.y);
         v[2 * k + 1] = pack2(x.z, x.w);
     }
+}
+
+// elements at a time that rows of `size` bytes an element, `ld` apart, can be copied by; 0: none
+inline int piece_of(const void* p, int64_t ld, int64_t D, int size)
+{
+    for (int e = 4; e * size >= 4; e /= 2)
+        if (reinterpret_cast<uintptr_t>(p) % (e * size) == 0 && ld % e == 0 && D % e == 0)
+            return e;
+    return 0;
 }
 
 __device__ __forceinline__ void asked() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -144,7 +187,7 @@ __device__ __forceinline__ void mul16(u64 (&v)[8], float w)
 }
 
 // this thread's chain of S(a (x) b); terms past the width count as -0, which leaves a sum alone
-template <bool FULL>
+template <int W>
 __device__ __forceinline__ float chain16(const u64 (&a)[8], const u64 (&b)[8], const RowLane& r)
 {
     float s = -0.0f;
@@ -153,12 +196,14 @@ __device__ __forceinline__ float chain16(const u64 (&a)[8], const u64 (&b)[8], c
         float p[4];
         unpack2(fmul2_rn(a[2 * k], b[2 * k]), p[0], p[1]);
         unpack2(fmul2_rn(a[2 * k + 1], b[2 * k + 1]), p[2], p[3]);
-        if (!FULL) {
+        if (W == ELEMENTS) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 p[e] = r.at(k) + e < r.D ? p[e] : -0.0f;
         }
-        const float g = fadd_ftz(fadd_ftz(fadd_ftz(p[0], p[1]), p[2]), p[3]);
+        float g = fadd_ftz(fadd_ftz(fadd_ftz(p[0], p[1]), p[2]), p[3]);
+        if (W == GROUPS)
+            g = r.at(k) < r.D ? g : -0.0f;
         s = k == 0 ? g : fadd_ftz(s, g);
     }
     return s;
