@@ -24,7 +24,7 @@ LIB = os.path.join(HERE, "librepro.so")
 SOURCES = ["api.cu", "k_scale.cu", "k_quant.cu", "k_fwd.cu", "k_fwd_tc.cu", "k_bwd.cu", "k_bwd_prefetch.cu", "k_bwd_tma.cu",
            "k_reduce.cu", "k_scale_noalloc.cu", "k_optim.cu", "k_hash.cu", "k_attn_fwd.cu", "k_attn_bwd.cu", "k_selftest.cu",
            "k_embed.cu", "k_qknorm.cu", "k_distill.cu", "k_rowtree.cu",
-           "k_blocknorm.cu", "k_quant_rows.cu", "k_matmul_i8.cu", "k_matmul_few.cu", "k_swiglu.cu"]
+           "k_blocknorm.cu", "k_blocknorm_bwd.cu", "k_quant_rows.cu", "k_matmul_i8.cu", "k_matmul_few.cu", "k_swiglu.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [

@@ -5,7 +5,8 @@
 // and t + 3 TPR, so that neighbouring threads load neighbouring 16 bytes, and the row's sum
 // has the order that these threads can add in: a thread's groups are one chain of S, the
 // tree over the chains is five exchanges inside a warp, one trip through shared memory and
-// up to five exchanges over the warps.
+// up to five exchanges over the warps.  (Half a chain a thread, twice the threads at half the
+// registers: the norm's backward at 16,384 x 2048 took 139 us against 133.)
 #pragma once
 
 #include "elem.cuh"
@@ -14,23 +15,36 @@ namespace repro {
 
 typedef unsigned long long u64;
 
-constexpr int ROW_E = 16;    // elements a thread holds of a row
-
 // threads of a row's group
 inline int row_threads(int64_t D)
 {
     int t = 32;
-    while (ROW_E * (int64_t)t < D)
+    while (16 * (int64_t)t < D)
         t *= 2;
     return t;
 }
 
-// Where a thread stands in its row's group
+// Where a thread stands in its row's group.  What is known when a kernel is compiled becomes offsets of
+// its loads: with TPR read from the arguments the backward took 203 us at 4096 x 8192 instead of 163.
 struct RowLane {
     int t, tpr, D;      // thread in the group, threads of the group, width
+    int threads;        // of the CTA
     int bar;            // named barrier of the group
     __device__ __forceinline__ int at(int k) const { return 4 * (t + k * tpr); }   // first element of group k
 };
+
+// TPR: threads of the row, or 0 where `tpr` says it
+template <int THREADS, int TPR> __device__ __forceinline__ RowLane row_lane(int64_t D, int tpr, int& sub)
+{
+    RowLane r;
+    r.threads = THREADS;
+    r.tpr = TPR == 0 ? tpr : TPR;
+    sub = TPR == THREADS ? 0 : threadIdx.x / r.tpr;
+    r.t = threadIdx.x - sub * r.tpr;
+    r.D = (int)D;
+    r.bar = 1 + sub;
+    return r;
+}
 
 __device__ __forceinline__ void group_barrier(const RowLane& r)
 {
@@ -43,7 +57,7 @@ constexpr int ELEMENTS = 0, GROUPS = 1, WHOLE = 2;
 
 // What lies past D reads as 0.
 template <int W, bool STREAM, typename T>
-__device__ __forceinline__ void load_row16(const T* p, const RowLane& r, u64 (&v)[8])
+__device__ __forceinline__ void load_row(const T* p, const RowLane& r, u64 (&v)[8])
 {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -64,7 +78,7 @@ __device__ __forceinline__ void load_row16(const T* p, const RowLane& r, u64 (&v
 }
 
 template <int W, typename T>
-__device__ __forceinline__ void store_row16(T* p, const RowLane& r, const u64 (&v)[8])
+__device__ __forceinline__ void store_row(T* p, const RowLane& r, const u64 (&v)[8])
 {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -89,7 +103,7 @@ __device__ __forceinline__ void store_row16(T* p, const RowLane& r, const u64 (&
 }
 
 // A thread's share of a row on its way through shared memory: asked for early, taken when it is needed.
-// Each thread copies and reads its own 16 elements only, so no barrier stands between; group k of
+// Each thread copies and reads its own elements only, so no barrier stands between; group k of
 // thread t lies at k threads + t.  piece (ELEMENTS): elements copied at a time, 4, 2 or 1, whatever the
 // rows' boundaries and width allow (a copy has 4 bytes at least).
 template <typename T> struct alignas(4 * sizeof(T)) Four {
@@ -106,13 +120,13 @@ template <int BYTES> __device__ __forceinline__ void copy_async(void* to, const 
 }
 
 template <int W, typename T>
-__device__ __forceinline__ void ask_row16(Four<T>* slot, const T* p, const RowLane& r, int piece)
+__device__ __forceinline__ void ask_row(Four<T>* slot, const T* p, const RowLane& r, int piece)
 {
     constexpr int SZ = (int)sizeof(T);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int d = r.at(k);
-        T* to = slot[k * blockDim.x + threadIdx.x].v;
+        T* to = slot[k * r.threads + threadIdx.x].v;
         if (W != ELEMENTS) {
             if (W == WHOLE || d < r.D)
                 copy_async<4 * SZ>(to, p + d);
@@ -133,13 +147,13 @@ __device__ __forceinline__ void ask_row16(Four<T>* slot, const T* p, const RowLa
     }
 }
 
-template <int W, typename T> __device__ __forceinline__ void take_row16(const Four<T>* slot, const RowLane& r, u64 (&v)[8])
+template <int W, typename T> __device__ __forceinline__ void take_row(const Four<T>* slot, const RowLane& r, u64 (&v)[8])
 {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (W != GROUPS || r.at(k) < r.D)
-            x = load4(slot[k * blockDim.x + threadIdx.x].v);
+            x = load4(slot[k * r.threads + threadIdx.x].v);
         if (W == ELEMENTS) {
             const int left = r.D - r.at(k);
             x.x = left > 0 ? x.x : 0.0f, x.y = left > 1 ? x.y : 0.0f, x.z = left > 2 ? x.z : 0.0f, x.w = left > 3 ? x.w : 0.0f;
@@ -161,7 +175,7 @@ inline int piece_of(const void* p, int64_t ld, int64_t D, int size)
 __device__ __forceinline__ void asked() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT> __device__ __forceinline__ void wait_asked() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
-__device__ __forceinline__ void flush16(u64 (&v)[8])
+__device__ __forceinline__ void flush_row(u64 (&v)[8])
 {
     const u64 z = pack2(-0.0f, -0.0f);
 #pragma unroll
@@ -170,7 +184,7 @@ __device__ __forceinline__ void flush16(u64 (&v)[8])
 }
 
 // v (x) w, flushed (both operands flushed already)
-__device__ __forceinline__ void mul16(u64 (&v)[8], const u64 (&w)[8])
+__device__ __forceinline__ void mul_row(u64 (&v)[8], const u64 (&w)[8])
 {
     const u64 z = pack2(-0.0f, -0.0f);
 #pragma unroll
@@ -178,7 +192,7 @@ __device__ __forceinline__ void mul16(u64 (&v)[8], const u64 (&w)[8])
         v[i] = fadd2_ftz(fmul2_rn(v[i], w[i]), z);
 }
 
-__device__ __forceinline__ void mul16(u64 (&v)[8], float w)
+__device__ __forceinline__ void mul_row(u64 (&v)[8], float w)
 {
     const u64 z = pack2(-0.0f, -0.0f), ww = pack2(w, w);
 #pragma unroll
@@ -188,9 +202,9 @@ __device__ __forceinline__ void mul16(u64 (&v)[8], float w)
 
 // this thread's chain of S(a (x) b); terms past the width count as -0, which leaves a sum alone
 template <int W>
-__device__ __forceinline__ float chain16(const u64 (&a)[8], const u64 (&b)[8], const RowLane& r)
+__device__ __forceinline__ float chain_of(const u64 (&a)[8], const u64 (&b)[8], const RowLane& r)
 {
-    float s = -0.0f;
+    float g[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         float p[4];
@@ -201,12 +215,11 @@ __device__ __forceinline__ float chain16(const u64 (&a)[8], const u64 (&b)[8], c
             for (int e = 0; e < 4; ++e)
                 p[e] = r.at(k) + e < r.D ? p[e] : -0.0f;
         }
-        float g = fadd_ftz(fadd_ftz(fadd_ftz(p[0], p[1]), p[2]), p[3]);
+        g[k] = fadd_ftz(fadd_ftz(fadd_ftz(p[0], p[1]), p[2]), p[3]);
         if (W == GROUPS)
-            g = r.at(k) < r.D ? g : -0.0f;
-        s = k == 0 ? g : fadd_ftz(s, g);
+            g[k] = r.at(k) < r.D ? g[k] : -0.0f;
     }
-    return s;
+    return fadd_ftz(fadd_ftz(fadd_ftz(g[0], g[1]), g[2]), g[3]);
 }
 
 // the tree over the group's chains, the same bits in every thread.  red: 64 floats of the
