@@ -3,7 +3,8 @@
 //   p = (y r1) gain_post, gated; h = x alpha + p beta; u = (h r2) gain_pre, r = 1 / sqrt(mean v^2 + eps)
 //
 // Bound by HBM: x and y in, h and u out (16 bytes an element in fp32).  A row stays in the registers
-// of its threads between its sums (rows.cuh).
+// of its threads between its sums (rows.cuh).  Measured: 16,384 x 2048 fp32 80 us, 6.7 TB/s, floor 79;
+// 4096 x 8192 81 us; 8192 x 4096 bf16 53 us, floor 40.
 #include "blocknorm.cuh"
 
 namespace repro {

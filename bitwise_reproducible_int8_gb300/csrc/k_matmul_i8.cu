@@ -11,7 +11,14 @@
 //     32 KB for 64 terms of K instead of 48 KB, because with one SM a tile of 128 x 256 the operands'
 //     way from L2 bound the product, not the tensor pipe;
 //   * the epilogue has a scale for each of its rows and columns.
-// Products of few tokens are bound by the weights' bytes and run on the CUDA cores (k_mm_rows).
+// Products of few tokens are bound by the weights' bytes: up to 4 on the CUDA cores (k_mm_rows), up to
+// 128 in k_matmul_few.cu.
+//
+// Measured, 16384 x 11264 x 2048 with fp32 results: 485 us, 25 of them the widened copies and 460 the
+// product, which has 394 us of tensor work at cuBLAS's bf16 rate, and 738 MB to store beside it (with
+// bf16 results 429 us); 2048 x 5632 x 16384 with both sides transposed and added on: 284 us, 65 of them
+// the copies.  What bounds it now is the way out: an accumulator is free again only once 16 warps have
+// read it, and their results' stores take L2 from the operands.
 //
 // Roles in a CTA of the pair, as in k_fwd_tc.cu: warp 0 loads, warp 1 of the leading CTA issues the
 // MMAs for both (warp 1 of the other holds its tensor memory), the others are the epilogue.  The
@@ -366,8 +373,7 @@ __device__ __forceinline__ void cluster_sync()
 }
 
 // an arrival on a barrier of either CTA.  What it orders are tensor memory's reads, which the
-// tcgen05 fences around it order; waits and arrivals of cluster scope (this one's release, every
-// wait's acquire) cost the pipeline half of its rate
+// tcgen05 fences around it order
 __device__ __forceinline__ void arrive_at(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -516,9 +522,10 @@ __device__ __forceinline__ Item item_at(const PairArgs& a, int i)
 
 // A warp's 32 rows x EW columns: scaled, added to what is there, stored.  own: the columns' scales,
 // two a lane.  They go through the warp's buffer in blocks of 128 bytes a row (chunk k of row r at
-// k ^ (r mod 8)): rows on 16-byte boundaries by one tensor store a block, others row by row.  (Straight to memory, 4 lanes to a row's line
-// after a turn by shuffles, 16384 x 11264 x 2048 took 87 us longer, although the operands' ring then
-// has two stages more; a lane's own 32 bytes at a time took 41 us longer still.)
+// k ^ (r mod 8)): rows on 16-byte boundaries by one tensor store a block, others row by row (9034 x
+// 9034 x 64 bf16 134 us; 754 by a lane's own row).  (Straight to memory, 4 lanes to a row's line after
+// a turn by shuffles, 16384 x 11264 x 2048 took 46 us longer, although the operands' ring then has two
+// stages more; a lane's own 32 bytes at a time took 34 us longer still.)
 template <typename Y>
 __device__ __forceinline__ void finish(const PairArgs& p, const CUtensorMap* map, const uint32_t (&acc)[EW], uint8_t* stg, int lane,
                                        float sa, const float (&own)[2], int r0, int n)

@@ -7,6 +7,9 @@
 // 8,192 elements is read again, out of L2).  By columns: one pass takes the columns' maxima, the
 // second reads the matrix again from its end, whose last part L2 (129 MB) still holds.  A maximum
 // does not depend on its order, so the columns' may meet in atomics.
+//
+// Measured: 16384 x 5632 fp32 by rows 68 us, 6.8 TB/s, which is its floor; 4099 x 2003 fp32 by columns
+// with a multiplier (rows off 16-byte boundaries, so elements one by one) 23 us against 6 for one pass.
 #include "codes.cuh"
 #include "elem.cuh"
 #include "internal.h"
@@ -74,7 +77,7 @@ constexpr int G = 8;     // groups of 4 a thread holds of a row
 
 // VEC: rows of x and q on 4-element boundaries, whole groups of 4 (and mul on 16 bytes): every load is
 // issued before the first value is looked at.  (With a branch around each load, one was in flight at a
-// time: 198 us against 81 for 16384 x 5632 fp32.)
+// time: 198 us for 16384 x 5632 fp32, 81 without, 68 now with the divisions out of the loop.)
 template <typename T, bool VEC, bool LONG>
 __global__ void __launch_bounds__(256, 4)
 k_quant_tokens(const __grid_constant__ Kernel k)
