@@ -23,26 +23,26 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int GROUP = 128;
-constexpr int RUN = 2;       // groups whose loads a warp has in flight
+constexpr int RUN = 2;       // neighbouring groups of a row a warp takes at a time
 
 struct Kernel {
     SwigluArgs s;
-    int64_t G, items;      // groups of a row, of all rows
-    int64_t rows, groups;  // how far a warp steps: so many rows and groups
+    int64_t G, R, items;   // groups of a row; runs of RUN of them, of a row and of all rows
+    int64_t rows, runs;    // how far a warp steps: so many rows and runs
 };
 
 // four neighbours from element d of F; VEC: on a boundary of 4 elements, F a multiple of 4
-template <bool VEC, typename T> __device__ __forceinline__ void take4(const T* p, int64_t d, int64_t F, bool live, float (&v)[4])
+template <bool VEC, typename T> __device__ __forceinline__ void take4(const T* p, int64_t d, int64_t F, float (&v)[4])
 {
     if (VEC) {
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (live && d < F)
+        if (d < F)
             x = stream4(p + d);
         v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            v[e] = live && d + e < F ? to_f32<T>(p[d + e]) : 0.0f;
+            v[e] = d + e < F ? to_f32<T>(p[d + e]) : 0.0f;
     }
 }
 
@@ -93,65 +93,64 @@ template <bool REST> __device__ __forceinline__ u64 sigmoids(u64 g, u64& rest)
 // scale of 2^-100 or more they are nothing
 __device__ __forceinline__ void keep(const float (&v)[4], int8_t* codes, float* scale, int lane)
 {
-    const float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));   // passes over NaN
-    const unsigned top = __reduce_max_sync(0xffffffffu, m != m ? 0u : __float_as_uint(m));
+    const float m = fmaxf(fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fabsf(v[2])), fabsf(v[3])), 0.0f);   // passes over NaN
+    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
     const CodeScale c = code_scale_of_max(__uint_as_float(top));
     reinterpret_cast<uint32_t*>(codes)[lane] = codes4(v, c);
     if (lane == 0)
         *scale = c.s;
 }
 
-// The groups a warp takes: every so many, without a division for each
+// The runs a warp takes: every so many, without a division for each
 struct Walk {
-    int64_t it, i, gr;   // group of all, row, group of the row
+    int64_t it, i, run;   // run of all, row, run of the row
 
     __device__ __forceinline__ Walk(const Kernel& k)
     {
         it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-        i = it / k.G;
-        gr = it - i * k.G;
+        i = it / k.R;
+        run = it - i * k.R;
     }
     __device__ __forceinline__ void next(const Kernel& k)
     {
         it += (int64_t)gridDim.x * 8;
         i += k.rows;
-        gr += k.groups;
-        if (gr >= k.G) {
-            gr -= k.G;
+        run += k.runs;
+        if (run >= k.R) {
+            run -= k.R;
             ++i;
         }
     }
 };
 
 template <typename T, typename A, bool KEEP, bool VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, KEEP ? 6 : 4)
 k_swiglu_fwd(const __grid_constant__ Kernel k)
 {
     const int lane = threadIdx.x & 31;
     const int64_t F = k.s.F;
     pdl_wait();
     pdl_trigger();
-    for (Walk w(k); w.it < k.items;) {
+    for (Walk w(k); w.it < k.items; w.next(k)) {
+        const int64_t gr = RUN * w.run, d = gr * GROUP + 4 * lane;
+        const T* row = static_cast<const T*>(k.s.gu) + w.i * k.s.gu_ld;
+        A* out = static_cast<A*>(k.s.a) + w.i * k.s.a_ld;
         float g[RUN][4], u[RUN][4];
-        int64_t i[RUN], gr[RUN];
-        bool live[RUN];
 #pragma unroll
         for (int r = 0; r < RUN; ++r) {
-            live[r] = w.it < k.items;
-            i[r] = w.i, gr[r] = w.gr;
-            const T* row = static_cast<const T*>(k.s.gu) + i[r] * k.s.gu_ld;
-            take4<VEC>(row, gr[r] * GROUP + 4 * lane, F, live[r], g[r]);
-            take4<VEC>(row + F, gr[r] * GROUP + 4 * lane, F, live[r], u[r]);
-            w.next(k);
+            take4<VEC>(row, d + r * GROUP, F, g[r]);
+            take4<VEC>(row + F, d + r * GROUP, F, u[r]);
         }
+        const int64_t at = 2 * w.i * k.G + gr;
+        int8_t* const codes = k.s.codes + at * GROUP;
+        float* const scales = k.s.scales + at;
 #pragma unroll
         for (int r = 0; r < RUN; ++r) {
-            if (!live[r])
+            if (r > 0 && gr + r >= k.G)
                 break;
             if (KEEP) {
-                const int64_t at = 2 * i[r] * k.G + gr[r];
-                keep(g[r], k.s.codes + at * GROUP, k.s.scales + at, lane);
-                keep(u[r], k.s.codes + (at + k.G) * GROUP, k.s.scales + at + k.G, lane);
+                keep(g[r], codes + r * GROUP, scales + r, lane);
+                keep(u[r], codes + (k.G + r) * GROUP, scales + k.G + r, lane);
             }
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {   // a subnormal g is flushed with its product, sig being at most 1
@@ -160,7 +159,7 @@ k_swiglu_fwd(const __grid_constant__ Kernel k)
                 const u64 a = mul_flush2(mul_flush2(gg, sigmoids<false>(gg, none)), flush2(pack2(u[r][e], u[r][e + 1])));
                 unpack2(a, g[r][e], g[r][e + 1]);
             }
-            put4<VEC>(static_cast<A*>(k.s.a) + i[r] * k.s.a_ld, gr[r] * GROUP + 4 * lane, F, g[r]);
+            put4<VEC>(out, d + r * GROUP, F, g[r]);
         }
     }
 }
@@ -172,47 +171,43 @@ __device__ __forceinline__ u64 decode(uint32_t c, int e, float s)
 }
 
 template <typename T, typename A, bool KEPT, bool VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
 k_swiglu_bwd(const __grid_constant__ Kernel k)
 {
     const int lane = threadIdx.x & 31;
     const int64_t F = k.s.F;
     pdl_wait();
     pdl_trigger();
-    for (Walk w(k); w.it < k.items;) {
-        float g[RUN][4], u[RUN][4], da[RUN][4], s[RUN][2];
-        uint32_t c[RUN][2];
-        int64_t i[RUN], gr[RUN];
-        bool live[RUN];
+    for (Walk w(k); w.it < k.items; w.next(k)) {
+        const int64_t gr = RUN * w.run, d = gr * GROUP + 4 * lane, at = 2 * w.i * k.G + gr;
+        float g[RUN][4], u[RUN][4], da[RUN][4], sg[RUN], su[RUN];
+        uint32_t cg[RUN], cu[RUN];
+        const A* in = static_cast<const A*>(k.s.da) + w.i * k.s.a_ld;
+        const T* row = static_cast<const T*>(k.s.gu) + w.i * k.s.gu_ld;
+        T* out = static_cast<T*>(k.s.dgu) + w.i * k.s.dgu_ld;
+        const uint32_t* codes = reinterpret_cast<const uint32_t*>(k.s.codes + at * GROUP) + lane;
 #pragma unroll
         for (int r = 0; r < RUN; ++r) {
-            live[r] = w.it < k.items;
-            i[r] = w.i, gr[r] = w.gr;
-            const int64_t d = gr[r] * GROUP + 4 * lane;
-            take4<VEC>(static_cast<const A*>(k.s.da) + i[r] * k.s.a_ld, d, F, live[r], da[r]);
+            take4<VEC>(in, d + r * GROUP, F, da[r]);
             if (KEPT) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t at = (2 * i[r] + h) * k.G + gr[r];
-                    c[r][h] = live[r] ? __ldg(reinterpret_cast<const uint32_t*>(k.s.codes + at * GROUP) + lane) : 0u;
-                    s[r][h] = live[r] ? __ldg(k.s.scales + at) : 0.0f;
-                }
+                const bool live = r == 0 || gr + r < k.G;
+                cg[r] = live ? __ldg(codes + r * (GROUP / 4)) : 0u;
+                cu[r] = live ? __ldg(codes + (k.G + r) * (GROUP / 4)) : 0u;
+                sg[r] = live ? flush(__ldg(k.s.scales + at + r)) : 0.0f;
+                su[r] = live ? flush(__ldg(k.s.scales + at + k.G + r)) : 0.0f;
             } else {
-                const T* row = static_cast<const T*>(k.s.gu) + i[r] * k.s.gu_ld;
-                take4<VEC>(row, d, F, live[r], g[r]);
-                take4<VEC>(row + F, d, F, live[r], u[r]);
+                take4<VEC>(row, d + r * GROUP, F, g[r]);
+                take4<VEC>(row + F, d + r * GROUP, F, u[r]);
             }
-            w.next(k);
         }
 #pragma unroll
         for (int r = 0; r < RUN; ++r) {
-            if (!live[r])
+            if (r > 0 && gr + r >= k.G)
                 break;
-            const float sg = KEPT ? flush(s[r][0]) : 0.0f, su = KEPT ? flush(s[r][1]) : 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-                const u64 gg = KEPT ? decode(c[r][0], e, sg) : flush2(pack2(g[r][e], g[r][e + 1]));
-                const u64 uu = KEPT ? decode(c[r][1], e, su) : flush2(pack2(u[r][e], u[r][e + 1]));
+                const u64 gg = KEPT ? decode(cg[r], e, sg[r]) : flush2(pack2(g[r][e], g[r][e + 1]));
+                const u64 uu = KEPT ? decode(cu[r], e, su[r]) : flush2(pack2(u[r][e], u[r][e + 1]));
                 const u64 x = flush2(pack2(da[r][e], da[r][e + 1]));
                 u64 rest;
                 const u64 sig = sigmoids<true>(gg, rest);
@@ -220,9 +215,8 @@ k_swiglu_bwd(const __grid_constant__ Kernel k)
                 unpack2(mul_flush2(mul_flush2(mul_flush2(x, uu), sig), slope), g[r][e], g[r][e + 1]);
                 unpack2(mul_flush2(x, mul_flush2(gg, sig)), u[r][e], u[r][e + 1]);
             }
-            T* out = static_cast<T*>(k.s.dgu) + i[r] * k.s.dgu_ld;
-            put4<VEC>(out, gr[r] * GROUP + 4 * lane, F, g[r]);
-            put4<VEC>(out + F, gr[r] * GROUP + 4 * lane, F, u[r]);
+            put4<VEC>(out, d + r * GROUP, F, g[r]);
+            put4<VEC>(out + F, d + r * GROUP, F, u[r]);
         }
     }
 }
@@ -239,8 +233,8 @@ template <typename T, typename A> cudaError_t launch(Kernel& k, bool fwd, cudaSt
     const int64_t ctas = (k.items + 7) / 8, most = (int64_t)num_sms() * 32;
     const dim3 grid((unsigned)(ctas < most ? ctas : most));
     const int64_t step = 8 * (int64_t)grid.x;
-    k.rows = step / k.G;
-    k.groups = step - k.rows * k.G;
+    k.rows = step / k.R;
+    k.runs = step - k.rows * k.R;
     count_launches(1);
 #define GO(F) (s.codes ? (vec ? launch_pdl(F<T, A, true, true>, grid, dim3(256), 0, st, k) \
                               : launch_pdl(F<T, A, true, false>, grid, dim3(256), 0, st, k)) \
@@ -255,7 +249,8 @@ cudaError_t dispatch(const SwigluArgs& a, bool fwd, cudaStream_t st)
     Kernel k = {};
     k.s = a;
     k.G = (a.F + GROUP - 1) / GROUP;
-    k.items = a.n * k.G;
+    k.R = (k.G + RUN - 1) / RUN;
+    k.items = a.n * k.R;
     if (a.type == 0)
         return a.a_type == 0 ? launch<float, float>(k, fwd, st) : launch<float, __nv_bfloat16>(k, fwd, st);
     return a.a_type == 0 ? launch<__nv_bfloat16, float>(k, fwd, st) : launch<__nv_bfloat16, __nv_bfloat16>(k, fwd, st);
