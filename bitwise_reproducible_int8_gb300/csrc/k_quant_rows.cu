@@ -4,12 +4,14 @@
 //
 // Bound by HBM: the values in, a byte each out (5 bytes an element from fp32).  By rows: a row stays
 // in its threads' registers between the maximum and the codes (32 elements a thread; what lies past
-// 8,192 elements is read again, out of L2).  By columns: one pass takes the columns' maxima, the
+// 16,384 elements is read again, out of L2).  By columns: one pass takes the columns' maxima, the
 // second reads the matrix again from its end, whose last part L2 (129 MB) still holds.  A maximum
 // does not depend on its order, so the columns' may meet in atomics.
 //
-// Measured: 16384 x 5632 fp32 by rows 68 us, 6.8 TB/s, which is its floor; 4099 x 2003 fp32 by columns
-// with a multiplier (rows off 16-byte boundaries, so elements one by one) 23 us against 6 for one pass.
+// Measured, 16384 x 5632: by rows fp32 67 us, 6.9 TB/s, which is its floor, bf16 54 us (floor 41; issue
+// slots); by columns, where two passes have 122 and 68 us of bytes, fp32 128 us and bf16 104.  4099 x
+// 2003 fp32 by columns with a multiplier (rows off 16-byte boundaries, so elements one by one) 22 us.
+// 16384 x 11264 fp32 by rows 141 us, floor 136 (170 with 256 threads a row and a third of it read again).
 #include "codes.cuh"
 #include "elem.cuh"
 #include "internal.h"
@@ -77,9 +79,9 @@ constexpr int G = 8;     // groups of 4 a thread holds of a row
 
 // VEC: rows of x and q on 4-element boundaries, whole groups of 4 (and mul on 16 bytes): every load is
 // issued before the first value is looked at.  (With a branch around each load, one was in flight at a
-// time: 198 us for 16384 x 5632 fp32, 81 without, 68 now with the divisions out of the loop.)
-template <typename T, bool VEC, bool LONG>
-__global__ void __launch_bounds__(256, 4)
+// time: 198 us for 16384 x 5632 fp32, 81 without.)
+template <typename T, bool VEC, bool LONG, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 k_quant_tokens(const __grid_constant__ Kernel k)
 {
     __shared__ unsigned red[2][16];
@@ -140,10 +142,9 @@ k_quant_tokens(const __grid_constant__ Kernel k)
         unsigned divide = 0;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            bool far;
-            const uint32_t o = codes4_near(v[g], all, far);
+            uint32_t o;
+            divide |= (unsigned)!codes4(v[g], all, o) << g;
             put4<VEC>(q, d0 + g * hop, tpr, D, o);
-            divide |= (unsigned)!far << g;
         }
         // what has to be divided is read once more: kept in registers beside 8 inlined divisions, the
         // values left room for two rows on an SM instead of five
@@ -157,7 +158,10 @@ k_quant_tokens(const __grid_constant__ Kernel k)
             for (int d = d0 + G * hop; d < D; d += hop) {
                 float x[4];
                 again(d, x);
-                put4<VEC>(q, d, tpr, D, codes4(x, c));
+                uint32_t o;
+                if (!codes4(x, all, o))
+                    o = codes4_divided(x, all);
+                put4<VEC>(q, d, tpr, D, o);
             }
         if (t == 0)
             k.a.scales[i] = c.s;
@@ -166,17 +170,19 @@ k_quant_tokens(const __grid_constant__ Kernel k)
 
 constexpr int RUN = 8;   // tokens whose loads a warp has in flight by columns
 
-// four columns of RUN tokens, 8 apart, times their multipliers; 0 past the last
+// four columns of RUN tokens, 8 apart from token i on, times their multipliers; 0 past the last, `rows` of
+// them being there
 template <typename T, bool VEC>
-__device__ __forceinline__ void take_run(const Kernel& k, int64_t i, int64_t hi, int d, float (&v)[RUN][4])
+__device__ __forceinline__ void take_run(const Kernel& k, const T* row, int64_t i, int rows, int d, float (&v)[RUN][4])
 {
-    const T* x = static_cast<const T*>(k.a.x);
+    const int64_t step = 8 * k.a.x_ld;
     float f[RUN];
 #pragma unroll
     for (int u = 0; u < RUN; ++u) {
-        const int64_t r = i + 8 * u;
-        take4<VEC, false>(x + r * k.a.x_ld, d, 32, r < hi ? (int)k.a.D : 0, v[u]);
-        f[u] = k.a.mul && r < hi ? __ldg(k.a.mul + r) : 1.0f;
+        take4<VEC, false>(row, d, 32, u < rows ? (int)k.a.D : 0, v[u]);
+        row += step;
+        if (k.a.mul)
+            f[u] = u < rows ? __ldg(k.a.mul + i + 8 * u) : 1.0f;
     }
     if (k.a.mul)
 #pragma unroll
@@ -199,9 +205,10 @@ k_column_max(const __grid_constant__ Kernel k)
     pdl_wait();
     pdl_trigger();
     float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t i = lo + warp; i < hi; i += 8 * RUN) {
+    const T* row = static_cast<const T*>(k.a.x) + (lo + warp) * k.a.x_ld;
+    for (int64_t i = lo + warp; i < hi; i += 8 * RUN, row += 8 * RUN * k.a.x_ld) {
         float v[RUN][4];
-        take_run<T, VEC>(k, i, hi, d, v);
+        take_run<T, VEC>(k, row, i, (int)((hi - i + 7) >> 3), d, v);
 #pragma unroll
         for (int u = 0; u < RUN; ++u)
 #pragma unroll
@@ -241,28 +248,33 @@ k_quant_columns(const __grid_constant__ Kernel k)
         if (slab == 0 && warp == 0 && col < D)
             k.a.scales[col] = c[e].s;
     }
+    const T* row = static_cast<const T*>(k.a.x) + (lo + warp) * k.a.x_ld;
+    int8_t* out = k.a.q + (lo + warp) * k.a.q_ld;
     for (int64_t i = lo + warp; i < hi; i += 8 * RUN) {
+        const int rows = (int)((hi - i + 7) >> 3);
         float v[RUN][4];
-        take_run<T, VEC>(k, i, hi, d, v);
+        take_run<T, VEC>(k, row, i, rows, d, v);
         unsigned divide = 0;
+        int8_t* to = out;
 #pragma unroll
         for (int u = 0; u < RUN; ++u) {
-            const int64_t r = i + 8 * u;
-            bool far;
-            const uint32_t q = codes4_near(v[u], c, far);
-            put4<VEC>(k.a.q + r * k.a.q_ld, d, 32, r < hi ? D : 0, q);
-            divide |= (unsigned)(!far && r < hi) << u;
+            uint32_t q;
+            divide |= (unsigned)(!codes4(v[u], c, q) && u < rows) << u;
+            put4<VEC>(to, d, 32, u < rows ? D : 0, q);
+            to += 8 * k.a.q_ld;
         }
         for (; divide; divide &= divide - 1) {     // read once more, as by rows
-            const int64_t r = i + 8 * (__ffs(divide) - 1);
+            const int u = __ffs(divide) - 1;
             float x[4];
-            take4<VEC, false>(static_cast<const T*>(k.a.x) + r * k.a.x_ld, d, 32, D, x);
+            take4<VEC, false>(row + 8 * u * k.a.x_ld, d, 32, D, x);
             if (k.a.mul) {
-                const float f = __ldg(k.a.mul + r), all[4] = {f, f, f, f};
+                const float f = __ldg(k.a.mul + i + 8 * u), all[4] = {f, f, f, f};
                 times4(x, all);
             }
-            put4<VEC>(k.a.q + r * k.a.q_ld, d, 32, D, codes4_divided(x, c));
+            put4<VEC>(out + 8 * u * k.a.q_ld, d, 32, D, codes4_divided(x, c));
         }
+        row += 8 * RUN * k.a.x_ld;
+        out += 8 * RUN * k.a.q_ld;
     }
 }
 
@@ -271,16 +283,17 @@ template <typename T> cudaError_t launch(Kernel& k, cudaStream_t st)
     const QuantRowsArgs& a = k.a;
     if (!a.columns) {
         const int64_t want = (a.D + 4 * G * 32 - 1) / (4 * G * 32);   // warps of a row
-        k.tpr = 32 * (int)(want < 8 ? want : 8);
+        k.tpr = 32 * (int)(want < 16 ? want : 16);
         const int threads = k.tpr == 32 ? 128 : k.tpr, per = threads / k.tpr;
         const int64_t ctas = (a.n + per - 1) / per, most = (int64_t)num_sms() * 64;
         count_launches(1);
         const dim3 grid((unsigned)(ctas < most ? ctas : most));
         const bool fits = a.D <= 4 * G * k.tpr;
-        return k.vec ? (fits ? launch_pdl(k_quant_tokens<T, true, false>, grid, dim3(threads), 0, st, k)
-                             : launch_pdl(k_quant_tokens<T, true, true>, grid, dim3(threads), 0, st, k))
-                     : (fits ? launch_pdl(k_quant_tokens<T, false, false>, grid, dim3(threads), 0, st, k)
-                             : launch_pdl(k_quant_tokens<T, false, true>, grid, dim3(threads), 0, st, k));
+#define GO(V, L, N) launch_pdl(k_quant_tokens<T, V, L, N>, grid, dim3(threads), 0, st, k)
+        return threads <= 256 ? (k.vec ? GO(true, false, 256) : GO(false, false, 256))
+               : fits         ? (k.vec ? GO(true, false, 512) : GO(false, false, 512))
+                              : (k.vec ? GO(true, true, 512) : GO(false, true, 512));
+#undef GO
     }
     k.tiles = (int)((a.D + 127) / 128);
     // slabs of a multiple of 64 tokens, about eight CTAs on every SM

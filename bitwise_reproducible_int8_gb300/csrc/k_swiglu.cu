@@ -9,8 +9,8 @@
 // 2.06 of codes and scales; backward 4 + 2.06 in, 8 out) where keeping the inputs themselves would
 // take 20 in the backward.  A warp takes a group of 128 pairs: a lane 4 neighbours of either, the
 // group's scales from two warp-wide maxima.
-// Measured, 16,384 x 5632 fp32: forward 222 us, 5.8 TB/s, backward 212 us, 6.1 TB/s, floor 191 each; the
-// exponential, the reciprocal and the two codes' divisions are what the rest goes to.
+// Measured, 16,384 x 5632 fp32: forward 204 us, 6.4 TB/s, backward 193 us, 6.7 TB/s, floor 191 each.  In
+// bf16 instructions bound it (forward 194 us, 114 without the copy, floors 110 and 82; backward 166).
 #include "codes.cuh"
 #include "elem.cuh"
 #include "expr.cuh"
@@ -89,14 +89,28 @@ template <bool REST> __device__ __forceinline__ u64 sigmoids(u64 g, u64& rest)
     return pack2(up0 ? w0 : s0, up1 ? w1 : s1);
 }
 
-// the group's codes and scale.  Subnormals are not flushed one by one: the maximum is, and beside a
-// scale of 2^-100 or more they are nothing
-__device__ __forceinline__ void keep(const float (&v)[4], int8_t* codes, float* scale, int lane)
+// the largest magnitude of a group.  Subnormals are not flushed one by one: it is, and beside a scale
+// of 2^-100 or more they are nothing
+__device__ __forceinline__ unsigned top_of(const float (&v)[4])
 {
     const float m = fmaxf(fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fabsf(v[2])), fabsf(v[3])), 0.0f);   // passes over NaN
-    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    const CodeScale c = code_scale_of_max(__uint_as_float(top));
-    reinterpret_cast<uint32_t*>(codes)[lane] = codes4(v, c);
+    return __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+}
+
+__device__ __forceinline__ uint32_t codes_of(const float (&v)[4], const CodeScale& c)
+{
+    const CodeScale all[4] = {c, c, c, c};
+    uint32_t q;
+    if (!codes4(v, all, q))
+        q = codes4_divided(v, all);
+    return q;
+}
+
+// codes and scale of a group
+__device__ __forceinline__ void keep(const float (&v)[4], uint32_t* codes, float* scale, int lane)
+{
+    const CodeScale c = code_scale_of_max(__uint_as_float(top_of(v)));
+    *codes = codes_of(v, c);
     if (lane == 0)
         *scale = c.s;
 }
@@ -142,15 +156,15 @@ k_swiglu_fwd(const __grid_constant__ Kernel k)
             take4<VEC>(row + F, d + r * GROUP, F, u[r]);
         }
         const int64_t at = 2 * w.i * k.G + gr;
-        int8_t* const codes = k.s.codes + at * GROUP;
+        uint32_t* const codes = reinterpret_cast<uint32_t*>(k.s.codes + at * GROUP) + lane;
         float* const scales = k.s.scales + at;
 #pragma unroll
         for (int r = 0; r < RUN; ++r) {
             if (r > 0 && gr + r >= k.G)
                 break;
             if (KEEP) {
-                keep(g[r], codes + r * GROUP, scales + r, lane);
-                keep(u[r], codes + (k.G + r) * GROUP, scales + k.G + r, lane);
+                keep(g[r], codes + r * (GROUP / 4), scales + r, lane);
+                keep(u[r], codes + (k.G + r) * (GROUP / 4), scales + k.G + r, lane);
             }
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {   // a subnormal g is flushed with its product, sig being at most 1

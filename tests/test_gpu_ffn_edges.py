@@ -74,6 +74,66 @@ def calls():
     return out
 
 
+def test_codes_near_a_half_s_last_place(orc):
+    """Quotients next to where the rounded one stops being a tie: k + 1/2 +- half a last place.  v = V and
+    s = S as whole numbers leave V 2^24 - S f = n, f = (2 k + 1) 2^(23 - E) +- 1 odd, so each small n has one S;
+    of those, the scales that a maximum by 127 gives."""
+    tops, vals = [], []
+    for k in range(127):
+        E = -1 if k == 0 else (2 * k + 1).bit_length() - 2
+        for sign in (-1, 1):
+            f = (2 * k + 1) * 2 ** (23 - E) + sign
+            inv = pow(f, -1, 1 << 24)
+            for n in range(-40, 41):
+                S = -n * inv % (1 << 24)
+                if S < 1 << 23:
+                    continue
+                s = f32(S * 2.0 ** -23)
+                near = np.spacing(f32(127 * s)) * np.arange(-2, 3, dtype=f32) + f32(127 * s)
+                m = near[near / f32(127) == s]
+                if m.size:
+                    v = f32((k + 0.5 + sign * 2.0 ** (E - 24)) * float(s))
+                    tops.append(m[0])
+                    vals.append(v + np.spacing(v) * np.arange(-3, 4, dtype=f32))
+    x = np.concatenate([f32(tops)[:, None], f32(vals)], 1)
+    x[::2, 1:] *= -1
+    assert x.shape[0] > 5000
+    x *= (2.0 ** rng(1).integers(-30, 31, (x.shape[0], 1))).astype(f32)
+    eq, es = orc.quant_rows(x)
+    for columns in (False, True):
+        t = dev(np.ascontiguousarray(x.T if columns else x))
+        q, s = torch.empty(t.shape, dtype=torch.int8, device="cuda"), torch.empty(x.shape[0], device="cuda")
+        R.repro_quant_rows_i8(t, q, s, columns=columns)
+        same(host(s), es)
+        assert np.array_equal(host(q).T if columns else host(q), eq)
+
+
+def test_codes_of_few_bits(orc):
+    """bf16 values, whose quotients are ties often, by every significand of the maximum; NaN among them."""
+    g = rng(4)
+    top = (1 + np.arange(128) / 128).astype(f32)
+    x = np.concatenate([top[:, None], T.bf((g.random((128, 700)) * top[:, None]).astype(f32))], 1)
+    x[x > top[:, None]] = 0
+    x[5, 9], x[6, 3::7] = np.nan, np.nan
+    for kind in (F32, BF):
+        for a in (x, np.ascontiguousarray(x.T)):
+            for columns in (False, True):
+                t = dev(a).to(kind)
+                q, s = torch.empty(t.shape, dtype=torch.int8, device="cuda"), torch.empty(t.shape[columns], device="cuda")
+                R.repro_quant_rows_i8(t, q, s, columns=columns)
+                eq, es = orc.quant_rows(a, None, columns)
+                same(host(s), es)
+                assert np.array_equal(host(q), eq)
+    gu = np.ascontiguousarray(np.tile(x[:, :512], (1, 2)))
+    codes, scales = torch.empty((128, 2, 4, 128), dtype=torch.int8, device="cuda"), torch.empty((128, 2, 4), device="cuda")
+    a = torch.empty((128, 512), device="cuda")
+    R.repro_swiglu_fwd(dev(gu), a, codes, scales)
+    ea, ec, es = orc.swiglu_fwd(gu)
+    same(host(a), ea)
+    same(host(scales), es)
+    assert np.array_equal(host(codes), ec)
+
+
 NAMES = ["norm_fwd_channel", "norm_fwd_rows", "norm_bwd_channel", "norm_bwd_rows", "quant_0", "quant_1", "matmul_3", "matmul_40",
          "matmul_700", "matmul_300", "matmul_30", "swiglu_fwd", "swiglu_bwd", "swiglu_bwd_kept"]
 
