@@ -7,16 +7,11 @@
 // memory.  A block of 64 terms of a row is 4 threads' 16 bytes; each thread has four blocks on their
 // way at a time, so a CTA keeps 32 KB of weights in flight, and three CTAs (of up to 64 tokens) an SM.
 //
-// Here the codes go in as fp16, which takes 5 instructions for 4 codes (bf16's shorter significand
-// takes 8): u = code + 128 below the bits of 1024, less 1152.  Products and sums are the same integers.
-//
 // Every slice of a tile leaves its int32 sums in the workspace; k_mm_few_join adds them up, exact in
 // any order, and scales them.  (Atomic additions into one sum took 53 us for 128 x 11264 x 2048, the
 // last CTA of a tile adding up its parts 64 us.)  64 x 11264 x 2048 takes 20 us and
 // 16 x 11264 x 2048 13 us; a widened copy of the weights and tiles for 256 tokens 27 us each: five
 // bytes moved for each of the weights, and most of the MMAs on nothing.
-#include <cuda_fp16.h>
-
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
@@ -41,16 +36,6 @@ struct FewArgs {
     int* sums;            // [tile][part][M][128]
     int* err;
 };
-
-// four codes to two words of fp16 pairs, all exact
-__device__ __forceinline__ uint2 widen4_half(uint32_t c)
-{
-    const uint32_t u = c ^ 0x80808080u;
-    const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);   // u, 0x64, u, 0x64
-    const __half2 off = __half2(__float2half_rn(-1152.0f), __float2half_rn(-1152.0f));
-    const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&lo), off), b = __hadd2(*reinterpret_cast<const __half2*>(&hi), off);
-    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
 
 // kind::f16 with fp16 operands, both K-major, fp32 accumulator, M = 128, N = MT
 template <int MT> __device__ __forceinline__ void mma_half(uint32_t dtmem, uint64_t a, uint64_t b, uint32_t acc)
@@ -144,7 +129,7 @@ k_mm_few(const __grid_constant__ FewArgs p)
                 // 16-byte chunks 2 chunk and 2 chunk + 1 of row r, at chunk ^ (r mod 8)
                 uint8_t* to = (i < WR ? A : A + A_BYTES) + r * 128;
                 const uint4 c = v[b % AHEAD][i];
-                const uint2 w0 = widen4_half(c.x), w1 = widen4_half(c.y), w2 = widen4_half(c.z), w3 = widen4_half(c.w);
+                const uint2 w0 = widen4(c.x), w1 = widen4(c.y), w2 = widen4(c.z), w3 = widen4(c.w);
                 *reinterpret_cast<uint4*>(to + 16 * ((2 * chunk) ^ (r & 7))) = make_uint4(w0.x, w0.y, w1.x, w1.y);
                 *reinterpret_cast<uint4*>(to + 16 * ((2 * chunk + 1) ^ (r & 7))) = make_uint4(w2.x, w2.y, w3.x, w3.y);
             }

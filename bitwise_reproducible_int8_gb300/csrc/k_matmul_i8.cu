@@ -3,7 +3,7 @@
 //
 //   y_mn = (i2f(sum_k A(m, k) B(n, k)) (x) s_a[m]) (x) s_b[n], the integer sum exact
 //
-// As in k_fwd_tc.cu the codes go to tcgen05.mma kind::f16 as bf16 (exact), fp32 accumulators over
+// As in k_fwd_tc.cu the codes go to tcgen05.mma kind::f16 (as fp16, exact), fp32 accumulators over
 // slices of 512 terms (integers below 2^23, exact), the slices added up in int32.  What differs:
 //   * the widening pass also transposes (a reduction over tokens has its operands the other way
 //     round) and pads the rows, so any K, stride and layout reaches the tensor cores;
@@ -16,7 +16,7 @@
 //
 // Measured, 16384 x 11264 x 2048 with fp32 results: 485 us, 25 of them the widened copies and 460 the
 // product, which has 394 us of tensor work at cuBLAS's bf16 rate, and 738 MB to store beside it (with
-// bf16 results 429 us); 2048 x 5632 x 16384 with both sides transposed and added on: 284 us, 65 of them
+// bf16 results 429 us); 2048 x 5632 x 16384 with both sides transposed and added on: 281 us, 63 of them
 // the copies.  What bounds it now is the way out: an accumulator is free again only once 16 warps have
 // read it, and their results' stores take L2 from the operands.
 //
@@ -26,7 +26,6 @@
 // accumulator, in both; both epilogues free the accumulator on the leader's barrier.  Every wait is
 // bounded as there.
 #include <cuda.h>
-#include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -45,7 +44,7 @@ namespace {
 
 typedef unsigned long long u64;
 
-// ---------------------------------------------------------------- operands to bf16
+// ---------------------------------------------------------------- operands to fp16
 
 inline int64_t pad8(int64_t k) { return (k + 7) / 8 * 8; }
 inline int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
@@ -53,7 +52,7 @@ inline int64_t align256(int64_t b) { return (b + 255) & ~(int64_t)255; }
 struct Widen {
     const int8_t* q;
     int64_t ld, rows, K, Kp;    // source rows of K (or, transposed, K rows of `rows`); pitch of the copy
-    __nv_bfloat16* out;
+    __half* out;
     const int8_t* end;          // behind the last code
     bool vec;                   // source rows on 8-byte (transposed: 16-byte) boundaries
 };
@@ -78,7 +77,7 @@ __device__ __forceinline__ uint2 codes8(const int8_t* p, int64_t left, const int
     return make_uint2(v[0], v[1]);
 }
 
-// rows of K codes to rows of Kp bf16, zeros behind K; 8 at a time
+// rows of K codes to rows of Kp fp16, zeros behind K; 8 at a time
 __global__ void __launch_bounds__(256)
 k_mm_widen(const __grid_constant__ Widen w)
 {
@@ -108,7 +107,7 @@ k_mm_widen(const __grid_constant__ Widen w)
 // terms of a warp's stores nor the 8 octets of terms of its loads meet in a bank
 __device__ __forceinline__ int tile_word(int k, int c) { return 32 * k + ((c + 4 * (k >> 3) + (k & 3)) & 31); }
 
-// K rows of codes to `rows` rows of Kp bf16, through tiles of 128 terms x 128 rows in shared memory
+// K rows of codes to `rows` rows of Kp fp16, through tiles of 128 terms x 128 rows in shared memory
 __global__ void __launch_bounds__(256)
 k_mm_widen_t(const __grid_constant__ Widen w, int tiles_r)
 {
@@ -177,7 +176,7 @@ k_mm_widen_t(const __grid_constant__ Widen w, int tiles_r)
     }
 }
 
-cudaError_t widen(const int8_t* q, int64_t ld, int64_t rows, int64_t K, bool t, __nv_bfloat16* out, cudaStream_t st)
+cudaError_t widen(const int8_t* q, int64_t ld, int64_t rows, int64_t K, bool t, __half* out, cudaStream_t st)
 {
     const size_t b = t ? 16 : 8;
     Widen w = {q, ld, rows, K, pad8(K), out, q + (t ? (K - 1) * ld + rows : (rows - 1) * ld + K), reinterpret_cast<uintptr_t>(q) % b == 0 && ld % (int64_t)b == 0};
@@ -319,7 +318,7 @@ template <typename Y> cudaError_t run_rows(const MatmulI8Args& g, cudaStream_t s
 
 constexpr int HM = 128;                   // rows of a tile that one CTA of the pair holds
 constexpr int TN = 256;
-constexpr int TK = 64;                    // terms a stage: one 128-byte swizzle row of bf16
+constexpr int TK = 64;                    // terms a stage: one 128-byte swizzle row of fp16
 constexpr int SLICE_KB = 8;               // stages an exact slice: 8 * 64 = 512 terms
 constexpr int STAGES = 5;
 constexpr int HALF_BYTES = HM * TK * 2;   // 16 KB: a CTA's rows of A, and as much of B
@@ -391,8 +390,8 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map,
 
 __device__ __forceinline__ void mma_pair(uint32_t dtmem, uint64_t a, uint64_t b, uint32_t acc)
 {
-    // kind::f16: fp32 accumulator, bf16 A and B, both K-major, M = 256, N = 256
-    constexpr uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(2 * HM >> 4) << 24);
+    // kind::f16: fp32 accumulator, fp16 A and B, both K-major, M = 256, N = 256
+    constexpr uint32_t id = (1u << 4) | ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(2 * HM >> 4) << 24);
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
@@ -908,7 +907,7 @@ bool make_map(CUtensorMap* map, const void* p, CUtensorMapDataType type, int siz
 }
 
 template <typename Y>
-cudaError_t run_pair(const MatmulI8Args& g, const __nv_bfloat16* xa, const __nv_bfloat16* xb, int* parts, cudaStream_t st)
+cudaError_t run_pair(const MatmulI8Args& g, const __half* xa, const __half* xb, int* parts, cudaStream_t st)
 {
     PairArgs p = {};
     p.g = g;
@@ -922,8 +921,8 @@ cudaError_t run_pair(const MatmulI8Args& g, const __nv_bfloat16* xa, const __nv_
     p.y_tma = reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && y_ld * (int64_t)sizeof(Y) % 16 == 0;
     CUtensorMap ma, mb, my;
     memset(&my, 0, sizeof(my));
-    if (!make_map(&ma, xa, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.M, Kp, Kp, HM) ||
-        !make_map(&mb, xb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.N, Kp, Kp, HM) ||
+    if (!make_map(&ma, xa, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, g.M, Kp, Kp, HM) ||
+        !make_map(&mb, xb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, g.N, Kp, Kp, HM) ||
         (p.y_tma && !make_map(&my, g.y, sizeof(Y) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                               (int)sizeof(Y), g.M, g.N, y_ld, 32)))
         return cudaErrorInvalidValue;
@@ -980,8 +979,8 @@ size_t matmul_i8_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_t, bool b_t)
 
 cudaError_t launch_matmul_pair(const MatmulI8Args& g, void* ws, cudaStream_t st)
 {
-    __nv_bfloat16* xa = static_cast<__nv_bfloat16*>(ws);
-    __nv_bfloat16* xb = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(ws) + align256(2 * g.M * pad8(g.K)));
+    __half* xa = static_cast<__half*>(ws);
+    __half* xb = reinterpret_cast<__half*>(static_cast<uint8_t*>(ws) + align256(2 * g.M * pad8(g.K)));
     int* parts = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(xb) + align256(2 * g.N * pad8(g.K)));
     cudaError_t e = widen(g.a, g.a_ld, g.M, g.K, g.a_t, xa, st);
     if (e == cudaSuccess)

@@ -1,26 +1,22 @@
 // mm.cuh -- what the paths of the product of codes share (k_matmul_i8.cu, k_matmul_few.cu): codes to
-// bf16, and sums to outputs.
+// fp16, and sums to outputs.
 #pragma once
 
-#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "elem.cuh"
 
 namespace repro {
 
-// four codes to two words of bf16 pairs: 128 + low seven bits less 128 or 256, all exact
+// four codes to two words of fp16 pairs, all exact, in 5 instructions (bf16's shorter significand takes
+// 8): u = code + 128 below the bits of 1024, less 1152
 __device__ __forceinline__ uint2 widen4(uint32_t c)
 {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t b = __byte_perm(c, 0, i == 0 ? 0x4140 : 0x4342);      // code, 0, code, 0
-        const uint32_t hi = (b & 0x007f007fu) | 0x43004300u, lo = (b & 0x00800080u) | 0x43004300u;
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&hi),
-                                         *reinterpret_cast<const __nv_bfloat162*>(&lo));
-        w[i] = *reinterpret_cast<const uint32_t*>(&d);
-    }
-    return make_uint2(w[0], w[1]);
+    const uint32_t u = c ^ 0x80808080u;
+    const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);   // u, 0x64, u, 0x64
+    const __half2 off = __half2(__float2half_rn(-1152.0f), __float2half_rn(-1152.0f));
+    const __half2 a = __hadd2(*reinterpret_cast<const __half2*>(&lo), off), b = __hadd2(*reinterpret_cast<const __half2*>(&hi), off);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 // what every path ends with
