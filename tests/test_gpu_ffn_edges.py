@@ -1,6 +1,10 @@
 """GPU: the feed-forward calls where their forms meet -- rows on 2-element boundaries, few and many
 tokens of wide rows, calls at once on two streams, captured ones on new inputs, and the debug scan of
 every float input."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -211,3 +215,36 @@ def test_all_at_once():
             for o, w in zip(outs, want[name]):
                 same(host(o), w, name)
     assert R.repro_device_check() == R.REPRO_OK
+
+
+FIRST = """
+import torch, bitwise_reproducible_int8_gb300 as R
+a, b = (torch.randint(-127, 128, s, device="cuda", dtype=torch.int8) for s in ((%d, 700), (260, 700)))
+y, ws = torch.zeros(%d, 260, device="cuda"), torch.empty(R.repro_matmul_i8_ws_bytes(%d, 260, 700), device="cuda", dtype=torch.uint8)
+exact = (a.double() @ b.double().T).float()
+st = torch.cuda.Stream()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=st):
+    R.repro_matmul_i8(a, b, y, ws=ws, stream=st)
+for _ in range(2):
+    y.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        g.replay()
+    st.synchronize()
+    assert torch.equal(y, exact)
+    y2 = torch.zeros_like(y)
+    R.repro_matmul_i8(a, b, y2, ws=ws, stream=st)           # runs the check
+    st.synchronize()
+    assert torch.equal(y2, exact)
+assert R.repro_device_check() == R.REPRO_OK
+"""
+
+
+@pytest.mark.parametrize("M", [40, 300])
+def test_first_product_in_a_capture(M):
+    """A process whose first product is captured: the CUDA cores there, the check with the next eager call."""
+    r = subprocess.run([sys.executable, "-c", FIRST % (M, M, M)], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
