@@ -8,7 +8,7 @@
 namespace repro {
 namespace {
 
-template <int W> __device__ __forceinline__ void gain_row(const float* g, const RowLane& r, u64 (&v)[8])
+template <int W, int G2> __device__ __forceinline__ void gain_row(const float* g, const RowLane& r, u64 (&v)[G2])
 {
     load_row<W, false>(g, r, v);
     flush_row(v);

@@ -18,7 +18,7 @@ __device__ __forceinline__ float rms_of(float S, const NormArgs& a)
 // 64 registers a thread: with 94, five rows of 2048 on an SM instead of eight, 8192 x 4096 fp32 took
 // 93 us against 80.  TPR known: 16,384 x 2048 fp32 80 us against 85, 8192 x 4096 bf16 53 against 57; in
 // fp32 from 4096 on the registers spill with it (4096 x 8192 86 us against 81), so there it is read.
-template <typename T, typename U, int THREADS, int TPR, int W>
+template <typename T, typename U, int THREADS, int TPR, int G, int W>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 k_norm_fwd(const __grid_constant__ NormArgs a)
 {
@@ -29,10 +29,10 @@ k_norm_fwd(const __grid_constant__ NormArgs a)
     const float alpha = flush(a.alpha), beta = flush(a.beta);
     pdl_wait();
     for (int64_t i = (int64_t)blockIdx.x * per + sub; i < a.n; i += (int64_t)gridDim.x * per) {
-        u64 x[8], w[8];
+        u64 x[2 * G], w[2 * G];
         float r1 = 0.0f, r2 = 0.0f;
         if (a.y) {
-            u64 y[8];
+            u64 y[2 * G];
             load_row<W, true>(static_cast<const T*>(a.y) + i * a.y_ld, r, y);
             load_row<W, false>(static_cast<const T*>(a.x) + i * a.x_ld, r, x);
             flush_row(y);
@@ -56,7 +56,7 @@ k_norm_fwd(const __grid_constant__ NormArgs a)
             flush_row(x);
             const u64 al = pack2(alpha, alpha), be = pack2(beta, beta);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 2 * G; ++e) {
                 x[e] = fadd2_ftz(fmul2_rn(x[e], al), fmul2_rn(y[e], be));
                 if (sizeof(T) == 2) {   // the norm reads the stream as it is stored
                     float p, q;
@@ -88,9 +88,12 @@ k_norm_fwd(const __grid_constant__ NormArgs a)
 template <typename T, typename U> cudaError_t launch_fwd(const NormArgs& a, int threads, dim3 grid, cudaStream_t st)
 {
     const int w = check_of(a);
-#define GO(N, TPR) (w == WHOLE    ? launch_pdl(k_norm_fwd<T, U, N, TPR, WHOLE>, grid, dim3(threads), 0, st, a) \
-                    : w == GROUPS ? launch_pdl(k_norm_fwd<T, U, N, TPR, GROUPS>, grid, dim3(threads), 0, st, a) \
-                                  : launch_pdl(k_norm_fwd<T, U, N, TPR, ELEMENTS>, grid, dim3(threads), 0, st, a))
+#define RUN(N, TPR, G, W) launch_pdl(k_norm_fwd<T, U, N, TPR, G, W>, grid, dim3(threads), 0, st, a)
+#define GO(N, TPR) (w == WHOLE ? RUN(N, TPR, 4, WHOLE) : w == GROUPS ? RUN(N, TPR, 4, GROUPS) : RUN(N, TPR, 4, ELEMENTS))
+    if (a.D <= 128)
+        return w != ELEMENTS ? RUN(128, 32, 1, GROUPS) : RUN(128, 32, 1, ELEMENTS);
+    if (a.D <= 256)
+        return w != ELEMENTS ? RUN(128, 32, 2, GROUPS) : RUN(128, 32, 2, ELEMENTS);
     constexpr bool KNOWN = sizeof(T) == 2;
     return a.tpr < 128      ? GO(128, 0)
            : threads == 128 ? GO(128, 128)
@@ -98,6 +101,7 @@ template <typename T, typename U> cudaError_t launch_fwd(const NormArgs& a, int 
            : threads == 512 ? GO(512, (KNOWN ? 512 : 0))
                             : GO(1024, (KNOWN ? 1024 : 0));
 #undef GO
+#undef RUN
 }
 
 } // namespace

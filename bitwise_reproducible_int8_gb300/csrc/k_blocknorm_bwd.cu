@@ -22,30 +22,30 @@ namespace {
 constexpr int CHUNK = 8;        // tokens of a chunk of the sums over tokens: REPRO_NORM_CHUNK
 
 // v <- scale (x) (v (-) (unit (x) c)), c = S(v (x) unit) (/) D
-template <int W>
-__device__ __forceinline__ void norm_back(u64 (&v)[8], const u64 (&unit)[8], float scale, const NormArgs& a,
+template <int W, int G2>
+__device__ __forceinline__ void norm_back(u64 (&v)[G2], const u64 (&unit)[G2], float scale, const NormArgs& a,
                                           const RowLane& r, float* red, int& phase)
 {
     const float c = mean_of(tree_of_chains(chain_of<W>(v, unit, r), r, red, phase), (float)a.D, a.inv);
     const u64 cc = pack2(-c, -c), sc = pack2(scale, scale), z = pack2(-0.0f, -0.0f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < G2; ++e)
         v[e] = fadd2_ftz(fmul2_rn(sc, fadd2_ftz(v[e], fmul2_rn(unit[e], cc))), z);
 }
 
 // s (+) a (x) b
-__device__ __forceinline__ void column_sum(u64 (&s)[8], const u64 (&a)[8], const u64 (&b)[8])
+template <int G2> __device__ __forceinline__ void column_sum(u64 (&s)[G2], const u64 (&a)[G2], const u64 (&b)[G2])
 {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < G2; ++e)
         s[e] = fadd2_ftz(fmul2_rn(a[e], b[e]), s[e]);
 }
 
-template <int W>
-__device__ __forceinline__ void store_parts(float* parts, int64_t chunk, int64_t pitch, const RowLane& r, const u64 (&s)[8])
+template <int W, int G2>
+__device__ __forceinline__ void store_parts(float* parts, int64_t chunk, int64_t pitch, const RowLane& r, const u64 (&s)[G2])
 {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < G2 / 2; ++k) {
         const int d = r.at(k);
         float4 v;
         unpack2(s[2 * k], v.x, v.y);
@@ -59,7 +59,7 @@ __device__ __forceinline__ void store_parts(float* parts, int64_t chunk, int64_t
 // row of each stream on its way for every group on an SM); else loads where values are needed.
 // CHANNEL: a gate that is one row, whose sums take 16 more registers.  Three groups of 128 threads an
 // SM at 168 registers; with four at 128 the kernel spills.
-template <typename T, int THREADS, int TPR, bool AHEAD, int W, bool CHANNEL>
+template <typename T, int THREADS, int TPR, int G, bool AHEAD, int W, bool CHANNEL>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 384 / THREADS : 1)
 k_norm_bwd(const __grid_constant__ NormArgs a)
 {
@@ -70,7 +70,7 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
     const int per = THREADS / r.tpr;
     const float alpha = flush(a.alpha), beta = flush(a.beta);
     // slots of du, h, dh, y and the gate's rows
-    const size_t st = 4 * sizeof(Four<T>) * THREADS;
+    const size_t st = G * sizeof(Four<T>) * THREADS;
     Four<T>* const s_h = reinterpret_cast<Four<T>*>(slots);
     Four<T>* const s_dh = reinterpret_cast<Four<T>*>(slots + st);
     Four<T>* const s_y = reinterpret_cast<Four<T>*>(slots + 2 * st);
@@ -81,30 +81,30 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
     auto ask_norm = [&](int64_t i) {      // what the norm before the block needs of token i
         if (a.du) {
             if (a.u_type == 0)
-                ask_row<W>(static_cast<Four<float>*>(s_du), static_cast<const float*>(a.du) + i * a.du_ld, r, a.piece_u);
+                ask_row<W, G>(static_cast<Four<float>*>(s_du), static_cast<const float*>(a.du) + i * a.du_ld, r, a.piece_u);
             else
-                ask_row<W>(static_cast<Four<__nv_bfloat16>*>(s_du), static_cast<const __nv_bfloat16*>(a.du) + i * a.du_ld, r, a.piece_u);
-            ask_row<W>(s_h, row_t(a.hs, a.hs_ld, i), r, a.piece);
+                ask_row<W, G>(static_cast<Four<__nv_bfloat16>*>(s_du), static_cast<const __nv_bfloat16*>(a.du) + i * a.du_ld, r, a.piece_u);
+            ask_row<W, G>(s_h, row_t(a.hs, a.hs_ld, i), r, a.piece);
         }
         asked();
     };
     auto ask_rest = [&](int64_t i) {
         if (a.dh)
-            ask_row<W>(s_dh, row_t(a.dh, a.dh_ld, i), r, a.piece);
+            ask_row<W, G>(s_dh, row_t(a.dh, a.dh_ld, i), r, a.piece);
         if (a.y)
-            ask_row<W>(s_y, row_t(a.y, a.y_ld, i), r, a.piece);
+            ask_row<W, G>(s_y, row_t(a.y, a.y_ld, i), r, a.piece);
         if (gates)
-            ask_row<W>(s_gate, row_t(a.gate, a.gate_ld, i), r, a.piece);
+            ask_row<W, G>(s_gate, row_t(a.gate, a.gate_ld, i), r, a.piece);
         asked();
     };
     pdl_wait();
     pdl_trigger();
     const int64_t chunks = (a.n + a.chunk - 1) / a.chunk;
     for (int64_t ch = (int64_t)blockIdx.x * per + sub; ch < chunks; ch += (int64_t)gridDim.x * per) {
-        u64 s_pre[8], s_post[8], s_chan[8];
+        u64 s_pre[2 * G], s_post[2 * G], s_chan[2 * G];
         const int64_t lo = ch * a.chunk, hi = lo + a.chunk < a.n ? lo + a.chunk : a.n;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)   // -0 (+) v is v
+        for (int e = 0; e < 2 * G; ++e)   // -0 (+) v is v
             s_pre[e] = s_post[e] = s_chan[e] = pack2(-0.0f, -0.0f);
         if (AHEAD) {
             ask_norm(lo);
@@ -117,7 +117,7 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
                 next1 = __ldg(a.stats + 2 * (i + 1));
                 next2 = __ldg(a.stats + 2 * (i + 1) + 1);
             }
-            u64 g[8], v[8], unit[8], w[8];
+            u64 g[2 * G], v[2 * G], unit[2 * G], w[2 * G];
             if (AHEAD)
                 wait_asked<1>();
             if (a.du) {
@@ -162,11 +162,11 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
                 flush_row(g);
                 if (a.du)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < 2 * G; ++e)
                         g[e] = fadd2_ftz(g[e], v[e]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < 2 * G; ++e)
                     g[e] = v[e];
             }
             if (!a.y) {
@@ -180,7 +180,7 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
                 continue;
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 2 * G; ++e)
                 v[e] = g[e];
             mul_row(v, alpha);
             store_row<W>(static_cast<T*>(a.dx) + i * a.dx_ld, r, v);
@@ -207,10 +207,10 @@ k_norm_bwd(const __grid_constant__ NormArgs a)
                 mul_row(unit, r1);
             if (CHANNEL || gates) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < 2 * G; ++e)
                     v[e] = unit[e];
                 if (a.post && a.gain_post) {
-                    u64 gp[8];
+                    u64 gp[2 * G];
                     gain_row<W>(a.gain_post, r, gp);
                     mul_row(v, gp);
                 }
@@ -301,10 +301,10 @@ void set_pieces(NormArgs& a)
     a.piece_u = a.du ? piece_of(a.du, a.du_ld, a.D, u) : 4;
 }
 
-template <typename T, int N, int TPR, bool AHEAD, int W> cudaError_t run_bwd(const NormArgs& a, dim3 grid, cudaStream_t st)
+template <typename T, int N, int TPR, int G, bool AHEAD, int W> cudaError_t run_bwd(const NormArgs& a, dim3 grid, cudaStream_t st)
 {
-    const auto k = a.gate && !a.gate_rows ? k_norm_bwd<T, N, TPR, AHEAD, W, true> : k_norm_bwd<T, N, TPR, AHEAD, W, false>;
-    const size_t smem = AHEAD ? (size_t)N * 16 * ((a.gate_rows ? 4 : 3) * sizeof(T) + (a.u_type == 0 ? 4 : 2)) : 0;
+    const auto k = a.gate && !a.gate_rows ? k_norm_bwd<T, N, TPR, G, AHEAD, W, true> : k_norm_bwd<T, N, TPR, G, AHEAD, W, false>;
+    const size_t smem = AHEAD ? (size_t)N * 4 * G * ((a.gate_rows ? 4 : 3) * sizeof(T) + (a.u_type == 0 ? 4 : 2)) : 0;
     if (smem > 40 * 1024) {   // static shared memory counts too
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess)
@@ -313,25 +313,29 @@ template <typename T, int N, int TPR, bool AHEAD, int W> cudaError_t run_bwd(con
     return launch_pdl(k, grid, dim3(N), smem, st, a);
 }
 
-template <typename T, int N, int TPR> cudaError_t pick_bwd(const NormArgs& a, dim3 grid, cudaStream_t st)
+template <typename T, int N, int TPR, int G = 4> cudaError_t pick_bwd(const NormArgs& a, dim3 grid, cudaStream_t st)
 {
     if (a.piece == 0 || a.piece_u == 0)
-        return run_bwd<T, N, TPR, false, ELEMENTS>(a, grid, st);
+        return run_bwd<T, N, TPR, G, false, ELEMENTS>(a, grid, st);
     const int w = check_of(a);
-    return w == WHOLE ? run_bwd<T, N, TPR, true, WHOLE>(a, grid, st) : w == GROUPS ? run_bwd<T, N, TPR, true, GROUPS>(a, grid, st)
-                                                                              : run_bwd<T, N, TPR, true, ELEMENTS>(a, grid, st);
+    if (G < 4)
+        return w != ELEMENTS ? run_bwd<T, N, TPR, G, true, GROUPS>(a, grid, st) : run_bwd<T, N, TPR, G, true, ELEMENTS>(a, grid, st);
+    return w == WHOLE ? run_bwd<T, N, TPR, 4, true, WHOLE>(a, grid, st) : w == GROUPS ? run_bwd<T, N, TPR, G, true, GROUPS>(a, grid, st)
+                                                                              : run_bwd<T, N, TPR, G, true, ELEMENTS>(a, grid, st);
 }
 
 template <typename T> cudaError_t launch_bwd(NormArgs& a, int64_t items, cudaStream_t st)
 {
     int threads;
     const dim3 grid = grid_of(a, items, threads);
-    return a.tpr < 128      ? pick_bwd<T, 128, 0>(a, grid, st)
+    return a.D <= 128       ? pick_bwd<T, 128, 32, 1>(a, grid, st)
+           : a.D <= 256     ? pick_bwd<T, 128, 32, 2>(a, grid, st)
+           : a.tpr < 128    ? pick_bwd<T, 128, 0>(a, grid, st)
            : threads == 128 ? pick_bwd<T, 128, 128>(a, grid, st)
            : threads == 256 ? pick_bwd<T, 256, 256>(a, grid, st)
            : threads == 512 ? pick_bwd<T, 512, 512>(a, grid, st)
-           : check_of(a) == ELEMENTS ? run_bwd<T, 1024, 1024, false, ELEMENTS>(a, grid, st)   // the slots of 1,024 threads would not fit
-                                     : run_bwd<T, 1024, 1024, false, GROUPS>(a, grid, st);
+           : check_of(a) == ELEMENTS ? run_bwd<T, 1024, 1024, 4, false, ELEMENTS>(a, grid, st)   // the slots of 1,024 threads would not fit
+                                     : run_bwd<T, 1024, 1024, 4, false, GROUPS>(a, grid, st);
 }
 
 } // namespace

@@ -31,6 +31,16 @@ def test_block_norm_on_pairs(orc, monkeypatch, n, D, layout, gate, post, kind, u
     T.norm_check(orc, n, D, gate, post, True, "pairs", kind, u_kind)
 
 
+# rows that leave a thread one or two groups of 4, by tokens and by chunks
+@pytest.mark.parametrize("n,D", [(7, 124), (7, 129), (7, 252), (7, 257), (17000, 128), (17000, 126), (9000, 256), (9000, 255), (9000, 136)])
+@pytest.mark.parametrize("layout", [(0, 0), (3, 1)])
+@pytest.mark.parametrize("gate,post", [(None, True), ("channel", True), ("token", False)])
+@pytest.mark.parametrize("kind,u_kind", [(F32, F32), (BF, BF)])
+def test_block_norm_narrow(orc, monkeypatch, n, D, layout, gate, post, kind, u_kind):
+    monkeypatch.setitem(T.LAYOUTS, "narrow", layout)
+    T.norm_check(orc, n, D, gate, post, True, "narrow", kind, u_kind)
+
+
 def calls():
     """name -> (call, its float inputs, its outputs)."""
     g = torch.Generator(device="cuda").manual_seed(3)
