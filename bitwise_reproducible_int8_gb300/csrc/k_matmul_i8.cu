@@ -11,8 +11,8 @@
 //     32 KB for 64 terms of K instead of 48 KB, because with one SM a tile of 128 x 256 the operands'
 //     way from L2 bound the product, not the tensor pipe;
 //   * the epilogue has a scale for each of its rows and columns.
-// Products of few tokens are bound by the weights' bytes: up to 4 on the CUDA cores (k_mm_rows), up to
-// 128 in k_matmul_few.cu.
+// Products of few tokens are bound by the weights' bytes: up to 4 on the CUDA cores (k_mm_rows, k_mm_cols),
+// up to 128 in k_matmul_few.cu.
 //
 // Measured, 16384 x 11264 x 2048 with fp32 results: 485 us, 25 of them the widened copies and 460 the
 // product, which has 394 us of tensor work at cuBLAS's bf16 rate, and 738 MB to store beside it (with
@@ -312,6 +312,133 @@ template <typename Y> cudaError_t run_rows(const MatmulI8Args& g, cudaStream_t s
                    : launch_pdl(k_mm_rows<Y, 1, false>, grid, dim3(128), 0, st, g);
     return vec ? launch_pdl(k_mm_rows<Y, RM, true>, grid, dim3(128), 0, st, g)
                : launch_pdl(k_mm_rows<Y, RM, false>, grid, dim3(128), 0, st, g);
+}
+
+// The same against b = [K][N].  A CTA takes 512 columns of B (16 a lane) and a slab of its rows, 4 rows a
+// warp at a time: 4 x 4 codes are turned in registers and go to dp4a with 4 codes of each of the R rows
+// of A.  The warps' sums meet in shared memory, the slabs' in the workspace (exact in any order).
+// 1 x 4096 x 4096 8 us, 4 x 2048 x 5632 13 us; the widened copies and a tile for 256 tokens take 26.
+constexpr int CN = 512;          // columns of a CTA
+
+template <int R>
+__global__ void __launch_bounds__(256, 2)
+k_mm_cols(const __grid_constant__ MatmulI8Args g, int* sums, int slab, int slabs)
+{
+    __shared__ int red[8][CN];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t n0 = (int64_t)(blockIdx.x / slabs) * CN, n = n0 + 16 * lane;
+    const int part = blockIdx.x % slabs;
+    const int64_t lo = (int64_t)part * slab, hi = lo + slab < g.K ? lo + slab : g.K;
+    pdl_wait();
+    pdl_trigger();
+    const bool words = reinterpret_cast<uintptr_t>(g.a) % 4 == 0 && (g.M == 1 || g.a_ld % 4 == 0);   // slabs start on 32
+    int acc[R][16] = {};
+#pragma unroll 2
+    for (int64_t k = lo + 4 * warp; k < hi; k += 32) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (k + i < hi && n < g.N)   // N is a multiple of 16
+                v[i] = __ldg(reinterpret_cast<const uint4*>(g.b + (k + i) * g.b_ld + n));
+        }
+        int a[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint32_t w = 0;
+            const int8_t* p = g.a + r * g.a_ld + k;
+            if (r < g.M) {
+                if (words && k + 4 <= hi) {
+                    w = __ldg(reinterpret_cast<const uint32_t*>(p));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (k + i < hi)
+                            w |= (uint32_t)(uint8_t)__ldg(p + i) << (8 * i);
+                }
+            }
+            a[r] = (int)w;
+        }
+        const uint32_t in[4][4] = {{v[0].x, v[1].x, v[2].x, v[3].x}, {v[0].y, v[1].y, v[2].y, v[3].y},
+                                   {v[0].z, v[1].z, v[2].z, v[3].z}, {v[0].w, v[1].w, v[2].w, v[3].w}};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {   // 4 x 4 bytes transposed
+            const uint32_t p = __byte_perm(in[c][0], in[c][1], 0x5140), q = __byte_perm(in[c][0], in[c][1], 0x7362);
+            const uint32_t x = __byte_perm(in[c][2], in[c][3], 0x5140), y = __byte_perm(in[c][2], in[c][3], 0x7362);
+            const uint32_t t[4] = {__byte_perm(p, x, 0x5410), __byte_perm(p, x, 0x7632), __byte_perm(q, y, 0x5410),
+                                   __byte_perm(q, y, 0x7632)};
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[r][4 * c + e] = __dp4a((int)t[e], a[r], acc[r][4 * c + e]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (r >= g.M)
+            break;
+        if (r > 0)
+            __syncthreads();
+#pragma unroll
+        for (int c = 0; c < 16; c += 4)
+            *reinterpret_cast<int4*>(&red[warp][16 * lane + c]) = make_int4(acc[r][c], acc[r][c + 1], acc[r][c + 2], acc[r][c + 3]);
+        __syncthreads();
+        for (int c = threadIdx.x; c < CN; c += 256) {
+            int s = 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+                s += red[w][c];
+            if (n0 + c < g.N)
+                sums[((int64_t)part * g.M + r) * g.N + n0 + c] = s;
+        }
+    }
+}
+
+template <typename Y>
+__global__ void __launch_bounds__(128)
+k_mm_cols_join(const __grid_constant__ MatmulI8Args g, const int* sums, int slabs)
+{
+    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x, m = i / g.N, n = i - m * g.N;
+    pdl_wait();
+    if (i >= g.M * g.N)
+        return;
+    int s = 0;
+#pragma unroll 16
+    for (int k = 0; k < slabs; ++k)
+        s += __ldcg(sums + (int64_t)k * g.M * g.N + i);
+    put(static_cast<Y*>(g.y) + m * g.y_ld + n,
+        scaled(s, g.s_a, g.s_a ? flush(__ldg(g.s_a + m)) : 0.0f, g.s_b, g.s_b ? flush(__ldg(g.s_b + n)) : 0.0f), g.accumulate);
+}
+
+// rows of a slab: two CTAs on every SM, but 32 rows at least and 16 slabs at most, which one thread's
+// loads can have in flight when it adds them up (with 32, 1 x 4096 x 4096 took 9.6 us).  152 SMs,
+// whatever the device: the workspace's size depends on it
+int cols_slab(int64_t N, int64_t K)
+{
+    const int64_t tiles = (N + CN - 1) / CN, want = std::min<int64_t>(std::max<int64_t>(2 * 152 / tiles, 1), 16);
+    return (int)(((K + want - 1) / want + 31) / 32 * 32);
+}
+
+bool cols_of(int64_t M, int64_t K, bool a_t, bool b_t) { return M <= 4 && !a_t && b_t && K > 0; }
+
+size_t cols_ws_bytes(int64_t M, int64_t N, int64_t K)
+{
+    const int slab = cols_slab(N, K);
+    return (size_t)((K + slab - 1) / slab * M * N * 4);
+}
+
+cudaError_t run_cols(const MatmulI8Args& g, int* sums, cudaStream_t st)
+{
+    const int slab = cols_slab(g.N, g.K), slabs = (int)((g.K + slab - 1) / slab);
+    const dim3 grid((unsigned)((g.N + CN - 1) / CN * slabs)), join((unsigned)((g.M * g.N + 127) / 128));
+    count_launches(2);
+    cudaError_t e = g.M == 1 ? launch_pdl(k_mm_cols<1>, grid, dim3(256), 0, st, g, sums, slab, slabs)
+                             : launch_pdl(k_mm_cols<4>, grid, dim3(256), 0, st, g, sums, slab, slabs);
+    if (e == cudaSuccess)
+        e = g.y_type == 0 ? launch_pdl(k_mm_cols_join<float>, join, dim3(128), 0, st, g, static_cast<const int*>(sums), slabs)
+                          : launch_pdl(k_mm_cols_join<__nv_bfloat16>, join, dim3(128), 0, st, g, static_cast<const int*>(sums), slabs);
+    return e;
 }
 
 // ---------------------------------------------------------------- tensor cores, two SMs a tile
@@ -966,7 +1093,7 @@ bool aligned16(const MatmulI8Args& g)
 // weights widened on their way (k_matmul_few.cu: 5 tokens 12 us, 16 tokens 13, 64 tokens 20, 128 tokens
 // 30, or 18 for N 2048 and K 5632); else a widened copy and pairs of SMs (27 us up to 256 tokens, 23 for
 // N 2048, K 5632).  The CUDA cores also take up to 16 tokens where the tensor cores may not be used or
-// rows are not aligned.
+// rows are not aligned, and up to 4 by transposed weights (k_mm_cols).
 bool small_of(int64_t M, bool a_t, bool b_t) { return M <= 16 && !a_t && !b_t; }
 bool few_of(int64_t M, int64_t K, bool a_t, bool b_t) { return M > 4 && M <= 128 && !a_t && !b_t && K % 16 == 0 && K > 0; }
 
@@ -982,7 +1109,8 @@ size_t pair_ws_bytes(int64_t M, int64_t N, int64_t K)
 size_t matmul_i8_ws_bytes(int64_t M, int64_t N, int64_t K, bool a_t, bool b_t)
 {
     const size_t few = few_of(M, K, a_t, b_t) ? std::max<size_t>(matmul_few_ws_bytes(M, N, K), 16) : 0;
-    return small_of(M, a_t, b_t) ? few : std::max(few, pair_ws_bytes(M, N, K));
+    const size_t cols = cols_of(M, K, a_t, b_t) ? cols_ws_bytes(M, N, K) : 0;
+    return small_of(M, a_t, b_t) ? few : std::max({few, cols, pair_ws_bytes(M, N, K)});
 }
 
 cudaError_t launch_matmul_pair(const MatmulI8Args& g, void* ws, cudaStream_t st)
@@ -1004,6 +1132,9 @@ cudaError_t launch_matmul_i8(const MatmulI8Args& g, void* ws, bool tc, cudaStrea
         return launch_matmul_few(g, ws, st);
     if (small_of(g.M, g.a_t, g.b_t) && g.K > 0)
         return g.y_type == 0 ? run_rows<float>(g, st) : run_rows<__nv_bfloat16>(g, st);
+    if (cols_of(g.M, g.K, g.a_t, g.b_t) && reinterpret_cast<uintptr_t>(g.b) % 16 == 0 && g.N % 16 == 0 &&
+        (g.K == 1 || g.b_ld % 16 == 0))
+        return run_cols(g, static_cast<int*>(ws), st);
     if (!tc || g.K == 0)
         return g.y_type == 0 ? run_any<float>(g, st) : run_any<__nv_bfloat16>(g, st);
     return launch_matmul_pair(g, ws, st);

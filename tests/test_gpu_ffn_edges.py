@@ -258,3 +258,17 @@ def test_first_product_in_a_capture(M):
     r = subprocess.run([sys.executable, "-c", FIRST % (M, M, M)], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("M", [1, 2, 4, 5])
+@pytest.mark.parametrize("N,K", [(16, 1), (16, 3), (512, 31), (528, 33), (1040, 700), (2048, 5632), (11264, 130), (48, 133144)])
+@pytest.mark.parametrize("path", [0, -1])
+def test_few_tokens_by_transposed_weights(orc, M, N, K, path):
+    R.repro_set_launch_cfg(fwd_path=path)
+    try:
+        T.mm_check(orc, M, N, K, False, True)
+        T.mm_check(orc, M, N, K, False, True, "strided", F32, True)
+        T.mm_check(orc, M, N, K, False, True, "dense", BF, scales=False)
+    finally:
+        R.repro_set_launch_cfg(reset=True)
+    assert R.repro_device_check() == R.REPRO_OK
