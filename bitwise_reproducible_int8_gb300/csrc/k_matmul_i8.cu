@@ -567,6 +567,7 @@ __device__ __forceinline__ void store_block(const CUtensorMap* map, const void* 
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
+// p: on 32 bytes.  (Two stores of 16: 256 x 256 x 16384 27.0 us against 23.6, 1024 x 1024 x 16384 61 against 56)
 __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8])
 {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -602,13 +603,14 @@ Plan plan_of(int64_t M, int64_t N, int64_t K)
 }
 
 constexpr int64_t PART_BYTES = 2 * HM * TN * 4;
+constexpr int64_t PART_ALIGN = 32;     // of the cut tiles' sums, in a workspace that starts on 16
 
 struct PairArgs {
     MatmulI8Args g;
     Plan p;
     int K;
     bool y_tma;          // rows of y on 16-byte boundaries
-    int* parts;          // the cut tiles' sums, [part][256][256]
+    int* parts;          // the cut tiles' sums, [part][256][256], on a 32-byte boundary
     int* err;
 };
 
@@ -1101,7 +1103,7 @@ size_t pair_ws_bytes(int64_t M, int64_t N, int64_t K)
 {
     const Plan p = plan_of(M, N, K);
     const int64_t parts = p.split > 1 ? p.items - p.whole : 0;
-    return (size_t)(align256(2 * M * pad8(K)) + align256(2 * N * pad8(K)) + parts * PART_BYTES);
+    return (size_t)(align256(2 * M * pad8(K)) + align256(2 * N * pad8(K)) + (parts > 0 ? parts * PART_BYTES + PART_ALIGN - 16 : 0));
 }
 
 } // namespace
@@ -1117,7 +1119,8 @@ cudaError_t launch_matmul_pair(const MatmulI8Args& g, void* ws, cudaStream_t st)
 {
     __half* xa = static_cast<__half*>(ws);
     __half* xb = reinterpret_cast<__half*>(static_cast<uint8_t*>(ws) + align256(2 * g.M * pad8(g.K)));
-    int* parts = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(xb) + align256(2 * g.N * pad8(g.K)));
+    const uintptr_t behind = reinterpret_cast<uintptr_t>(xb) + align256(2 * g.N * pad8(g.K));
+    int* parts = reinterpret_cast<int*>((behind + PART_ALIGN - 1) / PART_ALIGN * PART_ALIGN);
     cudaError_t e = widen(g.a, g.a_ld, g.M, g.K, g.a_t, xa, st);
     if (e == cudaSuccess)
         e = widen(g.b, g.b_ld, g.N, g.K, g.b_t, xb, st);
