@@ -842,6 +842,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
                     s = 0, ph ^= 1;
             }
         }
+        const int s1 = s, ph1 = ph;
         // the leader sees both CTAs' last copies land before either can exit (cluster_sync below):
         // of the last `filled` stages, the newest first
         if (rank == 0)
@@ -851,6 +852,14 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
                 if (!mbar_wait(&sm->full[s], (uint32_t)(ph ^ 1)))
                     ok = false;
             }
+        // and either CTA the arrivals of its own stages' last products, which come from the leader's
+        // tensor core: none may be on its way into a CTA that has exited
+        s = s1, ph = ph1;
+        for (int k = 0; k < STAGES && ok; ++k) {
+            ok = mbar_wait(&sm->empty[s], (uint32_t)ph);
+            if (++s == STAGES)
+                s = 0, ph ^= 1;
+        }
         if (!ok && lane == 0)
             sm->failed = 1;
     } else if (warp == 1) {
@@ -885,12 +894,9 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
                         d = 0, dph ^= 1;
                 }
             }
-            // every MMA issued here has completed once `done` fires (in both CTAs)
             if (elect_one())
                 commit_pair(&sm->done);
             __syncwarp();
-            if (!mbar_wait(&sm->done, 0))
-                ok = false;
             if (!ok && lane == 0)
                 sm->failed = 1;
         }
@@ -977,6 +983,13 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
     __syncwarp();
     fence_before();
     __syncthreads();
+    // `done` arrives in both CTAs, by itself in each, once every MMA has completed: each waits for its own
+    // (here, behind all other waits, where it is on its way already, so that the limit fits any product)
+    if (warp == 1) {
+        if (!mbar_wait(&sm->done, 0) && lane == 0)
+            sm->failed = 1;
+        __syncwarp();
+    }
     cluster_sync();   // no barrier, tile or tensor memory of either CTA is used past here
     if (warp == 1) {
         fence_after();
