@@ -120,7 +120,7 @@ k_mm_few(const __grid_constant__ FewArgs p)
             const int s = b % STAGES;
             uint8_t* A = base + s * STAGE;
             if (b >= STAGES && ok)
-                ok = mbar_wait(&empty[s], ((b / STAGES) - 1) & 1);
+                ok = mbar_wait_warp(&empty[s], ((b / STAGES) - 1) & 1);
 #pragma unroll
             for (int i = 0; i < WR + TR; ++i) {
                 const int r = first + 64 * (i < WR ? i : i - WR);
@@ -150,7 +150,7 @@ k_mm_few(const __grid_constant__ FewArgs p)
             }
         }
     }
-    if (!mbar_wait(&done, 0))
+    if (!mbar_wait_warp(&done, 0))
         ok = false;
     if (!ok)
         failed = 1;

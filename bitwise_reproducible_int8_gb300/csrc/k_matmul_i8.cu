@@ -24,7 +24,7 @@
 // MMAs for both (warp 1 of the other holds its tensor memory), the others are the epilogue.  The
 // leader's full barriers count both CTAs' bytes; an MMA's commit frees its stage, and hands over its
 // accumulator, in both; both epilogues free the accumulator on the leader's barrier.  Every wait is
-// bounded as there.
+// bounded as there, with one outcome for a whole warp.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -823,11 +823,11 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
         bool ok = true;
         int s = 0, ph = 1;   // stage, and the parity whose end frees it (of a fresh barrier: at once)
         int filled = 0;
-        for (int i = pair; i < p.p.items && ok && !*(volatile int*)&sm->failed; i += pairs) {
+        for (int i = pair; i < p.p.items && ok && !__any_sync(0xffffffffu, *(volatile int*)&sm->failed); i += pairs) {
             const Item t = item_at(p, i);
             const int ya = t.m0 + (int)rank * HM, yb = t.n0 + (int)rank * HM;
             for (int kb = t.kb0; kb < t.kb1; ++kb) {
-                if (!mbar_wait(&sm->empty[s], (uint32_t)ph)) {
+                if (!mbar_wait_warp(&sm->empty[s], (uint32_t)ph)) {
                     ok = false;
                     break;
                 }
@@ -849,14 +849,14 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
             for (; filled > 0; --filled) {
                 if (--s < 0)
                     s = STAGES - 1, ph ^= 1;
-                if (!mbar_wait(&sm->full[s], (uint32_t)(ph ^ 1)))
+                if (!mbar_wait_warp(&sm->full[s], (uint32_t)(ph ^ 1)))
                     ok = false;
             }
         // and either CTA the arrivals of its own stages' last products, which come from the leader's
         // tensor core: none may be on its way into a CTA that has exited
         s = s1, ph = ph1;
         for (int k = 0; k < STAGES && ok; ++k) {
-            ok = mbar_wait(&sm->empty[s], (uint32_t)ph);
+            ok = mbar_wait_warp(&sm->empty[s], (uint32_t)ph);
             if (++s == STAGES)
                 s = 0, ph ^= 1;
         }
@@ -871,9 +871,9 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
                 const Item t = item_at(p, i);
                 for (int kb = t.kb0; kb < t.kb1 && ok; kb += SLICE_KB) {   // a slice; a part starts with one
                     const int end = min(kb + SLICE_KB, t.kb1);
-                    ok = mbar_wait(&sm->dempty[d], (uint32_t)dph);
+                    ok = mbar_wait_warp(&sm->dempty[d], (uint32_t)dph);
                     for (int j = kb; j < end && ok; ++j) {
-                        ok = mbar_wait(&sm->full[s], (uint32_t)ph);
+                        ok = mbar_wait_warp(&sm->full[s], (uint32_t)ph);
                         if (!ok)
                             break;
                         fence_after();
@@ -925,7 +925,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
             // exact) and both become int32 once the accumulator is free: what stands between a tile's
             // way out and the next tile's third slice is then the loads alone
             uint32_t acc[EW];
-            ok = mbar_wait(&sm->dfull[d], ph);
+            ok = mbar_wait_warp(&sm->dfull[d], ph);
             if (!ok)
                 break;
             fence_after();
@@ -938,7 +938,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
             release(lead + 8 * d, lane);
             turn_buffer(d, ph);
             if (NS > 1) {
-                ok = mbar_wait(&sm->dfull[d], ph);
+                ok = mbar_wait_warp(&sm->dfull[d], ph);
                 if (!ok)
                     break;
                 fence_after();
@@ -950,7 +950,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
             for (int j = 0; j < EW; ++j)
                 acc[j] = (uint32_t)__float2int_rn(__uint_as_float(acc[j]));
             for (int sl = 2; sl < NS && ok; ++sl) {
-                ok = mbar_wait(&sm->dfull[d], ph);
+                ok = mbar_wait_warp(&sm->dfull[d], ph);
                 if (!ok)
                     break;
                 fence_after();
@@ -986,7 +986,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUt
     // `done` arrives in both CTAs, by itself in each, once every MMA has completed: each waits for its own
     // (here, behind all other waits, where it is on its way already, so that the limit fits any product)
     if (warp == 1) {
-        if (!mbar_wait(&sm->done, 0) && lane == 0)
+        if (!mbar_wait_warp(&sm->done, 0) && lane == 0)
             sm->failed = 1;
         __syncwarp();
     }

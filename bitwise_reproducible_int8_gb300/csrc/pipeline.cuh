@@ -58,6 +58,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity)
     return true;
 }
 
+// The same by a whole warp: one outcome for all of its lanes, so that none leaves a loop whose other lanes
+// go on to an instruction that takes the whole warp, and lane 0 can report for all
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* b, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, mbar_wait(b, parity));
+}
+
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
                                             uint64_t* bar)
 {
