@@ -4,16 +4,18 @@
 // the fp32 accumulator holding every partial sum over a 512-term K-slice
 // exactly (each is an integer below 2^23).  The hardware documentation does
 // not promise how the tensor core adds inside a slice, so this check runs the
-// tensor-core paths (both tile widths of the forward, 128 x 256 and 128 x 128, and the products
-// of codes on pairs of SMs and for few tokens) and the
+// tensor-core paths (both tile widths of the forward, 128 x 256 and 128 x 128, the product of codes
+// on pairs of SMs, a whole tile of 256 x 256, and the one for few tokens in its three widths) and the
 // CUDA-core dp4a path (exact by construction) on
 // adversarial codes -- every code at the clamp, alternating signs, a sign flip
 // at the slice boundary, one small term among large ones, a slice whose
 // running sum reaches 511 * 16129 = 8,241,919 (just below 2^23) before a last
 // product of +-1 (so the accumulator's lowest integer bit is probed at the top
-// of its range), hashed codes -- and compares the outputs bit for bit.  With
-// unit scales and K = 1024 every output is an integer below 2^24, exact in
-// fp32, so a wrong integer shows.
+// of its range), hashed codes -- and compares the outputs bit for bit.  K is
+// three slices, so that an accumulator is used again; the third has small codes
+// on one side, so that with unit scales every output is an integer of at most
+// 1024 * 16129 + 512 * 4 * 127 < 2^24, exact in fp32, and a wrong integer shows.
+// The outputs are filled with NaN before each path, so that what it leaves out shows too.
 #include <algorithm>
 
 #include "internal.h"
@@ -21,7 +23,7 @@
 namespace repro {
 namespace {
 
-constexpr int ST_M = 128, ST_N = 256, ST_K = 1024;
+constexpr int ST_M = 256, ST_N = 256, ST_K = 1536;
 
 __device__ __forceinline__ int hashed_code(uint32_t r, uint32_t c)
 {
@@ -34,6 +36,8 @@ __device__ __forceinline__ int hashed_code(uint32_t r, uint32_t c)
 
 __device__ __forceinline__ int x_code(int r, int c)
 {
+    if (c >= 1024)
+        return hashed_code((uint32_t)r, (uint32_t)c) % 5;
     switch (r & 7) {
     case 0: return 127;
     case 1: return (c & 1) ? -127 : 127;
@@ -81,13 +85,24 @@ __global__ void k_selftest_compare(const float* __restrict__ a, const float* __r
 
 inline size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 
+// rows of the product of codes that a path takes: a pair's tile, and few tokens (k_matmul_few.cu)
+constexpr int MM_ROWS[4] = {ST_M, 128, 64, 32};
+
+size_t paths_ws_bytes()
+{
+    size_t b = fwd_tc_ws_bytes(ST_M, ST_N, ST_K);
+    for (int rows : MM_ROWS)
+        b = std::max(b, matmul_i8_ws_bytes(rows, ST_N, ST_K, false, false));
+    return b;
+}
+
 } // namespace
 
 size_t selftest_ws_bytes()
 {
     return align256(ST_M * ST_K) + align256(ST_N * ST_K) + align256(16) +
            2 * align256((size_t)ST_M * ST_N * 4) +
-           align256(std::max(fwd_tc_ws_bytes(ST_M, ST_N, ST_K), matmul_i8_ws_bytes(ST_M, ST_N, ST_K, false, false)));
+           align256(paths_ws_bytes());
 }
 
 // 0: identical, 1: a mismatch, negative: a CUDA error
@@ -107,28 +122,31 @@ int run_selftest(void* ws, cudaStream_t st)
     p += align256((size_t)ST_M * ST_N * 4);
     void* tc_ws = p;
 
-    k_selftest_fill<<<(ST_M * ST_K + 255) / 256, 256, 0, st>>>(xq, wq, scales, flag);
+    k_selftest_fill<<<(std::max(ST_M, ST_N) * ST_K + 255) / 256, 256, 0, st>>>(xq, wq, scales, flag);
     count_launches(1);
     if (cudaGetLastError() != cudaSuccess)
         return -1;
     if (launch_fwd_cuda_core(xq, wq, scales, scales + 1, y_cc, ST_M, ST_N, ST_K, st) != cudaSuccess)
         return -1;
+    auto compare = [&](int rows) {
+        k_selftest_compare<<<(rows * ST_N + 255) / 256, 256, 0, st>>>(y_tc, y_cc, rows * ST_N, flag);
+        count_launches(1);
+    };
+    auto clear = [&] { return cudaMemsetAsync(y_tc, 0xff, (size_t)ST_M * ST_N * 4, st) == cudaSuccess; };
     // both tensor-core tile widths (128 x 128 and 128 x 256), each against the
     // CUDA-core output
     for (int wide = 0; wide < 2; ++wide) {
-        if (launch_fwd_tc(xq, wq, scales, scales + 1, y_tc, ST_M, ST_N, ST_K, tc_ws, wide != 0,
-                          st) != cudaSuccess)
+        if (!clear() || launch_fwd_tc(xq, wq, scales, scales + 1, y_tc, ST_M, ST_N, ST_K, tc_ws, wide != 0,
+                                      st) != cudaSuccess)
             return -1;
-        k_selftest_compare<<<(ST_M * ST_N + 255) / 256, 256, 0, st>>>(y_tc, y_cc, ST_M * ST_N, flag);
-        count_launches(1);
+        compare(ST_M);
     }
     // and the products of codes on pairs of SMs and for few tokens (k_matmul_i8.cu, k_matmul_few.cu)
-    const MatmulI8Args mm = {xq, wq, ST_K, ST_K, false, false, nullptr, nullptr, ST_M, ST_N, ST_K, y_tc, 0, ST_N, false};
-    for (int few = 0; few < 2; ++few) {
-        if ((few ? launch_matmul_few(mm, tc_ws, st) : launch_matmul_pair(mm, tc_ws, st)) != cudaSuccess)
+    for (int rows : MM_ROWS) {
+        const MatmulI8Args mm = {xq, wq, ST_K, ST_K, false, false, nullptr, nullptr, rows, ST_N, ST_K, y_tc, 0, ST_N, false};
+        if (!clear() || (rows == ST_M ? launch_matmul_pair(mm, tc_ws, st) : launch_matmul_few(mm, tc_ws, st)) != cudaSuccess)
             return -1;
-        k_selftest_compare<<<(ST_M * ST_N + 255) / 256, 256, 0, st>>>(y_tc, y_cc, ST_M * ST_N, flag);
-        count_launches(1);
+        compare(rows);
     }
     int h = 0;
     if (cudaMemcpyAsync(&h, flag, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
