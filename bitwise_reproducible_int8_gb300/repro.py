@@ -786,7 +786,7 @@ def repro_quant_rows_i8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, 
 
 
 def _codes2d(t, name):
-    """_rows2d that keeps the rows of a matrix without columns."""
+    """_rows2d that keeps the rows of a matrix without columns (no terms, or no outputs)."""
     n, D, ld = _rows2d(t, name)
     return (n if D else math.prod(t.shape[:-1])), D, ld
 
@@ -807,7 +807,7 @@ def repro_matmul_i8(a: torch.Tensor, b: torch.Tensor, y: torch.Tensor, s_a=None,
     or bfloat16 without accumulate; rows at any stride."""
     ar, ac, a_ld = _codes2d(a, "a")
     br, bc, b_ld = _codes2d(b, "b")
-    My, Ny, y_ld = _rows2d(y, "y")
+    My, Ny, y_ld = _codes2d(y, "y")
     M, K = (ac, ar) if trans_a else (ar, ac)
     N, K2 = (bc, br) if trans_b else (br, bc)
     if K != K2 or (My, Ny) != (M, N):
