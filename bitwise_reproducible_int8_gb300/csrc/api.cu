@@ -1372,7 +1372,7 @@ int repro_distill_bwd(const void* z, int z_type, int64_t z_ld, const void* t_idx
 static int check_norm(bool has_y, int type, int u_type, const void* gate, int64_t gate_ld, const float* gain_post,
                       float alpha, float beta, int64_t n, int64_t D, int flags, int allowed)
 {
-    if (!float_type(type) || !float_type(u_type) || (flags & ~allowed) || !finite_f(alpha) || !finite_f(beta))
+    if (!float_type(type) || !float_type(u_type) || (flags & ~allowed) || (has_y && (!finite_f(alpha) || !finite_f(beta))))
         return REPRO_ERR_ARG;
     if ((!has_y && (gate || gain_post || (flags & (REPRO_NORM_POST | REPRO_NORM_GATE_ROWS)))) ||
         (gain_post && !(flags & REPRO_NORM_POST)) || (!gate && (flags & REPRO_NORM_GATE_ROWS)))

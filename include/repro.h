@@ -536,7 +536,7 @@ int repro_distill_bwd(const void* z, int z_type, int64_t z_ld, const void* t_idx
  * gate: with REPRO_NORM_GATE_ROWS a row for each token, gate_ld apart, in x's type; else one row
  * [D] fp32 for all.  x, y, h: `type`; u: u_type.  h may be x itself (same pointer and stride).
  * stats [n][2] fp32 (dense; NULL: not wanted): r1 (0 without a post norm) and r2 (0 without u).
- * 1 <= D <= REPRO_NORM_MAX_D, eps >= 0, alpha and beta finite. */
+ * 1 <= D <= REPRO_NORM_MAX_D, eps >= 0, with y alpha and beta finite. */
 #define REPRO_NORM_POST 4
 #define REPRO_NORM_GATE_ROWS 8
 #define REPRO_NORM_MAX_D 16384
@@ -552,7 +552,7 @@ int repro_block_norm_fwd(const void* x, int64_t x_ld, const void* y, int64_t y_l
  * and the forward's stats:
  *   hn_d = h_d (x) r2;  v_d = du_d (x) gain_pre_d;  c = S(v_d (x) hn_d) (/) D;
  *   g_d = dh_d (+) (r2 (x) (v_d (-) (hn_d (x) c)))  (without dh, or without du, the other alone);
- *   dx_d = g_d (x) alpha (g_d without y);  b_d = g_d (x) beta;
+ *   dx_d = g_d (x) alpha (g_d without y, alpha and beta not looked at);  b_d = g_d (x) beta;
  *   yn_d = y_d (x) r1 and p_d = yn_d (x) gain_post_d with REPRO_NORM_POST, else p_d = y_d;
  *   dgate_d = b_d (x) p_d;  q_d = b_d (x) gate_d (b_d without a gate);
  *   dy_d = q_d, or with REPRO_NORM_POST, w_d = q_d (x) gain_post_d and c' = S(w_d (x) yn_d) (/) D,

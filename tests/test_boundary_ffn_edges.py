@@ -4,6 +4,8 @@ import pytest
 import torch
 
 from bitwise_reproducible_int8_gb300 import build_lib, repro
+from test_boundary_blocks import B, BAD, INF, NAN, call
+from test_boundary_ffn import NORM
 
 
 class Device(torch.Tensor):                  # host memory that passes for a device's
@@ -37,3 +39,16 @@ def test_products_without_outputs(L, M, N, K, ta, tb, accumulate):
     if M != N:
         with pytest.raises(ValueError):
             repro.repro_matmul_i8(a, b, d(N, M), d(M), d(N), ta, tb, accumulate, stream=0)
+
+
+@pytest.mark.parametrize("alpha,beta", [(NAN, 1.0), (1.0, -INF), (INF, NAN)])
+def test_a_norm_alone_takes_any_residual_scales(L, alpha, beta):
+    """Without a block's output alpha and beta are not looked at; with one they are finite."""
+    scales = dict(alpha=alpha, beta=beta)
+    assert call(L.repro_block_norm_fwd, NORM, **scales) == -1
+    assert call(L.repro_block_norm_fwd, NORM, y=None, h=None, **scales) not in BAD
+    ok = dict(dh=B, dh_ld=64, du=2 * B, u_type=0, du_ld=64, h=3 * B, h_ld=64, y=None, y_ld=0, type=0, gate=None, gate_ld=0,
+              gain_post=None, gain_pre=None, stats=6 * B, alpha=1.0, beta=1.0, n=10, D=64, flags=0, dx=7 * B, dx_ld=64, dy=None,
+              dy_ld=0, dgate=None, dgate_ld=0, dgain_post=None, dgain_pre=None, ws=None, ws_bytes=0, stream=None)
+    assert call(L.repro_block_norm_bwd, ok, **scales) not in BAD
+    assert call(L.repro_block_norm_bwd, ok, y=4 * B, y_ld=64, dy=8 * B, dy_ld=64, **scales) == -1
