@@ -250,22 +250,71 @@ k_mm_any(const __grid_constant__ MatmulI8Args g, int64_t tiles_n)
 
 constexpr int RM = 8;    // rows of A a pass
 
-// codes k .. k + 15 of a row of K, 0 past its end
-template <bool VEC> __device__ __forceinline__ int4 codes16(const int8_t* p, int64_t k, int64_t K)
+// this lane's part of the sums over a row of B, 16 codes at a time, against up to R rows of A (out of L1)
+template <int R> __device__ __forceinline__ void rows_by_16(const MatmulI8Args& g, const int8_t* a, const int8_t* b, int64_t m0, int lane, int (&acc)[R])
 {
-    if (VEC)
-        return __ldg(reinterpret_cast<const int4*>(p + k));
-    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int64_t k = 16 * lane; k < g.K; k += 512) {
+        const int4 v = __ldg(reinterpret_cast<const int4*>(b + k));
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-        if (k + e < K)
-            w[e >> 2] |= (uint32_t)(uint8_t)__ldg(p + k + e) << (8 * (e & 3));
-    return make_int4((int)w[0], (int)w[1], (int)w[2], (int)w[3]);
+        for (int r = 0; r < R; ++r) {
+            if (R > 1 && m0 + r >= g.M)
+                break;
+            const int4 x = __ldg(reinterpret_cast<const int4*>(a + r * g.a_ld + k));
+            acc[r] = __dp4a(x.x, v.x, __dp4a(x.y, v.y, __dp4a(x.z, v.z, __dp4a(x.w, v.w, acc[r]))));
+        }
+    }
 }
 
-// A warp takes a row of B at a time, 16 codes a lane, against up to R rows of A (out of L1).
-// VEC: rows of both on 16-byte boundaries and K a multiple of 16.
-template <typename Y, int R, bool VEC>
+// four codes from p on, wherever p lies, out of the two words that cover them
+__device__ __forceinline__ int word_at(const int8_t* p)
+{
+    const uint32_t s = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 3);
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p - s);
+    return (int)__funnelshift_r(__ldg(q), __ldg(q + 1), 8 * s);
+}
+
+// The same for any K and rows on any byte.  Groups of 4 codes from the fourth code on, neighbouring lanes
+// neighbouring groups, as far as the words that cover them lie inside the row; the 11 codes at most that
+// are left at its ends one a lane.  U: groups a lane has in flight.  (16 codes a lane, byte by byte, took
+// 200 us for 16 x 11264 x 2049, 25 for one token; this takes 65 and 15, where 17 tokens take 36 through the
+// widened copies.)
+template <int U, int R> __device__ __forceinline__ void rows_by_4(const MatmulI8Args& g, const int8_t* a, const int8_t* b, int64_t m0, int lane, int (&acc)[R])
+{
+    const int K = (int)g.K, G = K < 12 ? 0 : (K - 8) / 4;
+    for (int i0 = lane; i0 - lane < G; i0 += 32 * U) {
+        int v[U], k[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + 32 * u;
+            k[u] = 4 + 4 * min(i, G - 1);      // a group past the last is the last, times 0
+            const int w = word_at(b + k[u]);
+            v[u] = i < G ? w : 0;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (R > 1 && m0 + r >= g.M)
+                break;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                acc[r] = __dp4a(word_at(a + r * g.a_ld + k[u]), v[u], acc[r]);
+        }
+    }
+    const int k = lane < 4 ? lane : 4 * G + lane;
+    if (lane < 12 && k < K) {
+        const int v = __ldg(b + k);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (R > 1 && m0 + r >= g.M)
+                break;
+            acc[r] += v * __ldg(a + r * g.a_ld + k);
+        }
+    }
+}
+
+// A warp takes a row of B at a time.  U 0: rows of both on 16-byte boundaries and K a multiple of 16; else
+// of rows_by_4.
+template <typename Y, int R, int U>
 __global__ void __launch_bounds__(128)
 k_mm_rows(const __grid_constant__ MatmulI8Args g)
 {
@@ -277,17 +326,10 @@ k_mm_rows(const __grid_constant__ MatmulI8Args g)
     int acc[R] = {};
     const int8_t* b = g.b + n * g.b_ld;
     const int8_t* a = g.a + m0 * g.a_ld;
-#pragma unroll 4
-    for (int64_t k = 16 * lane; k < g.K; k += 512) {
-        const int4 v = codes16<VEC>(b, k, g.K);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (R > 1 && m0 + r >= g.M)
-                break;
-            const int4 x = codes16<VEC>(a + r * g.a_ld, k, g.K);
-            acc[r] = __dp4a(x.x, v.x, __dp4a(x.y, v.y, __dp4a(x.z, v.z, __dp4a(x.w, v.w, acc[r]))));
-        }
-    }
+    if (U == 0)
+        rows_by_16(g, a, b, m0, lane, acc);
+    else
+        rows_by_4<U == 0 ? 1 : U>(g, a, b, m0, lane, acc);
 #pragma unroll
     for (int r = 0; r < R; ++r)
         acc[r] = __reduce_add_sync(0xffffffffu, acc[r]);
@@ -307,11 +349,12 @@ template <typename Y> cudaError_t run_rows(const MatmulI8Args& g, cudaStream_t s
                      (g.M == 1 || g.a_ld % 16 == 0) && (g.N == 1 || g.b_ld % 16 == 0) && g.K % 16 == 0;
     const dim3 grid((unsigned)((g.N + 3) / 4), (unsigned)(g.M == 1 ? 1 : (g.M + RM - 1) / RM));
     count_launches(1);
-    if (g.M == 1)
-        return vec ? launch_pdl(k_mm_rows<Y, 1, true>, grid, dim3(128), 0, st, g)
-                   : launch_pdl(k_mm_rows<Y, 1, false>, grid, dim3(128), 0, st, g);
-    return vec ? launch_pdl(k_mm_rows<Y, RM, true>, grid, dim3(128), 0, st, g)
-               : launch_pdl(k_mm_rows<Y, RM, false>, grid, dim3(128), 0, st, g);
+    if (g.M == 1)   // 2048 x 5633 by 8 groups 19 us, by 4 22; 1001 x 1001 by 8 2.9, by 4 2.5
+        return vec          ? launch_pdl(k_mm_rows<Y, 1, 0>, grid, dim3(128), 0, st, g)
+               : g.K > 1024 ? launch_pdl(k_mm_rows<Y, 1, 8>, grid, dim3(128), 0, st, g)
+                            : launch_pdl(k_mm_rows<Y, 1, 4>, grid, dim3(128), 0, st, g);
+    return vec ? launch_pdl(k_mm_rows<Y, RM, 0>, grid, dim3(128), 0, st, g)
+               : launch_pdl(k_mm_rows<Y, RM, 4>, grid, dim3(128), 0, st, g);
 }
 
 // The same against b = [K][N].  A CTA takes 512 columns of B (16 a lane) and a slab of its rows, 4 rows a
@@ -1108,7 +1151,8 @@ bool aligned16(const MatmulI8Args& g)
 // weights widened on their way (k_matmul_few.cu: 5 tokens 12 us, 16 tokens 13, 64 tokens 20, 128 tokens
 // 30, or 18 for N 2048 and K 5632); else a widened copy and pairs of SMs (27 us up to 256 tokens, 23 for
 // N 2048, K 5632).  The CUDA cores also take up to 16 tokens where the tensor cores may not be used or
-// rows are not aligned, and up to 4 by transposed weights (k_mm_cols).
+// rows are not aligned (K 2049: 1 token 15 us, 4 tokens 27, 8 tokens 41, 16 tokens 65; 17 tokens by widened
+// copies 36), and up to 4 by transposed weights (k_mm_cols).
 bool small_of(int64_t M, bool a_t, bool b_t) { return M <= 16 && !a_t && !b_t; }
 bool few_of(int64_t M, int64_t K, bool a_t, bool b_t) { return M > 4 && M <= 128 && !a_t && !b_t && K % 16 == 0 && K > 0; }
 
