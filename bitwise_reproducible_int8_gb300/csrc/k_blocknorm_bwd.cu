@@ -274,7 +274,8 @@ k_norm_fold(const __grid_constant__ Fold f)
 // Few tokens: up to 2^21 elements, where the terms' way through L2 (16 MB for two sums) takes less than
 // the rows of a chunk one after another, or chunks for less than half of the groups that run at once
 // (three CTAs of 128 threads on an SM, one of more; 152 SMs, whatever the device, as the rule sets the
-// workspace's size).  788 x 7296 fp32: 68 us against 87; 11000 x 3000, which is above: 211 in chunks.
+// workspace's size).  300 x 7296 fp32 26 us, 35 in chunks, bf16 24 and 40; 600 x 7296, at the border, 41 and
+// 37, bf16 37 and 40; in chunks above it: 788 x 7296 38 us, 52 by tokens, 11000 x 3000 174 and 326.
 inline bool by_tokens(int64_t n, int64_t D)
 {
     const int tpr = row_threads(D);

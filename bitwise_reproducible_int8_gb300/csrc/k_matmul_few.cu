@@ -9,7 +9,7 @@
 //
 // Every slice of a tile leaves its int32 sums in the workspace; k_mm_few_join adds them up, exact in
 // any order, and scales them.  (Atomic additions into one sum took 53 us for 128 x 11264 x 2048, the
-// last CTA of a tile adding up its parts 64 us.)  64 x 11264 x 2048 takes 20 us and
+// last CTA of a tile adding up its parts 64 us.)  64 x 11264 x 2048 takes 21 us and
 // 16 x 11264 x 2048 13 us; a widened copy of the weights and tiles for 256 tokens 27 us each: five
 // bytes moved for each of the weights, and most of the MMAs on nothing.
 #include "common.cuh"

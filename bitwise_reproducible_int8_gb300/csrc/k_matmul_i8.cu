@@ -14,11 +14,13 @@
 // Products of few tokens are bound by the weights' bytes: up to 4 on the CUDA cores (k_mm_rows, k_mm_cols),
 // up to 128 in k_matmul_few.cu.
 //
-// Measured, 16384 x 11264 x 2048 with fp32 results: 485 us, 25 of them the widened copies and 460 the
-// product, which has 394 us of tensor work at cuBLAS's bf16 rate, and 738 MB to store beside it (with
-// bf16 results 429 us); 2048 x 5632 x 16384 with both sides transposed and added on: 281 us, 63 of them
-// the copies.  What bounds it now is the way out: an accumulator is free again only once 16 warps have
-// read it, and their results' stores take L2 from the operands.
+// Measured, 16384 x 11264 x 2048 with fp32 results: 475 to 510 us (boards differ, and so does one board
+// warm and cold), 25 of them the widened copies, beside 394 us of tensor work at cuBLAS's bf16 rate and
+// 738 MB to store (with bf16 results 429 to 450); the input gradient's layout, 16384 x 2048 x 11264 by
+// weights [K][N], 490 to 525 (394) and 16384 x 5632 x 2048 260 to 270 (197); 2048 x 5632 x 16384 with both
+// sides transposed and added on: 281 to 294 us, 63 of them the copies.  What bounds it now is the way out: an
+// accumulator is free again only once 16 warps have read it, and their results' stores take L2 from the
+// operands.
 //
 // Roles in a CTA of the pair, as in k_fwd_tc.cu: warp 0 loads, warp 1 of the leading CTA issues the
 // MMAs for both (warp 1 of the other holds its tensor memory), the others are the epilogue.  The
@@ -694,7 +696,7 @@ __device__ __forceinline__ Item item_at(const PairArgs& a, int i)
 // A warp's 32 rows x EW columns: scaled, added to what is there, stored.  own: the columns' scales,
 // two a lane.  They go through the warp's buffer in blocks of 128 bytes a row (chunk k of row r at
 // k ^ (r mod 8)): rows on 16-byte boundaries by one tensor store a block, others row by row (9034 x
-// 9034 x 64 bf16 134 us; 754 by a lane's own row).  (Straight to memory, 4 lanes to a row's line after
+// 9034 x 64 bf16 114 us; 754 by a lane's own row).  (Straight to memory, 4 lanes to a row's line after
 // a turn by shuffles, 16384 x 11264 x 2048 took 46 us longer, although the operands' ring then has two
 // stages more; a lane's own 32 bytes at a time took 34 us longer still.)
 template <typename Y>
@@ -1147,12 +1149,12 @@ bool aligned16(const MatmulI8Args& g)
 }
 
 // Which kernel, for a = [M][K], b = [N][K] (times for N 11264, K 2048 out of HBM): up to 4 tokens the
-// weights' bytes against each of them on the CUDA cores (4 tokens 12 us, 16 tokens 20); up to 128 the
-// weights widened on their way (k_matmul_few.cu: 5 tokens 12 us, 16 tokens 13, 64 tokens 20, 128 tokens
-// 30, or 18 for N 2048 and K 5632); else a widened copy and pairs of SMs (27 us up to 256 tokens, 23 for
-// N 2048, K 5632).  The CUDA cores also take up to 16 tokens where the tensor cores may not be used or
-// rows are not aligned (K 2049: 1 token 15 us, 4 tokens 27, 8 tokens 41, 16 tokens 65; 17 tokens by widened
-// copies 36), and up to 4 by transposed weights (k_mm_cols).
+// weights' bytes against each of them on the CUDA cores (1 token 7 us, 2 tokens 12, 4 tokens 15); up to 128 the
+// weights widened on their way (k_matmul_few.cu: 5 tokens 13 us, 16 tokens 13, 64 tokens 21, 128 tokens
+// 31, or 20 for N 2048 and K 5632); else a widened copy and pairs of SMs (31 us up to 256 tokens).  The CUDA
+// cores also take up to 16 tokens where the tensor cores may not be used or rows are not aligned (K 2049: 1
+// token 15 us, 4 tokens 27, 8 tokens 41, 16 tokens 65; 17 tokens by widened copies 36), and up to 4 by
+// transposed weights (k_mm_cols).
 bool small_of(int64_t M, bool a_t, bool b_t) { return M <= 16 && !a_t && !b_t; }
 bool few_of(int64_t M, int64_t K, bool a_t, bool b_t) { return M > 4 && M <= 128 && !a_t && !b_t && K % 16 == 0 && K > 0; }
 

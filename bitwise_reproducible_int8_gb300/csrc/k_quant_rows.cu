@@ -9,7 +9,7 @@
 // does not depend on its order, so the columns' may meet in atomics.
 //
 // Measured, 16384 x 5632: by rows fp32 67 us, 6.9 TB/s, which is its floor, bf16 54 us (floor 41; issue
-// slots); by columns, where two passes have 122 and 68 us of bytes, fp32 128 us and bf16 104.  4099 x
+// slots); by columns, where two passes have 122 and 68 us of bytes, fp32 127 us and bf16 105.  4099 x
 // 2003 fp32 by columns with a multiplier (rows off 16-byte boundaries, so elements one by one) 22 us.
 // 16384 x 11264 fp32 by rows 141 us, floor 136 (170 with 256 threads a row and a third of it read again).
 #include "codes.cuh"
@@ -67,7 +67,7 @@ struct Kernel {
 };
 
 // v (x) mul; without a multiplier v as it is: what is subnormal is flushed with the maximum, and beside
-// a scale of 2^-100 or more it is nothing
+// a scale of 2^-67 or more, below which values are divided, it is nothing
 __device__ __forceinline__ void times4(float (&v)[4], const float (&m)[4])
 {
 #pragma unroll
